@@ -273,6 +273,91 @@ int rpa_forward_noalloc(const RpaCfg* cfg, const void* q, const void* kv_pages,
 /* Free the workspace and the handle (synchronises the device first). NULL is ignored. */
 void rpa_destroy(RpaHandle* h);
 
+/* ------------------------------------------------------------------------
+ * Operators around the paged cache: writing new tokens into it with rotary
+ * positions, attention that reads a shared prefix once, and eviction by
+ * accumulated attention weight.  Each has its own handle, created from an
+ * RpaCfg (`cache`: the shapes, types and scales of the cache and of q, as
+ * rpa_create takes them, and checked as rpa_validate_cfg does) and used like
+ * an RpaHandle: the same tensors and alignments, asynchronous on the given
+ * stream, calls on one handle serialised on the GPU, capturable into a CUDA
+ * graph after one eager call.
+ *
+ * The status of these handles is sticky: each *_get_status synchronises
+ * `stream`, returns the first device-detected error of the calls since the
+ * last *_get_status (RPA_OK if none), and clears it.
+ * ------------------------------------------------------------------------ */
+
+/* Which elements of a head a rotation pairs: element i of the rotary part with
+ * element i + rotary_dim / 2 (HALF), or 2i with 2i + 1 (INTERLEAVED). */
+typedef enum RpaRopePairing { RPA_ROPE_HALF = 0, RPA_ROPE_INTERLEAVED = 1 } RpaRopePairing;
+
+/* Pair i of n = rotary_dim / 2 turns by w_i radians a position; w_i = base^(-i / n), then
+ *   NONE       as it is
+ *   LINEAR     w_i / factor (positions interpolated)
+ *   BASE       w_i of the larger base  base * factor^(n / (n - 1))
+ *   ROTATIONS  with r = trained_len * w_i / (2 pi) turns within the trained length and
+ *              t = clamp((r - low) / (high - low), 0, 1):  t w_i + (1 - t) w_i / factor
+ *   INDEX      the same two frequencies blended along the pair index:
+ *              at(r) = rotary_dim * ln(trained_len / (2 pi r)) / (2 ln base) is the index that makes r turns,
+ *              a = max(floor(at(high)), 0), b = min(ceil(at(low)), rotary_dim - 1),
+ *              t = 1 - clamp((i - a) / max(b - a, 0.001), 0, 1) */
+typedef enum RpaRopeScaling {
+    RPA_ROPE_NONE = 0,
+    RPA_ROPE_LINEAR = 1,
+    RPA_ROPE_BASE = 2,
+    RPA_ROPE_ROTATIONS = 3,
+    RPA_ROPE_INDEX = 4
+} RpaRopeScaling;
+
+typedef struct RpaRopeCfg {
+    RpaCfg cache;          /* q_dtype is the type of q, k, v and q_out */
+    int64_t rotary_dim;    /* elements rotated: a multiple of 16, 16 .. head_dim (else RPA_ERR_UNSUPPORTED) */
+    int64_t rotary_offset; /* first of them in the head: a multiple of 8, rotary_offset + rotary_dim <= head_dim */
+    int32_t pairing;       /* RpaRopePairing */
+    int32_t scaling;       /* RpaRopeScaling */
+    double base;           /* > 1 */
+    double factor;         /* >= 1 (all but NONE) */
+    double trained_len;    /* > 0 (ROTATIONS, INDEX) */
+    double low, high;      /* 0 < low < high (ROTATIONS, INDEX) */
+    double magnitude;      /* the rotated values are multiplied by it; finite */
+    int64_t reserved;      /* set to 0 */
+} RpaRopeCfg;
+
+typedef struct RpaRope RpaRope;
+
+/* Fill *cfg: cache by rpa_cfg_init from its shape fields, rotary_dim = head_dim, offset 0, HALF, NONE,
+ * base 10000, factor 1, trained_len 0, low 1, high 4, magnitude 1. */
+void rpa_rope_cfg_init(RpaRopeCfg* cfg);
+/* Host only: RPA_OK, RPA_ERR_INVALID_ARG or RPA_ERR_UNSUPPORTED. */
+int rpa_rope_validate_cfg(const RpaRopeCfg* cfg);
+/* w_i of the configuration, rotary_dim / 2 doubles (host only). */
+int rpa_rope_frequencies(const RpaRopeCfg* cfg, double* w);
+int rpa_rope_create(const RpaRopeCfg* cfg, RpaRope** out);
+
+/* Rotate q and k, and write the new tokens' K/V rows to their cache slots.
+ * Token i of sequence s (row t = cu_q_lens[s] + i) has slot kv_lens[s] - q_len + i and the position
+ * positions[t], or its slot's number where positions is NULL; kv_lens counts the new tokens, as in
+ * rpa_forward, which may follow on the same stream with q_out.
+ *   q, k, v    device, [num_q_tokens, Hq | Hkv | Hkv, D] in q_dtype: a token's heads contiguous, tokens
+ *              *_stride elements apart (slices of one fused projection), 16-byte aligned rows
+ *              (RPA_KV_LATENT: k is the whole row, v is NULL)
+ *   positions  device, int32 [num_q_tokens], or NULL
+ *   q_out      device, [num_q_tokens, Hq, D] q_dtype, contiguous, 16-byte aligned; may be q itself
+ * The arithmetic is in 32 bits with one rounding at the end.  Angles are exact to 2^-32 of a turn at
+ * any position.  Cache rows hold k / k_scale and v / v_scale (where set), rounded to nearest even;
+ * the 8-bit types saturate, NaN stays NaN (int8: 0); f16 rows overflow to infinity.
+ * Rows of q_out and slots of the cache that no token of the call stands for are left as they were, as
+ * are those of a sequence with bad lengths (RPA_ERR_BAD_LENGTHS); a token whose page id is bad writes
+ * no cache row (RPA_ERR_BAD_PAGE_INDEX).  Two tokens never share a slot unless page_indices names one
+ * page twice; which of them then remains is unspecified. */
+int rpa_rope_append(RpaRope* h, const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                    int64_t v_stride, void* kv_pages, const int32_t* kv_lens, const int32_t* page_indices,
+                    const int32_t* cu_q_lens, const int32_t* positions, int32_t num_seqs, void* q_out,
+                    void* stream);
+int rpa_rope_get_status(RpaRope* h, void* stream);
+void rpa_rope_destroy(RpaRope* h);
+
 /* Static description of a status code. */
 const char* rpa_strerror(int code);
 

@@ -38,3 +38,8 @@ from .binding import (  # noqa: F401
     make_cfg,
     validate_cfg,
 )
+from .cache import (  # noqa: F401
+    RopeAppend,
+    rope_frequencies,
+    validate_rope_cfg,
+)

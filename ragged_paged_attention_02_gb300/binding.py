@@ -41,7 +41,9 @@ KV_DTYPES = {"bf16": RPA_DT_BF16, "f16": RPA_DT_F16, "fp8_e4m3": RPA_DT_FP8_E4M3
 # every entry point declared in include/rpa.h
 EXPORTS = ("rpa_cfg_init", "rpa_validate_cfg", "rpa_create", "rpa_forward", "rpa_forward_host",
            "rpa_get_status", "rpa_read_plan", "rpa_profile_begin", "rpa_profile_read", "rpa_set_option",
-           "rpa_forward_noalloc", "rpa_destroy", "rpa_strerror", "rpa_version")
+           "rpa_forward_noalloc", "rpa_destroy", "rpa_strerror", "rpa_version",
+           "rpa_rope_cfg_init", "rpa_rope_validate_cfg", "rpa_rope_frequencies", "rpa_rope_create", "rpa_rope_append",
+           "rpa_rope_get_status", "rpa_rope_destroy")
 
 RPA_OPT_WAIT_TIMEOUT_MS = 1
 RPA_OPT_SERIAL = 2
@@ -66,6 +68,15 @@ class RpaCfg(ctypes.Structure):
         ("has_sliding_window", ctypes.c_int32), ("has_sinks", ctypes.c_int32),
         ("kv_layout", ctypes.c_int32), ("reserved", ctypes.c_int32),
         ("v_head_dim", ctypes.c_int64), ("sinks", ctypes.c_void_p),
+    ]
+
+
+class RpaRopeCfg(ctypes.Structure):
+    _fields_ = [
+        ("cache", RpaCfg), ("rotary_dim", ctypes.c_int64), ("rotary_offset", ctypes.c_int64),
+        ("pairing", ctypes.c_int32), ("scaling", ctypes.c_int32), ("base", ctypes.c_double),
+        ("factor", ctypes.c_double), ("trained_len", ctypes.c_double), ("low", ctypes.c_double),
+        ("high", ctypes.c_double), ("magnitude", ctypes.c_double), ("reserved", ctypes.c_int64),
     ]
 
 
@@ -120,6 +131,16 @@ def lib():
         L.rpa_strerror.restype = ctypes.c_char_p
         L.rpa_version.argtypes = []
         L.rpa_version.restype = ctypes.c_int
+        ropecfg = ctypes.POINTER(RpaRopeCfg)
+        L.rpa_rope_cfg_init.argtypes = [ropecfg]
+        L.rpa_rope_cfg_init.restype = None
+        L.rpa_rope_validate_cfg.argtypes = [ropecfg]
+        L.rpa_rope_frequencies.argtypes = [ropecfg, vp]
+        L.rpa_rope_create.argtypes = [ropecfg, ctypes.POINTER(vp)]
+        L.rpa_rope_append.argtypes = [vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, i32, vp, vp]
+        L.rpa_rope_get_status.argtypes = [vp, vp]
+        L.rpa_rope_destroy.argtypes = [vp]
+        L.rpa_rope_destroy.restype = None
         _lib = L
     return _lib
 

@@ -1,0 +1,204 @@
+"""The paged cache's operators beside attention, over the C ABI of include/rpa.h.
+
+Argument checks and marshalling only, as in ``binding``: every step of the
+computation runs in the CUDA library.  Each class owns one library handle,
+made on the current device from the keywords of ``RaggedPagedAttention``
+(shapes, types and scales of the cache and of q) and its own.  Calls on one
+object share its workspace and must be serialised on the GPU.
+"""
+
+from __future__ import annotations
+
+import ctypes
+
+import numpy as np
+
+from .binding import (RPA_DT_BF16, RPA_DT_F16, RPA_DT_F32, RPA_KV_LATENT, RPA_OK, RpaError, RpaRopeCfg,
+                      lib, make_cfg)
+
+ROPE_PAIRINGS = {"half": 0, "interleaved": 1}
+ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "rotations": 3, "index": 4}
+
+
+def _q_type(code):
+    import torch
+
+    return {RPA_DT_BF16: torch.bfloat16, RPA_DT_F16: torch.float16, RPA_DT_F32: torch.float32}[code]
+
+
+class _Handle:
+    """A library handle on the device that was current when it was made."""
+
+    _prefix = ""  # of the C entry points
+
+    def _create(self, cfg, *more):
+        import torch
+
+        h = ctypes.c_void_p()
+        r = getattr(lib(), self._prefix + "create")(ctypes.byref(cfg), *more, ctypes.byref(h))
+        if r != RPA_OK:
+            raise RpaError(r, self._prefix + "create")
+        self._h = h
+        self._device = torch.cuda.current_device()
+
+    def _checks(self, c):
+        """What the calls' tensors have to be, from the RpaCfg."""
+        import torch
+
+        self._latent = c.kv_layout == RPA_KV_LATENT
+        self._q_dtype = _q_type(c.q_dtype)
+        self._q_shape = (c.num_q_tokens, c.num_q_heads, c.head_dim)
+        self._kv_shape = (c.total_num_pages, c.page_size, c.num_kv_heads * (1 if self._latent else 2), c.head_dim)
+        self._kv_dtype = {RPA_DT_BF16: torch.bfloat16, RPA_DT_F16: torch.float16}.get(c.kv_dtype)  # None: one byte
+        self._table_shape = (c.max_num_seqs, c.pages_per_seq)
+        self._scores_shape = (c.total_num_pages, c.num_kv_heads, c.page_size)
+
+    def _need(self, name, t, dtype, shape):
+        if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)}")
+
+    def _need_cache(self, kv_pages):
+        if kv_pages.shape != self._kv_shape or not kv_pages.is_contiguous():
+            raise ValueError(f"kv_pages must be contiguous {self._kv_shape}")
+        if (kv_pages.dtype != self._kv_dtype) if self._kv_dtype else (kv_pages.element_size() != 1):
+            raise ValueError(f"kv_pages must hold {self._kv_dtype or 'one byte'} elements")
+
+    def _need_lengths(self, kv_lens, page_indices, cu_q_lens):
+        import torch
+
+        self._need("kv_lens", kv_lens, torch.int32, self._table_shape[:1])
+        self._need("page_indices", page_indices, torch.int32, self._table_shape)
+        if cu_q_lens is not None:
+            self._need("cu_q_lens", cu_q_lens, torch.int32, (self._table_shape[0] + 1,))
+
+    def _need_here(self, *tensors):
+        for t in tensors:
+            if t is not None and t.get_device() != self._device:
+                raise ValueError(f"every tensor must be on cuda:{self._device}, where the handle was made")
+
+    def _stream(self, stream, *tensors):
+        """The stream's pointer.  On another stream than the current one the tensors' memory is kept until it is done."""
+        import torch
+
+        here = torch.cuda.current_stream(self._device)
+        if stream is None or stream == here:
+            return here.cuda_stream
+        if stream.device.index != self._device:
+            raise ValueError(f"the stream must be one of cuda:{self._device}, where the handle was made")
+        for t in tensors:
+            if t is not None:
+                t.record_stream(stream)
+        return stream.cuda_stream
+
+    def _call(self, name, *args):
+        if not self._h:
+            raise ValueError("the handle is closed")
+        r = getattr(lib(), self._prefix + name)(self._h, *args)
+        if r != RPA_OK:
+            raise RpaError(r, self._prefix + name)
+
+    def status(self, stream=None) -> int:
+        """The first device-detected error since the last status(), which this clears; synchronises the stream."""
+        if not self._h:
+            raise ValueError("the handle is closed")
+        return int(getattr(lib(), self._prefix + "get_status")(self._h, self._stream(stream)))
+
+    def close(self):
+        if getattr(self, "_h", None):
+            getattr(lib(), self._prefix + "destroy")(self._h)
+            self._h = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def make_rope_cfg(*, rotary_dim=None, rotary_offset=0, pairing="half", scaling="none", base=10000.0, factor=1.0,
+                  trained_len=0, low=1.0, high=4.0, magnitude=1.0, **cfg) -> RpaRopeCfg:
+    c = RpaRopeCfg()
+    c.cache = make_cfg(**cfg)
+    c.rotary_dim = c.cache.head_dim if rotary_dim is None else int(rotary_dim)
+    c.rotary_offset = int(rotary_offset)
+    c.pairing, c.scaling = ROPE_PAIRINGS[pairing], ROPE_SCALINGS[scaling]
+    c.base, c.factor, c.trained_len = float(base), float(factor), float(trained_len)
+    c.low, c.high, c.magnitude = float(low), float(high), float(magnitude)
+    return c
+
+
+def validate_rope_cfg(**cfg) -> int:
+    """Host-only check of RopeAppend's keywords: the status code."""
+    return int(lib().rpa_rope_validate_cfg(ctypes.byref(make_rope_cfg(**cfg))))
+
+
+def rope_frequencies(**cfg) -> np.ndarray:
+    """Radians a position turns each pair by (float64 [rotary_dim / 2]) for RopeAppend's keywords."""
+    c = make_rope_cfg(**cfg)
+    w = np.zeros(max(1, c.rotary_dim // 2), np.float64)
+    r = lib().rpa_rope_frequencies(ctypes.byref(c), w.ctypes.data)
+    if r != RPA_OK:
+        raise RpaError(r, "rpa_rope_frequencies")
+    return w
+
+
+class RopeAppend(_Handle):
+    """Rotary positions on q and the new keys, and the write of the new K/V rows to the paged cache.
+
+    Keywords beside RaggedPagedAttention's: ``rotary_dim`` (a multiple of 16; default the head) and
+    ``rotary_offset`` (a multiple of 8) say which part of a head turns, ``pairing`` "half" or
+    "interleaved" which elements form a pair; ``base``, ``scaling`` ("none", "linear", "base",
+    "rotations", "index"), ``factor``, ``trained_len``, ``low`` and ``high`` the frequencies
+    (include/rpa.h, RpaRopeScaling), ``magnitude`` a factor of the rotated values.
+    """
+
+    _prefix = "rpa_rope_"
+
+    def __init__(self, **cfg):
+        self._h = None
+        self._c = make_rope_cfg(**cfg)
+        self._create(self._c)
+        self._checks(self._c.cache)
+
+    def _check(self, q, k, v, kv_pages, kv_lens, page_indices, cu_q_lens, positions, q_out):
+        import torch
+
+        T, Hq, D = self._q_shape
+        rows = (T, self._c.cache.num_kv_heads, D)
+        if (v is None) != self._latent:
+            raise ValueError("v is None with the latent layout, whose rows are k, and only there")
+        for name, t, shape in (("q", q, self._q_shape), ("k", k, rows), ("v", v, rows)):
+            if t is None:
+                continue
+            if t.dtype != self._q_dtype or t.shape != shape or (T and (t.stride(2) != 1 or t.stride(1) != D)):
+                raise ValueError(f"{name} must be a {self._q_dtype} tensor {tuple(shape)} whose tokens' heads are contiguous")
+        self._need_cache(kv_pages)
+        self._need_lengths(kv_lens, page_indices, cu_q_lens)
+        if positions is not None:
+            self._need("positions", positions, torch.int32, (T,))
+        self._need("q_out", q_out, self._q_dtype, self._q_shape)
+
+    def append(self, q, k, v, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, positions=None, q_out=None, stream=None):
+        """Write the tokens' K/V rows into kv_pages and return the rotated q (q_out; q itself where that is given).
+
+        q [T, Hq, D], k and v [T, Hkv, D] in q's type: tokens may be any multiple of 16 bytes apart (slices of a
+        fused projection).  kv_lens counts the new tokens: token i of a sequence goes to slot kv_len - q_len + i,
+        which is its position too unless ``positions`` (int32 [T]) gives another.
+        """
+        import torch
+
+        if q_out is None:
+            with torch.cuda.stream(stream):
+                q_out = torch.zeros(self._q_shape, dtype=self._q_dtype, device=q.device)
+        self._check(q, k, v, kv_pages, kv_lens, page_indices, cu_q_lens, positions, q_out)
+        tensors = (q, k, v, kv_pages, kv_lens, page_indices, cu_q_lens, positions, q_out)
+        self._need_here(*tensors)
+        # the distance of two tokens; with one token any will do
+        far = self._q_shape[0] > 1
+        rows = self._c.cache.num_kv_heads * self._q_shape[2]
+        self._call("append", q.data_ptr(), q.stride(0) if far else self._q_shape[1] * self._q_shape[2],
+                   k.data_ptr(), k.stride(0) if far else rows, None if v is None else v.data_ptr(),
+                   0 if v is None else v.stride(0) if far else rows, kv_pages.data_ptr(), kv_lens.data_ptr(),
+                   page_indices.data_ptr(), cu_q_lens.data_ptr(), None if positions is None else positions.data_ptr(),
+                   int(num_seqs), q_out.data_ptr(), self._stream(stream, *tensors))
+        return q_out

@@ -54,24 +54,6 @@ size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
 size_t q_elt_bytes(int32_t dt) { return dt == RPA_DT_F32 ? 4 : 2; }
 
-struct DeviceGuard {
-    int prev = -1;
-    bool ok = true;
-    explicit DeviceGuard(int dev) {
-        if (cudaGetDevice(&prev) != cudaSuccess) {
-            ok = false;
-            return;
-        }
-        if (prev != dev && cudaSetDevice(dev) != cudaSuccess) ok = false;
-    }
-    ~DeviceGuard() {
-        int cur;
-        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
-    }
-};
-
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
 void prof_free(RpaHandle* h) {
     if (!h->prof_ev) return;
     for (int i = 0; i < h->prof_cap * kProfEvents; ++i)

@@ -321,6 +321,35 @@ int enqueue_forward(const RpaCfg& c, const KernelSet& ks, const Workspace& ws, M
                     const void* kv_pages, const int32_t* kv_lens, const int32_t* page_indices,
                     const int32_t* cu_q_lens, int32_t num_seqs, void* o, const EnqueueOpts& eo);
 
+// ---------------------------------------------------------------- host helpers of the entry points
+// Makes a handle's device current for a scope.
+struct DeviceGuard {
+    int prev = -1;
+    bool ok = true;
+    explicit DeviceGuard(int dev) {
+        if (cudaGetDevice(&prev) != cudaSuccess) {
+            ok = false;
+            return;
+        }
+        if (prev != dev && cudaSetDevice(dev) != cudaSuccess) ok = false;
+    }
+    ~DeviceGuard() {
+        int cur;
+        if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
+    }
+};
+inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
+// Synchronises st, reads a sticky device status word and clears it where it holds an error.
+inline int take_status(int* word, cudaStream_t st) {
+    int v = 0;
+    if (cudaMemcpyAsync(&v, word, sizeof v, cudaMemcpyDeviceToHost, st) != cudaSuccess ||
+        cudaStreamSynchronize(st) != cudaSuccess)
+        return RPA_ERR_CUDA;
+    if (v != RPA_OK && (cudaMemsetAsync(word, 0, sizeof v, st) != cudaSuccess || cudaStreamSynchronize(st) != cudaSuccess))
+        return RPA_ERR_CUDA;
+    return v;
+}
+
 // ---------------------------------------------------------------- device helpers
 #ifdef __CUDACC__
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
@@ -535,6 +564,21 @@ __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.lau
 
 __device__ __forceinline__ void set_status(int* ctrl, int code) {
     atomicCAS(ctrl + kStatus, 0, code);
+}
+
+// The sequence whose query tokens hold token t: the last s in [0, S) with cu[s] <= t, or -1 (also
+// when t >= cu[s + 1]).  One warp, 32 probes a round; any cu gives a result in range.
+__device__ __forceinline__ int find_seq(const int* cu, int S, int t, int lane) {
+    int lo = 0, n = S + 1;
+    while (n > 1) {
+        const int step = (n + 31) / 32, at = lo + lane * step;
+        const int below = __popc(__ballot_sync(0xffffffffu, at < lo + n && cu[min(at, S)] <= t));
+        if (below == 0) return -1;
+        const int end = lo + n;
+        lo += (below - 1) * step;
+        n = min(step, end - lo);
+    }
+    return lo < S && cu[lo] <= t && t < cu[lo + 1] ? lo : -1;
 }
 
 // ---- mbarrier, bulk tensor copies, timer

@@ -1,0 +1,475 @@
+// rpa_rope.cu -- rotary positions and the write of new tokens into the paged cache.
+//
+// One launch takes q, k and v of a ragged batch (slices of a fused projection), rotates the rotary
+// part of every q and k head by its token's position, writes q in its own type and K/V rows in the
+// cache's type to the slots the page table names.
+//
+// The angle of pair i at position p is p w_i.  The handle keeps w_i / (2 pi) as a 64-bit binary
+// fraction of a turn f_i, so that p f_i mod 2^64 is the angle's fraction of a turn in one integer
+// product, exact but for f_i's own rounding (2^-65 of a turn a position, below 2^-34 over 31 bits of
+// positions; w_i itself is a double).  In 32-bit floating point the same product would be off by a
+// tenth of a radian at a million positions, and in 64 bits the GPU runs it at 1/64 of the rate.
+// Sines are computed once per token and pair, into shared memory, and serve all heads.
+//
+// A CTA takes one token: units of 16 elements (two 16-byte vectors of 2-byte types) of one row
+// (q head, K row or V row).  A rotary unit is 8 pairs, both partners in one thread's registers
+// (HALF: two vectors rotary_dim / 2 apart; INTERLEAVED: 16 neighbours), so that a row is read once
+// and written once.  Each thread keeps its place in the row and steps over the rows, so that its
+// sines stay in registers; its first rows' loads go out before the token's sequence is looked up
+// (cu_q_lens by a 32-ary search of one warp, then kv_lens, then the page id: four dependent loads).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <string.h>
+
+#include <cmath>
+#include <new>
+
+#include "rpa_internal.cuh"
+
+using namespace rpa;
+
+struct RpaRope {
+    RpaRopeCfg cfg;
+    int device;
+    unsigned long long* turns;  // device [rotary_dim / 2]: f_i
+    int* status;                // device: first error since the last rpa_rope_get_status
+};
+
+namespace rpa {
+namespace {
+
+constexpr int kUnit = 16;       // elements of a unit
+constexpr int kMaxThreads = 288;
+constexpr int kMaxPairs = 288;  // rotary_dim <= 576
+
+struct RopeParams {
+    const uint8_t *q, *k, *v;
+    size_t q_stride, k_stride, v_stride;  // bytes between tokens
+    uint8_t *q_out, *kv;
+    const int *kv_lens, *page_indices, *cu, *positions;
+    const unsigned long long* turns;
+    int* status;
+    int S, T, Hq, Hkv, D, ps, P, N, latent;
+    int rd, off;
+    int rows;       // q heads + K rows + V rows of a token
+    int per_row;    // units of a row
+    int row_step;   // rows the CTA takes at once
+    int kt;         // KvType of the cache
+    int has_ks, has_vs;
+    float magnitude, k_scale, v_scale;
+};
+
+template <typename T>
+struct Vec8;  // eight elements as loaded
+template <>
+struct Vec8<float> {
+    float4 a, b;
+};
+struct Half8 {
+    uint4 a;
+};
+template <>
+struct Vec8<__nv_bfloat16> : Half8 {};
+template <>
+struct Vec8<__half> : Half8 {};
+
+__device__ __forceinline__ void load8(const uint8_t* p, Vec8<float>& v) {
+    v.a = *reinterpret_cast<const float4*>(p);
+    v.b = *reinterpret_cast<const float4*>(p + 16);
+}
+__device__ __forceinline__ void load8(const uint8_t* p, Half8& v) { v.a = *reinterpret_cast<const uint4*>(p); }
+
+__device__ __forceinline__ void widen(const Vec8<float>& v, float* f) {
+    f[0] = v.a.x; f[1] = v.a.y; f[2] = v.a.z; f[3] = v.a.w;
+    f[4] = v.b.x; f[5] = v.b.y; f[6] = v.b.z; f[7] = v.b.w;
+}
+__device__ __forceinline__ void widen(const Vec8<__nv_bfloat16>& v, float* f) {
+    const uint32_t w[4] = {v.a.x, v.a.y, v.a.z, v.a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        f[2 * i] = __uint_as_float(w[i] << 16);
+        f[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+}
+__device__ __forceinline__ void widen(const Vec8<__half>& v, float* f) {
+    const uint32_t w[4] = {v.a.x, v.a.y, v.a.z, v.a.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float2 h = f16x2_to_f32x2(w[i]);
+        f[2 * i] = h.x;
+        f[2 * i + 1] = h.y;
+    }
+}
+
+template <bool F16>
+__device__ __forceinline__ uint4 round8(const float* f) {
+    return make_uint4(pack2<F16>(f[0], f[1]), pack2<F16>(f[2], f[3]), pack2<F16>(f[4], f[5]), pack2<F16>(f[6], f[7]));
+}
+__device__ __forceinline__ void store_q8(float* p, const float* f) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+}
+__device__ __forceinline__ void store_q8(__nv_bfloat16* p, const float* f) { *reinterpret_cast<uint4*>(p) = round8<false>(f); }
+__device__ __forceinline__ void store_q8(__half* p, const float* f) { *reinterpret_cast<uint4*>(p) = round8<true>(f); }
+
+template <bool E5M2>
+__device__ __forceinline__ uint32_t fp8x4(const float* f) {
+    uint16_t lo, hi;
+    if constexpr (E5M2) {
+        asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;\n" : "=h"(lo) : "f"(f[1]), "f"(f[0]));
+        asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;\n" : "=h"(hi) : "f"(f[3]), "f"(f[2]));
+    } else {
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(lo) : "f"(f[1]), "f"(f[0]));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;\n" : "=h"(hi) : "f"(f[3]), "f"(f[2]));
+    }
+    return (uint32_t)lo | ((uint32_t)hi << 16);
+}
+__device__ __forceinline__ uint32_t int8x4(const float* f) {
+    uint32_t r = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r |= (uint32_t)(uint8_t)(int8_t)max(-128, min(127, __float2int_rn(f[i]))) << (8 * i);
+    return r;
+}
+// Eight cache elements at element e of the row that starts at byte offset `row` of the cache.
+__device__ __forceinline__ void store_kv8(uint8_t* kv, size_t row, int e, const float* f, int kt) {
+    switch (kt) {
+        case KT_BF16: *reinterpret_cast<uint4*>(kv + row + 2 * e) = round8<false>(f); break;
+        case KT_F16: *reinterpret_cast<uint4*>(kv + row + 2 * e) = round8<true>(f); break;
+        case KT_E4M3: *reinterpret_cast<uint2*>(kv + row + e) = make_uint2(fp8x4<false>(f), fp8x4<false>(f + 4)); break;
+        case KT_E5M2: *reinterpret_cast<uint2*>(kv + row + e) = make_uint2(fp8x4<true>(f), fp8x4<true>(f + 4)); break;
+        default: *reinterpret_cast<uint2*>(kv + row + e) = make_uint2(int8x4(f), int8x4(f + 4)); break;
+    }
+}
+
+template <typename QT, bool HALF>
+__global__ void __launch_bounds__(kMaxThreads) rpa_rope_kernel(const RopeParams p) {
+    constexpr int kBatch = sizeof(QT) == 4 ? 2 : 4;  // rows whose loads a thread has in flight
+    __shared__ float2 s_cs[kMaxPairs];
+    __shared__ long long s_slot;  // cache slot of the token (page * page_size + place), or -1
+    __shared__ int s_pos, s_live;
+    const int t = blockIdx.x, tid = threadIdx.x;
+    const int place = tid % p.per_row, row0 = tid / p.per_row;
+    // this thread's unit: elements [e0, e0 + 8) and [e1, e1 + 8) of a row
+    const int rot_units = p.rd / kUnit;
+    const bool rot = place < rot_units;
+    int e0, e1;
+    if (rot) {
+        e0 = p.off + place * (HALF ? 8 : 16);
+        e1 = e0 + (HALF ? p.rd / 2 : 8);
+    } else {
+        const int c = (place - rot_units) * 16;  // of the elements outside the rotary part
+        e0 = c < p.off ? c : c + p.rd;
+        e1 = c + 8 < p.off ? c + 8 : c + 8 + p.rd;
+    }
+    auto source = [&](int r) -> const uint8_t* {
+        const size_t eb = sizeof(QT);
+        if (r < p.Hq) return p.q + (size_t)t * p.q_stride + (size_t)r * p.D * eb;
+        r -= p.Hq;
+        if (r < p.Hkv) return p.k + (size_t)t * p.k_stride + (size_t)r * p.D * eb;
+        return p.v + (size_t)t * p.v_stride + (size_t)(r - p.Hkv) * p.D * eb;
+    };
+    pdl_trigger();
+    pdl_wait();
+    Vec8<QT> x0[kBatch], x1[kBatch];
+    auto fetch = [&](int r0) {
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int r = r0 + b * p.row_step;
+            if (r < p.rows && t < p.T) {
+                const uint8_t* s = source(r);
+                load8(s + e0 * sizeof(QT), x0[b]);
+                load8(s + e1 * sizeof(QT), x1[b]);
+            }
+        }
+    };
+    fetch(row0);
+    if (tid < 32) {
+        const int s = find_seq(p.cu, p.S, t, tid);
+        if (tid == 0) {
+            int live = 0, pos = 0;
+            long long slot = -1;
+            if (s >= 0) {
+                const int q0 = p.cu[s], ql = p.cu[s + 1] - q0, kl = p.kv_lens[s];
+                if (q0 >= 0 && kl <= p.P * p.ps && ql <= kl && q0 + ql <= p.T) {
+                    live = 1;
+                    const int j = kl - ql + (t - q0);
+                    const int pg = p.page_indices[(size_t)s * p.P + j / p.ps];
+                    pos = p.positions ? p.positions[t] : j;
+                    if ((unsigned)pg < (unsigned)p.N) slot = (long long)pg * p.ps + j % p.ps;
+                    else set_status(p.status, RPA_ERR_BAD_PAGE_INDEX);
+                }
+            }
+            s_live = live;
+            s_pos = pos;
+            s_slot = slot;
+        }
+    }
+    __syncthreads();
+    const long long slot = s_slot;
+    if (s_live) {
+        for (int i = tid; i < p.rd / 2; i += blockDim.x) {
+            // the angle's fraction of a turn, its upper 32 bits as half turns in [-1, 1)
+            const unsigned long long f = p.turns[i] * (unsigned long long)(long long)s_pos;
+            float sn, cs;
+            sincospif((float)(int)((f + 0x80000000ull) >> 32) * 4.656612873077393e-10f, &sn, &cs);
+            s_cs[i] = make_float2(cs * p.magnitude, sn * p.magnitude);
+        }
+    }
+    __syncthreads();
+    if (s_live) {
+        float cs[8], sn[8];
+        if (rot) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float2 v = s_cs[place * 8 + i];
+                cs[i] = v.x;
+                sn[i] = v.y;
+            }
+        }
+        for (int r0 = row0; r0 < p.rows; r0 += kBatch * p.row_step) {
+            if (r0 != row0) fetch(r0);
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                const int r = r0 + b * p.row_step;
+                if (r >= p.rows) continue;
+                float y[16];
+                widen(x0[b], y);
+                widen(x1[b], y + 8);
+                if (rot && r < p.Hq + p.Hkv) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int a = HALF ? i : 2 * i, c = HALF ? i + 8 : 2 * i + 1;
+                        const float u = y[a], w = y[c];
+                        y[a] = u * cs[i] - w * sn[i];
+                        y[c] = w * cs[i] + u * sn[i];
+                    }
+                }
+                if (r < p.Hq) {
+                    QT* o = reinterpret_cast<QT*>(p.q_out) + ((size_t)t * p.Hq + r) * p.D;
+                    store_q8(o + e0, y);
+                    store_q8(o + e1, y + 8);
+                } else if (slot >= 0) {
+                    const bool is_v = r >= p.Hq + p.Hkv;
+                    const int h = r - p.Hq - (is_v ? p.Hkv : 0);
+                    if (is_v ? p.has_vs : p.has_ks) {
+                        const float sc = is_v ? p.v_scale : p.k_scale;
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) y[i] = __fdiv_rn(y[i], sc);
+                    }
+                    const int rows = p.latent ? p.Hkv : 2 * p.Hkv;
+                    const size_t row = ((size_t)slot * rows + (p.latent ? h : 2 * h + (is_v ? 1 : 0))) * p.D *
+                                       (kt_8bit(p.kt) ? 1 : 2);
+                    store_kv8(p.kv, row, e0, y, p.kt);
+                    store_kv8(p.kv, row, e1, y + 8, p.kt);
+                }
+            }
+        }
+    }
+    // the lengths of every sequence, once
+    if (t == 0) {
+        for (int s = tid; s < p.S; s += blockDim.x) {
+            const int q0 = p.cu[s], q1 = p.cu[s + 1], kl = p.kv_lens[s];
+            if (q0 < 0 || q1 < q0 || kl < 0 || kl > p.P * p.ps || q1 - q0 > kl || q1 > p.T)
+                set_status(p.status, RPA_ERR_BAD_LENGTHS);
+        }
+    }
+}
+
+template <typename QT>
+cudaError_t launch_rope(const RopeParams& p, int half, int grid, int threads, cudaStream_t st) {
+    return half ? launch_pdl(rpa_rope_kernel<QT, true>, grid, threads, 0, st, p)
+                : launch_pdl(rpa_rope_kernel<QT, false>, grid, threads, 0, st, p);
+}
+
+constexpr double kTwoPi = 6.283185307179586476925286766559;
+
+void frequencies(const RpaRopeCfg& c, double* w) {
+    const int n = (int)(c.rotary_dim / 2);
+    const double rd = (double)c.rotary_dim;
+    double base = c.base;
+    if (c.scaling == RPA_ROPE_BASE) base *= std::pow(c.factor, (double)n / (n - 1));
+    double a = 0, b = 0;
+    if (c.scaling == RPA_ROPE_INDEX) {
+        const double at_high = rd * std::log(c.trained_len / (c.high * kTwoPi)) / (2 * std::log(c.base));
+        const double at_low = rd * std::log(c.trained_len / (c.low * kTwoPi)) / (2 * std::log(c.base));
+        a = std::fmax(std::floor(at_high), 0.0);
+        b = std::fmin(std::ceil(at_low), rd - 1);
+    }
+    for (int i = 0; i < n; ++i) {
+        const double x = std::pow(base, -(double)i / n);
+        double t = 1;
+        if (c.scaling == RPA_ROPE_LINEAR) t = 0;
+        if (c.scaling == RPA_ROPE_ROTATIONS)
+            t = std::fmin(std::fmax((c.trained_len * x / kTwoPi - c.low) / (c.high - c.low), 0.0), 1.0);
+        if (c.scaling == RPA_ROPE_INDEX) t = 1 - std::fmin(std::fmax((i - a) / std::fmax(b - a, 1e-3), 0.0), 1.0);
+        w[i] = x * t + x / c.factor * (1 - t);
+    }
+}
+
+}  // namespace
+}  // namespace rpa
+
+extern "C" {
+
+void rpa_rope_cfg_init(RpaRopeCfg* cfg) {
+    if (!cfg) return;
+    RpaCfg cache = cfg->cache;
+    rpa_cfg_init(&cache);
+    memset(cfg, 0, sizeof *cfg);
+    cfg->cache = cache;
+    cfg->rotary_dim = cache.head_dim;
+    cfg->base = 10000.0;
+    cfg->factor = 1.0;
+    cfg->low = 1.0;
+    cfg->high = 4.0;
+    cfg->magnitude = 1.0;
+}
+
+int rpa_rope_validate_cfg(const RpaRopeCfg* c) {
+    if (!c) return RPA_ERR_INVALID_ARG;
+    const int v = rpa_validate_cfg(&c->cache);
+    if (v != RPA_OK) return v;
+    if (c->pairing != RPA_ROPE_HALF && c->pairing != RPA_ROPE_INTERLEAVED) return RPA_ERR_INVALID_ARG;
+    if (c->scaling < RPA_ROPE_NONE || c->scaling > RPA_ROPE_INDEX) return RPA_ERR_INVALID_ARG;
+    if (c->reserved != 0) return RPA_ERR_INVALID_ARG;
+    if (!(std::isfinite(c->base) && c->base > 1.0)) return RPA_ERR_INVALID_ARG;
+    if (!std::isfinite(c->magnitude) || !std::isfinite((float)c->magnitude)) return RPA_ERR_INVALID_ARG;
+    if (c->scaling != RPA_ROPE_NONE && !(std::isfinite(c->factor) && c->factor >= 1.0)) return RPA_ERR_INVALID_ARG;
+    if (c->scaling == RPA_ROPE_ROTATIONS || c->scaling == RPA_ROPE_INDEX) {
+        if (!(std::isfinite(c->trained_len) && c->trained_len > 0)) return RPA_ERR_INVALID_ARG;
+        if (!(c->low > 0 && c->low < c->high && std::isfinite(c->high))) return RPA_ERR_INVALID_ARG;
+    }
+    if (c->rotary_dim < 1 || c->rotary_offset < 0 || c->rotary_dim > c->cache.head_dim ||
+        c->rotary_offset > c->cache.head_dim - c->rotary_dim)
+        return RPA_ERR_INVALID_ARG;
+    // a unit is eight pairs, in 16-byte vectors
+    if (c->rotary_dim % kUnit || c->rotary_offset % 8) return RPA_ERR_UNSUPPORTED;
+    // zero scales have no quotient
+    if ((c->cache.has_k_scale && c->cache.k_scale == 0.f) || (c->cache.has_v_scale && c->cache.v_scale == 0.f))
+        return RPA_ERR_INVALID_ARG;
+    return RPA_OK;
+}
+
+int rpa_rope_frequencies(const RpaRopeCfg* cfg, double* w) {
+    if (!w) return RPA_ERR_INVALID_ARG;
+    const int v = rpa_rope_validate_cfg(cfg);
+    if (v == RPA_OK) frequencies(*cfg, w);
+    return v;
+}
+
+int rpa_rope_create(const RpaRopeCfg* cfg, RpaRope** out) {
+    if (!out) return RPA_ERR_INVALID_ARG;
+    *out = nullptr;
+    const int v = rpa_rope_validate_cfg(cfg);
+    if (v != RPA_OK) return v;
+    RpaRope* h = new (std::nothrow) RpaRope;
+    if (!h) return RPA_ERR_CUDA;
+    memset(h, 0, sizeof *h);
+    h->cfg = *cfg;
+    // f_i = w_i / (2 pi) in units of 2^-64 turns (w_i <= 1 rad, so f_i < 2^62)
+    double w[kMaxPairs];
+    unsigned long long f[kMaxPairs + 1] = {};  // the status word behind them starts at 0
+    frequencies(*cfg, w);
+    const int n = (int)(cfg->rotary_dim / 2);
+    for (int i = 0; i < n; ++i) f[i] = (unsigned long long)std::ldexp(w[i] / kTwoPi, 64);
+    if (cudaGetDevice(&h->device) != cudaSuccess ||
+        cudaMalloc(&h->turns, (size_t)(n + 1) * sizeof f[0]) != cudaSuccess) {
+        cudaGetLastError();
+        delete h;
+        return RPA_ERR_CUDA;
+    }
+    if (cudaMemcpy(h->turns, f, (size_t)(n + 1) * sizeof f[0], cudaMemcpyHostToDevice) != cudaSuccess) {
+        cudaGetLastError();
+        cudaFree(h->turns);
+        delete h;
+        return RPA_ERR_CUDA;
+    }
+    h->status = reinterpret_cast<int*>(h->turns + n);
+    *out = h;
+    return RPA_OK;
+}
+
+int rpa_rope_append(RpaRope* h, const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                    int64_t v_stride, void* kv_pages, const int32_t* kv_lens, const int32_t* page_indices,
+                    const int32_t* cu_q_lens, const int32_t* positions, int32_t num_seqs, void* q_out, void* stream) {
+    if (!h) return RPA_ERR_INVALID_ARG;
+    const RpaCfg& c = h->cfg.cache;
+    const bool latent = c.kv_layout == RPA_KV_LATENT;
+    const int64_t eb = c.q_dtype == RPA_DT_F32 ? 4 : 2;
+    if (num_seqs < 0 || num_seqs > c.max_num_seqs) return RPA_ERR_INVALID_ARG;
+    if (!kv_pages || !kv_lens || !page_indices || !cu_q_lens) return RPA_ERR_INVALID_ARG;
+    if (latent ? v != nullptr : (c.num_q_tokens > 0 && !v)) return RPA_ERR_INVALID_ARG;
+    if (c.num_q_tokens > 0 && (!q || !k || !q_out)) return RPA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || !aligned(kv_pages, 16) ||
+        !aligned(kv_lens, 4) || !aligned(page_indices, 4) || !aligned(cu_q_lens, 4) || !aligned(positions, 4))
+        return RPA_ERR_INVALID_ARG;
+    const int64_t strides[3] = {q_stride, k_stride, latent ? c.num_kv_heads * c.head_dim : v_stride};
+    for (int i = 0; i < 3; ++i)
+        if (strides[i] < (i ? c.num_kv_heads : c.num_q_heads) * c.head_dim || strides[i] % (16 / eb) ||
+            strides[i] >= (int64_t)1 << 40)
+            return RPA_ERR_INVALID_ARG;
+    DeviceGuard g(h->device);
+    if (!g.ok) return RPA_ERR_CUDA;
+    RopeParams p;
+    p.q = static_cast<const uint8_t*>(q);
+    p.k = static_cast<const uint8_t*>(k);
+    p.v = static_cast<const uint8_t*>(v);
+    p.q_stride = (size_t)(strides[0] * eb);
+    p.k_stride = (size_t)(strides[1] * eb);
+    p.v_stride = (size_t)(strides[2] * eb);
+    p.q_out = static_cast<uint8_t*>(q_out);
+    p.kv = static_cast<uint8_t*>(kv_pages);
+    p.kv_lens = kv_lens;
+    p.page_indices = page_indices;
+    p.cu = cu_q_lens;
+    p.positions = positions;
+    p.turns = h->turns;
+    p.status = h->status;
+    p.S = num_seqs;
+    p.T = (int)c.num_q_tokens;
+    p.Hq = (int)c.num_q_heads;
+    p.Hkv = (int)c.num_kv_heads;
+    p.D = (int)c.head_dim;
+    p.ps = (int)c.page_size;
+    p.P = (int)c.pages_per_seq;
+    p.N = (int)c.total_num_pages;
+    p.latent = latent;
+    p.rd = (int)h->cfg.rotary_dim;
+    p.off = (int)h->cfg.rotary_offset;
+    p.rows = p.Hq + (latent ? 1 : 2) * p.Hkv;
+    p.per_row = p.D / kUnit;
+    p.row_step = (p.per_row == 36 ? 288 : 256) / p.per_row;
+    p.kt = c.kv_dtype == RPA_DT_F16 ? KT_F16 : c.kv_dtype == RPA_DT_FP8_E4M3 ? KT_E4M3
+         : c.kv_dtype == RPA_DT_FP8_E5M2 ? KT_E5M2 : c.kv_dtype == RPA_DT_INT8 ? KT_I8 : KT_BF16;
+    p.has_ks = c.has_k_scale;
+    p.has_vs = c.has_v_scale;
+    p.k_scale = c.k_scale;
+    p.v_scale = c.v_scale;
+    p.magnitude = (float)h->cfg.magnitude;
+    const int threads = p.per_row * p.row_step, half = h->cfg.pairing == RPA_ROPE_HALF;
+    const int grid = p.T > 0 ? p.T : 1;  // without tokens one CTA still checks the lengths
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = c.q_dtype == RPA_DT_F32   ? launch_rope<float>(p, half, grid, threads, st)
+                          : c.q_dtype == RPA_DT_F16 ? launch_rope<__half>(p, half, grid, threads, st)
+                                                    : launch_rope<__nv_bfloat16>(p, half, grid, threads, st);
+    if (e != cudaSuccess) {
+        cudaGetLastError();
+        return RPA_ERR_CUDA;
+    }
+    return RPA_OK;
+}
+
+int rpa_rope_get_status(RpaRope* h, void* stream) {
+    if (!h) return RPA_ERR_INVALID_ARG;
+    DeviceGuard g(h->device);
+    return g.ok ? take_status(h->status, static_cast<cudaStream_t>(stream)) : RPA_ERR_CUDA;
+}
+
+void rpa_rope_destroy(RpaRope* h) {
+    if (!h) return;
+    DeviceGuard g(h->device);
+    cudaFree(h->turns);
+    delete h;
+}
+
+}  // extern "C"
