@@ -358,6 +358,55 @@ int rpa_rope_append(RpaRope* h, const void* q, int64_t q_stride, const void* k, 
 int rpa_rope_get_status(RpaRope* h, void* stream);
 void rpa_rope_destroy(RpaRope* h);
 
+/* Eviction by accumulated attention weight.  scores: device, float32 [total_num_pages, Hkv, page_size],
+ * beside the cache: what each cached key of each kv head has received. */
+typedef struct RpaEvictCfg {
+    RpaCfg cache;     /* RPA_KV_SPLIT */
+    int64_t budget;   /* keys a sequence keeps, 1 .. pages_per_seq * page_size */
+    int64_t protect;  /* the first keys, never evicted */
+    int64_t recent;   /* the last keys, never evicted; protect + recent <= budget */
+    int64_t reserved; /* set to 0 */
+} RpaEvictCfg;
+
+typedef struct RpaEvict RpaEvict;
+/* Host only. */
+int rpa_evict_validate_cfg(const RpaEvictCfg* cfg);
+int rpa_evict_create(const RpaEvictCfg* cfg, RpaEvict** out);
+
+/* Add to scores the softmax weights (rpa_forward's: causal and window masks, soft cap, sinks in the
+ * denominator, k_scale) that the call's queries give each key they can see, summed over the query tokens
+ * of the sequence and the query heads of the kv head:
+ *   scores[page, h, slot] += sum over i, g of p(i, h, g, key)
+ * The keys of the call's own query tokens, the last q_len of each sequence, start from 0 instead of what
+ * scores held.  Sums in 32 bits, in a fixed order.  Keys that no query of the call sees keep their value.
+ * A page that two sequences share receives both sequences' weights in an order that is not fixed.
+ * Bad lengths: RPA_ERR_BAD_LENGTHS, scores unchanged; a bad page id: its keys are left out of the softmax
+ * (RPA_ERR_BAD_PAGE_INDEX). */
+int rpa_evict_accumulate(RpaEvict* h, const void* q, const void* kv_pages, const int32_t* kv_lens,
+                         const int32_t* page_indices, const int32_t* cu_q_lens, int32_t num_seqs, float* scores,
+                         void* stream);
+
+/* Cut every sequence longer than the budget to `budget` keys: of each kv head, the first `protect`, the
+ * last `recent`, and of the keys between those of the highest score (ties: the lowest slot; NaN below
+ * every number).  The kept keys' K/V rows and scores move, in order, to the first slots of the
+ * sequence's new pages.
+ *   new_page_indices  device, int32 [max_num_seqs, pages_per_seq].  page_indices itself: the cache is
+ *                     compacted in place.  Else each entry in use is the page of the same place in
+ *                     page_indices, or a page that no sequence of the call reads; no two sequences
+                     write one page (the first pages may stay shared where `protect` covers them whole).
+ *   new_kv_lens       device, int32 [max_num_seqs], written: min(kv_len, budget)  (may be kv_lens itself)
+ *   kept              device, int32 [max_num_seqs, Hkv, budget], or NULL; written: the slots kept, in order,
+ *                     -1 behind the last
+ * Slots behind the kept keys, and entries of new_kv_lens and kept of sequences >= num_seqs, are left as
+ * they were.  Bad lengths (kv_len < 0 or > pages_per_seq * page_size): RPA_ERR_BAD_LENGTHS, that sequence
+ * and its entries are left as they were.  A bad page id: its keys are neither read nor written
+ * (RPA_ERR_BAD_PAGE_INDEX), their scores count as NaN. */
+int rpa_evict_compact(RpaEvict* h, void* kv_pages, float* scores, const int32_t* kv_lens,
+                      const int32_t* page_indices, int32_t num_seqs, const int32_t* new_page_indices,
+                      int32_t* new_kv_lens, int32_t* kept, void* stream);
+int rpa_evict_get_status(RpaEvict* h, void* stream);
+void rpa_evict_destroy(RpaEvict* h);
+
 /* Static description of a status code. */
 const char* rpa_strerror(int code);
 

@@ -39,7 +39,9 @@ from .binding import (  # noqa: F401
     validate_cfg,
 )
 from .cache import (  # noqa: F401
+    CacheEviction,
     RopeAppend,
     rope_frequencies,
+    validate_evict_cfg,
     validate_rope_cfg,
 )

@@ -43,7 +43,9 @@ EXPORTS = ("rpa_cfg_init", "rpa_validate_cfg", "rpa_create", "rpa_forward", "rpa
            "rpa_get_status", "rpa_read_plan", "rpa_profile_begin", "rpa_profile_read", "rpa_set_option",
            "rpa_forward_noalloc", "rpa_destroy", "rpa_strerror", "rpa_version",
            "rpa_rope_cfg_init", "rpa_rope_validate_cfg", "rpa_rope_frequencies", "rpa_rope_create", "rpa_rope_append",
-           "rpa_rope_get_status", "rpa_rope_destroy")
+           "rpa_rope_get_status", "rpa_rope_destroy",
+           "rpa_evict_validate_cfg", "rpa_evict_create", "rpa_evict_accumulate", "rpa_evict_compact",
+           "rpa_evict_get_status", "rpa_evict_destroy")
 
 RPA_OPT_WAIT_TIMEOUT_MS = 1
 RPA_OPT_SERIAL = 2
@@ -78,6 +80,11 @@ class RpaRopeCfg(ctypes.Structure):
         ("factor", ctypes.c_double), ("trained_len", ctypes.c_double), ("low", ctypes.c_double),
         ("high", ctypes.c_double), ("magnitude", ctypes.c_double), ("reserved", ctypes.c_int64),
     ]
+
+
+class RpaEvictCfg(ctypes.Structure):
+    _fields_ = [("cache", RpaCfg), ("budget", ctypes.c_int64), ("protect", ctypes.c_int64), ("recent", ctypes.c_int64),
+                ("reserved", ctypes.c_int64)]
 
 
 class RpaError(RuntimeError):
@@ -141,6 +148,14 @@ def lib():
         L.rpa_rope_get_status.argtypes = [vp, vp]
         L.rpa_rope_destroy.argtypes = [vp]
         L.rpa_rope_destroy.restype = None
+        evictcfg = ctypes.POINTER(RpaEvictCfg)
+        L.rpa_evict_validate_cfg.argtypes = [evictcfg]
+        L.rpa_evict_create.argtypes = [evictcfg, ctypes.POINTER(vp)]
+        L.rpa_evict_accumulate.argtypes = [vp, vp, vp, vp, vp, vp, i32, vp, vp]
+        L.rpa_evict_compact.argtypes = [vp, vp, vp, vp, vp, i32, vp, vp, vp, vp]
+        L.rpa_evict_get_status.argtypes = [vp, vp]
+        L.rpa_evict_destroy.argtypes = [vp]
+        L.rpa_evict_destroy.restype = None
         _lib = L
     return _lib
 

@@ -13,8 +13,8 @@ import ctypes
 
 import numpy as np
 
-from .binding import (RPA_DT_BF16, RPA_DT_F16, RPA_DT_F32, RPA_KV_LATENT, RPA_OK, RpaError, RpaRopeCfg,
-                      lib, make_cfg)
+from .binding import (RPA_DT_BF16, RPA_DT_F16, RPA_DT_F32, RPA_KV_LATENT, RPA_OK, RpaError, RpaEvictCfg,
+                      RpaRopeCfg, lib, make_cfg)
 
 ROPE_PAIRINGS = {"half": 0, "interleaved": 1}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "rotations": 3, "index": 4}
@@ -202,3 +202,88 @@ class RopeAppend(_Handle):
                    page_indices.data_ptr(), cu_q_lens.data_ptr(), None if positions is None else positions.data_ptr(),
                    int(num_seqs), q_out.data_ptr(), self._stream(stream, *tensors))
         return q_out
+
+
+def make_evict_cfg(*, budget, protect=0, recent=0, **cfg) -> RpaEvictCfg:
+    c = RpaEvictCfg()
+    c.cache = make_cfg(**cfg)
+    c.budget, c.protect, c.recent = int(budget), int(protect), int(recent)
+    return c
+
+
+def validate_evict_cfg(**cfg) -> int:
+    """Host-only check of CacheEviction's keywords: the status code."""
+    return int(lib().rpa_evict_validate_cfg(ctypes.byref(make_evict_cfg(_host_ok=True, **cfg))))
+
+
+class CacheEviction(_Handle):
+    """Eviction from the paged cache by accumulated attention weight.
+
+    Keywords beside RaggedPagedAttention's: ``budget``, the keys a sequence keeps, of them the first
+    ``protect`` and the last ``recent`` always.  ``scores`` [total_num_pages, Hkv, page_size] float32 lies
+    beside kv_pages: ``accumulate`` adds to it, ``compact`` goes by it.
+    """
+
+    _prefix = "rpa_evict_"
+
+    def __init__(self, **cfg):
+        import torch
+
+        self._h = None
+        if isinstance(cfg.get("sinks"), np.ndarray):
+            cfg["sinks"] = torch.from_numpy(np.ascontiguousarray(cfg["sinks"], np.float32)).cuda()
+        self._sinks = cfg.get("sinks")  # read by every accumulate: kept alive
+        self._c = make_evict_cfg(**cfg)
+        self._create(self._c)
+        self._checks(self._c.cache)
+
+    def _check_accumulate(self, q, kv_pages, kv_lens, page_indices, cu_q_lens, scores):
+        import torch
+
+        self._need("q", q, self._q_dtype, self._q_shape)
+        self._need_cache(kv_pages)
+        self._need_lengths(kv_lens, page_indices, cu_q_lens)
+        self._need("scores", scores, torch.float32, self._scores_shape)
+
+    def accumulate(self, q, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, scores, stream=None):
+        """Add the softmax weight each key gets from the call's queries to ``scores``, and return it.  The keys of
+        the call's own tokens (each sequence's last q_len) start from 0."""
+        self._check_accumulate(q, kv_pages, kv_lens, page_indices, cu_q_lens, scores)
+        tensors = (q, kv_pages, kv_lens, page_indices, cu_q_lens, scores)
+        self._need_here(*tensors)
+        self._call("accumulate", q.data_ptr(), kv_pages.data_ptr(), kv_lens.data_ptr(), page_indices.data_ptr(),
+                   cu_q_lens.data_ptr(), int(num_seqs), scores.data_ptr(), self._stream(stream, *tensors))
+        return scores
+
+    def _check_compact(self, kv_pages, scores, kv_lens, page_indices, new_page_indices, new_kv_lens, kept):
+        import torch
+
+        self._need_cache(kv_pages)
+        self._need("scores", scores, torch.float32, self._scores_shape)
+        self._need_lengths(kv_lens, page_indices, None)
+        self._need("new_page_indices", new_page_indices, torch.int32, self._table_shape)
+        self._need("new_kv_lens", new_kv_lens, torch.int32, self._table_shape[:1])
+        if kept is not None:
+            self._need("kept", kept, torch.int32, (self._table_shape[0], self._c.cache.num_kv_heads, self._c.budget))
+
+    def compact(self, kv_pages, scores, kv_lens, page_indices, num_seqs, new_page_indices=None, new_kv_lens=None, kept=None,
+                stream=None):
+        """Cut every sequence to the budget and return its new length (new_kv_lens, int32 [max_num_seqs]).
+
+        The kept keys' rows and scores move, in order, to the first slots of new_page_indices' pages (default:
+        page_indices, in place).  ``kept`` (int32 [max_num_seqs, Hkv, budget]) receives the slots they had.
+        """
+        import torch
+
+        if new_page_indices is None:
+            new_page_indices = page_indices
+        if new_kv_lens is None:
+            with torch.cuda.stream(stream):
+                new_kv_lens = kv_lens.clone()
+        self._check_compact(kv_pages, scores, kv_lens, page_indices, new_page_indices, new_kv_lens, kept)
+        tensors = (kv_pages, scores, kv_lens, page_indices, new_page_indices, new_kv_lens, kept)
+        self._need_here(*tensors)
+        self._call("compact", kv_pages.data_ptr(), scores.data_ptr(), kv_lens.data_ptr(), page_indices.data_ptr(), int(num_seqs),
+                   new_page_indices.data_ptr(), new_kv_lens.data_ptr(), None if kept is None else kept.data_ptr(),
+                   self._stream(stream, *tensors))
+        return new_kv_lens
