@@ -358,6 +358,30 @@ int rpa_rope_append(RpaRope* h, const void* q, int64_t q_stride, const void* k, 
 int rpa_rope_get_status(RpaRope* h, void* stream);
 void rpa_rope_destroy(RpaRope* h);
 
+/* rpa_forward for batches whose sequences share their first keys: the prefix of a group of sequences is
+ * read once for all their query rows (tensor-core tiles of tokens x heads, split over the keys), the keys
+ * behind it by each sequence for itself, and the two are merged.  The result is rpa_forward's, to its
+ * tolerance.  RPA_KV_SPLIT, causal, without a sliding window (else RPA_ERR_UNSUPPORTED). */
+typedef struct RpaPrefix RpaPrefix;
+/* Host only; 1 <= max_groups <= max_num_seqs. */
+int rpa_prefix_validate_cfg(const RpaCfg* cfg, int64_t max_groups);
+int rpa_prefix_create(const RpaCfg* cfg, int64_t max_groups, RpaPrefix** out);
+/* As rpa_forward, with
+ *   cu_groups    device, int32 [max_groups + 1]: group g is the sequences [cu_groups[g], cu_groups[g + 1]);
+ *                cu_groups[0] = 0, cu_groups[num_groups] = num_seqs
+ *   prefix_lens  device, int32 [max_groups]: the group's sequences have their first prefix_lens[g] keys in
+ *                common (0: none).  They are read through page_indices of the group's first sequence;
+ *                the other sequences' page ids of whole prefix pages are not read.  At most
+ *                kv_len - q_len of each sequence with query tokens.
+ *   num_groups   host, 0 <= num_groups <= max_groups (0 only with num_seqs 0)
+ * Bad lengths or groups: RPA_ERR_BAD_LENGTHS, o all zero. */
+int rpa_prefix_forward(RpaPrefix* h, const void* q, const void* kv_pages, const int32_t* kv_lens,
+                       const int32_t* page_indices, const int32_t* cu_q_lens, int32_t num_seqs,
+                       const int32_t* cu_groups, const int32_t* prefix_lens, int32_t num_groups, void* o,
+                       void* stream);
+int rpa_prefix_get_status(RpaPrefix* h, void* stream);
+void rpa_prefix_destroy(RpaPrefix* h);
+
 /* Eviction by accumulated attention weight.  scores: device, float32 [total_num_pages, Hkv, page_size],
  * beside the cache: what each cached key of each kv head has received. */
 typedef struct RpaEvictCfg {

@@ -41,7 +41,9 @@ from .binding import (  # noqa: F401
 from .cache import (  # noqa: F401
     CacheEviction,
     RopeAppend,
+    SharedPrefixAttention,
     rope_frequencies,
     validate_evict_cfg,
+    validate_prefix_cfg,
     validate_rope_cfg,
 )

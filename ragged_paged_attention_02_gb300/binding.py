@@ -45,7 +45,9 @@ EXPORTS = ("rpa_cfg_init", "rpa_validate_cfg", "rpa_create", "rpa_forward", "rpa
            "rpa_rope_cfg_init", "rpa_rope_validate_cfg", "rpa_rope_frequencies", "rpa_rope_create", "rpa_rope_append",
            "rpa_rope_get_status", "rpa_rope_destroy",
            "rpa_evict_validate_cfg", "rpa_evict_create", "rpa_evict_accumulate", "rpa_evict_compact",
-           "rpa_evict_get_status", "rpa_evict_destroy")
+           "rpa_evict_get_status", "rpa_evict_destroy",
+           "rpa_prefix_validate_cfg", "rpa_prefix_create", "rpa_prefix_forward", "rpa_prefix_get_status",
+           "rpa_prefix_destroy")
 
 RPA_OPT_WAIT_TIMEOUT_MS = 1
 RPA_OPT_SERIAL = 2
@@ -156,6 +158,12 @@ def lib():
         L.rpa_evict_get_status.argtypes = [vp, vp]
         L.rpa_evict_destroy.argtypes = [vp]
         L.rpa_evict_destroy.restype = None
+        L.rpa_prefix_validate_cfg.argtypes = [ctypes.POINTER(RpaCfg), i64]
+        L.rpa_prefix_create.argtypes = [ctypes.POINTER(RpaCfg), i64, ctypes.POINTER(vp)]
+        L.rpa_prefix_forward.argtypes = [vp, vp, vp, vp, vp, vp, i32, vp, vp, i32, vp, vp]
+        L.rpa_prefix_get_status.argtypes = [vp, vp]
+        L.rpa_prefix_destroy.argtypes = [vp]
+        L.rpa_prefix_destroy.restype = None
         _lib = L
     return _lib
 

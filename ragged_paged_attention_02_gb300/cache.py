@@ -287,3 +287,57 @@ class CacheEviction(_Handle):
                    new_page_indices.data_ptr(), new_kv_lens.data_ptr(), None if kept is None else kept.data_ptr(),
                    self._stream(stream, *tensors))
         return new_kv_lens
+
+
+def validate_prefix_cfg(*, max_groups=1, **cfg) -> int:
+    """Host-only check of SharedPrefixAttention's keywords: the status code."""
+    return int(lib().rpa_prefix_validate_cfg(ctypes.byref(make_cfg(_host_ok=True, **cfg)), int(max_groups)))
+
+
+class SharedPrefixAttention(_Handle):
+    """RaggedPagedAttention for batches whose sequences share their first keys: a group's prefix is read once for
+    all of its query tokens.  Keywords beside RaggedPagedAttention's: ``max_groups``, the most groups of a call.
+    """
+
+    _prefix = "rpa_prefix_"
+
+    def __init__(self, *, max_groups=1, **cfg):
+        import torch
+
+        self._h = None
+        if isinstance(cfg.get("sinks"), np.ndarray):
+            cfg["sinks"] = torch.from_numpy(np.ascontiguousarray(cfg["sinks"], np.float32)).cuda()
+        self._sinks = cfg.get("sinks")  # read by every call: kept alive
+        self._c = make_cfg(**cfg)
+        self._max_groups = int(max_groups)
+        self._create(self._c, self._max_groups)
+        self._checks(self._c)
+
+    def _check(self, q, kv_pages, kv_lens, page_indices, cu_q_lens, cu_groups, prefix_lens, num_groups, out):
+        import torch
+
+        self._need("q", q, self._q_dtype, self._q_shape)
+        self._need("out", out, self._q_dtype, self._q_shape)
+        self._need_cache(kv_pages)
+        self._need_lengths(kv_lens, page_indices, cu_q_lens)
+        for name, t, n in (("cu_groups", cu_groups, num_groups + 1), ("prefix_lens", prefix_lens, num_groups)):
+            if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] < n or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous int32 tensor of at least {n}")
+
+    def forward(self, q, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, cu_groups, prefix_lens, num_groups, out=None,
+                stream=None):
+        """RaggedPagedAttention.forward's result.  Group g is the sequences [cu_groups[g], cu_groups[g + 1]), which have
+        their first prefix_lens[g] keys in common, read through the first one's page table."""
+        import torch
+
+        num_groups = int(num_groups)
+        if out is None:
+            with torch.cuda.stream(stream):
+                out = torch.empty(self._q_shape, dtype=self._q_dtype, device=q.device)
+        self._check(q, kv_pages, kv_lens, page_indices, cu_q_lens, cu_groups, prefix_lens, num_groups, out)
+        tensors = (q, kv_pages, kv_lens, page_indices, cu_q_lens, cu_groups, prefix_lens, out)
+        self._need_here(*tensors)
+        self._call("forward", q.data_ptr(), kv_pages.data_ptr(), kv_lens.data_ptr(), page_indices.data_ptr(), cu_q_lens.data_ptr(),
+                   int(num_seqs), cu_groups.data_ptr(), prefix_lens.data_ptr(), num_groups, out.data_ptr(),
+                   self._stream(stream, *tensors))
+        return out

@@ -138,7 +138,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kvmap, const CUte
             const int q_start = a.cu_q_lens[item.seq];
             const int ql = a.cu_q_lens[item.seq + 1] - q_start;
             const int kl = a.kv_lens[item.seq];
-            const int* ptab = a.page_indices + (size_t)item.seq * a.P;
+            const int* ptab = a.page_indices + (size_t)page_row(a, item.seq) * a.P;
             const int key0 = item.kv_begin - (item.kv_begin & (BR - 1));
             const int nst = (item.kv_end - key0 + kKS - 1) / kKS;
             // page ids of 32 consecutive logical pages, one per lane

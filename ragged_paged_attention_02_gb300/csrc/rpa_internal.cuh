@@ -161,9 +161,14 @@ struct AttnParams {
     float* part_o;         // [max_part, kDecRows, D]
     float* part_ml;        // [max_part, kDecRows, 2]
     const float* sinks;    // [Hq] sink logits (natural-log domain), or nullptr
+    const int* page_rows;  // row of page_indices of each sequence, or nullptr: its own number
     int odt;               // OutType of o
     int q_f16;             // 8-bit K/V: q holds f16 values (else bf16, rounded to f16 in the kernel)
 };
+
+__device__ __forceinline__ int page_row(const AttnParams& a, int seq) {
+    return a.page_rows ? __ldg(a.page_rows + seq) : seq;
+}
 
 struct DecParams {
     AttnParams a;
@@ -316,6 +321,12 @@ void kernels_capacity(const RpaCfg& c, KernelSet* ks);
 cudaError_t kernels_prepare(const RpaCfg& c, KernelSet* ks);
 size_t workspace_bytes(const RpaCfg& c, const KernelSet& ks);
 Workspace workspace_carve(const RpaCfg& c, const KernelSet& ks, void* base);
+// The attention kernels of one call, between its planner and its merge: enqueue the decode and prefill
+// kernels over the unit lists of ws, on eo.st (and eo.side).  a: the call's parameters from attn_params.
+AttnParams attn_params(const RpaCfg& c, const KernelSet& ks, const Workspace& ws, const void* q, const void* kv_pages,
+                       const int32_t* kv_lens, const int32_t* page_indices, const int32_t* cu_q_lens, void* o);
+int enqueue_attention(const RpaCfg& c, const KernelSet& ks, const Workspace& ws, MapCache* maps, const AttnParams& a,
+                      const EnqueueOpts& eo);
 // Enqueue one call; returns an RpaStatus.  Allocates nothing.
 int enqueue_forward(const RpaCfg& c, const KernelSet& ks, const Workspace& ws, MapCache* maps, const void* q,
                     const void* kv_pages, const int32_t* kv_lens, const int32_t* page_indices,
@@ -538,6 +549,12 @@ __device__ __forceinline__ void store_o4(uint8_t* o, size_t e, float a, float b,
         *reinterpret_cast<uint2*>(o + e * 2) = make_uint2(pack2<false>(a, b), pack2<false>(c, d));
     }
 }
+// Eight consecutive floats as they are: one 32-byte store, a whole sector a lane.
+__device__ __forceinline__ void store_f32x8(float* p, const uint32_t* v) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
 // Eight consecutive elements v[0..7] * s (e a multiple of 8).
 __device__ __forceinline__ void store_o8(uint8_t* o, size_t e, const uint32_t* v, float s, int odt) {
     float f[8];
@@ -561,6 +578,13 @@ __device__ __forceinline__ void store_o8(uint8_t* o, size_t e, const uint32_t* v
 // predecessor writes.  pdl_trigger() lets the next kernel start early.
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+
+// The plan of call `epoch` is complete (control words included): a decode kernel launched behind
+// the prefill kernel waits for this word instead of the planner grid.
+__device__ __forceinline__ void publish_epoch(int* ctrl, int epoch) {
+    __threadfence();
+    asm volatile("st.release.gpu.global.b32 [%0], %1;\n" ::"l"(ctrl + kPlanEpoch), "r"(epoch) : "memory");
+}
 
 __device__ __forceinline__ void set_status(int* ctrl, int code) {
     atomicCAS(ctrl + kStatus, 0, code);

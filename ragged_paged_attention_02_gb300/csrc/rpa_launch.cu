@@ -187,71 +187,10 @@ Workspace workspace_carve(const RpaCfg& c, const KernelSet& ks, void* base) {
     return w;
 }
 
-int enqueue_forward(const RpaCfg& c, const KernelSet& ks, const Workspace& ws, MapCache* maps, const void* q,
-                    const void* kv_pages, const int32_t* kv_lens, const int32_t* page_indices,
-                    const int32_t* cu_q_lens, int32_t num_seqs, void* o, const EnqueueOpts& eo) {
-    cudaStream_t st = eo.st;
-    const cudaEvent_t* ev = eo.ev;
-    auto rec = [&](int k, cudaStream_t on) { return !ev[k] || cudaEventRecord(ev[k], on) == cudaSuccess; };
-    const bool has_q = c.num_q_tokens > 0;
-    if (!rec(kEvStart, st)) return RPA_ERR_CUDA;
-    // q in the MMA operand type, when the caller's is another
-    const void* qk = q;
-    if (has_q && ks.q_conv) {
-        const size_t n = (size_t)c.num_q_tokens * c.num_q_heads * ks.D;
-        if (launch_q_convert(q, c.q_dtype, ws.qbuf, ks.q_conv_f16, n, Launch{ks.sms * 4, st}) != cudaSuccess)
-            return RPA_ERR_CUDA;
-        qk = ws.qbuf;
-    }
-
-    PlanParams pp;
-    pp.kv_lens = kv_lens;
-    pp.cu_q_lens = cu_q_lens;
-    pp.num_seqs = num_seqs;
-    pp.T = (int)c.num_q_tokens;
-    pp.Hkv = ks.Hp;
-    pp.G = ks.Gp;
-    pp.P = (int)c.pages_per_seq;
-    pp.ps = (int)c.page_size;
-    pp.causal = c.is_causal ? 1 : 0;
-    pp.has_window = c.has_sliding_window ? 1 : 0;
-    pp.window = ks.window;
-    pp.dec_rows = ks.dec_rows;
-    pp.pf_tokens = ks.pf_tokens;
-    pp.dec_slots = ks.sms * ks.dec_bps;
-    pp.concurrent = eo.conc;
-    pp.n_sms = ks.sms;
-    pp.dec_bps = ks.dec_bps;
-    pp.pf_bps = ks.pf_bps;
-    pp.pf_mma_rows = ks.tc ? 2 * kTcRows : ks.mla ? kMlaRows : kTcRows;
-    pp.dec_on_pf = ks.tc8 || ks.mla;
-    pp.D = ks.D;
-    pp.kv_elt = kt_8bit(ks.kt) ? 1 : 2;
-    pp.pf_sm_gflops = ks.mla ? kPfSmGflopsMma : kPfSmGflopsTc;
-    pp.dec_sm_gbs = kDecSmGBs;
-    pp.hbm_gbs = kHbmGBs;
-    pp.force_pf_sms = eo.force_pf_sms;
-    pp.force_dec_sms = eo.force_dec_sms;
-    pp.dec_waves = ks.tc8 ? kDecWavesTc8 : kDecWaves;
-    pp.epoch = eo.epoch;
-    pp.early = eo.plan_early;
-    pp.max_units = ks.max_units;
-    pp.max_dec_units = ks.max_dec_units;
-    pp.max_pf_units = ks.max_pf_units;
-    pp.max_part = ks.max_part;
-    pp.max_comb = ks.max_comb;
-    pp.ctrl = ws.ctrl;
-    pp.seq_scratch = ws.seq_scratch;
-    pp.units = ws.units;
-    pp.keys = nullptr;
-    pp.dec_units = ws.dec_units;
-    pp.pf_units = ws.pf_units;
-    pp.comb = ws.comb;
-    if (launch_plan(pp, st, plan_smem_bytes()) != cudaSuccess) return RPA_ERR_CUDA;
-    if (!rec(kEvPlanEnd, st)) return RPA_ERR_CUDA;
-
+AttnParams attn_params(const RpaCfg& c, const KernelSet& ks, const Workspace& ws, const void* q, const void* kv_pages,
+                       const int32_t* kv_lens, const int32_t* page_indices, const int32_t* cu_q_lens, void* o) {
     AttnParams ap;
-    ap.q = static_cast<const uint8_t*>(qk);
+    ap.q = static_cast<const uint8_t*>(q);
     ap.kv = static_cast<const uint8_t*>(kv_pages);
     ap.o = static_cast<uint8_t*>(o);
     ap.kv_lens = kv_lens;
@@ -281,8 +220,21 @@ int enqueue_forward(const RpaCfg& c, const KernelSet& ks, const Workspace& ws, M
     ap.part_o = ws.part_o;
     ap.part_ml = ws.part_ml;
     ap.sinks = c.has_sinks ? c.sinks : nullptr;
+    ap.page_rows = nullptr;
     ap.odt = ks.odt;
     ap.q_f16 = ks.q_f16;
+    return ap;
+}
+
+int enqueue_attention(const RpaCfg& c, const KernelSet& ks, const Workspace& ws, MapCache* maps, const AttnParams& a,
+                      const EnqueueOpts& eo) {
+    cudaStream_t st = eo.st;
+    const cudaEvent_t* ev = eo.ev;
+    auto rec = [&](int k, cudaStream_t on) { return !ev[k] || cudaEventRecord(ev[k], on) == cudaSuccess; };
+    const bool has_q = c.num_q_tokens > 0;
+    const void* qk = a.q;
+    const void* kv_pages = a.kv;
+    AttnParams ap = a;
 
     // With the side stream forked (concurrent decode / prefill while profiling), every return
     // joins it back (st waits for whatever was enqueued there), so that no kernel of this call is
@@ -395,6 +347,75 @@ int enqueue_forward(const RpaCfg& c, const KernelSet& ks, const Workspace& ws, M
     if (!rec(kEvPfEnd, st)) return fail(RPA_ERR_CUDA);
     if (one_stream && !launch_dec(st, eo.epoch)) return RPA_ERR_CUDA;
     if (!join()) return RPA_ERR_CUDA;
+    return RPA_OK;
+}
+
+int enqueue_forward(const RpaCfg& c, const KernelSet& ks, const Workspace& ws, MapCache* maps, const void* q,
+                    const void* kv_pages, const int32_t* kv_lens, const int32_t* page_indices,
+                    const int32_t* cu_q_lens, int32_t num_seqs, void* o, const EnqueueOpts& eo) {
+    cudaStream_t st = eo.st;
+    const cudaEvent_t* ev = eo.ev;
+    auto rec = [&](int k, cudaStream_t on) { return !ev[k] || cudaEventRecord(ev[k], on) == cudaSuccess; };
+    const bool has_q = c.num_q_tokens > 0;
+    if (!rec(kEvStart, st)) return RPA_ERR_CUDA;
+    // q in the MMA operand type, when the caller's is another
+    const void* qk = q;
+    if (has_q && ks.q_conv) {
+        const size_t n = (size_t)c.num_q_tokens * c.num_q_heads * ks.D;
+        if (launch_q_convert(q, c.q_dtype, ws.qbuf, ks.q_conv_f16, n, Launch{ks.sms * 4, st}) != cudaSuccess)
+            return RPA_ERR_CUDA;
+        qk = ws.qbuf;
+    }
+
+    PlanParams pp;
+    pp.kv_lens = kv_lens;
+    pp.cu_q_lens = cu_q_lens;
+    pp.num_seqs = num_seqs;
+    pp.T = (int)c.num_q_tokens;
+    pp.Hkv = ks.Hp;
+    pp.G = ks.Gp;
+    pp.P = (int)c.pages_per_seq;
+    pp.ps = (int)c.page_size;
+    pp.causal = c.is_causal ? 1 : 0;
+    pp.has_window = c.has_sliding_window ? 1 : 0;
+    pp.window = ks.window;
+    pp.dec_rows = ks.dec_rows;
+    pp.pf_tokens = ks.pf_tokens;
+    pp.dec_slots = ks.sms * ks.dec_bps;
+    pp.concurrent = eo.conc;
+    pp.n_sms = ks.sms;
+    pp.dec_bps = ks.dec_bps;
+    pp.pf_bps = ks.pf_bps;
+    pp.pf_mma_rows = ks.tc ? 2 * kTcRows : ks.mla ? kMlaRows : kTcRows;
+    pp.dec_on_pf = ks.tc8 || ks.mla;
+    pp.D = ks.D;
+    pp.kv_elt = kt_8bit(ks.kt) ? 1 : 2;
+    pp.pf_sm_gflops = ks.mla ? kPfSmGflopsMma : kPfSmGflopsTc;
+    pp.dec_sm_gbs = kDecSmGBs;
+    pp.hbm_gbs = kHbmGBs;
+    pp.force_pf_sms = eo.force_pf_sms;
+    pp.force_dec_sms = eo.force_dec_sms;
+    pp.dec_waves = ks.tc8 ? kDecWavesTc8 : kDecWaves;
+    pp.epoch = eo.epoch;
+    pp.early = eo.plan_early;
+    pp.max_units = ks.max_units;
+    pp.max_dec_units = ks.max_dec_units;
+    pp.max_pf_units = ks.max_pf_units;
+    pp.max_part = ks.max_part;
+    pp.max_comb = ks.max_comb;
+    pp.ctrl = ws.ctrl;
+    pp.seq_scratch = ws.seq_scratch;
+    pp.units = ws.units;
+    pp.keys = nullptr;
+    pp.dec_units = ws.dec_units;
+    pp.pf_units = ws.pf_units;
+    pp.comb = ws.comb;
+    if (launch_plan(pp, st, plan_smem_bytes()) != cudaSuccess) return RPA_ERR_CUDA;
+    if (!rec(kEvPlanEnd, st)) return RPA_ERR_CUDA;
+
+    const AttnParams ap = attn_params(c, ks, ws, qk, kv_pages, kv_lens, page_indices, cu_q_lens, o);
+    const int r = enqueue_attention(c, ks, ws, maps, ap, eo);
+    if (r != RPA_OK) return r;
 
     CombParams cp;
     cp.o = static_cast<uint8_t*>(o);

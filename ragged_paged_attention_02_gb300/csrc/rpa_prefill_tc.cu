@@ -50,7 +50,7 @@ constexpr int kProducer = 8, kMma = 9;
 constexpr int kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.f;  // rescale O when the row max grows by more than 2^8
 
-enum TcMeta : int { tSeq = 0, tHead, tQStart, tQl, tKl, tKvBegin, tKvEnd, tTok0, tNtok, tNt, tKey0, tStop };
+enum TcMeta : int { tSeq = 0, tHead, tQStart, tQl, tKl, tKvBegin, tKvEnd, tTok0, tNtok, tNt, tKey0, tStop, tPart };
 
 template <int D>
 struct TcGeom {
@@ -163,7 +163,7 @@ __global__ void __launch_bounds__(kThreads, 1) rpa_prefill_tc(const __grid_const
             const int q_start = a.cu_q_lens[item.seq];
             const int ql = a.cu_q_lens[item.seq + 1] - q_start;
             const int kl = a.kv_lens[item.seq];
-            const int* ptab = a.page_indices + (size_t)item.seq * a.P;
+            const int* ptab = a.page_indices + (size_t)page_row(a, item.seq) * a.P;
             const int key0 = item.kv_begin - (item.kv_begin & (BR - 1));
             const int nt = (item.kv_end - key0 + kBN - 1) / kBN;
             if (lane == 0) {
@@ -176,6 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1) rpa_prefill_tc(const __grid_const
                 meta[tKvEnd] = item.kv_end;
                 meta[tTok0] = item.tok0;
                 meta[tNtok] = item.ntok;
+                meta[tPart] = item.part;
                 meta[tNt] = nt;
                 meta[tKey0] = key0;
                 meta[tStop] = 0;
@@ -366,7 +367,7 @@ __global__ void __launch_bounds__(kThreads, 1) rpa_prefill_tc(const __grid_const
             const int stop = meta[tStop];
             const int head = meta[tHead], q_start = meta[tQStart], ql = meta[tQl], kl = meta[tKl];
             const int kv_begin = meta[tKvBegin], kv_end = meta[tKvEnd], tok0 = meta[tTok0];
-            const int ntok = meta[tNtok], nt = meta[tNt], key0 = meta[tKey0];
+            const int ntok = meta[tNtok], nt = meta[tNt], key0 = meta[tKey0], part = meta[tPart];
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&meta_free));
             if (stop) break;
@@ -535,6 +536,27 @@ __global__ void __launch_bounds__(kThreads, 1) rpa_prefill_tc(const __grid_const
             if (!mbar_wait(smem_u32(&o_full), items & 1u, ctrl, tmo)) break;
             tc_fence_after();
             const int rows_used = ntx * G;
+            if (part >= 0) {
+                // a piece of a shared prefix, or the keys behind one: the unnormalised O, the running max
+                // (log2 domain) and the row sum go to the 256 rows (16 slots) from slot `part` on
+                const size_t prow = (size_t)part * kDecRows + x * kM + r;
+#pragma unroll 1
+                for (int c = 0; c < D / 32; ++c) {
+                    uint32_t ov[32];
+                    tmem_ld32(lane_addr + Gm::TM_O(x) + c * 32, ov);
+                    tmem_ld_wait();
+                    if (r < rows_used) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) store_f32x8(a.part_o + prow * D + c * 32 + i * 8, ov + 8 * i);
+                    }
+                }
+                if (r < rows_used) *reinterpret_cast<float2*>(a.part_ml + prow * 2) = make_float2(m_run, l_run);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_u32(&o_free));
+                ++items;
+                continue;
+            }
             const int t_tok = q_start + ttok0 + r / G;
             const int qh = head * G + r % G;
             const float l_fin = add_sink(l_run, a.sinks, qh, m_run);  // P was taken relative to m_run

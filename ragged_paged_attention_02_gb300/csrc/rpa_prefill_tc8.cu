@@ -310,7 +310,7 @@ __global__ void __launch_bounds__(kRegBoundThreads, 1) rpa_prefill_tc8(const __g
             const int q_start = a.cu_q_lens[item.seq];
             const int ql = a.cu_q_lens[item.seq + 1] - q_start;
             const int kl = a.kv_lens[item.seq];
-            const int* ptab = a.page_indices + (size_t)item.seq * a.P;
+            const int* ptab = a.page_indices + (size_t)page_row(a, item.seq) * a.P;
             const int key0 = item.kv_begin - (item.kv_begin & (BR - 1));
             const int nt = (item.kv_end - key0 + kBN - 1) / kBN;
             if (lane == 0) {

@@ -1,0 +1,599 @@
+// rpa_prefix.cu -- attention of a batch whose sequences share their first keys (rpa_prefix_*).
+//
+// Softmax attention over keys A then B is the merge of the two partial results: with a part's maximum
+// m_i, sum l_i and unnormalised O_i,  o = sum 2^(m_i - M) O_i / sum 2^(m_i - M) l_i.  So a group's shared
+// keys can be attended by all of its query rows at once.  Decode on its own reads 2 D elements of every
+// key for G rows; here B sequences of a group make B G rows of one kv head, dense tiles for the tensor
+// cores, and the shared keys are read once a tile instead of once a sequence.
+//
+// The attention kernels are rpa_forward's, over another plan.  Every group becomes a virtual sequence:
+// its query tokens are neighbours in q, its keys are the prefix, all visible to all of its tokens.  Every
+// sequence stays one too, with the keys behind the prefix.  A virtual sequence with few rows (q_len * G of
+// a decode tile) becomes pieces of the decode kernel, one with more becomes tiles of the prefill kernel, a
+// prefix's tiles split over the keys as well.  Every item writes a partial; one merge takes each row's
+// partials from both sources.
+//
+// How many pieces a prefix is cut into: tiles x kv heads are few (a batch of 64 and 8 heads has 8), so
+// pieces fill the SMs; but each costs a pipeline ramp and 256 partial rows of D floats, written and read
+// back.  The planner takes the number of pieces that makes  waves x (keys of a piece + kPieceCost)  least.
+#include <string.h>
+
+#include <new>
+
+#include "rpa_block.cuh"
+
+namespace rpa {
+
+namespace {
+
+constexpr int kPieceAlign = 128;   // keys: the prefill kernels' tiles
+constexpr int kPieceCost = 256;    // what a piece costs beside its keys, in keys
+constexpr int kMaxPieces = 512;    // candidates, one a planner thread
+static_assert(kMaxPieces == kPlanThreads, "a candidate a thread");
+
+struct PrefixPlan {
+    const int *cu, *kv_lens, *cu_groups, *prefix_lens;
+    int S, NG, T, Hkv, G, P, ps;
+    int dec_rows, pf_tokens, pf_slots;  // rows of a decode tile; tokens and partial slots (of 16 rows) of a prefill tile
+    int concurrent, n_sms, dec_bps, pf_bps, pf_mma_rows, dec_on_pf, D, kv_elt, dec_waves;
+    int epoch;
+    int max_dec_units, max_pf_units, max_part, item_room;
+    int* ctrl;
+    // per virtual sequence: groups 0 .. NG - 1, an empty one, sequences NG + 1 ..
+    int *vcu, *vkv, *vrow, *vpart, *vpieces, *dec_end, *pf_end;
+    Unit *dec_units, *pf_units;
+};
+
+// The class of a virtual sequence: 0 no work, 1 decode pieces, 2 prefill tiles
+struct Virtual {
+    int q0, ql, begin, end, row, cls;
+};
+
+__device__ __forceinline__ Virtual virtual_seq(const PrefixPlan& p, int v) {
+    Virtual r;
+    if (v < p.NG) {
+        r.row = p.cu_groups[v];
+        r.q0 = p.cu[r.row];
+        r.ql = p.cu[p.cu_groups[v + 1]] - r.q0;
+        r.begin = 0;
+        r.end = p.prefix_lens[v];
+    } else if (v == p.NG) {
+        r.row = r.ql = r.begin = r.end = 0;
+        r.q0 = 0;
+    } else {
+        r.row = v - p.NG - 1;
+        r.q0 = p.cu[r.row];
+        r.ql = p.cu[r.row + 1] - r.q0;
+        r.begin = p.prefix_lens[upper_seq(p.cu_groups + 1, p.NG, r.row)];
+        r.end = p.kv_lens[r.row];
+    }
+    r.cls = r.ql == 0 || r.end <= r.begin ? 0 : (long long)r.ql * p.G <= p.dec_rows ? 1 : 2;
+    return r;
+}
+
+__global__ void __launch_bounds__(kPlanThreads, 1) rpa_prefix_plan_kernel(const PrefixPlan p) {
+    __shared__ int s_scan[33 * 3];
+    __shared__ unsigned long long s_red[64];
+    __shared__ int s_bad, s_longest;
+    const int tid = threadIdx.x, S = p.S, NG = p.NG, V = S > 0 ? NG + 1 + S : 0;
+    int* ctrl = p.ctrl;
+    const int Tq = p.pf_tokens;
+    pdl_trigger();
+    pdl_wait();
+    auto give_up = [&](int code) {  // no items; the merge writes zeros
+        if (tid == 0) {
+            for (int w = 1; w < kCtrlWords; ++w) ctrl[w] = 0;
+            ctrl[kNumComb] = -1;
+            set_status(ctrl, code);
+            publish_epoch(ctrl, p.epoch);
+        }
+    };
+    if (tid == 0) {
+        s_bad = NG > 0 ? p.cu_groups[0] != 0 || p.cu_groups[NG] != S : S != 0;
+        s_longest = 0;
+    }
+    __syncthreads();
+    // ---- 1. groups first (the sequences' checks look theirs up), then sequences
+    for (int g = tid; g < NG; g += kPlanThreads) {
+        const int a = p.cu_groups[g], b = p.cu_groups[g + 1], n = p.prefix_lens[g];
+        if (a < 0 || b < a || b > S || n < 0 || n > p.P * p.ps) s_bad = 1;
+    }
+    __syncthreads();
+    if (s_bad) {
+        give_up(RPA_ERR_BAD_LENGTHS);
+        return;
+    }
+    for (int s = tid; s < S; s += kPlanThreads) {
+        const int q0 = p.cu[s], q1 = p.cu[s + 1], kl = p.kv_lens[s], ql = q1 - q0;
+        if (q0 < 0 || ql < 0 || kl < 0 || kl > p.P * p.ps || ql > kl || q1 > p.T) s_bad = 1;
+        else if (ql > 0 && p.prefix_lens[upper_seq(p.cu_groups + 1, NG, s)] > kl - ql) s_bad = 1;
+    }
+    __syncthreads();
+    if (s_bad) {
+        give_up(RPA_ERR_BAD_LENGTHS);
+        return;
+    }
+    // ---- 2. work of the two kernels: key x kv head pairs of decode pieces, tile x key x kv head of prefill tiles
+    unsigned long long dec_keys = 0, pf_keys = 0;
+    for (int v = tid; v < V; v += kPlanThreads) {
+        const Virtual r = virtual_seq(p, v);
+        if (r.cls == 1) dec_keys += (unsigned long long)(r.end - r.begin) * p.Hkv;
+        if (r.cls == 2) {
+            pf_keys += (unsigned long long)((r.ql + Tq - 1) / Tq) * (unsigned long long)(r.end - r.begin) * p.Hkv;
+            if (v < NG) atomicMax(&s_longest, r.end);
+        }
+    }
+    block_sum64x2(dec_keys, pf_keys, s_red);
+    // ---- 3. SMs of each kernel (both at once: the split that ends them together), as rpa_forward's planner
+    int pf_ctas = p.n_sms * p.pf_bps, dec_ctas = p.n_sms * p.dec_bps;
+    if (p.concurrent && dec_keys && pf_keys) {
+        const unsigned long long bytes = dec_keys * (unsigned long long)(2 * p.D * p.kv_elt);
+        const unsigned long long flops = pf_keys * (unsigned long long)p.pf_mma_rows * (unsigned long long)(4 * p.D);
+        unsigned long long mine = ~0ull;
+        for (int x = 1 + tid; x < p.n_sms; x += kPlanThreads) {
+            const unsigned long long tp = flops / ((unsigned long long)x * kPfSmGflopsTc);
+            const unsigned long long td =
+                bytes / min((unsigned long long)kHbmGBs, (unsigned long long)(p.n_sms - x) * kDecSmGBs);
+            const unsigned long long k = (min(max(tp, td), (1ull << 47) - 1) << 16) | (unsigned long long)x;
+            mine = min(mine, k);
+        }
+        const int x = (int)(block_min64(mine, s_red) & 0xffffull);
+        pf_ctas = x * p.pf_bps;
+        dec_ctas = (p.n_sms - x) * p.dec_bps;
+    }
+    // ---- 4. keys of a decode piece, and of a piece of a prefix's tiles
+    const int on = p.dec_on_pf ? pf_ctas : dec_ctas;
+    unsigned long long want = dec_keys / (unsigned long long)max(1, p.dec_waves * on) + 1;
+    const int chunk = (int)min(max((want + kChunkAlign - 1) / kChunkAlign * kChunkAlign, (unsigned long long)kMinChunk), 1ull << 30);
+    int pf_chunk = kPieceAlign;
+    if (s_longest > 0) {
+        const int c = ((s_longest + tid) / (tid + 1) + kPieceAlign - 1) / kPieceAlign * kPieceAlign;
+        long long items = 0, least = 0;
+        for (int g = 0; g < NG; ++g) {
+            const Virtual r = virtual_seq(p, g);
+            if (r.cls != 2) continue;
+            const long long tiles = (long long)((r.ql + Tq - 1) / Tq) * p.Hkv;
+            items += tiles * ((r.end + c - 1) / c);
+            least += tiles;
+        }
+        const unsigned long long cost = (unsigned long long)((items + pf_ctas - 1) / pf_ctas) * (unsigned long long)(c + kPieceCost);
+        const unsigned long long k = tid > 0 && items > least + p.item_room ? ~0ull : (min(cost, (1ull << 47) - 1) << 16) | (unsigned long long)tid;
+        const int t = (int)(block_min64(k, s_red) & 0xffffull);
+        pf_chunk = ((s_longest + t) / (t + 1) + kPieceAlign - 1) / kPieceAlign * kPieceAlign;
+    }
+    // ---- 5. units and partial slots of each virtual sequence
+    int n_dec = 0, n_pf = 0, n_part = 0;
+    for (int base = 0; base < V; base += kPlanThreads) {
+        const int v = base + tid;
+        int add[3] = {0, 0, 0}, off[3], tot[3];
+        Virtual r;
+        r.cls = 0;
+        int pieces = 0;
+        if (v < V) {
+            r = virtual_seq(p, v);
+            if (r.cls == 1) {
+                pieces = (r.end - r.begin + chunk - 1) / chunk;
+                add[0] = pieces;
+                add[2] = pieces * p.Hkv;
+            } else if (r.cls == 2) {
+                pieces = v < NG ? (r.end + pf_chunk - 1) / pf_chunk : 1;
+                add[1] = (r.ql + Tq - 1) / Tq * pieces;
+                add[2] = add[1] * p.Hkv * p.pf_slots;
+            }
+        }
+        block_scan<3>(add, off, tot, s_scan);
+        if (v < V) {
+            p.vcu[v] = r.q0;
+            // the empty one's end is the last group's: the pair (v, v + 1) of every other is its tokens
+            if (v == NG) p.vcu[v] = p.cu[S];
+            if (v == V - 1) p.vcu[V] = p.cu[S];
+            // positions behind the prefix: a group's keys are visible to all of its tokens
+            p.vkv[v] = v < NG ? r.end + r.ql : r.end;
+            p.vrow[v] = r.row;
+            p.vpart[v] = n_part + off[2];
+            p.vpieces[v] = r.cls == 2 ? -pieces : pieces;
+            p.dec_end[v] = n_dec + off[0] + add[0];
+            p.pf_end[v] = n_pf + off[1] + add[1];
+        }
+        n_dec += tot[0];
+        n_pf += tot[1];
+        n_part += tot[2];
+    }
+    const int n_list = p.dec_on_pf ? n_pf + n_dec : n_pf;
+    if (n_dec > p.max_dec_units || n_list > p.max_pf_units || n_part > p.max_part) {
+        give_up(RPA_ERR_INVALID_ARG);  // cannot happen with the create-time sizing; refuse rather than overflow
+        return;
+    }
+    __syncthreads();
+    // ---- 6. the unit lists: prefix tiles first, a piece's tiles together (they share its keys)
+    for (int u = tid; u < n_dec + n_pf; u += kPlanThreads) {
+        const bool dec = u >= n_pf;
+        const int* ends = dec ? p.dec_end : p.pf_end;
+        const int x = dec ? u - n_pf : u;
+        const int v = upper_seq(ends, V, x);
+        const Virtual r = virtual_seq(p, v);
+        const int pieces = p.vpieces[v] < 0 ? -p.vpieces[v] : p.vpieces[v];
+        const int first = v > 0 ? ends[v - 1] : 0, k = x - first;
+        int4 a, b;
+        if (dec) {
+            const int kb = r.begin + k * chunk;
+            a = make_int4(v, 0, r.ql, kb);
+            b = make_int4(min(r.end, kb + chunk), p.vpart[v], k, pieces);
+        } else {
+            const int tiles = (r.ql + Tq - 1) / Tq, tile = k % tiles, piece = k / tiles;
+            const int t0 = tile * Tq, nt = min(Tq, r.ql - t0);
+            const int kb = v < NG ? piece * pf_chunk : r.begin;
+            const int ke = v < NG ? min(r.end, kb + pf_chunk) : min(r.end, r.end - r.ql + t0 + nt);
+            a = make_int4(v, t0, nt, kb);
+            b = make_int4(ke, p.vpart[v] + tile * p.Hkv * pieces * p.pf_slots, piece * p.pf_slots, pieces * p.pf_slots);
+        }
+        Unit* dst = dec && !p.dec_on_pf ? p.dec_units + x : p.pf_units + u;
+        reinterpret_cast<int4*>(dst)[0] = a;
+        reinterpret_cast<int4*>(dst)[1] = b;
+    }
+    __threadfence();
+    __syncthreads();
+    if (tid == 0) {
+        ctrl[kNumDecItems] = p.dec_on_pf ? 0 : n_dec * p.Hkv;
+        ctrl[kNumPfItems] = n_list * p.Hkv;
+        ctrl[kNumComb] = 0;
+        ctrl[kDecChunk] = chunk;
+        ctrl[kDecCounter] = 0;
+        ctrl[kPfCounter] = 0;
+        ctrl[kNumPart] = n_part;
+        ctrl[kNumUnits] = n_dec + n_pf;
+        ctrl[kPfCtas] = pf_ctas;
+        ctrl[kDecCtas] = dec_ctas;
+        publish_epoch(ctrl, p.epoch);
+    }
+}
+
+// ---------------------------------------------------------------- merge
+struct PrefixMerge {
+    uint8_t* o;
+    const int *cu, *cu_groups, *vcu, *vpart, *vpieces, *ctrl;
+    int S, NG, T, Hq, Hkv, G, D;
+    int pf_tokens, pf_slots;
+    int per_token;  // CTAs of a token
+    float v_scale;
+    const float* sinks;
+    int odt;
+    const float *part_o, *part_ml;
+};
+
+constexpr int kMergeThreads = 256;
+
+// A row's partials of one virtual sequence: row `row` of slots slot, slot + stride, ...
+struct Source {
+    int slot, stride, n, row;
+};
+__device__ __forceinline__ Source source(const PrefixMerge& p, int v, int t, int h, int g) {
+    Source r;
+    const int pieces = p.vpieces[v], tl = t - p.vcu[v];
+    r.n = pieces < 0 ? -pieces : pieces;
+    if (pieces >= 0) {
+        r.slot = p.vpart[v] + h * pieces;
+        r.stride = 1;
+        r.row = tl * p.G + g;
+    } else {
+        // a prefill tile: one or (16 slots) two halves of 128 rows
+        const int tile = tl / p.pf_tokens, tt = tl - tile * p.pf_tokens;
+        const int half_tokens = p.pf_slots == 16 ? p.pf_tokens / 2 : p.pf_tokens;
+        r.stride = p.pf_slots;
+        r.slot = p.vpart[v] + (tile * p.Hkv + h) * r.n * p.pf_slots;
+        r.row = tt / half_tokens * kTcRows + tt % half_tokens * p.G + g;
+    }
+    return r;
+}
+
+__global__ void __launch_bounds__(kMergeThreads, 4) rpa_prefix_merge_kernel(const PrefixMerge p) {
+    constexpr int kBatch = 6;  // partial O loads a lane has in flight
+    pdl_trigger();
+    pdl_wait();
+    const int lane = threadIdx.x & 31, t = blockIdx.x / p.per_token;
+    const int task = (blockIdx.x - t * p.per_token) * (kMergeThreads / 32) + (threadIdx.x >> 5);
+    const int quads = p.D / 4, chunks = (quads + 31) / 32;  // 128-column chunks of a row
+    if (task >= p.Hq * chunks) return;
+    const int qh = task / chunks, c4 = (task - qh * chunks) * 32 + lane;
+    const bool act = c4 < quads;
+    const int s = p.ctrl[kNumComb] < 0 ? -1 : find_seq(p.cu, p.S, t, lane);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    float inv = 0.f;
+    if (s >= 0) {
+        const int h = qh / p.G, g = qh - h * p.G;
+        const Source a = source(p, find_seq(p.cu_groups, p.NG, s, lane), t, h, g);
+        const Source b = source(p, p.NG + 1 + s, t, h, g);
+        const int n = a.n + b.n;
+        float M = -INFINITY, L = 0.f;
+        for (int k0 = 0; k0 < n; k0 += 32) {
+            // lane k: partial k0 + k
+            const int k = k0 + lane;
+            const bool in_a = k < a.n;
+            const size_t at = k < n ? (size_t)(in_a ? a.slot + k * a.stride : b.slot + (k - a.n) * b.stride) * kDecRows +
+                                          (in_a ? a.row : b.row)
+                                    : 0;
+            const float2 ml = k < n ? *reinterpret_cast<const float2*>(p.part_ml + at * 2) : make_float2(-INFINITY, 0.f);
+            float m = ml.x;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+            const float Mn = fmaxf(M, m), keep = M == -INFINITY ? 0.f : ex2(M - Mn);
+            // a part whose keys are all hidden has l = 0 and an O that may hold anything finite
+            const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - Mn);
+            float l = w * ml.y;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+            L = L * keep + l;
+            M = Mn;
+            acc.x *= keep; acc.y *= keep; acc.z *= keep; acc.w *= keep;
+            const int most = min(32, n - k0);
+            for (int j0 = 0; j0 < most; j0 += kBatch) {
+                float4 x[kBatch];
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    const unsigned long long from = __shfl_sync(0xffffffffu, (unsigned long long)at, (j0 + j) & 31);
+                    if (act && j0 + j < most) x[j] = *(reinterpret_cast<const float4*>(p.part_o + (size_t)from * p.D) + c4);
+                }
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    const float wj = __shfl_sync(0xffffffffu, w, (j0 + j) & 31);
+                    if (act && j0 + j < most) {
+                        acc.x += wj * x[j].x;
+                        acc.y += wj * x[j].y;
+                        acc.z += wj * x[j].z;
+                        acc.w += wj * x[j].w;
+                    }
+                }
+            }
+        }
+        L = add_sink(L, p.sinks, qh, M);
+        inv = L > 0.f ? p.v_scale / L : 0.f;
+        if (M == -INFINITY) acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    if (act)
+        store_o4(p.o, ((size_t)t * p.Hq + qh) * p.D + 4 * c4, acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv, p.odt);
+}
+
+}  // namespace
+}  // namespace rpa
+
+using namespace rpa;
+
+struct RpaPrefix {
+    RpaCfg cfg;
+    int64_t max_groups;
+    int device;
+    KernelSet ks;
+    MapCache maps;
+    void* ws;
+    Workspace w;
+    int pf_slots, item_room, max_dec_units, max_pf_units, max_part;
+    int *vcu, *vkv, *vrow, *vpart, *vpieces, *dec_end, *pf_end;
+    cudaStream_t side;
+    cudaEvent_t ev_plan, ev_dec;
+    int epoch;
+};
+
+namespace {
+
+void prefix_free(RpaPrefix* h) {
+    if (h->ev_dec) cudaEventDestroy(h->ev_dec);
+    if (h->ev_plan) cudaEventDestroy(h->ev_plan);
+    if (h->side) cudaStreamDestroy(h->side);
+    if (h->ws) cudaFree(h->ws);
+    delete h;
+}
+
+bool prefix_allocate(RpaPrefix* h) {
+    const RpaCfg& c = h->cfg;
+    KernelSet& ks = h->ks;
+    int sms = 0;
+    if (cudaGetDevice(&h->device) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess)
+        return false;
+    kernels_choose(c, sms, &ks);
+    if (kernels_prepare(c, &ks) != cudaSuccess) return false;
+    // worst cases.  Decode: a piece of each virtual sequence, and dec_waves pieces a CTA.  Prefill tiles: of T tokens
+    // and one part-empty tile a virtual sequence of that class (more than dec_rows rows), item_room pieces more
+    const int64_t S = c.max_num_seqs, T = c.num_q_tokens, Hkv = ks.Hp, NG = h->max_groups, Tq = ks.pf_tokens;
+    h->pf_slots = ks.tc ? 16 : 8;
+    h->item_room = 4 * sms * ks.pf_bps;
+    const int64_t big = T * ks.G / (ks.dec_rows + 1);  // sequences, or groups, of the prefill class
+    const int64_t group_tiles = T / Tq + (NG < big ? NG : big) + 1, seq_tiles = T / Tq + (S < big ? S : big) + 1;
+    const int64_t dec_units = S + NG + (kDecWaves * (int64_t)sms * ks.dec_bps + Hkv - 1) / Hkv + 1;
+    const int64_t pf_units = group_tiles + seq_tiles + h->item_room / Hkv + 1;
+    const int64_t part = dec_units * Hkv + (pf_units * Hkv + h->item_room) * h->pf_slots;
+    if (part >= ((int64_t)1 << 31) / kDecRows) return false;
+    h->max_dec_units = (int)dec_units;
+    h->max_pf_units = (int)(ks.tc8 ? pf_units + dec_units : pf_units);
+    h->max_part = (int)part;
+    const size_t V = (size_t)(NG + S + 2);
+    size_t off = 0;
+    auto take = [&](size_t bytes) {
+        const size_t at = off;
+        off = (off + bytes + 255) & ~(size_t)255;
+        return at;
+    };
+    const size_t o_ctrl = take(kCtrlWords * sizeof(int)), o_v = take(7 * V * sizeof(int)),
+                 o_dec = take((size_t)h->max_dec_units * sizeof(Unit)), o_pf = take((size_t)h->max_pf_units * sizeof(Unit)),
+                 o_po = take((size_t)part * kDecRows * ks.D * sizeof(float)), o_ml = take((size_t)part * kDecRows * 2 * sizeof(float)),
+                 o_q = take(ks.q_conv ? (size_t)T * c.num_q_heads * ks.D * 2 : 0);
+    if (cudaMalloc(&h->ws, off) != cudaSuccess) return false;
+    if (cudaMemset(h->ws, 0, kCtrlWords * sizeof(int)) != cudaSuccess) return false;
+    uint8_t* b = static_cast<uint8_t*>(h->ws);
+    h->w.ctrl = reinterpret_cast<int*>(b + o_ctrl);
+    h->w.dec_units = reinterpret_cast<Unit*>(b + o_dec);
+    h->w.pf_units = reinterpret_cast<Unit*>(b + o_pf);
+    h->w.part_o = reinterpret_cast<float*>(b + o_po);
+    h->w.part_ml = reinterpret_cast<float*>(b + o_ml);
+    h->w.qbuf = ks.q_conv ? b + o_q : nullptr;
+    int* v = reinterpret_cast<int*>(b + o_v);
+    int** parts[7] = {&h->vcu, &h->vkv, &h->vrow, &h->vpart, &h->vpieces, &h->dec_end, &h->pf_end};
+    for (int i = 0; i < 7; ++i) *parts[i] = v + (size_t)i * V;
+    return !ks.tc || (cudaStreamCreateWithFlags(&h->side, cudaStreamNonBlocking) == cudaSuccess &&
+                      cudaEventCreateWithFlags(&h->ev_plan, cudaEventDisableTiming) == cudaSuccess &&
+                      cudaEventCreateWithFlags(&h->ev_dec, cudaEventDisableTiming) == cudaSuccess);
+}
+
+}  // namespace
+
+extern "C" {
+
+int rpa_prefix_validate_cfg(const RpaCfg* cfg, int64_t max_groups) {
+    const int v = rpa_validate_cfg(cfg);
+    if (v != RPA_OK) return v;
+    if (max_groups < 1 || max_groups > cfg->max_num_seqs) return RPA_ERR_INVALID_ARG;
+    if (cfg->kv_layout != RPA_KV_SPLIT || !cfg->is_causal || cfg->has_sliding_window) return RPA_ERR_UNSUPPORTED;
+    // positions of a group's tokens behind its prefix, and rows of the virtual batch, in 32 bits
+    if (cfg->pages_per_seq * cfg->page_size + cfg->num_q_tokens >= (int64_t)1 << 31 ||
+        cfg->num_q_tokens * cfg->num_q_heads >= (int64_t)1 << 31)
+        return RPA_ERR_UNSUPPORTED;
+    return RPA_OK;
+}
+
+int rpa_prefix_create(const RpaCfg* cfg, int64_t max_groups, RpaPrefix** out) {
+    if (!out) return RPA_ERR_INVALID_ARG;
+    *out = nullptr;
+    const int v = rpa_prefix_validate_cfg(cfg, max_groups);
+    if (v != RPA_OK) return v;
+    RpaPrefix* h = new (std::nothrow) RpaPrefix;
+    if (!h) return RPA_ERR_CUDA;
+    memset(h, 0, sizeof *h);
+    h->cfg = *cfg;
+    h->max_groups = max_groups;
+    if (!prefix_allocate(h)) {
+        cudaGetLastError();
+        prefix_free(h);
+        return RPA_ERR_CUDA;
+    }
+    *out = h;
+    return RPA_OK;
+}
+
+int rpa_prefix_forward(RpaPrefix* h, const void* q, const void* kv_pages, const int32_t* kv_lens,
+                       const int32_t* page_indices, const int32_t* cu_q_lens, int32_t num_seqs, const int32_t* cu_groups,
+                       const int32_t* prefix_lens, int32_t num_groups, void* o, void* stream) {
+    if (!h) return RPA_ERR_INVALID_ARG;
+    const RpaCfg& c = h->cfg;
+    const KernelSet& ks = h->ks;
+    if (num_seqs < 0 || num_seqs > c.max_num_seqs) return RPA_ERR_INVALID_ARG;
+    if (num_groups < 0 || num_groups > h->max_groups || (num_groups == 0 && num_seqs > 0)) return RPA_ERR_INVALID_ARG;
+    if (!kv_pages || !kv_lens || !page_indices || !cu_q_lens || !cu_groups || !prefix_lens) return RPA_ERR_INVALID_ARG;
+    if (c.num_q_tokens > 0 && (!q || !o)) return RPA_ERR_INVALID_ARG;
+    if (!aligned(q, 16) || !aligned(o, 16) || !aligned(kv_pages, 16) || !aligned(kv_lens, 4) || !aligned(page_indices, 4) ||
+        !aligned(cu_q_lens, 4) || !aligned(cu_groups, 4) || !aligned(prefix_lens, 4))
+        return RPA_ERR_INVALID_ARG;
+    DeviceGuard g(h->device);
+    if (!g.ok) return RPA_ERR_CUDA;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const void* qk = q;
+    if (c.num_q_tokens > 0 && ks.q_conv) {
+        const size_t n = (size_t)c.num_q_tokens * c.num_q_heads * ks.D;
+        if (launch_q_convert(q, c.q_dtype, h->w.qbuf, ks.q_conv_f16, n, Launch{ks.sms * 4, st}) != cudaSuccess) {
+            cudaGetLastError();
+            return RPA_ERR_CUDA;
+        }
+        qk = h->w.qbuf;
+    }
+    EnqueueOpts eo;
+    memset(&eo, 0, sizeof eo);
+    eo.st = st;
+    eo.conc = ks.tc;
+    eo.side = h->side;
+    eo.ev_plan = h->ev_plan;
+    eo.ev_dec = h->ev_dec;
+    eo.timeout_ns = 1000000000ull;
+    eo.epoch = h->epoch = (h->epoch + 1) & 0x7FFFFFFF;
+    PrefixPlan p;
+    p.cu = cu_q_lens;
+    p.kv_lens = kv_lens;
+    p.cu_groups = cu_groups;
+    p.prefix_lens = prefix_lens;
+    p.S = num_seqs;
+    p.NG = num_groups;
+    p.T = (int)c.num_q_tokens;
+    p.Hkv = ks.Hp;
+    p.G = ks.G;
+    p.P = (int)c.pages_per_seq;
+    p.ps = (int)c.page_size;
+    p.dec_rows = ks.dec_rows;
+    p.pf_tokens = ks.pf_tokens;
+    p.pf_slots = h->pf_slots;
+    p.concurrent = eo.conc;
+    p.n_sms = ks.sms;
+    p.dec_bps = ks.dec_bps;
+    p.pf_bps = ks.pf_bps;
+    p.pf_mma_rows = ks.tc ? 2 * kTcRows : kTcRows;
+    p.dec_on_pf = ks.tc8;
+    p.D = ks.D;
+    p.kv_elt = kt_8bit(ks.kt) ? 1 : 2;
+    p.dec_waves = ks.tc8 ? kDecWavesTc8 : kDecWaves;
+    p.epoch = eo.epoch;
+    p.max_dec_units = h->max_dec_units;
+    p.max_pf_units = h->max_pf_units;
+    p.max_part = h->max_part;
+    p.item_room = h->item_room;
+    p.ctrl = h->w.ctrl;
+    p.vcu = h->vcu;
+    p.vkv = h->vkv;
+    p.vrow = h->vrow;
+    p.vpart = h->vpart;
+    p.vpieces = h->vpieces;
+    p.dec_end = h->dec_end;
+    p.pf_end = h->pf_end;
+    p.dec_units = h->w.dec_units;
+    p.pf_units = h->w.pf_units;
+    if (launch_pdl(rpa_prefix_plan_kernel, 1, kPlanThreads, 0, st, p) != cudaSuccess) {
+        cudaGetLastError();
+        return RPA_ERR_CUDA;
+    }
+    AttnParams ap = attn_params(c, ks, h->w, qk, kv_pages, h->vkv, page_indices, h->vcu, o);
+    ap.page_rows = h->vrow;
+    const int r = enqueue_attention(c, ks, h->w, &h->maps, ap, eo);
+    if (r != RPA_OK) {
+        cudaGetLastError();
+        return r;
+    }
+    if (c.num_q_tokens == 0) return RPA_OK;
+    PrefixMerge m;
+    m.o = static_cast<uint8_t*>(o);
+    m.cu = cu_q_lens;
+    m.cu_groups = cu_groups;
+    m.vcu = h->vcu;
+    m.vpart = h->vpart;
+    m.vpieces = h->vpieces;
+    m.ctrl = h->w.ctrl;
+    m.S = num_seqs;
+    m.NG = num_groups;
+    m.T = (int)c.num_q_tokens;
+    m.Hq = (int)c.num_q_heads;
+    m.Hkv = ks.Hp;
+    m.G = ks.G;
+    m.D = ks.D;
+    m.pf_tokens = ks.pf_tokens;
+    m.pf_slots = h->pf_slots;
+    m.per_token = (m.Hq * ((m.D + 127) / 128) + kMergeThreads / 32 - 1) / (kMergeThreads / 32);
+    m.v_scale = ks.v_scale;
+    m.sinks = ap.sinks;
+    m.odt = ks.odt;
+    m.part_o = h->w.part_o;
+    m.part_ml = h->w.part_ml;
+    if (launch_pdl(rpa_prefix_merge_kernel, m.T * m.per_token, kMergeThreads, 0, st, m) != cudaSuccess) {
+        cudaGetLastError();
+        return RPA_ERR_CUDA;
+    }
+    return RPA_OK;
+}
+
+int rpa_prefix_get_status(RpaPrefix* h, void* stream) {
+    if (!h) return RPA_ERR_INVALID_ARG;
+    DeviceGuard g(h->device);
+    return g.ok ? take_status(h->w.ctrl + kStatus, static_cast<cudaStream_t>(stream)) : RPA_ERR_CUDA;
+}
+
+void rpa_prefix_destroy(RpaPrefix* h) {
+    if (!h) return;
+    DeviceGuard g(h->device);
+    prefix_free(h);
+}
+
+}  // extern "C"
