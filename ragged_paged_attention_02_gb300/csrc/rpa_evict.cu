@@ -3,13 +3,16 @@
 //
 // Two launches:
 //
-//   select   a CTA per (sequence, kv head).  The keys between the protected first and the recent last
-//            ones compete for the budget's other places: the k-th largest score by a radix select over
-//            the scores as ordered integers (three digits of 11, 11 and 10 bits, a shared-memory
-//            histogram each: the first digit holds the sign, the exponent and two bits of the mantissa,
-//            so that scores of all sizes spread over its bins), then one ordered pass that lists the
-//            kept slots.  Each warp lists a run of neighbouring keys, so that one scan over the warps
-//            gives every warp its place and its share of the ties, which go to the lowest slots.
+//   select   a cluster of 1 to 8 CTAs per (sequence, kv head).  The keys between the protected first and
+//            the recent last ones compete for the budget's other places: the k-th largest score by a radix
+//            select over the scores as ordered integers (three digits of 11, 11 and 10 bits, a histogram in
+//            shared memory each; the first digit holds the sign, the exponent and two bits of the mantissa,
+//            so that scores of all sizes spread over its bins).  Each CTA keeps the scores of its share of
+//            the keys in shared memory, and adds up all CTAs' histograms for itself through distributed
+//            shared memory.  Then one ordered pass lists the kept slots: each warp lists a run of
+//            neighbouring keys, so that one scan over the warps and CTAs gives every warp its place and its
+//            share of the ties, which go to the lowest slots.  Bound by its rounds of waits (three digits,
+//            a few microseconds each), so a cluster is as large as leaves no SM without one.
 //   move     blocks of 64 kept rows: K and V of a head are neighbours in a slot, one copy of 2 D
 //            elements a row.  Bound by reading and writing those rows.  Onto fresh pages all blocks are
 //            independent.  Where the new pages hold other kept rows (in place), a sequence's head is
@@ -27,10 +30,12 @@ namespace rpa {
 
 namespace {
 
-constexpr int kSelThreads = 1024;
+constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kSelCached = 40 * 1024;  // scores a CTA keeps at most (160 KB); further ones are read again
 constexpr int kMoveThreads = 256;
+constexpr int kMoveCtas = 4;  // resident an SM
 constexpr int kMoveRows = 64;
 
 // A score as an integer of the same order; NaN lowest, -0 as +0
@@ -40,35 +45,77 @@ __device__ __forceinline__ uint32_t ordered(float x) {
     return (u & 0x80000000u) ? ~u : u | 0x80000000u;
 }
 
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;\n" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;\n" ::: "memory");
+}
+// Two words of CTA `rank`'s shared memory, at the place that `addr` has in this CTA's
+__device__ __forceinline__ uint2 cluster_load2(uint32_t addr, uint32_t rank) {
+    uint32_t at;
+    uint2 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(at) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+    return v;
+}
+// Exclusive sum of v over the block's threads before this one, and the total
+__device__ __forceinline__ uint32_t block_before(uint32_t v, uint32_t* s_warp, uint32_t& total) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t sum = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += y;
+    }
+    if (lane == 31) s_warp[warp] = sum;
+    __syncthreads();
+    uint32_t w = lane < kSelWarps ? s_warp[lane] : 0u;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, w, o);
+        if (lane >= o) w += y;
+    }
+    total = __shfl_sync(0xffffffffu, w, 31);
+    const uint32_t before = __shfl_sync(0xffffffffu, w, (warp + 31) & 31);
+    return sum - v + (warp > 0 ? before : 0u);
+}
+
 __global__ void __launch_bounds__(kSelThreads) rpa_evict_select_kernel(const CompactParams p) {
-    extern __shared__ uint32_t s_key[];  // [cached] the first competing keys' scores
-    __shared__ uint32_t s_hist[kBins];
-    __shared__ uint32_t s_warp[kSelWarps][2];
+    extern __shared__ uint32_t s_key[];  // [cached] the scores of the first of this CTA's competing keys
+    __shared__ __align__(16) uint32_t s_hist[2][kBins];
+    __shared__ uint32_t s_warp[kSelWarps], s_warp2[kSelWarps];
+    __shared__ __align__(8) uint32_t s_count[2];  // of this CTA: keys above the threshold, keys equal to it
     __shared__ uint32_t s_digit, s_left;
     __shared__ int s_order;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int s = blockIdx.x / p.Hkv, h = blockIdx.x - s * p.Hkv;
+    const int C = p.cluster, rank = (int)cluster_rank(), unit = blockIdx.x / C;
+    const int s = unit / p.Hkv, h = unit - s * p.Hkv;
     pdl_trigger();
     pdl_wait();
     const int n = p.kv_lens[s];
-    if (n < 0 || n > p.P * p.ps) {
+    const bool first = rank == 0 && h == 0;
+    if (n < 0 || n > p.P * p.ps) {  // the whole cluster leaves
         if (tid == 0) {
             set_status(p.status, RPA_ERR_BAD_LENGTHS);
-            if (h == 0) p.seq_n[s] = -1;
+            if (first) p.seq_n[s] = -1;
         }
         return;
     }
     const int* table = p.page_indices + (size_t)s * p.P;
     const int kept = min(n, p.budget);
     int* list = p.list + ((size_t)s * p.Hkv + h) * p.budget;
-    if (h == 0) {
-        // rows on pages that stay where they are: in order, unless those pages are protected whole or nothing moves
+    const int step = C * kSelThreads, me = rank * kSelThreads + tid;  // of the cluster's threads
+    if (first) {
+        // rows on pages that stay where they are move in order, unless those pages are protected whole or nothing moves
         if (tid == 0) s_order = 0;
         __syncthreads();
         if (n > p.budget) {
-            const int first = p.protect / p.ps, pages = (kept + p.ps - 1) / p.ps;
+            const int from = p.protect / p.ps, pages = (kept + p.ps - 1) / p.ps;
             const int* to = p.new_pages + (size_t)s * p.P;
-            for (int i = first + tid; i < pages; i += kSelThreads)
+            for (int i = from + tid; i < pages; i += kSelThreads)
                 if (table[i] == to[i]) s_order = 1;
         }
         __syncthreads();
@@ -78,16 +125,20 @@ __global__ void __launch_bounds__(kSelThreads) rpa_evict_select_kernel(const Com
         }
     }
     if (p.fill)
-        for (int i = kept + tid; i < p.budget; i += kSelThreads) list[i] = -1;
+        for (int i = kept + me; i < p.budget; i += step) list[i] = -1;
     if (n <= p.budget) {
-        for (int i = tid; i < n; i += kSelThreads) list[i] = i;
+        for (int i = me; i < n; i += step) list[i] = i;
         return;
     }
-    // the competing keys [protect, protect + m) and their places
+    for (int i = me; i < p.protect; i += step) list[i] = i;
+    for (int i = me; i < p.recent; i += step) list[p.budget - p.recent + i] = n - p.recent + i;
+    // the competing keys [protect, protect + m) and their places; this CTA's share [a, b) of them
     const int m = n - p.protect - p.recent;
     const uint32_t k = (uint32_t)(p.budget - p.protect - p.recent);
-    auto score = [&](int i) -> uint32_t {  // of competing key i
-        const int j = p.protect + i, lp = p.page.div(j), pg = __ldg(table + lp);
+    if (k == 0) return;
+    const int share = (m + C - 1) / C, a = min(m, rank * share), b = min(m, a + share), mine = b - a;
+    auto score = [&](int i) -> uint32_t {  // of this CTA's key i
+        const int j = p.protect + a + i, lp = p.page.div(j), pg = __ldg(table + lp);
         if ((unsigned)pg >= (unsigned)p.N) {
             set_status(p.status, RPA_ERR_BAD_PAGE_INDEX);
             return 0u;
@@ -95,54 +146,72 @@ __global__ void __launch_bounds__(kSelThreads) rpa_evict_select_kernel(const Com
         return ordered(p.scores[((size_t)pg * p.Hkv + h) * p.ps + (j - lp * p.ps)]);
     };
     auto key = [&](int i) { return i < p.cached ? s_key[i] : score(i); };
-    for (int i = tid; i < min(m, p.cached); i += kSelThreads) s_key[i] = score(i);
-    // the k-th largest key: digit by digit, the prefix found so far and how many are still wanted below it
-    uint32_t prefix = 0, left = k;
-    if (k > 0) {
-#pragma unroll
-        for (int d = 0; d < 3; ++d) {
-            const int shift = d == 0 ? 21 : d == 1 ? 10 : 0, bits = d == 2 ? 10 : 11;
-            for (int i = tid; i < kBins; i += kSelThreads) s_hist[i] = 0;
-            __syncthreads();
-            for (int i = tid; i < m; i += kSelThreads) {
-                const uint32_t u = key(i);
-                if (d == 0 || (u >> (shift + bits)) == prefix) atomicAdd(&s_hist[(u >> shift) & ((1u << bits) - 1)], 1u);
-            }
-            __syncthreads();
-            // thread t: bins kBins - 1 - 2t and the one below; an inclusive scan from the highest bin down
-            const int b0 = kBins - 1 - 2 * tid;
-            const uint32_t c0 = s_hist[b0], c1 = s_hist[b0 - 1];
-            uint32_t sum = c0 + c1;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const uint32_t y = __shfl_up_sync(0xffffffffu, sum, o);
-                if (lane >= o) sum += y;
-            }
-            if (lane == 31) s_warp[warp][0] = sum;
-            __syncthreads();
-            uint32_t before = 0;
-            for (int w = 0; w < warp; ++w) before += s_warp[w][0];
-            const uint32_t above = before + sum - c0 - c1;  // keys in higher bins
-            if (above < left && left <= above + c0) {
-                s_digit = (uint32_t)b0;
-                s_left = left - above;
-            } else if (above + c0 < left && left <= above + c0 + c1) {
-                s_digit = (uint32_t)b0 - 1;
-                s_left = left - above - c0;
-            }
-            __syncthreads();
-            prefix = (prefix << bits) | s_digit;
-            left = s_left;
-        }
-    } else {
-        prefix = 0xffffffffu;  // above every score: none competes
-    }
-    // list the kept slots in order: protected, keys above the threshold and the first `left` that equal it, recent
-    for (int i = tid; i < p.protect; i += kSelThreads) list[i] = i;
-    for (int i = tid; i < p.recent; i += kSelThreads) list[p.budget - p.recent + i] = n - p.recent + i;
-    const int run = ((m + kSelWarps - 1) / kSelWarps + 31) & ~31, lo = min(m, warp * run), hi = min(m, lo + run);
-    uint32_t gt = 0, eq = 0;
+    // the first digit's histogram while the scores come in
+    for (int i = tid; i < kBins; i += kSelThreads) s_hist[0][i] = 0;
     __syncthreads();
+    constexpr int kFly = 4;
+    for (int i0 = tid; i0 < mine; i0 += kFly * kSelThreads) {
+        uint32_t u[kFly];
+#pragma unroll
+        for (int f = 0; f < kFly; ++f) {
+            const int i = i0 + f * kSelThreads;
+            u[f] = i < mine ? score(i) : 0u;
+        }
+#pragma unroll
+        for (int f = 0; f < kFly; ++f) {
+            const int i = i0 + f * kSelThreads;
+            if (i < mine) {
+                if (i < p.cached) s_key[i] = u[f];
+                atomicAdd(&s_hist[0][u[f] >> 21], 1u);
+            }
+        }
+    }
+    // the k-th largest key: digit by digit, the prefix found so far and how many are still wanted at and below it
+    uint32_t prefix = 0, left = k;
+#pragma unroll
+    for (int d = 0; d < 3; ++d) {
+        const int shift = d == 0 ? 21 : d == 1 ? 10 : 0, bits = d == 2 ? 10 : 11;
+        uint32_t* hist = s_hist[d & 1];
+        if (d > 0) {
+            // (every CTA has read this half's last histogram before the barrier of the digit in between)
+            for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
+            __syncthreads();
+            for (int i = tid; i < mine; i += kSelThreads) {
+                const uint32_t u = key(i);
+                if ((u >> (shift + bits)) == prefix) atomicAdd(&hist[(u >> shift) & ((1u << bits) - 1)], 1u);
+            }
+        }
+        cluster_sync();
+        // thread t: bins kBins - 1 - 4 t down to kBins - 4 - 4 t, over all CTAs
+        constexpr int kMine = kBins / kSelThreads;
+        static_assert(kMine == 4, "two 8-byte loads a CTA");
+        const int low = kBins - kMine * (tid + 1);
+        uint32_t c[kMine] = {0, 0, 0, 0};
+        const uint32_t at = smem_u32(hist + low);
+        for (int r = 0; r < C; ++r) {
+            const uint2 x = cluster_load2(at, r), y = cluster_load2(at + 8, r);
+            c[3] += x.x;
+            c[2] += x.y;
+            c[1] += y.x;
+            c[0] += y.y;  // the highest of the four
+        }
+        uint32_t total, above = block_before(c[0] + c[1] + c[2] + c[3], s_warp, total);
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+            if (above < left && left <= above + c[i]) {
+                s_digit = (uint32_t)(low + kMine - 1 - i);
+                s_left = left - above;
+            }
+            above += c[i];
+        }
+        __syncthreads();
+        prefix = (prefix << bits) | s_digit;
+        left = s_left;
+        __syncthreads();  // s_digit, s_left and s_warp are free again
+    }
+    // list the kept slots in order: keys above the threshold and the first `left` that equal it
+    const int run = ((mine + kSelWarps - 1) / kSelWarps + 31) & ~31, lo = min(mine, warp * run), hi = min(mine, lo + run);
+    uint32_t gt = 0, eq = 0;
     for (int i = lo + lane; i < hi; i += 32) {
         const uint32_t u = key(i);
         gt += u > prefix;
@@ -150,56 +219,48 @@ __global__ void __launch_bounds__(kSelThreads) rpa_evict_select_kernel(const Com
     }
     gt = __reduce_add_sync(0xffffffffu, gt);
     eq = __reduce_add_sync(0xffffffffu, eq);
-    if (lane == 0) {
-        s_warp[warp][0] = gt;
-        s_warp[warp][1] = eq;
+    uint32_t all_gt, all_eq;
+    uint32_t g0 = block_before(lane == 0 ? gt : 0u, s_warp, all_gt), e0 = block_before(lane == 0 ? eq : 0u, s_warp2, all_eq);
+    g0 = __shfl_sync(0xffffffffu, g0, 0);
+    e0 = __shfl_sync(0xffffffffu, e0, 0);
+    if (tid == 0) {
+        s_count[0] = all_gt;
+        s_count[1] = all_eq;
     }
-    __syncthreads();
-    uint32_t g0 = 0, e0 = 0;
-    for (int w = 0; w < warp; ++w) {
-        g0 += s_warp[w][0];
-        e0 += s_warp[w][1];
+    cluster_sync();
+    for (int r = 0; r < rank; ++r) {
+        const uint2 v = cluster_load2(smem_u32(s_count), r);
+        g0 += v.x;
+        e0 += v.y;
     }
-    if (k == 0) return;
     for (int i = lo; i < hi; i += 32) {
         const bool in = i + lane < hi;
         const uint32_t u = in ? key(i + lane) : 0u;
-        const uint32_t mg = __ballot_sync(0xffffffffu, in && u > prefix), me = __ballot_sync(0xffffffffu, in && u == prefix);
+        const uint32_t mg = __ballot_sync(0xffffffffu, in && u > prefix), me_ = __ballot_sync(0xffffffffu, in && u == prefix);
         const uint32_t below = (1u << lane) - 1u;
-        const uint32_t e = e0 + __popc(me & below);
+        const uint32_t e = e0 + __popc(me_ & below);
         if (in && (u > prefix || (u == prefix && e < left)))
-            list[p.protect + g0 + __popc(mg & below) + min(e, left)] = p.protect + i + lane;
+            list[p.protect + g0 + __popc(mg & below) + min(e, left)] = p.protect + a + i + lane;
         g0 += __popc(mg);
-        e0 += __popc(me);
+        e0 += __popc(me_);
     }
+    cluster_sync();  // no CTA leaves while another may read its counts
 }
 
-// Where kept row i of (s, h) comes from and goes to: slots of the cache (page * page_size + place), -1: no move
-__device__ __forceinline__ void route(const CompactParams& p, int s, int h, int i, const int* list, long long& from, long long& to) {
-    const int j = list[i];
-    const int a = p.page.div(j), b = p.page.div(i);
-    const int pa = __ldg(p.page_indices + (size_t)s * p.P + a), pb = __ldg(p.new_pages + (size_t)s * p.P + b);
-    from = (long long)pa * p.ps + (j - a * p.ps);
-    to = (long long)pb * p.ps + (i - b * p.ps);
-    if ((unsigned)pa >= (unsigned)p.N || (unsigned)pb >= (unsigned)p.N) {
-        set_status(p.status, RPA_ERR_BAD_PAGE_INDEX);
-        to = -1;
-    }
-    if (from == to) to = -1;
-}
-
-__global__ void __launch_bounds__(kMoveThreads) rpa_evict_move_kernel(const CompactParams p) {
-    __shared__ long long s_from[kMoveRows], s_to[kMoveRows];
+__global__ void __launch_bounds__(kMoveThreads, kMoveCtas) rpa_evict_move_kernel(const CompactParams p) {
+    __shared__ long long s_from[kMoveRows], s_to[kMoveRows];  // first 16-byte vectors of the rows; s_to -1: no move
     const int tid = threadIdx.x;
     pdl_trigger();
     pdl_wait();
     const int blocks = (p.budget + kMoveRows - 1) / kMoveRows;
-    const long long items = (long long)p.S * p.Hkv * blocks;
-    const int vecs = p.row_bytes / 16;  // 16-byte vectors of a row: 8, 16, 32 or 64
+    const int items = p.S * p.Hkv * blocks;
+    const int vshift = p.vec_shift, vecs = 1 << vshift;  // 16-byte vectors of a row: 8, 16, 32 or 64
     const int slot_vecs = vecs * p.Hkv;
     uint4* kv = reinterpret_cast<uint4*>(p.kv);
-    for (long long it = blockIdx.x; it < items; it += gridDim.x) {
-        const int h = (int)(it % p.Hkv), b = (int)(it / p.Hkv % blocks), s = (int)(it / p.Hkv / blocks);
+    constexpr int kFly = 8;
+    const int sub = min(kMoveRows, kFly * kMoveThreads >> vshift);  // rows whose vectors the CTA's registers hold at once
+    for (int it = blockIdx.x; it < items; it += gridDim.x) {
+        const int h = it % p.Hkv, b = it / p.Hkv % blocks, s = it / p.Hkv / blocks;
         const int kept = p.seq_n[s];
         if (kept < 0) continue;
         if (b == 0 && h == 0 && tid == 0) p.new_kv_lens[s] = kept;
@@ -210,70 +271,83 @@ __global__ void __launch_bounds__(kMoveThreads) rpa_evict_move_kernel(const Comp
         for (int i0 = b * kMoveRows; i0 < end; i0 += kMoveRows) {
             const int rows = min(kMoveRows, end - i0);
             float sc = 0.f;
+            float* sc_to = nullptr;
             __syncthreads();
             if (tid < kMoveRows) {
                 long long from = 0, to = -1;
-                if (tid < rows) route(p, s, h, i0 + tid, list, from, to);
+                if (tid < rows) {
+                    const int i = i0 + tid, j = list[i], pj = p.page.div(j), pi = p.page.div(i);
+                    const int pa = __ldg(p.page_indices + (size_t)s * p.P + pj), pb = __ldg(p.new_pages + (size_t)s * p.P + pi);
+                    if ((unsigned)pa >= (unsigned)p.N || (unsigned)pb >= (unsigned)p.N) {
+                        set_status(p.status, RPA_ERR_BAD_PAGE_INDEX);
+                    } else {
+                        const int at = j - pj * p.ps, bt = i - pi * p.ps;
+                        from = ((long long)pa * p.ps + at) * slot_vecs + h * vecs;
+                        to = ((long long)pb * p.ps + bt) * slot_vecs + h * vecs;
+                        if (from == to) {
+                            to = -1;
+                        } else {
+                            sc = p.scores[((size_t)pa * p.Hkv + h) * p.ps + at];
+                            sc_to = p.scores + ((size_t)pb * p.Hkv + h) * p.ps + bt;
+                        }
+                    }
+                }
                 s_from[tid] = from;
                 s_to[tid] = to;
-                if (to >= 0) {
-                    const long long a = from / p.ps;
-                    sc = p.scores[((size_t)a * p.Hkv + h) * p.ps + (from - a * p.ps)];
-                }
             }
             __syncthreads();
-            // 64 rows of up to 64 vectors: 16 a thread at most, eight in flight
-            constexpr int kFly = 8;
-            const int total = rows * vecs;
-            if (!order) {
-                for (int v0 = tid; v0 < total; v0 += kFly * kMoveThreads) {
-                    uint4 x[kFly];
+            // `sub` rows at a time, eight vectors a thread in flight; in order, all are read before any is written
+            for (int r0 = 0; r0 < rows; r0 += sub) {
+                const int first = r0 << vshift, total = min(rows, r0 + sub) << vshift;
+                uint4 x[kFly];
 #pragma unroll
-                    for (int f = 0; f < kFly; ++f) {
-                        const int v = v0 + f * kMoveThreads, r = v / vecs;
-                        if (v < total && s_to[r] >= 0) x[f] = kv[(size_t)s_from[r] * slot_vecs + h * vecs + (v - r * vecs)];
-                    }
-#pragma unroll
-                    for (int f = 0; f < kFly; ++f) {
-                        const int v = v0 + f * kMoveThreads, r = v / vecs;
-                        if (v < total && s_to[r] >= 0) kv[(size_t)s_to[r] * slot_vecs + h * vecs + (v - r * vecs)] = x[f];
-                    }
+                for (int f = 0; f < kFly; ++f) {
+                    const int v = first + tid + f * kMoveThreads, r = v >> vshift;
+                    if (v < total && s_to[r] >= 0) x[f] = __ldcs(kv + s_from[r] + (v & (vecs - 1)));
                 }
-            } else {
-                // the whole block is read before any of it is written
-                uint4 x[2 * kFly];
+                if (order) __syncthreads();
 #pragma unroll
-                for (int f = 0; f < 2 * kFly; ++f) {
-                    const int v = tid + f * kMoveThreads, r = v / vecs;
-                    if (v < total && s_to[r] >= 0) x[f] = kv[(size_t)s_from[r] * slot_vecs + h * vecs + (v - r * vecs)];
+                for (int f = 0; f < kFly; ++f) {
+                    const int v = first + tid + f * kMoveThreads, r = v >> vshift;
+                    if (v < total && s_to[r] >= 0) __stcs(kv + s_to[r] + (v & (vecs - 1)), x[f]);
                 }
-                __syncthreads();
-#pragma unroll
-                for (int f = 0; f < 2 * kFly; ++f) {
-                    const int v = tid + f * kMoveThreads, r = v / vecs;
-                    if (v < total && s_to[r] >= 0) kv[(size_t)s_to[r] * slot_vecs + h * vecs + (v - r * vecs)] = x[f];
-                }
+                if (order) __syncthreads();
             }
-            if (tid < rows && s_to[tid] >= 0) {
-                const long long a = s_to[tid] / p.ps;
-                p.scores[((size_t)a * p.Hkv + h) * p.ps + (s_to[tid] - a * p.ps)] = sc;
-            }
+            if (sc_to) *sc_to = sc;
         }
     }
 }
 
 }  // namespace
 
-// Shared memory of select: the scores of up to max_keys competing keys, as many as fit (40 k)
-cudaError_t compact_prepare(int max_keys, int* cached) {
-    *cached = max_keys < 40 * 1024 ? max_keys : 40 * 1024;
-    return cudaFuncSetAttribute(rpa_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 40 * 1024 * 4);
+// Clusters and shared memory of select for `units` (sequence, kv head) pairs of up to max_keys competing keys
+cudaError_t compact_prepare(int64_t units, int max_keys, int sms, int* cluster, int* cached) {
+    // as many CTAs a unit as two an SM allow, of 2 k keys at least
+    int c = 1;
+    while (c < 8 && units * (2 * c) <= 2 * sms && max_keys / (2 * c) >= 2048) c *= 2;
+    *cluster = c;
+    const int share = (max_keys + c - 1) / c;
+    *cached = share < kSelCached ? share : kSelCached;
+    return cudaFuncSetAttribute(rpa_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelCached * 4);
 }
 
 cudaError_t launch_compact(const CompactParams& p, int sms, cudaStream_t st) {
     if (p.S == 0) return cudaSuccess;
-    cudaError_t e = launch_pdl(rpa_evict_select_kernel, p.S * p.Hkv, kSelThreads, (size_t)p.cached * 4, st, p);
-    if (e == cudaSuccess) e = launch_pdl(rpa_evict_move_kernel, sms * 8, kMoveThreads, 0, st, p);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.S * p.Hkv * p.cluster);
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = (size_t)p.cached * 4;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = p.cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, rpa_evict_select_kernel, p);
+    if (e == cudaSuccess) e = launch_pdl(rpa_evict_move_kernel, sms * kMoveCtas, kMoveThreads, 0, st, p);
     return e;
 }
 
@@ -285,8 +359,10 @@ struct RpaEvict {
     RpaEvictCfg cfg;
     int device, sms;
     KernelSet ks;      // element types and scales of the attention of `cfg.cache`
-    int weigh_bps;     // resident stats CTAs an SM
-    int cached;
+    int stats_bps, weigh_bps;  // resident CTAs an SM of the two weight kernels
+    CUtensorMap kmap;  // K rows of the cache of the last call
+    const void* kmap_ptr;
+    int cluster, cached;  // of select
     void* ws;
     int* status;
     WeighParams w;     // workspace pointers and constants
@@ -298,7 +374,7 @@ struct RpaEvict {
 namespace {
 
 constexpr long long kMostLogits = 1ll << 28;  // floats: 1 GiB
-constexpr int kMostPieces = 64;
+constexpr int kMostPieces = 128;
 
 }  // namespace
 
@@ -313,9 +389,11 @@ int rpa_evict_validate_cfg(const RpaEvictCfg* c) {
     if (c->protect < 0 || c->recent < 0 || c->protect > c->budget || c->recent > c->budget - c->protect)
         return RPA_ERR_INVALID_ARG;
     if (c->cache.kv_layout != RPA_KV_SPLIT) return RPA_ERR_UNSUPPORTED;
-    // 32-bit row numbers, and grids of a CTA for each sequence and kv head
-    if (c->cache.num_q_tokens * (c->cache.num_q_heads / c->cache.num_kv_heads) >= (int64_t)1 << 31 ||
-        c->cache.max_num_seqs * c->cache.num_kv_heads >= (int64_t)1 << 31)
+    // 32-bit numbers of rows, slots, grids' CTAs and blocks of kept keys
+    const int64_t lim = (int64_t)1 << 31, units = c->cache.max_num_seqs * c->cache.num_kv_heads;
+    if (c->cache.num_q_tokens * (c->cache.num_q_heads / c->cache.num_kv_heads) >= lim ||
+        c->cache.total_num_pages >= lim / c->cache.page_size || units >= lim / 8 ||
+        units >= lim / ((c->budget + kMoveRows - 1) / kMoveRows))
         return RPA_ERR_UNSUPPORTED;
     return RPA_OK;
 }
@@ -338,8 +416,8 @@ int rpa_evict_create(const RpaEvictCfg* cfg, RpaEvict** out) {
     }
     kernels_choose(c, h->sms, &h->ks);
     const int64_t max_keys = c.pages_per_seq * c.page_size;
-    if (weigh_prepare(h->ks.D, h->ks.kt, &h->weigh_bps) != cudaSuccess || h->weigh_bps < 1 ||
-        compact_prepare((int)max_keys, &h->cached) != cudaSuccess) {
+    if (weigh_prepare(h->ks.D, h->ks.kt, &h->stats_bps, &h->weigh_bps) != cudaSuccess || h->stats_bps < 1 || h->weigh_bps < 1 ||
+        compact_prepare(c.max_num_seqs * c.num_kv_heads, (int)max_keys, h->sms, &h->cluster, &h->cached) != cudaSuccess) {
         cudaGetLastError();
         delete h;
         return RPA_ERR_CUDA;
@@ -350,7 +428,7 @@ int rpa_evict_create(const RpaEvictCfg* cfg, RpaEvict** out) {
     int64_t pieces = ((int64_t)1 << 20) / blocks;
     pieces = pieces < 1 ? 1 : pieces > kMostPieces ? kMostPieces : pieces;
     const int64_t small_rows = rows + S < S * kWeighRows ? rows + S : S * kWeighRows;
-    double most = (double)small_rows * (double)Hkv * (double)max_keys;
+    double most = (double)small_rows * (double)Hkv * (double)max_keys + 4.0 * (double)S;
     if (most > (double)kMostLogits) most = (double)kMostLogits;
     size_t off = 0;
     auto take = [&](size_t bytes) {
@@ -360,7 +438,7 @@ int rpa_evict_create(const RpaEvictCfg* cfg, RpaEvict** out) {
     };
     const size_t o_status = take(4), o_ctrl = take(16), o_stat0 = take((S + 1) * 4), o_item0 = take((S + 1) * 4),
                  o_block0 = take((S + 1) * 4), o_logit0 = take(S * 8), o_done = take(blocks * 4),
-                 o_part = take((size_t)blocks * pieces * kWeighRows * 8), o_stat = take((size_t)blocks * kWeighRows * 8),
+                 o_part = take((size_t)blocks * pieces * 4 * kWeighRows * 8), o_stat = take((size_t)blocks * kWeighRows * 4),
                  o_logits = take((size_t)most * 4), o_n = take(S * 4), o_order = take(S * 4),
                  o_list = take((size_t)S * Hkv * cfg->budget * 4),
                  o_q = take(h->ks.q_conv ? (size_t)c.num_q_tokens * c.num_q_heads * c.head_dim * 2 : 0);
@@ -402,7 +480,10 @@ int rpa_evict_create(const RpaEvictCfg* cfg, RpaEvict** out) {
     w.page.set((uint32_t)w.ps);
     w.group.set((uint32_t)w.G);
     w.max_pieces = (int)pieces;
-    w.target = 4 * h->sms * h->weigh_bps;
+    w.ctas = h->sms * h->stats_bps;
+    w.BR = h->ks.BR;
+    w.br_shift = h->ks.br_shift;
+    w.all_runs = (1u << (64 / w.BR)) - 1u;
     w.max_logits = (long long)most;
     w.status = h->status;
     w.ctrl = reinterpret_cast<int*>(b + o_ctrl);
@@ -412,7 +493,7 @@ int rpa_evict_create(const RpaEvictCfg* cfg, RpaEvict** out) {
     w.logit0 = reinterpret_cast<long long*>(b + o_logit0);
     w.done = reinterpret_cast<int*>(b + o_done);
     w.part = reinterpret_cast<float2*>(b + o_part);
-    w.stat = reinterpret_cast<float2*>(b + o_stat);
+    w.stat = reinterpret_cast<float*>(b + o_stat);
     w.logits = reinterpret_cast<float*>(b + o_logits);
     *out = h;
     return RPA_OK;
@@ -448,7 +529,13 @@ int rpa_evict_accumulate(RpaEvict* h, const void* q, const void* kv_pages, const
         }
         p.q = h->qbuf;
     }
-    if (launch_weigh(p, h->ks.kt, h->sms * h->weigh_bps, st) != cudaSuccess) {
+    if (h->kmap_ptr != kv_pages) {
+        h->kmap_ptr = nullptr;
+        if (encode_k_map(&h->kmap, kv_pages, p.D * (kt_8bit(h->ks.kt) ? 1 : 2), c.total_num_pages, p.ps, p.Hkv, p.BR) != 0)
+            return RPA_ERR_INVALID_ARG;
+        h->kmap_ptr = kv_pages;
+    }
+    if (launch_weigh(h->kmap, p, h->ks.kt, h->sms * h->weigh_bps, st) != cudaSuccess) {
         cudaGetLastError();
         return RPA_ERR_CUDA;
     }
@@ -484,10 +571,13 @@ int rpa_evict_compact(RpaEvict* h, void* kv_pages, float* scores, const int32_t*
     p.ps = (int)c.page_size;
     p.P = (int)c.pages_per_seq;
     p.N = (int)c.total_num_pages;
-    p.row_bytes = (int)(2 * c.head_dim * (kt_8bit(h->ks.kt) ? 1 : 2));
+    const int vecs = (int)(2 * c.head_dim * (kt_8bit(h->ks.kt) ? 1 : 2) / 16);
+    p.vec_shift = 0;
+    while (1 << p.vec_shift < vecs) ++p.vec_shift;
     p.budget = (int)h->cfg.budget;
     p.protect = (int)h->cfg.protect;
     p.recent = (int)h->cfg.recent;
+    p.cluster = h->cluster;
     p.cached = h->cached;
     p.page.set((uint32_t)p.ps);
     if (launch_compact(p, h->sms, static_cast<cudaStream_t>(stream)) != cudaSuccess) {

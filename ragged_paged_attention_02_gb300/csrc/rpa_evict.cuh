@@ -22,8 +22,9 @@ struct FastDiv {
 
 // ---------------------------------------------------------------- accumulated weights
 constexpr int kWeighRows = 16;     // query rows (tokens x heads of a group) of a block
-constexpr int kWeighAlign = 128;   // pieces are multiples of this many keys (a 16-key tile for each of 8 warps)
-constexpr int kWeighThreads = 256;
+constexpr int kWeighAlign = 128;   // pieces are multiples of this many keys
+constexpr int kWeighKeys = 128;    // keys of a weigh item
+constexpr int kWeighThreads = 128;
 
 struct WeighParams {
     const uint8_t* q;        // in the MMA operand type, or bf16 with q_bf16
@@ -39,18 +40,20 @@ struct WeighParams {
     const float* sinks;
     FastDiv page, group;
     int max_pieces;          // most pieces of a sequence
-    int target;              // items wanted
+    int ctas;                // of the stats kernel (all resident)
+    int BR, br_shift;        // keys of a copied page run: gcd(page_size, 64), and its log2
+    uint32_t all_runs;       // a bit for each run of 64 keys
     long long max_logits;    // floats the logit buffer holds
     // workspace
     int* status;             // sticky
-    int* ctrl;               // [0] stat items, [1] weight items, [2] chunk (keys)
+    int* ctrl;               // [0] stat items, [1] weigh items, [2] stat items taken
     int* stat0;              // [S + 1] first stat item of a sequence
-    int* item0;              // [S + 1] first weight item
+    int* item0;              // [S + 1] first weigh item
     int* block0;             // [S + 1] first row block (counting kv heads)
     long long* logit0;       // [S] first float of the sequence's logits, or -1: they are computed again
-    int* done;               // [blocks] pieces of a row block whose statistics are out
-    float2* part;            // [blocks, max_pieces, kWeighRows] maximum (log2) and sum of a piece
-    float2* stat;            // [blocks, kWeighRows] maximum (log2) and 1 / sum
+    int* done;               // [blocks] warps of a row block whose statistics are out
+    float2* part;            // [blocks, max_pieces, 4 warps, kWeighRows] maximum (log2) and sum
+    float* stat;             // [blocks, kWeighRows] maximum + log2 of the sum; infinite: nothing is seen
     float* logits;
 };
 
@@ -66,16 +69,18 @@ struct CompactParams {
     int* seq_order;          // [S] 1: rows move onto pages that hold other kept rows, in order then
     int* status;
     int S, Hkv, ps, P, N;
-    int row_bytes;           // K and V of one head in a slot
+    int vec_shift;           // log2 of the 16-byte vectors of a row: K and V of one head in a slot
     int budget, protect, recent;
-    int cached;              // scores a CTA keeps in shared memory
+    int cluster;             // CTAs of a select cluster
+    int cached;              // scores a CTA of it keeps in shared memory
     FastDiv page;
 };
 
 // host launchers
-cudaError_t weigh_prepare(int D, int kt, int* blocks_per_sm);
-cudaError_t launch_weigh(const WeighParams& p, int kt, int grid, cudaStream_t st);
-cudaError_t compact_prepare(int max_keys, int* cached);
+// resident CTAs an SM of the stats kernel and the weigh kernel
+cudaError_t weigh_prepare(int D, int kt, int* stats, int* weigh);
+cudaError_t launch_weigh(const CUtensorMap& kmap, const WeighParams& p, int kt, int grid_weigh, cudaStream_t st);
+cudaError_t compact_prepare(int64_t units, int max_keys, int sms, int* cluster, int* cached);
 cudaError_t launch_compact(const CompactParams& p, int sms, cudaStream_t st);
 
 }  // namespace rpa

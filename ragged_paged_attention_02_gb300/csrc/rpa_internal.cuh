@@ -250,6 +250,8 @@ int encode_kv_map_runs(CUtensorMap* m, const void* kv, int byte_elems, long long
 // cache [N, ps, H, D] (2-byte elements; the split cache as H = 2 Hkv): one box = BR slots of one
 // row, all its column blocks
 int encode_kv_map_heads(CUtensorMap* m, const void* kv, long long N, int ps, int H, int D, int BR);
+// K rows of a split cache whose rows are `row` bytes: one box = BR slots of one row, in 64-byte columns
+int encode_k_map(CUtensorMap* m, const void* kv, int row, long long N, int ps, int Hkv, int BR);
 // occupancy / attributes (call once per device)
 size_t plan_smem_bytes();
 cudaError_t plan_prepare();

@@ -105,6 +105,23 @@ int encode_kv_map_heads(CUtensorMap* m, const void* kv, long long N, int ps, int
     return r == CUDA_SUCCESS ? 0 : (int)r;
 }
 
+// A split cache of `row`-byte rows viewed as (64 bytes of a column, slots, columns of a slot: 2 Hkv row / 64).
+// One box = BR slots of one row (K of head h starts at column 2 h row / 64), landing as [row / 64][BR][64 B]:
+// neighbouring slots' columns lie side by side, so that lanes which each read 16 bytes of a column, four a
+// slot, read 128 neighbouring bytes.
+int encode_k_map(CUtensorMap* m, const void* kv, int row, long long N, int ps, int Hkv, int BR) {
+    EncodeTiledFn fn = encoder();
+    if (!fn) return -1;
+    const cuuint64_t dims[3] = {64u, (cuuint64_t)(N * ps), (cuuint64_t)(2 * Hkv * (row / 64))};
+    const cuuint64_t strides[2] = {(cuuint64_t)2 * Hkv * row, 64u};
+    const cuuint32_t box[3] = {64u, (cuuint32_t)BR, (cuuint32_t)(row / 64)};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(kv), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                          CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? 0 : (int)r;
+}
+
 // q viewed as (D, Hq, T): one box = 64 elements x the G heads of a kv group x
 // Tt tokens, 128-byte swizzle; tokens past T read as zero.  q holds 2-byte
 // elements (bf16 or f16: the copy moves bits).

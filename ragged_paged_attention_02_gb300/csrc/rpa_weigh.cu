@@ -1,26 +1,36 @@
 // rpa_weigh.cu -- the softmax weight every cached key receives.
 //
-//   scores[j] += sum over rows r (query tokens x heads of the group) of 2^(x_rj - M_r) / L_r
+//   scores[j] += sum over rows r (query tokens x heads of the group) of 2^(x_rj - S_r),  S_r = M_r + log2 L_r
 //
 // x_rj = log2(e) * logit, M_r and L_r the row's maximum and sum over all keys it sees.  A key's weight
 // needs L_r, which needs every key: two passes over the logits.  Three launches:
 //
 //   plan     one CTA: checks the lengths, cuts every sequence into pieces of keys
-//   stats    item = (sequence, kv head, block of 16 rows, piece): x = q K^T on warp MMAs; the piece's
-//            maxima and sums; the block's last piece to finish merges them, in piece order.  Where a
-//            sequence has one block of rows (decode), x itself goes to the workspace.
-//   weigh    item = (sequence, kv head, piece): reads x back, or with more blocks computes it again
-//            (K from L2), and adds the weights' sum to the scores
+//   stats    item = (sequence, kv head, block of 16 rows, piece): x = q K^T on warp MMAs, maxima and
+//            sums; a block's last warp to finish merges all of them, in order.  Where a sequence has
+//            one block of rows (decode), x itself goes to the workspace.
+//   weigh    a warp takes (sequence, kv head, 64 keys): reads x back, or with more blocks computes it
+//            again (K from L2, all row blocks past the keys in its registers), and adds the weights'
+//            sum to the scores
 //
 // Decode is bound by reading K: 2 D bytes a key and head, beside which x is 4 G bytes (6 % at D 128,
 // G 4) and stays in L2, where a second pass over K would double the traffic.  S^T = K Q^T: 16 keys on
-// the MMA's M side, 8 rows on N.  K goes from global memory straight into the operand registers: the
-// contraction may take its terms in any order, so a thread's 16-byte load (8 or 16 neighbouring
-// elements of one key) is dealt to its own places of consecutive MMAs, and Q is dealt the same way.
-// No shared memory, no barrier in the key loop, the next tile's loads in flight behind this one's MMAs.
+// the MMA's M side, 8 rows on N.  The contraction may take its terms in any order, so a thread's 16-byte
+// load (8 or 16 neighbouring elements of one key) is dealt to its own places of consecutive MMAs, and Q is
+// dealt the same way: one load feeds two MMAs, for 16-bit and (through a conversion) for 8-bit K alike.
+//
+// The stats kernel is persistent, three CTAs an SM: a producer warp looks up items and page ids and copies
+// K rows in stages of 64 keys, one bulk tensor copy a page run, into a ring; four warps take 16 keys of a
+// stage each and share nothing but the ring.  The copies land in blocks of 64-byte columns, so that the
+// eight lanes that a shared-memory access serves at once (four of two neighbouring keys) read 128
+// neighbouring bytes.  (Warps that loaded their own keys were bound by their own instructions and waits:
+// 16-byte loads into registers read 4.4 TB/s, 16-byte asynchronous copies 4.8, row copies by each lane 3.9.)
 //
 // Maxima, sums and weights are 32-bit; the products are exact (16-bit operands, 32-bit accumulator)
 // where q has the operands' type; q of another type is rounded to it as rpa_forward does.
+#include <type_traits>
+
+#include "rpa_block.cuh"
 #include "rpa_evict.cuh"
 
 namespace rpa {
@@ -28,6 +38,7 @@ namespace rpa {
 namespace {
 
 constexpr int kWarps = kWeighThreads / 32;
+constexpr uint64_t kWeighWaitNs = 1000000000ull;  // bound of a wait for copies; then RPA_ERR_TIMEOUT
 
 // The first key, rounded down to a piece boundary, that a sequence's first query token sees: pieces start there.
 __device__ __forceinline__ int first_key(const WeighParams& p, int kl, int ql) {
@@ -35,29 +46,26 @@ __device__ __forceinline__ int first_key(const WeighParams& p, int kl, int ql) {
 }
 
 // ---------------------------------------------------------------- plan
-__global__ void __launch_bounds__(512) rpa_weigh_plan_kernel(const WeighParams p) {
-    __shared__ unsigned long long s_sum[512];
-    __shared__ long long s_part[512][4];
+__global__ void __launch_bounds__(kPlanThreads, 1) rpa_weigh_plan_kernel(const WeighParams p) {
+    __shared__ int s_scan[33 * 3];
+    __shared__ unsigned long long s_red[64];
     __shared__ int s_bad;
-    const int tid = threadIdx.x, n = blockDim.x;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_trigger();
     pdl_wait();
     if (tid == 0) s_bad = 0;
     __syncthreads();
-    // a thread's sequences are neighbours
-    const int per = (p.S + n - 1) / n, s_lo = min(p.S, tid * per), s_hi = min(p.S, s_lo + per);
-    unsigned long long keys = 0;
-    for (int s = s_lo; s < s_hi; ++s) {
+    unsigned long long keys = 0, none = 0;
+    for (int s = tid; s < p.S; s += kPlanThreads) {
         const int q0 = p.cu[s], q1 = p.cu[s + 1], kl = p.kv_lens[s];
         if (q0 < 0 || q1 < q0 || kl < 0 || kl > p.P * p.ps || q1 - q0 > kl || q1 > p.T) {
             s_bad = 1;
-            break;
+        } else {
+            const long long blocks = ((long long)(q1 - q0) * p.G + kWeighRows - 1) / kWeighRows;
+            keys += (unsigned long long)(blocks * (kl - first_key(p, kl, q1 - q0))) * p.Hkv;
         }
-        const long long blocks = ((long long)(q1 - q0) * p.G + kWeighRows - 1) / kWeighRows;
-        keys += (unsigned long long)(blocks * (kl - first_key(p, kl, q1 - q0))) * p.Hkv;
     }
-    s_sum[tid] = keys;
-    __syncthreads();
+    block_sum64x2(keys, none, s_red);
     if (s_bad) {
         if (tid == 0) {
             p.ctrl[0] = p.ctrl[1] = p.ctrl[2] = 0;
@@ -65,65 +73,64 @@ __global__ void __launch_bounds__(512) rpa_weigh_plan_kernel(const WeighParams p
         }
         return;
     }
-    for (int o = n / 2; o > 0; o >>= 1) {
-        if (tid < o) s_sum[tid] += s_sum[tid + o];
+    // keys of a piece: eight pieces a resident CTA, so that uneven ones even out, but not under 512 keys (a piece costs
+    // about what 100 keys do) unless that leaves CTAs without any
+    const unsigned long long slots = (unsigned long long)p.ctas;
+    const unsigned long long want = max(keys / (8 * slots), min(512ull, keys / slots));
+    const int chunk = (int)min((want / kWeighAlign + (want % kWeighAlign ? 1 : 0)) * kWeighAlign + (want ? 0 : kWeighAlign), 1ull << 30);
+    // per sequence: stat items, weigh items, row blocks; and logits
+    int n[3] = {0, 0, 0};
+    long long n_logits = 0;
+    for (int base = 0; base < p.S; base += kPlanThreads) {
+        const int s = base + tid;
+        int add[3] = {0, 0, 0}, off[3], tot[3];
+        long long logits = 0;
+        if (s < p.S) {
+            const int ql = p.cu[s + 1] - p.cu[s], kl = p.kv_lens[s], n_keys = kl - first_key(p, kl, ql);
+            const long long rows = (long long)ql * p.G;
+            if (rows > 0) {
+                const int pieces = min((n_keys + chunk - 1) / chunk, p.max_pieces);
+                add[2] = (int)((rows + kWeighRows - 1) / kWeighRows) * p.Hkv;
+                add[0] = add[2] * pieces;
+                add[1] = (n_keys + kWeighKeys - 1) / kWeighKeys * p.Hkv;
+                // (each sequence's start on 16 bytes)
+                if (rows <= kWeighRows) logits = ((long long)n_keys * p.Hkv * ((rows + 1) & ~1ll) + 3) & ~3ll;
+            }
+        }
+        block_scan<3>(add, off, tot, s_scan);
+        // the same scan of the 64-bit logit counts
+        long long sum = logits;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += y;
+        }
+        if (lane == 31) s_red[warp] = (unsigned long long)sum;
         __syncthreads();
-    }
-    const unsigned long long want = s_sum[0] / (unsigned long long)p.target;
-    const int chunk = (int)min((want / kWeighAlign + 1) * kWeighAlign, 1ull << 30);
-    // per sequence: pieces, then stat items, weight items, row blocks and logits
-    auto of = [&](int s, long long (&v)[4]) {
-        const int ql = p.cu[s + 1] - p.cu[s], kl = p.kv_lens[s], n_keys = kl - first_key(p, kl, ql);
-        const long long rows = (long long)ql * p.G, blocks = (rows + kWeighRows - 1) / kWeighRows * p.Hkv;
-        long long pieces = ((long long)n_keys + chunk - 1) / chunk;
-        pieces = min(pieces, (long long)p.max_pieces);
-        if (rows == 0) pieces = 0;
-        v[0] = blocks * pieces;
-        v[1] = pieces * p.Hkv;
-        v[2] = blocks;
-        v[3] = rows <= kWeighRows ? (long long)n_keys * p.Hkv * ((rows + 1) & ~1ll) : 0;
-    };
-    long long mine[4] = {0, 0, 0, 0};
-    for (int s = s_lo; s < s_hi; ++s) {
-        long long v[4];
-        of(s, v);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) mine[i] += v[i];
-    }
-#pragma unroll
-    for (int i = 0; i < 4; ++i) s_part[tid][i] = mine[i];
-    __syncthreads();
-    for (int o = 1; o < n; o <<= 1) {
-        long long v[4] = {0, 0, 0, 0};
-        if (tid >= o) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = s_part[tid - o][i];
+        long long before = 0, all = 0;
+        for (int w = 0; w < kPlanThreads / 32; ++w) {
+            const long long y = (long long)s_red[w];
+            if (w < warp) before += y;
+            all += y;
         }
         __syncthreads();
+        if (s < p.S) {
+            const long long at = n_logits + before + sum - logits;
+            p.stat0[s] = n[0] + off[0];
+            p.item0[s] = n[1] + off[1];
+            p.block0[s] = n[2] + off[2];
+            p.logit0[s] = logits > 0 && at + logits <= p.max_logits ? at : -1;
+        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) s_part[tid][i] += v[i];
-        __syncthreads();
+        for (int i = 0; i < 3; ++i) n[i] += tot[i];
+        n_logits += all;
     }
-    long long at[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) at[i] = s_part[tid][i] - mine[i];
-    for (int s = s_lo; s < s_hi; ++s) {
-        long long v[4];
-        of(s, v);
-        p.stat0[s] = (int)at[0];
-        p.item0[s] = (int)at[1];
-        p.block0[s] = (int)at[2];
-        p.logit0[s] = v[3] > 0 && at[3] + v[3] <= p.max_logits ? at[3] : -1;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) at[i] += v[i];
-    }
-    const int blocks = (int)s_part[n - 1][2];
-    for (int i = tid; i < blocks; i += n) p.done[i] = 0;
+    for (int i = tid; i < n[2]; i += kPlanThreads) p.done[i] = 0;
     if (tid == 0) {
-        p.stat0[p.S] = p.ctrl[0] = (int)s_part[n - 1][0];
-        p.item0[p.S] = p.ctrl[1] = (int)s_part[n - 1][1];
-        p.block0[p.S] = blocks;
-        p.ctrl[2] = chunk;
+        p.ctrl[2] = 0;
+        p.stat0[p.S] = p.ctrl[0] = n[0];
+        p.item0[p.S] = p.ctrl[1] = n[1];
+        p.block0[p.S] = n[2];
     }
 }
 
@@ -164,6 +171,19 @@ __device__ __forceinline__ void load_q(const WeighParams& p, int q0, int h, int 
         }
 }
 
+__device__ __forceinline__ uint4 load_stream(const uint8_t* p, uint64_t policy) {
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.L2::cache_hint.v4.b32 {%0,%1,%2,%3}, [%4], %5;\n"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p), "l"(policy));
+    return v;
+}
+__device__ __forceinline__ uint64_t l2_policy_normal() {
+    uint64_t pol;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;\n" : "=l"(pol));
+    return pol;
+}
+
 // A 16-key tile: this thread's shares of keys `lane / 4` and `lane / 4 + 8`, as stored.
 template <int D, int KT>
 struct KeyTile {
@@ -171,7 +191,8 @@ struct KeyTile {
     bool ok[2];   // the key is one of [0, kv_end) on a page that exists
 };
 template <int D, int KT>
-__device__ __forceinline__ void load_k(const WeighParams& p, const int* table, int h, int k0, int k_end, int lane, KeyTile<D, KT>& t) {
+__device__ __forceinline__ void load_k(const WeighParams& p, const int* table, int h, int k0, int k_end, int lane, uint64_t policy,
+                                       KeyTile<D, KT>& t) {
     using L = Deal<D, KT>;
     constexpr int EB = kt_8bit(KT) ? 1 : 2;
 #pragma unroll
@@ -190,51 +211,103 @@ __device__ __forceinline__ void load_k(const WeighParams& p, const int* table, i
         }
         const uint8_t* src = p.kv + (((size_t)pg * p.ps + at) * 2 * p.Hkv + 2 * h) * (size_t)(D * EB) + (lane % 4) * 16;
 #pragma unroll
-        for (int b = 0; b < L::LOADS; ++b) t.v[i][b] = t.ok[i] ? *reinterpret_cast<const uint4*>(src + b * 64) : make_uint4(0, 0, 0, 0);
+        for (int b = 0; b < L::LOADS; ++b) t.v[i][b] = t.ok[i] ? load_stream(src + b * 64, policy) : make_uint4(0, 0, 0, 0);
     }
 }
 
-// acc += the tile's 16 keys x 8 rows: acc[0], [1] key lane / 4, rows 2 (lane % 4) and + 1; [2], [3] key + 8
-template <int D, int KT>
-__device__ __forceinline__ void tile_dot(const KeyTile<D, KT>& t, const uint32_t* q, float* acc) {
-    using L = Deal<D, KT>;
+// acc += 16 keys x 8 rows over the elements of load b: lo and hi are the thread's shares of keys lane / 4 and + 8.
+// acc[0], [1]: key lane / 4, rows 2 (lane % 4) and + 1; [2], [3]: key + 8
+template <int KT, int NB, int REGS>
+__device__ __forceinline__ void load_dot(const uint4& lo, const uint4& hi, int b, const uint32_t (&q)[NB][REGS], float (&acc)[NB][4]) {
     constexpr bool F16 = kt_f16_mma(KT);
+    if constexpr (kt_8bit(KT)) {
+        const uint4 lo0 = cvt8x8_to_f16x8<KT>(lo.x, lo.y), lo1 = cvt8x8_to_f16x8<KT>(lo.z, lo.w);
+        const uint4 hi0 = cvt8x8_to_f16x8<KT>(hi.x, hi.y), hi1 = cvt8x8_to_f16x8<KT>(hi.z, hi.w);
+        const uint32_t a[4][4] = {{lo0.x, hi0.x, lo0.y, hi0.y}, {lo0.z, hi0.z, lo0.w, hi0.w},
+                                  {lo1.x, hi1.x, lo1.y, hi1.y}, {lo1.z, hi1.z, lo1.w, hi1.w}};
 #pragma unroll
-    for (int b = 0; b < L::LOADS; ++b) {
-        if constexpr (kt_8bit(KT)) {
-            const uint4 lo0 = cvt8x8_to_f16x8<KT>(t.v[0][b].x, t.v[0][b].y), lo1 = cvt8x8_to_f16x8<KT>(t.v[0][b].z, t.v[0][b].w);
-            const uint4 hi0 = cvt8x8_to_f16x8<KT>(t.v[1][b].x, t.v[1][b].y), hi1 = cvt8x8_to_f16x8<KT>(t.v[1][b].z, t.v[1][b].w);
-            const uint32_t a0[4] = {lo0.x, hi0.x, lo0.y, hi0.y}, a1[4] = {lo0.z, hi0.z, lo0.w, hi0.w};
-            const uint32_t a2[4] = {lo1.x, hi1.x, lo1.y, hi1.y}, a3[4] = {lo1.z, hi1.z, lo1.w, hi1.w};
-            mma16816<F16>(acc, a0, q[8 * b], q[8 * b + 1]);
-            mma16816<F16>(acc, a1, q[8 * b + 2], q[8 * b + 3]);
-            mma16816<F16>(acc, a2, q[8 * b + 4], q[8 * b + 5]);
-            mma16816<F16>(acc, a3, q[8 * b + 6], q[8 * b + 7]);
-        } else {
-            const uint4 lo = t.v[0][b], hi = t.v[1][b];
-            const uint32_t a0[4] = {lo.x, hi.x, lo.y, hi.y}, a1[4] = {lo.z, hi.z, lo.w, hi.w};
-            mma16816<F16>(acc, a0, q[4 * b], q[4 * b + 1]);
-            mma16816<F16>(acc, a1, q[4 * b + 2], q[4 * b + 3]);
-        }
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) mma16816<F16>(acc[n], a[i], q[n][8 * b + 2 * i], q[n][8 * b + 2 * i + 1]);
+    } else {
+        const uint32_t a[2][4] = {{lo.x, hi.x, lo.y, hi.y}, {lo.z, hi.z, lo.w, hi.w}};
+#pragma unroll
+        for (int n = 0; n < NB; ++n)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) mma16816<F16>(acc[n], a[i], q[n][4 * b + 2 * i], q[n][4 * b + 2 * i + 1]);
     }
 }
+template <int D, int KT, int NB>
+__device__ __forceinline__ void tile_dot(const KeyTile<D, KT>& t, const uint32_t (&q)[NB][Deal<D, KT>::REGS], float (&acc)[NB][4]) {
+#pragma unroll
+    for (int b = 0; b < Deal<D, KT>::LOADS; ++b) load_dot<KT>(t.v[0][b], t.v[1][b], b, q, acc);
+}
 
-// x in the log2 domain; keys the row does not see are -infinity
-__device__ __forceinline__ float logit(const WeighParams& p, float dot, int j, int pos, bool ok) {
-    const float x = p.has_cap ? p.cap_log2 * tanhf(dot * p.cap_arg) : dot * p.qk_log2;
+// ---- the stats kernel's ring
+template <int D, int KT>
+struct Ring {
+    static constexpr int ROW = D * (kt_8bit(KT) ? 1 : 2);
+    static constexpr int KEYS = 64;             // of a stage: 16 a consumer warp
+    static constexpr int STAGE = KEYS * ROW;
+    // resident an SM: at D 256 two, of 168 registers a thread, else three of 128
+    static constexpr int CTAS = D == 256 ? 2 : 3;
+    static constexpr int STAGES = ROW == 512 ? 3 : ROW == 256 ? 4 : 6;
+    static constexpr int SMEM = STAGES * STAGE + 128;
+    static_assert(CTAS * SMEM <= 220 * 1024, "shared memory of an SM");
+};
+constexpr int kConsumers = 4;
+constexpr int kStatThreads = 32 * (kConsumers + 1);
+
+struct Piece {
+    int s, h, rb, nb, piece, pieces, base, k_lo, k_hi, q0, ql, kl;
+};
+// What a stage holds: keys [k0, k0 + 64) of an item, those below k_last; a bit for each page run that is there
+struct StageMeta {
+    Piece c;
+    int k0, k_first, k_last;
+    uint32_t runs;
+    int stop;
+};
+
+__device__ __forceinline__ uint4 read16(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];\n" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at) : "memory");
+    return v;
+}
+
+// Soft cap of N products, in the log2 domain.  A function of its own: the inlined tanh would cost the key
+// loops their registers.
+__device__ __noinline__ float capped(float dot, float arg, float cap_log2) { return cap_log2 * tanhf(dot * arg); }
+template <int N>
+__device__ __forceinline__ void scale(const WeighParams& p, float (&x)[N]) {
+    if (p.has_cap) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = capped(x[i], p.cap_arg, p.cap_log2);
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] *= p.qk_log2;
+    }
+}
+// With MASK, keys the row does not see are -infinity
+template <bool MASK>
+__device__ __forceinline__ float hide(const WeighParams& p, float x, int j, int pos, bool ok) {
+    if constexpr (!MASK) return x;
     const bool sees = ok && (!p.causal || j <= pos) && (!p.has_window || j > pos - p.window);
     return sees ? x : -INFINITY;
 }
-
-// A sequence's keys that the rows at positions [p_lo, p_hi] see: [lo, hi)
-__device__ __forceinline__ void seen_keys(const WeighParams& p, int kl, int p_lo, int p_hi, int& lo, int& hi) {
-    hi = p.causal ? min(kl, p_hi + 1) : kl;
-    lo = p.has_window ? max(0, p_lo - p.window + 1) : 0;
+// Whether some of the keys [k0, k1) is hidden from some row at positions [p_lo, p_hi]
+__device__ __forceinline__ bool some_hidden(const WeighParams& p, int k0, int k1, int p_lo, int p_hi) {
+    return (p.causal && k1 - 1 > p_lo) || (p.has_window && k0 <= p_hi - p.window);
 }
 
-struct Piece {
-    int s, h, piece, pieces, base, k_lo, k_hi, q0, ql, kl;
-};
+// (m, l) of a set of keys joined with another's
+__device__ __forceinline__ void join(float& m, float& l, float m2, float l2) {
+    const float mn = fmaxf(m, m2);
+    if (mn != -INFINITY) l = l * ex2(m - mn) + l2 * ex2(m2 - mn);
+    m = mn;
+}
+
+// ---------------------------------------------------------------- stats
 // Piece `piece` of a sequence's keys from `base` on (pieces are equal multiples of kWeighAlign keys, the last the rest)
 __device__ __forceinline__ void cut(const WeighParams& p, Piece& c) {
     c.base = first_key(p, c.kl, c.ql);
@@ -243,17 +316,31 @@ __device__ __forceinline__ void cut(const WeighParams& p, Piece& c) {
     c.k_hi = (int)min((long long)c.kl, c.k_lo + len);
 }
 
-// ---------------------------------------------------------------- stats
-// NB: n8 blocks of rows a pass takes (1: at most 8 rows)
+// Rows of an item's block, positions and the keys some of them sees: [k_first, k_last) of the piece
+__device__ __forceinline__ void seen(const WeighParams& p, const Piece& c, int& k_first, int& k_last) {
+    const int row0 = c.rb * kWeighRows, n_rows = min(kWeighRows, c.ql * p.G - row0), pos0 = c.kl - c.ql;
+    const int p_lo = pos0 + p.group.div(row0), p_hi = pos0 + p.group.div(row0 + n_rows - 1);
+    const int hi = p.causal ? min(c.kl, p_hi + 1) : c.kl, lo = p.has_window ? max(0, p_lo - p.window + 1) : 0;
+    k_first = max(c.k_lo, lo & ~(kWeighAlign - 1));
+    k_last = min(c.k_hi, hi);
+}
+
+// A consumer warp's work on one item, from its first stage (already full) to its last.  NB: n8 blocks of rows.
 template <int D, int KT, int NB>
-__device__ __forceinline__ void stat_item(const WeighParams& p, const Piece& c, int rb, float2* s_ml) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, quad = lane % 4;
-    const int rows = c.ql * p.G, row0 = rb * kWeighRows;
-    const int pos0 = c.kl - c.ql;
+__device__ __forceinline__ bool stat_item(const WeighParams& p, const StageMeta* meta, uint32_t ring, uint32_t full, uint32_t empty,
+                                          int warp, int& st, uint32_t& phase) {
+    using R = Ring<D, KT>;
+    constexpr int LOADS = Deal<D, KT>::LOADS;
+    using Acc = float[NB][4];
+    const int lane = threadIdx.x & 31, quad = lane % 4;
+    const Piece& c = meta[st].c;  // until the stage is freed
+    const int k_first = meta[st].k_first, k_last = meta[st].k_last, base = c.base;
+    const int rows = c.ql * p.G, row0 = c.rb * kWeighRows, pos0 = c.kl - c.ql, head0 = c.h * p.G;
     const int n_rows = min(kWeighRows, rows - row0);
     const long long lo0 = p.logit0[c.s];
     const int rs = (rows + 1) & ~1;  // floats of a key's logits
-    float* x_out = lo0 >= 0 ? p.logits + lo0 + (size_t)c.h * (c.kl - c.base) * rs : nullptr;
+    float* x_out = lo0 >= 0 ? p.logits + lo0 + (size_t)c.h * (c.kl - base) * rs : nullptr;
+    const int block = p.block0[c.s] + c.h * c.nb + c.rb, parts = c.pieces * kConsumers, my_part = c.piece * kConsumers + warp;
     uint32_t q[NB][Deal<D, KT>::REGS];
 #pragma unroll
     for (int b = 0; b < NB; ++b) load_q<D, KT>(p, c.q0, c.h, row0 + 8 * b + lane / 4, rows, quad, q[b]);
@@ -267,235 +354,414 @@ __device__ __forceinline__ void stat_item(const WeighParams& p, const Piece& c, 
             m[b][i] = -INFINITY;
             l[b][i] = 0.f;
         }
-    int lo, hi;
-    seen_keys(p, c.kl, pos0 + p.group.div(row0), pos0 + p.group.div(row0 + n_rows - 1), lo, hi);
-    // tiles of the piece that some row sees (all of them where there is one block of rows)
-    const int k_first = max(c.k_lo, lo & ~(kWeighAlign - 1)), k_last = min(c.k_hi, hi);
-    const int* table = p.page_indices + (size_t)c.s * p.P;
-    auto use = [&](const KeyTile<D, KT>& t, int k0) {
-        float acc[NB][4];
+    const int p_lo = pos0 + p.group.div(row0), p_hi = pos0 + p.group.div(row0 + n_rows - 1);
+    // where this thread's two keys of a stage sit: run, place in the run; a run is [ROW / 64][BR][64 bytes]
+    uint32_t key_at[2], key_run[2];
+    const uint32_t column = (uint32_t)p.BR * 64u;
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-            acc[b][0] = acc[b][1] = acc[b][2] = acc[b][3] = 0.f;
-            tile_dot<D, KT>(t, q[b], acc[b]);
+    for (int i = 0; i < 2; ++i) {
+        const int kk = 16 * warp + lane / 4 + 8 * i;
+        key_run[i] = (uint32_t)kk >> p.br_shift;
+        key_at[i] = key_run[i] * (uint32_t)(p.BR * R::ROW) + (uint32_t)(kk & (p.BR - 1)) * 64u + quad * 16;
+    }
+    auto finish = [&](auto masked, Acc& acc, uint32_t runs, int kw) {
+        constexpr bool MASK = decltype(masked)::value;
+        if constexpr (MASK) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int j = kw + lane / 4 + 8 * (e >> 1);
+                    acc[b][e] = hide<true>(p, acc[b][e], j, pos[b][e & 1], j < k_last && (runs >> key_run[e >> 1] & 1u));
+                }
         }
+        if (x_out) {
+            float* x = x_out + (size_t)(kw - base + lane / 4) * rs + 2 * quad;
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
+            for (int i = 0; i < 2; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) acc[b][e] = logit(p, acc[b][e], k0 + lane / 4 + 8 * (e >> 1), pos[b][e & 1], t.ok[e >> 1]);
-            if (x_out) {
-                const int r = 8 * b + 2 * quad;
+                for (int b = 0; b < NB; ++b)
+                    if ((!MASK || kw + lane / 4 + 8 * i < k_last) && 8 * b + 2 * quad < rs)
+                        *reinterpret_cast<float2*>(x + 8 * i * rs + 8 * b) = make_float2(acc[b][2 * i], acc[b][2 * i + 1]);
+        }
+        // new maxima; mostly there are none
+        bool grow = false;
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) grow = grow || fmaxf(acc[b][i], acc[b][2 + i]) > m[b][i];
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    const int j = k0 + lane / 4 + 8 * i;
-                    if (j < k_last && r < rs)
-                        *reinterpret_cast<float2*>(x_out + (size_t)(j - c.base) * rs + r) = make_float2(acc[b][2 * i], acc[b][2 * i + 1]);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const float x0 = acc[b][i], x1 = acc[b][2 + i];
-                const float mn = fmaxf(m[b][i], fmaxf(x0, x1));
-                if (mn != -INFINITY) {
-                    l[b][i] = l[b][i] * ex2(m[b][i] - mn) + (ex2(x0 - mn) + ex2(x1 - mn));
+                    const float mn = fmaxf(m[b][i], fmaxf(acc[b][i], acc[b][2 + i]));
+                    if (mn != -INFINITY) l[b][i] *= ex2(m[b][i] - mn);
                     m[b][i] = mn;
                 }
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                // before the first key that is seen there is no maximum: nothing to add
+                const float at = m[b][i] == -INFINITY ? 0.f : m[b][i];
+                l[b][i] += ex2(acc[b][i] - at) + ex2(acc[b][2 + i] - at);
+            }
+    };
+    for (int k0 = k_first;;) {
+        const int kw = k0 + 16 * warp;
+        const uint32_t runs = meta[st].runs;
+        const uint32_t from = ring + st * R::STAGE;
+        const bool any = kw < k_last;
+        // the rows go to registers first, and the stage's place back to the producer, where they fit
+        constexpr bool kEarly = 8 * LOADS + NB * Deal<D, KT>::REGS <= 48;
+        uint4 lo[LOADS], hi[LOADS];
+        auto free_stage = [&]() {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty + st * 8);
+            if (++st == R::STAGES) {
+                st = 0;
+                phase ^= 1u;
+            }
+        };
+        if (kEarly) {
+            if (any) {
+#pragma unroll
+                for (int b = 0; b < LOADS; ++b) {
+                    lo[b] = read16(from + key_at[0] + b * column);
+                    hi[b] = read16(from + key_at[1] + b * column);
+                }
+            }
+            free_stage();
+        }
+        Acc acc;
+        if (any) {
+            // two chains of MMAs where there is one block of rows
+            float odd[NB][4];
+#pragma unroll
+            for (int n = 0; n < NB; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[n][e] = odd[n][e] = 0.f;
+#pragma unroll
+            for (int b = 0; b < LOADS; ++b) {
+                if (!kEarly) {
+                    lo[b] = read16(from + key_at[0] + b * column);
+                    hi[b] = read16(from + key_at[1] + b * column);
+                }
+                if (NB == 1 && (b & 1)) load_dot<KT>(lo[b], hi[b], b, q, odd);
+                else load_dot<KT>(lo[b], hi[b], b, q, acc);
+            }
+#pragma unroll
+            for (int n = 0; n < NB; ++n) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[n][e] += odd[n][e];
+                scale(p, acc[n]);
             }
         }
-    };
-    // a second tile's loads in flight where its registers, and the rows' operands, leave 48 of 128 for the rest
-    constexpr bool kAhead = 2 * 8 * Deal<D, KT>::LOADS + NB * Deal<D, KT>::REGS <= 80;
-    int k0 = k_first + 16 * warp;
-    if constexpr (kAhead) {
-        KeyTile<D, KT> a, b;
-        if (k0 < k_last) load_k<D, KT>(p, table, c.h, k0, k_last, lane, a);
-        while (k0 < k_last) {
-            const int k1 = k0 + 16 * kWarps;
-            if (k1 < k_last) load_k<D, KT>(p, table, c.h, k1, k_last, lane, b);
-            use(a, k0);
-            k0 = k1 + 16 * kWarps;
-            if (k0 < k_last) load_k<D, KT>(p, table, c.h, k0, k_last, lane, a);
-            if (k1 < k_last) use(b, k1);
+        if (!kEarly) free_stage();
+        if (any) {
+            if (runs == p.all_runs && kw + 16 <= k_last && !some_hidden(p, kw, kw + 16, p_lo, p_hi)) finish(std::false_type{}, acc, runs, kw);
+            else finish(std::true_type{}, acc, runs, kw);
         }
-    } else {
-        for (; k0 < k_last; k0 += 16 * kWarps) {
-            KeyTile<D, KT> a;
-            load_k<D, KT>(p, table, c.h, k0, k_last, lane, a);
-            use(a, k0);
-        }
+        k0 += R::KEYS;
+        if (k0 >= k_last) break;
+        if (!mbar_wait(full + st * 8, phase, p.status, kWeighWaitNs)) return false;
     }
-    // the piece's maximum and sum of each row: over a warp's keys, then over the warps
+    // the warp's maximum and sum of each row, over the lanes that hold its keys
+    float2* part = p.part + (size_t)block * (p.max_pieces * kConsumers) * kWeighRows;
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            float mm = m[b][i], ll = l[b][i];
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) {
-                const float m2 = __shfl_xor_sync(0xffffffffu, mm, o), l2 = __shfl_xor_sync(0xffffffffu, ll, o);
-                const float mn = fmaxf(mm, m2);
-                if (mn != -INFINITY) ll = ll * ex2(mm - mn) + l2 * ex2(m2 - mn);
-                mm = mn;
+                const float m2 = __shfl_xor_sync(0xffffffffu, m[b][i], o), l2 = __shfl_xor_sync(0xffffffffu, l[b][i], o);
+                join(m[b][i], l[b][i], m2, l2);
             }
-            if (lane < 4) s_ml[warp * kWeighRows + 8 * b + 2 * lane + i] = make_float2(mm, ll);
+            if (lane < 4) part[my_part * kWeighRows + 8 * b + 2 * lane + i] = make_float2(m[b][i], l[b][i]);
         }
-    __syncthreads();
-    const int nb = (rows + kWeighRows - 1) / kWeighRows;
-    const int block = p.block0[c.s] + c.h * nb + rb;
-    float2* part = p.part + (size_t)block * p.max_pieces * kWeighRows;
-    __shared__ int s_last;
-    if (warp == 0) {
-        if (lane < n_rows) {
-            float mm = -INFINITY, ll = 0.f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float2 v = s_ml[w * kWeighRows + lane];
-                const float mn = fmaxf(mm, v.x);
-                if (mn != -INFINITY) ll = ll * ex2(mm - mn) + v.y * ex2(v.x - mn);
-                mm = mn;
-            }
-            part[c.piece * kWeighRows + lane] = make_float2(mm, ll);
-        }
-        __threadfence();
-        __syncwarp();
-        if (lane == 0) s_last = atomicAdd(p.done + block, 1) == c.pieces - 1;
-        __syncwarp();
-    }
-    __syncthreads();
-    // the block's last piece merges all of them, each row's in piece order
-    if (s_last) {
-        __threadfence();
-        for (int r = warp; r < n_rows; r += kWarps) {
-            float mm = -INFINITY, ll = 0.f;
-            for (int k = lane; k < c.pieces; k += 32) {
-                const float2 v = __ldcg(part + k * kWeighRows + r);
-                const float mn = fmaxf(mm, v.x);
-                if (mn != -INFINITY) ll = ll * ex2(mm - mn) + v.y * ex2(v.x - mn);
-                mm = mn;
-            }
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const float m2 = __shfl_xor_sync(0xffffffffu, mm, o), l2 = __shfl_xor_sync(0xffffffffu, ll, o);
-                const float mn = fmaxf(mm, m2);
-                if (mn != -INFINITY) ll = ll * ex2(mm - mn) + l2 * ex2(m2 - mn);
-                mm = mn;
-            }
-            if (lane == 0) {
-                const int row = row0 + r, g = row - p.group.div(row) * p.G;
-                ll = add_sink(ll, p.sinks, c.h * p.G + g, mm);
-                // a row that sees nothing gives nothing
-                p.stat[(size_t)block * kWeighRows + r] = mm == -INFINITY ? make_float2(0.f, 0.f) : make_float2(mm, 1.f / ll);
-            }
+    __threadfence();
+    __syncwarp();
+    int last = 0;
+    if (lane == 0) last = atomicAdd(p.done + block, 1) == parts - 1;
+    if (!__shfl_sync(0xffffffffu, last, 0)) return true;
+    // the block's last warp merges all parts: a lane half of a row's, in order
+    __threadfence();
+    const int r = lane % kWeighRows;
+    float mm = -INFINITY, ll = 0.f;
+    if (r < 8 * NB) {
+#pragma unroll 8
+        for (int k = lane / kWeighRows; k < parts; k += 2) {
+            const float2 v = __ldcg(part + k * kWeighRows + r);
+            join(mm, ll, v.x, v.y);
         }
     }
-    __syncthreads();  // s_ml and s_last are free again
+    join(mm, ll, __shfl_down_sync(0xffffffffu, mm, kWeighRows), __shfl_down_sync(0xffffffffu, ll, kWeighRows));
+    if (lane < n_rows) {
+        const int row = row0 + r, g = row - p.group.div(row) * p.G;
+        ll = add_sink(ll, p.sinks, head0 + g, mm);
+        // a row that sees nothing gives nothing
+        p.stat[(size_t)block * kWeighRows + r] = mm == -INFINITY ? INFINITY : mm + log2f(ll);
+    }
+    return true;
 }
 
 template <int D, int KT>
-__global__ void __launch_bounds__(kWeighThreads, D == 256 ? 1 : 2) rpa_weigh_stats_kernel(const WeighParams p) {
-    __shared__ float2 s_ml[kWarps * kWeighRows];
+__global__ void __launch_bounds__(kStatThreads, Ring<D, KT>::CTAS) rpa_weigh_stats_kernel(const __grid_constant__ CUtensorMap kmap,
+                                                                                          const WeighParams p) {
+    using R = Ring<D, KT>;
+    extern __shared__ uint8_t s_raw[];
+    __shared__ __align__(8) uint64_t s_full[R::STAGES], s_empty[R::STAGES];
+    __shared__ StageMeta meta[R::STAGES];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t ring = (smem_u32(s_raw) + 127u) & ~127u, full = smem_u32(s_full), empty = smem_u32(s_empty);
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < R::STAGES; ++i) {
+            mbar_init(full + i * 8, 1);
+            mbar_init(empty + i * 8, kConsumers);
+        }
+        fence_mbar_init();
+    }
+    __syncthreads();
     pdl_trigger();
     pdl_wait();
-    const int items = p.ctrl[0], lane = threadIdx.x & 31;
-    for (int it = blockIdx.x; it < items; it += gridDim.x) {
-        // items of a sequence: piece, then row block, then kv head (neighbours read neighbouring rows)
-        Piece c;
-        c.s = find_seq(p.stat0, p.S, it, lane);
-        c.q0 = p.cu[c.s];
-        c.ql = p.cu[c.s + 1] - c.q0;
-        c.kl = p.kv_lens[c.s];
-        const int at = it - p.stat0[c.s], nb = (c.ql * p.G + kWeighRows - 1) / kWeighRows;
-        c.pieces = (p.stat0[c.s + 1] - p.stat0[c.s]) / (nb * p.Hkv);
-        c.h = at % p.Hkv;
-        const int rb = at / p.Hkv % nb;
-        c.piece = at / p.Hkv / nb;
-        cut(p, c);
-        if (min(kWeighRows, c.ql * p.G - rb * kWeighRows) <= 8) stat_item<D, KT, 1>(p, c, rb, s_ml);
-        else stat_item<D, KT, 2>(p, c, rb, s_ml);
+    int st = 0;
+    uint32_t phase = 0;
+    if (warp == kConsumers) {
+        // ---- producer
+        const int items = p.ctrl[0], BR = p.BR, runs = R::KEYS / BR;
+        bool ok = true;
+        int it = 0, nxt = 0;
+        if (lane == 0) it = atomicAdd(p.ctrl + 2, 1);
+        it = __shfl_sync(0xffffffffu, it, 0);
+        while (ok && it < items) {
+            if (lane == 0) nxt = atomicAdd(p.ctrl + 2, 1);
+            // items of a sequence: piece, then row block, then kv head (neighbours read neighbouring rows)
+            Piece c;
+            c.s = find_seq(p.stat0, p.S, it, lane);
+            c.q0 = p.cu[c.s];
+            c.ql = p.cu[c.s + 1] - c.q0;
+            c.kl = p.kv_lens[c.s];
+            const int first = p.stat0[c.s], at = it - first;
+            c.nb = (c.ql * p.G + kWeighRows - 1) / kWeighRows;
+            c.pieces = (p.stat0[c.s + 1] - first) / (c.nb * p.Hkv);
+            c.h = at % p.Hkv;
+            c.rb = at / p.Hkv % c.nb;
+            c.piece = at / p.Hkv / c.nb;
+            cut(p, c);
+            int k_first, k_last;
+            seen(p, c, k_first, k_last);
+            // K is read once where there is one row block: it leaves L2 to the logits
+            const uint64_t policy = c.nb == 1 ? l2_policy_evict_first() : l2_policy_normal();
+            const int* table = p.page_indices + (size_t)c.s * p.P;
+            // lane r: page run r of a stage, its page id looked up a stage ahead
+            auto look = [&](int k0) { return __ldg(table + p.page.div(min(k0 + lane * BR, max(k_last, 1) - 1))); };
+            int page = look(k_first);
+            int k0 = k_first;
+            do {
+                if (!mbar_wait(empty + st * 8, phase ^ 1u, p.status, kWeighWaitNs)) {
+                    ok = false;
+                    break;
+                }
+                const int k = k0 + lane * BR;
+                const bool want = lane < runs && k < k_last, good = want && (unsigned)page < (unsigned)p.N;
+                if (want && !good) set_status(p.status, RPA_ERR_BAD_PAGE_INDEX);
+                const uint32_t mask = __ballot_sync(0xffffffffu, good);
+                if (lane == 0) {
+                    StageMeta& m = meta[st];
+                    if (k0 == k_first) {
+                        m.c = c;
+                        m.k_first = k_first;
+                        m.k_last = k_last;
+                    }
+                    m.k0 = k0;
+                    m.runs = mask;
+                    m.stop = 0;
+                    mbar_arrive_expect_tx(full + st * 8, (uint32_t)__popc(mask) * (uint32_t)(BR * R::ROW));
+                }
+                __syncwarp();
+                if (good)
+                    tma_load_3d_hint(ring + st * R::STAGE + lane * (BR * R::ROW), &kmap, full + st * 8, 0,
+                                     page * p.ps + (k - p.page.div(k) * p.ps), 2 * c.h * (R::ROW / 64), policy);
+                if (++st == R::STAGES) {
+                    st = 0;
+                    phase ^= 1u;
+                }
+                k0 += R::KEYS;
+                if (k0 < k_last) page = look(k0);
+            } while (k0 < k_last);
+            it = __shfl_sync(0xffffffffu, nxt, 0);
+        }
+        if (ok && mbar_wait(empty + st * 8, phase ^ 1u, p.status, kWeighWaitNs)) {
+            if (lane == 0) {
+                meta[st].stop = 1;
+                mbar_arrive(full + st * 8);
+            }
+        } else {
+            // gave up: let the copies already issued land before leaving
+            for (int i = 0; i < R::STAGES; ++i) mbar_wait(full + i * 8, i < st ? phase : phase ^ 1u, p.status, kWeighWaitNs);
+        }
+        return;
+    }
+    // ---- consumers
+    for (;;) {
+        if (!mbar_wait(full + st * 8, phase, p.status, kWeighWaitNs)) return;
+        if (meta[st].stop) return;
+        const Piece& c = meta[st].c;
+        const bool few = min(kWeighRows, c.ql * p.G - c.rb * kWeighRows) <= 8;
+        const bool ok = few ? stat_item<D, KT, 1>(p, meta, ring, full, empty, warp, st, phase)
+                            : stat_item<D, KT, 2>(p, meta, ring, full, empty, warp, st, phase);
+        if (!ok) return;
     }
 }
 
 // ---------------------------------------------------------------- weigh
-__device__ __forceinline__ void add_score(const WeighParams& p, const int* table, int h, int j, int fresh, float w) {
+// Where key j's score of kv head h is (nullptr: on no page)
+__device__ __forceinline__ float* score_at(const WeighParams& p, const int* table, int h, int j) {
     const int lp = p.page.div(j), pg = __ldg(table + lp);
-    if ((unsigned)pg >= (unsigned)p.N) return;
-    float* dst = p.scores + ((size_t)pg * p.Hkv + h) * p.ps + (j - lp * p.ps);
-    // the call's own keys start from 0; the others add (a page may be shared by sequences)
-    if (j >= fresh) *dst = w;
+    return (unsigned)pg < (unsigned)p.N ? p.scores + ((size_t)pg * p.Hkv + h) * p.ps + (j - lp * p.ps) : nullptr;
+}
+// the call's own keys start from 0; the others add (a page may be shared by sequences)
+__device__ __forceinline__ void add_score(float* dst, bool fresh, float w) {
+    if (dst == nullptr) return;
+    if (fresh) *dst = w;
     else atomicAdd(dst, w);
 }
 
 template <int D, int KT>
-__global__ void __launch_bounds__(kWeighThreads) rpa_weigh_kernel(const WeighParams p) {
-    __shared__ float2 s_stat[kWeighRows];
+__global__ void __launch_bounds__(kWeighThreads, D == 256 ? 2 : 4) rpa_weigh_kernel(const WeighParams p) {
+    // key tiles of 16 a warp holds while it goes through the rows: 32 registers of K (64 at D 256)
+    constexpr int kTiles = Deal<D, KT>::LOADS >= 4 ? 1 : 4 / Deal<D, KT>::LOADS;
     pdl_trigger();
     pdl_wait();
-    const int items = p.ctrl[1], tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    for (int it = blockIdx.x; it < items; it += gridDim.x) {
-        Piece c;
-        c.s = find_seq(p.item0, p.S, it, lane);
-        c.q0 = p.cu[c.s];
-        c.ql = p.cu[c.s + 1] - c.q0;
-        c.kl = p.kv_lens[c.s];
-        c.pieces = (p.item0[c.s + 1] - p.item0[c.s]) / p.Hkv;
-        const int at = it - p.item0[c.s];
-        c.h = at % p.Hkv;
-        c.piece = at / p.Hkv;
-        cut(p, c);
-        const int rows = c.ql * p.G, nb = (rows + kWeighRows - 1) / kWeighRows, pos0 = c.kl - c.ql;
-        const int* table = p.page_indices + (size_t)c.s * p.P;
-        const float2* stat = p.stat + (size_t)(p.block0[c.s] + c.h * nb) * kWeighRows;
-        int lo, hi;
-        seen_keys(p, c.kl, pos0, c.kl - 1, lo, hi);
-        const int k_lo = max(c.k_lo, lo);
-        const long long lo0 = p.logit0[c.s];
+    const int items = p.ctrl[1], lane = threadIdx.x & 31, quad = lane % 4;
+    for (int it = blockIdx.x * kWarps + (threadIdx.x >> 5); it < items; it += gridDim.x * kWarps) {
+        const int s = find_seq(p.item0, p.S, it, lane);
+        const int q0 = p.cu[s], ql = p.cu[s + 1] - q0, kl = p.kv_lens[s], pos0 = kl - ql;
+        const int base = first_key(p, kl, ql), at = it - p.item0[s], h = at % p.Hkv;
+        const int j0 = base + at / p.Hkv * kWeighKeys, j1 = min(kl, j0 + kWeighKeys);
+        const int lo = p.has_window ? max(0, pos0 - p.window + 1) : 0;  // keys below are seen by no row
+        const int rows = ql * p.G, nb = (rows + kWeighRows - 1) / kWeighRows;
+        const int* table = p.page_indices + (size_t)s * p.P;
+        const float* stat = p.stat + (size_t)(p.block0[s] + h * nb) * kWeighRows;
+        const long long lo0 = p.logit0[s];
         if (lo0 >= 0) {
-            __syncthreads();
-            if (tid < kWeighRows) s_stat[tid] = tid < rows ? stat[tid] : make_float2(0.f, 0.f);
-            __syncthreads();
+            // four keys a lane; lane r holds row r's statistic
+            constexpr int KL = kWeighKeys / 32;
             const int rs = (rows + 1) & ~1;
-            const float* x = p.logits + lo0 + (size_t)c.h * (c.kl - c.base) * rs;
-            for (int j = k_lo + tid; j < c.k_hi; j += kWeighThreads) {
-                float w = 0.f;
-                for (int r = 0; r < rs; r += 2) {
-                    const float2 v = *reinterpret_cast<const float2*>(x + (size_t)(j - c.base) * rs + r);
-                    w += ex2(v.x - s_stat[r].x) * s_stat[r].y;
-                    if (r + 1 < rows) w += ex2(v.y - s_stat[r + 1].x) * s_stat[r + 1].y;
-                }
-                add_score(p, table, c.h, j, pos0, w);
+            const float st = lane < rows ? stat[lane] : 0.f;
+            const float* x = p.logits + lo0 + (size_t)h * (kl - base) * rs;
+            float w[KL];
+            const float* xk[KL];
+            float* dst[KL];
+#pragma unroll
+            for (int k = 0; k < KL; ++k) {
+                const int j = j0 + lane + 32 * k;
+                const bool in = j >= lo && j < j1;
+                xk[k] = x + (size_t)((in ? j : j1 - 1) - base) * rs;
+                dst[k] = in ? score_at(p, table, h, j) : nullptr;
+                w[k] = 0.f;
             }
+            int r = 0;
+            if (rs % 4 == 0) {
+                for (; r < rs; r += 4) {
+                    float4 v[KL];
+#pragma unroll
+                    for (int k = 0; k < KL; ++k) v[k] = *reinterpret_cast<const float4*>(xk[k] + r);
+                    // the place behind an odd number of rows is no row's (0 times a K that may be infinite)
+                    if (r + 3 >= rows) {
+#pragma unroll
+                        for (int k = 0; k < KL; ++k) v[k].w = -INFINITY;
+                    }
+                    const float s0 = __shfl_sync(0xffffffffu, st, r), s1 = __shfl_sync(0xffffffffu, st, r + 1);
+                    const float s2 = __shfl_sync(0xffffffffu, st, r + 2), s3 = __shfl_sync(0xffffffffu, st, r + 3);
+#pragma unroll
+                    for (int k = 0; k < KL; ++k)
+                        w[k] += (ex2(v[k].x - s0) + ex2(v[k].y - s1)) + (ex2(v[k].z - s2) + ex2(v[k].w - s3));
+                }
+            } else {
+                for (; r < rs; r += 2) {
+                    float2 v[KL];
+#pragma unroll
+                    for (int k = 0; k < KL; ++k) v[k] = *reinterpret_cast<const float2*>(xk[k] + r);
+                    if (r + 1 >= rows) {
+#pragma unroll
+                        for (int k = 0; k < KL; ++k) v[k].y = -INFINITY;
+                    }
+                    const float s0 = __shfl_sync(0xffffffffu, st, r), s1 = __shfl_sync(0xffffffffu, st, r + 1);
+#pragma unroll
+                    for (int k = 0; k < KL; ++k) w[k] += ex2(v[k].x - s0) + ex2(v[k].y - s1);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < KL; ++k) add_score(dst[k], j0 + lane + 32 * k >= pos0, w[k]);
         } else {
-            const int quad = lane % 4;
-            for (int k0 = (k_lo & ~15) + 16 * warp; k0 < c.k_hi; k0 += 16 * kWarps) {
-                KeyTile<D, KT> t;
-                load_k<D, KT>(p, table, c.h, k0, c.k_hi, lane, t);
-                float w0 = 0.f, w1 = 0.f;
-                // rows whose tokens see the tile: from the first token at or behind its first key
+            for (int k0 = j0; k0 < j1; k0 += 16 * kTiles) {
+                KeyTile<D, KT> t[kTiles];
+                float w[kTiles][2];
+                const uint64_t policy = l2_policy_normal();
+#pragma unroll
+                for (int i = 0; i < kTiles; ++i) {
+                    load_k<D, KT>(p, table, h, k0 + 16 * i, j1, lane, policy, t[i]);
+                    w[i][0] = w[i][1] = 0.f;
+                }
+                const int k1 = min(j1, k0 + 16 * kTiles);
+                bool full = true;  // every key of the tiles is there
+#pragma unroll
+                for (int i = 0; i < kTiles; ++i) full = full && t[i].ok[0] && t[i].ok[1];
+                full = __all_sync(0xffffffffu, full);
+                // rows whose tokens see one of the keys
                 int r_lo = 0, r_hi = rows;
                 if (p.causal) r_lo = max(0, k0 - pos0) * p.G & ~7;
-                if (p.has_window) r_hi = min((long long)rows, max(0ll, (long long)k0 + 15 + p.window - pos0) * p.G);
-                for (int r0 = r_lo; r0 < r_hi; r0 += 8) {
-                    uint32_t q[Deal<D, KT>::REGS];
-                    load_q<D, KT>(p, c.q0, c.h, r0 + lane / 4, rows, quad, q);
-                    float acc[4] = {0.f, 0.f, 0.f, 0.f};
-                    tile_dot<D, KT>(t, q, acc);
+                if (p.has_window) r_hi = (int)min((long long)rows, max(0ll, (long long)k1 - 1 + p.window - pos0) * p.G);
+                uint32_t q[2][1][Deal<D, KT>::REGS];
+                float2 st[2];  // of rows 2 quad and 2 quad + 1
+                auto fetch = [&](int r0, int b) {
+                    load_q<D, KT>(p, q0, h, r0 + lane / 4, rows, quad, q[b][0]);
+                    st[b] = *reinterpret_cast<const float2*>(stat + r0 + 2 * quad);
+                };
+                auto add = [&](auto masked, int r0, int b) {
+                    constexpr bool MASK = decltype(masked)::value;
+                    const int r = r0 + 2 * quad;
+                    const int pa = MASK ? pos0 + p.group.div(r) : 0, pb = MASK ? pos0 + p.group.div(r + 1) : 0;
+                    // rows behind the last are no rows (0 times a K that may be infinite; no statistics)
+                    const bool ra = r < rows, rb = r + 1 < rows;
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int r = r0 + 2 * quad + i;
-                        if (r >= rows) continue;
-                        const float2 st = stat[r];
-                        const int pos = pos0 + p.group.div(r);
-                        w0 += ex2(logit(p, acc[i], k0 + lane / 4, pos, t.ok[0]) - st.x) * st.y;
-                        w1 += ex2(logit(p, acc[2 + i], k0 + lane / 4 + 8, pos, t.ok[1]) - st.x) * st.y;
+                    for (int i = 0; i < kTiles; ++i) {
+                        float acc[1][4] = {{0.f, 0.f, 0.f, 0.f}};
+                        tile_dot<D, KT, 1>(t[i], q[b], acc);
+                        scale(p, acc[0]);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int j = k0 + 16 * i + 8 * k + lane / 4;
+                            w[i][k] += (ra ? ex2(hide<MASK>(p, acc[0][2 * k], j, pa, t[i].ok[k]) - st[b].x) : 0.f) +
+                                       (rb ? ex2(hide<MASK>(p, acc[0][2 * k + 1], j, pb, t[i].ok[k]) - st[b].y) : 0.f);
+                        }
                     }
+                };
+                auto step = [&](int r0, int b) {
+                    const int a = pos0 + p.group.div(r0), z = pos0 + p.group.div(min(r0 + 7, rows - 1));
+                    if (full && !some_hidden(p, k0, k0 + 16 * kTiles, a, z)) add(std::false_type{}, r0, b);
+                    else add(std::true_type{}, r0, b);
+                };
+                if (r_lo < r_hi) fetch(r_lo, 0);
+                for (int r0 = r_lo; r0 < r_hi; r0 += 16) {
+                    if (r0 + 8 < r_hi) fetch(r0 + 8, 1);
+                    step(r0, 0);
+                    if (r0 + 16 < r_hi) fetch(r0 + 16, 0);
+                    if (r0 + 8 < r_hi) step(r0 + 8, 1);
                 }
 #pragma unroll
-                for (int o = 1; o < 4; o <<= 1) {
-                    w0 += __shfl_xor_sync(0xffffffffu, w0, o);
-                    w1 += __shfl_xor_sync(0xffffffffu, w1, o);
+                for (int i = 0; i < kTiles; ++i) {
+#pragma unroll
+                    for (int o = 1; o < 4; o <<= 1) {
+                        w[i][0] += __shfl_xor_sync(0xffffffffu, w[i][0], o);
+                        w[i][1] += __shfl_xor_sync(0xffffffffu, w[i][1], o);
+                    }
+                    const int j = k0 + 16 * i + lane / 4 + 8 * quad;
+                    if (quad < 2 && j >= lo && j < j1) add_score(score_at(p, table, h, j), j >= pos0, quad ? w[i][1] : w[i][0]);
                 }
-                const int j = k0 + lane / 4 + 8 * quad;
-                if (quad < 2 && j >= k_lo && j < c.k_hi) add_score(p, table, c.h, j, pos0, quad ? w1 : w0);
             }
         }
     }
@@ -503,13 +769,16 @@ __global__ void __launch_bounds__(kWeighThreads) rpa_weigh_kernel(const WeighPar
 
 template <int D, int KT>
 struct WeighKern {
-    static cudaError_t prepare(int* bps) {
-        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(bps, rpa_weigh_stats_kernel<D, KT>, kWeighThreads, 0);
+    static cudaError_t prepare(int* stats, int* weigh) {
+        cudaError_t e = cudaFuncSetAttribute(rpa_weigh_stats_kernel<D, KT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ring<D, KT>::SMEM);
+        if (e == cudaSuccess)
+            e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(stats, rpa_weigh_stats_kernel<D, KT>, kStatThreads, Ring<D, KT>::SMEM);
+        return e != cudaSuccess ? e : cudaOccupancyMaxActiveBlocksPerMultiprocessor(weigh, rpa_weigh_kernel<D, KT>, kWeighThreads, 0);
     }
-    static cudaError_t launch(const WeighParams& p, int grid, cudaStream_t st) {
-        cudaError_t e = launch_pdl(rpa_weigh_plan_kernel, 1, 512, 0, st, p);
-        if (e == cudaSuccess) e = launch_pdl(rpa_weigh_stats_kernel<D, KT>, grid, kWeighThreads, 0, st, p);
-        if (e == cudaSuccess) e = launch_pdl(rpa_weigh_kernel<D, KT>, grid, kWeighThreads, 0, st, p);
+    static cudaError_t launch(const CUtensorMap& kmap, const WeighParams& p, int grid_weigh, cudaStream_t st) {
+        cudaError_t e = launch_pdl(rpa_weigh_plan_kernel, 1, kPlanThreads, 0, st, p);
+        if (e == cudaSuccess) e = launch_pdl(rpa_weigh_stats_kernel<D, KT>, p.ctas, kStatThreads, Ring<D, KT>::SMEM, st, kmap, p);
+        if (e == cudaSuccess) e = launch_pdl(rpa_weigh_kernel<D, KT>, grid_weigh, kWeighThreads, 0, st, p);
         return e;
     }
 };
@@ -531,11 +800,11 @@ cudaError_t weigh_dispatch(int D, int kt, Op op) {
 
 }  // namespace
 
-cudaError_t weigh_prepare(int D, int kt, int* bps) {
-    return weigh_dispatch(D, kt, [&](auto k) { return decltype(k)::prepare(bps); });
+cudaError_t weigh_prepare(int D, int kt, int* stats, int* weigh) {
+    return weigh_dispatch(D, kt, [&](auto k) { return decltype(k)::prepare(stats, weigh); });
 }
-cudaError_t launch_weigh(const WeighParams& p, int kt, int grid, cudaStream_t st) {
-    return weigh_dispatch(p.D, kt, [&](auto k) { return decltype(k)::launch(p, grid, st); });
+cudaError_t launch_weigh(const CUtensorMap& kmap, const WeighParams& p, int kt, int grid_weigh, cudaStream_t st) {
+    return weigh_dispatch(p.D, kt, [&](auto k) { return decltype(k)::launch(kmap, p, grid_weigh, st); });
 }
 
 }  // namespace rpa
