@@ -383,7 +383,7 @@ int rpa_prefix_get_status(RpaPrefix* h, void* stream);
 void rpa_prefix_destroy(RpaPrefix* h);
 
 /* Eviction by accumulated attention weight.  scores: device, float32 [total_num_pages, Hkv, page_size],
- * beside the cache: what each cached key of each kv head has received. */
+ * 16-byte aligned, beside the cache: what each cached key of each kv head has received. */
 typedef struct RpaEvictCfg {
     RpaCfg cache;     /* RPA_KV_SPLIT */
     int64_t budget;   /* keys a sequence keeps, 1 .. pages_per_seq * page_size */

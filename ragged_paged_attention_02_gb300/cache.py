@@ -30,6 +30,7 @@ class _Handle:
     """A library handle on the device that was current when it was made."""
 
     _prefix = ""  # of the C entry points
+    _names = ()   # of the calls among them
 
     def _create(self, cfg, *more):
         import torch
@@ -40,21 +41,26 @@ class _Handle:
             raise RpaError(r, self._prefix + "create")
         self._h = h
         self._device = torch.cuda.current_device()
+        self._current = torch._C._cuda_getCurrentRawStream  # what torch.cuda.current_stream(device).cuda_stream is
+        self._calls = {name: getattr(lib(), self._prefix + name) for name in self._names}
 
     def _checks(self, c):
         """What the calls' tensors have to be, from the RpaCfg."""
         import torch
 
         self._latent = c.kv_layout == RPA_KV_LATENT
+        self._i32, self._f32 = torch.int32, torch.float32
         self._q_dtype = _q_type(c.q_dtype)
         self._q_shape = (c.num_q_tokens, c.num_q_heads, c.head_dim)
+        self._kv_rows = (c.num_q_tokens, c.num_kv_heads, c.head_dim)  # of new keys
         self._kv_shape = (c.total_num_pages, c.page_size, c.num_kv_heads * (1 if self._latent else 2), c.head_dim)
         self._kv_dtype = {RPA_DT_BF16: torch.bfloat16, RPA_DT_F16: torch.float16}.get(c.kv_dtype)  # None: one byte
         self._table_shape = (c.max_num_seqs, c.pages_per_seq)
+        self._lens_shape, self._cu_shape = (c.max_num_seqs,), (c.max_num_seqs + 1,)
         self._scores_shape = (c.total_num_pages, c.num_kv_heads, c.page_size)
 
     def _need(self, name, t, dtype, shape):
-        if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
             raise ValueError(f"{name} must be a contiguous {dtype} tensor {tuple(shape)}")
 
     def _need_cache(self, kv_pages):
@@ -64,25 +70,22 @@ class _Handle:
             raise ValueError(f"kv_pages must hold {self._kv_dtype or 'one byte'} elements")
 
     def _need_lengths(self, kv_lens, page_indices, cu_q_lens):
-        import torch
-
-        self._need("kv_lens", kv_lens, torch.int32, self._table_shape[:1])
-        self._need("page_indices", page_indices, torch.int32, self._table_shape)
+        self._need("kv_lens", kv_lens, self._i32, self._lens_shape)
+        self._need("page_indices", page_indices, self._i32, self._table_shape)
         if cu_q_lens is not None:
-            self._need("cu_q_lens", cu_q_lens, torch.int32, (self._table_shape[0] + 1,))
+            self._need("cu_q_lens", cu_q_lens, self._i32, self._cu_shape)
 
-    def _need_here(self, *tensors):
+    def _need_here(self, tensors):
+        here = self._device
         for t in tensors:
-            if t is not None and t.get_device() != self._device:
-                raise ValueError(f"every tensor must be on cuda:{self._device}, where the handle was made")
+            if t is not None and t.get_device() != here:
+                raise ValueError(f"every tensor must be on cuda:{here}, where the handle was made")
 
-    def _stream(self, stream, *tensors):
+    def _stream(self, stream, tensors=()):
         """The stream's pointer.  On another stream than the current one the tensors' memory is kept until it is done."""
-        import torch
-
-        here = torch.cuda.current_stream(self._device)
-        if stream is None or stream == here:
-            return here.cuda_stream
+        here = self._current(self._device)
+        if stream is None or stream.cuda_stream == here:
+            return here
         if stream.device.index != self._device:
             raise ValueError(f"the stream must be one of cuda:{self._device}, where the handle was made")
         for t in tensors:
@@ -93,7 +96,7 @@ class _Handle:
     def _call(self, name, *args):
         if not self._h:
             raise ValueError("the handle is closed")
-        r = getattr(lib(), self._prefix + name)(self._h, *args)
+        r = self._calls[name](self._h, *args)
         if r != RPA_OK:
             raise RpaError(r, self._prefix + name)
 
@@ -153,6 +156,7 @@ class RopeAppend(_Handle):
     """
 
     _prefix = "rpa_rope_"
+    _names = ("append",)
 
     def __init__(self, **cfg):
         self._h = None
@@ -161,21 +165,19 @@ class RopeAppend(_Handle):
         self._checks(self._c.cache)
 
     def _check(self, q, k, v, kv_pages, kv_lens, page_indices, cu_q_lens, positions, q_out):
-        import torch
-
         T, Hq, D = self._q_shape
-        rows = (T, self._c.cache.num_kv_heads, D)
+        rows = self._kv_rows
         if (v is None) != self._latent:
             raise ValueError("v is None with the latent layout, whose rows are k, and only there")
         for name, t, shape in (("q", q, self._q_shape), ("k", k, rows), ("v", v, rows)):
             if t is None:
                 continue
-            if t.dtype != self._q_dtype or t.shape != shape or (T and (t.stride(2) != 1 or t.stride(1) != D)):
+            if t.dtype is not self._q_dtype or t.shape != shape or (T and t.stride()[1:] != (D, 1)):
                 raise ValueError(f"{name} must be a {self._q_dtype} tensor {tuple(shape)} whose tokens' heads are contiguous")
         self._need_cache(kv_pages)
         self._need_lengths(kv_lens, page_indices, cu_q_lens)
         if positions is not None:
-            self._need("positions", positions, torch.int32, (T,))
+            self._need("positions", positions, self._i32, (T,))
         self._need("q_out", q_out, self._q_dtype, self._q_shape)
 
     def append(self, q, k, v, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, positions=None, q_out=None, stream=None):
@@ -185,22 +187,22 @@ class RopeAppend(_Handle):
         fused projection).  kv_lens counts the new tokens: token i of a sequence goes to slot kv_len - q_len + i,
         which is its position too unless ``positions`` (int32 [T]) gives another.
         """
-        import torch
-
         if q_out is None:
+            import torch
+
             with torch.cuda.stream(stream):
                 q_out = torch.zeros(self._q_shape, dtype=self._q_dtype, device=q.device)
         self._check(q, k, v, kv_pages, kv_lens, page_indices, cu_q_lens, positions, q_out)
         tensors = (q, k, v, kv_pages, kv_lens, page_indices, cu_q_lens, positions, q_out)
-        self._need_here(*tensors)
+        self._need_here(tensors)
         # the distance of two tokens; with one token any will do
         far = self._q_shape[0] > 1
-        rows = self._c.cache.num_kv_heads * self._q_shape[2]
+        rows = self._kv_rows[1] * self._kv_rows[2]
         self._call("append", q.data_ptr(), q.stride(0) if far else self._q_shape[1] * self._q_shape[2],
                    k.data_ptr(), k.stride(0) if far else rows, None if v is None else v.data_ptr(),
                    0 if v is None else v.stride(0) if far else rows, kv_pages.data_ptr(), kv_lens.data_ptr(),
                    page_indices.data_ptr(), cu_q_lens.data_ptr(), None if positions is None else positions.data_ptr(),
-                   int(num_seqs), q_out.data_ptr(), self._stream(stream, *tensors))
+                   int(num_seqs), q_out.data_ptr(), self._stream(stream, tensors))
         return q_out
 
 
@@ -225,6 +227,7 @@ class CacheEviction(_Handle):
     """
 
     _prefix = "rpa_evict_"
+    _names = ("accumulate", "compact")
 
     def __init__(self, **cfg):
         import torch
@@ -238,33 +241,29 @@ class CacheEviction(_Handle):
         self._checks(self._c.cache)
 
     def _check_accumulate(self, q, kv_pages, kv_lens, page_indices, cu_q_lens, scores):
-        import torch
-
         self._need("q", q, self._q_dtype, self._q_shape)
         self._need_cache(kv_pages)
         self._need_lengths(kv_lens, page_indices, cu_q_lens)
-        self._need("scores", scores, torch.float32, self._scores_shape)
+        self._need("scores", scores, self._f32, self._scores_shape)
 
     def accumulate(self, q, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, scores, stream=None):
         """Add the softmax weight each key gets from the call's queries to ``scores``, and return it.  The keys of
         the call's own tokens (each sequence's last q_len) start from 0."""
         self._check_accumulate(q, kv_pages, kv_lens, page_indices, cu_q_lens, scores)
         tensors = (q, kv_pages, kv_lens, page_indices, cu_q_lens, scores)
-        self._need_here(*tensors)
+        self._need_here(tensors)
         self._call("accumulate", q.data_ptr(), kv_pages.data_ptr(), kv_lens.data_ptr(), page_indices.data_ptr(),
-                   cu_q_lens.data_ptr(), int(num_seqs), scores.data_ptr(), self._stream(stream, *tensors))
+                   cu_q_lens.data_ptr(), int(num_seqs), scores.data_ptr(), self._stream(stream, tensors))
         return scores
 
     def _check_compact(self, kv_pages, scores, kv_lens, page_indices, new_page_indices, new_kv_lens, kept):
-        import torch
-
         self._need_cache(kv_pages)
-        self._need("scores", scores, torch.float32, self._scores_shape)
+        self._need("scores", scores, self._f32, self._scores_shape)
         self._need_lengths(kv_lens, page_indices, None)
-        self._need("new_page_indices", new_page_indices, torch.int32, self._table_shape)
-        self._need("new_kv_lens", new_kv_lens, torch.int32, self._table_shape[:1])
+        self._need("new_page_indices", new_page_indices, self._i32, self._table_shape)
+        self._need("new_kv_lens", new_kv_lens, self._i32, self._lens_shape)
         if kept is not None:
-            self._need("kept", kept, torch.int32, (self._table_shape[0], self._c.cache.num_kv_heads, self._c.budget))
+            self._need("kept", kept, self._i32, (self._table_shape[0], self._c.cache.num_kv_heads, self._c.budget))
 
     def compact(self, kv_pages, scores, kv_lens, page_indices, num_seqs, new_page_indices=None, new_kv_lens=None, kept=None,
                 stream=None):
@@ -273,19 +272,19 @@ class CacheEviction(_Handle):
         The kept keys' rows and scores move, in order, to the first slots of new_page_indices' pages (default:
         page_indices, in place).  ``kept`` (int32 [max_num_seqs, Hkv, budget]) receives the slots they had.
         """
-        import torch
-
         if new_page_indices is None:
             new_page_indices = page_indices
         if new_kv_lens is None:
+            import torch
+
             with torch.cuda.stream(stream):
                 new_kv_lens = kv_lens.clone()
         self._check_compact(kv_pages, scores, kv_lens, page_indices, new_page_indices, new_kv_lens, kept)
         tensors = (kv_pages, scores, kv_lens, page_indices, new_page_indices, new_kv_lens, kept)
-        self._need_here(*tensors)
+        self._need_here(tensors)
         self._call("compact", kv_pages.data_ptr(), scores.data_ptr(), kv_lens.data_ptr(), page_indices.data_ptr(), int(num_seqs),
                    new_page_indices.data_ptr(), new_kv_lens.data_ptr(), None if kept is None else kept.data_ptr(),
-                   self._stream(stream, *tensors))
+                   self._stream(stream, tensors))
         return new_kv_lens
 
 
@@ -300,6 +299,7 @@ class SharedPrefixAttention(_Handle):
     """
 
     _prefix = "rpa_prefix_"
+    _names = ("forward",)
 
     def __init__(self, *, max_groups=1, **cfg):
         import torch
@@ -314,30 +314,28 @@ class SharedPrefixAttention(_Handle):
         self._checks(self._c)
 
     def _check(self, q, kv_pages, kv_lens, page_indices, cu_q_lens, cu_groups, prefix_lens, num_groups, out):
-        import torch
-
         self._need("q", q, self._q_dtype, self._q_shape)
         self._need("out", out, self._q_dtype, self._q_shape)
         self._need_cache(kv_pages)
         self._need_lengths(kv_lens, page_indices, cu_q_lens)
         for name, t, n in (("cu_groups", cu_groups, num_groups + 1), ("prefix_lens", prefix_lens, num_groups)):
-            if t.dtype != torch.int32 or t.dim() != 1 or t.shape[0] < n or not t.is_contiguous():
+            if t.dtype is not self._i32 or t.dim() != 1 or t.shape[0] < n or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous int32 tensor of at least {n}")
 
     def forward(self, q, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, cu_groups, prefix_lens, num_groups, out=None,
                 stream=None):
         """RaggedPagedAttention.forward's result.  Group g is the sequences [cu_groups[g], cu_groups[g + 1]), which have
         their first prefix_lens[g] keys in common, read through the first one's page table."""
-        import torch
-
         num_groups = int(num_groups)
         if out is None:
+            import torch
+
             with torch.cuda.stream(stream):
                 out = torch.empty(self._q_shape, dtype=self._q_dtype, device=q.device)
         self._check(q, kv_pages, kv_lens, page_indices, cu_q_lens, cu_groups, prefix_lens, num_groups, out)
         tensors = (q, kv_pages, kv_lens, page_indices, cu_q_lens, cu_groups, prefix_lens, out)
-        self._need_here(*tensors)
+        self._need_here(tensors)
         self._call("forward", q.data_ptr(), kv_pages.data_ptr(), kv_lens.data_ptr(), page_indices.data_ptr(), cu_q_lens.data_ptr(),
                    int(num_seqs), cu_groups.data_ptr(), prefix_lens.data_ptr(), num_groups, out.data_ptr(),
-                   self._stream(stream, *tensors))
+                   self._stream(stream, tensors))
         return out

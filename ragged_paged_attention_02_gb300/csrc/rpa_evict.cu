@@ -33,6 +33,7 @@ namespace {
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
+constexpr int kMaxCluster = 8;
 constexpr int kSelCached = 40 * 1024;  // scores a CTA keeps at most (160 KB); further ones are read again
 constexpr int kMoveThreads = 256;
 constexpr int kMoveCtas = 4;  // resident an SM
@@ -53,12 +54,22 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 __device__ __forceinline__ void cluster_sync() {
     asm volatile("barrier.cluster.arrive.aligned;\nbarrier.cluster.wait.aligned;\n" ::: "memory");
 }
-// Two words of CTA `rank`'s shared memory, at the place that `addr` has in this CTA's
+// Words of CTA `rank`'s shared memory, at the place that `addr` has in this CTA's
 __device__ __forceinline__ uint2 cluster_load2(uint32_t addr, uint32_t rank) {
     uint32_t at;
     uint2 v;
     asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(at) : "r"(addr), "r"(rank));
     asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint4 cluster_load4(uint32_t addr, uint32_t rank) {
+    uint32_t at;
+    uint4 v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(at) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];\n"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(at)
+                 : "memory");
     return v;
 }
 // Exclusive sum of v over the block's threads before this one, and the total
@@ -83,15 +94,18 @@ __device__ __forceinline__ uint32_t block_before(uint32_t v, uint32_t* s_warp, u
     return sum - v + (warp > 0 ? before : 0u);
 }
 
-__global__ void __launch_bounds__(kSelThreads) rpa_evict_select_kernel(const CompactParams p) {
-    extern __shared__ uint32_t s_key[];  // [cached] the scores of the first of this CTA's competing keys
+// CLUSTER: several CTAs a unit (few units); else one (many: as many resident as there are registers for, three an SM).
+// (1024 threads a CTA of a cluster took 42 us for 2 x 100 k keys where 512 take 34.)
+template <bool CLUSTER>
+__global__ void __launch_bounds__(kSelThreads, CLUSTER ? 1 : 3) rpa_evict_select_kernel(const CompactParams p) {
+    extern __shared__ __align__(16) uint32_t s_key[];  // [cached] the scores of the first of this CTA's competing keys
     __shared__ __align__(16) uint32_t s_hist[2][kBins];
     __shared__ uint32_t s_warp[kSelWarps], s_warp2[kSelWarps];
     __shared__ __align__(8) uint32_t s_count[2];  // of this CTA: keys above the threshold, keys equal to it
     __shared__ uint32_t s_digit, s_left;
     __shared__ int s_order;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int C = p.cluster, rank = (int)cluster_rank(), unit = blockIdx.x / C;
+    const int C = CLUSTER ? p.cluster : 1, rank = CLUSTER ? (int)cluster_rank() : 0, unit = blockIdx.x / C;
     const int s = unit / p.Hkv, h = unit - s * p.Hkv;
     pdl_trigger();
     pdl_wait();
@@ -132,37 +146,54 @@ __global__ void __launch_bounds__(kSelThreads) rpa_evict_select_kernel(const Com
     }
     for (int i = me; i < p.protect; i += step) list[i] = i;
     for (int i = me; i < p.recent; i += step) list[p.budget - p.recent + i] = n - p.recent + i;
-    // the competing keys [protect, protect + m) and their places; this CTA's share [a, b) of them
-    const int m = n - p.protect - p.recent;
     const uint32_t k = (uint32_t)(p.budget - p.protect - p.recent);
     if (k == 0) return;
-    const int share = (m + C - 1) / C, a = min(m, rank * share), b = min(m, a + share), mine = b - a;
-    auto score = [&](int i) -> uint32_t {  // of this CTA's key i
-        const int j = p.protect + a + i, lp = p.page.div(j), pg = __ldg(table + lp);
+    // the competing keys [lo_key, hi_key), in quads of neighbouring slots (page sizes are multiples of 4); this CTA's
+    // share is `mine` quads from quad q0 on, of which the first and the last may hold keys that do not compete
+    const int lo_key = p.protect, hi_key = n - p.recent;
+    const int quads = (hi_key + 3) / 4 - lo_key / 4, share = (quads + C - 1) / C;
+    const int q0 = lo_key / 4 + min(quads, rank * share), mine = min(share, max(0, quads - rank * share));
+    auto load = [&](int i) -> uint4 {  // quad i of this CTA's
+        const int j = 4 * (q0 + i), lp = p.page.div(j), pg = __ldg(table + lp);
         if ((unsigned)pg >= (unsigned)p.N) {
             set_status(p.status, RPA_ERR_BAD_PAGE_INDEX);
-            return 0u;
+            return make_uint4(0u, 0u, 0u, 0u);
         }
-        return ordered(p.scores[((size_t)pg * p.Hkv + h) * p.ps + (j - lp * p.ps)]);
+        const float4 x = *reinterpret_cast<const float4*>(p.scores + ((size_t)pg * p.Hkv + h) * p.ps + (j - lp * p.ps));
+        return make_uint4(ordered(x.x), ordered(x.y), ordered(x.z), ordered(x.w));
     };
-    auto key = [&](int i) { return i < p.cached ? s_key[i] : score(i); };
+    uint4* s_quad = reinterpret_cast<uint4*>(s_key);
+    const int cached = p.cached / 4;
+    auto quad = [&](int i) { return i < cached ? s_quad[i] : load(i); };
+    // bit e: element e of quad i competes
+    auto inside = [&](int i) -> uint32_t {
+        const int j = 4 * (q0 + i);
+        uint32_t m = 15u;
+        if (j < lo_key) m &= 15u << (lo_key - j);
+        if (j + 4 > hi_key) m &= 15u >> (j + 4 - hi_key);
+        return m;
+    };
     // the first digit's histogram while the scores come in
     for (int i = tid; i < kBins; i += kSelThreads) s_hist[0][i] = 0;
     __syncthreads();
     constexpr int kFly = 4;
     for (int i0 = tid; i0 < mine; i0 += kFly * kSelThreads) {
-        uint32_t u[kFly];
+        uint4 u[kFly];
 #pragma unroll
         for (int f = 0; f < kFly; ++f) {
             const int i = i0 + f * kSelThreads;
-            u[f] = i < mine ? score(i) : 0u;
+            if (i < mine) u[f] = load(i);
         }
 #pragma unroll
         for (int f = 0; f < kFly; ++f) {
             const int i = i0 + f * kSelThreads;
             if (i < mine) {
-                if (i < p.cached) s_key[i] = u[f];
-                atomicAdd(&s_hist[0][u[f] >> 21], 1u);
+                if (i < cached) s_quad[i] = u[f];
+                const uint32_t in = inside(i);
+                if (in & 1u) atomicAdd(&s_hist[0][u[f].x >> 21], 1u);
+                if (in & 2u) atomicAdd(&s_hist[0][u[f].y >> 21], 1u);
+                if (in & 4u) atomicAdd(&s_hist[0][u[f].z >> 21], 1u);
+                if (in & 8u) atomicAdd(&s_hist[0][u[f].w >> 21], 1u);
             }
         }
     }
@@ -177,25 +208,44 @@ __global__ void __launch_bounds__(kSelThreads) rpa_evict_select_kernel(const Com
             for (int i = tid; i < kBins; i += kSelThreads) hist[i] = 0;
             __syncthreads();
             for (int i = tid; i < mine; i += kSelThreads) {
-                const uint32_t u = key(i);
-                if ((u >> (shift + bits)) == prefix) atomicAdd(&hist[(u >> shift) & ((1u << bits) - 1)], 1u);
+                const uint4 u = quad(i);
+                const uint32_t in = inside(i);
+                auto count = [&](uint32_t v, uint32_t bit) {
+                    if ((v >> (shift + bits)) == prefix && (in & bit)) atomicAdd(&hist[(v >> shift) & ((1u << bits) - 1)], 1u);
+                };
+                count(u.x, 1u);
+                count(u.y, 2u);
+                count(u.z, 4u);
+                count(u.w, 8u);
             }
         }
-        cluster_sync();
-        // thread t: bins kBins - 1 - 4 t down to kBins - 4 - 4 t, over all CTAs
+        if (CLUSTER) cluster_sync();
+        else __syncthreads();
+        // thread t: the kMine bins from kBins - 1 - kMine t down, over all CTAs; c[0] the highest
         constexpr int kMine = kBins / kSelThreads;
-        static_assert(kMine == 4, "two 8-byte loads a CTA");
+        static_assert(kMine == 4, "one load a CTA");
         const int low = kBins - kMine * (tid + 1);
-        uint32_t c[kMine] = {0, 0, 0, 0};
-        const uint32_t at = smem_u32(hist + low);
-        for (int r = 0; r < C; ++r) {
-            const uint2 x = cluster_load2(at, r), y = cluster_load2(at + 8, r);
-            c[3] += x.x;
-            c[2] += x.y;
-            c[1] += y.x;
-            c[0] += y.y;  // the highest of the four
+        uint32_t c[kMine];
+        if constexpr (CLUSTER) {
+            uint4 x[kMaxCluster];  // all CTAs' loads in flight
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r) x[r] = r < C ? cluster_load4(smem_u32(hist + low), r) : make_uint4(0u, 0u, 0u, 0u);
+            c[0] = c[1] = c[2] = c[3] = 0;
+#pragma unroll
+            for (int r = 0; r < kMaxCluster; ++r) {
+                c[3] += x[r].x;
+                c[2] += x[r].y;
+                c[1] += x[r].z;
+                c[0] += x[r].w;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kMine; ++i) c[i] = hist[low + kMine - 1 - i];
         }
-        uint32_t total, above = block_before(c[0] + c[1] + c[2] + c[3], s_warp, total);
+        uint32_t mine_sum = 0;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) mine_sum += c[i];
+        uint32_t total, above = block_before(mine_sum, s_warp, total);
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
             if (above < left && left <= above + c[i]) {
@@ -211,40 +261,66 @@ __global__ void __launch_bounds__(kSelThreads) rpa_evict_select_kernel(const Com
     }
     // list the kept slots in order: keys above the threshold and the first `left` that equal it
     const int run = ((mine + kSelWarps - 1) / kSelWarps + 31) & ~31, lo = min(mine, warp * run), hi = min(mine, lo + run);
+    // of quad i: bits of the keys above the threshold, and 4 places up of those that equal it
+    auto sift = [&](int i) -> uint32_t {
+        const uint4 u = quad(i);
+        const uint32_t in = inside(i);
+        const uint32_t g = (u.x > prefix ? 1u : 0u) | (u.y > prefix ? 2u : 0u) | (u.z > prefix ? 4u : 0u) | (u.w > prefix ? 8u : 0u);
+        const uint32_t e = (u.x == prefix ? 1u : 0u) | (u.y == prefix ? 2u : 0u) | (u.z == prefix ? 4u : 0u) | (u.w == prefix ? 8u : 0u);
+        return (g & in) | (e & in) << 4;
+    };
     uint32_t gt = 0, eq = 0;
     for (int i = lo + lane; i < hi; i += 32) {
-        const uint32_t u = key(i);
-        gt += u > prefix;
-        eq += u == prefix;
+        const uint32_t m = sift(i);
+        gt += __popc(m & 15u);
+        eq += __popc(m >> 4);
     }
     gt = __reduce_add_sync(0xffffffffu, gt);
     eq = __reduce_add_sync(0xffffffffu, eq);
     uint32_t all_gt, all_eq;
-    uint32_t g0 = block_before(lane == 0 ? gt : 0u, s_warp, all_gt), e0 = block_before(lane == 0 ? eq : 0u, s_warp2, all_eq);
+    uint32_t g0 = block_before(lane == 0 ? gt : 0u, s_warp, all_gt);
+    uint32_t e0 = block_before(lane == 0 ? eq : 0u, s_warp2, all_eq);
     g0 = __shfl_sync(0xffffffffu, g0, 0);
     e0 = __shfl_sync(0xffffffffu, e0, 0);
-    if (tid == 0) {
-        s_count[0] = all_gt;
-        s_count[1] = all_eq;
-    }
-    cluster_sync();
-    for (int r = 0; r < rank; ++r) {
-        const uint2 v = cluster_load2(smem_u32(s_count), r);
-        g0 += v.x;
-        e0 += v.y;
+    if constexpr (CLUSTER) {
+        if (tid == 0) {
+            s_count[0] = all_gt;
+            s_count[1] = all_eq;
+        }
+        cluster_sync();
+        const uint2 v = lane < rank ? cluster_load2(smem_u32(s_count), lane) : make_uint2(0u, 0u);  // lane r: CTA r
+        g0 += __reduce_add_sync(0xffffffffu, v.x);
+        e0 += __reduce_add_sync(0xffffffffu, v.y);
     }
     for (int i = lo; i < hi; i += 32) {
-        const bool in = i + lane < hi;
-        const uint32_t u = in ? key(i + lane) : 0u;
-        const uint32_t mg = __ballot_sync(0xffffffffu, in && u > prefix), me_ = __ballot_sync(0xffffffffu, in && u == prefix);
-        const uint32_t below = (1u << lane) - 1u;
-        const uint32_t e = e0 + __popc(me_ & below);
-        if (in && (u > prefix || (u == prefix && e < left)))
-            list[p.protect + g0 + __popc(mg & below) + min(e, left)] = p.protect + a + i + lane;
-        g0 += __popc(mg);
-        e0 += __popc(me_);
+        const uint32_t m = i + lane < hi ? sift(i + lane) : 0u;
+        // both counts of the lanes before this one in one scan (at most 128 each)
+        const uint32_t own = __popc(m & 15u) | __popc(m >> 4) << 16;
+        uint32_t sum = own;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint32_t y = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o) sum += y;
+        }
+        uint32_t g = g0 + ((sum - own) & 0xffffu), e = e0 + ((sum - own) >> 16);
+        const uint32_t all = __shfl_sync(0xffffffffu, sum, 31);
+        g0 += all & 0xffffu;
+        e0 += all >> 16;
+        if (m == 0u) continue;
+        int* out = list + p.protect;
+        const int j = 4 * (q0 + i + lane);
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            if (m >> x & 1u) {
+                out[g + min(e, left)] = j + x;
+                ++g;
+            } else if (m >> (4 + x) & 1u) {
+                if (e < left) out[g + e] = j + x;
+                ++e;
+            }
+        }
     }
-    cluster_sync();  // no CTA leaves while another may read its counts
+    if (CLUSTER) cluster_sync();  // no CTA leaves while another may read its counts
 }
 
 __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) rpa_evict_move_kernel(const CompactParams p) {
@@ -324,11 +400,12 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) rpa_evict_move_kernel
 cudaError_t compact_prepare(int64_t units, int max_keys, int sms, int* cluster, int* cached) {
     // as many CTAs a unit as two an SM allow, of 2 k keys at least
     int c = 1;
-    while (c < 8 && units * (2 * c) <= 2 * sms && max_keys / (2 * c) >= 2048) c *= 2;
+    while (c < kMaxCluster && units * (2 * c) <= 2 * sms && max_keys / (2 * c) >= 2048) c *= 2;
     *cluster = c;
-    const int share = (max_keys + c - 1) / c;
+    const int share = ((max_keys + 3) / 4 + 1 + c - 1) / c * 4;  // (one quad more where neither end is a quad's)
     *cached = share < kSelCached ? share : kSelCached;
-    return cudaFuncSetAttribute(rpa_evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSelCached * 4);
+    return cudaFuncSetAttribute(c > 1 ? rpa_evict_select_kernel<true> : rpa_evict_select_kernel<false>,
+                                cudaFuncAttributeMaxDynamicSharedMemorySize, kSelCached * 4);
 }
 
 cudaError_t launch_compact(const CompactParams& p, int sms, cudaStream_t st) {
@@ -345,8 +422,8 @@ cudaError_t launch_compact(const CompactParams& p, int sms, cudaStream_t st) {
     attr[1].val.clusterDim.x = p.cluster;
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
-    cudaError_t e = cudaLaunchKernelEx(&cfg, rpa_evict_select_kernel, p);
+    cfg.numAttrs = p.cluster > 1 ? 2 : 1;
+    cudaError_t e = cudaLaunchKernelEx(&cfg, p.cluster > 1 ? rpa_evict_select_kernel<true> : rpa_evict_select_kernel<false>, p);
     if (e == cudaSuccess) e = launch_pdl(rpa_evict_move_kernel, sms * kMoveCtas, kMoveThreads, 0, st, p);
     return e;
 }
@@ -508,7 +585,7 @@ int rpa_evict_accumulate(RpaEvict* h, const void* q, const void* kv_pages, const
     if (!kv_pages || !kv_lens || !page_indices || !cu_q_lens || !scores) return RPA_ERR_INVALID_ARG;
     if (c.num_q_tokens > 0 && !q) return RPA_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(kv_pages, 16) || !aligned(kv_lens, 4) || !aligned(page_indices, 4) ||
-        !aligned(cu_q_lens, 4) || !aligned(scores, 4))
+        !aligned(cu_q_lens, 4) || !aligned(scores, 16))
         return RPA_ERR_INVALID_ARG;
     DeviceGuard g(h->device);
     if (!g.ok) return RPA_ERR_CUDA;
@@ -549,7 +626,7 @@ int rpa_evict_compact(RpaEvict* h, void* kv_pages, float* scores, const int32_t*
     const RpaCfg& c = h->cfg.cache;
     if (num_seqs < 0 || num_seqs > c.max_num_seqs) return RPA_ERR_INVALID_ARG;
     if (!kv_pages || !scores || !kv_lens || !page_indices || !new_page_indices || !new_kv_lens) return RPA_ERR_INVALID_ARG;
-    if (!aligned(kv_pages, 16) || !aligned(scores, 4) || !aligned(kv_lens, 4) || !aligned(page_indices, 4) ||
+    if (!aligned(kv_pages, 16) || !aligned(scores, 16) || !aligned(kv_lens, 4) || !aligned(page_indices, 4) ||
         !aligned(new_page_indices, 4) || !aligned(new_kv_lens, 4) || !aligned(kept, 4))
         return RPA_ERR_INVALID_ARG;
     DeviceGuard g(h->device);
