@@ -538,8 +538,10 @@ __global__ void __launch_bounds__(kThreads, 1) rpa_prefill_tc(const __grid_const
             const int rows_used = ntx * G;
             if (part >= 0) {
                 // a piece of a shared prefix, or the keys behind one: the unnormalised O, the running max
-                // (log2 domain) and the row sum go to the 256 rows (16 slots) from slot `part` on
+                // (log2 domain) and the row sum go to the 256 rows (16 slots) from slot `part` on.  O lies there
+                // in blocks of eight columns, [D / 8][256 rows][8]: a warp's store is 1 KB in one piece
                 const size_t prow = (size_t)part * kDecRows + x * kM + r;
+                float* po = a.part_o + (size_t)part * kDecRows * D + (x * kM + r) * 8;
 #pragma unroll 1
                 for (int c = 0; c < D / 32; ++c) {
                     uint32_t ov[32];
@@ -547,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1) rpa_prefill_tc(const __grid_const
                     tmem_ld_wait();
                     if (r < rows_used) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) store_f32x8(a.part_o + prow * D + c * 32 + i * 8, ov + 8 * i);
+                        for (int i = 0; i < 4; ++i) store_f32x8(po + (c * 4 + i) * (2 * kM * 8), ov + 8 * i);
                     }
                 }
                 if (r < rows_used) *reinterpret_cast<float2*>(a.part_ml + prow * 2) = make_float2(m_run, l_run);

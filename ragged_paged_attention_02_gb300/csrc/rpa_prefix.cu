@@ -27,6 +27,7 @@ namespace rpa {
 namespace {
 
 constexpr int kPieceAlign = 128;   // keys: the prefill kernels' tiles
+constexpr int kPieceKeys = 256;    // smallest decode piece: the keys behind a prefix are few, and so is what fills the SMs
 constexpr int kPieceCost = 256;    // what a piece costs beside its keys, in keys
 constexpr int kMaxPieces = 512;    // candidates, one a planner thread
 static_assert(kMaxPieces == kPlanThreads, "a candidate a thread");
@@ -40,44 +41,41 @@ struct PrefixPlan {
     int max_dec_units, max_pf_units, max_part, item_room;
     int* ctrl;
     // per virtual sequence: groups 0 .. NG - 1, an empty one, sequences NG + 1 ..
-    int *vcu, *vkv, *vrow, *vpart, *vpieces, *dec_end, *pf_end;
+    int *vcu, *vkv, *vrow;      // what the attention kernels read: first token, keys, row of the page table
+    int4* vrec;                 // what the merge reads: first token, first partial slot, pieces (< 0: of prefill tiles)
+    int2* token;                // [T]
+    int* scratch;               // [kArrays, virtual sequences], used where they overflow shared memory
     Unit *dec_units, *pf_units;
 };
 
-// The class of a virtual sequence: 0 no work, 1 decode pieces, 2 prefill tiles
-struct Virtual {
-    int q0, ql, begin, end, row, cls;
+constexpr int kArrays = 6;
+constexpr int kVirtualSmem = 1536;  // virtual sequences whose records fit in shared memory (36 KB)
+
+// The records of the virtual sequences: keys [begin, end) for ql tokens; class 0 no work, 1 decode pieces, 2 prefill
+// tiles; units of each kind up to and with this one
+struct Records {
+    int *q0, *ql, *begin, *end, *dec_end, *pf_end;
+    __device__ __forceinline__ int cls(const PrefixPlan& p, int v) const {
+        return ql[v] == 0 || end[v] <= begin[v] ? 0 : (long long)ql[v] * p.G <= p.dec_rows ? 1 : 2;
+    }
 };
 
-__device__ __forceinline__ Virtual virtual_seq(const PrefixPlan& p, int v) {
-    Virtual r;
-    if (v < p.NG) {
-        r.row = p.cu_groups[v];
-        r.q0 = p.cu[r.row];
-        r.ql = p.cu[p.cu_groups[v + 1]] - r.q0;
-        r.begin = 0;
-        r.end = p.prefix_lens[v];
-    } else if (v == p.NG) {
-        r.row = r.ql = r.begin = r.end = 0;
-        r.q0 = 0;
-    } else {
-        r.row = v - p.NG - 1;
-        r.q0 = p.cu[r.row];
-        r.ql = p.cu[r.row + 1] - r.q0;
-        r.begin = p.prefix_lens[upper_seq(p.cu_groups + 1, p.NG, r.row)];
-        r.end = p.kv_lens[r.row];
-    }
-    r.cls = r.ql == 0 || r.end <= r.begin ? 0 : (long long)r.ql * p.G <= p.dec_rows ? 1 : 2;
-    return r;
-}
-
 __global__ void __launch_bounds__(kPlanThreads, 1) rpa_prefix_plan_kernel(const PrefixPlan p) {
+    __shared__ int s_rec[kArrays * kVirtualSmem];
     __shared__ int s_scan[33 * 3];
     __shared__ unsigned long long s_red[64];
     __shared__ int s_bad, s_longest;
     const int tid = threadIdx.x, S = p.S, NG = p.NG, V = S > 0 ? NG + 1 + S : 0;
     int* ctrl = p.ctrl;
     const int Tq = p.pf_tokens;
+    Records R;
+    {
+        int* base = V <= kVirtualSmem ? s_rec : p.scratch;
+        const int n = V <= kVirtualSmem ? kVirtualSmem : V;
+        int** to[kArrays] = {&R.q0, &R.ql, &R.begin, &R.end, &R.dec_end, &R.pf_end};
+#pragma unroll
+        for (int i = 0; i < kArrays; ++i) *to[i] = base + (size_t)i * n;
+    }
     pdl_trigger();
     pdl_wait();
     auto give_up = [&](int code) {  // no items; the merge writes zeros
@@ -93,10 +91,18 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_prefix_plan_kernel(const 
         s_longest = 0;
     }
     __syncthreads();
-    // ---- 1. groups first (the sequences' checks look theirs up), then sequences
+    // ---- 1. groups first (the sequences look theirs up), then sequences
     for (int g = tid; g < NG; g += kPlanThreads) {
         const int a = p.cu_groups[g], b = p.cu_groups[g + 1], n = p.prefix_lens[g];
-        if (a < 0 || b < a || b > S || n < 0 || n > p.P * p.ps) s_bad = 1;
+        if (a < 0 || b < a || b > S || n < 0 || n > p.P * p.ps) {
+            s_bad = 1;
+        } else if (V > 0) {
+            R.q0[g] = p.cu[a];
+            R.ql[g] = p.cu[b] - p.cu[a];
+            R.begin[g] = 0;
+            R.end[g] = n;
+            p.vrow[g] = a;
+        }
     }
     __syncthreads();
     if (s_bad) {
@@ -104,9 +110,23 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_prefix_plan_kernel(const 
         return;
     }
     for (int s = tid; s < S; s += kPlanThreads) {
-        const int q0 = p.cu[s], q1 = p.cu[s + 1], kl = p.kv_lens[s], ql = q1 - q0;
-        if (q0 < 0 || ql < 0 || kl < 0 || kl > p.P * p.ps || ql > kl || q1 > p.T) s_bad = 1;
-        else if (ql > 0 && p.prefix_lens[upper_seq(p.cu_groups + 1, NG, s)] > kl - ql) s_bad = 1;
+        const int q0 = p.cu[s], q1 = p.cu[s + 1], kl = p.kv_lens[s], ql = q1 - q0, v = NG + 1 + s;
+        const int g = upper_seq(p.cu_groups + 1, NG, s), pre = R.end[g];
+        if (q0 < 0 || ql < 0 || kl < 0 || kl > p.P * p.ps || ql > kl || q1 > p.T || (ql > 0 && pre > kl - ql)) {
+            s_bad = 1;
+        } else {
+            R.q0[v] = q0;
+            R.ql[v] = ql;
+            R.begin[v] = pre;
+            R.end[v] = kl;
+            p.vrow[v] = s;
+        }
+    }
+    if (tid == 0 && V > 0) {
+        R.q0[NG] = p.cu[S];  // the last group's end: the pair (v, v + 1) of every other is its tokens
+        R.ql[NG] = R.begin[NG] = R.end[NG] = 0;
+        p.vrow[NG] = 0;
+        p.vcu[V] = p.cu[S];
     }
     __syncthreads();
     if (s_bad) {
@@ -116,11 +136,11 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_prefix_plan_kernel(const 
     // ---- 2. work of the two kernels: key x kv head pairs of decode pieces, tile x key x kv head of prefill tiles
     unsigned long long dec_keys = 0, pf_keys = 0;
     for (int v = tid; v < V; v += kPlanThreads) {
-        const Virtual r = virtual_seq(p, v);
-        if (r.cls == 1) dec_keys += (unsigned long long)(r.end - r.begin) * p.Hkv;
-        if (r.cls == 2) {
-            pf_keys += (unsigned long long)((r.ql + Tq - 1) / Tq) * (unsigned long long)(r.end - r.begin) * p.Hkv;
-            if (v < NG) atomicMax(&s_longest, r.end);
+        const int cls = R.cls(p, v), keys = R.end[v] - R.begin[v];
+        if (cls == 1) dec_keys += (unsigned long long)keys * p.Hkv;
+        if (cls == 2) {
+            pf_keys += (unsigned long long)((R.ql[v] + Tq - 1) / Tq) * (unsigned long long)keys * p.Hkv;
+            if (v < NG) atomicMax(&s_longest, R.end[v]);
         }
     }
     block_sum64x2(dec_keys, pf_keys, s_red);
@@ -144,16 +164,15 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_prefix_plan_kernel(const 
     // ---- 4. keys of a decode piece, and of a piece of a prefix's tiles
     const int on = p.dec_on_pf ? pf_ctas : dec_ctas;
     unsigned long long want = dec_keys / (unsigned long long)max(1, p.dec_waves * on) + 1;
-    const int chunk = (int)min(max((want + kChunkAlign - 1) / kChunkAlign * kChunkAlign, (unsigned long long)kMinChunk), 1ull << 30);
+    const int chunk = (int)min(max((want + kChunkAlign - 1) / kChunkAlign * kChunkAlign, (unsigned long long)kPieceKeys), 1ull << 30);
     int pf_chunk = kPieceAlign;
     if (s_longest > 0) {
         const int c = ((s_longest + tid) / (tid + 1) + kPieceAlign - 1) / kPieceAlign * kPieceAlign;
         long long items = 0, least = 0;
         for (int g = 0; g < NG; ++g) {
-            const Virtual r = virtual_seq(p, g);
-            if (r.cls != 2) continue;
-            const long long tiles = (long long)((r.ql + Tq - 1) / Tq) * p.Hkv;
-            items += tiles * ((r.end + c - 1) / c);
+            if (R.cls(p, g) != 2) continue;
+            const long long tiles = (long long)((R.ql[g] + Tq - 1) / Tq) * p.Hkv;
+            items += tiles * ((R.end[g] + c - 1) / c);
             least += tiles;
         }
         const unsigned long long cost = (unsigned long long)((items + pf_ctas - 1) / pf_ctas) * (unsigned long long)(c + kPieceCost);
@@ -165,35 +184,27 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_prefix_plan_kernel(const 
     int n_dec = 0, n_pf = 0, n_part = 0;
     for (int base = 0; base < V; base += kPlanThreads) {
         const int v = base + tid;
-        int add[3] = {0, 0, 0}, off[3], tot[3];
-        Virtual r;
-        r.cls = 0;
-        int pieces = 0;
+        int add[3] = {0, 0, 0}, off[3], tot[3], cls = 0, pieces = 0;
         if (v < V) {
-            r = virtual_seq(p, v);
-            if (r.cls == 1) {
-                pieces = (r.end - r.begin + chunk - 1) / chunk;
+            cls = R.cls(p, v);
+            if (cls == 1) {
+                pieces = (R.end[v] - R.begin[v] + chunk - 1) / chunk;
                 add[0] = pieces;
                 add[2] = pieces * p.Hkv;
-            } else if (r.cls == 2) {
-                pieces = v < NG ? (r.end + pf_chunk - 1) / pf_chunk : 1;
-                add[1] = (r.ql + Tq - 1) / Tq * pieces;
+            } else if (cls == 2) {
+                pieces = v < NG ? (R.end[v] + pf_chunk - 1) / pf_chunk : 1;
+                add[1] = (R.ql[v] + Tq - 1) / Tq * pieces;
                 add[2] = add[1] * p.Hkv * p.pf_slots;
             }
         }
         block_scan<3>(add, off, tot, s_scan);
         if (v < V) {
-            p.vcu[v] = r.q0;
-            // the empty one's end is the last group's: the pair (v, v + 1) of every other is its tokens
-            if (v == NG) p.vcu[v] = p.cu[S];
-            if (v == V - 1) p.vcu[V] = p.cu[S];
+            p.vcu[v] = R.q0[v];
             // positions behind the prefix: a group's keys are visible to all of its tokens
-            p.vkv[v] = v < NG ? r.end + r.ql : r.end;
-            p.vrow[v] = r.row;
-            p.vpart[v] = n_part + off[2];
-            p.vpieces[v] = r.cls == 2 ? -pieces : pieces;
-            p.dec_end[v] = n_dec + off[0] + add[0];
-            p.pf_end[v] = n_pf + off[1] + add[1];
+            p.vkv[v] = v < NG ? R.end[v] + R.ql[v] : R.end[v];
+            p.vrec[v] = make_int4(R.q0[v], n_part + off[2], cls == 2 ? -pieces : pieces, 0);
+            R.dec_end[v] = n_dec + off[0] + add[0];
+            R.pf_end[v] = n_pf + off[1] + add[1];
         }
         n_dec += tot[0];
         n_pf += tot[1];
@@ -208,28 +219,38 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_prefix_plan_kernel(const 
     // ---- 6. the unit lists: prefix tiles first, a piece's tiles together (they share its keys)
     for (int u = tid; u < n_dec + n_pf; u += kPlanThreads) {
         const bool dec = u >= n_pf;
-        const int* ends = dec ? p.dec_end : p.pf_end;
+        const int* ends = dec ? R.dec_end : R.pf_end;
         const int x = dec ? u - n_pf : u;
         const int v = upper_seq(ends, V, x);
-        const Virtual r = virtual_seq(p, v);
-        const int pieces = p.vpieces[v] < 0 ? -p.vpieces[v] : p.vpieces[v];
+        const int4 rec = p.vrec[v];
         const int first = v > 0 ? ends[v - 1] : 0, k = x - first;
         int4 a, b;
         if (dec) {
-            const int kb = r.begin + k * chunk;
-            a = make_int4(v, 0, r.ql, kb);
-            b = make_int4(min(r.end, kb + chunk), p.vpart[v], k, pieces);
+            const int kb = R.begin[v] + k * chunk;
+            a = make_int4(v, 0, R.ql[v], kb);
+            b = make_int4(min(R.end[v], kb + chunk), rec.y, k, rec.z);
         } else {
-            const int tiles = (r.ql + Tq - 1) / Tq, tile = k % tiles, piece = k / tiles;
-            const int t0 = tile * Tq, nt = min(Tq, r.ql - t0);
-            const int kb = v < NG ? piece * pf_chunk : r.begin;
-            const int ke = v < NG ? min(r.end, kb + pf_chunk) : min(r.end, r.end - r.ql + t0 + nt);
+            const int ql = R.ql[v], end = R.end[v], pieces = -rec.z;
+            const int tiles = (ql + Tq - 1) / Tq, tile = k % tiles, piece = k / tiles;
+            const int t0 = tile * Tq, nt = min(Tq, ql - t0);
+            const int kb = v < NG ? piece * pf_chunk : R.begin[v];
+            const int ke = v < NG ? min(end, kb + pf_chunk) : min(end, end - ql + t0 + nt);
             a = make_int4(v, t0, nt, kb);
-            b = make_int4(ke, p.vpart[v] + tile * p.Hkv * pieces * p.pf_slots, piece * p.pf_slots, pieces * p.pf_slots);
+            b = make_int4(ke, rec.y + tile * p.Hkv * pieces * p.pf_slots, piece * p.pf_slots, pieces * p.pf_slots);
         }
         Unit* dst = dec && !p.dec_on_pf ? p.dec_units + x : p.pf_units + u;
         reinterpret_cast<int4*>(dst)[0] = a;
         reinterpret_cast<int4*>(dst)[1] = b;
+    }
+    // ---- 7. each token's virtual sequences
+    const int t_lo = S > 0 ? R.q0[NG + 1] : 0, t_hi = S > 0 ? R.q0[NG] : 0;
+    for (int t = tid; t < p.T; t += kPlanThreads) {
+        int2 who = make_int2(-1, -1);
+        if (t >= t_lo && t < t_hi) {
+            const int s = upper_seq(R.q0 + NG + 2, S, t);  // the first whose successor starts behind t
+            who = make_int2(upper_seq(p.cu_groups + 1, NG, s), NG + 1 + s);
+        }
+        p.token[t] = who;
     }
     __threadfence();
     __syncthreads();
@@ -251,8 +272,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_prefix_plan_kernel(const 
 // ---------------------------------------------------------------- merge
 struct PrefixMerge {
     uint8_t* o;
-    const int *cu, *cu_groups, *vcu, *vpart, *vpieces, *ctrl;
-    int S, NG, T, Hq, Hkv, G, D;
+    const int2* token;  // [T] virtual sequences of a token's group and of its sequence (y -1: of none)
+    const int4* vrec;   // [virtual sequences] first token, first partial slot, pieces (< 0: of prefill tiles)
+    const int* ctrl;
+    int T, Hq, Hkv, G, D;
     int pf_tokens, pf_slots;
     int per_token;  // CTAs of a token
     float v_scale;
@@ -267,12 +290,12 @@ constexpr int kMergeThreads = 256;
 struct Source {
     int slot, stride, n, row;
 };
-__device__ __forceinline__ Source source(const PrefixMerge& p, int v, int t, int h, int g) {
+__device__ __forceinline__ Source source(const PrefixMerge& p, const int4& v, int t, int h, int g) {
     Source r;
-    const int pieces = p.vpieces[v], tl = t - p.vcu[v];
+    const int pieces = v.z, tl = t - v.x;
     r.n = pieces < 0 ? -pieces : pieces;
     if (pieces >= 0) {
-        r.slot = p.vpart[v] + h * pieces;
+        r.slot = v.y + h * pieces;
         r.stride = 1;
         r.row = tl * p.G + g;
     } else {
@@ -280,14 +303,14 @@ __device__ __forceinline__ Source source(const PrefixMerge& p, int v, int t, int
         const int tile = tl / p.pf_tokens, tt = tl - tile * p.pf_tokens;
         const int half_tokens = p.pf_slots == 16 ? p.pf_tokens / 2 : p.pf_tokens;
         r.stride = p.pf_slots;
-        r.slot = p.vpart[v] + (tile * p.Hkv + h) * r.n * p.pf_slots;
+        r.slot = v.y + (tile * p.Hkv + h) * r.n * p.pf_slots;
         r.row = tt / half_tokens * kTcRows + tt % half_tokens * p.G + g;
     }
     return r;
 }
 
 __global__ void __launch_bounds__(kMergeThreads, 4) rpa_prefix_merge_kernel(const PrefixMerge p) {
-    constexpr int kBatch = 6;  // partial O loads a lane has in flight
+    constexpr int kBatch = 8;  // partial O loads a lane has in flight
     pdl_trigger();
     pdl_wait();
     const int lane = threadIdx.x & 31, t = blockIdx.x / p.per_token;
@@ -296,28 +319,46 @@ __global__ void __launch_bounds__(kMergeThreads, 4) rpa_prefix_merge_kernel(cons
     if (task >= p.Hq * chunks) return;
     const int qh = task / chunks, c4 = (task - qh * chunks) * 32 + lane;
     const bool act = c4 < quads;
-    const int s = p.ctrl[kNumComb] < 0 ? -1 : find_seq(p.cu, p.S, t, lane);
+    const int2 who = p.token[t];  // virtual sequences of the token's group and of its sequence
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
     float inv = 0.f;
-    if (s >= 0) {
+    if (who.y >= 0 && p.ctrl[kNumComb] >= 0) {
         const int h = qh / p.G, g = qh - h * p.G;
-        const Source a = source(p, find_seq(p.cu_groups, p.NG, s, lane), t, h, g);
-        const Source b = source(p, p.NG + 1 + s, t, h, g);
+        const int4 va = p.vrec[who.x], vb = p.vrec[who.y];
+        const Source a = source(p, va, t, h, g), b = source(p, vb, t, h, g);
         const int n = a.n + b.n;
+        // this lane's four columns in a slot's rows: row-major, or the prefill kernel's blocks of eight columns
+        const bool a_blocked = va.z < 0 && p.pf_slots == 16, b_blocked = vb.z < 0 && p.pf_slots == 16;
+        const int blocked = (c4 / 2) * (2 * kTcRows * 8) + (c4 & 1) * 4;
         float M = -INFINITY, L = 0.f;
         for (int k0 = 0; k0 < n; k0 += 32) {
             // lane k: partial k0 + k
             const int k = k0 + lane;
             const bool in_a = k < a.n;
-            const size_t at = k < n ? (size_t)(in_a ? a.slot + k * a.stride : b.slot + (k - a.n) * b.stride) * kDecRows +
-                                          (in_a ? a.row : b.row)
-                                    : 0;
-            const float2 ml = k < n ? *reinterpret_cast<const float2*>(p.part_ml + at * 2) : make_float2(-INFINITY, 0.f);
+            const int slot = in_a ? a.slot + k * a.stride : b.slot + (k - a.n) * b.stride;
+            const float2 ml = k < n ? *reinterpret_cast<const float2*>(p.part_ml + ((size_t)slot * kDecRows + (in_a ? a.row : b.row)) * 2)
+                                    : make_float2(-INFINITY, 0.f);
+            const int most = min(32, n - k0);
+            float4 x[kBatch];
+            auto fetch = [&](int j0) {
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    const int kk = k0 + j0 + j;
+                    if (act && j0 + j < most) {
+                        const bool ina = kk < a.n;
+                        const int sl = ina ? a.slot + kk * a.stride : b.slot + (kk - a.n) * b.stride, row = ina ? a.row : b.row;
+                        const float* o = p.part_o + (size_t)sl * kDecRows * p.D;
+                        o += (ina ? a_blocked : b_blocked) ? blocked + row * 8 : row * p.D + c4 * 4;
+                        x[j] = __ldcs(reinterpret_cast<const float4*>(o));
+                    }
+                }
+            };
+            fetch(0);  // beside the maxima and sums
             float m = ml.x;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
             const float Mn = fmaxf(M, m), keep = M == -INFINITY ? 0.f : ex2(M - Mn);
-            // a part whose keys are all hidden has l = 0 and an O that may hold anything finite
+            // a part whose keys are all hidden has no maximum and joins with weight 0
             const float w = ml.x == -INFINITY ? 0.f : ex2(ml.x - Mn);
             float l = w * ml.y;
 #pragma unroll
@@ -325,14 +366,8 @@ __global__ void __launch_bounds__(kMergeThreads, 4) rpa_prefix_merge_kernel(cons
             L = L * keep + l;
             M = Mn;
             acc.x *= keep; acc.y *= keep; acc.z *= keep; acc.w *= keep;
-            const int most = min(32, n - k0);
             for (int j0 = 0; j0 < most; j0 += kBatch) {
-                float4 x[kBatch];
-#pragma unroll
-                for (int j = 0; j < kBatch; ++j) {
-                    const unsigned long long from = __shfl_sync(0xffffffffu, (unsigned long long)at, (j0 + j) & 31);
-                    if (act && j0 + j < most) x[j] = *(reinterpret_cast<const float4*>(p.part_o + (size_t)from * p.D) + c4);
-                }
+                if (j0 > 0) fetch(j0);
 #pragma unroll
                 for (int j = 0; j < kBatch; ++j) {
                     const float wj = __shfl_sync(0xffffffffu, w, (j0 + j) & 31);
@@ -367,7 +402,9 @@ struct RpaPrefix {
     void* ws;
     Workspace w;
     int pf_slots, item_room, max_dec_units, max_pf_units, max_part;
-    int *vcu, *vkv, *vrow, *vpart, *vpieces, *dec_end, *pf_end;
+    int *vcu, *vkv, *vrow, *scratch;
+    int4* vrec;
+    int2* token;
     cudaStream_t side;
     cudaEvent_t ev_plan, ev_dec;
     int epoch;
@@ -413,7 +450,8 @@ bool prefix_allocate(RpaPrefix* h) {
         off = (off + bytes + 255) & ~(size_t)255;
         return at;
     };
-    const size_t o_ctrl = take(kCtrlWords * sizeof(int)), o_v = take(7 * V * sizeof(int)),
+    const size_t o_ctrl = take(kCtrlWords * sizeof(int)), o_v = take(3 * V * sizeof(int)), o_rec = take(V * sizeof(int4)),
+                 o_scratch = take(V > kVirtualSmem ? kArrays * V * sizeof(int) : 0), o_token = take((size_t)T * sizeof(int2)),
                  o_dec = take((size_t)h->max_dec_units * sizeof(Unit)), o_pf = take((size_t)h->max_pf_units * sizeof(Unit)),
                  o_po = take((size_t)part * kDecRows * ks.D * sizeof(float)), o_ml = take((size_t)part * kDecRows * 2 * sizeof(float)),
                  o_q = take(ks.q_conv ? (size_t)T * c.num_q_heads * ks.D * 2 : 0);
@@ -427,8 +465,12 @@ bool prefix_allocate(RpaPrefix* h) {
     h->w.part_ml = reinterpret_cast<float*>(b + o_ml);
     h->w.qbuf = ks.q_conv ? b + o_q : nullptr;
     int* v = reinterpret_cast<int*>(b + o_v);
-    int** parts[7] = {&h->vcu, &h->vkv, &h->vrow, &h->vpart, &h->vpieces, &h->dec_end, &h->pf_end};
-    for (int i = 0; i < 7; ++i) *parts[i] = v + (size_t)i * V;
+    h->vcu = v;
+    h->vkv = v + V;
+    h->vrow = v + 2 * V;
+    h->vrec = reinterpret_cast<int4*>(b + o_rec);
+    h->scratch = reinterpret_cast<int*>(b + o_scratch);
+    h->token = reinterpret_cast<int2*>(b + o_token);
     return !ks.tc || (cudaStreamCreateWithFlags(&h->side, cudaStreamNonBlocking) == cudaSuccess &&
                       cudaEventCreateWithFlags(&h->ev_plan, cudaEventDisableTiming) == cudaSuccess &&
                       cudaEventCreateWithFlags(&h->ev_dec, cudaEventDisableTiming) == cudaSuccess);
@@ -536,10 +578,9 @@ int rpa_prefix_forward(RpaPrefix* h, const void* q, const void* kv_pages, const 
     p.vcu = h->vcu;
     p.vkv = h->vkv;
     p.vrow = h->vrow;
-    p.vpart = h->vpart;
-    p.vpieces = h->vpieces;
-    p.dec_end = h->dec_end;
-    p.pf_end = h->pf_end;
+    p.vrec = h->vrec;
+    p.token = h->token;
+    p.scratch = h->scratch;
     p.dec_units = h->w.dec_units;
     p.pf_units = h->w.pf_units;
     if (launch_pdl(rpa_prefix_plan_kernel, 1, kPlanThreads, 0, st, p) != cudaSuccess) {
@@ -556,14 +597,9 @@ int rpa_prefix_forward(RpaPrefix* h, const void* q, const void* kv_pages, const 
     if (c.num_q_tokens == 0) return RPA_OK;
     PrefixMerge m;
     m.o = static_cast<uint8_t*>(o);
-    m.cu = cu_q_lens;
-    m.cu_groups = cu_groups;
-    m.vcu = h->vcu;
-    m.vpart = h->vpart;
-    m.vpieces = h->vpieces;
+    m.token = h->token;
+    m.vrec = h->vrec;
     m.ctrl = h->w.ctrl;
-    m.S = num_seqs;
-    m.NG = num_groups;
     m.T = (int)c.num_q_tokens;
     m.Hq = (int)c.num_q_heads;
     m.Hkv = ks.Hp;
