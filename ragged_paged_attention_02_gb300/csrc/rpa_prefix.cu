@@ -29,8 +29,8 @@ namespace {
 constexpr int kPieceAlign = 128;   // keys: the prefill kernels' tiles
 constexpr int kPieceKeys = 256;    // smallest decode piece: the keys behind a prefix are few, and so is what fills the SMs
 constexpr int kPieceCost = 256;    // what a piece costs beside its keys, in keys
-constexpr int kMaxPieces = 512;    // candidates, one a planner thread
-static_assert(kMaxPieces == kPlanThreads, "a candidate a thread");
+static_assert(kPlanThreads >= 160, "a candidate a thread");
+constexpr int kMaxPieces = 160;    // most pieces of a prefix: one an SM where a single head and tile have all of them
 
 struct PrefixPlan {
     const int *cu, *kv_lens, *cu_groups, *prefix_lens;
@@ -60,12 +60,50 @@ struct Records {
     }
 };
 
+// Sums of a and b and the largest m over the block, and whether any thread found a fault: one round of barriers
+__device__ __forceinline__ bool block_totals(unsigned long long& a, unsigned long long& b, int& m, bool bad, unsigned long long* s_red) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    m = __reduce_max_sync(0xffffffffu, m);
+    if (lane == 0) {
+        s_red[warp] = a;
+        s_red[32 + warp] = b;
+        s_red[64 + warp] = (unsigned long long)m;
+    }
+    if (__syncthreads_or(bad)) return true;
+    a = lane < nwarps ? s_red[lane] : 0ull;
+    b = lane < nwarps ? s_red[32 + lane] : 0ull;
+    m = __reduce_max_sync(0xffffffffu, lane < nwarps ? (int)s_red[64 + lane] : 0);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        a += __shfl_xor_sync(0xffffffffu, a, o);
+        b += __shfl_xor_sync(0xffffffffu, b, o);
+    }
+    return false;
+}
+
+// The warp's least cost and its candidate, the lowest of equal costs
+__device__ __forceinline__ void warp_least(float& cost, int& candidate) {
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) {
+        const float c = __shfl_xor_sync(0xffffffffu, cost, o);
+        const int x = __shfl_xor_sync(0xffffffffu, candidate, o);
+        if (c < cost || (c == cost && x < candidate)) {
+            cost = c;
+            candidate = x;
+        }
+    }
+}
+
 __global__ void __launch_bounds__(kPlanThreads, 1) rpa_prefix_plan_kernel(const PrefixPlan p) {
     __shared__ int s_rec[kArrays * kVirtualSmem];
     __shared__ int s_scan[33 * 3];
-    __shared__ unsigned long long s_red[64];
-    __shared__ int s_bad, s_longest;
-    const int tid = threadIdx.x, S = p.S, NG = p.NG, V = S > 0 ? NG + 1 + S : 0;
+    __shared__ unsigned long long s_red[96];
+    const int tid = threadIdx.x, lane = tid & 31, S = p.S, NG = p.NG, V = S > 0 ? NG + 1 + S : 0;
     int* ctrl = p.ctrl;
     const int Tq = p.pf_tokens;
     Records R;
@@ -86,101 +124,104 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_prefix_plan_kernel(const 
             publish_epoch(ctrl, p.epoch);
         }
     };
-    if (tid == 0) {
-        s_bad = NG > 0 ? p.cu_groups[0] != 0 || p.cu_groups[NG] != S : S != 0;
-        s_longest = 0;
-    }
-    __syncthreads();
-    // ---- 1. groups first (the sequences look theirs up), then sequences
-    for (int g = tid; g < NG; g += kPlanThreads) {
-        const int a = p.cu_groups[g], b = p.cu_groups[g + 1], n = p.prefix_lens[g];
-        if (a < 0 || b < a || b > S || n < 0 || n > p.P * p.ps) {
-            s_bad = 1;
-        } else if (V > 0) {
-            R.q0[g] = p.cu[a];
-            R.ql[g] = p.cu[b] - p.cu[a];
-            R.begin[g] = 0;
-            R.end[g] = n;
-            p.vrow[g] = a;
-        }
-    }
-    __syncthreads();
-    if (s_bad) {
-        give_up(RPA_ERR_BAD_LENGTHS);
-        return;
-    }
-    for (int s = tid; s < S; s += kPlanThreads) {
-        const int q0 = p.cu[s], q1 = p.cu[s + 1], kl = p.kv_lens[s], ql = q1 - q0, v = NG + 1 + s;
-        const int g = upper_seq(p.cu_groups + 1, NG, s), pre = R.end[g];
-        if (q0 < 0 || ql < 0 || kl < 0 || kl > p.P * p.ps || ql > kl || q1 > p.T || (ql > 0 && pre > kl - ql)) {
-            s_bad = 1;
-        } else {
-            R.q0[v] = q0;
-            R.ql[v] = ql;
-            R.begin[v] = pre;
-            R.end[v] = kl;
-            p.vrow[v] = s;
-        }
-    }
-    if (tid == 0 && V > 0) {
-        R.q0[NG] = p.cu[S];  // the last group's end: the pair (v, v + 1) of every other is its tokens
-        R.ql[NG] = R.begin[NG] = R.end[NG] = 0;
-        p.vrow[NG] = 0;
-        p.vcu[V] = p.cu[S];
-    }
-    __syncthreads();
-    if (s_bad) {
-        give_up(RPA_ERR_BAD_LENGTHS);
-        return;
-    }
-    // ---- 2. work of the two kernels: key x kv head pairs of decode pieces, tile x key x kv head of prefill tiles
+    // ---- 1. records, checks, and the work of the two kernels: key x kv head pairs of decode pieces, tile x key x kv
+    // head of prefill tiles.  A group's bounds are checked by its own thread; a sequence's lookup of its group stays
+    // in range whatever they hold.
+    bool bad = tid == 0 && (NG > 0 ? p.cu_groups[0] != 0 || p.cu_groups[NG] != S : S != 0);
     unsigned long long dec_keys = 0, pf_keys = 0;
-    for (int v = tid; v < V; v += kPlanThreads) {
-        const int cls = R.cls(p, v), keys = R.end[v] - R.begin[v];
+    int longest = 0;
+    for (int v = tid; v < max(V, NG); v += kPlanThreads) {
+        int q0 = 0, ql = 0, begin = 0, end = 0, row = 0;
+        if (v < NG) {
+            const int a = p.cu_groups[v], b = p.cu_groups[v + 1];
+            end = p.prefix_lens[v];
+            if (a < 0 || b < a || b > S || end < 0 || end > p.P * p.ps) {
+                bad = true;
+                end = 0;
+            } else {
+                row = a;
+                q0 = p.cu[a];
+                ql = p.cu[b] - q0;
+            }
+        } else if (v == NG) {
+            q0 = p.cu[S];  // the last group's end: the pair (v, v + 1) of every other virtual sequence is its tokens
+        } else {
+            row = v - NG - 1;
+            q0 = p.cu[row];
+            ql = p.cu[row + 1] - q0;
+            end = p.kv_lens[row];
+            if (NG > 0) begin = p.prefix_lens[upper_seq(p.cu_groups + 1, NG, row)];
+            if (q0 < 0 || ql < 0 || end < 0 || end > p.P * p.ps || ql > end || q0 + (long long)ql > p.T || (ql > 0 && begin > end - ql)) {
+                bad = true;
+                ql = 0;
+            }
+        }
+        if (v >= V) continue;
+        R.q0[v] = q0;
+        R.ql[v] = ql;
+        R.begin[v] = begin;
+        R.end[v] = end;
+        p.vrow[v] = row;
+        const int cls = R.cls(p, v), keys = end - begin;
         if (cls == 1) dec_keys += (unsigned long long)keys * p.Hkv;
         if (cls == 2) {
-            pf_keys += (unsigned long long)((R.ql[v] + Tq - 1) / Tq) * (unsigned long long)keys * p.Hkv;
-            if (v < NG) atomicMax(&s_longest, R.end[v]);
+            pf_keys += (unsigned long long)((ql + Tq - 1) / Tq) * (unsigned long long)keys * p.Hkv;
+            if (v < NG) longest = max(longest, end);
         }
     }
-    block_sum64x2(dec_keys, pf_keys, s_red);
-    // ---- 3. SMs of each kernel (both at once: the split that ends them together), as rpa_forward's planner
+    if (tid == 0 && V > 0) p.vcu[V] = p.cu[S];
+    if (block_totals(dec_keys, pf_keys, longest, bad, s_red)) {
+        give_up(RPA_ERR_BAD_LENGTHS);
+        return;
+    }
+    // ---- 2. SMs of each kernel when both run at once, by rpa_forward's rates: x SMs of prefill take F / (x a), the
+    // others B / ((n - x) d), but no less than B / hbm; they end together where F d (n - x) = B a x, and SMs past
+    // those that saturate the memory are prefill's
     int pf_ctas = p.n_sms * p.pf_bps, dec_ctas = p.n_sms * p.dec_bps;
     if (p.concurrent && dec_keys && pf_keys) {
-        const unsigned long long bytes = dec_keys * (unsigned long long)(2 * p.D * p.kv_elt);
-        const unsigned long long flops = pf_keys * (unsigned long long)p.pf_mma_rows * (unsigned long long)(4 * p.D);
-        unsigned long long mine = ~0ull;
-        for (int x = 1 + tid; x < p.n_sms; x += kPlanThreads) {
-            const unsigned long long tp = flops / ((unsigned long long)x * kPfSmGflopsTc);
-            const unsigned long long td =
-                bytes / min((unsigned long long)kHbmGBs, (unsigned long long)(p.n_sms - x) * kDecSmGBs);
-            const unsigned long long k = (min(max(tp, td), (1ull << 47) - 1) << 16) | (unsigned long long)x;
-            mine = min(mine, k);
-        }
-        const int x = (int)(block_min64(mine, s_red) & 0xffffull);
+        const float B = (float)dec_keys * (float)(2 * p.D * p.kv_elt), F = (float)pf_keys * (float)p.pf_mma_rows * (float)(4 * p.D);
+        const float fd = F * (float)kDecSmGBs, ba = B * (float)kPfSmGflopsTc;
+        int x = (int)((float)p.n_sms * fd / (fd + ba) + 0.5f);
+        x = min(max(max(x, 1), p.n_sms - (kHbmGBs + kDecSmGBs - 1) / kDecSmGBs), p.n_sms - 1);
         pf_ctas = x * p.pf_bps;
         dec_ctas = (p.n_sms - x) * p.dec_bps;
     }
-    // ---- 4. keys of a decode piece, and of a piece of a prefix's tiles
+    // ---- 3. keys of a decode piece, and of a piece of a prefix's tiles
     const int on = p.dec_on_pf ? pf_ctas : dec_ctas;
-    unsigned long long want = dec_keys / (unsigned long long)max(1, p.dec_waves * on) + 1;
+    const unsigned long long want = dec_keys / (unsigned long long)max(1, p.dec_waves * on) + 1;
     const int chunk = (int)min(max((want + kChunkAlign - 1) / kChunkAlign * kChunkAlign, (unsigned long long)kPieceKeys), 1ull << 30);
     int pf_chunk = kPieceAlign;
-    if (s_longest > 0) {
-        const int c = ((s_longest + tid) / (tid + 1) + kPieceAlign - 1) / kPieceAlign * kPieceAlign;
-        long long items = 0, least = 0;
-        for (int g = 0; g < NG; ++g) {
-            if (R.cls(p, g) != 2) continue;
-            const long long tiles = (long long)((R.ql[g] + Tq - 1) / Tq) * p.Hkv;
-            items += tiles * ((R.end[g] + c - 1) / c);
-            least += tiles;
+    if (longest > 0) {
+        // pieces of the longest prefix: a candidate a thread, the warps' bests by cost and then by number
+        float cost = INFINITY;
+        if (tid < kMaxPieces) {
+            const int c = ((longest + tid) / (tid + 1) + kPieceAlign - 1) / kPieceAlign * kPieceAlign;
+            long long items = 0, fewest = 0;
+            for (int g = 0; g < NG; ++g) {
+                if (R.cls(p, g) != 2) continue;
+                const int tiles = (R.ql[g] + Tq - 1) / Tq * p.Hkv;
+                items += (long long)tiles * ((R.end[g] + c - 1) / c);
+                fewest += tiles;
+            }
+            // (whole waves of whole keys: exact in a float up to 2^24, and far from it where a choice is close)
+            if (tid == 0 || items <= fewest + p.item_room) cost = ceilf((float)items / (float)pf_ctas) * (float)(c + kPieceCost);
         }
-        const unsigned long long cost = (unsigned long long)((items + pf_ctas - 1) / pf_ctas) * (unsigned long long)(c + kPieceCost);
-        const unsigned long long k = tid > 0 && items > least + p.item_room ? ~0ull : (min(cost, (1ull << 47) - 1) << 16) | (unsigned long long)tid;
-        const int t = (int)(block_min64(k, s_red) & 0xffffull);
-        pf_chunk = ((s_longest + t) / (t + 1) + kPieceAlign - 1) / kPieceAlign * kPieceAlign;
+        float* costs = reinterpret_cast<float*>(s_red);
+        int* who = reinterpret_cast<int*>(s_red + 32);
+        int best = tid;
+        warp_least(cost, best);
+        __syncthreads();  // block_totals' reads
+        if (lane == 0) {
+            costs[tid >> 5] = cost;
+            who[tid >> 5] = best;
+        }
+        __syncthreads();
+        cost = lane < kPlanThreads / 32 ? costs[lane] : INFINITY;
+        best = lane < kPlanThreads / 32 ? who[lane] : kMaxPieces;
+        warp_least(cost, best);
+        pf_chunk = ((longest + best) / (best + 1) + kPieceAlign - 1) / kPieceAlign * kPieceAlign;
     }
-    // ---- 5. units and partial slots of each virtual sequence
+    // ---- 4. units and partial slots of each virtual sequence
     int n_dec = 0, n_pf = 0, n_part = 0;
     for (int base = 0; base < V; base += kPlanThreads) {
         const int v = base + tid;
@@ -216,7 +257,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_prefix_plan_kernel(const 
         return;
     }
     __syncthreads();
-    // ---- 6. the unit lists: prefix tiles first, a piece's tiles together (they share its keys)
+    // ---- 5. the unit lists: prefix tiles first, a piece's tiles together (they share its keys)
     for (int u = tid; u < n_dec + n_pf; u += kPlanThreads) {
         const bool dec = u >= n_pf;
         const int* ends = dec ? R.dec_end : R.pf_end;
@@ -242,7 +283,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_prefix_plan_kernel(const 
         reinterpret_cast<int4*>(dst)[0] = a;
         reinterpret_cast<int4*>(dst)[1] = b;
     }
-    // ---- 7. each token's virtual sequences
+    // ---- 6. each token's virtual sequences
     const int t_lo = S > 0 ? R.q0[NG + 1] : 0, t_hi = S > 0 ? R.q0[NG] : 0;
     for (int t = tid; t < p.T; t += kPlanThreads) {
         int2 who = make_int2(-1, -1);
@@ -252,8 +293,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_prefix_plan_kernel(const 
         }
         p.token[t] = who;
     }
-    __threadfence();
-    __syncthreads();
+    __syncthreads();  // (publish_epoch's fence covers what the barrier has gathered)
     if (tid == 0) {
         ctrl[kNumDecItems] = p.dec_on_pf ? 0 : n_dec * p.Hkv;
         ctrl[kNumPfItems] = n_list * p.Hkv;
