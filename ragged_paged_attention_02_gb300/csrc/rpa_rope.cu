@@ -11,12 +11,18 @@
 // tenth of a radian at a million positions, and in 64 bits the GPU runs it at 1/64 of the rate.
 // Sines are computed once per token and pair, into shared memory, and serve all heads.
 //
-// A CTA takes one token: units of 16 elements (two 16-byte vectors of 2-byte types) of one row
-// (q head, K row or V row).  A rotary unit is 8 pairs, both partners in one thread's registers
-// (HALF: two vectors rotary_dim / 2 apart; INTERLEAVED: 16 neighbours), so that a row is read once
-// and written once.  Each thread keeps its place in the row and steps over the rows, so that its
-// sines stay in registers; its first rows' loads go out before the token's sequence is looked up
-// (cu_q_lens by a 32-ary search of one warp, then kv_lens, then the page id: four dependent loads).
+// A CTA takes a run of neighbouring tokens, up to 16 at a time: its warps look their sequences, positions and
+// slots up at once (cu_q_lens by a 32-ary search, then kv_lens, then the page id: four dependent loads, some
+// two microseconds that one token a CTA paid each time), all threads compute the sines, and from there on
+// there is only streaming: units of 16 elements (two 16-byte vectors of 2-byte types) of one row (q head, K
+// row or V row).  A rotary unit is 8 pairs, both partners in one thread's registers (HALF: two vectors
+// rotary_dim / 2 apart; INTERLEAVED: 16 neighbours), so that a row is read once and written once.  A thread
+// keeps its place in the row and steps over the rows of all tokens, two rows' loads in flight; the first
+// go out before the lookups.
+//
+// Bound by HBM: 8192 tokens of 64 q and 8 kv heads at D 128 (bf16, 344 MB) take 61 us, 5.6 TB/s, 0.83 of the
+// measured copy.  Five CTAs an SM with two rows in flight a thread: 61 us; four CTAs: 63 us with two rows, 64
+// with four (spilled); one token a CTA: 79 to 87 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <string.h>
@@ -30,7 +36,7 @@ using namespace rpa;
 
 struct RpaRope {
     RpaRopeCfg cfg;
-    int device;
+    int device, sms;
     unsigned long long* turns;  // device [rotary_dim / 2]: f_i
     int* status;                // device: first error since the last rpa_rope_get_status
 };
@@ -39,7 +45,9 @@ namespace rpa {
 namespace {
 
 constexpr int kUnit = 16;       // elements of a unit
-constexpr int kMaxThreads = 288;
+constexpr int kRopeThreads = 256;
+constexpr int kRopeCtas = 5;    // resident an SM
+constexpr int kTokens = 16;     // tokens of a CTA's round
 constexpr int kMaxPairs = 288;  // rotary_dim <= 576
 
 struct RopeParams {
@@ -53,7 +61,7 @@ struct RopeParams {
     int rd, off;
     int rows;       // q heads + K rows + V rows of a token
     int per_row;    // units of a row
-    int row_step;   // rows the CTA takes at once
+    int row_step;   // rows the CTA takes at once (its threads / per_row)
     int kt;         // KvType of the cache
     int has_ks, has_vs;
     float magnitude, k_scale, v_scale;
@@ -142,131 +150,142 @@ __device__ __forceinline__ void store_kv8(uint8_t* kv, size_t row, int e, const 
 }
 
 template <typename QT, bool HALF>
-__global__ void __launch_bounds__(kMaxThreads) rpa_rope_kernel(const RopeParams p) {
-    constexpr int kBatch = sizeof(QT) == 4 ? 2 : 4;  // rows whose loads a thread has in flight
-    __shared__ float2 s_cs[kMaxPairs];
-    __shared__ long long s_slot;  // cache slot of the token (page * page_size + place), or -1
-    __shared__ int s_pos, s_live;
-    const int t = blockIdx.x, tid = threadIdx.x;
+__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rpa_rope_kernel(const RopeParams p) {
+    constexpr int kBatch = sizeof(QT) == 4 ? 1 : 2;  // rows whose loads a thread has in flight
+    // [tokens][4][places] pairs of (cos, sin): place's pairs 2 i and 2 i + 1 at [i][place], so that neighbouring
+    // places read neighbouring 16 bytes
+    extern __shared__ float4 s_cs[];
+    __shared__ long long s_slot[kTokens];  // cache slot of a token (page * page_size + place), or -1
+    __shared__ int s_pos[kTokens], s_live[kTokens];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
     const int place = tid % p.per_row, row0 = tid / p.per_row;
     // this thread's unit: elements [e0, e0 + 8) and [e1, e1 + 8) of a row
-    const int rot_units = p.rd / kUnit;
-    const bool rot = place < rot_units;
+    const int places = p.rd / kUnit;  // rotary units of a row
+    const bool rot = place < places;
     int e0, e1;
     if (rot) {
         e0 = p.off + place * (HALF ? 8 : 16);
         e1 = e0 + (HALF ? p.rd / 2 : 8);
     } else {
-        const int c = (place - rot_units) * 16;  // of the elements outside the rotary part
+        const int c = (place - places) * 16;  // of the elements outside the rotary part
         e0 = c < p.off ? c : c + p.rd;
         e1 = c + 8 < p.off ? c + 8 : c + 8 + p.rd;
     }
-    auto source = [&](int r) -> const uint8_t* {
-        const size_t eb = sizeof(QT);
-        if (r < p.Hq) return p.q + (size_t)t * p.q_stride + (size_t)r * p.D * eb;
-        r -= p.Hq;
-        if (r < p.Hkv) return p.k + (size_t)t * p.k_stride + (size_t)r * p.D * eb;
-        return p.v + (size_t)t * p.v_stride + (size_t)(r - p.Hkv) * p.D * eb;
+    const int t_end = (int)((long long)p.T * (blockIdx.x + 1) / gridDim.x);
+    int t0 = (int)((long long)p.T * blockIdx.x / gridDim.x);
+    auto source = [&](int t, int r) -> const uint8_t* {
+        const uint8_t* base = r < p.Hq ? p.q + (size_t)t * p.q_stride : r < p.Hq + p.Hkv ? p.k + (size_t)t * p.k_stride : p.v + (size_t)t * p.v_stride;
+        const int h = r < p.Hq ? r : r < p.Hq + p.Hkv ? r - p.Hq : r - p.Hq - p.Hkv;
+        return base + (size_t)h * p.D * sizeof(QT);
     };
     pdl_trigger();
     pdl_wait();
-    Vec8<QT> x0[kBatch], x1[kBatch];
-    auto fetch = [&](int r0) {
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int r = r0 + b * p.row_step;
-            if (r < p.rows && t < p.T) {
-                const uint8_t* s = source(r);
-                load8(s + e0 * sizeof(QT), x0[b]);
-                load8(s + e1 * sizeof(QT), x1[b]);
+    for (; t0 < t_end; t0 += kTokens) {
+        const int n = min(kTokens, t_end - t0);
+        Vec8<QT> x0[kBatch], x1[kBatch];
+        // rows from (token `tk` of the round, row r) on, row_step apart, through the tokens
+        auto next = [&](int& tk, int& r) {
+            r += p.row_step;
+            while (r >= p.rows) {
+                r -= p.rows;
+                ++tk;
             }
-        }
-    };
-    fetch(row0);
-    if (tid < 32) {
-        const int s = find_seq(p.cu, p.S, t, tid);
-        if (tid == 0) {
-            int live = 0, pos = 0;
-            long long slot = -1;
-            if (s >= 0) {
-                const int q0 = p.cu[s], ql = p.cu[s + 1] - q0, kl = p.kv_lens[s];
-                if (q0 >= 0 && kl <= p.P * p.ps && ql <= kl && q0 + ql <= p.T) {
-                    live = 1;
-                    const int j = kl - ql + (t - q0);
-                    const int pg = p.page_indices[(size_t)s * p.P + j / p.ps];
-                    pos = p.positions ? p.positions[t] : j;
-                    if ((unsigned)pg < (unsigned)p.N) slot = (long long)pg * p.ps + j % p.ps;
-                    else set_status(p.status, RPA_ERR_BAD_PAGE_INDEX);
-                }
-            }
-            s_live = live;
-            s_pos = pos;
-            s_slot = slot;
-        }
-    }
-    __syncthreads();
-    const long long slot = s_slot;
-    if (s_live) {
-        for (int i = tid; i < p.rd / 2; i += blockDim.x) {
-            // the angle's fraction of a turn, its upper 32 bits as half turns in [-1, 1)
-            const unsigned long long f = p.turns[i] * (unsigned long long)(long long)s_pos;
-            float sn, cs;
-            sincospif((float)(int)((f + 0x80000000ull) >> 32) * 4.656612873077393e-10f, &sn, &cs);
-            s_cs[i] = make_float2(cs * p.magnitude, sn * p.magnitude);
-        }
-    }
-    __syncthreads();
-    if (s_live) {
-        float cs[8], sn[8];
-        if (rot) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float2 v = s_cs[place * 8 + i];
-                cs[i] = v.x;
-                sn[i] = v.y;
-            }
-        }
-        for (int r0 = row0; r0 < p.rows; r0 += kBatch * p.row_step) {
-            if (r0 != row0) fetch(r0);
+        };
+        auto fetch = [&](int tk, int r) {
 #pragma unroll
             for (int b = 0; b < kBatch; ++b) {
-                const int r = r0 + b * p.row_step;
-                if (r >= p.rows) continue;
-                float y[16];
-                widen(x0[b], y);
-                widen(x1[b], y + 8);
-                if (rot && r < p.Hq + p.Hkv) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int a = HALF ? i : 2 * i, c = HALF ? i + 8 : 2 * i + 1;
-                        const float u = y[a], w = y[c];
-                        y[a] = u * cs[i] - w * sn[i];
-                        y[c] = w * cs[i] + u * sn[i];
+                if (tk < n) {
+                    const uint8_t* s = source(t0 + tk, r);
+                    load8(s + e0 * sizeof(QT), x0[b]);
+                    load8(s + e1 * sizeof(QT), x1[b]);
+                }
+                next(tk, r);
+            }
+        };
+        int tk = row0 < p.row_step ? row0 / p.rows : n, r = row0 % p.rows;  // (576: 252 threads have a place)
+        fetch(tk, r);
+        for (int i = warp; i < n; i += warps) {
+            const int t = t0 + i, s = find_seq(p.cu, p.S, t, lane);
+            if (lane == 0) {
+                int live = 0, pos = 0;
+                long long slot = -1;
+                if (s >= 0) {
+                    const int q0 = p.cu[s], ql = p.cu[s + 1] - q0, kl = p.kv_lens[s];
+                    if (q0 >= 0 && kl <= p.P * p.ps && ql <= kl && q0 + ql <= p.T) {
+                        live = 1;
+                        const int j = kl - ql + (t - q0);
+                        const int pg = p.page_indices[(size_t)s * p.P + j / p.ps];
+                        pos = p.positions ? p.positions[t] : j;
+                        if ((unsigned)pg < (unsigned)p.N) slot = (long long)pg * p.ps + j % p.ps;
+                        else set_status(p.status, RPA_ERR_BAD_PAGE_INDEX);
                     }
                 }
-                if (r < p.Hq) {
-                    QT* o = reinterpret_cast<QT*>(p.q_out) + ((size_t)t * p.Hq + r) * p.D;
-                    store_q8(o + e0, y);
-                    store_q8(o + e1, y + 8);
-                } else if (slot >= 0) {
-                    const bool is_v = r >= p.Hq + p.Hkv;
-                    const int h = r - p.Hq - (is_v ? p.Hkv : 0);
-                    if (is_v ? p.has_vs : p.has_ks) {
-                        const float sc = is_v ? p.v_scale : p.k_scale;
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) y[i] = __fdiv_rn(y[i], sc);
-                    }
-                    const int rows = p.latent ? p.Hkv : 2 * p.Hkv;
-                    const size_t row = ((size_t)slot * rows + (p.latent ? h : 2 * h + (is_v ? 1 : 0))) * p.D *
-                                       (kt_8bit(p.kt) ? 1 : 2);
-                    store_kv8(p.kv, row, e0, y, p.kt);
-                    store_kv8(p.kv, row, e1, y + 8, p.kt);
-                }
+                s_live[i] = live;
+                s_pos[i] = pos;
+                s_slot[i] = slot;
             }
         }
+        __syncthreads();
+        float2* cs2 = reinterpret_cast<float2*>(s_cs);
+        for (int i = tid; i < n * (p.rd / 2); i += blockDim.x) {
+            const int k = i / (p.rd / 2), pair = i - k * (p.rd / 2);
+            // the angle's fraction of a turn, its upper 32 bits as half turns in [-1, 1)
+            const unsigned long long f = p.turns[pair] * (unsigned long long)(long long)s_pos[k];
+            float sn, cs;
+            sincospif((float)(int)((f + 0x80000000ull) >> 32) * 4.656612873077393e-10f, &sn, &cs);
+            cs2[((k * 4 + (pair & 7) / 2) * places + pair / 8) * 2 + (pair & 1)] = make_float2(cs * p.magnitude, sn * p.magnitude);
+        }
+        __syncthreads();
+        while (tk < n) {
+            int tb = tk, rb = r;
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                if (tb < n && s_live[tb]) {
+                    float y[16];
+                    widen(x0[b], y);
+                    widen(x1[b], y + 8);
+                    if (rot && rb < p.Hq + p.Hkv) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float4 cs = s_cs[(tb * 4 + i) * places + place];  // cos, sin of pairs 2 i and 2 i + 1
+#pragma unroll
+                            for (int j = 0; j < 2; ++j) {
+                                const int m = 2 * i + j, a = HALF ? m : 2 * m, c = HALF ? m + 8 : 2 * m + 1;
+                                const float co = j ? cs.z : cs.x, si = j ? cs.w : cs.y, u = y[a], w = y[c];
+                                y[a] = u * co - w * si;
+                                y[c] = w * co + u * si;
+                            }
+                        }
+                    }
+                    if (rb < p.Hq) {
+                        QT* o = reinterpret_cast<QT*>(p.q_out) + ((size_t)(t0 + tb) * p.Hq + rb) * p.D;
+                        store_q8(o + e0, y);
+                        store_q8(o + e1, y + 8);
+                    } else if (s_slot[tb] >= 0) {
+                        const bool is_v = rb >= p.Hq + p.Hkv;
+                        const int h = rb - p.Hq - (is_v ? p.Hkv : 0);
+                        if (is_v ? p.has_vs : p.has_ks) {
+                            const float sc = is_v ? p.v_scale : p.k_scale;
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) y[i] = __fdiv_rn(y[i], sc);
+                        }
+                        const int rows = p.latent ? p.Hkv : 2 * p.Hkv;
+                        const size_t row = ((size_t)s_slot[tb] * rows + (p.latent ? h : 2 * h + (is_v ? 1 : 0))) * p.D *
+                                           (kt_8bit(p.kt) ? 1 : 2);
+                        store_kv8(p.kv, row, e0, y, p.kt);
+                        store_kv8(p.kv, row, e1, y + 8, p.kt);
+                    }
+                }
+                next(tb, rb);
+            }
+            tk = tb;
+            r = rb;
+            if (tk < n) fetch(tk, r);
+        }
+        __syncthreads();  // the round's tables are free again
     }
     // the lengths of every sequence, once
-    if (t == 0) {
+    if (blockIdx.x == 0) {
         for (int s = tid; s < p.S; s += blockDim.x) {
             const int q0 = p.cu[s], q1 = p.cu[s + 1], kl = p.kv_lens[s];
             if (q0 < 0 || q1 < q0 || kl < 0 || kl > p.P * p.ps || q1 - q0 > kl || q1 > p.T)
@@ -277,8 +296,9 @@ __global__ void __launch_bounds__(kMaxThreads) rpa_rope_kernel(const RopeParams 
 
 template <typename QT>
 cudaError_t launch_rope(const RopeParams& p, int half, int grid, int threads, cudaStream_t st) {
-    return half ? launch_pdl(rpa_rope_kernel<QT, true>, grid, threads, 0, st, p)
-                : launch_pdl(rpa_rope_kernel<QT, false>, grid, threads, 0, st, p);
+    const size_t smem = (size_t)kTokens * (p.rd / 2) * sizeof(float2);  // at most 36 KB
+    return half ? launch_pdl(rpa_rope_kernel<QT, true>, grid, threads, smem, st, p)
+                : launch_pdl(rpa_rope_kernel<QT, false>, grid, threads, smem, st, p);
 }
 
 constexpr double kTwoPi = 6.283185307179586476925286766559;
@@ -373,6 +393,7 @@ int rpa_rope_create(const RpaRopeCfg* cfg, RpaRope** out) {
     const int n = (int)(cfg->rotary_dim / 2);
     for (int i = 0; i < n; ++i) f[i] = (unsigned long long)std::ldexp(w[i] / kTwoPi, 64);
     if (cudaGetDevice(&h->device) != cudaSuccess ||
+        cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess ||
         cudaMalloc(&h->turns, (size_t)(n + 1) * sizeof f[0]) != cudaSuccess) {
         cudaGetLastError();
         delete h;
@@ -438,7 +459,7 @@ int rpa_rope_append(RpaRope* h, const void* q, int64_t q_stride, const void* k, 
     p.off = (int)h->cfg.rotary_offset;
     p.rows = p.Hq + (latent ? 1 : 2) * p.Hkv;
     p.per_row = p.D / kUnit;
-    p.row_step = (p.per_row == 36 ? 288 : 256) / p.per_row;
+    p.row_step = kRopeThreads / p.per_row;
     p.kt = c.kv_dtype == RPA_DT_F16 ? KT_F16 : c.kv_dtype == RPA_DT_FP8_E4M3 ? KT_E4M3
          : c.kv_dtype == RPA_DT_FP8_E5M2 ? KT_E5M2 : c.kv_dtype == RPA_DT_INT8 ? KT_I8 : KT_BF16;
     p.has_ks = c.has_k_scale;
@@ -446,8 +467,9 @@ int rpa_rope_append(RpaRope* h, const void* q, int64_t q_stride, const void* k, 
     p.k_scale = c.k_scale;
     p.v_scale = c.v_scale;
     p.magnitude = (float)h->cfg.magnitude;
-    const int threads = p.per_row * p.row_step, half = h->cfg.pairing == RPA_ROPE_HALF;
-    const int grid = p.T > 0 ? p.T : 1;  // without tokens one CTA still checks the lengths
+    const int threads = kRopeThreads, half = h->cfg.pairing == RPA_ROPE_HALF;
+    // a token a CTA at least; without tokens one CTA still checks the lengths
+    const int most = h->sms * kRopeCtas, grid = p.T < 1 ? 1 : p.T < most ? p.T : most;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = c.q_dtype == RPA_DT_F32   ? launch_rope<float>(p, half, grid, threads, st)
                           : c.q_dtype == RPA_DT_F16 ? launch_rope<__half>(p, half, grid, threads, st)
