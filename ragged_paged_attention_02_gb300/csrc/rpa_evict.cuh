@@ -23,7 +23,7 @@ struct FastDiv {
 // ---------------------------------------------------------------- accumulated weights
 constexpr int kWeighRows = 16;     // query rows (tokens x heads of a group) of a block
 constexpr int kWeighAlign = 128;   // pieces are multiples of this many keys
-constexpr int kWeighKeys = 128;    // keys of a weigh item
+constexpr int kWeighKeys = 128;    // keys of a weigh item that reads logits back
 constexpr int kWeighThreads = 128;
 
 struct WeighParams {
@@ -40,6 +40,7 @@ struct WeighParams {
     const float* sinks;
     FastDiv page, group;
     int max_pieces;          // most pieces of a sequence
+    int item_keys;           // keys of a weigh item that computes them again
     int ctas;                // of the stats kernel (all resident)
     int BR, br_shift;        // keys of a copied page run: gcd(page_size, 64), and its log2
     uint32_t all_runs;       // a bit for each run of 64 keys

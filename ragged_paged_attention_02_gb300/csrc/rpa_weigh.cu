@@ -9,9 +9,9 @@
 //   stats    item = (sequence, kv head, block of 16 rows, piece): x = q K^T on warp MMAs, maxima and
 //            sums; a block's last warp to finish merges all of them, in order.  Where a sequence has
 //            one block of rows (decode), x itself goes to the workspace.
-//   weigh    a warp takes (sequence, kv head, 64 keys): reads x back, or with more blocks computes it
-//            again (K from L2, all row blocks past the keys in its registers), and adds the weights'
-//            sum to the scores
+//   weigh    a warp takes (sequence, kv head, 128 keys) and reads x back, or with more blocks takes 16 to
+//            64 keys and computes it again (K from L2, all row blocks past the keys in its registers),
+//            and adds the weights' sum to the scores
 //
 // Decode is bound by reading K: 2 D bytes a key and head, beside which x is 4 G bytes (6 % at D 128,
 // G 4) and stays in L2, where a second pass over K would double the traffic.  S^T = K Q^T: 16 keys on
@@ -83,22 +83,16 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_weigh_plan_kernel(const W
     long long n_logits = 0;
     for (int base = 0; base < p.S; base += kPlanThreads) {
         const int s = base + tid;
-        int add[3] = {0, 0, 0}, off[3], tot[3];
-        long long logits = 0;
+        int add[3] = {0, 0, 0}, off[3], tot[3], n_keys = 0;
+        long long logits = 0, rows = 0;
         if (s < p.S) {
-            const int ql = p.cu[s + 1] - p.cu[s], kl = p.kv_lens[s], n_keys = kl - first_key(p, kl, ql);
-            const long long rows = (long long)ql * p.G;
-            if (rows > 0) {
-                const int pieces = min((n_keys + chunk - 1) / chunk, p.max_pieces);
-                add[2] = (int)((rows + kWeighRows - 1) / kWeighRows) * p.Hkv;
-                add[0] = add[2] * pieces;
-                add[1] = (n_keys + kWeighKeys - 1) / kWeighKeys * p.Hkv;
-                // (each sequence's start on 16 bytes)
-                if (rows <= kWeighRows) logits = ((long long)n_keys * p.Hkv * ((rows + 1) & ~1ll) + 3) & ~3ll;
-            }
+            const int ql = p.cu[s + 1] - p.cu[s], kl = p.kv_lens[s];
+            n_keys = kl - first_key(p, kl, ql);
+            rows = (long long)ql * p.G;
+            // (each sequence's start on 16 bytes)
+            if (rows > 0 && rows <= kWeighRows) logits = ((long long)n_keys * p.Hkv * ((rows + 1) & ~1ll) + 3) & ~3ll;
         }
-        block_scan<3>(add, off, tot, s_scan);
-        // the same scan of the 64-bit logit counts
+        // where each sequence's logits start: a scan of 64-bit counts
         long long sum = logits;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -113,13 +107,20 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_weigh_plan_kernel(const W
             if (w < warp) before += y;
             all += y;
         }
-        __syncthreads();
+        const long long at = n_logits + before + sum - logits;
+        const bool keep = logits > 0 && at + logits <= p.max_logits;
+        if (rows > 0) {
+            const int pieces = min((n_keys + chunk - 1) / chunk, p.max_pieces), item = keep ? kWeighKeys : p.item_keys;
+            add[2] = (int)((rows + kWeighRows - 1) / kWeighRows) * p.Hkv;
+            add[0] = add[2] * pieces;
+            add[1] = (n_keys + item - 1) / item * p.Hkv;
+        }
+        block_scan<3>(add, off, tot, s_scan);
         if (s < p.S) {
-            const long long at = n_logits + before + sum - logits;
             p.stat0[s] = n[0] + off[0];
             p.item0[s] = n[1] + off[1];
             p.block0[s] = n[2] + off[2];
-            p.logit0[s] = logits > 0 && at + logits <= p.max_logits ? at : -1;
+            p.logit0[s] = keep ? at : -1;
         }
 #pragma unroll
         for (int i = 0; i < 3; ++i) n[i] += tot[i];
@@ -438,26 +439,30 @@ __device__ __forceinline__ bool stat_item(const WeighParams& p, const StageMeta*
         Acc acc;
         if (any) {
             // two chains of MMAs where there is one block of rows
-            float odd[NB][4];
+            float odd[1][4] = {{0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
             for (int n = 0; n < NB; ++n)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[n][e] = odd[n][e] = 0.f;
+                for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
 #pragma unroll
             for (int b = 0; b < LOADS; ++b) {
                 if (!kEarly) {
                     lo[b] = read16(from + key_at[0] + b * column);
                     hi[b] = read16(from + key_at[1] + b * column);
                 }
-                if (NB == 1 && (b & 1)) load_dot<KT>(lo[b], hi[b], b, q, odd);
-                else load_dot<KT>(lo[b], hi[b], b, q, acc);
+                if constexpr (NB == 1) {
+                    if (b & 1) load_dot<KT>(lo[b], hi[b], b, q, odd);
+                    else load_dot<KT>(lo[b], hi[b], b, q, acc);
+                } else {
+                    load_dot<KT>(lo[b], hi[b], b, q, acc);
+                }
+            }
+            if (NB == 1) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[0][e] += odd[0][e];
             }
 #pragma unroll
-            for (int n = 0; n < NB; ++n) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) acc[n][e] += odd[n][e];
-                scale(p, acc[n]);
-            }
+            for (int n = 0; n < NB; ++n) scale(p, acc[n]);
         }
         if (!kEarly) free_stage();
         if (any) {
@@ -481,13 +486,13 @@ __device__ __forceinline__ bool stat_item(const WeighParams& p, const StageMeta*
             }
             if (lane < 4) part[my_part * kWeighRows + 8 * b + 2 * lane + i] = make_float2(m[b][i], l[b][i]);
         }
-    __threadfence();
     __syncwarp();
-    int last = 0;
-    if (lane == 0) last = atomicAdd(p.done + block, 1) == parts - 1;
-    if (!__shfl_sync(0xffffffffu, last, 0)) return true;
+    int before = 0;
+    if (lane == 0)
+        asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;\n" : "=r"(before) : "l"(p.done + block) : "memory");
+    if (__shfl_sync(0xffffffffu, before, 0) != parts - 1) return true;
     // the block's last warp merges all parts: a lane half of a row's, in order
-    __threadfence();
+    __syncwarp();
     const int r = lane % kWeighRows;
     float mm = -INFINITY, ll = 0.f;
     if (r < 8 * NB) {
@@ -629,10 +634,12 @@ __device__ __forceinline__ void add_score(float* dst, bool fresh, float w) {
     else atomicAdd(dst, w);
 }
 
+// Key tiles of 16 a warp holds while it goes through the rows: 32 registers of K (64 at D 256)
+__host__ __device__ constexpr int weigh_tiles(int loads) { return loads >= 4 ? 1 : 4 / loads; }
+
 template <int D, int KT>
 __global__ void __launch_bounds__(kWeighThreads, D == 256 ? 2 : 4) rpa_weigh_kernel(const WeighParams p) {
-    // key tiles of 16 a warp holds while it goes through the rows: 32 registers of K (64 at D 256)
-    constexpr int kTiles = Deal<D, KT>::LOADS >= 4 ? 1 : 4 / Deal<D, KT>::LOADS;
+    constexpr int kTiles = weigh_tiles(Deal<D, KT>::LOADS);
     pdl_trigger();
     pdl_wait();
     const int items = p.ctrl[1], lane = threadIdx.x & 31, quad = lane % 4;
@@ -640,12 +647,13 @@ __global__ void __launch_bounds__(kWeighThreads, D == 256 ? 2 : 4) rpa_weigh_ker
         const int s = find_seq(p.item0, p.S, it, lane);
         const int q0 = p.cu[s], ql = p.cu[s + 1] - q0, kl = p.kv_lens[s], pos0 = kl - ql;
         const int base = first_key(p, kl, ql), at = it - p.item0[s], h = at % p.Hkv;
-        const int j0 = base + at / p.Hkv * kWeighKeys, j1 = min(kl, j0 + kWeighKeys);
+        const long long lo0 = p.logit0[s];
+        const int n_keys = lo0 >= 0 ? kWeighKeys : 16 * kTiles;
+        const int j0 = base + at / p.Hkv * n_keys, j1 = min(kl, j0 + n_keys);
         const int lo = p.has_window ? max(0, pos0 - p.window + 1) : 0;  // keys below are seen by no row
         const int rows = ql * p.G, nb = (rows + kWeighRows - 1) / kWeighRows;
         const int* table = p.page_indices + (size_t)s * p.P;
         const float* stat = p.stat + (size_t)(p.block0[s] + h * nb) * kWeighRows;
-        const long long lo0 = p.logit0[s];
         if (lo0 >= 0) {
             // four keys a lane; lane r holds row r's statistic
             constexpr int KL = kWeighKeys / 32;
@@ -697,71 +705,74 @@ __global__ void __launch_bounds__(kWeighThreads, D == 256 ? 2 : 4) rpa_weigh_ker
 #pragma unroll
             for (int k = 0; k < KL; ++k) add_score(dst[k], j0 + lane + 32 * k >= pos0, w[k]);
         } else {
-            for (int k0 = j0; k0 < j1; k0 += 16 * kTiles) {
-                KeyTile<D, KT> t[kTiles];
-                float w[kTiles][2];
-                const uint64_t policy = l2_policy_normal();
+            KeyTile<D, KT> t[kTiles];
+            float w[kTiles][2];
+            const uint64_t policy = l2_policy_normal();
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) {
+                load_k<D, KT>(p, table, h, j0 + 16 * i, j1, lane, policy, t[i]);
+                w[i][0] = w[i][1] = 0.f;
+            }
+            bool full = true;  // every key of the tiles is there
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) full = full && t[i].ok[0] && t[i].ok[1];
+            full = __all_sync(0xffffffffu, full);
+            // rows whose tokens see one of the keys
+            int r_lo = 0, r_hi = rows;
+            if (p.causal) r_lo = max(0, j0 - pos0) * p.G & ~7;
+            if (p.has_window) r_hi = (int)min((long long)rows, max(0ll, (long long)j1 - 1 + p.window - pos0) * p.G);
+            // operands of kDeep row blocks: the loads of the next ones (an L2 latency of several blocks) behind this one
+            constexpr int kDeep = D == 64 ? 4 : D == 128 && !kt_8bit(KT) ? 3 : 2;
+            uint32_t q[kDeep][1][Deal<D, KT>::REGS];
+            float2 st[kDeep];  // of rows 2 quad and 2 quad + 1
+            auto fetch = [&](int r0, int b) {
+                load_q<D, KT>(p, q0, h, r0 + lane / 4, rows, quad, q[b][0]);
+                st[b] = *reinterpret_cast<const float2*>(stat + r0 + 2 * quad);
+            };
+            auto add = [&](auto masked, int r0, int b) {
+                constexpr bool MASK = decltype(masked)::value;
+                const int r = r0 + 2 * quad;
+                const int pa = MASK ? pos0 + p.group.div(r) : 0, pb = MASK ? pos0 + p.group.div(r + 1) : 0;
+                // rows behind the last are no rows (0 times a K that may be infinite; no statistics)
+                const bool ra = r < rows, rb = r + 1 < rows;
 #pragma unroll
                 for (int i = 0; i < kTiles; ++i) {
-                    load_k<D, KT>(p, table, h, k0 + 16 * i, j1, lane, policy, t[i]);
-                    w[i][0] = w[i][1] = 0.f;
-                }
-                const int k1 = min(j1, k0 + 16 * kTiles);
-                bool full = true;  // every key of the tiles is there
+                    float acc[1][4] = {{0.f, 0.f, 0.f, 0.f}};
+                    tile_dot<D, KT, 1>(t[i], q[b], acc);
+                    scale(p, acc[0]);
 #pragma unroll
-                for (int i = 0; i < kTiles; ++i) full = full && t[i].ok[0] && t[i].ok[1];
-                full = __all_sync(0xffffffffu, full);
-                // rows whose tokens see one of the keys
-                int r_lo = 0, r_hi = rows;
-                if (p.causal) r_lo = max(0, k0 - pos0) * p.G & ~7;
-                if (p.has_window) r_hi = (int)min((long long)rows, max(0ll, (long long)k1 - 1 + p.window - pos0) * p.G);
-                uint32_t q[2][1][Deal<D, KT>::REGS];
-                float2 st[2];  // of rows 2 quad and 2 quad + 1
-                auto fetch = [&](int r0, int b) {
-                    load_q<D, KT>(p, q0, h, r0 + lane / 4, rows, quad, q[b][0]);
-                    st[b] = *reinterpret_cast<const float2*>(stat + r0 + 2 * quad);
-                };
-                auto add = [&](auto masked, int r0, int b) {
-                    constexpr bool MASK = decltype(masked)::value;
-                    const int r = r0 + 2 * quad;
-                    const int pa = MASK ? pos0 + p.group.div(r) : 0, pb = MASK ? pos0 + p.group.div(r + 1) : 0;
-                    // rows behind the last are no rows (0 times a K that may be infinite; no statistics)
-                    const bool ra = r < rows, rb = r + 1 < rows;
-#pragma unroll
-                    for (int i = 0; i < kTiles; ++i) {
-                        float acc[1][4] = {{0.f, 0.f, 0.f, 0.f}};
-                        tile_dot<D, KT, 1>(t[i], q[b], acc);
-                        scale(p, acc[0]);
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int j = k0 + 16 * i + 8 * k + lane / 4;
-                            w[i][k] += (ra ? ex2(hide<MASK>(p, acc[0][2 * k], j, pa, t[i].ok[k]) - st[b].x) : 0.f) +
-                                       (rb ? ex2(hide<MASK>(p, acc[0][2 * k + 1], j, pb, t[i].ok[k]) - st[b].y) : 0.f);
-                        }
+                    for (int k = 0; k < 2; ++k) {
+                        const int j = j0 + 16 * i + 8 * k + lane / 4;
+                        w[i][k] += (ra ? ex2(hide<MASK>(p, acc[0][2 * k], j, pa, t[i].ok[k]) - st[b].x) : 0.f) +
+                                   (rb ? ex2(hide<MASK>(p, acc[0][2 * k + 1], j, pb, t[i].ok[k]) - st[b].y) : 0.f);
                     }
-                };
-                auto step = [&](int r0, int b) {
-                    const int a = pos0 + p.group.div(r0), z = pos0 + p.group.div(min(r0 + 7, rows - 1));
-                    if (full && !some_hidden(p, k0, k0 + 16 * kTiles, a, z)) add(std::false_type{}, r0, b);
-                    else add(std::true_type{}, r0, b);
-                };
-                if (r_lo < r_hi) fetch(r_lo, 0);
-                for (int r0 = r_lo; r0 < r_hi; r0 += 16) {
-                    if (r0 + 8 < r_hi) fetch(r0 + 8, 1);
-                    step(r0, 0);
-                    if (r0 + 16 < r_hi) fetch(r0 + 16, 0);
-                    if (r0 + 8 < r_hi) step(r0 + 8, 1);
                 }
+            };
+            auto step = [&](int r0, int b) {
+                const int a = pos0 + p.group.div(r0), z = pos0 + p.group.div(min(r0 + 7, rows - 1));
+                if (full && !some_hidden(p, j0, j0 + 16 * kTiles, a, z)) add(std::false_type{}, r0, b);
+                else add(std::true_type{}, r0, b);
+            };
 #pragma unroll
-                for (int i = 0; i < kTiles; ++i) {
+            for (int b = 0; b + 1 < kDeep; ++b)
+                if (r_lo + 8 * b < r_hi) fetch(r_lo + 8 * b, b);
+            for (int r0 = r_lo; r0 < r_hi; r0 += 8 * kDeep) {
 #pragma unroll
-                    for (int o = 1; o < 4; o <<= 1) {
-                        w[i][0] += __shfl_xor_sync(0xffffffffu, w[i][0], o);
-                        w[i][1] += __shfl_xor_sync(0xffffffffu, w[i][1], o);
-                    }
-                    const int j = k0 + 16 * i + lane / 4 + 8 * quad;
-                    if (quad < 2 && j >= lo && j < j1) add_score(score_at(p, table, h, j), j >= pos0, quad ? w[i][1] : w[i][0]);
+                for (int b = 0; b < kDeep; ++b) {
+                    const int r = r0 + 8 * b;
+                    if (r + 8 * (kDeep - 1) < r_hi) fetch(r + 8 * (kDeep - 1), (b + kDeep - 1) % kDeep);
+                    if (r < r_hi) step(r, b);
                 }
+            }
+#pragma unroll
+            for (int i = 0; i < kTiles; ++i) {
+#pragma unroll
+                for (int o = 1; o < 4; o <<= 1) {
+                    w[i][0] += __shfl_xor_sync(0xffffffffu, w[i][0], o);
+                    w[i][1] += __shfl_xor_sync(0xffffffffu, w[i][1], o);
+                }
+                const int j = j0 + 16 * i + lane / 4 + 8 * quad;
+                if (quad < 2 && j >= lo && j < j1) add_score(score_at(p, table, h, j), j >= pos0, quad ? w[i][1] : w[i][0]);
             }
         }
     }
@@ -775,7 +786,8 @@ struct WeighKern {
             e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(stats, rpa_weigh_stats_kernel<D, KT>, kStatThreads, Ring<D, KT>::SMEM);
         return e != cudaSuccess ? e : cudaOccupancyMaxActiveBlocksPerMultiprocessor(weigh, rpa_weigh_kernel<D, KT>, kWeighThreads, 0);
     }
-    static cudaError_t launch(const CUtensorMap& kmap, const WeighParams& p, int grid_weigh, cudaStream_t st) {
+    static cudaError_t launch(const CUtensorMap& kmap, WeighParams p, int grid_weigh, cudaStream_t st) {
+        p.item_keys = 16 * weigh_tiles(Deal<D, KT>::LOADS);
         cudaError_t e = launch_pdl(rpa_weigh_plan_kernel, 1, kPlanThreads, 0, st, p);
         if (e == cudaSuccess) e = launch_pdl(rpa_weigh_stats_kernel<D, KT>, p.ctas, kStatThreads, Ring<D, KT>::SMEM, st, kmap, p);
         if (e == cudaSuccess) e = launch_pdl(rpa_weigh_kernel<D, KT>, grid_weigh, kWeighThreads, 0, st, p);
