@@ -26,9 +26,11 @@ namespace rpa {
 
 namespace {
 
+// FLOP/ns of one SM on a prefix's tiles beside the decode kernel: above rpa_forward's 6500 of prompt chunks, whose
+// diagonal tiles are masked.  (256 x 16 k: 151 us a call from 8100 to 9300, 163 at 6500, 171 at 10800.)
+constexpr int kPrefixSmGflops = 8700;
 constexpr int kPieceAlign = 128;   // keys: the prefill kernels' tiles
-constexpr int kPieceKeys = 256;    // smallest decode piece: the keys behind a prefix are few, and so is what fills the SMs
-constexpr int kPieceCost = 256;    // what a piece costs beside its keys, in keys
+constexpr int kPieceCost = 512;    // what a piece costs beside its keys, in keys (256: 167 us, 512 and 1024: 163, for 256 x 16 k)
 static_assert(kPlanThreads >= 160, "a candidate a thread");
 constexpr int kMaxPieces = 160;    // most pieces of a prefix: one an SM where a single head and tile have all of them
 
@@ -174,22 +176,21 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_prefix_plan_kernel(const 
         give_up(RPA_ERR_BAD_LENGTHS);
         return;
     }
-    // ---- 2. SMs of each kernel when both run at once, by rpa_forward's rates: x SMs of prefill take F / (x a), the
-    // others B / ((n - x) d), but no less than B / hbm; they end together where F d (n - x) = B a x, and SMs past
-    // those that saturate the memory are prefill's
+    // ---- 2. SMs of each kernel when both run at once: x SMs of prefill take F / (x a), the others B / ((n - x) d);
+    // they end together where F d (n - x) = B a x
     int pf_ctas = p.n_sms * p.pf_bps, dec_ctas = p.n_sms * p.dec_bps;
     if (p.concurrent && dec_keys && pf_keys) {
         const float B = (float)dec_keys * (float)(2 * p.D * p.kv_elt), F = (float)pf_keys * (float)p.pf_mma_rows * (float)(4 * p.D);
-        const float fd = F * (float)kDecSmGBs, ba = B * (float)kPfSmGflopsTc;
+        const float fd = F * (float)kDecSmGBs, ba = B * (float)kPrefixSmGflops;
         int x = (int)((float)p.n_sms * fd / (fd + ba) + 0.5f);
-        x = min(max(max(x, 1), p.n_sms - (kHbmGBs + kDecSmGBs - 1) / kDecSmGBs), p.n_sms - 1);
+        x = min(max(x, 1), p.n_sms - 1);
         pf_ctas = x * p.pf_bps;
         dec_ctas = (p.n_sms - x) * p.dec_bps;
     }
     // ---- 3. keys of a decode piece, and of a piece of a prefix's tiles
     const int on = p.dec_on_pf ? pf_ctas : dec_ctas;
     const unsigned long long want = dec_keys / (unsigned long long)max(1, p.dec_waves * on) + 1;
-    const int chunk = (int)min(max((want + kChunkAlign - 1) / kChunkAlign * kChunkAlign, (unsigned long long)kPieceKeys), 1ull << 30);
+    const int chunk = (int)min(max((want + kChunkAlign - 1) / kChunkAlign * kChunkAlign, (unsigned long long)kMinChunk), 1ull << 30);
     int pf_chunk = kPieceAlign;
     if (longest > 0) {
         // pieces of the longest prefix: a candidate a thread, the warps' bests by cost and then by number
