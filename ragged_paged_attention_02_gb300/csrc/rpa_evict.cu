@@ -30,10 +30,8 @@ namespace rpa {
 
 namespace {
 
-constexpr int kSelThreads = 512;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kMaxCluster = 8;
+constexpr int kMaxCluster = 4;
 constexpr int kSelCached = 40 * 1024;  // scores a CTA keeps at most (160 KB); further ones are read again
 constexpr int kMoveThreads = 256;
 constexpr int kMoveCtas = 4;  // resident an SM
@@ -62,17 +60,8 @@ __device__ __forceinline__ uint2 cluster_load2(uint32_t addr, uint32_t rank) {
     asm volatile("ld.shared::cluster.v2.u32 {%0, %1}, [%2];\n" : "=r"(v.x), "=r"(v.y) : "r"(at) : "memory");
     return v;
 }
-__device__ __forceinline__ uint4 cluster_load4(uint32_t addr, uint32_t rank) {
-    uint32_t at;
-    uint4 v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;\n" : "=r"(at) : "r"(addr), "r"(rank));
-    asm volatile("ld.shared::cluster.v4.u32 {%0, %1, %2, %3}, [%4];\n"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(at)
-                 : "memory");
-    return v;
-}
 // Exclusive sum of v over the block's threads before this one, and the total
+template <int kSelWarps>
 __device__ __forceinline__ uint32_t block_before(uint32_t v, uint32_t* s_warp, uint32_t& total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint32_t sum = v;
@@ -94,10 +83,11 @@ __device__ __forceinline__ uint32_t block_before(uint32_t v, uint32_t* s_warp, u
     return sum - v + (warp > 0 ? before : 0u);
 }
 
-// CLUSTER: several CTAs a unit (few units); else one (many: as many resident as there are registers for, three an SM).
-// (1024 threads a CTA of a cluster took 42 us for 2 x 100 k keys where 512 take 34.)
+// CLUSTER: several CTAs of 1024 threads a unit (few units: their own time counts), one an SM, for two on one SM would
+// share its issue slots while others idle; else one of 512 (many units: three CTAs an SM)
 template <bool CLUSTER>
-__global__ void __launch_bounds__(kSelThreads, CLUSTER ? 1 : 3) rpa_evict_select_kernel(const CompactParams p) {
+__global__ void __launch_bounds__(CLUSTER ? 1024 : 512, CLUSTER ? 1 : 3) rpa_evict_select_kernel(const CompactParams p) {
+    constexpr int kSelThreads = CLUSTER ? 1024 : 512, kSelWarps = kSelThreads / 32;
     extern __shared__ __align__(16) uint32_t s_key[];  // [cached] the scores of the first of this CTA's competing keys
     __shared__ __align__(16) uint32_t s_hist[2][kBins];
     __shared__ uint32_t s_warp[kSelWarps], s_warp2[kSelWarps];
@@ -223,20 +213,18 @@ __global__ void __launch_bounds__(kSelThreads, CLUSTER ? 1 : 3) rpa_evict_select
         else __syncthreads();
         // thread t: the kMine bins from kBins - 1 - kMine t down, over all CTAs; c[0] the highest
         constexpr int kMine = kBins / kSelThreads;
-        static_assert(kMine == 4, "one load a CTA");
+        static_assert(kMine == (CLUSTER ? 2 : 4), "one load a CTA");
         const int low = kBins - kMine * (tid + 1);
         uint32_t c[kMine];
         if constexpr (CLUSTER) {
-            uint4 x[kMaxCluster];  // all CTAs' loads in flight
+            uint2 x[kMaxCluster];  // all CTAs' loads in flight
 #pragma unroll
-            for (int r = 0; r < kMaxCluster; ++r) x[r] = r < C ? cluster_load4(smem_u32(hist + low), r) : make_uint4(0u, 0u, 0u, 0u);
-            c[0] = c[1] = c[2] = c[3] = 0;
+            for (int r = 0; r < kMaxCluster; ++r) x[r] = r < C ? cluster_load2(smem_u32(hist + low), r) : make_uint2(0u, 0u);
+            c[0] = c[1] = 0;
 #pragma unroll
             for (int r = 0; r < kMaxCluster; ++r) {
-                c[3] += x[r].x;
-                c[2] += x[r].y;
-                c[1] += x[r].z;
-                c[0] += x[r].w;
+                c[1] += x[r].x;
+                c[0] += x[r].y;
             }
         } else {
 #pragma unroll
@@ -245,7 +233,7 @@ __global__ void __launch_bounds__(kSelThreads, CLUSTER ? 1 : 3) rpa_evict_select
         uint32_t mine_sum = 0;
 #pragma unroll
         for (int i = 0; i < kMine; ++i) mine_sum += c[i];
-        uint32_t total, above = block_before(mine_sum, s_warp, total);
+        uint32_t total, above = block_before<kSelWarps>(mine_sum, s_warp, total);
 #pragma unroll
         for (int i = 0; i < kMine; ++i) {
             if (above < left && left <= above + c[i]) {
@@ -278,8 +266,8 @@ __global__ void __launch_bounds__(kSelThreads, CLUSTER ? 1 : 3) rpa_evict_select
     gt = __reduce_add_sync(0xffffffffu, gt);
     eq = __reduce_add_sync(0xffffffffu, eq);
     uint32_t all_gt, all_eq;
-    uint32_t g0 = block_before(lane == 0 ? gt : 0u, s_warp, all_gt);
-    uint32_t e0 = block_before(lane == 0 ? eq : 0u, s_warp2, all_eq);
+    uint32_t g0 = block_before<kSelWarps>(lane == 0 ? gt : 0u, s_warp, all_gt);
+    uint32_t e0 = block_before<kSelWarps>(lane == 0 ? eq : 0u, s_warp2, all_eq);
     g0 = __shfl_sync(0xffffffffu, g0, 0);
     e0 = __shfl_sync(0xffffffffu, e0, 0);
     if constexpr (CLUSTER) {
@@ -400,7 +388,7 @@ __global__ void __launch_bounds__(kMoveThreads, kMoveCtas) rpa_evict_move_kernel
 cudaError_t compact_prepare(int64_t units, int max_keys, int sms, int* cluster, int* cached) {
     // as many CTAs a unit as two an SM allow, of 2 k keys at least
     int c = 1;
-    while (c < kMaxCluster && units * (2 * c) <= 2 * sms && max_keys / (2 * c) >= 2048) c *= 2;
+    while (c < kMaxCluster && 3 * units * (2 * c) <= 2 * sms && max_keys / (2 * c) >= 2048) c *= 2;
     *cluster = c;
     const int share = ((max_keys + 3) / 4 + 1 + c - 1) / c * 4;  // (one quad more where neither end is a quad's)
     *cached = share < kSelCached ? share : kSelCached;
@@ -412,7 +400,7 @@ cudaError_t launch_compact(const CompactParams& p, int sms, cudaStream_t st) {
     if (p.S == 0) return cudaSuccess;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(p.S * p.Hkv * p.cluster);
-    cfg.blockDim = dim3(kSelThreads);
+    cfg.blockDim = dim3(p.cluster > 1 ? 1024 : 512);
     cfg.dynamicSmemBytes = (size_t)p.cached * 4;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
