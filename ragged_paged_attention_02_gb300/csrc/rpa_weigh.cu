@@ -73,10 +73,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_weigh_plan_kernel(const W
         }
         return;
     }
-    // keys of a piece: eight pieces a resident CTA, so that uneven ones even out, but not under 512 keys (a piece costs
+    // keys of a piece: four pieces a resident CTA, so that uneven ones even out, but not under 512 keys (a piece costs
     // about what 100 keys do) unless that leaves CTAs without any
     const unsigned long long slots = (unsigned long long)p.ctas;
-    const unsigned long long want = max(keys / (8 * slots), min(512ull, keys / slots));
+    const unsigned long long want = max(keys / (4 * slots), min(512ull, keys / slots));
     const int chunk = (int)min((want / kWeighAlign + (want % kWeighAlign ? 1 : 0)) * kWeighAlign + (want ? 0 : kWeighAlign), 1ull << 30);
     // per sequence: stat items, weigh items, row blocks; and logits
     int n[3] = {0, 0, 0};
