@@ -416,8 +416,8 @@ int rpa_evict_accumulate(RpaEvict* h, const void* q, const void* kv_pages, const
  * sequence's new pages.
  *   new_page_indices  device, int32 [max_num_seqs, pages_per_seq].  page_indices itself: the cache is
  *                     compacted in place.  Else each entry in use is the page of the same place in
- *                     page_indices, or a page that no sequence of the call reads; no two sequences
-                     write one page (the first pages may stay shared where `protect` covers them whole).
+ *                     page_indices, or a page that no sequence of the call reads; no page is written
+                     twice (the first pages may stay shared where `protect` covers them whole).
  *   new_kv_lens       device, int32 [max_num_seqs], written: min(kv_len, budget)  (may be kv_lens itself)
  *   kept              device, int32 [max_num_seqs, Hkv, budget], or NULL; written: the slots kept, in order,
  *                     -1 behind the last

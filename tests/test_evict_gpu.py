@@ -279,6 +279,31 @@ def test_accumulate_in_a_graph_and_on_another_stream():
         assert torch.equal(scores, other)
 
 
+def test_many_sequences():
+    rng = np.random.default_rng(28)
+    q_lens = [int(x) for x in rng.choice([0, 1, 1, 2, 9], 1100)]
+    b = Batch(rng, q_lens, [n + int(x) for n, x in zip(q_lens, rng.integers(0, 60, 1100))], 8, 4, 2, 64)
+    run_and_check(b)
+
+
+def test_long_rows_beside_short_ones():
+    """Hundreds of rows of a prompt, whose logits are computed again, beside decodes, whose logits are kept, windowed
+    or not; two sequences of different kinds in every order."""
+    for seed, q_lens, kv_lens, more in ((29, [1, 150, 1], [3000, 150, 20], {}), (30, [150, 1], [1500, 2500], {}),
+                                        (31, [130, 1, 16], [400, 1900, 16], dict(sliding_window=200))):
+        run_and_check(Batch(np.random.default_rng(seed), q_lens, kv_lens, 16, 8, 2, 64, **more))
+
+
+def test_unaligned_scores_are_refused():
+    b = Batch(np.random.default_rng(32), [1], [20], 16, 2, 2, 64)
+    op = rpa.CacheEviction(budget=4, **b.cfg())
+    scores = torch.zeros(b.N * 2 * 16 + 1, device="cuda")[1:].view(b.N, 2, 16)
+    with pytest.raises(rpa.RpaError):
+        op.accumulate(b.queries(), b.cache(), *b.lens(), 1, scores)
+    with pytest.raises(rpa.RpaError):
+        op.compact(b.cache(), scores, *b.lens()[:2], 1)
+
+
 # ---------------------------------------------------------------- compaction
 def kept_slots(x, n, budget, protect, recent):
     """The definition: x [n] scores -> kept slots in order."""
@@ -389,6 +414,39 @@ def test_compact_on_another_stream_and_in_a_graph():
     assert torch.equal(c1, c2) and torch.equal(s1, s2) and torch.equal(lens[0], l1)
     g.replay()  # nothing is over the budget now
     assert torch.equal(c1, c2) and torch.equal(s1, s2) and op.status() == rpa.RPA_OK
+
+
+def test_compact_clusters_in_a_graph():
+    """Long sequences, whose scores several CTAs share, captured and replayed with other lengths and scores."""
+    rng = np.random.default_rng(44)
+    b = Batch(rng, [0] * 2, [20000, 17000], 64, Hq=2, Hkv=2, D=64, spare_pages=330)
+    new = b.table.copy()
+    new[:2, :157] = b.free_pages[:314].reshape(2, 157)
+    new = torch.from_numpy(new).cuda()
+    cache, lens = b.cache(), b.lens()
+    op = rpa.CacheEviction(budget=10000, protect=7, recent=130, **b.cfg())
+    sc, out = torch.rand(b.N, 2, 64, device="cuda"), torch.zeros(b.max_seqs, dtype=torch.int32, device="cuda")
+    kept = torch.zeros(b.max_seqs, 2, 10000, dtype=torch.int32, device="cuda")
+    c2, s2 = cache.clone(), sc.clone()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        op.compact(c2, s2, lens[0], lens[1], 2, new, out, kept=kept)
+    for n in ([20000, 17000], [9000, 16999]):
+        lens[0][:2] = torch.tensor(n, dtype=torch.int32)
+        sc = torch.rand(b.N, 2, 64, device="cuda")
+        s2.copy_(sc)
+        c2.copy_(cache)
+        g.replay()
+        c1, s1, k1 = cache.clone(), sc.clone(), torch.zeros_like(kept)
+        l1 = op.compact(c1, s1, lens[0], lens[1], 2, new, kept=k1)
+        assert torch.equal(c1, c2) and torch.equal(s1, s2) and torch.equal(out[:2], l1[:2]) and torch.equal(kept[:2], k1[:2])
+        x = f64(sc)
+        for s in range(2):
+            p0, a0 = b.slots(s, np.arange(n[s]))
+            for h in range(2):
+                want = kept_slots(x[p0, h, a0], n[s], 10000, 7, 130)
+                assert (kept[s, h].cpu().numpy()[:len(want)] == want).all()
+    assert op.status() == rpa.RPA_OK
 
 
 def test_compact_bad_lengths_and_pages():

@@ -123,6 +123,36 @@ def test_long_prefix_many_pieces():
     Shared(22, [(30000, one(9))], ps=64, Hq=2, Hkv=2, D=64).check()  # decode pieces of a prefix
 
 
+def test_many_sequences():
+    """More virtual sequences than the planner keeps in shared memory, and many groups."""
+    rng = np.random.default_rng(29)
+    groups = [(int(pre), [(1, int(n)) for n in rng.integers(1, 20, int(k))]) for pre, k in ((200, 900), (0, 300), (17, 400))]
+    Shared(29, groups, ps=16, Hq=4, Hkv=2, D=64, lead=2, tail=1).check()
+    groups = [(int(rng.integers(0, 300)), [(int(rng.integers(0, 3)), int(n)) for n in rng.integers(1, 40, int(k))]) for k in rng.integers(0, 6, 70)]
+    groups.append((64, one(5)))
+    Shared(30, groups, ps=16, Hq=8, Hkv=2, D=128).check()
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3"])
+def test_garbage_in_front_of_a_suffix(kv):
+    """The other sequences' copies of the keys before the prefix's end, and everything behind the keys, may hold any bits."""
+    scale = dict(k_scale=0.05, v_scale=0.07) if kv == "fp8_e4m3" else {}
+    x = Shared(31, [(100, one(5, 30, 1, 200)), (1000, [(2, 9), (40, 50)])], ps=16, Hq=8, Hkv=2, D=128, kv=kv, **scale)
+    ref = x.reference()
+    b, raw = x.b, x.cache.view(torch.uint8)
+    used = torch.zeros(b.N, 16, dtype=torch.bool)
+    for g, (pre, members) in enumerate(x.groups):
+        for s in range(x.cu_groups[g], x.cu_groups[g + 1]):
+            first = 0 if s == x.cu_groups[g] else pre
+            page, at = b.slots(s, np.arange(first, b.kv_lens_list[s]))
+            used[page, at] = True
+    raw[~used.cuda()] = 0x7F if kv == "fp8_e4m3" else 0xFF  # NaN
+    op = x.op()
+    o = op.forward(*x.args())
+    assert op.status() == rpa.RPA_OK
+    assert_close(f64(o), ref, kv, "garbage around the keys")
+
+
 def test_large_scores_meet_across_the_parts():
     """Logits of very different sizes before and behind the prefix's end: either side may hold all the weight."""
     for where in (0, 1):

@@ -303,3 +303,37 @@ def test_append_then_attend():
     p = ri.Problem(**b.cfg(), num_seqs=b.S, q=bits(q), kv_pages=bits(cache), kv_lens=b.kv_lens, page_indices=b.table, cu_q_lens=b.cu)
     ref = oracle.forward(p)
     assert (np.abs(f64(o) - ref) <= 2e-2 + 2e-2 * np.abs(ref)).all()
+
+
+def test_many_sequences():
+    """More sequences than two rounds of the lookup tell apart, some of them empty; tokens in every part of a CTA's run."""
+    rng = np.random.default_rng(19)
+    q_lens = [int(x) for x in rng.integers(0, 4, 2500)]
+    b = Batch(rng, q_lens, [n + int(x) for n, x in zip(q_lens, rng.integers(0, 9, 2500))], 4, 2, 1, 64, lead=1, tail=1)
+    rope = dict(rotary_dim=64)
+    x = inputs(b, rng)
+    cache = b.cache()
+    before = cache.clone()
+    op = rpa.RopeAppend(**b.cfg())
+    out = op.append(*x, cache, *b.lens(), b.S)
+    assert op.status() == rpa.RPA_OK
+    check(b, *x, out, before, cache, rope)
+
+
+def test_one_call_after_another():
+    """Calls that follow each other on a stream without a wait, each writing the cache that the next rotates into."""
+    rng = np.random.default_rng(20)
+    b = Batch(rng, [7, 1, 30], [7, 20, 90], 16, 8, 2, 128)
+    lens = b.lens()
+    op = rpa.RopeAppend(**b.cfg())
+    xs = [inputs(b, rng) for _ in range(8)]
+    cache = b.cache()
+    torch.cuda.synchronize()
+    outs = [op.append(*x, cache, *lens, b.S) for x in xs]
+    assert op.status() == rpa.RPA_OK
+    for x, o in zip(xs, outs):
+        again = b.cache()
+        assert torch.equal(o, op.append(*x, again, *lens, b.S))
+    last = cache.clone()
+    op.append(*xs[-1], last, *lens, b.S)
+    assert torch.equal(last, cache)
