@@ -361,7 +361,8 @@ void rpa_rope_destroy(RpaRope* h);
 /* rpa_forward for batches whose sequences share their first keys: the prefix of a group of sequences is
  * read once for all their query rows (tensor-core tiles of tokens x heads, split over the keys), the keys
  * behind it by each sequence for itself, and the two are merged.  The result is rpa_forward's, to its
- * tolerance.  RPA_KV_SPLIT, causal, without a sliding window (else RPA_ERR_UNSUPPORTED). */
+ * tolerance.  RPA_KV_SPLIT, causal, without a sliding window, pages_per_seq * page_size <= 2^30 (else
+ * RPA_ERR_UNSUPPORTED). */
 typedef struct RpaPrefix RpaPrefix;
 /* Host only; 1 <= max_groups <= max_num_seqs. */
 int rpa_prefix_validate_cfg(const RpaCfg* cfg, int64_t max_groups);
@@ -385,7 +386,7 @@ void rpa_prefix_destroy(RpaPrefix* h);
 /* Eviction by accumulated attention weight.  scores: device, float32 [total_num_pages, Hkv, page_size],
  * 16-byte aligned, beside the cache: what each cached key of each kv head has received. */
 typedef struct RpaEvictCfg {
-    RpaCfg cache;     /* RPA_KV_SPLIT */
+    RpaCfg cache;     /* RPA_KV_SPLIT, pages_per_seq * page_size <= 2^30 */
     int64_t budget;   /* keys a sequence keeps, 1 .. pages_per_seq * page_size */
     int64_t protect;  /* the first keys, never evicted */
     int64_t recent;   /* the last keys, never evicted; protect + recent <= budget */

@@ -3,7 +3,7 @@
 //
 // Two launches:
 //
-//   select   a cluster of 1 to 8 CTAs per (sequence, kv head).  The keys between the protected first and
+//   select   a cluster of 1 to 4 CTAs per (sequence, kv head).  The keys between the protected first and
 //            the recent last ones compete for the budget's other places: the k-th largest score by a radix
 //            select over the scores as ordered integers (three digits of 11, 11 and 10 bits, a histogram in
 //            shared memory each; the first digit holds the sign, the exponent and two bits of the mantissa,
@@ -15,9 +15,14 @@
 //            a few microseconds each), so a cluster is as large as leaves no SM without one.
 //   move     blocks of 64 kept rows: K and V of a head are neighbours in a slot, one copy of 2 D
 //            elements a row.  Bound by reading and writing those rows.  Onto fresh pages all blocks are
-//            independent.  Where the new pages hold other kept rows (in place), a sequence's head is
-//            done by one CTA in ascending order, a block read before it is written: kept row i sits at
-//            slot j >= i and goes to slot i, so that a block's writes never reach a later block's rows.
+//            independent.  Where the new pages hold other kept rows (in place), a head's rows move in
+//            ascending order: kept row i sits at slot j >= i and goes to slot i, so that a row may be
+//            written once all rows up to it are read, and what is read later is never written before.
+//            A cluster of up to 8 CTAs takes a head and meets between a round's reads and its writes.
+//
+// 64 sequences of up to 8 k keys cut to 2 k (8 heads, D 128, bf16; 1.09 GB): select 25 us, move 170 us,
+// 6.4 TB/s; in place 229 us in all.  Two of 100 k keys cut to 16 k (e4m3, 139 MB): 23 and 28 us; in place 84
+// us in all (16 heads, one CTA each: 240 us; each round's lookups not ahead of it: 530).
 #include <math.h>
 #include <string.h>
 
@@ -36,6 +41,7 @@ constexpr int kSelCached = 40 * 1024;  // scores a CTA keeps at most (160 KB); f
 constexpr int kMoveThreads = 256;
 constexpr int kMoveCtas = 4;  // resident an SM
 constexpr int kMoveRows = 64;
+constexpr int kMaxMoveCluster = 8;
 
 // A score as an integer of the same order; NaN lowest, -0 as +0
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -311,85 +317,148 @@ __global__ void __launch_bounds__(CLUSTER ? 1024 : 512, CLUSTER ? 1 : 3) rpa_evi
     if (CLUSTER) cluster_sync();  // no CTA leaves while another may read its counts
 }
 
-__global__ void __launch_bounds__(kMoveThreads, kMoveCtas) rpa_evict_move_kernel(const CompactParams p) {
-    __shared__ long long s_from[kMoveRows], s_to[kMoveRows];  // first 16-byte vectors of the rows; s_to -1: no move
+// Kept row i of head h: where it is and where it goes (first 16-byte vectors; to -1: it stays, or has no page), and its score's
+// new place (nullptr: none) and value
+struct Row {
+    long long from, to;
+    float* sc_to;
+    float sc;
+};
+__device__ __forceinline__ Row look_up(const CompactParams& p, int s, int h, int i, int j) {
+    Row r = {0, -1, nullptr, 0.f};
+    const int pj = p.page.div(j), pi = p.page.div(i);
+    const int pa = __ldg(p.page_indices + (size_t)s * p.P + pj), pb = __ldg(p.new_pages + (size_t)s * p.P + pi);
+    if ((unsigned)pa >= (unsigned)p.N || (unsigned)pb >= (unsigned)p.N) {
+        set_status(p.status, RPA_ERR_BAD_PAGE_INDEX);
+        return r;
+    }
+    const int at = j - pj * p.ps, bt = i - pi * p.ps;
+    r.from = (((long long)pa * p.ps + at) * p.Hkv + h) << p.vec_shift;
+    const long long to = (((long long)pb * p.ps + bt) * p.Hkv + h) << p.vec_shift;
+    if (to != r.from) {
+        r.to = to;
+        r.sc = p.scores[((size_t)pa * p.Hkv + h) * p.ps + at];
+        r.sc_to = p.scores + ((size_t)pb * p.Hkv + h) * p.ps + bt;
+    }
+    return r;
+}
+
+constexpr int kFly = 8;  // 16-byte vectors a thread has in flight
+
+// All kept rows of a head onto pages that hold other kept rows, by the C CTAs of a cluster (or one).  A round takes as many
+// neighbouring rows as their registers hold: all CTAs read theirs, meet, and write.  Where rows are is looked up a
+// round ahead, their slots two, beside the reads.
+template <bool CLUSTER>
+__device__ __forceinline__ void move_in_order(const CompactParams& p, int s, int h, int kept, int C, int rank, long long (*s_from)[kMoveThreads],
+                                              long long (*s_to)[kMoveThreads]) {
+    uint4* kv = reinterpret_cast<uint4*>(p.kv);
+    const int tid = threadIdx.x, vecs = 1 << p.vec_shift, per_cta = kFly * kMoveThreads >> p.vec_shift, step = C * per_cta;
+    const int* list = p.list + ((size_t)s * p.Hkv + h) * p.budget;
+    const int mine = rank * per_cta + tid;  // this thread's row of a round, if tid < per_cta
+    auto slot = [&](int i0) { return tid < per_cta && i0 + mine < kept ? list[i0 + mine] : -1; };
+    auto where = [&](int i0, int j) {
+        Row r = {0, -1, nullptr, 0.f};
+        if (j >= 0) r = look_up(p, s, h, i0 + mine, j);
+        return r;
+    };
+    int j = slot(0), at = 0;  // at: the round's third of the tables
+    Row row = where(0, j);
+    j = slot(step);
+    __syncthreads();  // the last head's tables
+    s_from[0][tid] = row.from;
+    s_to[0][tid] = row.to;
+    __syncthreads();
+    for (int i0 = 0; i0 < kept; i0 += step) {
+        const int next = at == 2 ? 0 : at + 1;
+        uint4 x[kFly];
+#pragma unroll
+        for (int f = 0; f < kFly; ++f) {
+            const int v = tid + f * kMoveThreads, r = v >> p.vec_shift;
+            if (s_to[at][r] >= 0) x[f] = __ldcs(kv + s_from[at][r] + (v & (vecs - 1)));
+        }
+        const Row ahead = where(i0 + step, j);
+        j = slot(i0 + 2 * step);
+        s_from[next][tid] = ahead.from;
+        s_to[next][tid] = ahead.to;
+        if (CLUSTER) cluster_sync();
+        else __syncthreads();
+#pragma unroll
+        for (int f = 0; f < kFly; ++f) {
+            const int v = tid + f * kMoveThreads, r = v >> p.vec_shift;
+            if (s_to[at][r] >= 0) __stcs(kv + s_to[at][r] + (v & (vecs - 1)), x[f]);
+        }
+        if (row.sc_to) *row.sc_to = row.sc;
+        row = ahead;
+        at = next;
+    }
+}
+
+// IN_PLACE: the new pages are the old ones, rows move in order or not at all, a cluster a head.  Else each sequence by its own rule
+template <bool IN_PLACE>
+__global__ void __launch_bounds__(kMoveThreads, IN_PLACE ? 2 : kMoveCtas) rpa_evict_move_kernel(const CompactParams p) {
+    __shared__ long long s_from[3][kMoveThreads], s_to[3][kMoveThreads];  // Row::from and to
     const int tid = threadIdx.x;
     pdl_trigger();
     pdl_wait();
+    const int units = p.S * p.Hkv, C = IN_PLACE ? p.move_cluster : 1, rank = IN_PLACE ? (int)cluster_rank() : 0;
+    for (int u = blockIdx.x / C; u < units; u += gridDim.x / C) {
+        const int s = u / p.Hkv, h = u - s * p.Hkv, kept = p.seq_n[s];
+        if (IN_PLACE && kept >= 0 && h == 0 && rank == 0 && tid == 0) p.new_kv_lens[s] = kept;
+        if (kept > 0 && p.seq_order[s] != 0) move_in_order<IN_PLACE>(p, s, h, kept, C, rank, s_from, s_to);
+    }
+    if (IN_PLACE) return;
+    // onto fresh pages: blocks of rows in any order
     const int blocks = (p.budget + kMoveRows - 1) / kMoveRows;
-    const int items = p.S * p.Hkv * blocks;
+    const int items = units * blocks;
     const int vshift = p.vec_shift, vecs = 1 << vshift;  // 16-byte vectors of a row: 8, 16, 32 or 64
-    const int slot_vecs = vecs * p.Hkv;
     uint4* kv = reinterpret_cast<uint4*>(p.kv);
-    constexpr int kFly = 8;
     const int sub = min(kMoveRows, kFly * kMoveThreads >> vshift);  // rows whose vectors the CTA's registers hold at once
     for (int it = blockIdx.x; it < items; it += gridDim.x) {
         const int h = it % p.Hkv, b = it / p.Hkv % blocks, s = it / p.Hkv / blocks;
-        const int kept = p.seq_n[s];
+        const int kept = p.seq_n[s], i0 = b * kMoveRows;
         if (kept < 0) continue;
         if (b == 0 && h == 0 && tid == 0) p.new_kv_lens[s] = kept;
-        const bool order = p.seq_order[s] != 0;
-        if (order && b > 0) continue;
-        const int* list = p.list + ((size_t)s * p.Hkv + h) * p.budget;
-        const int end = order ? kept : min(kept, (b + 1) * kMoveRows);
-        for (int i0 = b * kMoveRows; i0 < end; i0 += kMoveRows) {
-            const int rows = min(kMoveRows, end - i0);
-            float sc = 0.f;
-            float* sc_to = nullptr;
-            __syncthreads();
-            if (tid < kMoveRows) {
-                long long from = 0, to = -1;
-                if (tid < rows) {
-                    const int i = i0 + tid, j = list[i], pj = p.page.div(j), pi = p.page.div(i);
-                    const int pa = __ldg(p.page_indices + (size_t)s * p.P + pj), pb = __ldg(p.new_pages + (size_t)s * p.P + pi);
-                    if ((unsigned)pa >= (unsigned)p.N || (unsigned)pb >= (unsigned)p.N) {
-                        set_status(p.status, RPA_ERR_BAD_PAGE_INDEX);
-                    } else {
-                        const int at = j - pj * p.ps, bt = i - pi * p.ps;
-                        from = ((long long)pa * p.ps + at) * slot_vecs + h * vecs;
-                        to = ((long long)pb * p.ps + bt) * slot_vecs + h * vecs;
-                        if (from == to) {
-                            to = -1;
-                        } else {
-                            sc = p.scores[((size_t)pa * p.Hkv + h) * p.ps + at];
-                            sc_to = p.scores + ((size_t)pb * p.Hkv + h) * p.ps + bt;
-                        }
-                    }
-                }
-                s_from[tid] = from;
-                s_to[tid] = to;
-            }
-            __syncthreads();
-            // `sub` rows at a time, eight vectors a thread in flight; in order, all are read before any is written
-            for (int r0 = 0; r0 < rows; r0 += sub) {
-                const int first = r0 << vshift, total = min(rows, r0 + sub) << vshift;
-                uint4 x[kFly];
-#pragma unroll
-                for (int f = 0; f < kFly; ++f) {
-                    const int v = first + tid + f * kMoveThreads, r = v >> vshift;
-                    if (v < total && s_to[r] >= 0) x[f] = __ldcs(kv + s_from[r] + (v & (vecs - 1)));
-                }
-                if (order) __syncthreads();
-#pragma unroll
-                for (int f = 0; f < kFly; ++f) {
-                    const int v = first + tid + f * kMoveThreads, r = v >> vshift;
-                    if (v < total && s_to[r] >= 0) __stcs(kv + s_to[r] + (v & (vecs - 1)), x[f]);
-                }
-                if (order) __syncthreads();
-            }
-            if (sc_to) *sc_to = sc;
+        if (p.seq_order[s] != 0 || i0 >= kept) continue;
+        const int rows = min(kMoveRows, kept - i0);
+        Row row = {0, -1, nullptr, 0.f};
+        __syncthreads();
+        if (tid < kMoveRows) {
+            if (tid < rows) row = look_up(p, s, h, i0 + tid, p.list[((size_t)s * p.Hkv + h) * p.budget + i0 + tid]);
+            s_from[0][tid] = row.from;
+            s_to[0][tid] = row.to;
         }
+        __syncthreads();
+        // `sub` rows at a time, eight vectors a thread in flight
+        for (int r0 = 0; r0 < rows; r0 += sub) {
+            const int first = r0 << vshift, total = min(rows, r0 + sub) << vshift;
+            uint4 x[kFly];
+#pragma unroll
+            for (int f = 0; f < kFly; ++f) {
+                const int v = first + tid + f * kMoveThreads, r = v >> vshift;
+                if (v < total && s_to[0][r] >= 0) x[f] = __ldcs(kv + s_from[0][r] + (v & (vecs - 1)));
+            }
+#pragma unroll
+            for (int f = 0; f < kFly; ++f) {
+                const int v = first + tid + f * kMoveThreads, r = v >> vshift;
+                if (v < total && s_to[0][r] >= 0) __stcs(kv + s_to[0][r] + (v & (vecs - 1)), x[f]);
+            }
+        }
+        if (row.sc_to) *row.sc_to = row.sc;
     }
 }
 
 }  // namespace
 
 // Clusters and shared memory of select for `units` (sequence, kv head) pairs of up to max_keys competing keys
-cudaError_t compact_prepare(int64_t units, int max_keys, int sms, int* cluster, int* cached) {
+cudaError_t compact_prepare(int64_t units, int max_keys, int sms, int* cluster, int* move_cluster, int* cached) {
     // as many CTAs a unit as two an SM allow, of 2 k keys at least
     int c = 1;
     while (c < kMaxCluster && 3 * units * (2 * c) <= 2 * sms && max_keys / (2 * c) >= 2048) c *= 2;
     *cluster = c;
+    // rows that move in order: as many CTAs a unit as there are
+    int m = 1;
+    while (m < kMaxMoveCluster && units * (2 * m) <= sms * kMoveCtas) m *= 2;
+    *move_cluster = m;
     const int share = ((max_keys + 3) / 4 + 1 + c - 1) / c * 4;  // (one quad more where neither end is a quad's)
     *cached = share < kSelCached ? share : kSelCached;
     return cudaFuncSetAttribute(c > 1 ? rpa_evict_select_kernel<true> : rpa_evict_select_kernel<false>,
@@ -412,8 +481,15 @@ cudaError_t launch_compact(const CompactParams& p, int sms, cudaStream_t st) {
     cfg.attrs = attr;
     cfg.numAttrs = p.cluster > 1 ? 2 : 1;
     cudaError_t e = cudaLaunchKernelEx(&cfg, p.cluster > 1 ? rpa_evict_select_kernel<true> : rpa_evict_select_kernel<false>, p);
-    if (e == cudaSuccess) e = launch_pdl(rpa_evict_move_kernel, sms * kMoveCtas, kMoveThreads, 0, st, p);
-    return e;
+    if (e != cudaSuccess) return e;
+    if (p.new_pages != p.page_indices) return launch_pdl(rpa_evict_move_kernel<false>, sms * kMoveCtas, kMoveThreads, 0, st, p);
+    const int m = p.move_cluster, units = p.S * p.Hkv, most = sms * kMoveCtas / m;
+    cfg.gridDim = dim3((units < most ? units : most) * m);
+    cfg.blockDim = dim3(kMoveThreads);
+    cfg.dynamicSmemBytes = 0;
+    attr[1].val.clusterDim.x = m;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, rpa_evict_move_kernel<true>, p);
 }
 
 }  // namespace rpa
@@ -425,9 +501,8 @@ struct RpaEvict {
     int device, sms;
     KernelSet ks;      // element types and scales of the attention of `cfg.cache`
     int stats_bps, weigh_bps;  // resident CTAs an SM of the two weight kernels
-    CUtensorMap kmap;  // K rows of the cache of the last call
-    const void* kmap_ptr;
     int cluster, cached;  // of select
+    int move_cluster;
     void* ws;
     int* status;
     WeighParams w;     // workspace pointers and constants
@@ -454,7 +529,8 @@ int rpa_evict_validate_cfg(const RpaEvictCfg* c) {
     if (c->protect < 0 || c->recent < 0 || c->protect > c->budget || c->recent > c->budget - c->protect)
         return RPA_ERR_INVALID_ARG;
     if (c->cache.kv_layout != RPA_KV_SPLIT) return RPA_ERR_UNSUPPORTED;
-    // 32-bit numbers of rows, slots, grids' CTAs and blocks of kept keys
+    // 32-bit numbers of keys (with room for sums of two), rows, slots, grids' CTAs and blocks of kept keys
+    if (c->cache.pages_per_seq * c->cache.page_size > (int64_t)1 << 30) return RPA_ERR_UNSUPPORTED;
     const int64_t lim = (int64_t)1 << 31, units = c->cache.max_num_seqs * c->cache.num_kv_heads;
     if (c->cache.num_q_tokens * (c->cache.num_q_heads / c->cache.num_kv_heads) >= lim ||
         c->cache.total_num_pages >= lim / c->cache.page_size || units >= lim / 8 ||
@@ -482,7 +558,7 @@ int rpa_evict_create(const RpaEvictCfg* cfg, RpaEvict** out) {
     kernels_choose(c, h->sms, &h->ks);
     const int64_t max_keys = c.pages_per_seq * c.page_size;
     if (weigh_prepare(h->ks.D, h->ks.kt, &h->stats_bps, &h->weigh_bps) != cudaSuccess || h->stats_bps < 1 || h->weigh_bps < 1 ||
-        compact_prepare(c.max_num_seqs * c.num_kv_heads, (int)max_keys, h->sms, &h->cluster, &h->cached) != cudaSuccess) {
+        compact_prepare(c.max_num_seqs * c.num_kv_heads, (int)max_keys, h->sms, &h->cluster, &h->move_cluster, &h->cached) != cudaSuccess) {
         cudaGetLastError();
         delete h;
         return RPA_ERR_CUDA;
@@ -594,13 +670,10 @@ int rpa_evict_accumulate(RpaEvict* h, const void* q, const void* kv_pages, const
         }
         p.q = h->qbuf;
     }
-    if (h->kmap_ptr != kv_pages) {
-        h->kmap_ptr = nullptr;
-        if (encode_k_map(&h->kmap, kv_pages, p.D * (kt_8bit(h->ks.kt) ? 1 : 2), c.total_num_pages, p.ps, p.Hkv, p.BR) != 0)
-            return RPA_ERR_INVALID_ARG;
-        h->kmap_ptr = kv_pages;
-    }
-    if (launch_weigh(h->kmap, p, h->ks.kt, h->sms * h->weigh_bps, st) != cudaSuccess) {
+    CUtensorMap kmap;
+    if (encode_k_map(&kmap, kv_pages, p.D * (kt_8bit(h->ks.kt) ? 1 : 2), c.total_num_pages, p.ps, p.Hkv, p.BR) != 0)
+        return RPA_ERR_INVALID_ARG;
+    if (launch_weigh(kmap, p, h->ks.kt, h->sms * h->weigh_bps, st) != cudaSuccess) {
         cudaGetLastError();
         return RPA_ERR_CUDA;
     }
@@ -643,6 +716,7 @@ int rpa_evict_compact(RpaEvict* h, void* kv_pages, float* scores, const int32_t*
     p.protect = (int)h->cfg.protect;
     p.recent = (int)h->cfg.recent;
     p.cluster = h->cluster;
+    p.move_cluster = h->move_cluster;
     p.cached = h->cached;
     p.page.set((uint32_t)p.ps);
     if (launch_compact(p, h->sms, static_cast<cudaStream_t>(stream)) != cudaSuccess) {

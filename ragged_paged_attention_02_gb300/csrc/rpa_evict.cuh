@@ -73,6 +73,7 @@ struct CompactParams {
     int vec_shift;           // log2 of the 16-byte vectors of a row: K and V of one head in a slot
     int budget, protect, recent;
     int cluster;             // CTAs of a select cluster
+    int move_cluster;        // CTAs of a move cluster
     int cached;              // scores a CTA of it keeps in shared memory
     FastDiv page;
 };
@@ -81,7 +82,7 @@ struct CompactParams {
 // resident CTAs an SM of the stats kernel and the weigh kernel
 cudaError_t weigh_prepare(int D, int kt, int* stats, int* weigh);
 cudaError_t launch_weigh(const CUtensorMap& kmap, const WeighParams& p, int kt, int grid_weigh, cudaStream_t st);
-cudaError_t compact_prepare(int64_t units, int max_keys, int sms, int* cluster, int* cached);
+cudaError_t compact_prepare(int64_t units, int max_keys, int sms, int* cluster, int* move_cluster, int* cached);
 cudaError_t launch_compact(const CompactParams& p, int sms, cudaStream_t st);
 
 }  // namespace rpa

@@ -439,7 +439,6 @@ struct RpaPrefix {
     int64_t max_groups;
     int device;
     KernelSet ks;
-    MapCache maps;
     void* ws;
     Workspace w;
     int pf_slots, item_room, max_dec_units, max_pf_units, max_part;
@@ -526,8 +525,8 @@ int rpa_prefix_validate_cfg(const RpaCfg* cfg, int64_t max_groups) {
     if (v != RPA_OK) return v;
     if (max_groups < 1 || max_groups > cfg->max_num_seqs) return RPA_ERR_INVALID_ARG;
     if (cfg->kv_layout != RPA_KV_SPLIT || !cfg->is_causal || cfg->has_sliding_window) return RPA_ERR_UNSUPPORTED;
-    // positions of a group's tokens behind its prefix, and rows of the virtual batch, in 32 bits
-    if (cfg->pages_per_seq * cfg->page_size + cfg->num_q_tokens >= (int64_t)1 << 31 ||
+    // keys and a piece's, positions of a group's tokens behind its prefix, and rows of the virtual batch, in 32 bits
+    if (cfg->pages_per_seq * cfg->page_size > (int64_t)1 << 30 || cfg->num_q_tokens >= (int64_t)1 << 30 ||
         cfg->num_q_tokens * cfg->num_q_heads >= (int64_t)1 << 31)
         return RPA_ERR_UNSUPPORTED;
     return RPA_OK;
@@ -630,7 +629,8 @@ int rpa_prefix_forward(RpaPrefix* h, const void* q, const void* kv_pages, const 
     }
     AttnParams ap = attn_params(c, ks, h->w, qk, kv_pages, h->vkv, page_indices, h->vcu, o);
     ap.page_rows = h->vrow;
-    const int r = enqueue_attention(c, ks, h->w, &h->maps, ap, eo);
+    MapCache maps = {};
+    const int r = enqueue_attention(c, ks, h->w, &maps, ap, eo);
     if (r != RPA_OK) {
         cudaGetLastError();
         return r;

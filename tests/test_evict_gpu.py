@@ -384,6 +384,14 @@ def test_compact(seed, shape, ps, kv_lens, budget, protect, recent, mode, kv):
     check_compact(b, budget, protect, recent, mode=mode)
 
 
+@pytest.mark.parametrize("mode", ["place", "equal"])
+def test_more_heads_than_ctas(mode):
+    """Every (sequence, kv head) of a large batch moves in order."""
+    rng = np.random.default_rng(46)
+    b = Batch(rng, [0] * 90, [int(n) for n in rng.integers(20, 400, 90)], 16, Hq=8, Hkv=8, D=64)
+    check_compact(b, 100, 5, 9, mode=mode)
+
+
 @pytest.mark.parametrize("kind", ["equal", "few", "special", "negative", "tiny"])
 def test_ties_and_special_scores(kind):
     rng = np.random.default_rng(40)

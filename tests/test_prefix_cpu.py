@@ -30,6 +30,8 @@ def _built():
     (dict(head_dim=576, v_head_dim=512, kv_layout="latent", num_q_heads=16, num_kv_heads=1), rpa.RPA_ERR_UNSUPPORTED),
     (dict(num_q_tokens=(1 << 31) - 60), rpa.RPA_ERR_UNSUPPORTED),
     (dict(head_dim=80), rpa.RPA_ERR_UNSUPPORTED),
+    (dict(page_size=1 << 20, pages_per_seq=1 << 10), rpa.RPA_OK),
+    (dict(page_size=1 << 20, pages_per_seq=(1 << 10) + 1), rpa.RPA_ERR_UNSUPPORTED),  # keys of a piece behind 2^30 others
 ])
 def test_validate(change, code):
     assert rpa.validate_prefix_cfg(**dict(CFG, **change)) == code
