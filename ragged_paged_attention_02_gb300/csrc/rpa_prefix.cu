@@ -31,6 +31,7 @@ namespace {
 constexpr int kPrefixSmGflops = 8700;
 constexpr int kPieceAlign = 128;   // keys: the prefill kernels' tiles
 constexpr int kPieceCost = 512;    // what a piece costs beside its keys, in keys (256: 167 us, 512 and 1024: 163, for 256 x 16 k)
+constexpr int kUnitCost = 200;     // the same of a decode piece on the prefill kernel (3.8 us, where 64 keys take 1.2)
 static_assert(kPlanThreads >= 160, "a candidate a thread");
 constexpr int kMaxPieces = 160;    // most pieces of a prefix: one an SM where a single head and tile have all of them
 
@@ -205,7 +206,12 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_prefix_plan_kernel(const 
                 fewest += tiles;
             }
             // (whole waves of whole keys: exact in a float up to 2^24, and far from it where a choice is close)
-            if (tid == 0 || items <= fewest + p.item_room) cost = ceilf((float)items / (float)pf_ctas) * (float)(c + kPieceCost);
+            if (tid == 0 || items <= fewest + p.item_room) {
+                // the decode pieces' keys fill the CTAs that have no prefix tile, where they are items of the same kernel
+                const float others = (float)(pf_keys + dec_keys) + (float)S * (float)(p.Hkv * kUnitCost);
+                cost = p.dec_on_pf ? fmaxf((float)(c + kPieceCost), ((float)items * kPieceCost + others) / (float)pf_ctas)
+                                   : ceilf((float)items / (float)pf_ctas) * (float)(c + kPieceCost);
+            }
         }
         float* costs = reinterpret_cast<float*>(s_red);
         int* who = reinterpret_cast<int*>(s_red + 32);
