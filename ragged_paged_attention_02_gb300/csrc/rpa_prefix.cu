@@ -15,7 +15,15 @@
 //
 // How many pieces a prefix is cut into: tiles x kv heads are few (a batch of 64 and 8 heads has 8), so
 // pieces fill the SMs; but each costs a pipeline ramp and 256 partial rows of D floats, written and read
-// back.  The planner takes the number of pieces that makes  waves x (keys of a piece + kPieceCost)  least.
+// back.  The planner takes the number of pieces that makes  waves x (keys of a piece + kPieceCost)  least; where
+// the sequences' pieces are items of the same kernel (8-bit pages), the larger of the longest item and the list's
+// work a CTA: there fewer pieces, whose CTAs' gaps the others fill, take 65 us where a whole wave takes 69 (fp8).
+//
+// 61 sequences of 32 heads behind 8 k shared keys (bf16, D 128, 8 kv heads; 121 MB, 8.3 GFLOP): 49 us, of which plan
+// 7, attention 34 and merge 7, 2.5 TB/s; 256 behind 16 k (593 MB, 71 GFLOP): 151 us, 3.9 TB/s and 470 TFLOP/s; 48 of
+// three groups over fp8 pages (D 256; 99 MB): 65 us.  A sequence at a time the prefixes would be 2.0, 17 and
+// 0.7 GB.  Bound by latencies: four dependent kernels, and in the attention kernels a few items an SM, each with its
+// ramp (3.8 us a decode piece of 8-bit pages, where a tile of 64 keys takes 1.2).
 #include <string.h>
 
 #include <new>
@@ -51,13 +59,13 @@ struct PrefixPlan {
     Unit *dec_units, *pf_units;
 };
 
-constexpr int kArrays = 6;
-constexpr int kVirtualSmem = 1536;  // virtual sequences whose records fit in shared memory (36 KB)
+constexpr int kArrays = 7;
+constexpr int kVirtualSmem = 1536;  // virtual sequences whose records fit in shared memory (42 KB)
 
 // The records of the virtual sequences: keys [begin, end) for ql tokens; class 0 no work, 1 decode pieces, 2 prefill
-// tiles; units of each kind up to and with this one
+// tiles; units of each kind (decode pieces: of sequences of more than half a piece, then of the others) up to and with this one
 struct Records {
-    int *q0, *ql, *begin, *end, *dec_end, *pf_end;
+    int *q0, *ql, *begin, *end, *long_end, *short_end, *pf_end;
     __device__ __forceinline__ int cls(const PrefixPlan& p, int v) const {
         return ql[v] == 0 || end[v] <= begin[v] ? 0 : (long long)ql[v] * p.G <= p.dec_rows ? 1 : 2;
     }
@@ -104,7 +112,7 @@ __device__ __forceinline__ void warp_least(float& cost, int& candidate) {
 
 __global__ void __launch_bounds__(kPlanThreads, 1) rpa_prefix_plan_kernel(const PrefixPlan p) {
     __shared__ int s_rec[kArrays * kVirtualSmem];
-    __shared__ int s_scan[33 * 3];
+    __shared__ int s_scan[33 * 4];
     __shared__ unsigned long long s_red[96];
     const int tid = threadIdx.x, lane = tid & 31, S = p.S, NG = p.NG, V = S > 0 ? NG + 1 + S : 0;
     int* ctrl = p.ctrl;
@@ -113,7 +121,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_prefix_plan_kernel(const 
     {
         int* base = V <= kVirtualSmem ? s_rec : p.scratch;
         const int n = V <= kVirtualSmem ? kVirtualSmem : V;
-        int** to[kArrays] = {&R.q0, &R.ql, &R.begin, &R.end, &R.dec_end, &R.pf_end};
+        int** to[kArrays] = {&R.q0, &R.ql, &R.begin, &R.end, &R.long_end, &R.short_end, &R.pf_end};
 #pragma unroll
         for (int i = 0; i < kArrays; ++i) *to[i] = base + (size_t)i * n;
     }
@@ -229,15 +237,15 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_prefix_plan_kernel(const 
         pf_chunk = ((longest + best) / (best + 1) + kPieceAlign - 1) / kPieceAlign * kPieceAlign;
     }
     // ---- 4. units and partial slots of each virtual sequence
-    int n_dec = 0, n_pf = 0, n_part = 0;
+    int n_long = 0, n_short = 0, n_pf = 0, n_part = 0;
     for (int base = 0; base < V; base += kPlanThreads) {
         const int v = base + tid;
-        int add[3] = {0, 0, 0}, off[3], tot[3], cls = 0, pieces = 0;
+        int add[4] = {0, 0, 0, 0}, off[4], tot[4], cls = 0, pieces = 0;
         if (v < V) {
             cls = R.cls(p, v);
             if (cls == 1) {
                 pieces = (R.end[v] - R.begin[v] + chunk - 1) / chunk;
-                add[0] = pieces;
+                add[R.end[v] - R.begin[v] > chunk / 2 ? 0 : 3] = pieces;
                 add[2] = pieces * p.Hkv;
             } else if (cls == 2) {
                 pieces = v < NG ? (R.end[v] + pf_chunk - 1) / pf_chunk : 1;
@@ -245,33 +253,36 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_prefix_plan_kernel(const 
                 add[2] = add[1] * p.Hkv * p.pf_slots;
             }
         }
-        block_scan<3>(add, off, tot, s_scan);
+        block_scan<4>(add, off, tot, s_scan);
         if (v < V) {
             p.vcu[v] = R.q0[v];
             // positions behind the prefix: a group's keys are visible to all of its tokens
             p.vkv[v] = v < NG ? R.end[v] + R.ql[v] : R.end[v];
             p.vrec[v] = make_int4(R.q0[v], n_part + off[2], cls == 2 ? -pieces : pieces, 0);
-            R.dec_end[v] = n_dec + off[0] + add[0];
+            R.long_end[v] = n_long + off[0] + add[0];
+            R.short_end[v] = n_short + off[3] + add[3];
             R.pf_end[v] = n_pf + off[1] + add[1];
         }
-        n_dec += tot[0];
+        n_long += tot[0];
+        n_short += tot[3];
         n_pf += tot[1];
         n_part += tot[2];
     }
-    const int n_list = p.dec_on_pf ? n_pf + n_dec : n_pf;
+    const int n_dec = n_long + n_short, n_list = p.dec_on_pf ? n_pf + n_dec : n_pf;
     if (n_dec > p.max_dec_units || n_list > p.max_pf_units || n_part > p.max_part) {
         give_up(RPA_ERR_INVALID_ARG);  // cannot happen with the create-time sizing; refuse rather than overflow
         return;
     }
     __syncthreads();
-    // ---- 5. the unit lists: prefix tiles first, a piece's tiles together (they share its keys)
+    // ---- 5. the unit lists: prefix tiles first, a piece's tiles together (they share its keys); then the decode pieces,
+    // the longer ones first, so that short ones even out the end (61 x 8 k: 49.8 -> 48.9 us; the others as before)
     for (int u = tid; u < n_dec + n_pf; u += kPlanThreads) {
         const bool dec = u >= n_pf;
-        const int* ends = dec ? R.dec_end : R.pf_end;
-        const int x = dec ? u - n_pf : u;
-        const int v = upper_seq(ends, V, x);
+        const int x = dec ? u - n_pf : u, of = dec && x >= n_long ? x - n_long : x;  // of: its number in its list
+        const int* ends = !dec ? R.pf_end : x < n_long ? R.long_end : R.short_end;
+        const int v = upper_seq(ends, V, of);
         const int4 rec = p.vrec[v];
-        const int first = v > 0 ? ends[v - 1] : 0, k = x - first;
+        const int first = v > 0 ? ends[v - 1] : 0, k = of - first;
         int4 a, b;
         if (dec) {
             const int kb = R.begin[v] + k * chunk;

@@ -26,6 +26,12 @@
 // neighbouring bytes.  (Warps that loaded their own keys were bound by their own instructions and waits:
 // 16-byte loads into registers read 4.4 TB/s, 16-byte asynchronous copies 4.8, row copies by each lane 3.9.)
 //
+// 64 decodes over 612 MB of K (32 heads, 8 kv heads, D 128, bf16): 131 us, of which plan 3.5, stats 109 (5.5 TB/s; its
+// copies alone, computing nothing, take 100: K rows are every other 256 bytes) and weigh 19.  The last 202 tokens of six
+// prompts of 1 to 6 k keys (16 heads, 8 kv heads, D 64, f16; 1.1 GFLOP): 48 us, 3.5 / 26 / 18: bound by
+// instructions, some 300 a warp for a tile of 16 keys x 16 rows, and by a row block's end (1.8 us: reductions, the counter,
+// the next item).  Measured there: two or four row blocks a warp over the same keys 50 and 52 us; four CTAs an SM 49.5.
+//
 // Maxima, sums and weights are 32-bit; the products are exact (16-bit operands, 32-bit accumulator)
 // where q has the operands' type; q of another type is rounded to it as rpa_forward does.
 #include <type_traits>
