@@ -2,7 +2,8 @@
 
 The computation lives in ``librpa.so`` (CUDA kernels behind the C ABI of
 ``include/rpa.h``); this package is the Python binding used by the tests and
-the benchmark.  Build the library with ``__graft_entry__.build()`` or
+the benchmark: ``RaggedPagedAttention``, and around its paged cache
+``RopeAppend``, ``SharedPrefixAttention`` and ``CacheEviction``.  Build the library with ``__graft_entry__.build()`` or
 ``python -m ragged_paged_attention_02_gb300._build``.
 """
 
