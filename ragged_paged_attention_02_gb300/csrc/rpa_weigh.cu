@@ -639,6 +639,19 @@ __device__ __forceinline__ void add_score(float* dst, bool fresh, float w) {
     if (fresh) *dst = w;
     else atomicAdd(dst, w);
 }
+// the same of four keys from k0 on, those of negative weight left out, in one operation of 16 bytes where it can be
+__device__ __forceinline__ void add_scores4(float* dst, int k0, int pos0, const float (&w)[4]) {
+    const bool all = w[0] >= 0.f && w[1] >= 0.f && w[2] >= 0.f && w[3] >= 0.f;
+    if (all && k0 + 4 <= pos0) {
+        asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};\n" ::"l"(dst), "f"(w[0]), "f"(w[1]), "f"(w[2]), "f"(w[3]) : "memory");
+    } else if (all && k0 >= pos0) {
+        *reinterpret_cast<float4*>(dst) = make_float4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (!(w[k] < 0.f)) add_score(dst + k, k0 + k >= pos0, w[k]);
+    }
+}
 
 // Key tiles of 16 a warp holds while it goes through the rows: 32 registers of K (64 at D 256)
 __host__ __device__ constexpr int weigh_tiles(int loads) { return loads >= 4 ? 1 : 4 / loads; }
@@ -661,20 +674,18 @@ __global__ void __launch_bounds__(kWeighThreads, D == 256 ? 2 : 4) rpa_weigh_ker
         const int* table = p.page_indices + (size_t)s * p.P;
         const float* stat = p.stat + (size_t)(p.block0[s] + h * nb) * kWeighRows;
         if (lo0 >= 0) {
-            // four keys a lane; lane r holds row r's statistic
+            // four neighbouring keys a lane (of one page: page sizes are multiples of 4); lane r holds row r's statistic
             constexpr int KL = kWeighKeys / 32;
-            const int rs = (rows + 1) & ~1;
+            static_assert(KL == 4, "add_scores4");
+            const int rs = (rows + 1) & ~1, k0 = j0 + KL * lane;
             const float st = lane < rows ? stat[lane] : 0.f;
             const float* x = p.logits + lo0 + (size_t)h * (kl - base) * rs;
+            float* dst = k0 < j1 && k0 + KL > lo ? score_at(p, table, h, k0) : nullptr;
             float w[KL];
             const float* xk[KL];
-            float* dst[KL];
 #pragma unroll
             for (int k = 0; k < KL; ++k) {
-                const int j = j0 + lane + 32 * k;
-                const bool in = j >= lo && j < j1;
-                xk[k] = x + (size_t)((in ? j : j1 - 1) - base) * rs;
-                dst[k] = in ? score_at(p, table, h, j) : nullptr;
+                xk[k] = x + (size_t)(min(k0 + k, j1 - 1) - base) * rs;
                 w[k] = 0.f;
             }
             int r = 0;
@@ -709,7 +720,9 @@ __global__ void __launch_bounds__(kWeighThreads, D == 256 ? 2 : 4) rpa_weigh_ker
                 }
             }
 #pragma unroll
-            for (int k = 0; k < KL; ++k) add_score(dst[k], j0 + lane + 32 * k >= pos0, w[k]);
+            for (int k = 0; k < KL; ++k)
+                if (k0 + k < lo || k0 + k >= j1) w[k] = -1.f;
+            if (dst) add_scores4(dst, k0, pos0, w);
         } else {
             KeyTile<D, KT> t[kTiles];
             float w[kTiles][2];
