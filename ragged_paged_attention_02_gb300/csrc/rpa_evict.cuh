@@ -42,12 +42,13 @@ struct WeighParams {
     int max_pieces;          // most pieces of a sequence
     int item_keys;           // keys of a weigh item that computes them again
     int ctas;                // of the stats kernel (all resident)
+    int weigh_warps;         // of the weigh kernel
     int BR, br_shift;        // keys of a copied page run: gcd(page_size, 64), and its log2
     uint32_t all_runs;       // a bit for each run of 64 keys
     long long max_logits;    // floats the logit buffer holds
     // workspace
     int* status;             // sticky
-    int* ctrl;               // [0] stat items, [1] weigh items, [2] stat items taken
+    int* ctrl;               // [0] stat items, [1] weigh items, [2] stat items taken, [3] kv heads of a weigh item
     int* stat0;              // [S + 1] first stat item of a sequence
     int* item0;              // [S + 1] first weigh item
     int* block0;             // [S + 1] first row block (counting kv heads)

@@ -9,7 +9,7 @@
 //   stats    item = (sequence, kv head, block of 16 rows, piece): x = q K^T on warp MMAs, maxima and
 //            sums; a block's last warp to finish merges all of them, in order.  Where a sequence has
 //            one block of rows (decode), x itself goes to the workspace.
-//   weigh    a warp takes (sequence, kv head, 128 keys) and reads x back, or with more blocks takes 16 to
+//   weigh    a warp takes (sequence, 1 to 8 kv heads, 128 keys) and reads x back, or with more blocks takes 16 to
 //            64 keys and computes it again (K from L2, all row blocks past the keys in its registers),
 //            and adds the weights' sum to the scores
 //
@@ -26,9 +26,9 @@
 // neighbouring bytes.  (Warps that loaded their own keys were bound by their own instructions and waits:
 // 16-byte loads into registers read 4.4 TB/s, 16-byte asynchronous copies 4.8, row copies by each lane 3.9.)
 //
-// 64 decodes over 612 MB of K (32 heads, 8 kv heads, D 128, bf16): 131 us, of which plan 3.5, stats 109 (5.5 TB/s; its
-// copies alone, computing nothing, take 100: K rows are every other 256 bytes) and weigh 19.  The last 202 tokens of six
-// prompts of 1 to 6 k keys (16 heads, 8 kv heads, D 64, f16; 1.1 GFLOP): 48 us, 3.5 / 26 / 18: bound by
+// 64 decodes over 612 MB of K (32 heads, 8 kv heads, D 128, bf16): 124 us, of which plan 4, stats 109 (5.5 TB/s; its
+// copies alone, computing nothing, take 100: K rows are every other 256 bytes) and weigh 11.  The last 202 tokens of six
+// prompts of 1 to 6 k keys (16 heads, 8 kv heads, D 64, f16; 1.1 GFLOP): 48.5 us, 4 / 26 / 18: bound by
 // instructions, some 300 a warp for a tile of 16 keys x 16 rows, and by a row block's end (1.8 us: reductions, the counter,
 // the next item).  Measured there: two or four row blocks a warp over the same keys 50 and 52 us; four CTAs an SM 49.5.
 //
@@ -84,6 +84,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_weigh_plan_kernel(const W
     const unsigned long long slots = (unsigned long long)p.ctas;
     const unsigned long long want = max(keys / (4 * slots), min(512ull, keys / slots));
     const int chunk = (int)min((want / kWeighAlign + (want % kWeighAlign ? 1 : 0)) * kWeighAlign + (want ? 0 : kWeighAlign), 1ull << 30);
+    // kv heads of a weigh item that reads logits back: more where every warp has several items all the same, for what an
+    // item looks up takes longer than a head's sums (64 decodes, 7 items a warp: 20, 14.6, 11.8 and 10.7 us with 1, 2, 4, 8)
+    const unsigned long long share = keys / kWeighKeys / (unsigned long long)p.weigh_warps;
+    const int heads = share >= 4 ? 8 : share >= 2 ? 4 : share >= 1 ? 2 : 1;
     // per sequence: stat items, weigh items, row blocks; and logits
     int n[3] = {0, 0, 0};
     long long n_logits = 0;
@@ -119,7 +123,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_weigh_plan_kernel(const W
             const int pieces = min((n_keys + chunk - 1) / chunk, p.max_pieces), item = keep ? kWeighKeys : p.item_keys;
             add[2] = (int)((rows + kWeighRows - 1) / kWeighRows) * p.Hkv;
             add[0] = add[2] * pieces;
-            add[1] = (n_keys + item - 1) / item * p.Hkv;
+            add[1] = (n_keys + item - 1) / item * (keep ? (p.Hkv + heads - 1) / heads : p.Hkv);
         }
         block_scan<3>(add, off, tot, s_scan);
         if (s < p.S) {
@@ -135,6 +139,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_weigh_plan_kernel(const W
     for (int i = tid; i < n[2]; i += kPlanThreads) p.done[i] = 0;
     if (tid == 0) {
         p.ctrl[2] = 0;
+        p.ctrl[3] = heads;
         p.stat0[p.S] = p.ctrl[0] = n[0];
         p.item0[p.S] = p.ctrl[1] = n[1];
         p.block0[p.S] = n[2];
@@ -661,14 +666,15 @@ __global__ void __launch_bounds__(kWeighThreads, D == 256 ? 2 : 4) rpa_weigh_ker
     constexpr int kTiles = weigh_tiles(Deal<D, KT>::LOADS);
     pdl_trigger();
     pdl_wait();
-    const int items = p.ctrl[1], lane = threadIdx.x & 31, quad = lane % 4;
+    const int items = p.ctrl[1], heads = p.ctrl[3], lane = threadIdx.x & 31, quad = lane % 4;
     for (int it = blockIdx.x * kWarps + (threadIdx.x >> 5); it < items; it += gridDim.x * kWarps) {
         const int s = find_seq(p.item0, p.S, it, lane);
         const int q0 = p.cu[s], ql = p.cu[s + 1] - q0, kl = p.kv_lens[s], pos0 = kl - ql;
-        const int base = first_key(p, kl, ql), at = it - p.item0[s], h = at % p.Hkv;
         const long long lo0 = p.logit0[s];
+        const int hp = lo0 >= 0 ? heads : 1, groups = (p.Hkv + hp - 1) / hp;  // kv heads of an item
+        const int base = first_key(p, kl, ql), at = it - p.item0[s], h = at % groups * hp;
         const int n_keys = lo0 >= 0 ? kWeighKeys : 16 * kTiles;
-        const int j0 = base + at / p.Hkv * n_keys, j1 = min(kl, j0 + n_keys);
+        const int j0 = base + at / groups * n_keys, j1 = min(kl, j0 + n_keys);
         const int lo = p.has_window ? max(0, pos0 - p.window + 1) : 0;  // keys below are seen by no row
         const int rows = ql * p.G, nb = (rows + kWeighRows - 1) / kWeighRows;
         const int* table = p.page_indices + (size_t)s * p.P;
@@ -678,51 +684,55 @@ __global__ void __launch_bounds__(kWeighThreads, D == 256 ? 2 : 4) rpa_weigh_ker
             constexpr int KL = kWeighKeys / 32;
             static_assert(KL == 4, "add_scores4");
             const int rs = (rows + 1) & ~1, k0 = j0 + KL * lane;
-            const float st = lane < rows ? stat[lane] : 0.f;
-            const float* x = p.logits + lo0 + (size_t)h * (kl - base) * rs;
             float* dst = k0 < j1 && k0 + KL > lo ? score_at(p, table, h, k0) : nullptr;
-            float w[KL];
-            const float* xk[KL];
+            const int h_end = min(p.Hkv, h + hp);
+#pragma unroll 1
+            for (int head = h; head < h_end; ++head, stat += kWeighRows) {
+                const float st = lane < rows ? stat[lane] : 0.f;
+                const float* x = p.logits + lo0 + (size_t)head * (kl - base) * rs;
+                float w[KL];
+                const float* xk[KL];
 #pragma unroll
-            for (int k = 0; k < KL; ++k) {
-                xk[k] = x + (size_t)(min(k0 + k, j1 - 1) - base) * rs;
-                w[k] = 0.f;
-            }
-            int r = 0;
-            if (rs % 4 == 0) {
-                for (; r < rs; r += 4) {
-                    float4 v[KL];
-#pragma unroll
-                    for (int k = 0; k < KL; ++k) v[k] = *reinterpret_cast<const float4*>(xk[k] + r);
-                    // the place behind an odd number of rows is no row's (0 times a K that may be infinite)
-                    if (r + 3 >= rows) {
-#pragma unroll
-                        for (int k = 0; k < KL; ++k) v[k].w = -INFINITY;
-                    }
-                    const float s0 = __shfl_sync(0xffffffffu, st, r), s1 = __shfl_sync(0xffffffffu, st, r + 1);
-                    const float s2 = __shfl_sync(0xffffffffu, st, r + 2), s3 = __shfl_sync(0xffffffffu, st, r + 3);
-#pragma unroll
-                    for (int k = 0; k < KL; ++k)
-                        w[k] += (ex2(v[k].x - s0) + ex2(v[k].y - s1)) + (ex2(v[k].z - s2) + ex2(v[k].w - s3));
+                for (int k = 0; k < KL; ++k) {
+                    xk[k] = x + (size_t)(min(k0 + k, j1 - 1) - base) * rs;
+                    w[k] = 0.f;
                 }
-            } else {
-                for (; r < rs; r += 2) {
-                    float2 v[KL];
+                int r = 0;
+                if (rs % 4 == 0) {
+                    for (; r < rs; r += 4) {
+                        float4 v[KL];
 #pragma unroll
-                    for (int k = 0; k < KL; ++k) v[k] = *reinterpret_cast<const float2*>(xk[k] + r);
-                    if (r + 1 >= rows) {
+                        for (int k = 0; k < KL; ++k) v[k] = *reinterpret_cast<const float4*>(xk[k] + r);
+                        // the place behind an odd number of rows is no row's (0 times a K that may be infinite)
+                        if (r + 3 >= rows) {
 #pragma unroll
-                        for (int k = 0; k < KL; ++k) v[k].y = -INFINITY;
+                            for (int k = 0; k < KL; ++k) v[k].w = -INFINITY;
+                        }
+                        const float s0 = __shfl_sync(0xffffffffu, st, r), s1 = __shfl_sync(0xffffffffu, st, r + 1);
+                        const float s2 = __shfl_sync(0xffffffffu, st, r + 2), s3 = __shfl_sync(0xffffffffu, st, r + 3);
+#pragma unroll
+                        for (int k = 0; k < KL; ++k)
+                            w[k] += (ex2(v[k].x - s0) + ex2(v[k].y - s1)) + (ex2(v[k].z - s2) + ex2(v[k].w - s3));
                     }
-                    const float s0 = __shfl_sync(0xffffffffu, st, r), s1 = __shfl_sync(0xffffffffu, st, r + 1);
+                } else {
+                    for (; r < rs; r += 2) {
+                        float2 v[KL];
 #pragma unroll
-                    for (int k = 0; k < KL; ++k) w[k] += ex2(v[k].x - s0) + ex2(v[k].y - s1);
+                        for (int k = 0; k < KL; ++k) v[k] = *reinterpret_cast<const float2*>(xk[k] + r);
+                        if (r + 1 >= rows) {
+#pragma unroll
+                            for (int k = 0; k < KL; ++k) v[k].y = -INFINITY;
+                        }
+                        const float s0 = __shfl_sync(0xffffffffu, st, r), s1 = __shfl_sync(0xffffffffu, st, r + 1);
+#pragma unroll
+                        for (int k = 0; k < KL; ++k) w[k] += ex2(v[k].x - s0) + ex2(v[k].y - s1);
+                    }
                 }
-            }
 #pragma unroll
-            for (int k = 0; k < KL; ++k)
-                if (k0 + k < lo || k0 + k >= j1) w[k] = -1.f;
-            if (dst) add_scores4(dst, k0, pos0, w);
+                for (int k = 0; k < KL; ++k)
+                    if (k0 + k < lo || k0 + k >= j1) w[k] = -1.f;
+                if (dst) add_scores4(dst + (size_t)(head - h) * p.ps, k0, pos0, w);
+            }
         } else {
             KeyTile<D, KT> t[kTiles];
             float w[kTiles][2];
@@ -806,6 +816,7 @@ struct WeighKern {
         return e != cudaSuccess ? e : cudaOccupancyMaxActiveBlocksPerMultiprocessor(weigh, rpa_weigh_kernel<D, KT>, kWeighThreads, 0);
     }
     static cudaError_t launch(const CUtensorMap& kmap, WeighParams p, int grid_weigh, cudaStream_t st) {
+        p.weigh_warps = grid_weigh * kWarps;
         p.item_keys = 16 * weigh_tiles(Deal<D, KT>::LOADS);
         cudaError_t e = launch_pdl(rpa_weigh_plan_kernel, 1, kPlanThreads, 0, st, p);
         if (e == cudaSuccess) e = launch_pdl(rpa_weigh_stats_kernel<D, KT>, p.ctas, kStatThreads, Ring<D, KT>::SMEM, st, kmap, p);

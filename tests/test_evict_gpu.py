@@ -294,6 +294,14 @@ def test_long_rows_beside_short_ones():
         run_and_check(Batch(np.random.default_rng(seed), q_lens, kv_lens, 16, 8, 2, 64, **more))
 
 
+@pytest.mark.parametrize("keys", [1300, 2700, 5300])
+def test_many_heads(keys):
+    """Enough keys and heads that a warp adds the weights of 2, 4 or 8 heads of 61, for whole and partial quads of keys."""
+    for seed, shape in ((47, dict(Hq=61, Hkv=61)), (48, dict(Hq=122, Hkv=61, sliding_window=keys - 70))):
+        rng = np.random.default_rng(seed)
+        run_and_check(Batch(rng, [1, 3, 1, 2, 0], [keys, keys + 1, keys - 3, keys + 130, keys], 16, D=64, **shape))
+
+
 def test_unaligned_scores_are_refused():
     b = Batch(np.random.default_rng(32), [1], [20], 16, 2, 2, 64)
     op = rpa.CacheEviction(budget=4, **b.cfg())
