@@ -11,7 +11,7 @@
 //            the keys in shared memory, and adds up all CTAs' histograms for itself through distributed
 //            shared memory.  Then one ordered pass lists the kept slots: each warp lists a run of
 //            neighbouring keys, so that one scan over the warps and CTAs gives every warp its place and its
-//            share of the ties, which go to the lowest slots.  Bound by its rounds of waits (three digits,
+//            share of the ties, which go to the lowest slots.  A digit whose bin is wanted whole is the last.  Bound by its rounds of waits (three digits,
 //            a few microseconds each), so a cluster is as large as leaves no SM without one.
 //   move     blocks of 64 kept rows: K and V of a head are neighbours in a slot, one copy of 2 D
 //            elements a row.  Bound by reading and writing those rows.  Onto fresh pages all blocks are
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(CLUSTER ? 1024 : 512, CLUSTER ? 1 : 3) rpa_evi
     __shared__ __align__(16) uint32_t s_hist[2][kBins];
     __shared__ uint32_t s_warp[kSelWarps], s_warp2[kSelWarps];
     __shared__ __align__(8) uint32_t s_count[2];  // of this CTA: keys above the threshold, keys equal to it
-    __shared__ uint32_t s_digit, s_left;
+    __shared__ uint32_t s_digit, s_left, s_all;
     __shared__ int s_order;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int C = CLUSTER ? p.cluster : 1, rank = CLUSTER ? (int)cluster_rank() : 0, unit = blockIdx.x / C;
@@ -245,12 +245,18 @@ __global__ void __launch_bounds__(CLUSTER ? 1024 : 512, CLUSTER ? 1 : 3) rpa_evi
             if (above < left && left <= above + c[i]) {
                 s_digit = (uint32_t)(low + kMine - 1 - i);
                 s_left = left - above;
+                s_all = left == above + c[i];  // every key of the bin
             }
             above += c[i];
         }
         __syncthreads();
         prefix = (prefix << bits) | s_digit;
         left = s_left;
+        if (s_all && prefix != 0u) {  // the keys from `prefix` on and no ties: the threshold is below its lowest key
+            prefix = (prefix << shift) - 1u;
+            left = 0;
+            break;
+        }
         __syncthreads();  // s_digit, s_left and s_warp are free again
     }
     // list the kept slots in order: keys above the threshold and the first `left` that equal it
