@@ -270,7 +270,7 @@ class CacheEviction(_Handle):
         """Cut every sequence to the budget and return its new length (new_kv_lens, int32 [max_num_seqs]).
 
         The kept keys' rows and scores move, in order, to the first slots of new_page_indices' pages (default:
-        page_indices, in place).  ``kept`` (int32 [max_num_seqs, Hkv, budget]) receives the slots they had.
+        page_indices, in place, where rows wait for each other: fresh pages are faster).  ``kept`` (int32 [max_num_seqs, Hkv, budget]) receives the slots they had.
         """
         if new_page_indices is None:
             new_page_indices = page_indices

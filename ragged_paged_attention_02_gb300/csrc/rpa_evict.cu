@@ -13,16 +13,17 @@
 //            neighbouring keys, so that one scan over the warps and CTAs gives every warp its place and its
 //            share of the ties, which go to the lowest slots.  A digit whose bin is wanted whole is the last.  Bound by its rounds of waits (three digits,
 //            a few microseconds each), so a cluster is as large as leaves no SM without one.
-//   move     blocks of 64 kept rows: K and V of a head are neighbours in a slot, one copy of 2 D
-//            elements a row.  Bound by reading and writing those rows.  Onto fresh pages all blocks are
-//            independent.  Where the new pages hold other kept rows (in place), a head's rows move in
-//            ascending order: kept row i sits at slot j >= i and goes to slot i, so that a row may be
-//            written once all rows up to it are read, and what is read later is never written before.
-//            A cluster of up to 8 CTAs takes a head and meets between a round's reads and its writes.
+//   move     K and V of a head are neighbours in a slot, a row is one copy of 2 D elements.  A CTA takes as
+//            many rows a round as its registers hold (32 to 256: eight 16-byte vectors a thread), and looks
+//            the next round's up beside the reads.  Bound by reading and writing those rows.  Onto fresh
+//            pages all rounds are independent.  Where the new pages hold other kept rows (in place), a
+//            head's rows move in ascending order: kept row i sits at slot j >= i and goes to slot i, so that
+//            a row may be written once all rows up to it are read, and what is read later is never written
+//            before.  A cluster of up to 8 CTAs takes a head and meets between reads and writes.
 //
-// 64 sequences of up to 8 k keys cut to 2 k (8 heads, D 128, bf16; 1.09 GB): select 25 us, move 170 us,
-// 6.4 TB/s; in place 229 us in all.  Two of 100 k keys cut to 16 k (e4m3, 139 MB): 23 and 28 us; in place 84
-// us in all (16 heads, one CTA each: 240 us; each round's lookups not ahead of it: 530).
+// 64 sequences of up to 8 k keys cut to 2 k (8 heads, D 128, bf16; 1.09 GB): 194 us, of which select 23 and move
+// 170 (6.4 TB/s); in place 229.  Two of 100 k keys cut to 16 k (e4m3, 139 MB): 48 us, 23 and 25; in place 84 (16
+// heads, one CTA each: 240; the lookups not ahead of the reads: 532).
 #include <math.h>
 #include <string.h>
 
@@ -39,8 +40,8 @@ constexpr int kBins = 2048;
 constexpr int kMaxCluster = 4;
 constexpr int kSelCached = 40 * 1024;  // scores a CTA keeps at most (160 KB); further ones are read again
 constexpr int kMoveThreads = 256;
-constexpr int kMoveCtas = 4;  // resident an SM
-constexpr int kMoveRows = 64;
+constexpr int kMoveCtas = 3;   // resident an SM onto fresh pages (64 x 8 k: 194 us; two 207; four 322, their vectors spilled)
+constexpr int kPlaceCtas = 2;  // the same in place, where clusters are few
 constexpr int kMaxMoveCluster = 8;
 
 // A score as an integer of the same order; NaN lowest, -0 as +0
@@ -351,30 +352,20 @@ __device__ __forceinline__ Row look_up(const CompactParams& p, int s, int h, int
 
 constexpr int kFly = 8;  // 16-byte vectors a thread has in flight
 
-// All kept rows of a head onto pages that hold other kept rows, by the C CTAs of a cluster (or one).  A round takes as many
-// neighbouring rows as their registers hold: all CTAs read theirs, meet, and write.  Where rows are is looked up a
-// round ahead, their slots two, beside the reads.
-template <bool CLUSTER>
-__device__ __forceinline__ void move_in_order(const CompactParams& p, int s, int h, int kept, int C, int rank, long long (*s_from)[kMoveThreads],
-                                              long long (*s_to)[kMoveThreads]) {
+// Rounds of rows, as many as the CTA's registers hold: read, meet (with the CTAs of a cluster), write.  where(n) is this
+// thread's row of round n, looked up a round ahead, beside the reads.
+template <bool CLUSTER, typename Where>
+__device__ __forceinline__ void move_rounds(const CompactParams& p, int rounds, long long (*s_from)[kMoveThreads],
+                                            long long (*s_to)[kMoveThreads], Where where) {
     uint4* kv = reinterpret_cast<uint4*>(p.kv);
-    const int tid = threadIdx.x, vecs = 1 << p.vec_shift, per_cta = kFly * kMoveThreads >> p.vec_shift, step = C * per_cta;
-    const int* list = p.list + ((size_t)s * p.Hkv + h) * p.budget;
-    const int mine = rank * per_cta + tid;  // this thread's row of a round, if tid < per_cta
-    auto slot = [&](int i0) { return tid < per_cta && i0 + mine < kept ? list[i0 + mine] : -1; };
-    auto where = [&](int i0, int j) {
-        Row r = {0, -1, nullptr, 0.f};
-        if (j >= 0) r = look_up(p, s, h, i0 + mine, j);
-        return r;
-    };
-    int j = slot(0), at = 0;  // at: the round's third of the tables
-    Row row = where(0, j);
-    j = slot(step);
-    __syncthreads();  // the last head's tables
+    const int tid = threadIdx.x, vecs = 1 << p.vec_shift;  // 16-byte vectors of a row: 8, 16, 32 or 64
+    Row row = where(0);
+    __syncthreads();  // the tables' last round
     s_from[0][tid] = row.from;
     s_to[0][tid] = row.to;
     __syncthreads();
-    for (int i0 = 0; i0 < kept; i0 += step) {
+    int at = 0;  // the round's third of the tables
+    for (int n = 0; n < rounds; ++n) {
         const int next = at == 2 ? 0 : at + 1;
         uint4 x[kFly];
 #pragma unroll
@@ -382,8 +373,7 @@ __device__ __forceinline__ void move_in_order(const CompactParams& p, int s, int
             const int v = tid + f * kMoveThreads, r = v >> p.vec_shift;
             if (s_to[at][r] >= 0) x[f] = __ldcs(kv + s_from[at][r] + (v & (vecs - 1)));
         }
-        const Row ahead = where(i0 + step, j);
-        j = slot(i0 + 2 * step);
+        const Row ahead = where(n + 1);
         s_from[next][tid] = ahead.from;
         s_to[next][tid] = ahead.to;
         if (CLUSTER) cluster_sync();
@@ -401,56 +391,41 @@ __device__ __forceinline__ void move_in_order(const CompactParams& p, int s, int
 
 // IN_PLACE: the new pages are the old ones, rows move in order or not at all, a cluster a head.  Else each sequence by its own rule
 template <bool IN_PLACE>
-__global__ void __launch_bounds__(kMoveThreads, IN_PLACE ? 2 : kMoveCtas) rpa_evict_move_kernel(const CompactParams p) {
+__global__ void __launch_bounds__(kMoveThreads, IN_PLACE ? kPlaceCtas : kMoveCtas) rpa_evict_move_kernel(const CompactParams p) {
     __shared__ long long s_from[3][kMoveThreads], s_to[3][kMoveThreads];  // Row::from and to
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, per_cta = kFly * kMoveThreads >> p.vec_shift;  // rows of a CTA's round
     pdl_trigger();
     pdl_wait();
     const int units = p.S * p.Hkv, C = IN_PLACE ? p.move_cluster : 1, rank = IN_PLACE ? (int)cluster_rank() : 0;
     for (int u = blockIdx.x / C; u < units; u += gridDim.x / C) {
         const int s = u / p.Hkv, h = u - s * p.Hkv, kept = p.seq_n[s];
         if (IN_PLACE && kept >= 0 && h == 0 && rank == 0 && tid == 0) p.new_kv_lens[s] = kept;
-        if (kept > 0 && p.seq_order[s] != 0) move_in_order<IN_PLACE>(p, s, h, kept, C, rank, s_from, s_to);
+        if (kept <= 0 || p.seq_order[s] == 0) continue;
+        // all kept rows of a head onto pages that hold others of them; a row's slot is read two rounds ahead
+        const int* list = p.list + ((size_t)s * p.Hkv + h) * p.budget;
+        const int step = C * per_cta, mine = rank * per_cta + tid;
+        auto slot = [&](int n) { return tid < per_cta && (long long)n * step + mine < kept ? list[n * step + mine] : -1; };
+        int j = slot(0);
+        move_rounds<IN_PLACE>(p, (kept + step - 1) / step, s_from, s_to, [&](int n) {
+            Row r = {0, -1, nullptr, 0.f};
+            if (j >= 0) r = look_up(p, s, h, n * step + mine, j);
+            j = slot(n + 1);
+            return r;
+        });
     }
     if (IN_PLACE) return;
     // onto fresh pages: blocks of rows in any order
-    const int blocks = (p.budget + kMoveRows - 1) / kMoveRows;
-    const int items = units * blocks;
-    const int vshift = p.vec_shift, vecs = 1 << vshift;  // 16-byte vectors of a row: 8, 16, 32 or 64
-    uint4* kv = reinterpret_cast<uint4*>(p.kv);
-    const int sub = min(kMoveRows, kFly * kMoveThreads >> vshift);  // rows whose vectors the CTA's registers hold at once
-    for (int it = blockIdx.x; it < items; it += gridDim.x) {
-        const int h = it % p.Hkv, b = it / p.Hkv % blocks, s = it / p.Hkv / blocks;
-        const int kept = p.seq_n[s], i0 = b * kMoveRows;
-        if (kept < 0) continue;
-        if (b == 0 && h == 0 && tid == 0) p.new_kv_lens[s] = kept;
-        if (p.seq_order[s] != 0 || i0 >= kept) continue;
-        const int rows = min(kMoveRows, kept - i0);
-        Row row = {0, -1, nullptr, 0.f};
-        __syncthreads();
-        if (tid < kMoveRows) {
-            if (tid < rows) row = look_up(p, s, h, i0 + tid, p.list[((size_t)s * p.Hkv + h) * p.budget + i0 + tid]);
-            s_from[0][tid] = row.from;
-            s_to[0][tid] = row.to;
-        }
-        __syncthreads();
-        // `sub` rows at a time, eight vectors a thread in flight
-        for (int r0 = 0; r0 < rows; r0 += sub) {
-            const int first = r0 << vshift, total = min(rows, r0 + sub) << vshift;
-            uint4 x[kFly];
-#pragma unroll
-            for (int f = 0; f < kFly; ++f) {
-                const int v = first + tid + f * kMoveThreads, r = v >> vshift;
-                if (v < total && s_to[0][r] >= 0) x[f] = __ldcs(kv + s_from[0][r] + (v & (vecs - 1)));
-            }
-#pragma unroll
-            for (int f = 0; f < kFly; ++f) {
-                const int v = first + tid + f * kMoveThreads, r = v >> vshift;
-                if (v < total && s_to[0][r] >= 0) __stcs(kv + s_to[0][r] + (v & (vecs - 1)), x[f]);
-            }
-        }
-        if (row.sc_to) *row.sc_to = row.sc;
-    }
+    const int blocks = (p.budget + per_cta - 1) / per_cta, items = units * blocks;
+    const int rounds = (items - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x;
+    move_rounds<false>(p, rounds, s_from, s_to, [&](int n) {
+        Row r = {0, -1, nullptr, 0.f};
+        if (n >= rounds) return r;
+        const int it = blockIdx.x + n * gridDim.x, h = it % p.Hkv, b = it / p.Hkv % blocks, s = it / p.Hkv / blocks;
+        const int kept = p.seq_n[s], i = b * per_cta + tid;
+        if (b == 0 && h == 0 && tid == 0 && kept >= 0) p.new_kv_lens[s] = kept;
+        if (tid < per_cta && i < kept && p.seq_order[s] == 0) r = look_up(p, s, h, i, p.list[((size_t)s * p.Hkv + h) * p.budget + i]);
+        return r;
+    });
 }
 
 }  // namespace
@@ -463,7 +438,7 @@ cudaError_t compact_prepare(int64_t units, int max_keys, int sms, int* cluster, 
     *cluster = c;
     // rows that move in order: as many CTAs a unit as there are
     int m = 1;
-    while (m < kMaxMoveCluster && units * (2 * m) <= sms * kMoveCtas) m *= 2;
+    while (m < kMaxMoveCluster && units * (2 * m) <= sms * kPlaceCtas) m *= 2;
     *move_cluster = m;
     const int share = ((max_keys + 3) / 4 + 1 + c - 1) / c * 4;  // (one quad more where neither end is a quad's)
     *cached = share < kSelCached ? share : kSelCached;
@@ -489,8 +464,8 @@ cudaError_t launch_compact(const CompactParams& p, int sms, cudaStream_t st) {
     cudaError_t e = cudaLaunchKernelEx(&cfg, p.cluster > 1 ? rpa_evict_select_kernel<true> : rpa_evict_select_kernel<false>, p);
     if (e != cudaSuccess) return e;
     if (p.new_pages != p.page_indices) return launch_pdl(rpa_evict_move_kernel<false>, sms * kMoveCtas, kMoveThreads, 0, st, p);
-    const int m = p.move_cluster, units = p.S * p.Hkv, most = sms * kMoveCtas / m;
-    cfg.gridDim = dim3((units < most ? units : most) * m);
+    const int m = p.move_cluster;
+    cfg.gridDim = dim3(p.S * p.Hkv * m);
     cfg.blockDim = dim3(kMoveThreads);
     cfg.dynamicSmemBytes = 0;
     attr[1].val.clusterDim.x = m;
@@ -540,7 +515,7 @@ int rpa_evict_validate_cfg(const RpaEvictCfg* c) {
     const int64_t lim = (int64_t)1 << 31, units = c->cache.max_num_seqs * c->cache.num_kv_heads;
     if (c->cache.num_q_tokens * (c->cache.num_q_heads / c->cache.num_kv_heads) >= lim ||
         c->cache.total_num_pages >= lim / c->cache.page_size || units >= lim / 8 ||
-        units >= lim / ((c->budget + kMoveRows - 1) / kMoveRows))
+        units >= lim / 4 / (c->budget / (kFly * kMoveThreads / 64) + 1))
         return RPA_ERR_UNSUPPORTED;
     return RPA_OK;
 }
