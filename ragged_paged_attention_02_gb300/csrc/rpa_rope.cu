@@ -11,18 +11,19 @@
 // tenth of a radian at a million positions, and in 64 bits the GPU runs it at 1/64 of the rate.
 // Sines are computed once per token and pair, into shared memory, and serve all heads.
 //
-// A CTA takes a run of neighbouring tokens, up to 16 at a time: its warps look their sequences, positions and
-// slots up at once (cu_q_lens by a 32-ary search, then kv_lens, then the page id: four dependent loads, some
-// two microseconds that one token a CTA paid each time), all threads compute the sines, and from there on
+// A CTA takes a run of neighbouring tokens, up to 16 at a time, and looks their sequences, positions and slots up
+// at once: cu_q_lens and kv_lens of up to 512 sequences go to shared memory whole (two dependent loads to the page
+// id where a search in memory makes four: 8 k tokens 61.1 -> 60.1 us), beside more a warp searches a token's, 32
+// probes at a time.  Then all threads compute the sines, and from there on
 // there is only streaming: units of 16 elements (two 16-byte vectors of 2-byte types) of one row (q head, K
 // row or V row).  A rotary unit is 8 pairs, both partners in one thread's registers (HALF: two vectors
 // rotary_dim / 2 apart; INTERLEAVED: 16 neighbours), so that a row is read once and written once.  A thread
 // keeps its place in the row and steps over the rows of all tokens, two rows' loads in flight; the first
 // go out before the lookups.
 //
-// Bound by HBM: 8192 tokens of 64 q and 8 kv heads at D 128 (bf16, 344 MB) take 61 us, 5.6 TB/s, 0.83 of the
-// measured copy.  Five CTAs an SM with two rows in flight a thread: 61 us; four CTAs: 63 us with two rows, 64
-// with four (spilled); one token a CTA: 79 to 87 us.
+// Bound by HBM: 8192 tokens of 64 q and 8 kv heads at D 128 (bf16, 344 MB) take 60 us, 5.7 TB/s, 0.84 of the
+// measured copy.  Five CTAs an SM with two rows in flight a thread, when that took 61 us: four CTAs 63 us with two rows,
+// 64 with four (spilled); one token a CTA 79 to 87 us.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <string.h>
@@ -48,6 +49,7 @@ constexpr int kUnit = 16;       // elements of a unit
 constexpr int kRopeThreads = 256;
 constexpr int kRopeCtas = 5;    // resident an SM
 constexpr int kTokens = 16;     // tokens of a CTA's round
+constexpr int kSeqs = 512;      // sequences whose cu_q_lens and kv_lens a CTA reads into shared memory
 constexpr int kMaxPairs = 288;  // rotary_dim <= 576
 
 struct RopeParams {
@@ -157,6 +159,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rpa_rope_kernel(const
     extern __shared__ float4 s_cs[];
     __shared__ long long s_slot[kTokens];  // cache slot of a token (page * page_size + place), or -1
     __shared__ int s_pos[kTokens], s_live[kTokens];
+    __shared__ int s_cu[kSeqs + 1], s_kl[kSeqs];
+    __shared__ unsigned long long s_turns[kMaxPairs];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
     const int place = tid % p.per_row, row0 = tid / p.per_row;
     // this thread's unit: elements [e0, e0 + 8) and [e1, e1 + 8) of a row
@@ -178,8 +182,33 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rpa_rope_kernel(const
         const int h = r < p.Hq ? r : r < p.Hq + p.Hkv ? r - p.Hq : r - p.Hq - p.Hkv;
         return base + (size_t)h * p.D * sizeof(QT);
     };
+    // token i of a round: its sequence (< 0: none), where it starts and how many tokens and keys it has
+    auto look_up = [&](int i, int t, int s, int q0, int ql, int kl) {
+        int live = 0, pos = 0;
+        long long slot = -1;
+        if (s >= 0 && q0 >= 0 && kl <= p.P * p.ps && ql <= kl && q0 + ql <= p.T) {
+            live = 1;
+            const int j = kl - ql + (t - q0);
+            const int pg = p.page_indices[(size_t)s * p.P + j / p.ps];
+            pos = p.positions ? p.positions[t] : j;
+            if ((unsigned)pg < (unsigned)p.N) slot = (long long)pg * p.ps + j % p.ps;
+            else set_status(p.status, RPA_ERR_BAD_PAGE_INDEX);
+        }
+        s_live[i] = live;
+        s_pos[i] = pos;
+        s_slot[i] = slot;
+    };
     pdl_trigger();
+    for (int i = tid; i < p.rd / 2; i += kRopeThreads) s_turns[i] = p.turns[i];  // the handle's own
     pdl_wait();
+    const bool few = p.S <= kSeqs;
+    if (few) {
+        for (int i = tid; i < p.S; i += kRopeThreads) {
+            s_cu[i] = p.cu[i];
+            s_kl[i] = p.kv_lens[i];
+        }
+        if (tid == 0) s_cu[p.S] = p.cu[p.S];
+    }
     for (; t0 < t_end; t0 += kTokens) {
         const int n = min(kTokens, t_end - t0);
         Vec8<QT> x0[kBatch], x1[kBatch];
@@ -204,25 +233,24 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rpa_rope_kernel(const
         };
         int tk = row0 < p.row_step ? row0 / p.rows : n, r = row0 % p.rows;  // (576: 252 threads have a place)
         fetch(tk, r);
-        for (int i = warp; i < n; i += warps) {
-            const int t = t0 + i, s = find_seq(p.cu, p.S, t, lane);
-            if (lane == 0) {
-                int live = 0, pos = 0;
-                long long slot = -1;
-                if (s >= 0) {
-                    const int q0 = p.cu[s], ql = p.cu[s + 1] - q0, kl = p.kv_lens[s];
-                    if (q0 >= 0 && kl <= p.P * p.ps && ql <= kl && q0 + ql <= p.T) {
-                        live = 1;
-                        const int j = kl - ql + (t - q0);
-                        const int pg = p.page_indices[(size_t)s * p.P + j / p.ps];
-                        pos = p.positions ? p.positions[t] : j;
-                        if ((unsigned)pg < (unsigned)p.N) slot = (long long)pg * p.ps + j % p.ps;
-                        else set_status(p.status, RPA_ERR_BAD_PAGE_INDEX);
-                    }
+        if (few) {
+            __syncthreads();
+            if (tid < n) {
+                // the last sequence that starts at or before the token
+                const int t = t0 + tid;
+                int s = 0, end = p.S;
+                while (end - s > 1) {
+                    const int m = (s + end) / 2;
+                    if (s_cu[m] <= t) s = m;
+                    else end = m;
                 }
-                s_live[i] = live;
-                s_pos[i] = pos;
-                s_slot[i] = slot;
+                const bool in = p.S > 0 && s_cu[s] <= t && t < s_cu[s + 1];
+                look_up(tid, t, in ? s : -1, in ? s_cu[s] : 0, in ? s_cu[s + 1] - s_cu[s] : 0, in ? s_kl[s] : 0);
+            }
+        } else {
+            for (int i = warp; i < n; i += warps) {
+                const int t = t0 + i, s = find_seq(p.cu, p.S, t, lane);
+                if (lane == 0) look_up(i, t, s, s < 0 ? 0 : p.cu[s], s < 0 ? 0 : p.cu[s + 1] - p.cu[s], s < 0 ? 0 : p.kv_lens[s]);
             }
         }
         __syncthreads();
@@ -230,7 +258,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rpa_rope_kernel(const
         for (int i = tid; i < n * (p.rd / 2); i += blockDim.x) {
             const int k = i / (p.rd / 2), pair = i - k * (p.rd / 2);
             // the angle's fraction of a turn, its upper 32 bits as half turns in [-1, 1)
-            const unsigned long long f = p.turns[pair] * (unsigned long long)(long long)s_pos[k];
+            const unsigned long long f = s_turns[pair] * (unsigned long long)(long long)s_pos[k];
             float sn, cs;
             sincospif((float)(int)((f + 0x80000000ull) >> 32) * 4.656612873077393e-10f, &sn, &cs);
             cs2[((k * 4 + (pair & 7) / 2) * places + pair / 8) * 2 + (pair & 1)] = make_float2(cs * p.magnitude, sn * p.magnitude);
