@@ -366,6 +366,8 @@ void rpa_rope_destroy(RpaRope* h);
 typedef struct RpaPrefix RpaPrefix;
 /* Host only; 1 <= max_groups <= max_num_seqs. */
 int rpa_prefix_validate_cfg(const RpaCfg* cfg, int64_t max_groups);
+/* The handle's workspace holds float32 partial results of every query row, twice (prefix and own keys), and more for
+ * prefixes cut into pieces. */
 int rpa_prefix_create(const RpaCfg* cfg, int64_t max_groups, RpaPrefix** out);
 /* As rpa_forward, with
  *   cu_groups    device, int32 [max_groups + 1]: group g is the sequences [cu_groups[g], cu_groups[g + 1]);
@@ -396,6 +398,8 @@ typedef struct RpaEvictCfg {
 typedef struct RpaEvict RpaEvict;
 /* Host only. */
 int rpa_evict_validate_cfg(const RpaEvictCfg* cfg);
+/* The handle's workspace holds, beside lists of kept slots, the logits of sequences of few query rows, for all
+ * the keys that max_num_seqs sequences can have but at most 1 GiB (more keys: logits are computed twice). */
 int rpa_evict_create(const RpaEvictCfg* cfg, RpaEvict** out);
 
 /* Add to scores the softmax weights (rpa_forward's: causal and window masks, soft cap, sinks in the

@@ -320,6 +320,22 @@ def test_many_sequences():
     check(b, *x, out, before, cache, rope)
 
 
+@pytest.mark.parametrize("S", [1, 512, 513])
+def test_several_rounds_of_tokens(S):
+    """More tokens than all CTAs take at once, of as many sequences as their shared memory holds lengths for, and of one more."""
+    rng = np.random.default_rng(22)
+    q_lens = [int(x) for x in rng.integers(0, 2 * 13300 // S, S)] if S > 1 else [13300]
+    b = Batch(rng, q_lens, [n + int(x) for n, x in zip(q_lens, rng.integers(0, 9, S))], 16, 2, 1, 64, lead=3, tail=5)
+    assert b.T > 152 * 5 * 16
+    x = inputs(b, rng)
+    cache = b.cache()
+    before = cache.clone()
+    op = rpa.RopeAppend(**b.cfg())
+    out = op.append(*x, cache, *b.lens(), b.S)
+    assert op.status() == rpa.RPA_OK
+    check(b, *x, out, before, cache, dict(rotary_dim=64))
+
+
 def test_one_call_after_another():
     """Calls that follow each other on a stream without a wait, each writing the cache that the next rotates into."""
     rng = np.random.default_rng(20)
