@@ -28,7 +28,7 @@
 //
 // 64 decodes over 612 MB of K (32 heads, 8 kv heads, D 128, bf16): 124 us, of which plan 4, stats 109 (5.5 TB/s; its
 // copies alone, computing nothing, take 100: K rows are every other 256 bytes) and weigh 11.  The last 202 tokens of six
-// prompts of 1 to 6 k keys (16 heads, 8 kv heads, D 64, f16; 1.1 GFLOP): 48.5 us, 4 / 26 / 18: bound by
+// prompts of 1 to 6 k keys (16 heads, 8 kv heads, D 64, f16; 1.1 GFLOP): 47.6 us, 4 / 26 / 17: bound by
 // instructions, some 300 a warp for a tile of 16 keys x 16 rows, and by a row block's end (1.8 us: reductions, the counter,
 // the next item).  Measured there: two or four row blocks a warp over the same keys 50 and 52 us; four CTAs an SM 49.5.
 //
@@ -156,15 +156,12 @@ struct Deal {
     static constexpr int REGS = D / 8;          // 32-bit operand registers of one row's share
 };
 
-// One thread's share of query row `row` (tokens x heads of group h) of a sequence, in the operand type.
+// One thread's share of query row `row` (tokens x heads of group h) of a sequence, in the operand type; behind the last
+// row that row again, which brings no infinities or NaN of its own.
 template <int D, int KT>
 __device__ __forceinline__ void load_q(const WeighParams& p, int q0, int h, int row, int rows, int c, uint32_t* r) {
     using L = Deal<D, KT>;
-    if (row >= rows) {
-#pragma unroll
-        for (int i = 0; i < L::REGS; ++i) r[i] = 0;
-        return;
-    }
+    row = min(row, rows - 1);
     const int i = p.group.div(row), g = row - i * p.G;
     const uint8_t* src = p.q + (((size_t)(q0 + i) * p.Hq + (size_t)h * p.G + g) * D + c * L::E) * 2;
 #pragma unroll
@@ -703,7 +700,7 @@ __global__ void __launch_bounds__(kWeighThreads, D == 256 ? 2 : 4) rpa_weigh_ker
                         float4 v[KL];
 #pragma unroll
                         for (int k = 0; k < KL; ++k) v[k] = *reinterpret_cast<const float4*>(xk[k] + r);
-                        // the place behind an odd number of rows is no row's (0 times a K that may be infinite)
+                        // the place behind an odd number of rows is no row's (it holds the last one again)
                         if (r + 3 >= rows) {
 #pragma unroll
                             for (int k = 0; k < KL; ++k) v[k].w = -INFINITY;
@@ -756,14 +753,15 @@ __global__ void __launch_bounds__(kWeighThreads, D == 256 ? 2 : 4) rpa_weigh_ker
             float2 st[kDeep];  // of rows 2 quad and 2 quad + 1
             auto fetch = [&](int r0, int b) {
                 load_q<D, KT>(p, q0, h, r0 + lane / 4, rows, quad, q[b][0]);
+                // rows behind the last weigh nothing
                 st[b] = *reinterpret_cast<const float2*>(stat + r0 + 2 * quad);
+                if (r0 + 2 * quad >= rows) st[b].x = INFINITY;
+                if (r0 + 2 * quad + 1 >= rows) st[b].y = INFINITY;
             };
             auto add = [&](auto masked, int r0, int b) {
                 constexpr bool MASK = decltype(masked)::value;
                 const int r = r0 + 2 * quad;
                 const int pa = MASK ? pos0 + p.group.div(r) : 0, pb = MASK ? pos0 + p.group.div(r + 1) : 0;
-                // rows behind the last are no rows (0 times a K that may be infinite; no statistics)
-                const bool ra = r < rows, rb = r + 1 < rows;
 #pragma unroll
                 for (int i = 0; i < kTiles; ++i) {
                     float acc[1][4] = {{0.f, 0.f, 0.f, 0.f}};
@@ -772,8 +770,8 @@ __global__ void __launch_bounds__(kWeighThreads, D == 256 ? 2 : 4) rpa_weigh_ker
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const int j = j0 + 16 * i + 8 * k + lane / 4;
-                        w[i][k] += (ra ? ex2(hide<MASK>(p, acc[0][2 * k], j, pa, t[i].ok[k]) - st[b].x) : 0.f) +
-                                   (rb ? ex2(hide<MASK>(p, acc[0][2 * k + 1], j, pb, t[i].ok[k]) - st[b].y) : 0.f);
+                        w[i][k] += ex2(hide<MASK>(p, acc[0][2 * k], j, pa, t[i].ok[k]) - st[b].x) +
+                                   ex2(hide<MASK>(p, acc[0][2 * k + 1], j, pb, t[i].ok[k]) - st[b].y);
                     }
                 }
             };
