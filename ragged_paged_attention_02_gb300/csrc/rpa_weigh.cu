@@ -28,7 +28,7 @@
 //
 // 64 decodes over 612 MB of K (32 heads, 8 kv heads, D 128, bf16): 124 us, of which plan 4, stats 109 (5.5 TB/s; its
 // copies alone, computing nothing, take 100: K rows are every other 256 bytes) and weigh 11.  The last 202 tokens of six
-// prompts of 1 to 6 k keys (16 heads, 8 kv heads, D 64, f16; 1.1 GFLOP): 47.6 us, 4 / 26 / 17: bound by
+// prompts of 1 to 6 k keys (16 heads, 8 kv heads, D 64, f16; 1.1 GFLOP): 47.2 us, 4 / 26 / 17: bound by
 // instructions, some 300 a warp for a tile of 16 keys x 16 rows, and by a row block's end (1.8 us: reductions, the counter,
 // the next item).  Measured there: two or four row blocks a warp over the same keys 50 and 52 us; four CTAs an SM 49.5.
 //
@@ -775,7 +775,9 @@ __global__ void __launch_bounds__(kWeighThreads, D == 256 ? 2 : 4) rpa_weigh_ker
                     }
                 }
             };
+            const bool seen_by_all = full && !p.has_window && (!p.causal || j0 + 16 * kTiles - 1 <= pos0);
             auto step = [&](int r0, int b) {
+                if (seen_by_all) return add(std::false_type{}, r0, b);
                 const int a = pos0 + p.group.div(r0), z = pos0 + p.group.div(min(r0 + 7, rows - 1));
                 if (full && !some_hidden(p, j0, j0 + 16 * kTiles, a, z)) add(std::false_type{}, r0, b);
                 else add(std::true_type{}, r0, b);
