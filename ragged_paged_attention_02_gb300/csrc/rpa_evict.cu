@@ -569,7 +569,7 @@ int rpa_evict_create(const RpaEvictCfg* cfg, RpaEvict** out) {
         delete h;
         return RPA_ERR_CUDA;
     }
-    if (cudaMemset(h->ws, 0, 256) != cudaSuccess) {
+    if (!set_now(cudaMemset(h->ws, 0, 256))) {
         cudaGetLastError();
         cudaFree(h->ws);
         delete h;

@@ -190,7 +190,7 @@ int rpa_create(const RpaCfg* cfg, RpaHandle** out) {
         return RPA_ERR_CUDA;
     }
     h->w = workspace_carve(c, h->ks, h->ws);
-    if (cudaMemset(h->w.ctrl, 0, kCtrlWords * sizeof(int)) != cudaSuccess) {
+    if (!set_now(cudaMemset(h->w.ctrl, 0, kCtrlWords * sizeof(int)))) {
         cudaGetLastError();
         if (h->can_concurrent) {
             cudaEventDestroy(h->ev_dec);

@@ -351,6 +351,12 @@ struct DeviceGuard {
         if (prev >= 0 && cudaGetDevice(&cur) == cudaSuccess && cur != prev) cudaSetDevice(prev);
     }
 };
+// What a handle's memory starts with, on the device before its *_create returns: cudaMemset, and cudaMemcpy of a small
+// pageable buffer, return while the legacy default stream still has them to do, and a handle's first call may be on a
+// stream that does not wait for that one.
+inline bool set_now(cudaError_t queued) {
+    return queued == cudaSuccess && cudaStreamSynchronize(cudaStreamLegacy) == cudaSuccess;
+}
 inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 // Synchronises st, reads a sticky device status word and clears it where it holds an error.
 inline int take_status(int* word, cudaStream_t st) {

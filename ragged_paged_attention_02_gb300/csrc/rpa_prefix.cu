@@ -513,7 +513,7 @@ bool prefix_allocate(RpaPrefix* h) {
                  o_po = take((size_t)part * kDecRows * ks.D * sizeof(float)), o_ml = take((size_t)part * kDecRows * 2 * sizeof(float)),
                  o_q = take(ks.q_conv ? (size_t)T * c.num_q_heads * ks.D * 2 : 0);
     if (cudaMalloc(&h->ws, off) != cudaSuccess) return false;
-    if (cudaMemset(h->ws, 0, kCtrlWords * sizeof(int)) != cudaSuccess) return false;
+    if (!set_now(cudaMemset(h->ws, 0, kCtrlWords * sizeof(int)))) return false;
     uint8_t* b = static_cast<uint8_t*>(h->ws);
     h->w.ctrl = reinterpret_cast<int*>(b + o_ctrl);
     h->w.dec_units = reinterpret_cast<Unit*>(b + o_dec);

@@ -427,7 +427,7 @@ int rpa_rope_create(const RpaRopeCfg* cfg, RpaRope** out) {
         delete h;
         return RPA_ERR_CUDA;
     }
-    if (cudaMemcpy(h->turns, f, (size_t)(n + 1) * sizeof f[0], cudaMemcpyHostToDevice) != cudaSuccess) {
+    if (!set_now(cudaMemcpy(h->turns, f, (size_t)(n + 1) * sizeof f[0], cudaMemcpyHostToDevice))) {
         cudaGetLastError();
         cudaFree(h->turns);
         delete h;

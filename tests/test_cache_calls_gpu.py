@@ -1,0 +1,89 @@
+"""Calls of the paged cache's operators that their documentation allows and that the tests of each operator's values do
+not make: a fresh handle's first call on a stream of its own, and more."""
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import ragged_paged_attention_02_gb300 as rpa  # noqa: E402
+from cache_util import Batch  # noqa: E402
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import __graft_entry__
+
+    __graft_entry__.build()
+
+
+def same(a, b):
+    raw = lambda t: t.view(torch.uint8) if t.element_size() == 1 else t  # noqa: E731
+    return torch.equal(raw(a), raw(b))
+
+
+class Calls:
+    """One batch, and a call of each handle kind on it: make(kind) a handle, call(kind, handle, stream) its output."""
+
+    KINDS = ("forward", "rope", "prefix", "accumulate", "compact")
+
+    def __init__(self, seed, kv="bf16"):
+        scale = None if kv == "bf16" else 0.05
+        b = self.b = Batch(np.random.default_rng(seed), [1, 30, 2, 1], [300, 64, 90, 700], 16, 8, 2, 128, kv=kv, k_scale=scale, v_scale=scale)
+        self.cache, self.q, self.lens = b.cache(), b.queries(), b.lens()
+        self.kv = [b.queries()[:, :2].contiguous() for _ in range(2)]
+        self.groups = torch.tensor([0, 1, b.S], dtype=torch.int32, device="cuda")
+        self.prefix_lens = torch.tensor([200, 0], dtype=torch.int32, device="cuda")
+        self.scores = torch.rand(b.N, 2, 16, device="cuda")
+
+    def make(self, kind):
+        cfg = self.b.cfg()
+        return {"forward": lambda: rpa.RaggedPagedAttention(**cfg), "rope": lambda: rpa.RopeAppend(**cfg),
+                "prefix": lambda: rpa.SharedPrefixAttention(max_groups=2, **cfg),
+                "accumulate": lambda: rpa.CacheEviction(budget=60, **cfg), "compact": lambda: rpa.CacheEviction(budget=60, **cfg)}[kind]()
+
+    def buffers(self):
+        """What a call writes, in buffers of its own."""
+        return [torch.zeros_like(self.q), self.cache.clone(), self.scores.clone(), torch.zeros_like(self.lens[0])]
+
+    def call(self, kind, op, out, stream=None):
+        q, cache, scores, kvl = out
+        lens, table, cu = self.lens
+        S = self.b.S
+        if kind == "forward":
+            op.forward(self.q, cache, lens, table, cu, S, out=q, stream=stream)
+        elif kind == "rope":
+            op.append(self.q, *self.kv, cache, lens, table, cu, S, q_out=q, stream=stream)
+        elif kind == "prefix":
+            op.forward(self.q, cache, lens, table, cu, S, self.groups, self.prefix_lens, 2, out=q, stream=stream)
+        elif kind == "accumulate":
+            op.accumulate(self.q, cache, lens, table, cu, S, scores, stream=stream)
+        else:
+            op.compact(cache, scores, lens, table, S, new_kv_lens=kvl, stream=stream)
+
+
+@pytest.mark.parametrize("kind", Calls.KINDS)
+def test_first_call_of_a_fresh_handle_on_a_stream_of_its_own(kind):
+    """A side stream does not wait for the default one, which is still busy when the handle is made: what the handle's
+    memory starts with is there all the same."""
+    x = Calls(0)
+    old = x.make(kind)
+    want = x.buffers()
+    x.call(kind, old, want)
+    out, side = x.buffers(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(200_000_000)  # about 0.1 s
+    fresh = x.make(kind)
+    x.call(kind, fresh, out, side)
+    assert fresh.status(side) == rpa.RPA_OK
+    torch.cuda.synchronize()
+    assert fresh.status(side) == rpa.RPA_OK
+    assert all(same(a, b) for a, b in zip(out, want))
+    # the handle's memory was not set after its first call either
+    again = x.buffers()
+    x.call(kind, fresh, again, side)
+    torch.cuda.synchronize()
+    assert all(same(a, b) for a, b in zip(again, want)) and fresh.status(side) == rpa.RPA_OK
