@@ -166,8 +166,10 @@ struct AttnParams {
     int q_f16;             // 8-bit K/V: q holds f16 values (else bf16, rounded to f16 in the kernel)
 };
 
+// (A plain load: the planner of the same call may write page_rows while the decode kernel, which then waits for the
+// published epoch, already runs.  A read-only load wants data that nobody writes in the kernel's lifetime.)
 __device__ __forceinline__ int page_row(const AttnParams& a, int seq) {
-    return a.page_rows ? __ldg(a.page_rows + seq) : seq;
+    return a.page_rows ? a.page_rows[seq] : seq;
 }
 
 struct DecParams {

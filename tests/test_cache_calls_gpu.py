@@ -87,3 +87,54 @@ def test_first_call_of_a_fresh_handle_on_a_stream_of_its_own(kind):
     x.call(kind, fresh, again, side)
     torch.cuda.synchronize()
     assert all(same(a, b) for a, b in zip(again, want)) and fresh.status(side) == rpa.RPA_OK
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8_e4m3"])
+def test_prefix_calls_of_different_groupings_in_turn(kv):
+    """Calls on one handle that follow each other without a wait, each with other groups, so that the row of the page
+    table of every virtual sequence changes from call to call: a row of the call before would give other keys."""
+    from gpu_util import TOL
+
+    scale = dict(k_scale=0.05, v_scale=0.05) if kv != "bf16" else {}
+    rng = np.random.default_rng(1)
+    S, pre = 24, 160
+    q_lens = [int(n) for n in rng.choice([1, 1, 1, 3, 20], S)]
+    b = Batch(rng, q_lens, [pre + n + int(x) for n, x in zip(q_lens, rng.integers(0, 150, S))], 16, 8, 2, 128, kv=kv, **scale)
+    for s in range(S):  # pairs of neighbours share 160 keys: any grouping of whole pairs' halves is a valid one
+        b.table[s, :10] = b.table[s - s % 2, :10]
+    cache, q = b.cache(), b.queries()
+    kvl, table, cu = b.lens()
+    args = (q, cache, kvl, table, cu, S)
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
+    groupings = []
+    for n in range(8):
+        # pair p is one group with a prefix, or two groups of one, or a part of a group without a prefix
+        cu_groups, lens = [0], []
+        for p in range(S // 2):
+            kind = int(rng.integers(0, 3))
+            if kind == 0:
+                cu_groups.append(2 * p + 2)
+                lens.append(int(rng.integers(1, pre + 1)))
+            elif kind == 1:
+                cu_groups += [2 * p + 1, 2 * p + 2]
+                lens += [int(rng.integers(0, pre + 1)), 0]
+            elif lens and lens[-1] == 0:
+                cu_groups[-1] = 2 * p + 2
+            else:
+                cu_groups.append(2 * p + 2)
+                lens.append(0)
+        groupings.append((i32(cu_groups), i32(lens), len(lens)))
+    op, plain = rpa.SharedPrefixAttention(max_groups=S, **b.cfg()), rpa.RaggedPagedAttention(**b.cfg())
+    ref = plain.forward(*args).double().cpu().numpy()
+    want = []
+    for g in groupings:
+        want.append(op.forward(*args, *g))
+        torch.cuda.synchronize()
+        # the prefix's definition is plain attention's: both are within a + r |exact| of the exact result
+        a, r = TOL[kv]
+        assert (np.abs(want[-1].double().cpu().numpy() - ref) <= 2 * (a + r * (np.abs(ref) + a) / (1 - r))).all()
+    order = [int(n) for n in rng.integers(0, 8, 60)]
+    outs = [op.forward(*args, *groupings[n]) for n in order]
+    assert op.status() == rpa.RPA_OK
+    for n, got in zip(order, outs):
+        assert torch.equal(got, want[n])
