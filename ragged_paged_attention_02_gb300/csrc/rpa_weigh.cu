@@ -180,11 +180,14 @@ __device__ __forceinline__ void load_q(const WeighParams& p, int q0, int h, int 
         }
 }
 
+// (Not a read-only load: the kernel that writes these rows, an append in front of this call, may still run when this one
+// starts.)
 __device__ __forceinline__ uint4 load_stream(const uint8_t* p, uint64_t policy) {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.L2::cache_hint.v4.b32 {%0,%1,%2,%3}, [%4], %5;\n"
+    asm volatile("ld.global.L1::no_allocate.L2::cache_hint.v4.b32 {%0,%1,%2,%3}, [%4], %5;\n"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p), "l"(policy));
+                 : "l"(p), "l"(policy)
+                 : "memory");
     return v;
 }
 __device__ __forceinline__ uint64_t l2_policy_normal() {

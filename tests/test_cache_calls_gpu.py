@@ -138,3 +138,39 @@ def test_prefix_calls_of_different_groupings_in_turn(kv):
     assert op.status() == rpa.RPA_OK
     for n, got in zip(order, outs):
         assert torch.equal(got, want[n])
+
+
+class Chain:
+    """Appends of other values to the same slots, each read by an operator right behind it: nothing of the append before
+    may be seen."""
+
+    def __init__(self, seed, q_lens, kv_lens, kv="bf16", D=128):
+        scale = dict(k_scale=0.05, v_scale=0.05) if kv != "bf16" else {}
+        b = self.b = Batch(np.random.default_rng(seed), q_lens, kv_lens, 16, 8, 2, D, kv=kv, **scale)
+        self.inputs = [[b.queries(), b.queries()[:, :2].contiguous(), b.queries()[:, :2].contiguous()] for _ in range(4)]
+        self.cache, self.lens = b.cache(), b.lens()
+        self.rope = rpa.RopeAppend(**b.cfg())
+        self.order = [int(n) for n in b.rng.integers(0, 4, 40)]
+
+    def check(self, read):
+        """read(q) -> a fresh output tensor."""
+        step = lambda n: read(self.rope.append(*self.inputs[n], self.cache, *self.lens, self.b.S))  # noqa: E731
+        want = []
+        for n in range(4):
+            torch.cuda.synchronize()
+            want.append(step(n))
+        torch.cuda.synchronize()
+        assert not torch.equal(want[0], want[1])
+        outs = [step(n) for n in self.order]
+        assert self.rope.status() == rpa.RPA_OK
+        for n, got in zip(self.order, outs):
+            assert torch.equal(got, want[n])
+
+
+@pytest.mark.parametrize("kv,D", [("bf16", 128), ("bf16", 64), ("fp8_e4m3", 256)])
+def test_weights_of_keys_that_the_call_before_wrote(kv, D):
+    """Prompts of many rows, whose logits are computed twice, from K rows that an append in front of the call wrote."""
+    x = Chain(2, [40, 200, 1], [40, 260, 90], kv=kv, D=D)
+    op = rpa.CacheEviction(budget=1, **x.b.cfg())
+    x.check(lambda q: op.accumulate(q, x.cache, *x.lens, x.b.S, torch.zeros(x.b.N, 2, 16, device="cuda")))
+    assert op.status() == rpa.RPA_OK
