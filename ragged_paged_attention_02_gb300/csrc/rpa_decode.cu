@@ -109,7 +109,12 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kvmap, const CUte
     if (p.plan_epoch >= 0) {
         // behind the prefill kernel on one stream: the planner's items are complete once it has
         // published this call's epoch
-        if (tid == 0) s_plan_ok = flag_wait(ctrl + kPlanEpoch, p.plan_epoch, ctrl, tmo) ? 1 : 0;
+        if (tid == 0) {
+            s_plan_ok = flag_wait(ctrl + kPlanEpoch, p.plan_epoch, ctrl, tmo) ? 1 : 0;
+            // K/V and q are read by bulk copies; a kernel in front of the call that writes them (an append, a compaction)
+            // lets its successors start early, so this grid may have started before it ended
+            fence_proxy_async_global();
+        }
         __syncthreads();
         if (!s_plan_ok) return;
     } else {

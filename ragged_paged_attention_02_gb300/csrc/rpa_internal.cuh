@@ -700,6 +700,10 @@ __device__ __forceinline__ bool flag_wait(const int* flag, int v, int* ctrl, uin
 __device__ __forceinline__ void fence_proxy_async_smem() {
     asm volatile("fence.proxy.async.shared::cta;\n" ::: "memory");
 }
+// What this thread has acquired of global memory is seen by the bulk copies that follow.
+__device__ __forceinline__ void fence_proxy_async_global() {
+    asm volatile("fence.proxy.async.global;\n" ::: "memory");
+}
 // 2-D / 3-D tiled tensor copy global -> shared, completing on an mbarrier.
 __device__ __forceinline__ void tma_load_2d(uint32_t dst, const void* map, uint32_t bar, int x, int y) {
     asm volatile(

@@ -174,3 +174,20 @@ def test_weights_of_keys_that_the_call_before_wrote(kv, D):
     op = rpa.CacheEviction(budget=1, **x.b.cfg())
     x.check(lambda q: op.accumulate(q, x.cache, *x.lens, x.b.S, torch.zeros(x.b.N, 2, 16, device="cuda")))
     assert op.status() == rpa.RPA_OK
+
+
+@pytest.mark.parametrize("kind", ["forward", "prefix"])
+@pytest.mark.parametrize("kv,D", [("bf16", 128), ("f16", 64), ("fp8_e4m3", 128)])
+def test_attention_of_keys_that_the_call_before_wrote(kind, kv, D):
+    """Decodes beside prompts, whose kernels run at once, over K/V rows and queries that an append in front wrote."""
+    x = Chain(3, [1, 200, 1, 60, 1], [700, 260, 90, 60, 300], kv=kv, D=D)
+    b = x.b
+    if kind == "forward":
+        op = rpa.RaggedPagedAttention(**b.cfg())
+        read = lambda q: op.forward(q, x.cache, *x.lens, b.S)  # noqa: E731
+    else:
+        op = rpa.SharedPrefixAttention(max_groups=3, **b.cfg())
+        groups, lens = (torch.tensor(v, dtype=torch.int32, device="cuda") for v in ([0, 1, 4, 5], [600, 0, 250]))
+        read = lambda q: op.forward(q, x.cache, *x.lens, b.S, groups, lens, 3)  # noqa: E731
+    x.check(read)
+    assert op.status() == rpa.RPA_OK
