@@ -350,7 +350,7 @@ void frequencies(const RpaRopeCfg& c, double* w) {
         if (c.scaling == RPA_ROPE_ROTATIONS)
             t = std::fmin(std::fmax((c.trained_len * x / kTwoPi - c.low) / (c.high - c.low), 0.0), 1.0);
         if (c.scaling == RPA_ROPE_INDEX) t = 1 - std::fmin(std::fmax((i - a) / std::fmax(b - a, 1e-3), 0.0), 1.0);
-        w[i] = x * t + x / c.factor * (1 - t);
+        w[i] = t < 1 ? x * t + x / c.factor * (1 - t) : x;  // (the factor of NONE is not checked: it may be 0)
     }
 }
 

@@ -1,0 +1,28 @@
+"""Calls of the paged cache's operators that their documentation allows or has to refuse, as far as no GPU is needed."""
+import math
+
+import numpy as np
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import ragged_paged_attention_02_gb300 as rpa  # noqa: E402
+
+CFG = dict(num_q_tokens=22, num_q_heads=4, num_kv_heads=2, head_dim=64, total_num_pages=16, page_size=16, max_num_seqs=3,
+           pages_per_seq=4, sm_scale=0.125)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    import __graft_entry__
+
+    __graft_entry__.build()
+
+
+@pytest.mark.parametrize("factor", [0.0, -1.0, 0.5, math.nan, math.inf])
+def test_the_factor_of_plain_frequencies_does_not_count(factor):
+    """Without scaling the factor is neither checked nor used."""
+    want = rpa.rope_frequencies(**CFG)
+    assert rpa.validate_rope_cfg(factor=factor, **CFG) == rpa.RPA_OK
+    got = rpa.rope_frequencies(factor=factor, **CFG)
+    assert np.isfinite(want).all() and (got == want).all()
