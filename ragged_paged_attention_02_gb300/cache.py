@@ -121,7 +121,7 @@ class _Handle:
 def make_rope_cfg(*, rotary_dim=None, rotary_offset=0, pairing="half", scaling="none", base=10000.0, factor=1.0,
                   trained_len=0, low=1.0, high=4.0, magnitude=1.0, **cfg) -> RpaRopeCfg:
     c = RpaRopeCfg()
-    c.cache = make_cfg(**cfg)
+    c.cache = make_cfg(**dict(cfg, sinks=None))  # attention's alone: an append reads none
     c.rotary_dim = c.cache.head_dim if rotary_dim is None else int(rotary_dim)
     c.rotary_offset = int(rotary_offset)
     c.pairing, c.scaling = ROPE_PAIRINGS[pairing], ROPE_SCALINGS[scaling]

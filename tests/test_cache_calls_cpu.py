@@ -7,6 +7,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import ragged_paged_attention_02_gb300 as rpa  # noqa: E402
+from ragged_paged_attention_02_gb300.cache import make_rope_cfg  # noqa: E402
 
 CFG = dict(num_q_tokens=22, num_q_heads=4, num_kv_heads=2, head_dim=64, total_num_pages=16, page_size=16, max_num_seqs=3,
            pages_per_seq=4, sm_scale=0.125)
@@ -26,3 +27,13 @@ def test_the_factor_of_plain_frequencies_does_not_count(factor):
     assert rpa.validate_rope_cfg(factor=factor, **CFG) == rpa.RPA_OK
     got = rpa.rope_frequencies(factor=factor, **CFG)
     assert np.isfinite(want).all() and (got == want).all()
+
+
+def test_sinks_of_the_attention_do_not_hinder_an_append():
+    """RopeAppend takes RaggedPagedAttention's keywords, with sinks in host memory too, as that takes them."""
+    sinks = np.linspace(-1, 1, 4).astype(np.float32)
+    assert rpa.validate_cfg(sinks=sinks, **CFG) == rpa.RPA_OK
+    assert rpa.validate_rope_cfg(sinks=sinks, **CFG) == rpa.RPA_OK
+    assert (rpa.rope_frequencies(sinks=sinks, **CFG) == rpa.rope_frequencies(**CFG)).all()
+    c = make_rope_cfg(sinks=sinks, **CFG)
+    assert not c.cache.has_sinks and not c.cache.sinks  # a host address stays out of the handle
