@@ -84,10 +84,12 @@ class _Handle:
     def _stream(self, stream, tensors=()):
         """The stream's pointer.  On another stream than the current one the tensors' memory is kept until it is done."""
         here = self._current(self._device)
-        if stream is None or stream.cuda_stream == here:
+        if stream is None:
             return here
-        if stream.device.index != self._device:
+        if stream.device.index != self._device:  # (every device's default stream has the same pointer)
             raise ValueError(f"the stream must be one of cuda:{self._device}, where the handle was made")
+        if stream.cuda_stream == here:
+            return here
         for t in tensors:
             if t is not None:
                 t.record_stream(stream)

@@ -7,7 +7,7 @@ import pytest
 torch = pytest.importorskip("torch")
 
 import ragged_paged_attention_02_gb300 as rpa  # noqa: E402
-from ragged_paged_attention_02_gb300.cache import make_rope_cfg  # noqa: E402
+from ragged_paged_attention_02_gb300.cache import RopeAppend, make_rope_cfg  # noqa: E402
 
 CFG = dict(num_q_tokens=22, num_q_heads=4, num_kv_heads=2, head_dim=64, total_num_pages=16, page_size=16, max_num_seqs=3,
            pages_per_seq=4, sm_scale=0.125)
@@ -37,3 +37,28 @@ def test_sinks_of_the_attention_do_not_hinder_an_append():
     assert (rpa.rope_frequencies(sinks=sinks, **CFG) == rpa.rope_frequencies(**CFG)).all()
     c = make_rope_cfg(sinks=sinks, **CFG)
     assert not c.cache.has_sinks and not c.cache.sinks  # a host address stays out of the handle
+
+
+class FakeStream:
+    def __init__(self, device, pointer):
+        self.device, self.cuda_stream = torch.device("cuda", device), pointer
+
+
+class FakeTensor:
+    def __init__(self):
+        self.on = []
+
+    def record_stream(self, stream):
+        self.on.append(stream)
+
+
+def test_streams_of_other_devices_are_refused():
+    """Also their default streams, whose pointer is the one of this device's."""
+    op = object.__new__(RopeAppend)
+    op._h, op._device, op._current = None, 0, lambda device: 0
+    assert op._stream(None) == 0 and op._stream(FakeStream(0, 0)) == 0
+    for pointer in (0, 77):
+        with pytest.raises(ValueError, match="cuda:0"):
+            op._stream(FakeStream(1, pointer))
+    t, side = FakeTensor(), FakeStream(0, 77)
+    assert op._stream(side, (t, None)) == 77 and t.on == [side]
