@@ -174,7 +174,8 @@ class RopeAppend(_Handle):
         for name, t, shape in (("q", q, self._q_shape), ("k", k, rows), ("v", v, rows)):
             if t is None:
                 continue
-            if t.dtype is not self._q_dtype or t.shape != shape or (T and t.stride()[1:] != (D, 1)):
+            # (one head has no distance to another)
+            if t.dtype is not self._q_dtype or t.shape != shape or (T and (t.stride(2) != 1 or (shape[1] > 1 and t.stride(1) != D))):
                 raise ValueError(f"{name} must be a {self._q_dtype} tensor {tuple(shape)} whose tokens' heads are contiguous")
         self._need_cache(kv_pages)
         self._need_lengths(kv_lens, page_indices, cu_q_lens)

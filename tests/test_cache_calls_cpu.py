@@ -62,3 +62,22 @@ def test_streams_of_other_devices_are_refused():
             op._stream(FakeStream(1, pointer))
     t, side = FakeTensor(), FakeStream(0, 77)
     assert op._stream(side, (t, None)) == 77 and t.on == [side]
+
+
+def test_one_head_may_have_any_stride():
+    """Keys and values of a single kv head kept as [head, token, D], or taken out of a wider tensor: the heads of a token
+    are contiguous whatever the stride of a dimension of one."""
+    cfg = dict(CFG, num_kv_heads=1)
+    op = object.__new__(RopeAppend)
+    op._h, op._c = None, make_rope_cfg(**cfg)
+    op._checks(op._c.cache)
+    i = lambda *n: torch.zeros(*n, dtype=torch.int32)  # noqa: E731
+    args = dict(q=torch.zeros(22, 4, 64, dtype=torch.bfloat16), kv_pages=torch.zeros(16, 16, 2, 64, dtype=torch.bfloat16), kv_lens=i(3),
+                page_indices=i(3, 4), cu_q_lens=i(4), positions=None, q_out=torch.zeros(22, 4, 64, dtype=torch.bfloat16))
+    k = torch.zeros(1, 22, 64, dtype=torch.bfloat16).transpose(0, 1)
+    assert k.stride() == (64, 22 * 64, 1)
+    v = torch.zeros(22, 3, 192, dtype=torch.bfloat16)[:, 1:2, 64:128]
+    op._check(k=k, v=v, **args)
+    for bad in (torch.zeros(22, 1, 128, dtype=torch.bfloat16)[..., ::2], torch.zeros(1, 22, 64, dtype=torch.bfloat16)):
+        with pytest.raises(ValueError):
+            op._check(k=bad, v=v, **args)
