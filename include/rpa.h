@@ -376,7 +376,8 @@ int rpa_prefix_create(const RpaCfg* cfg, int64_t max_groups, RpaPrefix** out);
  *                common (0: none).  They are read through page_indices of the group's first sequence;
  *                the other sequences' page ids of whole prefix pages are not read.  At most
  *                kv_len - q_len of each sequence with query tokens.
- *   num_groups   host, 0 <= num_groups <= max_groups (0 only with num_seqs 0)
+ *   num_groups   host, 0 <= num_groups <= max_groups (0 only with num_seqs 0; cu_groups and prefix_lens
+ *                are not read then and may be NULL)
  * Bad lengths or groups: RPA_ERR_BAD_LENGTHS, o all zero. */
 int rpa_prefix_forward(RpaPrefix* h, const void* q, const void* kv_pages, const int32_t* kv_lens,
                        const int32_t* page_indices, const int32_t* cu_q_lens, int32_t num_seqs,

@@ -576,7 +576,8 @@ int rpa_prefix_forward(RpaPrefix* h, const void* q, const void* kv_pages, const 
     const KernelSet& ks = h->ks;
     if (num_seqs < 0 || num_seqs > c.max_num_seqs) return RPA_ERR_INVALID_ARG;
     if (num_groups < 0 || num_groups > h->max_groups || (num_groups == 0 && num_seqs > 0)) return RPA_ERR_INVALID_ARG;
-    if (!kv_pages || !kv_lens || !page_indices || !cu_q_lens || !cu_groups || !prefix_lens) return RPA_ERR_INVALID_ARG;
+    if (!kv_pages || !kv_lens || !page_indices || !cu_q_lens) return RPA_ERR_INVALID_ARG;
+    if (num_groups > 0 && (!cu_groups || !prefix_lens)) return RPA_ERR_INVALID_ARG;
     if (c.num_q_tokens > 0 && (!q || !o)) return RPA_ERR_INVALID_ARG;
     if (!aligned(q, 16) || !aligned(o, 16) || !aligned(kv_pages, 16) || !aligned(kv_lens, 4) || !aligned(page_indices, 4) ||
         !aligned(cu_q_lens, 4) || !aligned(cu_groups, 4) || !aligned(prefix_lens, 4))

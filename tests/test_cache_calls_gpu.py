@@ -191,3 +191,19 @@ def test_attention_of_keys_that_the_call_before_wrote(kind, kv, D):
         read = lambda q: op.forward(q, x.cache, *x.lens, b.S, groups, lens, 3)  # noqa: E731
     x.check(read)
     assert op.status() == rpa.RPA_OK
+
+
+def test_no_sequences_and_no_groups():
+    """A step without work: the tensor of the groups' prefixes is empty, its address NULL."""
+    b = Batch(np.random.default_rng(4), [3], [20], 16, 4, 2, 64)
+    op = rpa.SharedPrefixAttention(max_groups=1, **b.cfg())
+    kvl, table, cu = b.lens()
+    none = torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert none[:0].data_ptr() == 0
+    out = torch.full((b.T, 4, 64), 7.0, dtype=torch.bfloat16, device="cuda")
+    op.forward(b.queries(), b.cache(), kvl, table, cu, 0, none, none[:0], 0, out=out)
+    assert op.status() == rpa.RPA_OK and (out == 0).all()
+    with pytest.raises(rpa.RpaError):  # sequences have groups
+        op.forward(b.queries(), b.cache(), kvl, table, cu, 1, none, none[:0], 0, out=out)
+    op.forward(b.queries(), b.cache(), kvl, table, cu, 1, torch.tensor([0, 1], dtype=torch.int32, device="cuda"), none, 1, out=out)
+    assert op.status() == rpa.RPA_OK and not (out == 0).all()
