@@ -343,7 +343,8 @@ int rpa_rope_create(const RpaRopeCfg* cfg, RpaRope** out);
  *              *_stride elements apart (slices of one fused projection), 16-byte aligned rows
  *              (RPA_KV_LATENT: k is the whole row, v is NULL)
  *   positions  device, int32 [num_q_tokens], or NULL
- *   q_out      device, [num_q_tokens, Hq, D] q_dtype, contiguous, 16-byte aligned; may be q itself
+ *   q_out      device, [num_q_tokens, Hq, D] q_dtype, contiguous, 16-byte aligned; may be q itself where q is
+ *              contiguous too, and overlaps none of the other tensors
  * The arithmetic is in 32 bits with one rounding at the end.  Angles are exact to 2^-32 of a turn at
  * any position.  Cache rows hold k / k_scale and v / v_scale (where set), rounded to nearest even;
  * the 8-bit types saturate, NaN stays NaN (int8: 0); f16 rows overflow to infinity.

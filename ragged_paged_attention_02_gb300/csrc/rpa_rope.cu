@@ -457,6 +457,8 @@ int rpa_rope_append(RpaRope* h, const void* q, int64_t q_stride, const void* k, 
         if (strides[i] < (i ? c.num_kv_heads : c.num_q_heads) * c.head_dim || strides[i] % (16 / eb) ||
             strides[i] >= (int64_t)1 << 40)
             return RPA_ERR_INVALID_ARG;
+    // in place a token's row of q is its row of q_out, or the rows of other tokens would be written over before they are read
+    if (q_out == q && c.num_q_tokens > 1 && q_stride != c.num_q_heads * c.head_dim) return RPA_ERR_INVALID_ARG;
     DeviceGuard g(h->device);
     if (!g.ok) return RPA_ERR_CUDA;
     RopeParams p;

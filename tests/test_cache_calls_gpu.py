@@ -207,3 +207,40 @@ def test_no_sequences_and_no_groups():
         op.forward(b.queries(), b.cache(), kvl, table, cu, 1, none, none[:0], 0, out=out)
     op.forward(b.queries(), b.cache(), kvl, table, cu, 1, torch.tensor([0, 1], dtype=torch.int32, device="cuda"), none, 1, out=out)
     assert op.status() == rpa.RPA_OK and not (out == 0).all()
+
+
+def test_rotation_in_place_of_a_slice_is_refused():
+    """q_out is contiguous: with q a slice of wider rows from the same address on, the rows of one token would land on
+    those of others that are still to be read."""
+    b = Batch(np.random.default_rng(5), [9], [20], 16, 4, 2, 64)
+    wide = torch.zeros(b.T * 8 * 64, dtype=torch.bfloat16, device="cuda")
+    q, q_out = wide.view(b.T, 8, 64)[:, :4], wide[:b.T * 4 * 64].view(b.T, 4, 64)
+    k, v = b.queries()[:, :2].contiguous(), b.queries()[:, :2].contiguous()
+    cache, lens = b.cache(), b.lens()
+    before = cache.clone()
+    op = rpa.RopeAppend(**b.cfg())
+    with pytest.raises(rpa.RpaError) as e:
+        op.append(q, k, v, cache, *lens, 1, q_out=q_out)
+    assert e.value.code == rpa.RPA_ERR_INVALID_ARG and torch.equal(cache, before)
+    # contiguous in place, and one token of a wider row in place, are fine
+    x = b.queries()
+    want = op.append(x.clone(), k, v, cache, *lens, 1)
+    assert same(op.append(x, k, v, cache, *lens, 1, q_out=x), want)
+    one = Batch(np.random.default_rng(6), [1], [20], 16, 4, 2, 64, tail=0)
+    op1 = rpa.RopeAppend(**one.cfg())
+    row = torch.randn(1, 8, 64, device="cuda").bfloat16()
+    want = op1.append(row[:, :4].clone(), row[:, 4:6], row[:, 6:], one.cache(), *one.lens(), 1)
+    op1.append(row[:, :4], row[:, 4:6], row[:, 6:], one.cache(), *one.lens(), 1, q_out=row[:, :4])
+    assert same(row[:, :4], want) and op1.status() == op.status() == rpa.RPA_OK
+
+
+def test_one_head_of_any_stride():
+    """Keys kept as [head, token, D] and values out of a wider tensor give what contiguous ones give."""
+    b = Batch(np.random.default_rng(7), [5, 2], [20, 70], 16, 4, 1, 64)
+    q, op = b.queries(), rpa.RopeAppend(**b.cfg())
+    k, v = b.queries()[:, :1], b.queries()[:, 1:2]
+    cache = b.cache()
+    c1, c2 = cache.clone(), cache.clone()
+    op.append(q, k.contiguous(), v.contiguous(), c1, *b.lens(), b.S)
+    op.append(q, k.transpose(0, 1).contiguous().transpose(0, 1), v, c2, *b.lens(), b.S)
+    assert same(c1, c2) and not same(c1, cache) and op.status() == rpa.RPA_OK
