@@ -411,7 +411,8 @@ int rpa_evict_create(const RpaEvictCfg* cfg, RpaEvict** out);
  * The keys of the call's own query tokens, the last q_len of each sequence, start from 0 instead of what
  * scores held.  Sums in 32 bits, in a fixed order.  Keys that no query of the call sees keep their value.
  * A page that two sequences share receives both sequences' weights in an order that is not fixed.
- * Bad lengths: RPA_ERR_BAD_LENGTHS, scores unchanged; a bad page id: its keys are left out of the softmax
+ * Bad lengths: RPA_ERR_BAD_LENGTHS, scores unchanged; so are 2^31 - 2^20 blocks of 16 (head_dim 256, 2-byte K) to 64 keys
+ * of a kv head, over all sequences, and more.  A bad page id: its keys are left out of the softmax
  * (RPA_ERR_BAD_PAGE_INDEX). */
 int rpa_evict_accumulate(RpaEvict* h, const void* q, const void* kv_pages, const int32_t* kv_lens,
                          const int32_t* page_indices, const int32_t* cu_q_lens, int32_t num_seqs, float* scores,

@@ -46,6 +46,10 @@ namespace {
 constexpr int kWarps = kWeighThreads / 32;
 constexpr uint64_t kWeighWaitNs = 1000000000ull;  // bound of a wait for copies; then RPA_ERR_TIMEOUT
 
+// Weigh items of a call: their numbers, and a warp's next one, in 31 bits (sequences may share pages, so that no memory
+// bounds their keys)
+constexpr unsigned long long kMostItems = (1ull << 31) - (1ull << 20);
+
 // The first key, rounded down to a piece boundary, that a sequence's first query token sees: pieces start there.
 __device__ __forceinline__ int first_key(const WeighParams& p, int kl, int ql) {
     return p.has_window ? max(0, kl - ql - p.window + 1) & ~(kWeighAlign - 1) : 0;
@@ -61,18 +65,20 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_weigh_plan_kernel(const W
     pdl_wait();
     if (tid == 0) s_bad = 0;
     __syncthreads();
-    unsigned long long keys = 0, none = 0;
+    unsigned long long keys = 0, most_items = 0;  // weigh items, if all logits are computed again
     for (int s = tid; s < p.S; s += kPlanThreads) {
         const int q0 = p.cu[s], q1 = p.cu[s + 1], kl = p.kv_lens[s];
         if (q0 < 0 || q1 < q0 || kl < 0 || kl > p.P * p.ps || q1 - q0 > kl || q1 > p.T) {
             s_bad = 1;
         } else {
             const long long blocks = ((long long)(q1 - q0) * p.G + kWeighRows - 1) / kWeighRows;
-            keys += (unsigned long long)(blocks * (kl - first_key(p, kl, q1 - q0))) * p.Hkv;
+            const int n_keys = kl - first_key(p, kl, q1 - q0);
+            keys += (unsigned long long)(blocks * n_keys) * p.Hkv;
+            if (blocks > 0) most_items += (unsigned long long)((n_keys + p.item_keys - 1) / p.item_keys) * p.Hkv;
         }
     }
-    block_sum64x2(keys, none, s_red);
-    if (s_bad) {
+    block_sum64x2(keys, most_items, s_red);
+    if (s_bad || most_items > kMostItems) {
         if (tid == 0) {
             p.ctrl[0] = p.ctrl[1] = p.ctrl[2] = 0;
             set_status(p.status, RPA_ERR_BAD_LENGTHS);

@@ -244,3 +244,23 @@ def test_one_head_of_any_stride():
     op.append(q, k.contiguous(), v.contiguous(), c1, *b.lens(), b.S)
     op.append(q, k.transpose(0, 1).contiguous().transpose(0, 1), v, c2, *b.lens(), b.S)
     assert same(c1, c2) and not same(c1, cache) and op.status() == rpa.RPA_OK
+
+
+def test_more_keys_than_the_weights_can_count():
+    """Sequences that share one page as often as their tables allow: 17 x 2^30 keys of 8 heads are 17 x 2^27 blocks of 64,
+    past 31 bits.  Refused, and the scores are left as they were; 2^10 keys of the same sequences are weighed."""
+    S, ps = 17, 1 << 16
+    cfg = dict(num_q_tokens=S, num_q_heads=8, num_kv_heads=8, head_dim=64, total_num_pages=1, page_size=ps, max_num_seqs=S,
+               pages_per_seq=(1 << 30) // ps, sm_scale=0.125, kv_dtype="int8", k_scale=0.02)
+    op = rpa.CacheEviction(budget=1, **cfg)
+    q = torch.randn(S, 8, 64, device="cuda").bfloat16()
+    cache = torch.randint(-100, 100, (1, ps, 16, 64), dtype=torch.int8, device="cuda")
+    table = torch.zeros(S, cfg["pages_per_seq"], dtype=torch.int32, device="cuda")
+    cu = torch.arange(S + 1, dtype=torch.int32, device="cuda")
+    scores = torch.full((1, 8, ps), 3.0, device="cuda")
+    lens = torch.full((S,), 1 << 30, dtype=torch.int32, device="cuda")
+    op.accumulate(q, cache, lens, table, cu, S, scores)
+    assert op.status() == rpa.RPA_ERR_BAD_LENGTHS and (scores == 3.0).all()
+    lens.fill_(1 << 10)
+    op.accumulate(q, cache, lens, table, cu, S, scores)
+    assert op.status() == rpa.RPA_OK and (scores[0, :, 1 << 10:] == 3.0).all() and (scores[0, :, :1 << 10] != 3.0).all()
