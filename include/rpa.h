@@ -345,8 +345,9 @@ int rpa_rope_create(const RpaRopeCfg* cfg, RpaRope** out);
  *   positions  device, int32 [num_q_tokens], or NULL
  *   q_out      device, [num_q_tokens, Hq, D] q_dtype, contiguous, 16-byte aligned; may be q itself where q is
  *              contiguous too, and overlaps none of the other tensors
- * The arithmetic is in 32 bits with one rounding at the end.  Angles are exact to 2^-32 of a turn at
- * any position.  Cache rows hold k / k_scale and v / v_scale (where set), rounded to nearest even;
+ * The arithmetic is in 32 bits with one rounding at the end.  The angle of position p is p w_i, w_i as
+ * rpa_rope_frequencies gives it, modulo a turn, exact to 2^-32 of a turn at any position; the sine then
+ * takes it as a 32-bit float, within 2^-26 of a turn near half a turn and exact near 0.  Cache rows hold k / k_scale and v / v_scale (where set), rounded to nearest even;
  * the 8-bit types saturate, NaN stays NaN (int8: 0); f16 rows overflow to infinity.
  * Rows of q_out and slots of the cache that no token of the call stands for are left as they were, as
  * are those of a sequence with bad lengths (RPA_ERR_BAD_LENGTHS); a token whose page id is bad writes

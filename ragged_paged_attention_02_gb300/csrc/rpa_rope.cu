@@ -4,10 +4,12 @@
 // part of every q and k head by its token's position, writes q in its own type and K/V rows in the
 // cache's type to the slots the page table names.
 //
-// The angle of pair i at position p is p w_i.  The handle keeps w_i / (2 pi) as a 64-bit binary
-// fraction of a turn f_i, so that p f_i mod 2^64 is the angle's fraction of a turn in one integer
-// product, exact but for f_i's own rounding (2^-65 of a turn a position, below 2^-34 over 31 bits of
-// positions; w_i itself is a double).  In 32-bit floating point the same product would be off by a
+// The angle of pair i at position p is p w_i, w_i the double that rpa_rope_frequencies gives.  The handle
+// keeps w_i / (2 pi) as a 64-bit binary fraction of a turn f_i, so that p f_i mod 2^64 is the angle's
+// fraction of a turn in one integer product, exact but for f_i's own rounding (2^-65 of a turn a position, at
+// most 2^-34 at 31 bits of position; 128-bit arithmetic makes f_i, for a quotient of doubles would be off by 2^-55.5
+// a position).  The sine takes its upper 32 bits (2^-33 of a turn) as a float, whose 24 bits cost at most
+// 2^-26 of a turn near half a turn, and nothing near 0.  In 32-bit floating point p w_i would be off by a
 // tenth of a radian at a million positions, and in 64 bits the GPU runs it at 1/64 of the rate.
 // Sines are computed once per token and pair, into shared memory, and serve all heads.
 //
@@ -354,6 +356,17 @@ void frequencies(const RpaRopeCfg& c, double* w) {
     }
 }
 
+// w / (2 pi) in units of 2^-64, to the nearest, for 0 <= w <= 1.  With w = m 2^e, m of 53 bits, it is
+// m c 2^(e - 66), c = 2^129 / pi; of the product m c (181 bits) all but the lowest 64 are kept.
+unsigned long long turns_of(double w) {
+    constexpr unsigned long long c1 = 0xa2f9836e4e441529ull, c0 = 0xfc2757d1f534ddc1ull;  // c = c1 2^64 + c0
+    int e = 0;
+    const unsigned long long m = (unsigned long long)std::ldexp(std::frexp(w, &e), 53);
+    const unsigned __int128 p = (unsigned __int128)m * c1 + (((unsigned __int128)m * c0) >> 64);
+    const int drop = 55 - e;
+    return drop > 127 ? 0ull : (unsigned long long)((p + ((unsigned __int128)1 << (drop - 1))) >> drop);
+}
+
 }  // namespace
 }  // namespace rpa
 
@@ -419,7 +432,7 @@ int rpa_rope_create(const RpaRopeCfg* cfg, RpaRope** out) {
     unsigned long long f[kMaxPairs + 1] = {};  // the status word behind them starts at 0
     frequencies(*cfg, w);
     const int n = (int)(cfg->rotary_dim / 2);
-    for (int i = 0; i < n; ++i) f[i] = (unsigned long long)std::ldexp(w[i] / kTwoPi, 64);
+    for (int i = 0; i < n; ++i) f[i] = turns_of(w[i]);
     if (cudaGetDevice(&h->device) != cudaSuccess ||
         cudaDeviceGetAttribute(&h->sms, cudaDevAttrMultiProcessorCount, h->device) != cudaSuccess ||
         cudaMalloc(&h->turns, (size_t)(n + 1) * sizeof f[0]) != cudaSuccess) {

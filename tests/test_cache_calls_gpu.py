@@ -1,5 +1,8 @@
 """Calls of the paged cache's operators that their documentation allows and that the tests of each operator's values do
 not make: a fresh handle's first call on a stream of its own, and more."""
+import math
+from fractions import Fraction
+
 import numpy as np
 import pytest
 
@@ -264,3 +267,43 @@ def test_more_keys_than_the_weights_can_count():
     lens.fill_(1 << 10)
     op.accumulate(q, cache, lens, table, cu, S, scores)
     assert op.status() == rpa.RPA_OK and (scores[0, :, 1 << 10:] == 3.0).all() and (scores[0, :, :1 << 10] != 3.0).all()
+
+
+PI = Fraction("3.14159265358979323846264338327950288419716939937510582097494459230781640628620899")
+
+
+def turns(w, p):
+    """The angle p w as a fraction of a turn in [-1/2, 1/2), exact but for the 80 digits of pi."""
+    x = Fraction(w) * int(p) / (2 * PI)
+    return x - math.floor(x + Fraction(1, 2))
+
+
+@pytest.mark.parametrize("rope", [dict(base=10000.0), dict(base=500000.0, scaling="rotations", factor=8.0, trained_len=8192)])
+def test_angles_of_far_positions(rope):
+    """Pair i turned at positions p where p w_i is just beside a whole turn: there the sine shows the angle itself.  The
+    fraction of a turn is off by 2^-34 (p times the rounding of w_i / 2 pi, 2^-65) and 2^-33 (its upper 32 bits), the sine
+    relative to its size by 2^-24 (its argument as a float) and 2 units of 2^-23 (sincospi): of angles below 2^-9 of a
+    turn 2 pi (2^-34 + 2^-33 + 2.5 2^-23 2^-9) at most."""
+    b = Batch(np.random.default_rng(8), [128], [128], 16, 1, 1, 128, q="f32")
+    w = rpa.rope_frequencies(**rope, **b.cfg())
+    pos = np.zeros(128, np.int32)
+    for i in range(64):
+        f = int(Fraction(w[i]) * (1 << 300) / (2 * PI))  # turns a position, of 300 bits
+        at, n = ((1 << 31) - 1) * f >> 300, 0  # whole turns
+        while n < 2:
+            p = (at * (1 << 300) + (1 << 289)) // f  # about 2^-11 of a turn past them
+            if p < 1 << 31 and 1 << 286 < abs((p * f + (1 << 299)) % (1 << 300) - (1 << 299)) < 1 << 291:  # 2^-14 .. 2^-9
+                pos[2 * i + n] = -p if n else p
+                n += 1
+            at -= 1
+    q = torch.zeros(128, 1, 128, device="cuda")
+    q[:, 0, :64] = 1.0  # the sine of each pair lands in its second element
+    out = torch.zeros_like(q)
+    op = rpa.RopeAppend(**rope, **b.cfg())
+    kv = torch.zeros(128, 1, 128, device="cuda")
+    op.append(q, kv, kv, b.cache(), *b.lens(), 1, positions=torch.from_numpy(pos).cuda(), q_out=out)
+    assert op.status() == rpa.RPA_OK
+    out = out.double().cpu().numpy()
+    for k in range(128):
+        want = math.sin(2 * math.pi * float(turns(w[k // 2], pos[k])))
+        assert abs(out[k, 0, 64 + k // 2] - want) <= 2 * math.pi * (2.0 ** -34 + 2.0 ** -33 + 2.5 * 2.0 ** -32), (k, pos[k])
