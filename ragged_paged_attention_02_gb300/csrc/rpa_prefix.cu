@@ -495,7 +495,7 @@ bool prefix_allocate(RpaPrefix* h) {
     const int64_t group_tiles = T / Tq + (NG < big ? NG : big) + 1, seq_tiles = T / Tq + (S < big ? S : big) + 1;
     const int64_t dec_units = S + NG + (kDecWaves * (int64_t)sms * ks.dec_bps + Hkv - 1) / Hkv + 1;
     const int64_t pf_units = group_tiles + seq_tiles + h->item_room / Hkv + 1;
-    const int64_t part = dec_units * Hkv + (pf_units * Hkv + h->item_room) * h->pf_slots;
+    const int64_t part = dec_units * Hkv + pf_units * Hkv * h->pf_slots;  // (pf_units holds the item_room pieces)
     if (part >= ((int64_t)1 << 31) / kDecRows) return false;
     h->max_dec_units = (int)dec_units;
     h->max_pf_units = (int)(ks.tc8 ? pf_units + dec_units : pf_units);

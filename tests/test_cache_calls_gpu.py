@@ -307,3 +307,19 @@ def test_angles_of_far_positions(rope):
     for k in range(128):
         want = math.sin(2 * math.pi * float(turns(w[k // 2], pos[k])))
         assert abs(out[k, 0, 64 + k // 2] - want) <= 2 * math.pi * (2.0 ** -34 + 2.0 ** -33 + 2.5 * 2.0 ** -32), (k, pos[k])
+
+
+def test_memory_of_a_shared_prefix_handle():
+    """256 tokens and sequences of 32 / 8 heads, D 128, one group: partial rows of 130 floats for (2 x 4 + 113 + 1 + 3) tiles
+    of 256 rows a kv head (113 sequences can have more than 8 rows; 3 of rounding up), (257 + 1) pieces of 16 rows a kv head,
+    and for each of the GPU's CTAs 4 tiles (one an SM) and 4 pieces (three an SM); a MB for the rest."""
+    cfg = dict(num_q_tokens=256, num_q_heads=32, num_kv_heads=8, head_dim=128, total_num_pages=64, page_size=16, max_num_seqs=256,
+               pages_per_seq=64, sm_scale=0.1)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    rows = 8 * 256 * (2 * 4 + 113 + 1 + 3) + 8 * 16 * 258 + sms * (4 * 256 + 4 * 3 * 16)
+    torch.cuda.synchronize()
+    ops = [rpa.SharedPrefixAttention(**cfg)]  # what the first handle of a process loads is no handle's
+    before = torch.cuda.mem_get_info()[0]
+    ops += [rpa.SharedPrefixAttention(**cfg) for _ in range(4)]
+    each = (before - torch.cuda.mem_get_info()[0]) / 4
+    assert each <= rows * 130 * 4 + (4 << 20), (each, rows * 130 * 4)
