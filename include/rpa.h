@@ -281,7 +281,8 @@ void rpa_destroy(RpaHandle* h);
  * rpa_create takes them, and checked as rpa_validate_cfg does) and used like
  * an RpaHandle: the same tensors and alignments, asynchronous on the given
  * stream, calls on one handle serialised on the GPU, capturable into a CUDA
- * graph after one eager call.
+ * graph after one eager call (a graph uses the handle's workspace: the handle
+ * has to outlive its replays).
  *
  * The status of these handles is sticky: each *_get_status synchronises
  * `stream`, returns the first device-detected error of the calls since the
@@ -368,8 +369,12 @@ void rpa_rope_destroy(RpaRope* h);
 typedef struct RpaPrefix RpaPrefix;
 /* Host only; 1 <= max_groups <= max_num_seqs. */
 int rpa_prefix_validate_cfg(const RpaCfg* cfg, int64_t max_groups);
-/* The handle's workspace holds float32 partial results of every query row, twice (prefix and own keys), and more for
- * prefixes cut into pieces. */
+/* The handle's workspace holds float32 partial results, rows of head_dim + 2, for the worst case of cfg.  A kv head has
+ *   128 rows (256 with 2-byte K/V of head_dim 64 and 128) a tile: two for each 128 (256) query rows of num_q_tokens, and one
+ *   for each sequence and each group that can have more than 16 query rows (8 with 2-byte K/V and Hq / Hkv <= 8);
+ *   16 rows a piece: one for each sequence and each group,
+ * and all together have four such tiles more for each prefill CTA and four pieces for each decode CTA that the GPU holds.
+ * 256 tokens and sequences of 32 query and 8 kv heads at head_dim 128 (bf16): 246 MB, of which those for the CTAs are 96. */
 int rpa_prefix_create(const RpaCfg* cfg, int64_t max_groups, RpaPrefix** out);
 /* As rpa_forward, with
  *   cu_groups    device, int32 [max_groups + 1]: group g is the sequences [cu_groups[g], cu_groups[g + 1]);
@@ -377,7 +382,8 @@ int rpa_prefix_create(const RpaCfg* cfg, int64_t max_groups, RpaPrefix** out);
  *   prefix_lens  device, int32 [max_groups]: the group's sequences have their first prefix_lens[g] keys in
  *                common (0: none).  They are read through page_indices of the group's first sequence;
  *                the other sequences' page ids of whole prefix pages are not read.  At most
- *                kv_len - q_len of each sequence with query tokens.
+ *                kv_len - q_len of each sequence with query tokens, and, of groups without any too,
+ *                0 .. pages_per_seq * page_size.
  *   num_groups   host, 0 <= num_groups <= max_groups (0 only with num_seqs 0; cu_groups and prefix_lens
  *                are not read then and may be NULL)
  * Bad lengths or groups: RPA_ERR_BAD_LENGTHS, o all zero. */
@@ -401,8 +407,14 @@ typedef struct RpaEvictCfg {
 typedef struct RpaEvict RpaEvict;
 /* Host only. */
 int rpa_evict_validate_cfg(const RpaEvictCfg* cfg);
-/* The handle's workspace holds, beside lists of kept slots, the logits of sequences of few query rows, for all
- * the keys that max_num_seqs sequences can have but at most 1 GiB (more keys: logits are computed twice). */
+/* The handle's workspace holds, for the worst case of cfg,
+ *   the logits of sequences of at most 16 query rows a kv head, for all the keys that max_num_seqs sequences can have
+ *     but at most 1 GiB (more keys: logits are computed twice);
+ *   row statistics: with B = (num_q_tokens * Hq / Hkv / 16 + max_num_seqs) * Hkv blocks of 16 rows, 512 bytes for each
+ *     of B * max(1, min(128, 2^20 / B)) pieces (at most 512 MiB up to B = 2^20);
+ *   lists of kept slots, 4 * max_num_seqs * Hkv * budget bytes, and q once more where its type is not the products'.
+ * The launches of rpa_evict_compact are shaped by max_num_seqs * Hkv and pages_per_seq * page_size: a handle made for
+ * many more sequences, or longer ones, than a call has is slower at it than one made for that call. */
 int rpa_evict_create(const RpaEvictCfg* cfg, RpaEvict** out);
 
 /* Add to scores the softmax weights (rpa_forward's: causal and window masks, soft cap, sinks in the

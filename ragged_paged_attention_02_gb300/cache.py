@@ -4,7 +4,8 @@ Argument checks and marshalling only, as in ``binding``: every step of the
 computation runs in the CUDA library.  Each class owns one library handle,
 made on the current device from the keywords of ``RaggedPagedAttention``
 (shapes, types and scales of the cache and of q) and its own.  Calls on one
-object share its workspace and must be serialised on the GPU.
+object share its workspace and must be serialised on the GPU; a CUDA graph of
+its calls uses that workspace too, so the object has to outlive the replays.
 """
 
 from __future__ import annotations
@@ -273,7 +274,9 @@ class CacheEviction(_Handle):
         """Cut every sequence to the budget and return its new length (new_kv_lens, int32 [max_num_seqs]).
 
         The kept keys' rows and scores move, in order, to the first slots of new_page_indices' pages (default:
-        page_indices, in place, where rows wait for each other: fresh pages are faster).  ``kept`` (int32 [max_num_seqs, Hkv, budget]) receives the slots they had.
+        page_indices, in place, where rows wait for each other: fresh pages are faster).  ``kept`` (int32
+        [max_num_seqs, Hkv, budget]) receives the slots they had.  An object made for about as many and as long
+        sequences as a call has is fastest.
         """
         if new_page_indices is None:
             new_page_indices = page_indices

@@ -12,7 +12,7 @@
 //            shared memory.  Then one ordered pass lists the kept slots: each warp lists a run of
 //            neighbouring keys, so that one scan over the warps and CTAs gives every warp its place and its
 //            share of the ties, which go to the lowest slots.  A digit whose bin is wanted whole is the last.  Bound by its rounds of waits (three digits,
-//            a few microseconds each), so a cluster is as large as leaves no SM without one.
+//            a few microseconds each), so few units take large clusters, as long as two thirds of the SMs hold them.
 //   move     K and V of a head are neighbours in a slot, a row is one copy of 2 D elements.  A CTA takes as
 //            many rows a round as its registers hold (32 to 256: eight 16-byte vectors a thread), and looks
 //            the next round's up beside the reads.  Bound by reading and writing those rows.  Onto fresh
@@ -20,6 +20,8 @@
 //            head's rows move in ascending order: kept row i sits at slot j >= i and goes to slot i, so that
 //            a row may be written once all rows up to it are read, and what is read later is never written
 //            before.  A cluster of up to 8 CTAs takes a head and meets between reads and writes.
+//
+// Both launches are shaped by what the handle was made for (max_num_seqs, pages_per_seq), not by a call's num_seqs.
 //
 // 64 sequences of up to 8 k keys cut to 2 k (8 heads, D 128, bf16; 1.09 GB): 194 us, of which select 23 and move
 // 170 (6.4 TB/s); in place 229.  Two of 100 k keys cut to 16 k (e4m3, 139 MB): 48 us, 23 and 25; in place 84 (16
@@ -432,7 +434,7 @@ __global__ void __launch_bounds__(kMoveThreads, IN_PLACE ? kPlaceCtas : kMoveCta
 
 // Clusters and shared memory of select for `units` (sequence, kv head) pairs of up to max_keys competing keys
 cudaError_t compact_prepare(int64_t units, int max_keys, int sms, int* cluster, int* move_cluster, int* cached) {
-    // as many CTAs a unit as two an SM allow, of 2 k keys at least
+    // as many CTAs a unit as two thirds of the SMs hold, one each, with 2 k keys at least
     int c = 1;
     while (c < kMaxCluster && 3 * units * (2 * c) <= 2 * sms && max_keys / (2 * c) >= 2048) c *= 2;
     *cluster = c;

@@ -5,8 +5,9 @@
 
 namespace rpa {
 
-// j / d for 0 <= j < 2^31 by one 32-bit high product: with l = ceil(log2 d) and
-// m = floor(2^32 (2^l - d) / d) + 1, j / d = (umulhi(m, j) + j) >> l (the sum stays below 2^32).
+// j / d for 0 <= j < 2^31 by one 32-bit high product (T. Granlund and P. L. Montgomery, Division by Invariant Integers
+// using Multiplication, 1994): with l = ceil(log2 d) and m = floor(2^32 (2^l - d) / d) + 1,
+// j / d = (umulhi(m, j) + j) >> l (the sum stays below 2^32).
 struct FastDiv {
     uint32_t d, m, l;
     void set(uint32_t div) {

@@ -13,6 +13,10 @@
 // prefix's tiles split over the keys as well.  Every item writes a partial; one merge takes each row's
 // partials from both sources.
 //
+// As in rpa_forward the probabilities are rounded to the type of V's products (bf16 for bf16 K/V, else f16) before they meet
+// V, and a q of another type than the products' is rounded to it; sums, maxima and partials are 32-bit.  With bf16 K/V and
+// o a result is off by 2.2e-3 (root mean square, relative), of which 1.66e-3 are o's own rounding; with 8-bit K/V by 1.67e-3.
+//
 // How many pieces a prefix is cut into: tiles x kv heads are few (a batch of 64 and 8 heads has 8), so
 // pieces fill the SMs; but each costs a pipeline ramp and 256 partial rows of D floats, written and read
 // back.  The planner takes the number of pieces that makes  waves x (keys of a piece + kPieceCost)  least; where
