@@ -15,7 +15,7 @@
  *   qh reads kv head qh / (Hq/Hkv).  The logit of key j is
  *   sm_scale * <q, k_scale*K_j>, soft-capped as cap*tanh(x/cap) when a cap is
  *   set (before masking); key j is masked when j >= kv_len, when causal and
- *   j > p, or when p - sliding_window >= j.  The output is the softmax-weighted
+ *   j > p, or when p - sliding_window >= j and j >= first_keys.  The output is the softmax-weighted
  *   sum of v_scale*V_j, cast to the q dtype.
  *
  * Conventions for every entry point:
@@ -97,7 +97,12 @@ typedef struct RpaCfg {
     int32_t has_sliding_window;
     int32_t has_sinks;       /* 1: attention sinks, read from `sinks` */
     int32_t kv_layout;       /* RpaKvLayout: RPA_KV_SPLIT (the page's layout, default) or RPA_KV_LATENT */
-    int32_t reserved;        /* set to 0 */
+    union {
+        int32_t first_keys;  /* with has_sliding_window: the first keys of a sequence, which the window does not hide
+                                (0: none; a value without a window gives RPA_ERR_INVALID_ARG).  Page ids of the pages
+                                between them and the window of a call's first token are not used */
+        int32_t reserved;    /* the field's name where there are none: 0 */
+    };
     int64_t v_head_dim;      /* RPA_KV_SPLIT: 0 or head_dim.  RPA_KV_LATENT: the width of V and o */
     const float* sinks;      /* when has_sinks: device, [num_q_heads] fp32, 4-byte aligned; the
                                 sink logit of each query head (the "from_qwen_ops.rs" page,
@@ -397,7 +402,7 @@ void rpa_prefix_destroy(RpaPrefix* h);
 /* Eviction by accumulated attention weight.  scores: device, float32 [total_num_pages, Hkv, page_size],
  * 16-byte aligned, beside the cache: what each cached key of each kv head has received. */
 typedef struct RpaEvictCfg {
-    RpaCfg cache;     /* RPA_KV_SPLIT, pages_per_seq * page_size <= 2^30 */
+    RpaCfg cache;     /* RPA_KV_SPLIT, no first_keys, pages_per_seq * page_size <= 2^30 */
     int64_t budget;   /* keys a sequence keeps, 1 .. pages_per_seq * page_size */
     int64_t protect;  /* the first keys, never evicted */
     int64_t recent;   /* the last keys, never evicted; protect + recent <= budget */

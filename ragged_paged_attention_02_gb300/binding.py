@@ -57,7 +57,12 @@ RPA_OPT_PLAN_EARLY = 5
 RPA_OPT_TEST_STALL_PRODUCER = 100
 
 
+class _FirstKeys(ctypes.Union):
+    _fields_ = [("first_keys", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 class RpaCfg(ctypes.Structure):
+    _anonymous_ = ("_first",)
     _fields_ = [
         ("num_q_tokens", ctypes.c_int64), ("num_q_heads", ctypes.c_int64),
         ("num_kv_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64),
@@ -70,7 +75,7 @@ class RpaCfg(ctypes.Structure):
         ("has_soft_cap", ctypes.c_int32), ("has_k_scale", ctypes.c_int32),
         ("has_v_scale", ctypes.c_int32), ("is_causal", ctypes.c_int32),
         ("has_sliding_window", ctypes.c_int32), ("has_sinks", ctypes.c_int32),
-        ("kv_layout", ctypes.c_int32), ("reserved", ctypes.c_int32),
+        ("kv_layout", ctypes.c_int32), ("_first", _FirstKeys),
         ("v_head_dim", ctypes.c_int64), ("sinks", ctypes.c_void_p),
     ]
 
@@ -189,7 +194,7 @@ def _sinks_pointer(sinks, host_ok):
 def make_cfg(*, num_q_tokens, num_q_heads, num_kv_heads, head_dim, total_num_pages, page_size,
              max_num_seqs, pages_per_seq, sm_scale, kv_dtype="bf16", soft_cap=None, k_scale=None,
              v_scale=None, is_causal=True, sliding_window=None, mask_value=MASK_VALUE, sinks=None,
-             q_dtype="bf16", kv_layout="split", v_head_dim=None, _host_ok=False, **_ignored) -> RpaCfg:
+             q_dtype="bf16", kv_layout="split", v_head_dim=None, first_keys=0, _host_ok=False, **_ignored) -> RpaCfg:
     c = RpaCfg()
     c.num_q_tokens, c.num_q_heads, c.num_kv_heads = int(num_q_tokens), int(num_q_heads), int(num_kv_heads)
     c.head_dim, c.total_num_pages, c.page_size = int(head_dim), int(total_num_pages), int(page_size)
@@ -204,6 +209,7 @@ def make_cfg(*, num_q_tokens, num_q_heads, num_kv_heads, head_dim, total_num_pag
     c.has_v_scale, c.v_scale = (0, 1.0) if v_scale is None else (1, float(v_scale))
     c.is_causal = 1 if is_causal else 0
     c.has_sliding_window, c.sliding_window = (0, 0) if sliding_window is None else (1, int(sliding_window))
+    c.first_keys = int(first_keys or 0)
     ptr = _sinks_pointer(sinks, _host_ok)
     c.has_sinks, c.sinks = (0, None) if ptr is None else (1, ptr)
     c.kv_layout = KV_LAYOUTS[kv_layout]
@@ -238,7 +244,9 @@ class RaggedPagedAttention:
       cu_q_lens    [max_num_seqs + 1] int32
     and returns o [num_q_tokens, Hq, Dv] of q's dtype (Dv = D, or v_head_dim for
     kv_layout="latent").  ``sinks`` (optional) is a
-    float32 [Hq] array or CUDA tensor of attention-sink logits.
+    float32 [Hq] array or CUDA tensor of attention-sink logits.  With
+    ``sliding_window`` the first ``first_keys`` keys of a sequence stay visible
+    in front of the window.
     """
 
     def __init__(self, **cfg):

@@ -145,14 +145,17 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kvmap, const CUte
             const int kl = a.kv_lens[item.seq];
             const int* ptab = a.page_indices + (size_t)page_row(a, item.seq) * a.P;
             const int key0 = item.kv_begin - (item.kv_begin & (BR - 1));
-            const int nst = (item.kv_end - key0 + kKS - 1) / kKS;
+            const int nst0 = first_tiles(a, item, kKS);  // stages of the first keys
+            const int nst = nst0 + (item.kv_end - key0 + kKS - 1) / kKS;
             // page ids of 32 consecutive logical pages, one per lane
-            int win0 = key0 / ps;
+            int win0 = (nst0 ? 0 : key0) / ps;
             int win = (win0 + lane < a.P) ? __ldg(ptab + win0 + lane) : 0;
             for (int st = 0; st < nst && ok; ++st) {
-                const int k_stage = key0 + st * kKS;
+                const bool fs = st < nst0;
+                const int k_stage = fs ? st * kKS : key0 + (st - nst0) * kKS;
+                const int kv_begin = fs ? 0 : item.kv_begin, kv_end = fs ? a.first : item.kv_end;
                 // make sure the page-id window covers this stage
-                const int lp_last = min(k_stage + kKS - 1, item.kv_end - 1) / ps;
+                const int lp_last = min(k_stage + kKS - 1, kv_end - 1) / ps;
                 if (lp_last - win0 >= 32) {
                     win0 = k_stage / ps;
                     win = (win0 + lane < a.P) ? __ldg(ptab + win0 + lane) : 0;
@@ -167,7 +170,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kvmap, const CUte
                 const int k0 = k_stage + lane * BR;
                 const int lp = k0 / ps;
                 const int pg = __shfl_sync(0xffffffffu, win, (lp - win0) & 31);
-                const bool want = lane < runs && k0 < item.kv_end && k0 + BR > item.kv_begin;
+                const bool want = lane < runs && k0 < kv_end && k0 + BR > kv_begin;
                 const bool good = (unsigned)pg < (unsigned)a.N;
                 const int n_issue = __popc(__ballot_sync(0xffffffffu, want && good));
                 if (__any_sync(0xffffffffu, want && !good)) {
@@ -185,8 +188,8 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kvmap, const CUte
                     m[mQStart] = q_start;
                     m[mQl] = ql;
                     m[mKl] = kl;
-                    m[mKvBegin] = item.kv_begin;
-                    m[mKvEnd] = item.kv_end;
+                    m[mKvBegin] = kv_begin;
+                    m[mKvEnd] = kv_end;
                     m[mPart] = item.part;
                     m[mTok0] = item.tok0;
                     m[mNtok] = item.ntok;
@@ -341,7 +344,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kvmap, const CUte
                     if (need_mask) {
                         const int j = kw + nb * 8 + (lane & 3) * 2 + (e & 1);
                         const bool okk = j >= kv_begin && j < kv_end && (!a.causal || j <= pos[ri]) &&
-                                         (!a.has_window || j > pos[ri] - a.window);
+                                         (!a.has_window || j > pos[ri] - a.window || j < a.first);
                         x = okk ? x : -INFINITY;
                     }
                     sacc[nb][e] = x;
@@ -587,7 +590,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kvmap, const CUte
                 if (need_mask) {
                     const int j = kw + g + 8 * (e >> 1);
                     const bool okk = j >= kv_begin && j < kv_end && (!a.causal || j <= pos[ri]) &&
-                                     (!a.has_window || j > pos[ri] - a.window);
+                                     (!a.has_window || j > pos[ri] - a.window || j < a.first);
                     x = okk ? x : -INFINITY;
                 }
                 sacc[e] = x;

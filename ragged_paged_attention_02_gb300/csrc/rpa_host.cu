@@ -121,7 +121,7 @@ int rpa_validate_cfg(const RpaCfg* c) {
     if (c->has_v_scale && !is_finite(c->v_scale)) return RPA_ERR_INVALID_ARG;
     if (c->has_sliding_window && c->sliding_window < 1) return RPA_ERR_INVALID_ARG;
     if (c->has_sinks && (!c->sinks || !aligned(c->sinks, 4))) return RPA_ERR_INVALID_ARG;
-    if (c->reserved != 0) return RPA_ERR_INVALID_ARG;
+    if (c->first_keys < 0 || (c->first_keys > 0 && !c->has_sliding_window)) return RPA_ERR_INVALID_ARG;
     if (c->num_q_heads % c->num_kv_heads) return RPA_ERR_UNSUPPORTED;
     const int64_t G = c->num_q_heads / c->num_kv_heads;
     if (c->kv_layout == RPA_KV_LATENT) {

@@ -110,6 +110,7 @@ struct PlanParams {
     int G;           // q heads per kv head
     int P, ps;       // pages_per_seq, page_size
     int causal, has_window, window;
+    int first;       // with a window: the first keys of a sequence, visible in front of it
     int dec_rows;    // rows of a decode tile
     int pf_tokens;   // query tokens of a prefill tile
     int dec_slots;   // resident decode CTAs (all SMs)
@@ -149,6 +150,7 @@ struct AttnParams {
     const int* cu_q_lens;
     int T, Hq, Hkv, G, D, ps, P, N;
     int causal, has_window, window, has_cap;
+    int first;          // with a window: the first keys of a sequence, visible in front of it
     float qk_log2;      // sm_scale * k_scale * log2(e)  (no cap)
     float cap_exp;      // 2 * sm_scale * k_scale / cap * log2(e)
     float cap_log2;     // cap * log2(e)
@@ -170,6 +172,13 @@ struct AttnParams {
 // published epoch, already runs.  A read-only load wants data that nobody writes in the kernel's lifetime.)
 __device__ __forceinline__ int page_row(const AttnParams& a, int seq) {
     return a.page_rows ? a.page_rows[seq] : seq;
+}
+
+// Tiles of `tile` keys that piece 0 of a windowed unit spends on the sequence's first keys, in front of those of
+// [kv_begin, kv_end).  The planner leaves a gap behind the first keys only where no row of the unit sees keys of it; a unit
+// without a gap starts at key 0.
+__device__ __forceinline__ int first_tiles(const AttnParams& a, const Item& item, int tile) {
+    return item.piece == 0 && item.kv_begin > a.first && a.first > 0 ? (a.first + tile - 1) / tile : 0;
 }
 
 struct DecParams {
@@ -269,7 +278,7 @@ struct KernelSet {
     int q_conv_f16;      // ... to f16 (else bf16)
     int q_f16;           // 8-bit K/V: the q the kernels read holds f16 values
     int tc, tc8;         // prefill on the tensor-memory kernel for 2-byte / 8-bit K/V
-    int dec_rows, pf_tokens, Tt, BR, br_shift, window;
+    int dec_rows, pf_tokens, Tt, BR, br_shift, window, first;
     float qk_log2, cap_exp, cap_log2, v_scale;
     int sms, dec_bps, pf_bps;
     int max_dec_units, max_pf_units, max_units, max_part, max_comb;

@@ -106,6 +106,7 @@ void kernels_choose(const RpaCfg& c, int sms, KernelSet* ks) {
     ks->cap_log2 = c.has_soft_cap ? (float)(c.soft_cap * kLog2e) : 0.f;
     ks->v_scale = c.has_v_scale ? c.v_scale : 1.f;
     ks->window = c.has_sliding_window ? (int)(c.sliding_window > 0x7fffffff ? 0x7fffffff : c.sliding_window) : 0;
+    ks->first = c.has_sliding_window ? c.first_keys : 0;
     ks->BR = 64;
     while ((int)(c.page_size % ks->BR)) ks->BR >>= 1;
     ks->br_shift = 0;
@@ -207,6 +208,7 @@ AttnParams attn_params(const RpaCfg& c, const KernelSet& ks, const Workspace& ws
     ap.causal = c.is_causal ? 1 : 0;
     ap.has_window = c.has_sliding_window ? 1 : 0;
     ap.window = ks.window;
+    ap.first = ks.first;
     ap.has_cap = c.has_soft_cap ? 1 : 0;
     ap.qk_log2 = ks.qk_log2;
     ap.cap_exp = ks.cap_exp;
@@ -379,6 +381,7 @@ int enqueue_forward(const RpaCfg& c, const KernelSet& ks, const Workspace& ws, M
     pp.causal = c.is_causal ? 1 : 0;
     pp.has_window = c.has_sliding_window ? 1 : 0;
     pp.window = ks.window;
+    pp.first = ks.first;
     pp.dec_rows = ks.dec_rows;
     pp.pf_tokens = ks.pf_tokens;
     pp.dec_slots = ks.sms * ks.dec_bps;

@@ -20,7 +20,9 @@
 //
 // The key range of a unit is the band its rows can see (page: flashAttention
 // row_ids / col_ids masks): causal rows end at position p, windowed rows start
-// after p - sliding_window.  Everything here is integer and deterministic.
+// after p - sliding_window.  With visible first keys a unit whose rows all start
+// further back than they end has those first keys in front of its range (its piece
+// 0, when it is split).  Everything here is integer and deterministic.
 #include "rpa_block.cuh"
 
 namespace rpa {
@@ -39,7 +41,17 @@ __device__ __forceinline__ void key_band(int kl, int ql, int i0, int i1, const P
     const int p_hi = kl - ql + i1 - 1;
     hi = p.causal ? min(kl, p_hi + 1) : kl;
     lo = p.has_window ? max(0, p_lo - p.window + 1) : 0;
+    if (lo <= p.first) lo = 0;  // no gap behind the first keys
     if (hi < lo) hi = lo;
+}
+
+// Keys of a unit's cost that stand for the first keys, where a gap follows them (whole tiles of them).
+__device__ __forceinline__ int first_cost(int lo, const PlanParams& p) {
+    return p.first > 0 && lo > 0 ? (p.first + kChunkAlign - 1) / kChunkAlign * kChunkAlign : 0;
+}
+// ... and how much shorter a split sequence's piece 0, which has the first keys too, is for them.
+__device__ __forceinline__ int first_shift(int lo, int chunk, const PlanParams& p) {
+    return min(first_cost(lo, p), chunk - kChunkAlign);
 }
 
 __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p) {
@@ -94,7 +106,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
                 key_band(kl, ql, 0, ql, p, lo, hi);
                 cls = 1;
                 cnt = hi - lo;
-                my_total += (unsigned long long)cnt * (unsigned long long)p.Hkv;
+                my_total += (unsigned long long)(cnt + first_cost(lo, p)) * (unsigned long long)p.Hkv;
             } else {
                 cls = 2;
                 cnt = (ql + Tq - 1) / Tq;
@@ -103,8 +115,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
                 for (int k = 0; k < cnt; ++k) {
                     int lo, hi;
                     key_band(kl, ql, k * Tq, min(ql, (k + 1) * Tq), p, lo, hi);
-                    keys += (unsigned long long)(hi - lo);
-                    wmax = max(wmax, hi - lo);
+                    const int c = hi - lo + first_cost(lo, p);
+                    keys += (unsigned long long)c;
+                    wmax = max(wmax, c);
                 }
                 my_pf_keys += keys;
                 s_comb[s] = wmax;  // the sequence's heaviest unit (sort weight); combine offsets are decode-only
@@ -180,7 +193,15 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
         const int s = base + tid;
         int du = 0, pu = 0, pa = 0, cb = 0, pp = 0;
         if (s < S) {
-            const int cls = s_cls[s], cnt = s_cnt[s];
+            const int cls = s_cls[s];
+            int cnt = s_cnt[s];
+            if (cls == 1 && p.first > 0) {
+                // piece k is keys k chunk .. of an axis on which the first keys come before the band
+                int lo, hi;
+                key_band(s_kl[s], s_q0[s + 1] - s_q0[s], 0, s_q0[s + 1] - s_q0[s], p, lo, hi);
+                cnt += first_shift(lo, chunk, p);
+                s_cnt[s] = cnt;
+            }
             if (cls == 1) {
                 du = (cnt + chunk - 1) / chunk;
                 pp = cnt % chunk != 0 ? 1 : 0;  // a last piece shorter than the chunk
@@ -244,12 +265,13 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
             int lo, hi;
             key_band(kl, ql, 0, ql, p, lo, hi);
             const int pieces = (s_cnt[s] + chunk - 1) / chunk;
-            const int kb = lo + k * chunk;
-            const int ke = min(hi, kb + chunk);
+            const int at = lo + k * chunk - first_shift(lo, chunk, p);  // (piece 0 of a unit with a gap: before lo)
+            const int kb = max(lo, at);
+            const int ke = min(hi, at + chunk);
             d[0] = s; d[1] = 0; d[2] = ql; d[3] = kb; d[4] = ke;
             d[5] = pieces > 1 ? s_part[s] : -1;
             d[6] = k; d[7] = pieces;
-            cost = ke - kb;
+            cost = ke - at;
             cls_bit = 0;
             pos = cost == chunk ? (s_dend[s] - pieces - s_ppre[s]) + k : n_full + s_ppre[s];
         } else {
@@ -263,7 +285,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
             key_band(kl, ql, t0, t0 + nt, p, lo, hi);
             d[0] = s; d[1] = t0; d[2] = nt; d[3] = lo; d[4] = hi;
             d[5] = -1; d[6] = 0; d[7] = 1;
-            cost = hi - lo;
+            cost = hi - lo + first_cost(lo, p);
             wseq = s_comb[s];
             cls_bit = 1;
             pos = u;

@@ -50,7 +50,7 @@ constexpr int kProducer = 8, kMma = 9;
 constexpr int kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.f;  // rescale O when the row max grows by more than 2^8
 
-enum TcMeta : int { tSeq = 0, tHead, tQStart, tQl, tKl, tKvBegin, tKvEnd, tTok0, tNtok, tNt, tKey0, tStop, tPart };
+enum TcMeta : int { tSeq = 0, tHead, tQStart, tQl, tKl, tKvBegin, tKvEnd, tTok0, tNtok, tNt, tKey0, tStop, tPart, tNt0 };
 
 template <int D>
 struct TcGeom {
@@ -165,7 +165,8 @@ __global__ void __launch_bounds__(kThreads, 1) rpa_prefill_tc(const __grid_const
             const int kl = a.kv_lens[item.seq];
             const int* ptab = a.page_indices + (size_t)page_row(a, item.seq) * a.P;
             const int key0 = item.kv_begin - (item.kv_begin & (BR - 1));
-            const int nt = (item.kv_end - key0 + kBN - 1) / kBN;
+            const int nt0 = first_tiles(a, item, kBN);  // tiles of the first keys
+            const int nt = nt0 + (item.kv_end - key0 + kBN - 1) / kBN;
             if (lane == 0) {
                 meta[tSeq] = item.seq;
                 meta[tHead] = item.head;
@@ -178,6 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1) rpa_prefill_tc(const __grid_const
                 meta[tNtok] = item.ntok;
                 meta[tPart] = item.part;
                 meta[tNt] = nt;
+                meta[tNt0] = nt0;
                 meta[tKey0] = key0;
                 meta[tStop] = 0;
             }
@@ -193,11 +195,13 @@ __global__ void __launch_bounds__(kThreads, 1) rpa_prefill_tc(const __grid_const
                             q_start + item.tok0 + tile * Th);
             }
             qph ^= 1u;
-            int win0 = key0 / ps;
+            int win0 = (nt0 ? 0 : key0) / ps;
             int win = (win0 + lane < a.P) ? __ldg(ptab + win0 + lane) : 0;
             for (int t = 0; t < nt && ok; ++t) {
-                const int k_tile = key0 + t * kBN;
-                const int lp_last = min(k_tile + kBN - 1, item.kv_end - 1) / ps;
+                const bool ft = t < nt0;
+                const int k_tile = ft ? t * kBN : key0 + (t - nt0) * kBN;
+                const int kv_begin = ft ? 0 : item.kv_begin, kv_end = ft ? a.first : item.kv_end;
+                const int lp_last = min(k_tile + kBN - 1, kv_end - 1) / ps;
                 if (lp_last - win0 >= 32) {
                     win0 = k_tile / ps;
                     win = (win0 + lane < a.P) ? __ldg(ptab + win0 + lane) : 0;
@@ -215,7 +219,7 @@ __global__ void __launch_bounds__(kThreads, 1) rpa_prefill_tc(const __grid_const
                     const int k0 = k_tile + b * BR;
                     const int lp = k0 / ps;
                     const int pg = __shfl_sync(0xffffffffu, win, (lp - win0) & 31);
-                    if (tk >= tasks || k0 >= item.kv_end || k0 + BR <= item.kv_begin) return 0;
+                    if (tk >= tasks || k0 >= kv_end || k0 + BR <= kv_begin) return 0;
                     if ((unsigned)pg >= (unsigned)a.N) return 2;
                     x = (2 * item.head + kv) * D + cb * 64;
                     y = pg * ps + (k0 - lp * ps);
@@ -366,8 +370,8 @@ __global__ void __launch_bounds__(kThreads, 1) rpa_prefill_tc(const __grid_const
             if (!mbar_wait(smem_u32(&q_full), qph, ctrl, tmo)) break;
             const int stop = meta[tStop];
             const int head = meta[tHead], q_start = meta[tQStart], ql = meta[tQl], kl = meta[tKl];
-            const int kv_begin = meta[tKvBegin], kv_end = meta[tKvEnd], tok0 = meta[tTok0];
-            const int ntok = meta[tNtok], nt = meta[tNt], key0 = meta[tKey0], part = meta[tPart];
+            const int it_begin = meta[tKvBegin], it_end = meta[tKvEnd], tok0 = meta[tTok0];
+            const int ntok = meta[tNtok], nt = meta[tNt], key0 = meta[tKey0], part = meta[tPart], nt0 = meta[tNt0];
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&meta_free));
             if (stop) break;
@@ -386,7 +390,9 @@ __global__ void __launch_bounds__(kThreads, 1) rpa_prefill_tc(const __grid_const
                     break;
                 }
                 tc_fence_after();
-                const int k_lo = key0 + t * kBN;
+                const bool ft = t < nt0;
+                const int k_lo = ft ? t * kBN : key0 + (t - nt0) * kBN;
+                const int kv_begin = ft ? 0 : it_begin, kv_end = ft ? a.first : it_end;
                 const bool partial = k_lo < kv_begin || k_lo + kBN > kv_end;
                 const bool need_mask = partial || (a.causal && k_lo + kBN - 1 > pos_lo) ||
                                        (a.has_window && k_lo <= pos_hi - a.window);
@@ -462,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1) rpa_prefill_tc(const __grid_const
                                     : v * a.qk_log2;
                             const int j = k_lo + c * 32 + i;
                             const bool okk = j >= kv_begin && j < kv_end && (!a.causal || j <= pos) &&
-                                             (!a.has_window || j > pos - a.window);
+                                             (!a.has_window || j > pos - a.window || j < a.first);
                             v = (okk || !need_mask) ? v : -INFINITY;
                             mt = fmaxf(mt, v);
                             sv[i] = __float_as_uint(v);

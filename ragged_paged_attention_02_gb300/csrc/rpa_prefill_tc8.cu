@@ -66,7 +66,7 @@ constexpr float kRescaleLog2 = 8.f;
 constexpr uint32_t kIssueNapNs = 100;  // longest suspension of the MMA thread's idle wait
 constexpr int kMaxRaw = 8;             // raw 8-bit stages (the ring at D 64)
 
-enum Meta8 : int { eSeq = 0, eHead, eQStart, eQl, eKl, eKvBegin, eKvEnd, eTok0, eNtok, eNt, eKey0, eStop, ePart };
+enum Meta8 : int { eSeq = 0, eHead, eQStart, eQl, eKl, eKvBegin, eKvEnd, eTok0, eNtok, eNt, eKey0, eStop, ePart, eNt0 };
 
 template <int D, bool DIRECT>
 struct G8 {
@@ -146,9 +146,9 @@ __device__ __forceinline__ void store_rows(const uint4* v, uint8_t* dst, int cw,
 }
 
 // Logits of N keys of a row in the log2 domain, in place: scale (or soft cap), then keys
-// outside [lo, hi] (relative to the first) to -inf; returns their max.
+// outside [lo, hi] but for those below `first` (all relative to the first key of the N) to -inf; returns their max.
 template <bool CAP, bool MASK, int N>
-__device__ __forceinline__ float tile_logits(uint32_t* sv, float qk, float capl, float capt, int lo, int hi) {
+__device__ __forceinline__ float tile_logits(uint32_t* sv, float qk, float capl, float capt, int lo, int hi, int first) {
     float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
     const uint64_t qk2 = f32x2(qk, qk), capl2 = f32x2(capl, capl), capt2 = f32x2(capt, capt);
 #pragma unroll
@@ -163,8 +163,8 @@ __device__ __forceinline__ float tile_logits(uint32_t* sv, float qk, float capl,
             f32x2_split(fmul2(v2, qk2), v0, v1);
         }
         if constexpr (MASK) {
-            v0 = (i >= lo && i <= hi) ? v0 : -INFINITY;
-            v1 = (i + 1 >= lo && i + 1 <= hi) ? v1 : -INFINITY;
+            v0 = ((i >= lo || i < first) && i <= hi) ? v0 : -INFINITY;
+            v1 = ((i + 1 >= lo || i + 1 < first) && i + 1 <= hi) ? v1 : -INFINITY;
         }
         m4[(i >> 1) & 3] = fmax3(m4[(i >> 1) & 3], v0, v1);
         sv[i] = __float_as_uint(v0);
@@ -312,7 +312,8 @@ __global__ void __launch_bounds__(kRegBoundThreads, 1) rpa_prefill_tc8(const __g
             const int kl = a.kv_lens[item.seq];
             const int* ptab = a.page_indices + (size_t)page_row(a, item.seq) * a.P;
             const int key0 = item.kv_begin - (item.kv_begin & (BR - 1));
-            const int nt = (item.kv_end - key0 + kBN - 1) / kBN;
+            const int nt0 = first_tiles(a, item, kBN);  // tiles of the first keys
+            const int nt = nt0 + (item.kv_end - key0 + kBN - 1) / kBN;
             if (lane == 0) {
                 int* m = meta[ms];
                 m[eSeq] = item.seq;
@@ -325,6 +326,7 @@ __global__ void __launch_bounds__(kRegBoundThreads, 1) rpa_prefill_tc8(const __g
                 m[eTok0] = item.tok0;
                 m[eNtok] = item.ntok;
                 m[eNt] = nt;
+                m[eNt0] = nt0;
                 m[eKey0] = key0;
                 m[ePart] = item.part;
                 m[eStop] = 0;
@@ -348,11 +350,13 @@ __global__ void __launch_bounds__(kRegBoundThreads, 1) rpa_prefill_tc8(const __g
                                 q_start + item.tok0);
                 qph ^= 1u;
             }
-            int win0 = key0 / ps;
+            int win0 = (nt0 ? 0 : key0) / ps;
             int win = (win0 + lane < a.P) ? __ldg(ptab + win0 + lane) : 0;
             for (int t = 0; t < nt && ok; ++t) {
-                const int k_tile = key0 + t * kBN;
-                const int lp_last = min(k_tile + kBN - 1, item.kv_end - 1) / ps;
+                const bool ft = t < nt0;
+                const int k_tile = ft ? t * kBN : key0 + (t - nt0) * kBN;
+                const int kv_begin = ft ? 0 : item.kv_begin, kv_end = ft ? a.first : item.kv_end;
+                const int lp_last = min(k_tile + kBN - 1, kv_end - 1) / ps;
                 if (lp_last - win0 >= 32) {
                     win0 = k_tile / ps;
                     win = (win0 + lane < a.P) ? __ldg(ptab + win0 + lane) : 0;
@@ -377,7 +381,7 @@ __global__ void __launch_bounds__(kRegBoundThreads, 1) rpa_prefill_tc8(const __g
                         if (BR == kBN) {
                             const int lp = k_tile / ps;
                             const int pg = __shfl_sync(0xffffffffu, win, (lp - win0) & 31);
-                            const bool want = k_tile < item.kv_end && k_tile + BR > item.kv_begin;
+                            const bool want = k_tile < kv_end && k_tile + BR > kv_begin;
                             const bool good = (unsigned)pg < (unsigned)a.N;
                             const uint32_t fb = smem_u32(kv ? &v_land[b2] : &k_full[b2]);
                             if (lane == 0) {
@@ -395,7 +399,7 @@ __global__ void __launch_bounds__(kRegBoundThreads, 1) rpa_prefill_tc8(const __g
                             const int k0 = k_tile + b * BR;
                             const int lp = k0 / ps;
                             const int pg = __shfl_sync(0xffffffffu, win, (lp - win0) & 31);
-                            if (tk >= tasks || k0 >= item.kv_end || k0 + BR <= item.kv_begin) return 0;
+                            if (tk >= tasks || k0 >= kv_end || k0 + BR <= kv_begin) return 0;
                             if ((unsigned)pg >= (unsigned)a.N) return 2;
                             x = (2 * item.head + kv) * D + cb * 64;
                             y = pg * ps + (k0 - lp * ps);
@@ -431,7 +435,7 @@ __global__ void __launch_bounds__(kRegBoundThreads, 1) rpa_prefill_tc8(const __g
                 const int k0 = k_tile + lane * BR;
                 const int lp = k0 / ps;
                 const int pg = __shfl_sync(0xffffffffu, win, (lp - win0) & 31);
-                const bool want = lane < runs && k0 < item.kv_end && k0 + BR > item.kv_begin;
+                const bool want = lane < runs && k0 < kv_end && k0 + BR > kv_begin;
                 const bool good = (unsigned)pg < (unsigned)a.N;
                 const int n_issue = __popc(__ballot_sync(0xffffffffu, want && good));
                 if (__any_sync(0xffffffffu, want && !good) && lane == 0) set_status(ctrl, RPA_ERR_BAD_PAGE_INDEX);
@@ -461,8 +465,8 @@ __global__ void __launch_bounds__(kRegBoundThreads, 1) rpa_prefill_tc8(const __g
         for (;;) {
             if (!mbar_wait(smem_u32(&meta_full[ms]), mph, ctrl, tmo)) break;
             const int* mm = meta[ms];
-            const int stop = mm[eStop], kv_begin = mm[eKvBegin], kv_end = mm[eKvEnd], nt = mm[eNt],
-                      key0 = mm[eKey0], ntok = mm[eNtok];
+            const int stop = mm[eStop], it_begin = mm[eKvBegin], it_end = mm[eKvEnd], nt = mm[eNt],
+                      key0 = mm[eKey0], ntok = mm[eNtok], nt0 = mm[eNt0];
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&meta_free[ms]));
             if (stop) break;
@@ -509,6 +513,9 @@ __global__ void __launch_bounds__(kRegBoundThreads, 1) rpa_prefill_tc8(const __g
             for (int t = 0; t < nt; ++t, ++tg) {
                 const int b2 = tg & 1;
                 const uint32_t par = (tg >> 1) & 1u;
+                const bool ft = t < nt0;
+                const int k_lo = ft ? t * kBN : key0 + (t - nt0) * kBN;
+                const int kv_begin = ft ? 0 : it_begin, kv_end = ft ? a.first : it_end;
                 if constexpr (DIRECT) {
                     // the copies wrote V(t) into its tile: on the tile's edges, zero this warp's rows of
                     // keys outside [kv_begin, kv_end) (page tails may hold any bits; runs outside the
@@ -518,7 +525,6 @@ __global__ void __launch_bounds__(kRegBoundThreads, 1) rpa_prefill_tc8(const __g
                         ok = false;
                         break;
                     }
-                    const int k_lo = key0 + t * kBN;
                     if (k_lo < kv_begin || k_lo + kBN > kv_end) {
                         uint8_t* vt = smem + (v16_base - smem0) + vb * Gm::T16;
                         for (int i = lane; i < kConvRows * Gm::CB * 8; i += 32) {
@@ -550,7 +556,6 @@ __global__ void __launch_bounds__(kRegBoundThreads, 1) rpa_prefill_tc8(const __g
                     s = 0;
                     ph ^= 1u;
                 }
-                const int k_lo = key0 + t * kBN;
                 // K, then V, both converted exactly by the hardware conversion: K(t) into its buffer
                 // once QK(t - NBK), the buffer's last reader, is done
                 if (tg >= (uint32_t)Gm::NBK) {
@@ -723,8 +728,8 @@ __global__ void __launch_bounds__(kRegBoundThreads, 1) rpa_prefill_tc8(const __g
             const int* mm = meta[ms];
             const int stop = mm[eStop];
             const int head = mm[eHead], q_start = mm[eQStart], ql = mm[eQl], kl = mm[eKl];
-            const int kv_begin = mm[eKvBegin], kv_end = mm[eKvEnd], tok0 = mm[eTok0];
-            const int ntok = mm[eNtok], nt = mm[eNt], key0 = mm[eKey0], part = mm[ePart];
+            const int it_begin = mm[eKvBegin], it_end = mm[eKvEnd], tok0 = mm[eTok0];
+            const int ntok = mm[eNtok], nt = mm[eNt], key0 = mm[eKey0], part = mm[ePart], nt0 = mm[eNt0];
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&meta_free[ms]));
             if (stop) break;
@@ -754,7 +759,9 @@ __global__ void __launch_bounds__(kRegBoundThreads, 1) rpa_prefill_tc8(const __g
                         if (lane == 0) mbar_arrive(smem_u32(&pv_ready[b2]));
                         continue;
                     }
-                    const int k_lo = key0 + t * kBN;
+                    const bool ft = t < nt0;
+                    const int k_lo = ft ? t * kBN : key0 + (t - nt0) * kBN;
+                    const int kv_begin = ft ? 0 : it_begin, kv_end = ft ? a.first : it_end;
                     const bool partial = k_lo < kv_begin || k_lo + kBN > kv_end;
                     const bool need_mask = partial || (a.causal && k_lo + kBN - 1 > pos_lo) ||
                                            (a.has_window && k_lo <= pos_hi - a.window);
@@ -774,11 +781,13 @@ __global__ void __launch_bounds__(kRegBoundThreads, 1) rpa_prefill_tc8(const __g
                         const int k_first = k_lo + half * HC + c * NK;
                         lo -= k_first;
                         hi -= k_first;
-                        mh = a.has_cap ? tile_logits<true, true, NK>(kv, qk, capl, cape, lo, hi)
-                                       : tile_logits<false, true, NK>(kv, qk, capl, cape, lo, hi);
+                        // the visible first keys, where this range holds any (its tiles then start at their own keys)
+                        const int f = kv_begin <= a.first ? a.first - k_first : 0;
+                        mh = a.has_cap ? tile_logits<true, true, NK>(kv, qk, capl, cape, lo, hi, f)
+                                       : tile_logits<false, true, NK>(kv, qk, capl, cape, lo, hi, f);
                     } else {
-                        mh = a.has_cap ? tile_logits<true, false, NK>(kv, qk, capl, cape, 0, 0)
-                                       : tile_logits<false, false, NK>(kv, qk, capl, cape, 0, 0);
+                        mh = a.has_cap ? tile_logits<true, false, NK>(kv, qk, capl, cape, 0, 0, 0)
+                                       : tile_logits<false, false, NK>(kv, qk, capl, cape, 0, 0, 0);
                     }
                     // row max over the copies, then over both halves
 #pragma unroll
