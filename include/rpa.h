@@ -39,7 +39,7 @@ extern "C" {
 /* Element types ("ragged_paged.zig", Cfg.q_dtype / Cfg.kv_dtype).
  *   q (and o, which has q's type): bf16, f16 or f32.
  *   K/V: bf16, f16, fp8 e4m3fn, fp8 e5m2 or int8 (two's complement); the 8-bit
- *        types are usually paired with k_scale / v_scale.
+ *        types are usually paired with k_scale / v_scale.  4-bit codes: below.
  * The tensor cores take both operands of a product in one type: bf16 with bf16
  * K/V, f16 with every other K/V type.  K/V values convert exactly; q values
  * of another type are rounded to that type to nearest even (f32 q; f16 q with
@@ -52,8 +52,21 @@ typedef enum RpaDtype {
     RPA_DT_F16 = 2,
     RPA_DT_F32 = 3,       /* q only */
     RPA_DT_FP8_E5M2 = 4,  /* K/V only */
-    RPA_DT_INT8 = 5       /* K/V only */
+    RPA_DT_INT8 = 5,      /* K/V only */
+    RPA_DT_INT4_G32 = 16, /* K/V only: 4-bit codes, a scale and a zero for each 32 channels ... */
+    RPA_DT_INT4_G64 = 17, /* ... 64 ... */
+    RPA_DT_INT4_G128 = 18 /* ... 128 channels (at most head_dim) */
 } RpaDtype;
+
+/* A 4-bit cache (RPA_KV_SPLIT) is bytes, kv_pages[total_num_pages, Hkv, page_size * (D + 8 * D / group)], 16-byte aligned.
+ * The block of a page and kv head holds
+ *   K codes        [page_size][D / 2] bytes: byte i of a slot's row has channel 2 i in its low half, 2 i + 1 in its
+ *                  high half; the row's 16-byte chunk c lies at chunk  c ^ (slot * D / 256 mod D / 32)
+ *   V codes        alike
+ *   K scale, zero  [page_size][D / group] pairs of f16
+ *   V scale, zero  alike
+ * and a channel's value is  code * scale + zero  of its group (times k_scale or v_scale).  rpa_rope_append writes
+ * it, rpa_rope_read reads its rows as values, rpa_forward attends over it. */
 
 typedef enum RpaStatus {
     RPA_OK = 0,
@@ -354,7 +367,9 @@ int rpa_rope_create(const RpaRopeCfg* cfg, RpaRope** out);
  * The arithmetic is in 32 bits with one rounding at the end.  The angle of position p is p w_i, w_i as
  * rpa_rope_frequencies gives it, modulo a turn, exact to 2^-32 of a turn at any position; the sine then
  * takes it as a 32-bit float, within 2^-26 of a turn near half a turn and exact near 0.  Cache rows hold k / k_scale and v / v_scale (where set), rounded to nearest even;
- * the 8-bit types saturate, NaN stays NaN (int8: 0); f16 rows overflow to infinity.
+ * the 8-bit types saturate, NaN stays NaN (int8: 0); f16 rows overflow to infinity.  4-bit rows: values saturate at
+ * +-65504; a group's zero is its least value rounded down to f16, its scale (greatest - zero) / 15 rounded up to f16, a
+ * code (value - zero) / scale rounded to nearest even, at most 15; a group with a NaN reads as NaN.
  * Rows of q_out and slots of the cache that no token of the call stands for are left as they were, as
  * are those of a sequence with bad lengths (RPA_ERR_BAD_LENGTHS); a token whose page id is bad writes
  * no cache row (RPA_ERR_BAD_PAGE_INDEX).  Two tokens never share a slot unless page_indices names one
@@ -363,6 +378,14 @@ int rpa_rope_append(RpaRope* h, const void* q, int64_t q_stride, const void* k, 
                     int64_t v_stride, void* kv_pages, const int32_t* kv_lens, const int32_t* page_indices,
                     const int32_t* cu_q_lens, const int32_t* positions, int32_t num_seqs, void* q_out,
                     void* stream);
+/* The cached rows of the last q_len keys of each sequence as values (cu_q_lens = the running sum of kv_lens: whole
+ * sequences): token t's slot as in rpa_rope_append, whatever wrote it.
+ *   k_out, v_out  device, [num_q_tokens, Hkv, D] q_dtype, contiguous, 16-byte aligned (RPA_KV_LATENT: k_out is the whole
+ *                 row, v_out is NULL)
+ * A value is the cache's times k_scale (v_scale), in 32 bits, rounded to q_dtype once.  Rows that no token of the call
+ * stands for, of sequences with bad lengths, and of bad page ids, are left as they were (same status codes). */
+int rpa_rope_read(RpaRope* h, const void* kv_pages, const int32_t* kv_lens, const int32_t* page_indices,
+                  const int32_t* cu_q_lens, int32_t num_seqs, void* k_out, void* v_out, void* stream);
 int rpa_rope_get_status(RpaRope* h, void* stream);
 void rpa_rope_destroy(RpaRope* h);
 

@@ -30,19 +30,24 @@ RPA_DT_F16 = 2
 RPA_DT_F32 = 3
 RPA_DT_FP8_E5M2 = 4
 RPA_DT_INT8 = 5
+RPA_DT_INT4_G32 = 16
+RPA_DT_INT4_G64 = 17
+RPA_DT_INT4_G128 = 18
 RPA_KV_SPLIT = 0
 RPA_KV_LATENT = 1
 KV_LAYOUTS = {"split": RPA_KV_SPLIT, "latent": RPA_KV_LATENT}
 # dtype names of the configuration (q / o, and kv_pages)
 Q_DTYPES = {"bf16": RPA_DT_BF16, "f16": RPA_DT_F16, "f32": RPA_DT_F32}
 KV_DTYPES = {"bf16": RPA_DT_BF16, "f16": RPA_DT_F16, "fp8_e4m3": RPA_DT_FP8_E4M3, "fp8_e5m2": RPA_DT_FP8_E5M2,
-             "int8": RPA_DT_INT8}
+             "int8": RPA_DT_INT8, "int4_g32": RPA_DT_INT4_G32, "int4_g64": RPA_DT_INT4_G64, "int4_g128": RPA_DT_INT4_G128}
+INT4_GROUPS = {RPA_DT_INT4_G32: 32, RPA_DT_INT4_G64: 64, RPA_DT_INT4_G128: 128}
 
 # every entry point declared in include/rpa.h
 EXPORTS = ("rpa_cfg_init", "rpa_validate_cfg", "rpa_create", "rpa_forward", "rpa_forward_host",
            "rpa_get_status", "rpa_read_plan", "rpa_profile_begin", "rpa_profile_read", "rpa_set_option",
            "rpa_forward_noalloc", "rpa_destroy", "rpa_strerror", "rpa_version",
            "rpa_rope_cfg_init", "rpa_rope_validate_cfg", "rpa_rope_frequencies", "rpa_rope_create", "rpa_rope_append",
+           "rpa_rope_read",
            "rpa_rope_get_status", "rpa_rope_destroy",
            "rpa_evict_validate_cfg", "rpa_evict_create", "rpa_evict_accumulate", "rpa_evict_compact",
            "rpa_evict_get_status", "rpa_evict_destroy",
@@ -152,6 +157,7 @@ def lib():
         L.rpa_rope_frequencies.argtypes = [ropecfg, vp]
         L.rpa_rope_create.argtypes = [ropecfg, ctypes.POINTER(vp)]
         L.rpa_rope_append.argtypes = [vp, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, i32, vp, vp]
+        L.rpa_rope_read.argtypes = [vp, vp, vp, vp, vp, i32, vp, vp, vp]
         L.rpa_rope_get_status.argtypes = [vp, vp]
         L.rpa_rope_destroy.argtypes = [vp]
         L.rpa_rope_destroy.restype = None
@@ -223,6 +229,13 @@ def validate_cfg(**cfg) -> int:
     return int(lib().rpa_validate_cfg(ctypes.byref(c)))
 
 
+def cache_shape(c: RpaCfg) -> tuple:
+    """Shape of kv_pages: rows of elements, or the blocks of bytes of a 4-bit cache."""
+    if c.kv_dtype in INT4_GROUPS:
+        return (c.total_num_pages, c.num_kv_heads, c.page_size * (c.head_dim + 8 * c.head_dim // INT4_GROUPS[c.kv_dtype]))
+    return (c.total_num_pages, c.page_size, c.num_kv_heads * (1 if c.kv_layout == RPA_KV_LATENT else 2), c.head_dim)
+
+
 def _stream_ptr(stream):
     import torch
 
@@ -238,7 +251,9 @@ class RaggedPagedAttention:
       q            [num_q_tokens, Hq, D] bfloat16, float16 or float32 (q_dtype)
       kv_pages     [total_num_pages, page_size, 2*Hkv, D] bfloat16 / float16, or
                    one-byte elements for fp8 (e4m3, e5m2) and int8 K/V
-                   ([total_num_pages, page_size, Hkv, D] for kv_layout="latent")
+                   ([total_num_pages, page_size, Hkv, D] for kv_layout="latent";
+                   uint8 [total_num_pages, Hkv, page_size * (D + 8 * D / group)] for
+                   "int4_g32", "int4_g64" and "int4_g128")
       kv_lens      [max_num_seqs] int32
       page_indices [max_num_seqs, pages_per_seq] int32
       cu_q_lens    [max_num_seqs + 1] int32
@@ -287,16 +302,15 @@ class RaggedPagedAttention:
         Dv = self.out_dim
         if out.dtype != qt or tuple(out.shape) != (T, Hq, Dv) or not out.is_contiguous():
             raise ValueError(f"out must be a contiguous {qt} tensor [num_q_tokens, Hq, {Dv}]")
-        rows = c.num_kv_heads if c.kv_layout == RPA_KV_LATENT else 2 * c.num_kv_heads
-        want_kv = (c.total_num_pages, c.page_size, rows, D)
+        want_kv = cache_shape(c)
         if tuple(kv_pages.shape) != want_kv or not kv_pages.is_contiguous():
             raise ValueError(f"kv_pages must be contiguous {want_kv}")
         if c.kv_dtype == RPA_DT_BF16 and kv_pages.dtype != torch.bfloat16:
             raise ValueError("kv_pages must be bfloat16")
         if c.kv_dtype == RPA_DT_F16 and kv_pages.dtype != torch.float16:
             raise ValueError("kv_pages must be float16")
-        if c.kv_dtype in (RPA_DT_FP8_E4M3, RPA_DT_FP8_E5M2, RPA_DT_INT8) and kv_pages.element_size() != 1:
-            raise ValueError("kv_pages must hold one byte per element (fp8 / int8)")
+        if c.kv_dtype not in (RPA_DT_BF16, RPA_DT_F16) and kv_pages.element_size() != 1:
+            raise ValueError("kv_pages must hold one byte per element (fp8 / int8 / int4 blocks)")
         for name, t, shape in (("kv_lens", kv_lens, (c.max_num_seqs,)),
                                ("page_indices", page_indices, (c.max_num_seqs, c.pages_per_seq)),
                                ("cu_q_lens", cu_q_lens, (c.max_num_seqs + 1,))):

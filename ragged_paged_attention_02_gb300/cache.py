@@ -15,7 +15,7 @@ import ctypes
 import numpy as np
 
 from .binding import (RPA_DT_BF16, RPA_DT_F16, RPA_DT_F32, RPA_KV_LATENT, RPA_OK, RpaError, RpaEvictCfg,
-                      RpaRopeCfg, lib, make_cfg)
+                      RpaRopeCfg, cache_shape, lib, make_cfg)
 
 ROPE_PAIRINGS = {"half": 0, "interleaved": 1}
 ROPE_SCALINGS = {"none": 0, "linear": 1, "base": 2, "rotations": 3, "index": 4}
@@ -54,7 +54,7 @@ class _Handle:
         self._q_dtype = _q_type(c.q_dtype)
         self._q_shape = (c.num_q_tokens, c.num_q_heads, c.head_dim)
         self._kv_rows = (c.num_q_tokens, c.num_kv_heads, c.head_dim)  # of new keys
-        self._kv_shape = (c.total_num_pages, c.page_size, c.num_kv_heads * (1 if self._latent else 2), c.head_dim)
+        self._kv_shape = cache_shape(c)
         self._kv_dtype = {RPA_DT_BF16: torch.bfloat16, RPA_DT_F16: torch.float16}.get(c.kv_dtype)  # None: one byte
         self._table_shape = (c.max_num_seqs, c.pages_per_seq)
         self._lens_shape, self._cu_shape = (c.max_num_seqs,), (c.max_num_seqs + 1,)
@@ -149,7 +149,8 @@ def rope_frequencies(**cfg) -> np.ndarray:
 
 
 class RopeAppend(_Handle):
-    """Rotary positions on q and the new keys, and the write of the new K/V rows to the paged cache.
+    """Rotary positions on q and the new keys, and the write of the new K/V rows to the paged cache (``append``); its rows as
+    values (``read``).
 
     Keywords beside RaggedPagedAttention's: ``rotary_dim`` (a multiple of 16; default the head) and
     ``rotary_offset`` (a multiple of 8) say which part of a head turns, ``pairing`` "half" or
@@ -159,7 +160,7 @@ class RopeAppend(_Handle):
     """
 
     _prefix = "rpa_rope_"
-    _names = ("append",)
+    _names = ("append", "read")
 
     def __init__(self, **cfg):
         self._h = None
@@ -208,6 +209,32 @@ class RopeAppend(_Handle):
                    page_indices.data_ptr(), cu_q_lens.data_ptr(), None if positions is None else positions.data_ptr(),
                    int(num_seqs), q_out.data_ptr(), self._stream(stream, tensors))
         return q_out
+
+    def _check_read(self, kv_pages, kv_lens, page_indices, cu_q_lens, k_out, v_out):
+        self._need_cache(kv_pages)
+        self._need_lengths(kv_lens, page_indices, cu_q_lens)
+        self._need("k_out", k_out, self._q_dtype, self._kv_rows)
+        if (v_out is None) != self._latent:
+            raise ValueError("v_out is None with the latent layout, whose rows are k, and only there")
+        if v_out is not None:
+            self._need("v_out", v_out, self._q_dtype, self._kv_rows)
+
+    def read(self, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, k_out=None, v_out=None, stream=None):
+        """The cached rows of each sequence's last q_len keys as values: (k_out, v_out), [T, Hkv, D] in q's type, whatever
+        wrote them (v_out None with the latent layout).  With cu_q_lens the running sum of kv_lens, whole sequences."""
+        import torch
+
+        with torch.cuda.stream(stream):
+            if k_out is None:
+                k_out = torch.zeros(self._kv_rows, dtype=self._q_dtype, device=kv_pages.device)
+            if v_out is None and not self._latent:
+                v_out = torch.zeros(self._kv_rows, dtype=self._q_dtype, device=kv_pages.device)
+        self._check_read(kv_pages, kv_lens, page_indices, cu_q_lens, k_out, v_out)
+        tensors = (kv_pages, kv_lens, page_indices, cu_q_lens, k_out, v_out)
+        self._need_here(tensors)
+        self._call("read", kv_pages.data_ptr(), kv_lens.data_ptr(), page_indices.data_ptr(), cu_q_lens.data_ptr(), int(num_seqs),
+                   k_out.data_ptr(), None if v_out is None else v_out.data_ptr(), self._stream(stream, tensors))
+        return k_out, v_out
 
 
 def make_evict_cfg(*, budget, protect=0, recent=0, **cfg) -> RpaEvictCfg:

@@ -511,7 +511,7 @@ int rpa_evict_validate_cfg(const RpaEvictCfg* c) {
     if (c->budget < 1 || c->budget > c->cache.pages_per_seq * c->cache.page_size) return RPA_ERR_INVALID_ARG;
     if (c->protect < 0 || c->recent < 0 || c->protect > c->budget || c->recent > c->budget - c->protect)
         return RPA_ERR_INVALID_ARG;
-    if (c->cache.kv_layout != RPA_KV_SPLIT || c->cache.first_keys > 0) return RPA_ERR_UNSUPPORTED;
+    if (c->cache.kv_layout != RPA_KV_SPLIT || c->cache.first_keys > 0 || int4_group(c->cache.kv_dtype)) return RPA_ERR_UNSUPPORTED;
     // 32-bit numbers of keys (with room for sums of two), rows, slots, grids' CTAs and blocks of kept keys
     if (c->cache.pages_per_seq * c->cache.page_size > (int64_t)1 << 30) return RPA_ERR_UNSUPPORTED;
     const int64_t lim = (int64_t)1 << 31, units = c->cache.max_num_seqs * c->cache.num_kv_heads;

@@ -140,7 +140,8 @@ int rpa_validate_cfg(const RpaCfg* c) {
     }
     if (c->q_dtype != RPA_DT_BF16 && c->q_dtype != RPA_DT_F16 && c->q_dtype != RPA_DT_F32) return RPA_ERR_UNSUPPORTED;
     if (c->kv_dtype != RPA_DT_BF16 && c->kv_dtype != RPA_DT_F16 && c->kv_dtype != RPA_DT_FP8_E4M3 &&
-        c->kv_dtype != RPA_DT_FP8_E5M2 && c->kv_dtype != RPA_DT_INT8)
+        c->kv_dtype != RPA_DT_FP8_E5M2 && c->kv_dtype != RPA_DT_INT8 &&
+        !(int4_group(c->kv_dtype) && int4_group(c->kv_dtype) <= c->head_dim))
         return RPA_ERR_UNSUPPORTED;
     // masked keys get weight exactly 0 only if the additive mask value is huge and negative
     if (!(c->mask_value <= -1e30f)) return RPA_ERR_UNSUPPORTED;
@@ -152,6 +153,7 @@ int rpa_create(const RpaCfg* cfg, RpaHandle** out) {
     *out = nullptr;
     int v = rpa_validate_cfg(cfg);
     if (v != RPA_OK) return v;
+    if (int4_group(cfg->kv_dtype)) return RPA_ERR_UNSUPPORTED;
     RpaHandle* h = new (std::nothrow) RpaHandle;
     if (!h) return RPA_ERR_CUDA;
     memset(h, 0, sizeof *h);

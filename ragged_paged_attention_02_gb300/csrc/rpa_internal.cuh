@@ -69,9 +69,20 @@ struct __align__(16) Comb {
 
 // K/V element types inside the kernels (template arguments): 16-bit types feed the MMAs as they
 // are; 8-bit types are converted exactly to f16 first.
-enum KvType : int { KT_BF16 = 0, KT_F16 = 1, KT_E4M3 = 2, KT_E5M2 = 3, KT_I8 = 4 };
-__host__ __device__ constexpr bool kt_8bit(int kt) { return kt >= KT_E4M3; }
+enum KvType : int { KT_BF16 = 0, KT_F16 = 1, KT_E4M3 = 2, KT_E5M2 = 3, KT_I8 = 4, KT_I4 = 5 };
+__host__ __device__ constexpr bool kt_8bit(int kt) { return kt >= KT_E4M3 && kt <= KT_I8; }
 __host__ __device__ constexpr bool kt_f16_mma(int kt) { return kt != KT_BF16; }  // MMA operands in f16
+// 4-bit K/V.  The block of a page and kv head: K codes [ps][D / 2], V codes, K's (scale, zero) [ps][D / group] f16 pairs, V's.
+// 16-byte chunk c of slot r's codes lies at chunk int4_chunk(c, r): eight slots' chunks c then fall into eight different
+// 16-byte columns of a 128-byte line, so that the matrix loads of a copied block have no bank conflicts.
+inline int int4_group(int dtype) {
+    return dtype == RPA_DT_INT4_G32 ? 32 : dtype == RPA_DT_INT4_G64 ? 64 : dtype == RPA_DT_INT4_G128 ? 128 : 0;
+}
+__host__ __device__ constexpr int int4_key_bytes(int D, int group) { return D + 8 * (D / group); }
+template <typename T>
+__host__ __device__ constexpr T int4_chunk(T c, T r, int D) {
+    return c ^ ((r * D / 256) & (D / 32 - 1));
+}
 // Output element types (o has the q dtype)
 enum OutType : int { OT_BF16 = 0, OT_F16 = 1, OT_F32 = 2 };
 
@@ -263,6 +274,17 @@ int encode_kv_map_runs(CUtensorMap* m, const void* kv, int byte_elems, long long
 int encode_kv_map_heads(CUtensorMap* m, const void* kv, long long N, int ps, int H, int D, int BR);
 // K rows of a split cache whose rows are `row` bytes: one box = BR slots of one row, in 64-byte columns
 int encode_k_map(CUtensorMap* m, const void* kv, int row, long long N, int ps, int Hkv, int BR);
+// the cached rows of the batch's tokens as values of q_dtype (rpa_rope_read)
+struct ReadParams {
+    const uint8_t* kv;
+    uint8_t *k, *v;
+    const int *kv_lens, *page_indices, *cu;
+    int* status;
+    int S, T, Hkv, D, ps, P, N, latent;
+    int kt, group;  // KvType of the cache, channels of a group of a 4-bit cache
+    float k_scale, v_scale;
+};
+cudaError_t launch_read(const ReadParams& p, int q_dtype, int sms, cudaStream_t st);
 // occupancy / attributes (call once per device)
 size_t plan_smem_bytes();
 cudaError_t plan_prepare();
@@ -323,6 +345,8 @@ struct EnqueueOpts {
     int epoch;  // this call's number (concurrent decode / prefill on one stream)
     int plan_early;  // RPA_OPT_PLAN_EARLY
 };
+// KvType of an RpaDtype
+int kv_type(int32_t dt);
 // Host only: fill ks from a validated configuration (sms = the device's SM count).
 void kernels_choose(const RpaCfg& c, int sms, KernelSet* ks);
 // Kernel attributes and occupancy on the current device (dec_bps, pf_bps); an error if a kernel

@@ -34,7 +34,10 @@ const double kLog2e = 1.4426950408889634;
 
 size_t align256(size_t x) { return (x + 255) & ~(size_t)255; }
 
+}  // namespace
+
 int kv_type(int32_t dt) {
+    if (int4_group(dt)) return KT_I4;
     switch (dt) {
         case RPA_DT_F16: return KT_F16;
         case RPA_DT_FP8_E4M3: return KT_E4M3;
@@ -43,6 +46,8 @@ int kv_type(int32_t dt) {
         default: return KT_BF16;
     }
 }
+
+namespace {
 
 int out_type(int32_t dt) { return dt == RPA_DT_F32 ? OT_F32 : dt == RPA_DT_F16 ? OT_F16 : OT_BF16; }
 

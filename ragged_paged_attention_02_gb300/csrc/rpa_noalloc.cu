@@ -76,6 +76,7 @@ extern "C" int rpa_forward_noalloc(const RpaCfg* cfg, const void* q, const void*
     const int v = rpa_validate_cfg(cfg);
     if (v != RPA_OK) return v;
     const RpaCfg& c = *cfg;
+    if (int4_group(c.kv_dtype)) return RPA_ERR_UNSUPPORTED;
     if (num_seqs < 0 || num_seqs > c.max_num_seqs) return RPA_ERR_INVALID_ARG;
     if (!kv_pages || !kv_lens || !page_indices || !cu_q_lens) return RPA_ERR_INVALID_ARG;
     if (c.num_q_tokens > 0 && (!q || !o)) return RPA_ERR_INVALID_ARG;

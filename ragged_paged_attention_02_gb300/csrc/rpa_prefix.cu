@@ -545,7 +545,7 @@ int rpa_prefix_validate_cfg(const RpaCfg* cfg, int64_t max_groups) {
     const int v = rpa_validate_cfg(cfg);
     if (v != RPA_OK) return v;
     if (max_groups < 1 || max_groups > cfg->max_num_seqs) return RPA_ERR_INVALID_ARG;
-    if (cfg->kv_layout != RPA_KV_SPLIT || !cfg->is_causal || cfg->has_sliding_window) return RPA_ERR_UNSUPPORTED;
+    if (cfg->kv_layout != RPA_KV_SPLIT || !cfg->is_causal || cfg->has_sliding_window || int4_group(cfg->kv_dtype)) return RPA_ERR_UNSUPPORTED;
     // keys and a piece's, positions of a group's tokens behind its prefix, and rows of the virtual batch, in 32 bits
     if (cfg->pages_per_seq * cfg->page_size > (int64_t)1 << 30 || cfg->num_q_tokens >= (int64_t)1 << 30 ||
         cfg->num_q_tokens * cfg->num_q_heads >= (int64_t)1 << 31)

@@ -67,6 +67,7 @@ struct RopeParams {
     int per_row;    // units of a row
     int row_step;   // rows the CTA takes at once (its threads / per_row)
     int kt;         // KvType of the cache
+    int group;      // channels of a group of a 4-bit cache
     int has_ks, has_vs;
     float magnitude, k_scale, v_scale;
 };
@@ -153,13 +154,76 @@ __device__ __forceinline__ void store_kv8(uint8_t* kv, size_t row, int e, const 
     }
 }
 
-template <typename QT, bool HALF>
+// least / greatest of two, NaN where either is
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float r;
+    asm("min.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// A row of a 4-bit cache.  The row's D / 16 threads (neighbouring lanes, `mask`) hold its values by the pairs they turn;
+// through `row` (shared, D floats) each takes 16 neighbouring channels, and a group's extremes come by shuffles.
+// Differences and quotients are rounded towards the side that the scale and the zero are rounded to, so that no two roundings
+// of one value can meet; codes come from the exact quotient's nearest (a division, not a product with 1 / scale: beside a
+// border the product may fall on its other side).
+__device__ __forceinline__ void store_int4(const RopeParams& p, const float* y, int e0, int e1, float* row, int place, uint32_t mask,
+                                           long long slot, int h, bool is_v) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        reinterpret_cast<float4*>(row + e0)[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+        reinterpret_cast<float4*>(row + e1)[i] = make_float4(y[8 + 4 * i], y[9 + 4 * i], y[10 + 4 * i], y[11 + 4 * i]);
+    }
+    __syncwarp(mask);
+    float x[16];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float4 v = reinterpret_cast<const float4*>(row + 16 * place)[i];
+        x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+    }
+    __syncwarp(mask);  // the buffer is free again
+    float lo = INFINITY, hi = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        x[i] = max_nan(min_nan(x[i], 65504.f), -65504.f);
+        lo = min_nan(lo, x[i]);
+        hi = max_nan(hi, x[i]);
+    }
+    for (int o = 1; o < p.group / 16; o <<= 1) {
+        lo = min_nan(lo, __shfl_xor_sync(mask, lo, o));
+        hi = max_nan(hi, __shfl_xor_sync(mask, hi, o));
+    }
+    const __half zero = __float2half_rd(lo);
+    const float z = __half2float(zero);
+    const __half scale = __float2half_ru(__fdiv_ru(__fsub_ru(hi, z), 15.f));
+    const float s = __half2float(scale);
+    uint32_t w[2] = {0, 0};
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        const int c = min(max(__float2int_rn(__fdiv_rn(x[i] - z, s)), 0), 15);  // (0 / 0 and NaN give 0)
+        w[i / 8] |= (uint32_t)c << (4 * (i % 8));
+    }
+    const int page = (int)(slot >> 32), at = (int)slot, ng = p.D / p.group;
+    uint8_t* block = p.kv + ((size_t)page * p.Hkv + h) * ((size_t)p.ps * int4_key_bytes(p.D, p.group));
+    uint8_t* codes = block + (size_t)((is_v ? p.ps : 0) + at) * (p.D / 2);
+    *reinterpret_cast<uint2*>(codes + int4_chunk(place / 2, at, p.D) * 16 + (place & 1) * 8) = make_uint2(w[0], w[1]);
+    if ((16 * place) % p.group == 0)
+        reinterpret_cast<__half2*>(block + (size_t)p.ps * p.D)[(size_t)((is_v ? p.ps : 0) + at) * ng + 16 * place / p.group] =
+            __halves2half2(scale, zero);
+}
+
+template <typename QT, bool HALF, bool INT4>
 __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rpa_rope_kernel(const RopeParams p) {
     constexpr int kBatch = sizeof(QT) == 4 ? 1 : 2;  // rows whose loads a thread has in flight
     // [tokens][4][places] pairs of (cos, sin): place's pairs 2 i and 2 i + 1 at [i][place], so that neighbouring
     // places read neighbouring 16 bytes
     extern __shared__ float4 s_cs[];
-    __shared__ long long s_slot[kTokens];  // cache slot of a token (page * page_size + place), or -1
+    __shared__ long long s_slot[kTokens];  // cache slot of a token (page * page_size + place; INT4: page, place), or -1
+    __shared__ __align__(16) float s_rows[INT4 ? kRopeThreads * kUnit : 4];  // INT4: the rows that are being coded
     __shared__ int s_pos[kTokens], s_live[kTokens];
     __shared__ int s_cu[kSeqs + 1], s_kl[kSeqs];
     __shared__ unsigned long long s_turns[kMaxPairs];
@@ -193,7 +257,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rpa_rope_kernel(const
             const int j = kl - ql + (t - q0);
             const int pg = p.page_indices[(size_t)s * p.P + j / p.ps];
             pos = p.positions ? p.positions[t] : j;
-            if ((unsigned)pg < (unsigned)p.N) slot = (long long)pg * p.ps + j % p.ps;
+            if ((unsigned)pg < (unsigned)p.N) slot = INT4 ? ((long long)pg << 32) | (j % p.ps) : (long long)pg * p.ps + j % p.ps;
             else set_status(p.status, RPA_ERR_BAD_PAGE_INDEX);
         }
         s_live[i] = live;
@@ -299,6 +363,12 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rpa_rope_kernel(const
 #pragma unroll
                             for (int i = 0; i < 16; ++i) y[i] = __fdiv_rn(y[i], sc);
                         }
+                        if constexpr (INT4) {
+                            const uint32_t mask = ((1u << p.per_row) - 1u) << (lane - place % 32);
+                            store_int4(p, y, e0, e1, s_rows + (size_t)(tid - place) * kUnit, place, mask, s_slot[tb], h, is_v);
+                            next(tb, rb);
+                            continue;
+                        }
                         const int rows = p.latent ? p.Hkv : 2 * p.Hkv;
                         const size_t row = ((size_t)s_slot[tb] * rows + (p.latent ? h : 2 * h + (is_v ? 1 : 0))) * p.D *
                                            (kt_8bit(p.kt) ? 1 : 2);
@@ -327,8 +397,11 @@ __global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rpa_rope_kernel(const
 template <typename QT>
 cudaError_t launch_rope(const RopeParams& p, int half, int grid, int threads, cudaStream_t st) {
     const size_t smem = (size_t)kTokens * (p.rd / 2) * sizeof(float2);  // at most 36 KB
-    return half ? launch_pdl(rpa_rope_kernel<QT, true>, grid, threads, smem, st, p)
-                : launch_pdl(rpa_rope_kernel<QT, false>, grid, threads, smem, st, p);
+    if (p.kt == KT_I4)
+        return half ? launch_pdl(rpa_rope_kernel<QT, true, true>, grid, threads, smem, st, p)
+                    : launch_pdl(rpa_rope_kernel<QT, false, true>, grid, threads, smem, st, p);
+    return half ? launch_pdl(rpa_rope_kernel<QT, true, false>, grid, threads, smem, st, p)
+                : launch_pdl(rpa_rope_kernel<QT, false, false>, grid, threads, smem, st, p);
 }
 
 constexpr double kTwoPi = 6.283185307179586476925286766559;
@@ -503,8 +576,8 @@ int rpa_rope_append(RpaRope* h, const void* q, int64_t q_stride, const void* k, 
     p.rows = p.Hq + (latent ? 1 : 2) * p.Hkv;
     p.per_row = p.D / kUnit;
     p.row_step = kRopeThreads / p.per_row;
-    p.kt = c.kv_dtype == RPA_DT_F16 ? KT_F16 : c.kv_dtype == RPA_DT_FP8_E4M3 ? KT_E4M3
-         : c.kv_dtype == RPA_DT_FP8_E5M2 ? KT_E5M2 : c.kv_dtype == RPA_DT_INT8 ? KT_I8 : KT_BF16;
+    p.kt = kv_type(c.kv_dtype);
+    p.group = int4_group(c.kv_dtype);
     p.has_ks = c.has_k_scale;
     p.has_vs = c.has_v_scale;
     p.k_scale = c.k_scale;
@@ -518,6 +591,47 @@ int rpa_rope_append(RpaRope* h, const void* q, int64_t q_stride, const void* k, 
                           : c.q_dtype == RPA_DT_F16 ? launch_rope<__half>(p, half, grid, threads, st)
                                                     : launch_rope<__nv_bfloat16>(p, half, grid, threads, st);
     if (e != cudaSuccess) {
+        cudaGetLastError();
+        return RPA_ERR_CUDA;
+    }
+    return RPA_OK;
+}
+
+int rpa_rope_read(RpaRope* h, const void* kv_pages, const int32_t* kv_lens, const int32_t* page_indices,
+                  const int32_t* cu_q_lens, int32_t num_seqs, void* k_out, void* v_out, void* stream) {
+    if (!h) return RPA_ERR_INVALID_ARG;
+    const RpaCfg& c = h->cfg.cache;
+    const bool latent = c.kv_layout == RPA_KV_LATENT;
+    if (num_seqs < 0 || num_seqs > c.max_num_seqs) return RPA_ERR_INVALID_ARG;
+    if (!kv_pages || !kv_lens || !page_indices || !cu_q_lens) return RPA_ERR_INVALID_ARG;
+    if (c.num_q_tokens > 0 && (!k_out || (!latent && !v_out))) return RPA_ERR_INVALID_ARG;
+    if (latent && v_out) return RPA_ERR_INVALID_ARG;
+    if (!aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(kv_pages, 16) || !aligned(kv_lens, 4) ||
+        !aligned(page_indices, 4) || !aligned(cu_q_lens, 4))
+        return RPA_ERR_INVALID_ARG;
+    DeviceGuard g(h->device);
+    if (!g.ok) return RPA_ERR_CUDA;
+    ReadParams p;
+    p.kv = static_cast<const uint8_t*>(kv_pages);
+    p.k = static_cast<uint8_t*>(k_out);
+    p.v = static_cast<uint8_t*>(v_out);
+    p.kv_lens = kv_lens;
+    p.page_indices = page_indices;
+    p.cu = cu_q_lens;
+    p.status = h->status;
+    p.S = num_seqs;
+    p.T = (int)c.num_q_tokens;
+    p.Hkv = (int)c.num_kv_heads;
+    p.D = (int)c.head_dim;
+    p.ps = (int)c.page_size;
+    p.P = (int)c.pages_per_seq;
+    p.N = (int)c.total_num_pages;
+    p.latent = latent;
+    p.kt = kv_type(c.kv_dtype);
+    p.group = int4_group(c.kv_dtype);
+    p.k_scale = c.has_k_scale ? c.k_scale : 1.f;
+    p.v_scale = c.has_v_scale ? c.v_scale : 1.f;
+    if (launch_read(p, c.q_dtype, h->sms, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
         cudaGetLastError();
         return RPA_ERR_CUDA;
     }
