@@ -153,7 +153,6 @@ int rpa_create(const RpaCfg* cfg, RpaHandle** out) {
     *out = nullptr;
     int v = rpa_validate_cfg(cfg);
     if (v != RPA_OK) return v;
-    if (int4_group(cfg->kv_dtype)) return RPA_ERR_UNSUPPORTED;
     RpaHandle* h = new (std::nothrow) RpaHandle;
     if (!h) return RPA_ERR_CUDA;
     memset(h, 0, sizeof *h);
@@ -169,7 +168,7 @@ int rpa_create(const RpaCfg* cfg, RpaHandle** out) {
     }
     kernels_choose(c, sms, &h->ks);
     // the SM-split model is calibrated for the tensor-memory prefill of 2-byte K/V only
-    h->can_concurrent = h->ks.tc;
+    h->can_concurrent = h->ks.tc && h->ks.kt != KT_I4;
     if (kernels_prepare(c, &h->ks) != cudaSuccess) {
         cudaGetLastError();
         delete h;
@@ -389,13 +388,13 @@ int rpa_read_plan(RpaHandle* h, int32_t* info, int32_t* items, int64_t max_items
     info[12] = h->ks.sms;
     info[13] = h->ks.dec_bps;
     info[14] = h->ks.pf_bps;
-    info[15] = h->concurrent | ((h->ks.tc8 | h->ks.mla) << 1);
+    info[15] = h->concurrent | (((h->ks.tc8 && h->ks.kt != KT_I4) | h->ks.mla) << 1);
     if (items && max_items > 0) {
         // the kernels' unit lists, each unit expanded to its items (one per kv head, as item_at)
-        const int64_t H = h->ks.Hp;
+        const int64_t H = h->ks.Hp, HP = h->ks.pf_H;
         const int64_t nd = ctrl[kNumDecItems] < max_items ? ctrl[kNumDecItems] : max_items;
         const int64_t np = ctrl[kNumPfItems] < max_items - nd ? ctrl[kNumPfItems] : max_items - nd;
-        const int64_t ud = (nd + H - 1) / H, up = (np + H - 1) / H;
+        const int64_t ud = (nd + H - 1) / H, up = (np + HP - 1) / HP;
         Unit* u = static_cast<Unit*>(malloc((size_t)(ud + up + 1) * sizeof(Unit)));
         if (!u) return RPA_ERR_INVALID_ARG;
         if ((ud && cudaMemcpy(u, h->w.dec_units, ud * sizeof(Unit), cudaMemcpyDeviceToHost) != cudaSuccess) ||
@@ -405,8 +404,8 @@ int rpa_read_plan(RpaHandle* h, int32_t* info, int32_t* items, int64_t max_items
         }
         for (int64_t i = 0; i < nd + np; ++i) {
             const int64_t it = i < nd ? i : i - nd;
-            const Unit& x = u[(i < nd ? 0 : ud) + it / H];
-            const int hd = (int)(it % H);
+            const Unit& x = u[i < nd ? it / H : ud + it / HP];
+            const int hd = (int)(i < nd ? it % H : it % HP);
             int32_t* d = items + i * 8;
             d[0] = x.seq;
             d[1] = hd;

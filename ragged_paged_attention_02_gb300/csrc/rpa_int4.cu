@@ -1,0 +1,797 @@
+// rpa_int4.cu -- attention over a cache of 4-bit codes.
+//
+// A channel of a key is  code * s + z  with a scale s and a zero z of its group of channels, so a logit and an output are
+//   q . k  = sum over groups  s_g (q . code)_g + z_g (sum of q)_g
+//   o      = sum over keys  p s code + p z
+//          = sum over keys  P code  -  8 sum over keys P  +  sum over keys p (z + 8 s),     P = f16(p s)
+// The matrix products run on the codes themselves, exact in f16; scales and zeros act on 32-bit sums of a group and on the
+// probabilities.  P is the only rounded factor, and its rounding meets code - 8, at most half a group's range: with the codes
+// 0 .. 15 alone it would be twice to three times as large.  Sums of P come out of one more product, with ones.
+//
+// Codes become f16 operands with a mask: bits 0 - 3 of a 16-bit word are the subnormal code * 2^-24, bits 4 - 7 code * 2^-20,
+// and 8 bits further down the same again (5 instructions for 8 codes).  Codes of the two positions go to different accumulators
+// (logits) or output rows (values), whose powers of two are applied at the end.  q is rounded to f16.
+//
+//  * direct kernel: tiles of 8 or 16 query rows (tokens x heads of a kv head).  Keys are on the M side of m16n8k16: S^T = K Q^T,
+//    O^T += V^T P^T, so that one decoded operand serves all rows; matrix loads of 16-bit units give a thread four codes of a key
+//    (K) or of two keys (V, transposed) just as the operands want them.  One producer warp copies whole blocks of a page and kv
+//    head (or four pieces of one where the page size does not divide 128) into a ring of 128-key stages, four warps take 32
+//    keys of each.  Bound by the bytes of the cache; a key and kv head costs about 11 issue slots at D 128.
+//  * long prompts would decode every key once for each tile.  Sequences with more tokens are unfolded instead, once a call, to
+//    f16 rows in the workspace, over which the tensor-memory prefill kernels run.
+#include <cuda_fp16.h>
+#include <string.h>
+
+#include "rpa_internal.cuh"
+
+namespace rpa {
+namespace {
+
+constexpr int kCW = 4;                       // consumer warps
+constexpr int kI4Threads = (kCW + 1) * 32;
+constexpr int kKS = 128;                     // keys of a stage
+// The running maximum moves when a row's grows by more than 2^2: probabilities stay below 4, and P below 4 * 8734 (the
+// greatest scale of float16 values), in f16's range
+constexpr float kRescale = 2.f;
+
+enum I4Meta : int { mSeq = 0, mHead, mQStart, mQl, mKl, mKvBegin, mKvEnd, mPart, mTok0, mNtok, mSt, mNst, mKey0, mStop, mSwz, kMetaWords };
+
+struct I4Params {
+    AttnParams a;            // a.G: query heads of an item; a.Hkv: the cache's
+    int blocks;              // items' heads a kv head makes
+    int BR, brs;             // keys of a copied page run, log2
+    size_t block;            // bytes of a page's block
+    int qdt;                 // OutType of q
+    int stall;               // test hook: the producer issues nothing
+    unsigned long long timeout_ns;
+};
+
+template <int D, int NG, int NT>
+struct I4Geom {
+    static constexpr int R = 8 * NT;
+    static constexpr int KB = D + 8 * NG;        // bytes of a key
+    static constexpr int STAGE = kKS * KB;
+    static constexpr int LD = D + 4;             // floats of a row of the merge area: rows of four lanes fall into different banks
+    static constexpr int RED = kCW * R * LD * 4;
+    // resident CTAs that registers are allocated for, and stages: as many as fit beside them
+    static constexpr int CTAS = NG == 8 ? 1 : D == 256 ? 2 : NT == 2 ? 2 : D == 128 ? 3 : 4;
+    static constexpr int FIT = ((227 * 1024 / CTAS - 2048) - RED) / STAGE;
+    static constexpr int NS = FIT > 4 ? 4 : FIT;
+    static constexpr int SMEM = NS * STAGE + RED;
+    static_assert(NS >= 2, "a ring");
+};
+
+__device__ __forceinline__ void bulk_copy(uint32_t dst, const uint8_t* src, uint32_t bytes, uint32_t bar, uint64_t pol) {
+    asm volatile(
+        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1], %2, [%3], %4;\n" ::"r"(dst),
+        "l"(src), "r"(bytes), "r"(bar), "l"(pol)
+        : "memory");
+}
+// 8 x 8 matrix of 16-bit elements, transposed across the warp
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
+    return y;
+}
+// Eight neighbouring q values as f16 pairs, rounded to nearest even
+__device__ __forceinline__ uint4 load_q8(const uint8_t* q, size_t e, int qdt) {
+    if (qdt == OT_F32) {
+        const float4 a = __ldg(reinterpret_cast<const float4*>(q + e * 4)), b = __ldg(reinterpret_cast<const float4*>(q + e * 4) + 1);
+        return make_uint4(pack2<true>(a.x, a.y), pack2<true>(a.z, a.w), pack2<true>(b.x, b.y), pack2<true>(b.z, b.w));
+    }
+    uint4 w = __ldg(reinterpret_cast<const uint4*>(q + e * 2));
+    if (qdt == OT_BF16)
+        w = make_uint4(bf16x2_to_f16x2(w.x), bf16x2_to_f16x2(w.y), bf16x2_to_f16x2(w.z), bf16x2_to_f16x2(w.w));
+    return w;
+}
+template <int NG>
+__device__ __forceinline__ void load_meta(uint32_t addr, uint32_t* m) {
+    if constexpr (NG == 1) {
+        asm volatile("ld.shared.b32 %0, [%1];\n" : "=r"(m[0]) : "r"(addr));
+    } else if constexpr (NG == 2) {
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];\n" : "=r"(m[0]), "=r"(m[1]) : "r"(addr));
+    } else {
+#pragma unroll
+        for (int i = 0; i < NG; i += 4)
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];\n"
+                         : "=r"(m[i]), "=r"(m[i + 1]), "=r"(m[i + 2]), "=r"(m[i + 3])
+                         : "r"(addr + 4 * i));
+    }
+}
+
+template <int D, int NG, int NT>
+__global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int4_attn(const I4Params p) {
+    using Gm = I4Geom<D, NG, NT>;
+    constexpr int R = Gm::R, NS = Gm::NS, C = D / 32;  // 16-byte chunks of a row of codes
+    constexpr int CPG = C / NG;                        // ... of a group
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ __align__(8) uint64_t full_bar[NS], empty_bar[NS], merge_bar;
+    __shared__ int meta[NS][kMetaWords];
+    __shared__ float red_ml[kCW][R][2];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const AttnParams& a = p.a;
+    int* ctrl = a.ctrl;
+    const uint64_t tmo = p.timeout_ns;
+    const uint32_t smem0 = smem_u32(smem);
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(smem_u32(&full_bar[i]), 1);
+            mbar_init(smem_u32(&empty_bar[i]), kCW);
+        }
+        mbar_init(smem_u32(&merge_bar), kCW);
+        fence_mbar_init();
+    }
+    __syncthreads();
+    pdl_trigger();
+    pdl_wait();  // the planner's items are complete from here on
+    if ((int)blockIdx.x >= ctrl[kDecCtas]) return;
+    const int n_items = ctrl[a.item_count_word];
+    const int BR = p.BR, brs = p.brs, RB = BR * Gm::KB;
+
+    if (warp == kCW) {
+        // =============================== producer ===============================
+        if (p.stall) return;
+        const int ps = a.ps, runs = kKS / BR;
+        const uint64_t pol = l2_policy_evict_first();
+        int s = 0;
+        uint32_t ph = 0;
+        int it = 0;
+        if (lane == 0) it = atomicAdd(ctrl + a.counter_word, 1);
+        it = __shfl_sync(0xffffffffu, it, 0);
+        bool ok = true;
+        while (ok && it < n_items) {
+            const Item item = item_at(a.units, it, a.unit_heads);
+            int nxt = 0;
+            if (lane == 0) nxt = atomicAdd(ctrl + a.counter_word, 1);
+            const int q_start = a.cu_q_lens[item.seq];
+            const int ql = a.cu_q_lens[item.seq + 1] - q_start, kl = a.kv_lens[item.seq];
+            const int* ptab = a.page_indices + (size_t)item.seq * a.P;
+            const int kvh = item.head / p.blocks;
+            // the unit's keys are those that any tile of the sequence sees: this tile's of them (none: a stage without keys,
+            // whose item writes an empty partial)
+            const int p_lo = kl - ql + item.tok0, p_hi = p_lo + item.ntok - 1;
+            int lo = item.kv_begin, hi = item.kv_end;
+            if (a.causal) hi = min(hi, p_hi + 1);
+            if (a.has_window && (a.first == 0 || lo > a.first)) lo = max(lo, p_lo - a.window + 1);
+            hi = max(hi, lo);
+            const int key0 = lo & ~(BR - 1);
+            const int nst0 = first_tiles(a, item, kKS);
+            const int nst = max(1, nst0 + (hi > lo ? (hi - key0 + kKS - 1) / kKS : 0));
+            int win0 = (nst0 ? 0 : key0) / ps;
+            int win = (win0 + lane < a.P) ? __ldg(ptab + win0 + lane) : 0;
+            for (int st = 0; st < nst; ++st) {
+                const bool fs = st < nst0;
+                const int k_stage = fs ? st * kKS : key0 + (st - nst0) * kKS;
+                const int kv_begin = fs ? 0 : lo, kv_end = fs ? a.first : hi;
+                const int lp_last = max(k_stage, min(k_stage + kKS, kv_end) - 1) / ps;
+                if (lp_last - win0 >= 32) {
+                    win0 = k_stage / ps;
+                    win = (win0 + lane < a.P) ? __ldg(ptab + win0 + lane) : 0;
+                }
+                if (!mbar_wait(smem_u32(&empty_bar[s]), ph ^ 1u, ctrl, tmo)) {
+                    ok = false;
+                    break;
+                }
+                const uint32_t stage = smem0 + s * Gm::STAGE;
+                const int k0 = k_stage + lane * BR;
+                const int lp = k0 / ps;
+                const int pg = __shfl_sync(0xffffffffu, win, (lp - win0) & 31);
+                const bool want = lane < runs && k0 < kv_end && k0 + BR > kv_begin;
+                const bool good = (unsigned)pg < (unsigned)a.N;
+                const int n_issue = __popc(__ballot_sync(0xffffffffu, want && good));
+                if (__any_sync(0xffffffffu, want && !good)) {
+                    // a page id outside [0, N): never dereferenced; its keys read as zero
+                    if (lane == 0) set_status(ctrl, RPA_ERR_BAD_PAGE_INDEX);
+                    for (int i = lane; i < Gm::STAGE / 16; i += 32)
+                        reinterpret_cast<uint4*>(smem + s * Gm::STAGE)[i] = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();
+                }
+                // where the codes' chunks lie goes by a key's slot modulo 8: bit 2 of it for every four keys
+                const uint32_t swz = __ballot_sync(0xffffffffu, ((k_stage + 4 * lane) % ps) & 4);
+                if (lane == 0) {
+                    int* m = meta[s];
+                    m[mSeq] = item.seq;
+                    m[mHead] = item.head;
+                    m[mQStart] = q_start;
+                    m[mQl] = ql;
+                    m[mKl] = kl;
+                    m[mKvBegin] = kv_begin;
+                    m[mKvEnd] = kv_end;
+                    m[mPart] = item.part;
+                    m[mTok0] = item.tok0;
+                    m[mNtok] = item.ntok;
+                    m[mSt] = st;
+                    m[mNst] = nst;
+                    m[mKey0] = k_stage;
+                    m[mSwz] = (int)swz;
+                    m[mStop] = 0;
+                }
+                __syncwarp();
+                const uint32_t fb = smem_u32(&full_bar[s]);
+                if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)(n_issue * RB));
+                __syncwarp();
+                if (want && good) {
+                    const uint8_t* src = a.kv + ((size_t)pg * a.Hkv + kvh) * p.block;
+                    const uint32_t dst = stage + lane * RB;
+                    if (BR == ps) {
+                        bulk_copy(dst, src, RB, fb, pol);
+                    } else {
+                        const int r0 = k0 - lp * ps;
+                        bulk_copy(dst, src + r0 * (D / 2), BR * (D / 2), fb, pol);
+                        bulk_copy(dst + BR * (D / 2), src + (ps + r0) * (D / 2), BR * (D / 2), fb, pol);
+                        bulk_copy(dst + BR * D, src + (size_t)ps * D + r0 * (NG * 4), BR * NG * 4, fb, pol);
+                        bulk_copy(dst + BR * (D + NG * 4), src + (size_t)ps * D + (ps + r0) * (NG * 4), BR * NG * 4, fb, pol);
+                    }
+                }
+                if (++s == NS) {
+                    s = 0;
+                    ph ^= 1u;
+                }
+            }
+            it = __shfl_sync(0xffffffffu, nxt, 0);
+        }
+        if (ok && mbar_wait(smem_u32(&empty_bar[s]), ph ^ 1u, ctrl, tmo)) {
+            if (lane == 0) {
+                meta[s][mStop] = 1;
+                mbar_arrive(smem_u32(&full_bar[s]));
+            }
+        } else {
+            // gave up: let the copies already issued land before leaving
+            for (int i = 0; i < NS; ++i) mbar_wait(smem_u32(&full_bar[i]), 0, ctrl, tmo);
+        }
+        return;
+    }
+
+    // =============================== consumers ===============================
+    // Thread (g = lane / 4, t = lane % 4) holds, of S^T, rows 2t and 2t + 1 of keys g and g + 8 of each 16; of O^T those rows of
+    // channels 32 c + 4 g .. + 3.
+    const int w = warp, g = lane >> 2, t = lane & 3;
+    const int G = a.G, Hq = a.Hq;
+    float* red_o = reinterpret_cast<float*>(smem + NS * Gm::STAGE);  // [kCW][R][LD]
+    const uint32_t mb = smem_u32(&merge_bar);
+    int s = 0;
+    uint32_t ph = 0, mph = 0;
+    uint32_t qf[NT][C][4];
+    float qs[NT][2][NG];          // sums of q over a group, times 2^-20
+    float o_acc[C][2][NT][4];     // [.][i][.][0, 1]: channel 32 c + 4 g + 2 i, rows 2t, 2t + 1, times 2^-24; [2, 3]: the next channel, times 2^-20
+    float psum[NT][NG][4];        // sums of P (rows 2t, 2t + 1, twice)
+    float zs[NT][2][NG];          // sums of p (z + 8 s) over this thread's keys
+    float m_r[NT][2], l_r[NT][2];
+    int pos[NT][2];
+    constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
+    for (;;) {
+        if (!mbar_wait(smem_u32(&full_bar[s]), ph, ctrl, tmo)) return;
+        const int* m = meta[s];
+        if (m[mStop]) return;
+        const int st = m[mSt], nst = m[mNst];
+        const int kv_begin = m[mKvBegin], kv_end = m[mKvEnd];
+        const int tok0 = m[mTok0], ntok = m[mNtok];
+        const int p_lo = m[mKl] - m[mQl] + tok0;
+        if (st == 0) {
+            const int rows = ntok * G, q_start = m[mQStart], head = m[mHead];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                // row 8 nt + g of Q: channels 32 c + 8 t .. + 7 of each chunk, paired as the masks pair the codes
+                const int r = 8 * nt + g;
+                const bool live = r < rows;
+                const size_t e = ((size_t)(q_start + tok0 + (live ? r / G : 0)) * Hq + head * G + (live ? r % G : 0)) * D + 8 * t;
+                float sum[NG];
+#pragma unroll
+                for (int i = 0; i < NG; ++i) sum[i] = 0.f;
+                uint4 x[C];
+#pragma unroll
+                for (int c = 0; c < C; ++c) x[c] = live ? load_q8(a.q, e + 32 * c, p.qdt) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+                for (int c = 0; c < C; ++c) {
+                    qf[nt][c][0] = __byte_perm(x[c].x, x[c].z, 0x5410);  // channels 0, 4
+                    qf[nt][c][1] = __byte_perm(x[c].y, x[c].w, 0x5410);  // 2, 6
+                    qf[nt][c][2] = __byte_perm(x[c].x, x[c].z, 0x7632);  // 1, 5
+                    qf[nt][c][3] = __byte_perm(x[c].y, x[c].w, 0x7632);  // 3, 7
+                    const uint32_t xs[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float2 f = f16x2_to_f32x2(xs[i]);
+                        sum[c / CPG] += f.x + f.y;
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < NG; ++i) {
+                    sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
+                    sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
+#pragma unroll
+                    for (int ri = 0; ri < 2; ++ri) {
+                        qs[nt][ri][i] = __shfl_sync(0xffffffffu, sum[i], 4 * (2 * t + ri)) * 9.5367431640625e-7f;
+                        zs[nt][ri][i] = 0.f;
+                    }
+                    psum[nt][i][0] = psum[nt][i][1] = psum[nt][i][2] = psum[nt][i][3] = 0.f;
+                }
+#pragma unroll
+                for (int ri = 0; ri < 2; ++ri) {
+                    m_r[nt][ri] = -INFINITY;
+                    l_r[nt][ri] = 0.f;
+                    pos[nt][ri] = p_lo + (8 * nt + 2 * t + ri) / G;
+                }
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        o_acc[c][i][nt][0] = o_acc[c][i][nt][1] = o_acc[c][i][nt][2] = o_acc[c][i][nt][3] = 0.f;
+            }
+        }
+        // ---- this warp's 32 keys: [kw, kw + 32)
+        const int kw = m[mKey0] + 32 * w;
+        if (kw < kv_end && kw + 32 > kv_begin) {
+            const uint32_t swz = (uint32_t)m[mSwz], stage = smem0 + s * Gm::STAGE;
+            const bool need_mask = kw < kv_begin || kw + 32 > kv_end || (a.causal && kw + 31 > p_lo) ||
+                                   (a.has_window && kw <= p_lo + ntok - 1 - a.window);
+            uint32_t row[2], sw[2], kvm[2];  // per 16 keys: this lane's row of codes, its chunks' place, the pairs of key g
+            float x[2][NT][4];
+            uint32_t vm[2][2][NG];
+#pragma unroll
+            for (int sub = 0; sub < 2; ++sub) {
+                const int kk = 32 * w + 16 * sub + (lane & 15);
+                const int r8 = (int)((swz >> (kk >> 2)) & 1u) * 4 + (kk & 3);
+                row[sub] = stage + (kk >> brs) * RB + (kk & (BR - 1)) * (D / 2);
+                sw[sub] = (uint32_t)(r8 * D / 256) & (C - 1);
+                uint32_t km[2][NG];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int kg = 32 * w + 16 * sub + g + 8 * h;
+                    kvm[h] = stage + (kg >> brs) * RB + BR * D + (kg & (BR - 1)) * (NG * 4);
+                    load_meta<NG>(kvm[h], km[h]);
+                    load_meta<NG>(kvm[h] + BR * NG * 4, vm[sub][h]);
+                }
+                float e[NT][4], o[NT][4];
+#pragma unroll
+                for (int c = 0; c < C; c += 2) {
+                    uint32_t f[4];
+                    ldsm_x4(row[sub] + (((uint32_t)(c + (lane >> 4)) ^ sw[sub]) << 4), f[0], f[1], f[2], f[3]);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int cc = c + h;
+                        const uint32_t u0 = f[2 * h], u1 = f[2 * h + 1], v0 = u0 >> 8, v1 = u1 >> 8;
+                        const uint32_t ae[4] = {u0 & kLow, u1 & kLow, v0 & kLow, v1 & kLow};
+                        const uint32_t ao[4] = {u0 & kHigh, u1 & kHigh, v0 & kHigh, v1 & kHigh};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            if (cc % CPG == 0) {
+                                e[nt][0] = e[nt][1] = e[nt][2] = e[nt][3] = 0.f;
+                                o[nt][0] = o[nt][1] = o[nt][2] = o[nt][3] = 0.f;
+                            }
+                            mma16816<true>(e[nt], ae, qf[nt][cc][0], qf[nt][cc][1]);
+                            mma16816<true>(o[nt], ao, qf[nt][cc][2], qf[nt][cc][3]);
+                        }
+                        if ((cc + 1) % CPG == 0) {
+                            const int gi = cc / CPG;
+#pragma unroll
+                            for (int hk = 0; hk < 2; ++hk) {
+                                const float2 sz = f16x2_to_f32x2(km[hk][gi]);
+#pragma unroll
+                                for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                                    for (int ri = 0; ri < 2; ++ri) {
+                                        const int i = 2 * hk + ri;
+                                        const float y = fmaf(sz.x, fmaf(16.f, e[nt][i], o[nt][i]), sz.y * qs[nt][ri][gi]);
+                                        x[sub][nt][i] = gi == 0 ? y : x[sub][nt][i] + y;
+                                    }
+                                }
+                            }
+                        }
+                    }
+                }
+            }
+            // ---- scale, soft cap, masks (log2 domain); x[sub][nt][i]: key g + 8 (i >> 1) of 16, row 8 nt + 2t + (i & 1)
+            uint32_t seen = 0;  // keys that are inside the range: their scales count (others may hold any bits)
+            float mx[NT][2];
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mx[nt][0] = mx[nt][1] = -INFINITY;
+#pragma unroll
+            for (int sub = 0; sub < 2; ++sub) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int ri = i & 1;
+                        float y = x[sub][nt][i];
+                        if (a.has_cap) {
+                            const float u = ex2(y * (a.cap_exp * 1048576.f));
+                            y = a.cap_log2 - 2.f * a.cap_log2 * rcp_approx(1.f + u);
+                        } else {
+                            y *= a.qk_log2 * 1048576.f;
+                        }
+                        if (need_mask) {
+                            const int j = kw + 16 * sub + g + 8 * (i >> 1);
+                            const bool in = j >= kv_begin && j < kv_end;
+                            if (in) seen |= 1u << (2 * sub + (i >> 1));
+                            const bool okk = in && (!a.causal || j <= pos[nt][ri]) &&
+                                             (!a.has_window || j > pos[nt][ri] - a.window || j < a.first);
+                            y = okk ? y : -INFINITY;
+                        }
+                        x[sub][nt][i] = y;
+                        mx[nt][ri] = fmaxf(mx[nt][ri], y);
+                    }
+                }
+            }
+            if (need_mask) {
+#pragma unroll
+                for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int i = 0; i < NG; ++i)
+                            if (!(seen >> (2 * sub + h) & 1u)) vm[sub][h][i] = 0u;
+            }
+            bool grew = false;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int ri = 0; ri < 2; ++ri) {
+                    float v = mx[nt][ri];
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                    mx[nt][ri] = v;
+                    grew |= v > m_r[nt][ri] + kRescale;
+                }
+            if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int ri = 0; ri < 2; ++ri) {
+                        const float m_new = fmaxf(m_r[nt][ri], mx[nt][ri]);
+                        const float alpha = m_r[nt][ri] == -INFINITY ? 0.f : ex2(m_r[nt][ri] - m_new);
+                        m_r[nt][ri] = m_new;
+                        l_r[nt][ri] *= alpha;
+#pragma unroll
+                        for (int i = 0; i < NG; ++i) {
+                            zs[nt][ri][i] *= alpha;
+                            psum[nt][i][ri] *= alpha;
+                        }
+#pragma unroll
+                        for (int c = 0; c < C; ++c)
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                o_acc[c][i][nt][ri] *= alpha;
+                                o_acc[c][i][nt][ri + 2] *= alpha;
+                            }
+                    }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int ri = 0; ri < 2; ++ri) {
+                    const float base = m_r[nt][ri] == -INFINITY ? 0.f : m_r[nt][ri];
+#pragma unroll
+                    for (int sub = 0; sub < 2; ++sub)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float pe = ex2(x[sub][nt][2 * h + ri] - base);
+                            x[sub][nt][2 * h + ri] = pe;
+                            l_r[nt][ri] += pe;
+                        }
+                }
+            // ---- O^T += V^T P^T, group by group
+#pragma unroll
+            for (int sub = 0; sub < 2; ++sub) {
+                uint32_t pb[NT][2];
+#pragma unroll
+                for (int c = 0; c < C; c += 2) {
+                    uint32_t f[4];
+                    ldsm_x4_t(row[sub] + BR * (D / 2) + (((uint32_t)(c + (lane >> 4)) ^ sw[sub]) << 4), f[0], f[1], f[2], f[3]);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int cc = c + h, gi = cc / CPG;
+                        if (cc % CPG == 0) {
+                            const float2 a0 = f16x2_to_f32x2(vm[sub][0][gi]), a1 = f16x2_to_f32x2(vm[sub][1][gi]);
+                            const float mid0 = fmaf(8.f, a0.x, a0.y), mid1 = fmaf(8.f, a1.x, a1.y);
+#pragma unroll
+                            for (int nt = 0; nt < NT; ++nt) {
+                                const float* y = x[sub][nt];
+                                zs[nt][0][gi] += fmaf(y[0], mid0, y[2] * mid1);
+                                zs[nt][1][gi] += fmaf(y[1], mid0, y[3] * mid1);
+                                pb[nt][0] = transposed(pack2<true>(y[0] * a0.x, y[1] * a0.x));
+                                pb[nt][1] = transposed(pack2<true>(y[2] * a1.x, y[3] * a1.x));
+                                constexpr uint32_t one = 0x3c003c00u;
+                                const uint32_t ones[4] = {one, one, one, one};
+                                mma16816<true>(psum[nt][gi], ones, pb[nt][0], pb[nt][1]);
+                            }
+                        }
+                        const uint32_t u0 = f[2 * h], u1 = f[2 * h + 1], v0 = u0 >> 8, v1 = u1 >> 8;
+                        const uint32_t a0[4] = {u0 & kLow, u0 & kHigh, u1 & kLow, u1 & kHigh};
+                        const uint32_t a1[4] = {v0 & kLow, v0 & kHigh, v1 & kLow, v1 & kHigh};
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            mma16816<true>(o_acc[cc][0][nt], a0, pb[nt][0], pb[nt][1]);
+                            mma16816<true>(o_acc[cc][1][nt], a1, pb[nt][0], pb[nt][1]);
+                        }
+                    }
+                }
+            }
+        }
+        const int head = m[mHead], q_start = m[mQStart], part = m[mPart];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&empty_bar[s]));
+        if (++s == NS) {
+            s = 0;
+            ph ^= 1u;
+        }
+        if (st != nst - 1) continue;
+        // ---- the item's end: merge the four warps' partials through shared memory
+        if (lane == 0) mbar_arrive(mb);  // A: every warp has read the merge area's last contents
+        if (!mbar_wait(mb, mph, ctrl, tmo)) return;
+        mph ^= 1u;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int ri = 0; ri < 2; ++ri) {
+                float l = l_r[nt][ri];
+                l += __shfl_xor_sync(0xffffffffu, l, 4);
+                l += __shfl_xor_sync(0xffffffffu, l, 8);
+                l += __shfl_xor_sync(0xffffffffu, l, 16);
+                const int r = 8 * nt + 2 * t + ri;
+                if (g == 0) {
+                    red_ml[w][r][0] = m_r[nt][ri];
+                    red_ml[w][r][1] = l;
+                }
+                float add[NG];
+#pragma unroll
+                for (int i = 0; i < NG; ++i) {
+                    float z = zs[nt][ri][i];
+                    z += __shfl_xor_sync(0xffffffffu, z, 4);
+                    z += __shfl_xor_sync(0xffffffffu, z, 8);
+                    z += __shfl_xor_sync(0xffffffffu, z, 16);
+                    add[i] = fmaf(-8.f, psum[nt][i][ri], z);
+                }
+                float* out = red_o + (w * R + r) * Gm::LD + 4 * g;
+#pragma unroll
+                for (int c = 0; c < C; ++c)
+                    *reinterpret_cast<float4*>(out + 32 * c) =
+                        make_float4(fmaf(o_acc[c][0][nt][ri], 16777216.f, add[c / CPG]), fmaf(o_acc[c][0][nt][ri + 2], 1048576.f, add[c / CPG]),
+                                    fmaf(o_acc[c][1][nt][ri], 16777216.f, add[c / CPG]), fmaf(o_acc[c][1][nt][ri + 2], 1048576.f, add[c / CPG]));
+            }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(mb);  // B: every partial is in shared memory
+        if (!mbar_wait(mb, mph, ctrl, tmo)) return;
+        mph ^= 1u;
+        const int rows = ntok * G;
+        for (int e = w * 32 + lane; e < rows * (D / 4); e += kCW * 32) {
+            const int r = e / (D / 4), c = (e % (D / 4)) * 4;
+            float M = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < kCW; ++i) M = fmaxf(M, red_ml[i][r][0]);
+            float L = 0.f;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (M != -INFINITY) {
+#pragma unroll
+                for (int i = 0; i < kCW; ++i) {
+                    const float sc = ex2(red_ml[i][r][0] - M);
+                    L += sc * red_ml[i][r][1];
+                    const float4 v = *reinterpret_cast<const float4*>(red_o + (i * R + r) * Gm::LD + c);
+                    o.x += sc * v.x;
+                    o.y += sc * v.y;
+                    o.z += sc * v.z;
+                    o.w += sc * v.w;
+                }
+            }
+            if (part < 0) {
+                const int tok = q_start + tok0 + r / G, qh = head * G + r % G;
+                L = add_sink(L, a.sinks, qh, M);
+                const float inv = L > 0.f ? a.v_scale / L : 0.f;
+                store_o4(a.o, ((size_t)tok * Hq + qh) * D + c, o.x * inv, o.y * inv, o.z * inv, o.w * inv, a.odt);
+            } else {
+                *reinterpret_cast<float4*>(a.part_o + ((size_t)part * kDecRows + r) * D + c) = o;
+                if (c == 0) *reinterpret_cast<float2*>(a.part_ml + ((size_t)part * kDecRows + r) * 2) = make_float2(M, L);
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- long prompts: the cache's rows in f16
+struct UnfoldParams {
+    const uint8_t* kv;
+    uint8_t* rows;       // [room pages][64][2 Hkv][D] f16
+    int* table;          // [max_num_seqs][P64]
+    const int *kv_lens, *page_indices, *cu, *vbase;
+    const uint8_t* q;    // rounded to f16 into qbuf (where qbuf is set)
+    uint8_t* qbuf;
+    int* ctrl;
+    int S, T, Hq, Hkv, D, ps, P, N, P64, group, qdt;
+    int has_window, window, first;
+};
+
+constexpr int kUnfoldThreads = 256, kUnfoldCtas = 6;
+
+__global__ void __launch_bounds__(kUnfoldThreads, kUnfoldCtas) rpa_int4_unfold(const UnfoldParams p) {
+    pdl_trigger();
+    pdl_wait();
+    if (p.ctrl[kNumPfItems] == 0) return;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int total = p.vbase[p.S], per_row = p.D / 16;
+    __shared__ int s_seq;
+    // a task: 64 keys of one kv head
+    for (int task = blockIdx.x; task < total * p.Hkv; task += gridDim.x) {
+        const int v = task / p.Hkv, h = task - v * p.Hkv;
+        __syncthreads();
+        if (tid < 32) {
+            const int s = find_seq(p.vbase, p.S, v, lane);
+            if (lane == 0) s_seq = s;
+        }
+        __syncthreads();
+        const int s = s_seq;
+        if (s < 0) continue;  // (not reached: vbase covers the pages)
+        const int ql = p.cu[s + 1] - p.cu[s], kl = p.kv_lens[s];
+        int lo = p.has_window ? max(0, kl - ql - p.window + 1) : 0;
+        if (lo <= p.first) lo = 0;
+        const int nf = lo > 0 ? (p.first + 63) / 64 : 0, at = v - p.vbase[s];
+        const int page64 = at < nf ? at : lo / 64 + at - nf;
+        if (h == 0 && tid == 0) p.table[(size_t)s * p.P64 + page64] = v;
+        for (int u = tid; u < 64 * 2 * per_row; u += kUnfoldThreads) {
+            const int place = u % per_row, slot = u / per_row % 64, is_v = u / per_row / 64;
+            const int j = page64 * 64 + slot;
+            if (j >= kl) continue;  // (rows past the last are masked, whatever they hold)
+            const int pg = p.page_indices[(size_t)s * p.P + j / p.ps], ks = j % p.ps;
+            uint4 out[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+            if ((unsigned)pg < (unsigned)p.N) {
+                const uint8_t* block = p.kv + ((size_t)pg * p.Hkv + h) * ((size_t)p.ps * int4_key_bytes(p.D, p.group));
+                const size_t line = (size_t)(is_v ? p.ps : 0) + ks;
+                const uint2 codes = *reinterpret_cast<const uint2*>(block + line * (p.D / 2) + int4_chunk(place / 2, ks, p.D) * 16 + (place & 1) * 8);
+                const float2 sz = f16x2_to_f32x2(reinterpret_cast<const uint32_t*>(block + (size_t)p.ps * p.D)[line * (p.D / p.group) +
+                                                                                                             16 * place / p.group]);
+                const uint32_t w[2] = {codes.x, codes.y};
+                float f[16];
+#pragma unroll
+                for (int k = 0; k < 16; ++k) {
+                    // rounded to f16, a step of the scale / 15 at most for the sizes that meet in a group; the greatest code of a
+                    // group that ends at f16's largest value may pass it by the scale's rounding
+                    const float y = fmaf(__uint_as_float(((w[k / 8] >> (4 * (k % 8))) & 15u) | 0x4b000000u) - 8388608.f, sz.x, sz.y);
+                    f[k] = y > 65504.f ? 65504.f : y;
+                }
+#pragma unroll
+                for (int k = 0; k < 2; ++k)
+                    out[k] = make_uint4(pack2<true>(f[8 * k], f[8 * k + 1]), pack2<true>(f[8 * k + 2], f[8 * k + 3]),
+                                        pack2<true>(f[8 * k + 4], f[8 * k + 5]), pack2<true>(f[8 * k + 6], f[8 * k + 7]));
+            } else {
+                // (pages that no token of the call sees are not checked: the range of its page of 64 may be wider than the band)
+                const bool in = (j >= lo || j < p.first);
+                if (in) set_status(p.ctrl, RPA_ERR_BAD_PAGE_INDEX);
+            }
+            uint4* dst = reinterpret_cast<uint4*>(p.rows + ((((size_t)v * 64 + slot) * 2 * p.Hkv + 2 * h + is_v) * p.D + 16 * place) * 2);
+            dst[0] = out[0];
+            dst[1] = out[1];
+        }
+    }
+    if (p.qbuf) {
+        const size_t n = (size_t)p.T * p.Hq * p.D / 8;
+        for (size_t i = (size_t)blockIdx.x * kUnfoldThreads + tid; i < n; i += (size_t)gridDim.x * kUnfoldThreads)
+            reinterpret_cast<uint4*>(p.qbuf)[i] = load_q8(p.q, i * 8, p.qdt);
+    }
+}
+
+template <int D, int NG, int NT>
+struct I4Kern {
+    using Gm = I4Geom<D, NG, NT>;
+    static cudaError_t prepare(int* bps) {
+        cudaError_t e = cudaFuncSetAttribute(rpa_int4_attn<D, NG, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Gm::SMEM);
+        if (e != cudaSuccess) return e;
+        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(bps, rpa_int4_attn<D, NG, NT>, kI4Threads, Gm::SMEM);
+    }
+    static cudaError_t launch(const I4Params& p, const Launch& l) {
+        return launch_pdl(rpa_int4_attn<D, NG, NT>, l.grid, kI4Threads, Gm::SMEM, l.stream, p);
+    }
+};
+
+template <int D, int NG, typename Op>
+cudaError_t i4_rows(int rows, Op op) {
+    if constexpr (D < 256) {
+        if (rows == 16) return op(I4Kern<D, NG, 2>{});
+    }
+    return rows == 8 ? op(I4Kern<D, NG, 1>{}) : cudaErrorInvalidValue;
+}
+template <typename Op>
+cudaError_t i4_dispatch(int D, int group, int rows, Op op) {
+    if (D == 64) return group == 32 ? i4_rows<64, 2>(rows, op) : group == 64 ? i4_rows<64, 1>(rows, op) : cudaErrorInvalidValue;
+    if (D == 128) return group == 32 ? i4_rows<128, 4>(rows, op) : group == 64 ? i4_rows<128, 2>(rows, op) : i4_rows<128, 1>(rows, op);
+    if (D == 256) return group == 32 ? i4_rows<256, 8>(rows, op) : group == 64 ? i4_rows<256, 4>(rows, op) : i4_rows<256, 2>(rows, op);
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace
+
+cudaError_t int4_prepare(int D, int group, int rows, int* bps) {
+    return i4_dispatch(D, group, rows, [&](auto k) { return decltype(k)::prepare(bps); });
+}
+
+int enqueue_int4(const RpaCfg& c, const KernelSet& ks, const Workspace& ws, MapCache* maps, const AttnParams& a, int num_seqs,
+                 const EnqueueOpts& eo) {
+    cudaStream_t st = eo.st;
+    auto rec = [&](int k) { return !eo.ev[k] || cudaEventRecord(eo.ev[k], st) == cudaSuccess; };
+    const bool has_q = c.num_q_tokens > 0;
+    if (!rec(kEvDecStart)) return RPA_ERR_CUDA;
+    if (has_q) {
+        I4Params p;
+        p.a = a;
+        p.a.units = ws.dec_units;
+        p.a.item_count_word = kNumDecItems;
+        p.a.counter_word = kDecCounter;
+        p.blocks = ks.G / ks.Gp;
+        p.BR = kKS;
+        while (c.page_size % p.BR) p.BR >>= 1;
+        p.brs = 0;
+        while ((1 << p.brs) < p.BR) ++p.brs;
+        p.block = (size_t)c.page_size * int4_key_bytes(ks.D, ks.group);
+        p.qdt = ks.odt;
+        p.stall = eo.debug_stall;
+        p.timeout_ns = eo.timeout_ns;
+        if (i4_dispatch(ks.D, ks.group, ks.dec_rows,
+                        [&](auto k) { return decltype(k)::launch(p, Launch{ks.sms * ks.dec_bps, st}); }) != cudaSuccess)
+            return RPA_ERR_CUDA;
+    }
+    if (!rec(kEvDecEnd) || !rec(kEvPfStart)) return RPA_ERR_CUDA;
+    if (has_q && ks.room_pages > 0) {
+        UnfoldParams u;
+        u.kv = a.kv;
+        u.rows = ws.room;
+        u.table = ws.room_table;
+        u.kv_lens = a.kv_lens;
+        u.page_indices = a.page_indices;
+        u.cu = a.cu_q_lens;
+        u.vbase = ws.vbase;
+        u.q = a.q;
+        u.qbuf = ws.qbuf;
+        u.ctrl = ws.ctrl;
+        u.S = num_seqs;
+        u.T = (int)c.num_q_tokens;
+        u.Hq = a.Hq;
+        u.Hkv = a.Hkv;
+        u.D = ks.D;
+        u.ps = a.ps;
+        u.P = a.P;
+        u.N = a.N;
+        u.P64 = ks.P64;
+        u.group = ks.group;
+        u.qdt = ks.odt;
+        u.has_window = a.has_window;
+        u.window = a.window;
+        u.first = a.first;
+        if (launch_pdl(rpa_int4_unfold, ks.sms * kUnfoldCtas, kUnfoldThreads, 0, st, u) != cudaSuccess) return RPA_ERR_CUDA;
+        const void* q16 = ws.qbuf ? ws.qbuf : a.q;
+        if (maps->kv_ptr != ws.room) {
+            if ((ks.tc8 ? encode_kv_map_heads(&maps->kv_pf, ws.room, ks.room_pages, 64, 2 * a.Hkv, ks.D, 64)
+                        : encode_kv_map(&maps->kv_pf, ws.room, 0, ks.room_pages, 64, a.Hkv, ks.D, 64)) != 0) {
+                maps->kv_ptr = nullptr;
+                return RPA_ERR_INVALID_ARG;
+            }
+            maps->kv_ptr = ws.room;
+        }
+        if (maps->q_ptr != q16) {
+            if (encode_q_map(&maps->q_pf, q16, c.num_q_tokens, a.Hq, ks.D, ks.G, kTcRows / ks.G) != 0) {
+                maps->q_ptr = nullptr;
+                return RPA_ERR_INVALID_ARG;
+            }
+            maps->q_ptr = q16;
+        }
+        TcParams tp;
+        tp.a = a;
+        tp.a.q = static_cast<const uint8_t*>(q16);
+        tp.a.kv = ws.room;
+        tp.a.page_indices = ws.room_table;
+        tp.a.G = ks.G;
+        tp.a.P = ks.P64;
+        tp.a.ps = 64;
+        tp.a.N = ks.room_pages;
+        tp.a.units = ws.pf_units;
+        tp.a.unit_heads = a.Hkv;
+        tp.a.item_count_word = kNumPfItems;
+        tp.a.counter_word = kPfCounter;
+        tp.BR = 64;
+        tp.Tq = ks.pf_tokens;
+        tp.timeout_ns = eo.timeout_ns;
+        const Launch l{ks.sms * ks.pf_bps, st};
+        if ((ks.tc8 ? launch_prefill_tc8(maps->kv_pf, maps->q_pf, tp, KT_F16, l) : launch_prefill_tc(maps->kv_pf, maps->q_pf, tp, KT_F16, l)) !=
+            cudaSuccess)
+            return RPA_ERR_CUDA;
+    }
+    return rec(kEvPfEnd) ? RPA_OK : RPA_ERR_CUDA;
+}
+
+}  // namespace rpa

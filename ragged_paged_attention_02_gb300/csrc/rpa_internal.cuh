@@ -83,6 +83,10 @@ template <typename T>
 __host__ __device__ constexpr T int4_chunk(T c, T r, int D) {
     return c ^ ((r * D / 256) & (D / 32 - 1));
 }
+// Pages of 64 keys that a sequence's band [lo, hi) and, in front of a gap (lo > 0), its first keys take as f16 rows
+__host__ __device__ constexpr int int4_pages(int lo, int hi, int first) {
+    return (hi + 63) / 64 - lo / 64 + (lo > 0 ? (first + 63) / 64 : 0);
+}
 // Output element types (o has the q dtype)
 enum OutType : int { OT_BF16 = 0, OT_F16 = 1, OT_F32 = 2 };
 
@@ -91,6 +95,8 @@ constexpr int kDecRows = 16;       // rows of a decode tile (one m16 MMA tile)
 constexpr int kMlaDqk = 576;
 constexpr int kMlaDv = 512;
 constexpr int kMlaRows = 16;
+constexpr int kInt4DirectRows = 64;       // 4-bit K/V: sequences with more query rows a kv head are unfolded to f16
+constexpr int kInt4MaxRoom = 1 << 20;     // pages of 64 keys (the planner's sums of refused sequences count to this)
 constexpr int kMaxGroup = 64;      // query heads per kv head (a prefill tile holds 128 / G tokens)
 constexpr int kDecWaves = 4;       // target decode items per resident CTA (the most of any kernel)
 // ... on the 64-key-tile kernel, whose items pay a Q load into tensor memory and a pipeline ramp
@@ -139,6 +145,12 @@ struct PlanParams {
     int dec_waves;       // target decode items per CTA of the kernel that runs them
     int epoch;           // this call's number, published in ctrl[kPlanEpoch] once the plan is out
     int early;           // the inputs are complete at launch: read them before the grid dependency
+    // 4-bit K/V: decode units are tiles of dec_tokens tokens, of any sequence; one with more than direct_tokens tokens becomes
+    // prefill units where the f16 room has pages (of 64 keys) left for it
+    int int4, dec_tokens, direct_tokens;
+    int pf_Hkv;      // kv heads a prefill unit stands for
+    int room_pages;
+    int* vbase;      // [max_num_seqs + 1]: a sequence's first page of the room (ascending; none: the next one's)
     int max_units;   // capacity of the unit arrays
     int max_dec_units, max_pf_units;  // capacities of the two unit lists
     int max_part;    // capacity of partial slots
@@ -284,6 +296,8 @@ struct ReadParams {
     int kt, group;  // KvType of the cache, channels of a group of a 4-bit cache
     float k_scale, v_scale;
 };
+// 4-bit K/V (rows: 8 or 16 query rows of a tile); the attention kernels of one call, between its planner and its merge
+cudaError_t int4_prepare(int D, int group, int rows, int* blocks_per_sm);
 cudaError_t launch_read(const ReadParams& p, int q_dtype, int sms, cudaStream_t st);
 // occupancy / attributes (call once per device)
 size_t plan_smem_bytes();
@@ -302,6 +316,9 @@ struct KernelSet {
     int tc, tc8;         // prefill on the tensor-memory kernel for 2-byte / 8-bit K/V
     int dec_rows, pf_tokens, Tt, BR, br_shift, window, first;
     float qk_log2, cap_exp, cap_log2, v_scale;
+    // 4-bit K/V: channels of a group; kv heads of a prefill unit; most tokens of a sequence that the direct kernel takes; the room
+    // for f16 rows of longer prompts, in pages of 64 keys, and its page table's columns
+    int group, pf_H, direct_tokens, room_pages, P64;
     int sms, dec_bps, pf_bps;
     int max_dec_units, max_pf_units, max_units, max_part, max_comb;
 };
@@ -319,7 +336,10 @@ struct Workspace {
     Comb* comb;
     float* part_o;
     float* part_ml;
-    uint8_t* qbuf;  // q in the MMA operand type (when KernelSet::q_conv)
+    uint8_t* qbuf;  // q in the MMA operand type (when KernelSet::q_conv, or of f16 rows' prompts)
+    int* vbase;       // 4-bit K/V: [max_num_seqs + 1] (PlanParams::vbase)
+    int* room_table;  // [max_num_seqs][P64] pages of the room
+    uint8_t* room;    // [room_pages][64][2 Hkv][D] f16
 };
 // Tensor maps of the last call, re-encoded when the pointers change
 struct MapCache {
@@ -364,6 +384,8 @@ AttnParams attn_params(const RpaCfg& c, const KernelSet& ks, const Workspace& ws
                        const int32_t* kv_lens, const int32_t* page_indices, const int32_t* cu_q_lens, void* o);
 int enqueue_attention(const RpaCfg& c, const KernelSet& ks, const Workspace& ws, MapCache* maps, const AttnParams& a,
                       const EnqueueOpts& eo);
+int enqueue_int4(const RpaCfg& c, const KernelSet& ks, const Workspace& ws, MapCache* maps, const AttnParams& a, int num_seqs,
+                 const EnqueueOpts& eo);
 // Enqueue one call; returns an RpaStatus.  Allocates nothing.
 int enqueue_forward(const RpaCfg& c, const KernelSet& ks, const Workspace& ws, MapCache* maps, const void* q,
                     const void* kv_pages, const int32_t* kv_lens, const int32_t* page_indices,

@@ -53,7 +53,7 @@ int out_type(int32_t dt) { return dt == RPA_DT_F32 ? OT_F32 : dt == RPA_DT_F16 ?
 
 // Byte offsets of the workspace's parts (one layout for the handle and the fixed array)
 struct Layout {
-    size_t ctrl, seq, units, dec, pf, comb, po, pml, qbuf, total;
+    size_t ctrl, seq, units, dec, pf, comb, po, pml, qbuf, vbase, table, room, total;
 };
 
 Layout layout(const RpaCfg& c, const KernelSet& ks) {
@@ -69,7 +69,13 @@ Layout layout(const RpaCfg& c, const KernelSet& ks) {
     L.po = off; off = align256(off + (size_t)ks.max_part * kDecRows * ks.D * sizeof(float));
     L.pml = off; off = align256(off + (size_t)ks.max_part * kDecRows * 2 * sizeof(float));
     L.qbuf = off;
-    if (ks.q_conv) off = align256(off + (size_t)c.num_q_tokens * c.num_q_heads * ks.D * 2);
+    if (ks.q_conv || (ks.room_pages > 0 && c.q_dtype != RPA_DT_F16))
+        off = align256(off + (size_t)c.num_q_tokens * c.num_q_heads * ks.D * 2);
+    L.vbase = off;
+    if (ks.kt == KT_I4) off = align256(off + (size_t)(S + 1) * sizeof(int));
+    L.table = off;
+    if (ks.room_pages > 0) off = align256(off + (size_t)S * ks.P64 * sizeof(int));
+    L.room = off; off = align256(off + (size_t)ks.room_pages * 64 * 2 * c.num_kv_heads * ks.D * 2);
     L.total = off;
     return L;
 }
@@ -88,13 +94,25 @@ void kernels_choose(const RpaCfg& c, int sms, KernelSet* ks) {
     // heads are planned as blocks of up to 16 ("kv heads" of the planner, reading one latent row)
     ks->Gp = ks->mla && ks->G > kMlaRows ? kMlaRows : ks->G;
     ks->Hp = (int)c.num_kv_heads * (ks->G / ks->Gp);
+    ks->pf_H = ks->Hp;
+    if (ks->kt == KT_I4) {
+        // tiles of 16 query rows where a kv head has more than 8 query heads (D 256: always 8; registers), of a divisor of its heads
+        ks->group = int4_group(c.kv_dtype);
+        ks->dec_rows = ks->G <= 8 || ks->D == 256 ? 8 : kDecRows;
+        ks->Gp = ks->G < ks->dec_rows ? ks->G : ks->dec_rows;
+        while (ks->G % ks->Gp) --ks->Gp;
+        ks->Hp = (int)c.num_kv_heads * (ks->G / ks->Gp);
+        ks->pf_H = (int)c.num_kv_heads;
+    }
     const bool eight = kt_8bit(ks->kt);
     // the MMA operands of Q: bf16 with bf16 K/V, f16 otherwise; q of another type is rounded
     // into the workspace first, except bf16 q with 8-bit K/V, which the kernels round to f16 as
     // they load it
     const bool want_f16 = ks->kt != KT_BF16;
     const int qd = c.q_dtype;
-    if (qd == RPA_DT_F32) {
+    if (ks->kt == KT_I4) {
+        // (the direct kernel rounds q as it loads it, the prompts' f16 copy is made with their rows')
+    } else if (qd == RPA_DT_F32) {
         ks->q_conv = 1;
         ks->q_conv_f16 = want_f16;
     } else if (qd == RPA_DT_F16 && !want_f16) {
@@ -117,8 +135,8 @@ void kernels_choose(const RpaCfg& c, int sms, KernelSet* ks) {
     ks->br_shift = 0;
     while ((1 << ks->br_shift) < ks->BR) ++ks->br_shift;
     // 8-row decode tiles (keys on the MMA's M side) whenever a group fits: 2-byte K/V, G <= 8
-    ks->dec_rows = (!eight && ks->G <= 8) ? 8 : kDecRows;
-    ks->Tt = ks->G <= ks->dec_rows ? ks->dec_rows / ks->G : 1;
+    if (ks->kt != KT_I4) ks->dec_rows = (!eight && ks->G <= 8) ? 8 : kDecRows;
+    ks->Tt = ks->Gp <= ks->dec_rows ? ks->dec_rows / ks->Gp : 1;
     ks->tc = (!ks->mla && !eight && (ks->D == 64 || ks->D == 128)) ? 1 : 0;
     // the 64-key-tile tensor-memory kernel: 8-bit K/V (converted to f16), and 2-byte K/V at D 256
     // (copied straight into its tiles)
@@ -131,17 +149,33 @@ void kernels_choose(const RpaCfg& c, int sms, KernelSet* ks) {
         ks->Tt = kMlaRows / ks->Gp;
         ks->pf_tokens = ks->Tt;
     }
+    if (ks->kt == KT_I4) {
+        ks->direct_tokens = kInt4DirectRows / ks->G > ks->Tt ? kInt4DirectRows / ks->G : ks->Tt;
+        // room for prompts of longer sequences: 2^18 keys of 8 heads at D 128 (1 GiB), the longest sequence at least, all of them at most
+        const int64_t page = 64 * 4 * c.num_kv_heads * c.head_dim, most = (c.pages_per_seq * c.page_size + 63) / 64;
+        ks->P64 = (int)most;
+        if (c.num_q_tokens > ks->direct_tokens) {
+            int64_t pages = ((int64_t)1 << 30) / page;
+            if (pages < most + 1) pages = most + 1;
+            if (pages > c.max_num_seqs * (most + 1)) pages = c.max_num_seqs * (most + 1);
+            ks->room_pages = (int)(pages < kInt4MaxRoom ? pages : kInt4MaxRoom);
+        }
+    }
     ks->sms = sms;
 }
 
 cudaError_t kernels_occupancy(KernelSet* ks) {
     cudaError_t e = plan_prepare();
     if (e != cudaSuccess) return e;
+    const int pf_kt = ks->kt == KT_I4 ? KT_F16 : ks->kt;  // prompts over a 4-bit cache: f16 rows
     e = ks->mla  ? mla_prepare(ks->kt, &ks->pf_bps)
-        : ks->tc ? prefill_tc_prepare(ks->D, ks->kt, &ks->pf_bps)
-                 : prefill_tc8_prepare(ks->D, ks->kt, &ks->pf_bps);
+        : ks->tc ? prefill_tc_prepare(ks->D, pf_kt, &ks->pf_bps)
+                 : prefill_tc8_prepare(ks->D, pf_kt, &ks->pf_bps);
     if (e != cudaSuccess) return e;
-    if (ks->tc8 || ks->mla) {
+    if (ks->kt == KT_I4) {
+        e = int4_prepare(ks->D, ks->group, ks->dec_rows, &ks->dec_bps);
+        if (e != cudaSuccess) return e;
+    } else if (ks->tc8 || ks->mla) {
         // the 8-bit tensor-memory kernel (and the latent kernel) takes the decode rows too: the
         // decode kernel never runs
         ks->dec_bps = ks->pf_bps;
@@ -167,6 +201,14 @@ void kernels_capacity(const RpaCfg& c, KernelSet* ks) {
     ks->max_pf_units = (ks->tc8 || ks->mla) ? ks->max_units : pf_only_units;
     ks->max_part = (int)(ks->max_dec_units * Hkv);
     ks->max_comb = (int)(S * Hkv);
+    if (ks->kt == KT_I4) {
+        // a sequence makes tiles of Tt tokens; those with several pieces have at most twice the pieces that the chunk rule aims at
+        ks->max_dec_units += (int)(c.num_q_tokens / ks->Tt + 1);
+        ks->max_units = ks->max_dec_units + pf_only_units;
+        ks->max_pf_units = pf_only_units;
+        ks->max_part = (int)(2 * (kDecWaves * dec_slots + Hkv));
+        ks->max_comb = ks->max_part / 2;
+    }
 }
 
 cudaError_t kernels_prepare(const RpaCfg& c, KernelSet* ks) {
@@ -189,7 +231,10 @@ Workspace workspace_carve(const RpaCfg& c, const KernelSet& ks, void* base) {
     w.comb = reinterpret_cast<Comb*>(b + L.comb);
     w.part_o = reinterpret_cast<float*>(b + L.po);
     w.part_ml = reinterpret_cast<float*>(b + L.pml);
-    w.qbuf = ks.q_conv ? b + L.qbuf : nullptr;
+    w.qbuf = L.vbase > L.qbuf ? b + L.qbuf : nullptr;
+    w.vbase = reinterpret_cast<int*>(b + L.vbase);
+    w.room_table = reinterpret_cast<int*>(b + L.table);
+    w.room = b + L.room;
     return w;
 }
 
@@ -394,8 +439,14 @@ int enqueue_forward(const RpaCfg& c, const KernelSet& ks, const Workspace& ws, M
     pp.n_sms = ks.sms;
     pp.dec_bps = ks.dec_bps;
     pp.pf_bps = ks.pf_bps;
+    pp.int4 = ks.kt == KT_I4;
+    pp.dec_tokens = ks.Tt;
+    pp.direct_tokens = ks.direct_tokens;
+    pp.pf_Hkv = ks.pf_H;
+    pp.room_pages = ks.room_pages;
+    pp.vbase = ws.vbase;
     pp.pf_mma_rows = ks.tc ? 2 * kTcRows : ks.mla ? kMlaRows : kTcRows;
-    pp.dec_on_pf = ks.tc8 || ks.mla;
+    pp.dec_on_pf = (ks.tc8 && !pp.int4) || ks.mla;
     pp.D = ks.D;
     pp.kv_elt = kt_8bit(ks.kt) ? 1 : 2;
     pp.pf_sm_gflops = ks.mla ? kPfSmGflopsMma : kPfSmGflopsTc;
@@ -403,7 +454,7 @@ int enqueue_forward(const RpaCfg& c, const KernelSet& ks, const Workspace& ws, M
     pp.hbm_gbs = kHbmGBs;
     pp.force_pf_sms = eo.force_pf_sms;
     pp.force_dec_sms = eo.force_dec_sms;
-    pp.dec_waves = ks.tc8 ? kDecWavesTc8 : kDecWaves;
+    pp.dec_waves = ks.tc8 && !pp.int4 ? kDecWavesTc8 : kDecWaves;
     pp.epoch = eo.epoch;
     pp.early = eo.plan_early;
     pp.max_units = ks.max_units;
@@ -422,7 +473,7 @@ int enqueue_forward(const RpaCfg& c, const KernelSet& ks, const Workspace& ws, M
     if (!rec(kEvPlanEnd, st)) return RPA_ERR_CUDA;
 
     const AttnParams ap = attn_params(c, ks, ws, qk, kv_pages, kv_lens, page_indices, cu_q_lens, o);
-    const int r = enqueue_attention(c, ks, ws, maps, ap, eo);
+    const int r = pp.int4 ? enqueue_int4(c, ks, ws, maps, ap, num_seqs, eo) : enqueue_attention(c, ks, ws, maps, ap, eo);
     if (r != RPA_OK) return r;
 
     CombParams cp;

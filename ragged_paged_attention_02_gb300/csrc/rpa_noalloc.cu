@@ -30,10 +30,10 @@ static __device__ __align__(256) unsigned char g_rpa_scratch[kNoAllocScratchByte
 
 std::mutex g_mu;
 void* g_scratch_dev[kMaxDevices];
-// occupancy per device and kernel choice: [device][D: 64, 128, 256, latent][KvType][8-row decode tiles]
-int g_dec_bps[kMaxDevices][4][5][2];
-int g_pf_bps[kMaxDevices][4][5][2];
-bool g_ready[kMaxDevices][4][5][2];
+// occupancy per device and kernel choice: [device][D: 64, 128, 256, latent][KvType, 4-bit ones by their group][8-row decode tiles]
+int g_dec_bps[kMaxDevices][4][8][2];
+int g_pf_bps[kMaxDevices][4][8][2];
+bool g_ready[kMaxDevices][4][8][2];
 
 int d_index(const KernelSet& ks) { return ks.mla ? 3 : ks.D == 64 ? 0 : ks.D == 128 ? 1 : 2; }
 
@@ -52,7 +52,7 @@ int setup(int dev, KernelSet* ks, void** scratch) {
         }
         g_scratch_dev[dev] = ptr;
     }
-    const int di = d_index(*ks), kt = ks->kt, r8 = ks->dec_rows == 8 ? 1 : 0;
+    const int di = d_index(*ks), kt = ks->kt + (ks->group > 32) + (ks->group > 64), r8 = ks->dec_rows == 8 ? 1 : 0;
     if (!g_ready[dev][di][kt][r8]) {
         if (kernels_occupancy(ks) != cudaSuccess) {
             cudaGetLastError();
@@ -76,7 +76,6 @@ extern "C" int rpa_forward_noalloc(const RpaCfg* cfg, const void* q, const void*
     const int v = rpa_validate_cfg(cfg);
     if (v != RPA_OK) return v;
     const RpaCfg& c = *cfg;
-    if (int4_group(c.kv_dtype)) return RPA_ERR_UNSUPPORTED;
     if (num_seqs < 0 || num_seqs > c.max_num_seqs) return RPA_ERR_INVALID_ARG;
     if (!kv_pages || !kv_lens || !page_indices || !cu_q_lens) return RPA_ERR_INVALID_ARG;
     if (c.num_q_tokens > 0 && (!q || !o)) return RPA_ERR_INVALID_ARG;
@@ -96,6 +95,7 @@ extern "C" int rpa_forward_noalloc(const RpaCfg* cfg, const void* q, const void*
     void* scratch = nullptr;
     const int su = setup(dev, &ks, &scratch);
     if (su != RPA_OK) return su;
+    ks.room_pages = 0;         // (4-bit K/V: every row on the direct kernel)
     kernels_capacity(c, &ks);  // the same worst-case workspace as rpa_create's
     if (workspace_bytes(c, ks) > kNoAllocScratchBytes) return RPA_ERR_NO_ALLOC_LIMIT;
     const Workspace ws = workspace_carve(c, ks, scratch);

@@ -54,12 +54,54 @@ __device__ __forceinline__ int first_shift(int lo, int chunk, const PlanParams& 
     return min(first_cost(lo, p), chunk - kChunkAlign);
 }
 
+// Tiles that a decode sequence's tokens make.
+__device__ __forceinline__ int dec_tiles(int ql, const PlanParams& p) {
+    return p.int4 ? (ql + p.dec_tokens - 1) / p.dec_tokens : 1;
+}
+__device__ __forceinline__ bool bad_lengths(int q0, int q1, int kl, const PlanParams& p) {
+    return q0 < 0 || q1 < q0 || kl < 0 || kl > p.P * p.ps || q1 - q0 > kl || q1 > p.T;
+}
+
+// 4-bit K/V: the sequences that become prefill units, in order as long as the room has pages (cls[s] 1), and where their pages
+// start.
+__device__ void give_room(const PlanParams& p, int* cls, int* scan, int* taken) {
+    const int S = p.num_seqs;
+    if (threadIdx.x == 0) *taken = 0;
+    int carry = 0;
+    for (int base = 0; base < S; base += blockDim.x) {
+        const int s = base + threadIdx.x;
+        int pages = 0;
+        if (s < S) {
+            const int q0 = p.cu_q_lens[s], q1 = p.cu_q_lens[s + 1], kl = p.kv_lens[s];
+            if (!bad_lengths(q0, q1, kl, p) && q1 - q0 > p.direct_tokens) {
+                int lo, hi;
+                key_band(kl, q1 - q0, 0, q1 - q0, p, lo, hi);
+                pages = int4_pages(lo, hi, p.first);
+            }
+        }
+        // (what is refused counts on: the sum stays past the room; it saturates far below an overflow)
+        const int v[1] = {min(pages, 1 << 20)};
+        int off[1], tot[1];
+        block_scan<1>(v, off, tot, scan);
+        if (s < S) {
+            const int start = min(carry + off[0], 1 << 29), end = min(start + pages, 1 << 30);
+            cls[s] = pages > 0 && end <= p.room_pages;
+            p.vbase[s] = start;
+            if (cls[s]) atomicMax(taken, end);
+        }
+        carry = min(carry + tot[0], 1 << 29);
+    }
+    __syncthreads();
+    for (int s = threadIdx.x; s <= S; s += blockDim.x) p.vbase[s] = s < S ? min(p.vbase[s], *taken) : *taken;
+}
+
 __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p) {
     extern __shared__ __align__(16) unsigned long long s_keys[];  // kMaxSort keys, then sequence scratch
     __shared__ int s_scan[33 * 5];
     __shared__ unsigned long long s_red[64];
     __shared__ int s_bad;
     __shared__ int s_split[2];                // prefill CTAs, decode CTAs
+    __shared__ int s_taken;                   // pages of the room that are given away
     const int tid = threadIdx.x;
     const int S = p.num_seqs;
     int* ctrl = p.ctrl;
@@ -68,7 +110,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
     // run while that kernel does.  Unless the caller has said that the inputs are complete at
     // launch (RPA_OPT_PLAN_EARLY), it waits for that kernel before reading them; either way it
     // waits before rewriting what earlier kernels read (below)
-    if (!p.early) pdl_wait();
+    // (4-bit K/V: vbase is written on the way)
+    if (!p.early || p.int4) pdl_wait();
     // per-sequence scratch (shared memory when it fits): class, count, decode / prefill
     // unit ends, partial offset, combine offset, decode sequences with a partial last piece before
     // this one, first query token (S + 1 entries: cu_q_lens), kv_len
@@ -87,6 +130,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
     if (tid == 0) s_bad = 0;
     __syncthreads();
 
+    if (p.int4) give_room(p, s_cls, s_scan, &s_taken);  // (each thread reads back its own entries of s_cls)
     // ---- 1. validate and classify each sequence; per-thread sums of decode (key, kv head)
     // pairs and of the keys prefill units visit, reduced over the block below
     unsigned long long my_total = 0ull, my_pf_keys = 0ull;
@@ -96,17 +140,17 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
         s_q0[s] = q0;
         if (s == S - 1) s_q0[S] = q1;
         s_kl[s] = kl;
-        const bool bad = q0 < 0 || ql < 0 || kl < 0 || kl > p.P * p.ps || ql > kl || q1 > p.T;
+        const bool bad = bad_lengths(q0, q1, kl, p);
         int cls = 0, cnt = 0;
         if (bad) {
             s_bad = 1;
         } else if (ql > 0) {
-            if ((long long)ql * p.G <= p.dec_rows) {
+            if (p.int4 ? !s_cls[s] : (long long)ql * p.G <= p.dec_rows) {
                 int lo, hi;
                 key_band(kl, ql, 0, ql, p, lo, hi);
                 cls = 1;
                 cnt = hi - lo;
-                my_total += (unsigned long long)(cnt + first_cost(lo, p)) * (unsigned long long)p.Hkv;
+                my_total += (unsigned long long)(cnt + first_cost(lo, p)) * (unsigned long long)(p.Hkv * dec_tiles(ql, p));
             } else {
                 cls = 2;
                 cnt = (ql + Tq - 1) / Tq;
@@ -203,11 +247,12 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
                 s_cnt[s] = cnt;
             }
             if (cls == 1) {
-                du = (cnt + chunk - 1) / chunk;
-                pp = cnt % chunk != 0 ? 1 : 0;  // a last piece shorter than the chunk
-                if (du > 1) {
+                const int tiles = dec_tiles(s_q0[s + 1] - s_q0[s], p), pieces = (cnt + chunk - 1) / chunk;
+                du = tiles * pieces;
+                pp = cnt % chunk != 0 ? tiles : 0;  // last pieces shorter than the chunk
+                if (pieces > 1) {
                     pa = du * p.Hkv;
-                    cb = p.Hkv;
+                    cb = tiles * p.Hkv;
                 }
             } else if (cls == 2) {
                 pu = cnt;
@@ -260,20 +305,23 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
         int pos;  // the key's slot: a whole-chunk piece at its rank, the others in the range sorted below
         if (u < n_dec) {
             const int s = upper_seq(s_dend, S, u);
-            const int k = u - (s_dend[s] - (s_cnt[s] + chunk - 1) / chunk);  // piece index
             const int ql = s_q0[s + 1] - s_q0[s], kl = s_kl[s];
+            const int pieces = (s_cnt[s] + chunk - 1) / chunk, tiles = dec_tiles(ql, p);
+            const int d0 = s_dend[s] - tiles * pieces;  // the sequence's first unit
+            const int tile = (u - d0) / pieces, k = (u - d0) - tile * pieces;  // and its tile and piece
+            const int t0 = p.int4 ? tile * p.dec_tokens : 0;
             int lo, hi;
             key_band(kl, ql, 0, ql, p, lo, hi);
-            const int pieces = (s_cnt[s] + chunk - 1) / chunk;
             const int at = lo + k * chunk - first_shift(lo, chunk, p);  // (piece 0 of a unit with a gap: before lo)
             const int kb = max(lo, at);
             const int ke = min(hi, at + chunk);
-            d[0] = s; d[1] = 0; d[2] = ql; d[3] = kb; d[4] = ke;
-            d[5] = pieces > 1 ? s_part[s] : -1;
+            d[0] = s; d[1] = t0; d[2] = p.int4 ? min(p.dec_tokens, ql - t0) : ql; d[3] = kb; d[4] = ke;
+            d[5] = pieces > 1 ? s_part[s] + tile * pieces * p.Hkv : -1;
             d[6] = k; d[7] = pieces;
             cost = ke - at;
             cls_bit = 0;
-            pos = cost == chunk ? (s_dend[s] - pieces - s_ppre[s]) + k : n_full + s_ppre[s];
+            const int full = s_cnt[s] / chunk;  // whole pieces of a tile
+            pos = cost == chunk ? (d0 - s_ppre[s]) + tile * full + k : n_full + s_ppre[s] + tile;
         } else {
             const int v = u - n_dec;
             const int s = upper_seq(s_pend, S, v);
@@ -402,8 +450,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
                 if (++s >= S) break;
             }
             if (s_cls[s] != 1) continue;
-            const int pieces = s_dend[s] - (s > 0 ? s_dend[s - 1] : 0);  // the sequence's decode units
-            if (pieces <= 1) continue;
+            const int pieces = (s_cnt[s] + chunk - 1) / chunk;
+            if (pieces <= 1 || (p.int4 && s_q0[s + 1] - s_q0[s] > p.dec_tokens)) continue;
             const int h = rem >> 1;
             // Comb: q0, rows, head, part | pieces, 0, 0, 0
             int4* d4 = reinterpret_cast<int4*>(p.comb + s_comb[s] + h);
@@ -413,12 +461,26 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
                 d4[1] = make_int4(pieces, 0, 0, 0);
         }
     }
+    // ... of sequences of several tiles (4-bit K/V): all threads on one sequence at a time
+    if (p.int4 && n_dec > 0) {
+        for (int s = 0; s < S; ++s) {
+            const int ql = s_q0[s + 1] - s_q0[s];
+            const int pieces = (s_cnt[s] + chunk - 1) / chunk;
+            if (ql <= p.dec_tokens || s_cls[s] != 1 || pieces <= 1) continue;
+            for (int i = tid; i < dec_tiles(ql, p) * p.Hkv; i += blockDim.x) {
+                const int tile = i / p.Hkv, h = i - tile * p.Hkv, t0 = tile * p.dec_tokens;
+                int4* d4 = reinterpret_cast<int4*>(p.comb + s_comb[s] + i);
+                d4[0] = make_int4(s_q0[s] + t0, min(p.dec_tokens, ql - t0) * p.G, h, s_part[s] + i * pieces);
+                d4[1] = make_int4(pieces, 0, 0, 0);
+            }
+        }
+    }
     // every thread's unit-list and combine-entry stores, before the plan is published
     __threadfence();
     __syncthreads();
     if (tid == 0) {
         ctrl[kNumDecItems] = p.dec_on_pf ? 0 : n_dec * p.Hkv;
-        ctrl[kNumPfItems] = (p.dec_on_pf ? n_units : n_pf) * p.Hkv;
+        ctrl[kNumPfItems] = p.dec_on_pf ? n_units * p.Hkv : n_pf * p.pf_Hkv;
         ctrl[kNumComb] = carry_comb;
         ctrl[kDecChunk] = chunk;
         ctrl[kDecCounter] = 0;

@@ -5,13 +5,14 @@ import math
 import numpy as np
 
 
-def attend64(q, q_lens, kv_lens, cu, rows, *, window=None, first=0, cap=None, causal=True, sinks=None, scale=None, Dv=None):
+def attend64(q, q_lens, kv_lens, cu, rows, *, window=None, first=0, cap=None, causal=True, sinks=None, scale=None, Dv=None,
+             step=None):
     """q [T, Hq, D] float64; rows(s) the K and V [keys, Hkv, D] of sequence s.  Returns o [T, Hq, Dv] and for each element the
-    sum of |p v|, which the rounding of the probabilities is relative to."""
+    sum of |p v|, which the rounding of the probabilities is relative to; step(s) [keys, Hkv, D]: and the sum of p step."""
     T, Hq, D = q.shape
     Dv = Dv or D
     scale = scale or 1 / math.sqrt(D)
-    o, size = np.zeros((T, Hq, Dv)), np.zeros((T, Hq, Dv))
+    o, size, steps = np.zeros((T, Hq, Dv)), np.zeros((T, Hq, Dv)), np.zeros((T, Hq, Dv))
     for s, (a, n) in enumerate(zip(q_lens, kv_lens)):
         if not a:
             continue
@@ -39,7 +40,9 @@ def attend64(q, q_lens, kv_lens, cu, rows, *, window=None, first=0, cap=None, ca
             p = np.where(sees.any(1, keepdims=True), p / np.where(l > 0, l, 1), 0.0)
             o[t, h] = p @ V[:, h // G]
             size[t, h] = p @ np.abs(V[:, h // G])
-    return o, size
+            if step:
+                steps[t, h] = p @ step(s)[:, h // G]
+    return (o, size, steps) if step else (o, size)
 
 
 def cached_rows(batch, cache, scale=1.0, latent=False):
