@@ -324,8 +324,8 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
             const uint32_t swz = (uint32_t)m[mSwz], stage = smem0 + s * Gm::STAGE;
             const bool need_mask = kw < kv_begin || kw + 32 > kv_end || (a.causal && kw + 31 > p_lo) ||
                                    (a.has_window && kw <= p_lo + ntok - 1 - a.window);
-            uint32_t row[2], sw[2], kvm[2];  // per 16 keys: this lane's row of codes, its chunks' place, the pairs of key g
-            float x[2][NT][4];
+            uint32_t row[2], sw[2];  // per 16 keys: this lane's row of codes, its chunks' place
+            uint64_t x[2][NT][2];    // logits of rows 2t, 2t + 1: key g, key g + 8
             uint32_t vm[2][2][NG];
 #pragma unroll
             for (int sub = 0; sub < 2; ++sub) {
@@ -337,9 +337,9 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int kg = 32 * w + 16 * sub + g + 8 * h;
-                    kvm[h] = stage + (kg >> brs) * RB + BR * D + (kg & (BR - 1)) * (NG * 4);
-                    load_meta<NG>(kvm[h], km[h]);
-                    load_meta<NG>(kvm[h] + BR * NG * 4, vm[sub][h]);
+                    const uint32_t at = stage + (kg >> brs) * RB + BR * D + (kg & (BR - 1)) * (NG * 4);
+                    load_meta<NG>(at, km[h]);
+                    load_meta<NG>(at + BR * NG * 4, vm[sub][h]);
                 }
                 float e[NT][4], o[NT][4];
 #pragma unroll
@@ -366,79 +366,90 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
 #pragma unroll
                             for (int hk = 0; hk < 2; ++hk) {
                                 const float2 sz = f16x2_to_f32x2(km[hk][gi]);
+                                const uint64_t ss = f32x2(sz.x, sz.x), zz = f32x2(sz.y, sz.y);
 #pragma unroll
                                 for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                                    for (int ri = 0; ri < 2; ++ri) {
-                                        const int i = 2 * hk + ri;
-                                        const float y = fmaf(sz.x, fmaf(16.f, e[nt][i], o[nt][i]), sz.y * qs[nt][ri][gi]);
-                                        x[sub][nt][i] = gi == 0 ? y : x[sub][nt][i] + y;
-                                    }
+                                    const uint64_t raw = ffma2(f32x2(e[nt][2 * hk], e[nt][2 * hk + 1]), f32x2(16.f, 16.f),
+                                                               f32x2(o[nt][2 * hk], o[nt][2 * hk + 1]));
+                                    const uint64_t q2 = f32x2(qs[nt][0][gi], qs[nt][1][gi]);
+                                    x[sub][nt][hk] = ffma2(ss, raw, gi == 0 ? fmul2(zz, q2) : ffma2(zz, q2, x[sub][nt][hk]));
                                 }
                             }
                         }
                     }
                 }
             }
-            // ---- scale, soft cap, masks (log2 domain); x[sub][nt][i]: key g + 8 (i >> 1) of 16, row 8 nt + 2t + (i & 1)
-            uint32_t seen = 0;  // keys that are inside the range: their scales count (others may hold any bits)
-            float mx[NT][2];
+            // ---- scale or soft cap (log2 domain), then masks
+            if (a.has_cap) {
+                const float ce = a.cap_exp * 1048576.f, cl = a.cap_log2;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mx[nt][0] = mx[nt][1] = -INFINITY;
+                for (int i = 0; i < 4 * NT; ++i) {
+                    uint64_t& v = x[i / (2 * NT)][i / 2 % NT][i % 2];
+                    float y[2];
+                    f32x2_split(v, y[0], y[1]);
 #pragma unroll
-            for (int sub = 0; sub < 2; ++sub) {
+                    for (int ri = 0; ri < 2; ++ri) y[ri] = cl - 2.f * cl * rcp_approx(1.f + ex2(y[ri] * ce));
+                    v = f32x2(y[0], y[1]);
+                }
+            } else {
+                const float qk = a.qk_log2 * 1048576.f;
+                const uint64_t qk2 = f32x2(qk, qk);
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int ri = i & 1;
-                        float y = x[sub][nt][i];
-                        if (a.has_cap) {
-                            const float u = ex2(y * (a.cap_exp * 1048576.f));
-                            y = a.cap_log2 - 2.f * a.cap_log2 * rcp_approx(1.f + u);
-                        } else {
-                            y *= a.qk_log2 * 1048576.f;
-                        }
-                        if (need_mask) {
-                            const int j = kw + 16 * sub + g + 8 * (i >> 1);
-                            const bool in = j >= kv_begin && j < kv_end;
-                            if (in) seen |= 1u << (2 * sub + (i >> 1));
-                            const bool okk = in && (!a.causal || j <= pos[nt][ri]) &&
-                                             (!a.has_window || j > pos[nt][ri] - a.window || j < a.first);
-                            y = okk ? y : -INFINITY;
-                        }
-                        x[sub][nt][i] = y;
-                        mx[nt][ri] = fmaxf(mx[nt][ri], y);
-                    }
+                for (int i = 0; i < 4 * NT; ++i) {
+                    uint64_t& v = x[i / (2 * NT)][i / 2 % NT][i % 2];
+                    v = fmul2(v, qk2);
                 }
             }
             if (need_mask) {
 #pragma unroll
                 for (int sub = 0; sub < 2; ++sub)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
+                    for (int h = 0; h < 2; ++h) {
+                        const int j = kw + 16 * sub + g + 8 * h;
+                        const bool in = j >= kv_begin && j < kv_end;
+                        if (!in) {  // the scales of keys outside the range may hold any bits
 #pragma unroll
-                        for (int i = 0; i < NG; ++i)
-                            if (!(seen >> (2 * sub + h) & 1u)) vm[sub][h][i] = 0u;
+                            for (int i = 0; i < NG; ++i) vm[sub][h][i] = 0u;
+                        }
+#pragma unroll
+                        for (int nt = 0; nt < NT; ++nt) {
+                            float y[2];
+                            f32x2_split(x[sub][nt][h], y[0], y[1]);
+#pragma unroll
+                            for (int ri = 0; ri < 2; ++ri) {
+                                const bool okk = in && (!a.causal || j <= pos[nt][ri]) &&
+                                                 (!a.has_window || j > pos[nt][ri] - a.window || j < a.first);
+                                y[ri] = okk ? y[ri] : -INFINITY;
+                            }
+                            x[sub][nt][h] = f32x2(y[0], y[1]);
+                        }
+                    }
             }
+            // ---- the running maximum moves only when a key outgrows it (by 2^2): each lane looks at its own keys, and only
+            // then are the rows' maxima formed across lanes
+            float mx[NT][2];
             bool grew = false;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
+                float y[2][4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) f32x2_split(x[i >> 1][nt][i & 1], y[0][i], y[1][i]);
 #pragma unroll
                 for (int ri = 0; ri < 2; ++ri) {
-                    float v = mx[nt][ri];
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                    mx[nt][ri] = v;
-                    grew |= v > m_r[nt][ri] + kRescale;
+                    mx[nt][ri] = fmax3(fmaxf(y[ri][0], y[ri][1]), y[ri][2], y[ri][3]);
+                    grew |= mx[nt][ri] > m_r[nt][ri] + kRescale;
                 }
+            }
             if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                     for (int ri = 0; ri < 2; ++ri) {
-                        const float m_new = fmaxf(m_r[nt][ri], mx[nt][ri]);
+                        float v = mx[nt][ri];
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                        const float m_new = fmaxf(m_r[nt][ri], v);
                         const float alpha = m_r[nt][ri] == -INFINITY ? 0.f : ex2(m_r[nt][ri] - m_new);
                         m_r[nt][ri] = m_new;
                         l_r[nt][ri] *= alpha;
@@ -457,19 +468,18 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
                     }
             }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
+            for (int nt = 0; nt < NT; ++nt) {
+                const uint64_t nb = f32x2(m_r[nt][0] == -INFINITY ? 0.f : -m_r[nt][0], m_r[nt][1] == -INFINITY ? 0.f : -m_r[nt][1]);
+                uint64_t l2 = f32x2(l_r[nt][0], l_r[nt][1]);
 #pragma unroll
-                for (int ri = 0; ri < 2; ++ri) {
-                    const float base = m_r[nt][ri] == -INFINITY ? 0.f : m_r[nt][ri];
-#pragma unroll
-                    for (int sub = 0; sub < 2; ++sub)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const float pe = ex2(x[sub][nt][2 * h + ri] - base);
-                            x[sub][nt][2 * h + ri] = pe;
-                            l_r[nt][ri] += pe;
-                        }
+                for (int i = 0; i < 4; ++i) {
+                    float y[2];
+                    f32x2_split(fadd2(x[i >> 1][nt][i & 1], nb), y[0], y[1]);
+                    x[i >> 1][nt][i & 1] = f32x2(ex2(y[0]), ex2(y[1]));
+                    l2 = fadd2(l2, x[i >> 1][nt][i & 1]);
                 }
+                f32x2_split(l2, l_r[nt][0], l_r[nt][1]);
+            }
             // ---- O^T += V^T P^T, group by group
 #pragma unroll
             for (int sub = 0; sub < 2; ++sub) {
@@ -486,11 +496,14 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
                             const float mid0 = fmaf(8.f, a0.x, a0.y), mid1 = fmaf(8.f, a1.x, a1.y);
 #pragma unroll
                             for (int nt = 0; nt < NT; ++nt) {
-                                const float* y = x[sub][nt];
-                                zs[nt][0][gi] += fmaf(y[0], mid0, y[2] * mid1);
-                                zs[nt][1][gi] += fmaf(y[1], mid0, y[3] * mid1);
-                                pb[nt][0] = transposed(pack2<true>(y[0] * a0.x, y[1] * a0.x));
-                                pb[nt][1] = transposed(pack2<true>(y[2] * a1.x, y[3] * a1.x));
+                                const uint64_t y0 = x[sub][nt][0], y1 = x[sub][nt][1];
+                                f32x2_split(ffma2(y0, f32x2(mid0, mid0), ffma2(y1, f32x2(mid1, mid1), f32x2(zs[nt][0][gi], zs[nt][1][gi]))),
+                                            zs[nt][0][gi], zs[nt][1][gi]);
+                                float b0, b1, b2, b3;
+                                f32x2_split(fmul2(y0, f32x2(a0.x, a0.x)), b0, b1);
+                                f32x2_split(fmul2(y1, f32x2(a1.x, a1.x)), b2, b3);
+                                pb[nt][0] = transposed(pack2<true>(b0, b1));
+                                pb[nt][1] = transposed(pack2<true>(b2, b3));
                                 constexpr uint32_t one = 0x3c003c00u;
                                 const uint32_t ones[4] = {one, one, one, one};
                                 mma16816<true>(psum[nt][gi], ones, pb[nt][0], pb[nt][1]);
