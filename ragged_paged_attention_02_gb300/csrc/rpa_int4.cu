@@ -34,7 +34,8 @@ constexpr int kKS = 128;                     // keys of a stage
 // greatest scale of float16 values), in f16's range
 constexpr float kRescale = 2.f;
 
-enum I4Meta : int { mSeq = 0, mHead, mQStart, mQl, mKl, mKvBegin, mKvEnd, mPart, mTok0, mNtok, mSt, mNst, mKey0, mStop, mSwz, kMetaWords };
+// words of a stage's description: the first four, four and four in one load each
+enum I4Meta : int { mKey0 = 0, mKvBegin, mKvEnd, mLeft, mPos, mNtok, mSwz, mFirst, mHead, mTok, mPart, kMetaWords = 12 };
 
 struct I4Params {
     AttnParams a;            // a.G: query heads of an item; a.Hkv: the cache's
@@ -84,6 +85,17 @@ __device__ __forceinline__ uint4 load_q8(const uint8_t* q, size_t e, int qdt) {
         w = make_uint4(bf16x2_to_f16x2(w.x), bf16x2_to_f16x2(w.y), bf16x2_to_f16x2(w.z), bf16x2_to_f16x2(w.w));
     return w;
 }
+// D = A B + D, and D = A B, m16n8k16 in f16 with 32-bit sums (not volatile: the compiler may order them)
+__device__ __forceinline__ void mma(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};\n"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma_first(float* d, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};\n"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
 template <int NG>
 __device__ __forceinline__ void load_meta(uint32_t addr, uint32_t* m) {
     if constexpr (NG == 1) {
@@ -106,7 +118,7 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
     constexpr int CPG = C / NG;                        // ... of a group
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ __align__(8) uint64_t full_bar[NS], empty_bar[NS], merge_bar;
-    __shared__ int meta[NS][kMetaWords];
+    __shared__ __align__(16) int meta[NS][kMetaWords];
     __shared__ float red_ml[kCW][R][2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const AttnParams& a = p.a;
@@ -189,22 +201,10 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
                 // where the codes' chunks lie goes by a key's slot modulo 8: bit 2 of it for every four keys
                 const uint32_t swz = __ballot_sync(0xffffffffu, ((k_stage + 4 * lane) % ps) & 4);
                 if (lane == 0) {
-                    int* m = meta[s];
-                    m[mSeq] = item.seq;
-                    m[mHead] = item.head;
-                    m[mQStart] = q_start;
-                    m[mQl] = ql;
-                    m[mKl] = kl;
-                    m[mKvBegin] = kv_begin;
-                    m[mKvEnd] = kv_end;
-                    m[mPart] = item.part;
-                    m[mTok0] = item.tok0;
-                    m[mNtok] = item.ntok;
-                    m[mSt] = st;
-                    m[mNst] = nst;
-                    m[mKey0] = k_stage;
-                    m[mSwz] = (int)swz;
-                    m[mStop] = 0;
+                    int4* m = reinterpret_cast<int4*>(meta[s]);
+                    m[0] = make_int4(k_stage, kv_begin, kv_end, nst - 1 - st);
+                    m[1] = make_int4(p_lo, item.ntok, (int)swz, st == 0);
+                    m[2] = make_int4(item.head, q_start + item.tok0, item.part, 0);
                 }
                 __syncwarp();
                 const uint32_t fb = smem_u32(&full_bar[s]);
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
         }
         if (ok && mbar_wait(smem_u32(&empty_bar[s]), ph ^ 1u, ctrl, tmo)) {
             if (lane == 0) {
-                meta[s][mStop] = 1;
+                meta[s][mLeft] = -1;
                 mbar_arrive(smem_u32(&full_bar[s]));
             }
         } else {
@@ -259,22 +259,27 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
     float m_r[NT][2], l_r[NT][2];
     int pos[NT][2];
     constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
+    // Within a stage: this lane's row of codes for the matrix loads (of the warp's first 16 keys), the (scale, zero) pairs of key g,
+    // and how far on those of the next 16 keys, and of key g + 8, lie; the place of the row's chunk 0 (of matrices 2, 3: 1)
+    const uint32_t row0 = (uint32_t)(((32 * w + (lane & 15)) >> brs) * RB + ((32 * w + (lane & 15)) & (BR - 1)) * (D / 2));
+    const uint32_t pair0 = (uint32_t)(((32 * w + g) >> brs) * RB + BR * D + ((32 * w + g) & (BR - 1)) * (NG * 4));
+    const uint32_t row16 = BR >= 32 ? 16 * (D / 2) : (16 >> brs) * RB, pair16 = BR >= 32 ? 16 * (NG * 4) : (16 >> brs) * RB;
+    const uint32_t pair8 = BR >= 16 ? 8 * (NG * 4) : (8 >> brs) * RB;
+    uint32_t sw0 = ((lane >> 4) ^ ((lane & 7) * D / 256 & (C - 1))) << 4, sw1 = sw0;
     for (;;) {
         if (!mbar_wait(smem_u32(&full_bar[s]), ph, ctrl, tmo)) return;
-        const int* m = meta[s];
-        if (m[mStop]) return;
-        const int st = m[mSt], nst = m[mNst];
-        const int kv_begin = m[mKvBegin], kv_end = m[mKvEnd];
-        const int tok0 = m[mTok0], ntok = m[mNtok];
-        const int p_lo = m[mKl] - m[mQl] + tok0;
-        if (st == 0) {
-            const int rows = ntok * G, q_start = m[mQStart], head = m[mHead];
+        const int4 m0 = *reinterpret_cast<const int4*>(&meta[s][mKey0]), m1 = *reinterpret_cast<const int4*>(&meta[s][mPos]);
+        const int kv_begin = m0.y, kv_end = m0.z, left = m0.w;  // left: the item's stages behind this one (-1: no more items)
+        const int p_lo = m1.x, ntok = m1.y;                     // p_lo: position of the tile's first token
+        if (left < 0) return;
+        if (m1.w) {
+            const int rows = ntok * G, tok = meta[s][mTok], head = meta[s][mHead];
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 // row 8 nt + g of Q: channels 32 c + 8 t .. + 7 of each chunk, paired as the masks pair the codes
                 const int r = 8 * nt + g;
                 const bool live = r < rows;
-                const size_t e = ((size_t)(q_start + tok0 + (live ? r / G : 0)) * Hq + head * G + (live ? r % G : 0)) * D + 8 * t;
+                const size_t e = ((size_t)(tok + (live ? r / G : 0)) * Hq + head * G + (live ? r % G : 0)) * D + 8 * t;
                 float sum[NG];
 #pragma unroll
                 for (int i = 0; i < NG; ++i) sum[i] = 0.f;
@@ -319,33 +324,33 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
             }
         }
         // ---- this warp's 32 keys: [kw, kw + 32)
-        const int kw = m[mKey0] + 32 * w;
+        const int kw = m0.x + 32 * w;
         if (kw < kv_end && kw + 32 > kv_begin) {
-            const uint32_t swz = (uint32_t)m[mSwz], stage = smem0 + s * Gm::STAGE;
+            const uint32_t swz = (uint32_t)m1.z, stage = smem0 + s * Gm::STAGE;
             const bool need_mask = kw < kv_begin || kw + 32 > kv_end || (a.causal && kw + 31 > p_lo) ||
                                    (a.has_window && kw <= p_lo + ntok - 1 - a.window);
-            uint32_t row[2], sw[2];  // per 16 keys: this lane's row of codes, its chunks' place
+            if (BR == 4) {  // where the chunks lie goes by the slot modulo 8, which runs of 4 keys start at 0 or 4
+                const uint32_t r8 = (swz >> (8 * w + ((lane & 15) >> 2)) & 1u) * 4 + (lane & 3);
+                sw0 = ((lane >> 4) ^ (r8 * D / 256 & (C - 1))) << 4;
+                const uint32_t r9 = (swz >> (8 * w + 4 + ((lane & 15) >> 2)) & 1u) * 4 + (lane & 3);
+                sw1 = ((lane >> 4) ^ (r9 * D / 256 & (C - 1))) << 4;
+            }
             uint64_t x[2][NT][2];    // logits of rows 2t, 2t + 1: key g, key g + 8
             uint32_t vm[2][2][NG];
 #pragma unroll
             for (int sub = 0; sub < 2; ++sub) {
-                const int kk = 32 * w + 16 * sub + (lane & 15);
-                const int r8 = (int)((swz >> (kk >> 2)) & 1u) * 4 + (kk & 3);
-                row[sub] = stage + (kk >> brs) * RB + (kk & (BR - 1)) * (D / 2);
-                sw[sub] = (uint32_t)(r8 * D / 256) & (C - 1);
+                const uint32_t row = stage + row0 + (sub ? row16 : 0u), at = stage + pair0 + (sub ? pair16 : 0u);
                 uint32_t km[2][NG];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    const int kg = 32 * w + 16 * sub + g + 8 * h;
-                    const uint32_t at = stage + (kg >> brs) * RB + BR * D + (kg & (BR - 1)) * (NG * 4);
-                    load_meta<NG>(at, km[h]);
-                    load_meta<NG>(at + BR * NG * 4, vm[sub][h]);
+                    load_meta<NG>(at + (h ? pair8 : 0u), km[h]);
+                    load_meta<NG>(at + (h ? pair8 : 0u) + BR * (NG * 4), vm[sub][h]);
                 }
                 float e[NT][4], o[NT][4];
 #pragma unroll
                 for (int c = 0; c < C; c += 2) {
                     uint32_t f[4];
-                    ldsm_x4(row[sub] + (((uint32_t)(c + (lane >> 4)) ^ sw[sub]) << 4), f[0], f[1], f[2], f[3]);
+                    ldsm_x4(row + ((uint32_t)(c << 4) ^ (sub ? sw1 : sw0)), f[0], f[1], f[2], f[3]);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int cc = c + h;
@@ -355,11 +360,12 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
                             if (cc % CPG == 0) {
-                                e[nt][0] = e[nt][1] = e[nt][2] = e[nt][3] = 0.f;
-                                o[nt][0] = o[nt][1] = o[nt][2] = o[nt][3] = 0.f;
+                                mma_first(e[nt], ae, qf[nt][cc][0], qf[nt][cc][1]);
+                                mma_first(o[nt], ao, qf[nt][cc][2], qf[nt][cc][3]);
+                            } else {
+                                mma(e[nt], ae, qf[nt][cc][0], qf[nt][cc][1]);
+                                mma(o[nt], ao, qf[nt][cc][2], qf[nt][cc][3]);
                             }
-                            mma16816<true>(e[nt], ae, qf[nt][cc][0], qf[nt][cc][1]);
-                            mma16816<true>(o[nt], ao, qf[nt][cc][2], qf[nt][cc][3]);
                         }
                         if ((cc + 1) % CPG == 0) {
                             const int gi = cc / CPG;
@@ -483,11 +489,12 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
             // ---- O^T += V^T P^T, group by group
 #pragma unroll
             for (int sub = 0; sub < 2; ++sub) {
+                const uint32_t row = stage + row0 + (sub ? row16 : 0u) + BR * (D / 2);
                 uint32_t pb[NT][2];
 #pragma unroll
                 for (int c = 0; c < C; c += 2) {
                     uint32_t f[4];
-                    ldsm_x4_t(row[sub] + BR * (D / 2) + (((uint32_t)(c + (lane >> 4)) ^ sw[sub]) << 4), f[0], f[1], f[2], f[3]);
+                    ldsm_x4_t(row + ((uint32_t)(c << 4) ^ (sub ? sw1 : sw0)), f[0], f[1], f[2], f[3]);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int cc = c + h, gi = cc / CPG;
@@ -506,7 +513,7 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
                                 pb[nt][1] = transposed(pack2<true>(b2, b3));
                                 constexpr uint32_t one = 0x3c003c00u;
                                 const uint32_t ones[4] = {one, one, one, one};
-                                mma16816<true>(psum[nt][gi], ones, pb[nt][0], pb[nt][1]);
+                                mma(psum[nt][gi], ones, pb[nt][0], pb[nt][1]);
                             }
                         }
                         const uint32_t u0 = f[2 * h], u1 = f[2 * h + 1], v0 = u0 >> 8, v1 = u1 >> 8;
@@ -514,21 +521,21 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
                         const uint32_t a1[4] = {v0 & kLow, v0 & kHigh, v1 & kLow, v1 & kHigh};
 #pragma unroll
                         for (int nt = 0; nt < NT; ++nt) {
-                            mma16816<true>(o_acc[cc][0][nt], a0, pb[nt][0], pb[nt][1]);
-                            mma16816<true>(o_acc[cc][1][nt], a1, pb[nt][0], pb[nt][1]);
+                            mma(o_acc[cc][0][nt], a0, pb[nt][0], pb[nt][1]);
+                            mma(o_acc[cc][1][nt], a1, pb[nt][0], pb[nt][1]);
                         }
                     }
                 }
             }
         }
-        const int head = m[mHead], q_start = m[mQStart], part = m[mPart];
+        const int4 m2 = *reinterpret_cast<const int4*>(&meta[s][mHead]);
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(&empty_bar[s]));
         if (++s == NS) {
             s = 0;
             ph ^= 1u;
         }
-        if (st != nst - 1) continue;
+        if (left > 0) continue;
         // ---- the item's end: merge the four warps' partials through shared memory
         if (lane == 0) mbar_arrive(mb);  // A: every warp has read the merge area's last contents
         if (!mbar_wait(mb, mph, ctrl, tmo)) return;
@@ -566,7 +573,7 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
         if (lane == 0) mbar_arrive(mb);  // B: every partial is in shared memory
         if (!mbar_wait(mb, mph, ctrl, tmo)) return;
         mph ^= 1u;
-        const int rows = ntok * G;
+        const int rows = ntok * G, head = m2.x, part = m2.z;
         for (int e = w * 32 + lane; e < rows * (D / 4); e += kCW * 32) {
             const int r = e / (D / 4), c = (e % (D / 4)) * 4;
             float M = -INFINITY;
@@ -587,7 +594,7 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
                 }
             }
             if (part < 0) {
-                const int tok = q_start + tok0 + r / G, qh = head * G + r % G;
+                const int tok = m2.y + r / G, qh = head * G + r % G;
                 L = add_sink(L, a.sinks, qh, M);
                 const float inv = L > 0.f ? a.v_scale / L : 0.f;
                 store_o4(a.o, ((size_t)tok * Hq + qh) * D + c, o.x * inv, o.y * inv, o.z * inv, o.w * inv, a.odt);
