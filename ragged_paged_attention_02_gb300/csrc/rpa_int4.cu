@@ -29,7 +29,7 @@ namespace {
 
 constexpr int kCW = 4;                       // consumer warps
 constexpr int kI4Threads = (kCW + 1) * 32;
-constexpr int kKS = 128;                     // keys of a stage
+constexpr int kKS = kInt4Keys;               // keys of a stage
 // The running maximum moves when a row's grows by more than 2^2: probabilities stay below 4, and P below 4 * 8734 (the
 // greatest scale of float16 values), in f16's range
 constexpr float kRescale = 2.f;
@@ -56,9 +56,10 @@ struct I4Geom {
     static constexpr int RED = kCW * R * LD * 4;
     // resident CTAs that registers are allocated for, and stages: as many as fit beside them
     static constexpr int CTAS = NG == 8 ? 1 : D == 256 ? 2 : NT == 2 ? 2 : D == 128 ? 3 : 4;
-    static constexpr int FIT = ((227 * 1024 / CTAS - 2048) - RED) / STAGE;
+    static constexpr bool OWN = RED > STAGE;     // the merge area lies behind the stages, else in the item's last stage
+    static constexpr int FIT = ((227 * 1024 / CTAS - 2048) - (OWN ? RED : 0)) / STAGE;
     static constexpr int NS = FIT > 4 ? 4 : FIT;
-    static constexpr int SMEM = NS * STAGE + RED;
+    static constexpr int SMEM = NS * STAGE + (OWN ? RED : 0);
     static_assert(NS >= 2, "a ring");
 };
 
@@ -247,7 +248,6 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
     // channels 32 c + 4 g .. + 3.
     const int w = warp, g = lane >> 2, t = lane & 3;
     const int G = a.G, Hq = a.Hq;
-    float* red_o = reinterpret_cast<float*>(smem + NS * Gm::STAGE);  // [kCW][R][LD]
     const uint32_t mb = smem_u32(&merge_bar);
     int s = 0;
     uint32_t ph = 0, mph = 0;
@@ -530,14 +530,16 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
         }
         const int4 m2 = *reinterpret_cast<const int4*>(&meta[s][mHead]);
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&empty_bar[s]));
+        const uint32_t slot = smem_u32(&empty_bar[s]);
+        float* red_o = reinterpret_cast<float*>(smem + (Gm::OWN ? NS : s) * Gm::STAGE);  // [kCW][R][LD]
+        if (lane == 0 && (Gm::OWN || left > 0)) mbar_arrive(slot);
         if (++s == NS) {
             s = 0;
             ph ^= 1u;
         }
         if (left > 0) continue;
         // ---- the item's end: merge the four warps' partials through shared memory
-        if (lane == 0) mbar_arrive(mb);  // A: every warp has read the merge area's last contents
+        if (lane == 0) mbar_arrive(mb);  // A: every warp is done with the stage, and with the merge area's last contents
         if (!mbar_wait(mb, mph, ctrl, tmo)) return;
         mph ^= 1u;
 #pragma unroll
@@ -602,6 +604,11 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
                 *reinterpret_cast<float4*>(a.part_o + ((size_t)part * kDecRows + r) * D + c) = o;
                 if (c == 0) *reinterpret_cast<float2*>(a.part_ml + ((size_t)part * kDecRows + r) * 2) = make_float2(M, L);
             }
+        }
+        if (!Gm::OWN) {
+            fence_proxy_async_smem();  // the stage will be refilled by bulk copies
+            __syncwarp();
+            if (lane == 0) mbar_arrive(slot);
         }
     }
 }

@@ -95,6 +95,8 @@ constexpr int kDecRows = 16;       // rows of a decode tile (one m16 MMA tile)
 constexpr int kMlaDqk = 576;
 constexpr int kMlaDv = 512;
 constexpr int kMlaRows = 16;
+constexpr int kInt4Keys = 128;            // keys of a stage of the 4-bit kernel
+constexpr int kInt4MinChunk = 256;        // smallest piece of its items
 constexpr int kInt4DirectRows = 64;       // 4-bit K/V: sequences with more query rows a kv head are unfolded to f16
 constexpr int kInt4MaxRoom = 1 << 20;     // pages of 64 keys (the planner's sums of refused sequences count to this)
 constexpr int kMaxGroup = 64;      // query heads per kv head (a prefill tile holds 128 / G tokens)
@@ -150,6 +152,7 @@ struct PlanParams {
     int int4, dec_tokens, direct_tokens;
     int pf_Hkv;      // kv heads a prefill unit stands for
     int room_pages;
+    int min_chunk;   // smallest split-KV piece (keys)
     int* vbase;      // [max_num_seqs + 1]: a sequence's first page of the room (ascending; none: the next one's)
     int max_units;   // capacity of the unit arrays
     int max_dec_units, max_pf_units;  // capacities of the two unit lists

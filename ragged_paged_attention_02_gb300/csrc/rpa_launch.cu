@@ -154,7 +154,9 @@ void kernels_choose(const RpaCfg& c, int sms, KernelSet* ks) {
         // room for prompts of longer sequences: 2^18 keys of 8 heads at D 128 (1 GiB), the longest sequence at least, all of them at most
         const int64_t page = 64 * 4 * c.num_kv_heads * c.head_dim, most = (c.pages_per_seq * c.page_size + 63) / 64;
         ks->P64 = (int)most;
-        if (c.num_q_tokens > ks->direct_tokens) {
+        // (no room in a handle of at most a token a sequence: one that decodes, whose calls are then three kernels; a sequence of
+        // many tokens takes the direct kernel's tiles there)
+        if (c.num_q_tokens > ks->direct_tokens && c.num_q_tokens > c.max_num_seqs) {
             int64_t pages = ((int64_t)1 << 30) / page;
             if (pages < most + 1) pages = most + 1;
             if (pages > c.max_num_seqs * (most + 1)) pages = c.max_num_seqs * (most + 1);
@@ -445,6 +447,7 @@ int enqueue_forward(const RpaCfg& c, const KernelSet& ks, const Workspace& ws, M
     pp.pf_Hkv = ks.pf_H;
     pp.room_pages = ks.room_pages;
     pp.vbase = ws.vbase;
+    pp.min_chunk = pp.int4 ? kInt4MinChunk : kMinChunk;
     pp.pf_mma_rows = ks.tc ? 2 * kTcRows : ks.mla ? kMlaRows : kTcRows;
     pp.dec_on_pf = (ks.tc8 && !pp.int4) || ks.mla;
     pp.D = ks.D;

@@ -225,8 +225,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
         const int dec_ctas = p.dec_on_pf ? s_split[0] : s_split[1];
         const unsigned long long target = (unsigned long long)p.dec_waves * (unsigned long long)max(1, dec_ctas);
         unsigned long long c = (s_total + target - 1) / target;
-        if (c < (unsigned long long)kMinChunk) c = kMinChunk;
-        c = (c + kChunkAlign - 1) / kChunkAlign * kChunkAlign;
+        if (c < (unsigned long long)p.min_chunk) c = p.min_chunk;
+        const int align = p.int4 ? kInt4Keys : kChunkAlign;
+        c = (c + align - 1) / align * align;
         if (c > (1ull << 30)) c = 1ull << 30;
         chunk = (int)c;
     }
@@ -461,13 +462,13 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
                 d4[1] = make_int4(pieces, 0, 0, 0);
         }
     }
-    // ... of sequences of several tiles (4-bit K/V): all threads on one sequence at a time
+    // ... of sequences of several tiles (4-bit K/V): a warp on one sequence at a time
     if (p.int4 && n_dec > 0) {
-        for (int s = 0; s < S; ++s) {
+        for (int s = tid >> 5; s < S; s += (int)blockDim.x >> 5) {
             const int ql = s_q0[s + 1] - s_q0[s];
             const int pieces = (s_cnt[s] + chunk - 1) / chunk;
             if (ql <= p.dec_tokens || s_cls[s] != 1 || pieces <= 1) continue;
-            for (int i = tid; i < dec_tiles(ql, p) * p.Hkv; i += blockDim.x) {
+            for (int i = tid & 31; i < dec_tiles(ql, p) * p.Hkv; i += 32) {
                 const int tile = i / p.Hkv, h = i - tile * p.Hkv, t0 = tile * p.dec_tokens;
                 int4* d4 = reinterpret_cast<int4*>(p.comb + s_comb[s] + i);
                 d4[0] = make_int4(s_q0[s] + t0, min(p.dec_tokens, ql - t0) * p.G, h, s_part[s] + i * pieces);
