@@ -57,9 +57,10 @@ struct I4Geom {
     // resident CTAs that registers are allocated for, and stages: as many as fit beside them
     static constexpr int CTAS = NG == 8 ? 1 : D == 256 ? 2 : NT == 2 ? 2 : D == 128 ? 3 : 4;
     static constexpr bool OWN = RED > STAGE;     // the merge area lies behind the stages, else in the item's last stage
-    static constexpr int FIT = ((227 * 1024 / CTAS - 2048) - (OWN ? RED : 0)) / STAGE;
+    static constexpr int QB = R * D * 4;         // Q of an item (as the call has it, at most 4 bytes an element)
+    static constexpr int FIT = ((227 * 1024 / CTAS - 2048) - QB - (OWN ? RED : 0)) / STAGE;
     static constexpr int NS = FIT > 4 ? 4 : FIT;
-    static constexpr int SMEM = NS * STAGE + (OWN ? RED : 0);
+    static constexpr int SMEM = NS * STAGE + QB + (OWN ? RED : 0);
     static_assert(NS >= 2, "a ring");
 };
 
@@ -75,13 +76,13 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
     return y;
 }
-// Eight neighbouring q values as f16 pairs, rounded to nearest even
+// Eight neighbouring q values (global or shared) as f16 pairs, rounded to nearest even
 __device__ __forceinline__ uint4 load_q8(const uint8_t* q, size_t e, int qdt) {
     if (qdt == OT_F32) {
-        const float4 a = __ldg(reinterpret_cast<const float4*>(q + e * 4)), b = __ldg(reinterpret_cast<const float4*>(q + e * 4) + 1);
+        const float4 a = *reinterpret_cast<const float4*>(q + e * 4), b = *(reinterpret_cast<const float4*>(q + e * 4) + 1);
         return make_uint4(pack2<true>(a.x, a.y), pack2<true>(a.z, a.w), pack2<true>(b.x, b.y), pack2<true>(b.z, b.w));
     }
-    uint4 w = __ldg(reinterpret_cast<const uint4*>(q + e * 2));
+    uint4 w = *reinterpret_cast<const uint4*>(q + e * 2);
     if (qdt == OT_BF16)
         w = make_uint4(bf16x2_to_f16x2(w.x), bf16x2_to_f16x2(w.y), bf16x2_to_f16x2(w.z), bf16x2_to_f16x2(w.w));
     return w;
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
     constexpr int R = Gm::R, NS = Gm::NS, C = D / 32;  // 16-byte chunks of a row of codes
     constexpr int CPG = C / NG;                        // ... of a group
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ __align__(8) uint64_t full_bar[NS], empty_bar[NS], merge_bar;
+    __shared__ __align__(8) uint64_t full_bar[NS], empty_bar[NS], merge_bar, q_full, q_empty;
     __shared__ __align__(16) int meta[NS][kMetaWords];
     __shared__ float red_ml[kCW][R][2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -132,6 +133,8 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
             mbar_init(smem_u32(&empty_bar[i]), kCW);
         }
         mbar_init(smem_u32(&merge_bar), kCW);
+        mbar_init(smem_u32(&q_full), 1);
+        mbar_init(smem_u32(&q_empty), kCW);
         fence_mbar_init();
     }
     __syncthreads();
@@ -146,32 +149,66 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
         if (p.stall) return;
         const int ps = a.ps, runs = kKS / BR;
         const uint64_t pol = l2_policy_evict_first();
+        const uint32_t q_row = (uint32_t)(a.G * D) * (p.qdt == OT_F32 ? 4u : 2u);  // bytes of a token's heads of an item
         int s = 0;
-        uint32_t ph = 0;
+        uint32_t ph = 0, qph = 0;
+        // An item, and the next one's description, which is fetched while this one's keys are on their way: its number, then its
+        // unit, then its lengths, then its first page ids, each a stage after what it depends on.
+        struct Work {
+            Item item;
+            int q_start, q_end, kl, lo, hi, nst0, nst, win0, win;
+        } cur, nxt;
+        auto fetch_unit = [&](Work& x, int it) { x.item = item_at(a.units, it, a.unit_heads); };
+        auto fetch_lengths = [&](Work& x) {
+            x.q_start = a.cu_q_lens[x.item.seq];
+            x.q_end = a.cu_q_lens[x.item.seq + 1];
+            x.kl = a.kv_lens[x.item.seq];
+        };
+        auto fetch_pages = [&](Work& x) {
+            // the unit's keys are those that any tile of the sequence sees: this tile's of them (none: a stage without keys,
+            // whose item writes an empty partial)
+            const int p_lo = x.kl - (x.q_end - x.q_start) + x.item.tok0, p_hi = p_lo + x.item.ntok - 1;
+            x.lo = x.item.kv_begin;
+            x.hi = x.item.kv_end;
+            if (a.causal) x.hi = min(x.hi, p_hi + 1);
+            if (a.has_window && (a.first == 0 || x.lo > a.first)) x.lo = max(x.lo, p_lo - a.window + 1);
+            x.hi = max(x.hi, x.lo);
+            const int key0 = x.lo & ~(BR - 1);
+            x.nst0 = first_tiles(a, x.item, kKS);
+            x.nst = max(1, x.nst0 + (x.hi > x.lo ? (x.hi - key0 + kKS - 1) / kKS : 0));
+            x.win0 = (x.nst0 ? 0 : key0) / ps;
+            x.win = (x.win0 + lane < a.P) ? __ldg(a.page_indices + (size_t)x.item.seq * a.P + x.win0 + lane) : 0;
+        };
         int it = 0;
         if (lane == 0) it = atomicAdd(ctrl + a.counter_word, 1);
         it = __shfl_sync(0xffffffffu, it, 0);
         bool ok = true;
+        if (it < n_items) {
+            fetch_unit(cur, it);
+            fetch_lengths(cur);
+            fetch_pages(cur);
+        }
         while (ok && it < n_items) {
-            const Item item = item_at(a.units, it, a.unit_heads);
-            int nxt = 0;
-            if (lane == 0) nxt = atomicAdd(ctrl + a.counter_word, 1);
-            const int q_start = a.cu_q_lens[item.seq];
-            const int ql = a.cu_q_lens[item.seq + 1] - q_start, kl = a.kv_lens[item.seq];
+            int more = 0;
+            if (lane == 0) more = atomicAdd(ctrl + a.counter_word, 1);
+            const Item& item = cur.item;
             const int* ptab = a.page_indices + (size_t)item.seq * a.P;
             const int kvh = item.head / p.blocks;
-            // the unit's keys are those that any tile of the sequence sees: this tile's of them (none: a stage without keys,
-            // whose item writes an empty partial)
-            const int p_lo = kl - ql + item.tok0, p_hi = p_lo + item.ntok - 1;
-            int lo = item.kv_begin, hi = item.kv_end;
-            if (a.causal) hi = min(hi, p_hi + 1);
-            if (a.has_window && (a.first == 0 || lo > a.first)) lo = max(lo, p_lo - a.window + 1);
-            hi = max(hi, lo);
-            const int key0 = lo & ~(BR - 1);
-            const int nst0 = first_tiles(a, item, kKS);
-            const int nst = max(1, nst0 + (hi > lo ? (hi - key0 + kKS - 1) / kKS : 0));
-            int win0 = (nst0 ? 0 : key0) / ps;
-            int win = (win0 + lane < a.P) ? __ldg(ptab + win0 + lane) : 0;
+            const int lo = cur.lo, hi = cur.hi, nst0 = cur.nst0, nst = cur.nst, key0 = lo & ~(BR - 1);
+            const int p_lo = cur.kl - (cur.q_end - cur.q_start) + item.tok0, tok = cur.q_start + item.tok0;
+            int win0 = cur.win0, win = cur.win, stage_of_next = 0;
+            // Q, once the consumers have the last item's in registers
+            if (!mbar_wait(smem_u32(&q_empty), qph ^ 1u, ctrl, tmo)) {
+                ok = false;
+                break;
+            }
+            qph ^= 1u;
+            const uint32_t qfb = smem_u32(&q_full);
+            if (lane == 0) mbar_arrive_expect_tx(qfb, (uint32_t)item.ntok * q_row);
+            __syncwarp();
+            if (lane < item.ntok)
+                bulk_copy(smem0 + NS * Gm::STAGE + lane * q_row,
+                          a.q + ((size_t)(tok + lane) * a.Hq + (size_t)item.head * a.G) * (D * (p.qdt == OT_F32 ? 4 : 2)), q_row, qfb, pol);
             for (int st = 0; st < nst; ++st) {
                 const bool fs = st < nst0;
                 const int k_stage = fs ? st * kKS : key0 + (st - nst0) * kKS;
@@ -205,7 +242,7 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
                     int4* m = reinterpret_cast<int4*>(meta[s]);
                     m[0] = make_int4(k_stage, kv_begin, kv_end, nst - 1 - st);
                     m[1] = make_int4(p_lo, item.ntok, (int)swz, st == 0);
-                    m[2] = make_int4(item.head, q_start + item.tok0, item.part, 0);
+                    m[2] = make_int4(item.head, tok, item.part, 0);
                 }
                 __syncwarp();
                 const uint32_t fb = smem_u32(&full_bar[s]);
@@ -228,8 +265,21 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
                     s = 0;
                     ph ^= 1u;
                 }
+                if (stage_of_next == 0) more = __shfl_sync(0xffffffffu, more, 0);
+                if (more < n_items) {
+                    if (stage_of_next == 0) fetch_unit(nxt, more);
+                    else if (stage_of_next == 1) fetch_lengths(nxt);
+                    else if (stage_of_next == 2) fetch_pages(nxt);
+                }
+                ++stage_of_next;
             }
-            it = __shfl_sync(0xffffffffu, nxt, 0);
+            if (!ok) break;
+            it = more;
+            if (it < n_items) {
+                if (stage_of_next < 2) fetch_lengths(nxt);
+                if (stage_of_next < 3) fetch_pages(nxt);
+                cur = nxt;
+            }
         }
         if (ok && mbar_wait(smem_u32(&empty_bar[s]), ph ^ 1u, ctrl, tmo)) {
             if (lane == 0) {
@@ -239,6 +289,7 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
         } else {
             // gave up: let the copies already issued land before leaving
             for (int i = 0; i < NS; ++i) mbar_wait(smem_u32(&full_bar[i]), 0, ctrl, tmo);
+            mbar_wait(smem_u32(&q_full), 0, ctrl, tmo);
         }
         return;
     }
@@ -250,7 +301,7 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
     const int G = a.G, Hq = a.Hq;
     const uint32_t mb = smem_u32(&merge_bar);
     int s = 0;
-    uint32_t ph = 0, mph = 0;
+    uint32_t ph = 0, mph = 0, qph = 0;
     uint32_t qf[NT][C][4];
     float qs[NT][2][NG];          // sums of q over a group, times 2^-20
     float o_acc[C][2][NT][4];     // [.][i][.][0, 1]: channel 32 c + 4 g + 2 i, rows 2t, 2t + 1, times 2^-24; [2, 3]: the next channel, times 2^-20
@@ -273,19 +324,20 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
         const int p_lo = m1.x, ntok = m1.y;                     // p_lo: position of the tile's first token
         if (left < 0) return;
         if (m1.w) {
-            const int rows = ntok * G, tok = meta[s][mTok], head = meta[s][mHead];
+            const int rows = ntok * G;
+            if (!mbar_wait(smem_u32(&q_full), qph, ctrl, tmo)) return;
+            qph ^= 1u;
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 // row 8 nt + g of Q: channels 32 c + 8 t .. + 7 of each chunk, paired as the masks pair the codes
                 const int r = 8 * nt + g;
                 const bool live = r < rows;
-                const size_t e = ((size_t)(tok + (live ? r / G : 0)) * Hq + head * G + (live ? r % G : 0)) * D + 8 * t;
                 float sum[NG];
 #pragma unroll
                 for (int i = 0; i < NG; ++i) sum[i] = 0.f;
                 uint4 x[C];
 #pragma unroll
-                for (int c = 0; c < C; ++c) x[c] = live ? load_q8(a.q, e + 32 * c, p.qdt) : make_uint4(0, 0, 0, 0);
+                for (int c = 0; c < C; ++c) x[c] = live ? load_q8(smem + NS * Gm::STAGE, r * D + 8 * t + 32 * c, p.qdt) : make_uint4(0, 0, 0, 0);
 #pragma unroll
                 for (int c = 0; c < C; ++c) {
                     qf[nt][c][0] = __byte_perm(x[c].x, x[c].z, 0x5410);  // channels 0, 4
@@ -322,6 +374,8 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
                     for (int i = 0; i < 2; ++i)
                         o_acc[c][i][nt][0] = o_acc[c][i][nt][1] = o_acc[c][i][nt][2] = o_acc[c][i][nt][3] = 0.f;
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&q_empty));
         }
         // ---- this warp's 32 keys: [kw, kw + 32)
         const int kw = m0.x + 32 * w;
@@ -531,7 +585,7 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
         const int4 m2 = *reinterpret_cast<const int4*>(&meta[s][mHead]);
         __syncwarp();
         const uint32_t slot = smem_u32(&empty_bar[s]);
-        float* red_o = reinterpret_cast<float*>(smem + (Gm::OWN ? NS : s) * Gm::STAGE);  // [kCW][R][LD]
+        float* red_o = reinterpret_cast<float*>(smem + (Gm::OWN ? NS * Gm::STAGE + Gm::QB : s * Gm::STAGE));  // [kCW][R][LD]
         if (lane == 0 && (Gm::OWN || left > 0)) mbar_arrive(slot);
         if (++s == NS) {
             s = 0;
