@@ -222,13 +222,13 @@ class RopeAppend(_Handle):
     def read(self, kv_pages, kv_lens, page_indices, cu_q_lens, num_seqs, k_out=None, v_out=None, stream=None):
         """The cached rows of each sequence's last q_len keys as values: (k_out, v_out), [T, Hkv, D] in q's type, whatever
         wrote them (v_out None with the latent layout).  With cu_q_lens the running sum of kv_lens, whole sequences."""
-        import torch
+        if k_out is None or (v_out is None and not self._latent):
+            import torch
 
-        with torch.cuda.stream(stream):
-            if k_out is None:
-                k_out = torch.zeros(self._kv_rows, dtype=self._q_dtype, device=kv_pages.device)
-            if v_out is None and not self._latent:
-                v_out = torch.zeros(self._kv_rows, dtype=self._q_dtype, device=kv_pages.device)
+            with torch.cuda.stream(stream):
+                new = lambda: torch.zeros(self._kv_rows, dtype=self._q_dtype, device=kv_pages.device)  # noqa: E731
+                k_out = new() if k_out is None else k_out
+                v_out = new() if v_out is None and not self._latent else v_out
         self._check_read(kv_pages, kv_lens, page_indices, cu_q_lens, k_out, v_out)
         tensors = (kv_pages, kv_lens, page_indices, cu_q_lens, k_out, v_out)
         self._need_here(tensors)

@@ -706,39 +706,61 @@ __global__ void __launch_bounds__(kUnfoldThreads, kUnfoldCtas) rpa_int4_unfold(c
         const int nf = lo > 0 ? (p.first + 63) / 64 : 0, at = v - p.vbase[s];
         const int page64 = at < nf ? at : lo / 64 + at - nf;
         if (h == 0 && tid == 0) p.table[(size_t)s * p.P64 + page64] = v;
-        for (int u = tid; u < 64 * 2 * per_row; u += kUnfoldThreads) {
-            const int place = u % per_row, slot = u / per_row % 64, is_v = u / per_row / 64;
-            const int j = page64 * 64 + slot;
-            if (j >= kl) continue;  // (rows past the last are masked, whatever they hold)
-            const int pg = p.page_indices[(size_t)s * p.P + j / p.ps], ks = j % p.ps;
-            uint4 out[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-            if ((unsigned)pg < (unsigned)p.N) {
-                const uint8_t* block = p.kv + ((size_t)pg * p.Hkv + h) * ((size_t)p.ps * int4_key_bytes(p.D, p.group));
-                const size_t line = (size_t)(is_v ? p.ps : 0) + ks;
-                const uint2 codes = *reinterpret_cast<const uint2*>(block + line * (p.D / 2) + int4_chunk(place / 2, ks, p.D) * 16 + (place & 1) * 8);
-                const float2 sz = f16x2_to_f32x2(reinterpret_cast<const uint32_t*>(block + (size_t)p.ps * p.D)[line * (p.D / p.group) +
-                                                                                                             16 * place / p.group]);
-                const uint32_t w[2] = {codes.x, codes.y};
-                float f[16];
+        // a thread takes one unit of 16 channels of K and V of a key, kFly keys in flight
+        const int step = kUnfoldThreads / per_row, place = tid % per_row;
+        constexpr int kFly = 2;
+        for (int slot0 = tid / per_row; slot0 < 64; slot0 += kFly * step) {
+            uint2 codes[kFly][2];
+            uint32_t pairs[kFly][2];
+            bool good[kFly];
 #pragma unroll
-                for (int k = 0; k < 16; ++k) {
-                    // rounded to f16, a step of the scale / 15 at most for the sizes that meet in a group; the greatest code of a
-                    // group that ends at f16's largest value may pass it by the scale's rounding
-                    const float y = fmaf(__uint_as_float(((w[k / 8] >> (4 * (k % 8))) & 15u) | 0x4b000000u) - 8388608.f, sz.x, sz.y);
-                    f[k] = y > 65504.f ? 65504.f : y;
+            for (int b = 0; b < kFly; ++b) {
+                const int slot = slot0 + b * step, j = page64 * 64 + slot;
+                good[b] = false;
+                if (slot >= 64 || j >= kl) continue;  // (rows past the last are masked, whatever they hold)
+                const int pg = p.page_indices[(size_t)s * p.P + j / p.ps], ks = j % p.ps;
+                good[b] = (unsigned)pg < (unsigned)p.N;
+                if (!good[b]) {
+                    // (pages that no token of the call sees are not checked: a page of 64 may be wider than the band)
+                    if (j >= lo || j < p.first) set_status(p.ctrl, RPA_ERR_BAD_PAGE_INDEX);
+                    continue;
                 }
+                const uint8_t* block = p.kv + ((size_t)pg * p.Hkv + h) * ((size_t)p.ps * int4_key_bytes(p.D, p.group));
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
-                    out[k] = make_uint4(pack2<true>(f[8 * k], f[8 * k + 1]), pack2<true>(f[8 * k + 2], f[8 * k + 3]),
-                                        pack2<true>(f[8 * k + 4], f[8 * k + 5]), pack2<true>(f[8 * k + 6], f[8 * k + 7]));
-            } else {
-                // (pages that no token of the call sees are not checked: the range of its page of 64 may be wider than the band)
-                const bool in = (j >= lo || j < p.first);
-                if (in) set_status(p.ctrl, RPA_ERR_BAD_PAGE_INDEX);
+                for (int is_v = 0; is_v < 2; ++is_v) {
+                    const uint32_t line = (uint32_t)(is_v ? p.ps : 0) + ks;
+                    codes[b][is_v] = *reinterpret_cast<const uint2*>(block + (size_t)line * (p.D / 2) + int4_chunk(place / 2, ks, p.D) * 16 + (place & 1) * 8);
+                    pairs[b][is_v] = reinterpret_cast<const uint32_t*>(block + (size_t)p.ps * p.D)[(size_t)line * (p.D / p.group) + 16 * place / p.group];
+                }
             }
-            uint4* dst = reinterpret_cast<uint4*>(p.rows + ((((size_t)v * 64 + slot) * 2 * p.Hkv + 2 * h + is_v) * p.D + 16 * place) * 2);
-            dst[0] = out[0];
-            dst[1] = out[1];
+#pragma unroll
+            for (int b = 0; b < kFly; ++b) {
+                const int slot = slot0 + b * step;
+                if (slot >= 64 || page64 * 64 + slot >= kl) continue;
+#pragma unroll
+                for (int is_v = 0; is_v < 2; ++is_v) {
+                    uint4 out[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+                    if (good[b]) {
+                        const float2 sz = f16x2_to_f32x2(pairs[b][is_v]);
+                        const uint32_t w[2] = {codes[b][is_v].x, codes[b][is_v].y};
+                        float f[16];
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) {
+                            // rounded to f16; the greatest code of a group that ends at f16's largest value may pass it by the
+                            // scale's rounding
+                            const float y = fmaf(__uint_as_float(((w[k / 8] >> (4 * (k % 8))) & 15u) | 0x4b000000u) - 8388608.f, sz.x, sz.y);
+                            f[k] = y > 65504.f ? 65504.f : y;
+                        }
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            out[k] = make_uint4(pack2<true>(f[8 * k], f[8 * k + 1]), pack2<true>(f[8 * k + 2], f[8 * k + 3]),
+                                                pack2<true>(f[8 * k + 4], f[8 * k + 5]), pack2<true>(f[8 * k + 6], f[8 * k + 7]));
+                    }
+                    uint4* dst = reinterpret_cast<uint4*>(p.rows + ((((size_t)v * 64 + slot) * 2 * p.Hkv + 2 * h + is_v) * p.D + 16 * place) * 2);
+                    dst[0] = out[0];
+                    dst[1] = out[1];
+                }
+            }
         }
     }
     if (p.qbuf) {

@@ -4,9 +4,10 @@
 // values of q's type: a 2- or 1-byte element times the cache's scale, or code * scale + zero of a 4-bit group
 // (the product of a 4-bit code and an 11-bit scale is exact in 32 bits, so the sum rounds once), times the cache's scale.
 //
-// A CTA takes a run of neighbouring tokens, up to 32 at a time, looks their slots up at once, and streams units of
-// 16 elements of one row: neighbouring threads take a row's units, then the same row of the next token (in a
-// 4-bit block the rows of neighbouring slots lie side by side), then the next row.  Bound by HBM: the rows read and written.
+// A CTA takes blocks of neighbouring tokens (as many as its threads hold a row's units of 16 elements of: 32 at D 128), looks
+// their slots up at once, and then a thread steps over the rows of its token, four in flight.  Neighbouring threads hold a row's
+// units, then the same row of the next token: in a 4-bit block the rows of neighbouring slots lie side by side.  Few tokens spread
+// over CTAs by rows.  Bound by HBM: the rows read and written.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -17,8 +18,8 @@ namespace {
 
 constexpr int kReadThreads = 256;
 constexpr int kReadCtas = 4;     // resident an SM
-constexpr int kReadTokens = 32;  // tokens of a CTA's round
-constexpr int kReadFly = 4;      // units whose loads a thread has in flight
+constexpr int kReadSeqs = 512;    // sequences whose cu_q_lens and kv_lens a CTA reads into shared memory
+constexpr int kReadFly = 4;      // rows whose loads a thread has in flight
 
 enum ReadMode : int { kRead16 = 0, kRead8 = 1, kRead4 = 2 };
 
@@ -47,102 +48,138 @@ __device__ __forceinline__ void put16_2(void* o, const float* f) {
 __device__ __forceinline__ void put16(__nv_bfloat16* o, const float* f) { put16_2<false>(o, f); }
 __device__ __forceinline__ void put16(__half* o, const float* f) { put16_2<true>(o, f); }
 
+// Loads the unit `place` (16 elements) of a slot's row of kv head h.
+template <int MODE>
+__device__ __forceinline__ void load_unit(const ReadParams& p, int page, int at, int h, int is_v, int place, Unit16<MODE>& x) {
+    if constexpr (MODE == kRead4) {
+        const uint8_t* block = p.kv + ((size_t)page * p.Hkv + h) * ((size_t)p.ps * int4_key_bytes(p.D, p.group));
+        const uint32_t line = (uint32_t)(is_v ? p.ps : 0) + at;
+        x.codes = *reinterpret_cast<const uint2*>(block + (size_t)line * (p.D / 2) + int4_chunk(place / 2, at, p.D) * 16 + (place & 1) * 8);
+        x.scale_zero = reinterpret_cast<const uint32_t*>(block + (size_t)p.ps * p.D)[(size_t)line * (p.D / p.group) + 16 * place / p.group];
+    } else {
+        const int rows = (p.latent ? 1 : 2) * p.Hkv;
+        const size_t row = ((size_t)page * p.ps + at) * rows + (p.latent ? h : 2 * h + is_v);
+        const uint4* s = reinterpret_cast<const uint4*>(p.kv + (row * p.D + 16 * place) * (MODE == kRead16 ? 2 : 1));
+#pragma unroll
+        for (int k = 0; k < (MODE == kRead16 ? 2 : 1); ++k) x.a[k] = s[k];
+    }
+}
+template <int MODE>
+__device__ __forceinline__ void widen(const Unit16<MODE>& x, int kt, float* f) {
+    if constexpr (MODE == kRead4) {
+        const float2 sz = f16x2_to_f32x2(x.scale_zero);
+        const uint32_t w[2] = {x.codes.x, x.codes.y};
+#pragma unroll
+        for (int k = 0; k < 16; ++k)  // 2^23 + code, exactly
+            f[k] = fmaf(__uint_as_float(((w[k / 8] >> (4 * (k % 8))) & 15u) | 0x4b000000u) - 8388608.f, sz.x, sz.y);
+    } else if constexpr (MODE == kRead16) {
+        const uint32_t w[8] = {x.a[0].x, x.a[0].y, x.a[0].z, x.a[0].w, x.a[1].x, x.a[1].y, x.a[1].z, x.a[1].w};
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const float2 v = kt == KT_F16 ? f16x2_to_f32x2(w[k]) : make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
+            f[2 * k] = v.x;
+            f[2 * k + 1] = v.y;
+        }
+    } else {
+        const uint32_t w[4] = {x.a[0].x, x.a[0].y, x.a[0].z, x.a[0].w};
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const uint4 v = kt == KT_I8     ? cvt8x8_to_f16x8<KT_I8>(w[2 * k], w[2 * k + 1])
+                            : kt == KT_E5M2 ? cvt8x8_to_f16x8<KT_E5M2>(w[2 * k], w[2 * k + 1])
+                                            : cvt8x8_to_f16x8<KT_E4M3>(w[2 * k], w[2 * k + 1]);
+            const uint32_t hv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+            for (int m = 0; m < 4; ++m) {
+                const float2 d = f16x2_to_f32x2(hv[m]);
+                f[8 * k + 2 * m] = d.x;
+                f[8 * k + 2 * m + 1] = d.y;
+            }
+        }
+    }
+}
+
 template <typename QT, int MODE>
 __global__ void __launch_bounds__(kReadThreads, kReadCtas) rpa_read_kernel(const ReadParams p) {
-    __shared__ long long s_page[kReadTokens];  // page and place of a token's slot (page << 32 | place), or -1
+    __shared__ long long s_page[kReadThreads / 4];  // page and place of a token's slot (page << 32 | place), or -1
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per_row = p.D / 16, rows = (p.latent ? 1 : 2) * p.Hkv;
+    const int step = kReadThreads / per_row, place = tid % per_row, mine = tid / per_row;  // a thread: one unit of one token's rows
+    const int blocks = (p.T + step - 1) / step;
+    __shared__ int s_cu[kReadSeqs + 1], s_kl[kReadSeqs];
     pdl_trigger();
     pdl_wait();
-    const int t_end = (int)((long long)p.T * (blockIdx.x + 1) / gridDim.x);
-    for (int t0 = (int)((long long)p.T * blockIdx.x / gridDim.x); t0 < t_end; t0 += kReadTokens) {
-        const int n = min(kReadTokens, t_end - t0);
-        for (int i = warp; i < n; i += kReadThreads / 32) {
-            const int t = t0 + i, s = find_seq(p.cu, p.S, t, lane);
-            if (lane != 0) continue;
+    const bool few = p.S <= kReadSeqs;
+    if (few) {
+        for (int i = tid; i < p.S; i += kReadThreads) {
+            s_cu[i] = p.cu[i];
+            s_kl[i] = p.kv_lens[i];
+        }
+        if (tid == 0) s_cu[p.S] = p.cu[p.S];
+        __syncthreads();
+    }
+    const long long tasks = (long long)blocks * rows;  // (block of tokens, row)
+    long long task = tasks * blockIdx.x / gridDim.x;
+    const long long end = tasks * (blockIdx.x + 1) / gridDim.x;
+    while (task < end) {
+        const int block = (int)(task / rows), r0 = (int)(task - (long long)block * rows);
+        const int r1 = (int)min((long long)rows, r0 + (end - task));
+        const int t0 = block * step, n = min(step, p.T - t0);
+        // token i: its sequence (< 0: none), where that starts and how many tokens and keys it has
+        auto look_up = [&](int i, int t, int s, int q0, int ql, int kl) {
             long long at = -1;
-            if (s >= 0) {
-                const int q0 = p.cu[s], ql = p.cu[s + 1] - q0, kl = p.kv_lens[s];
-                if (q0 >= 0 && kl <= p.P * p.ps && ql <= kl && q0 + ql <= p.T) {
-                    const int j = kl - ql + (t - q0), pg = p.page_indices[(size_t)s * p.P + j / p.ps];
-                    if ((unsigned)pg < (unsigned)p.N) at = ((long long)pg << 32) | (j % p.ps);
-                    else set_status(p.status, RPA_ERR_BAD_PAGE_INDEX);
-                }
+            if (s >= 0 && q0 >= 0 && kl <= p.P * p.ps && ql <= kl && q0 + ql <= p.T) {
+                const int j = kl - ql + (t - q0), pg = p.page_indices[(size_t)s * p.P + j / p.ps];
+                if ((unsigned)pg < (unsigned)p.N) at = ((long long)pg << 32) | (j % p.ps);
+                else set_status(p.status, RPA_ERR_BAD_PAGE_INDEX);
             }
             s_page[i] = at;
+        };
+        if (few) {
+            if (tid < n) {
+                // the last sequence that starts at or before the token
+                const int t = t0 + tid;
+                int s = 0, e = p.S;
+                while (e - s > 1) {
+                    const int m = (s + e) / 2;
+                    if (s_cu[m] <= t) s = m;
+                    else e = m;
+                }
+                const bool in = p.S > 0 && s_cu[s] <= t && t < s_cu[s + 1];
+                look_up(tid, t, in ? s : -1, in ? s_cu[s] : 0, in ? s_cu[s + 1] - s_cu[s] : 0, in ? s_kl[s] : 0);
+            }
+        } else {
+            for (int i = warp; i < n; i += kReadThreads / 32) {
+                const int t = t0 + i, s = find_seq(p.cu, p.S, t, lane);
+                if (lane == 0) look_up(i, t, s, s < 0 ? 0 : p.cu[s], s < 0 ? 0 : p.cu[s + 1] - p.cu[s], s < 0 ? 0 : p.kv_lens[s]);
+            }
         }
         __syncthreads();
-        const int units = n * rows * per_row;
-        for (int u0 = tid; u0 < units; u0 += kReadFly * kReadThreads) {
-            Unit16<MODE> x[kReadFly];
+        const long long slot = mine < n ? s_page[mine] : -1;
+        if (slot >= 0) {
+            const int page = (int)(slot >> 32), at = (int)slot;
+            const size_t out = ((size_t)(t0 + mine) * p.Hkv) * p.D + 16 * place;
+            for (int r = r0; r < r1; r += kReadFly) {
+                Unit16<MODE> x[kReadFly];
 #pragma unroll
-            for (int b = 0; b < kReadFly; ++b) {
-                const int u = u0 + b * kReadThreads;
-                const int place = u % per_row, i = u / per_row % n, r = u / per_row / n;  // (rows past the last: not loaded)
-                const long long slot = u < units ? s_page[i] : -1;
-                if (slot < 0) continue;
-                const int page = (int)(slot >> 32), at = (int)slot, h = r < p.Hkv ? r : r - p.Hkv, is_v = r >= p.Hkv;
-                if constexpr (MODE == kRead4) {
-                    const uint8_t* block = p.kv + ((size_t)page * p.Hkv + h) * ((size_t)p.ps * int4_key_bytes(p.D, p.group));
-                    const size_t line = (size_t)(is_v ? p.ps : 0) + at;
-                    x[b].codes = *reinterpret_cast<const uint2*>(block + line * (p.D / 2) + int4_chunk(place / 2, at, p.D) * 16 +
-                                                                 (place & 1) * 8);
-                    x[b].scale_zero = reinterpret_cast<const uint32_t*>(block + (size_t)p.ps * p.D)[line * (p.D / p.group) +
-                                                                                                    16 * place / p.group];
-                } else {
-                    const size_t row = ((size_t)page * p.ps + at) * rows + (p.latent ? h : 2 * h + is_v);
-                    const uint4* s = reinterpret_cast<const uint4*>(p.kv + (row * p.D + 16 * place) * (MODE == kRead16 ? 2 : 1));
+                for (int b = 0; b < kReadFly; ++b)
+                    if (r + b < r1) load_unit<MODE>(p, page, at, r + b < p.Hkv ? r + b : r + b - p.Hkv, r + b >= p.Hkv, place, x[b]);
 #pragma unroll
-                    for (int k = 0; k < (MODE == kRead16 ? 2 : 1); ++k) x[b].a[k] = s[k];
-                }
-            }
+                for (int b = 0; b < kReadFly; ++b) {
+                    if (r + b >= r1) break;
+                    const bool is_v = r + b >= p.Hkv;
+                    float f[16];
+                    widen<MODE>(x[b], p.kt, f);
+                    const float sc = is_v ? p.v_scale : p.k_scale;
+                    if (sc != 1.f) {
 #pragma unroll
-            for (int b = 0; b < kReadFly; ++b) {
-                const int u = u0 + b * kReadThreads;
-                const int place = u % per_row, i = u / per_row % n, r = u / per_row / n;
-                if (u >= units || s_page[i] < 0) continue;
-                const int h = r < p.Hkv ? r : r - p.Hkv, is_v = r >= p.Hkv;
-                float f[16];
-                if constexpr (MODE == kRead4) {
-                    const float2 sz = f16x2_to_f32x2(x[b].scale_zero);
-                    const uint32_t w[2] = {x[b].codes.x, x[b].codes.y};
-#pragma unroll
-                    for (int k = 0; k < 16; ++k)  // 2^23 + code, exactly
-                        f[k] = fmaf(__uint_as_float(((w[k / 8] >> (4 * (k % 8))) & 15u) | 0x4b000000u) - 8388608.f, sz.x, sz.y);
-                } else if constexpr (MODE == kRead16) {
-                    const uint32_t w[8] = {x[b].a[0].x, x[b].a[0].y, x[b].a[0].z, x[b].a[0].w, x[b].a[1].x, x[b].a[1].y, x[b].a[1].z, x[b].a[1].w};
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float2 v = p.kt == KT_F16 ? f16x2_to_f32x2(w[k])
-                                                        : make_float2(__uint_as_float(w[k] << 16), __uint_as_float(w[k] & 0xffff0000u));
-                        f[2 * k] = v.x;
-                        f[2 * k + 1] = v.y;
+                        for (int k = 0; k < 16; ++k) f[k] *= sc;
                     }
-                } else {
-                    const uint32_t w[4] = {x[b].a[0].x, x[b].a[0].y, x[b].a[0].z, x[b].a[0].w};
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const uint4 v = p.kt == KT_I8     ? cvt8x8_to_f16x8<KT_I8>(w[2 * k], w[2 * k + 1])
-                                        : p.kt == KT_E5M2 ? cvt8x8_to_f16x8<KT_E5M2>(w[2 * k], w[2 * k + 1])
-                                                          : cvt8x8_to_f16x8<KT_E4M3>(w[2 * k], w[2 * k + 1]);
-                        const uint32_t hv[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int m = 0; m < 4; ++m) {
-                            const float2 d = f16x2_to_f32x2(hv[m]);
-                            f[8 * k + 2 * m] = d.x;
-                            f[8 * k + 2 * m + 1] = d.y;
-                        }
-                    }
+                    put16(reinterpret_cast<QT*>(is_v ? p.v : p.k) + out + (size_t)(is_v ? r + b - p.Hkv : r + b) * p.D, f);
                 }
-                const float sc = is_v ? p.v_scale : p.k_scale;
-                if (sc != 1.f) {
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) f[k] *= sc;
-                }
-                put16(reinterpret_cast<QT*>(is_v ? p.v : p.k) + ((size_t)(t0 + i) * p.Hkv + h) * p.D + 16 * place, f);
             }
         }
         __syncthreads();  // the slots are looked up anew
+        task += r1 - r0;
     }
     // the lengths of every sequence, once
     if (blockIdx.x == 0) {
@@ -164,8 +201,10 @@ cudaError_t launch_as(const ReadParams& p, int grid, cudaStream_t st) {
 }  // namespace
 
 cudaError_t launch_read(const ReadParams& p, int q_dtype, int sms, cudaStream_t st) {
-    // a token a CTA at least; without tokens one CTA still checks the lengths
-    const int most = sms * kReadCtas, grid = p.T < 1 ? 1 : p.T < most ? p.T : most;
+    // a (block of tokens, row) a CTA at least; without tokens one CTA still checks the lengths
+    const int step = kReadThreads / (p.D / 16);
+    const long long tasks = (long long)((p.T + step - 1) / step) * (p.latent ? 1 : 2) * p.Hkv, most = (long long)sms * kReadCtas;
+    const int grid = (int)(tasks < 1 ? 1 : tasks < most ? tasks : most);
     return q_dtype == RPA_DT_F32   ? launch_as<float>(p, grid, st)
            : q_dtype == RPA_DT_F16 ? launch_as<__half>(p, grid, st)
                                    : launch_as<__nv_bfloat16>(p, grid, st);

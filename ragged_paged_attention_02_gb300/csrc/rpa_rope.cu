@@ -50,6 +50,7 @@ namespace {
 constexpr int kUnit = 16;       // elements of a unit
 constexpr int kRopeThreads = 256;
 constexpr int kRopeCtas = 5;    // resident an SM
+constexpr int kRopeCtas4 = 4;   // ... that write a 4-bit cache
 constexpr int kTokens = 16;     // tokens of a CTA's round
 constexpr int kSeqs = 512;      // sequences whose cu_q_lens and kv_lens a CTA reads into shared memory
 constexpr int kMaxPairs = 288;  // rotary_dim <= 576
@@ -154,23 +155,22 @@ __device__ __forceinline__ void store_kv8(uint8_t* kv, size_t row, int e, const 
     }
 }
 
-// least / greatest of two, NaN where either is
-__device__ __forceinline__ float min_nan(float a, float b) {
+// least / greatest of three, NaN where any is
+__device__ __forceinline__ float min_nan(float a, float b, float c) {
     float r;
-    asm("min.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
+    asm("min.NaN.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
     float r;
-    asm("max.NaN.f32 %0, %1, %2;\n" : "=f"(r) : "f"(a), "f"(b));
+    asm("max.NaN.f32 %0, %1, %2, %3;\n" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
 
 // A row of a 4-bit cache.  The row's D / 16 threads (neighbouring lanes, `mask`) hold its values by the pairs they turn;
 // through `row` (shared, D floats) each takes 16 neighbouring channels, and a group's extremes come by shuffles.
 // Differences and quotients are rounded towards the side that the scale and the zero are rounded to, so that no two roundings
-// of one value can meet; codes come from the exact quotient's nearest (a division, not a product with 1 / scale: beside a
-// border the product may fall on its other side).
+// of one value can meet; codes come from the exact quotient's nearest.
 __device__ __forceinline__ void store_int4(const RopeParams& p, const float* y, int e0, int e1, float* row, int place, uint32_t mask,
                                            long long slot, int h, bool is_v) {
 #pragma unroll
@@ -186,26 +186,52 @@ __device__ __forceinline__ void store_int4(const RopeParams& p, const float* y, 
         x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
     }
     __syncwarp(mask);  // the buffer is free again
-    float lo = INFINITY, hi = -INFINITY;
+    float lo = x[0], hi = x[0];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        x[i] = max_nan(min_nan(x[i], 65504.f), -65504.f);
-        lo = min_nan(lo, x[i]);
-        hi = max_nan(hi, x[i]);
+    for (int i = 1; i < 16; i += 2) {
+        lo = min_nan(lo, x[i], x[min(i + 1, 15)]);
+        hi = max_nan(hi, x[i], x[min(i + 1, 15)]);
     }
     for (int o = 1; o < p.group / 16; o <<= 1) {
-        lo = min_nan(lo, __shfl_xor_sync(mask, lo, o));
-        hi = max_nan(hi, __shfl_xor_sync(mask, hi, o));
+        const float l = __shfl_xor_sync(mask, lo, o), h2 = __shfl_xor_sync(mask, hi, o);
+        lo = min_nan(lo, l, l);
+        hi = max_nan(hi, h2, h2);
+    }
+    if (lo < -65504.f || hi > 65504.f) {  // (all of a group's threads)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) x[i] = fminf(fmaxf(x[i], -65504.f), 65504.f);
+        lo = fminf(fmaxf(lo, -65504.f), 65504.f);
+        hi = fminf(fmaxf(hi, -65504.f), 65504.f);
     }
     const __half zero = __float2half_rd(lo);
     const float z = __half2float(zero);
     const __half scale = __float2half_ru(__fdiv_ru(__fsub_ru(hi, z), 15.f));
-    const float s = __half2float(scale);
+    const float s = __half2float(scale), inv = __frcp_rn(s);
+    // The quotient's nearest integer, to even: of x (1 / s), off by less than 2^-17 for codes up to 15, unless one of the
+    // thread's lies so near the middle of two that only the division says which.  (1.5 2^23 leaves a sum's integer in its low
+    // bits, which are collected with their factors 16^i; what that constant's own bits add comes off at the end.)
+    constexpr float kMagic = 12582912.f;
+    constexpr uint32_t kBits = 0x4b400000u * 0x11111111u;
     uint32_t w[2] = {0, 0};
+    float off = 0.f;
+    const uint64_t nz2 = f32x2(-z, -z), inv2 = f32x2(inv, inv), magic2 = f32x2(kMagic, kMagic), back2 = f32x2(-kMagic, -kMagic);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int c = min(max(__float2int_rn(__fdiv_rn(x[i] - z, s)), 0), 15);  // (0 / 0 and NaN give 0)
-        w[i / 8] |= (uint32_t)c << (4 * (i % 8));
+    for (int i = 0; i < 16; i += 2) {
+        const uint64_t t = fmul2(fadd2(f32x2(x[i], x[i + 1]), nz2), inv2), n = fadd2(t, magic2);
+        float r0, r1, t0, t1, n0, n1;
+        f32x2_split(fadd2(n, back2), r0, r1);
+        f32x2_split(t, t0, t1);
+        f32x2_split(n, n0, n1);
+        off = max_nan(off, fabsf(t0 - r0), fabsf(t1 - r1));
+        w[i / 8] += __float_as_uint(n0) * (1u << (4 * (i % 8))) + __float_as_uint(n1) * (1u << (4 * (i % 8) + 4));
+    }
+    w[0] -= kBits;
+    w[1] -= kBits;
+    if (!(off < 0.4999f)) {  // (also where the group has no range, or a NaN: 0 / 0 and NaN give 0)
+        w[0] = w[1] = 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            w[i / 8] |= (uint32_t)min(max(__float2int_rn(__fdiv_rn(x[i] - z, s)), 0), 15) << (4 * (i % 8));
     }
     const int page = (int)(slot >> 32), at = (int)slot, ng = p.D / p.group;
     uint8_t* block = p.kv + ((size_t)page * p.Hkv + h) * ((size_t)p.ps * int4_key_bytes(p.D, p.group));
@@ -217,7 +243,7 @@ __device__ __forceinline__ void store_int4(const RopeParams& p, const float* y, 
 }
 
 template <typename QT, bool HALF, bool INT4>
-__global__ void __launch_bounds__(kRopeThreads, kRopeCtas) rpa_rope_kernel(const RopeParams p) {
+__global__ void __launch_bounds__(kRopeThreads, INT4 ? kRopeCtas4 : kRopeCtas) rpa_rope_kernel(const RopeParams p) {
     constexpr int kBatch = sizeof(QT) == 4 ? 1 : 2;  // rows whose loads a thread has in flight
     // [tokens][4][places] pairs of (cos, sin): place's pairs 2 i and 2 i + 1 at [i][place], so that neighbouring
     // places read neighbouring 16 bytes
@@ -585,7 +611,7 @@ int rpa_rope_append(RpaRope* h, const void* q, int64_t q_stride, const void* k, 
     p.magnitude = (float)h->cfg.magnitude;
     const int threads = kRopeThreads, half = h->cfg.pairing == RPA_ROPE_HALF;
     // a token a CTA at least; without tokens one CTA still checks the lengths
-    const int most = h->sms * kRopeCtas, grid = p.T < 1 ? 1 : p.T < most ? p.T : most;
+    const int most = h->sms * (p.kt == KT_I4 ? kRopeCtas4 : kRopeCtas), grid = p.T < 1 ? 1 : p.T < most ? p.T : most;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = c.q_dtype == RPA_DT_F32   ? launch_rope<float>(p, half, grid, threads, st)
                           : c.q_dtype == RPA_DT_F16 ? launch_rope<__half>(p, half, grid, threads, st)
