@@ -208,7 +208,7 @@ __device__ __forceinline__ void store_int4(const RopeParams& p, const float* y, 
     const __half scale = __float2half_ru(__fdiv_ru(__fsub_ru(hi, z), 15.f));
     const float s = __half2float(scale), inv = __frcp_rn(s);
     // The quotient's nearest integer, to even: of x (1 / s), off by less than 2^-17 for codes up to 15, unless one of the
-    // thread's lies so near the middle of two that only the division says which.  (1.5 2^23 leaves a sum's integer in its low
+    // thread's lies so near the middle of two that only the exact remainder says which.  (1.5 2^23 leaves a sum's integer in its low
     // bits, which are collected with their factors 16^i; what that constant's own bits add comes off at the end.)
     constexpr float kMagic = 12582912.f;
     constexpr uint32_t kBits = 0x4b400000u * 0x11111111u;
@@ -227,11 +227,17 @@ __device__ __forceinline__ void store_int4(const RopeParams& p, const float* y, 
     }
     w[0] -= kBits;
     w[1] -= kBits;
-    if (!(off < 0.4999f)) {  // (also where the group has no range, or a NaN: 0 / 0 and NaN give 0)
+    if (!(off < 0.49999f)) {  // (also where the group has no range, or a NaN: 0 / 0 and NaN give 0)
         w[0] = w[1] = 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            w[i / 8] |= (uint32_t)min(max(__float2int_rn(__fdiv_rn(x[i] - z, s)), 0), 15) << (4 * (i % 8));
+        for (int i = 0; i < 16; ++i) {
+            // what the rounded product leaves of the difference, exactly, against half a step
+            const float d = x[i] - z, r = rintf(d * inv), e = fmaf(-r, s, d), h2 = 0.5f * s;
+            int c = r == r ? (int)r : 0;
+            if (e > h2 || (e == h2 && (c & 1))) ++c;
+            if (e < -h2 || (e == -h2 && (c & 1))) --c;
+            w[i / 8] |= (uint32_t)min(max(c, 0), 15) << (4 * (i % 8));
+        }
     }
     const int page = (int)(slot >> 32), at = (int)slot, ng = p.D / p.group;
     uint8_t* block = p.kv + ((size_t)page * p.Hkv + h) * ((size_t)p.ps * int4_key_bytes(p.D, p.group));
