@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(kCombThreads, kCombCtasPerSm) rpa_combine_kern
     pdl_trigger();  // the next call's planner may start its first phases now
     pdl_wait();     // the attention kernels' partials are complete from here on
     const int n_comb = p.ctrl[kNumComb];
-    const int D = p.D, G = p.G, Hq = p.Hq;
+    const int D = p.D, G = p.G, Hq = p.Hq, PR = p.part_rows;
     const int lane = threadIdx.x & 31;
     const int rmax = max(1, min(p.rows_max, kDecRows));
     const int quads = D / 4;
@@ -50,10 +50,12 @@ __global__ void __launch_bounds__(kCombThreads, kCombCtasPerSm) rpa_combine_kern
         const int q0 = c0.x, rows = c0.y, head = c0.z, part = c0.w, pieces = c1.x;
         if (r >= rows) continue;  // the same for every lane of the warp
         const bool act = c4 < quads;
-        const float* ml = p.part_ml + ((size_t)part * kDecRows + r) * 2;  // piece k at + k kDecRows 2
+        const int kvh = head / p.blocks, h0 = (head - kvh * p.blocks) * G;  // the entry's heads: from h0 of its kv head's on
+        if (h0 + r % G >= p.heads) continue;
+        const float* ml = p.part_ml + ((size_t)part * PR + r) * 2;  // piece k at + k PR 2
         // piece k's four columns at pv[k * kstride] (float4 units)
-        const float4* pv = reinterpret_cast<const float4*>(p.part_o + ((size_t)part * kDecRows + r) * D) + c4;
-        const int kstride = kDecRows * D / 4;
+        const float4* pv = reinterpret_cast<const float4*>(p.part_o + ((size_t)part * PR + r) * D) + c4;
+        const int kstride = PR * D / 4;
         // few pieces: every partial O load in flight before the m / l reduction
         const bool held = pieces <= kBatch;
         float4 v[kBatch];
@@ -64,13 +66,13 @@ __global__ void __launch_bounds__(kCombThreads, kCombCtasPerSm) rpa_combine_kern
         }
         // the row's M, and L over all pieces (lanes over the pieces, 32 at a time)
         float M = -INFINITY;
-        for (int k = lane; k < pieces; k += 32) M = fmaxf(M, ml[(size_t)k * kDecRows * 2]);
+        for (int k = lane; k < pieces; k += 32) M = fmaxf(M, ml[(size_t)k * PR * 2]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
         float L = 0.f, sc_mine = 0.f;  // sc_mine: 2^(m_lane - M) for piece `lane` (the first 32)
         if (M != -INFINITY) {
             for (int k = lane; k < pieces; k += 32) {
-                const float2 w = *reinterpret_cast<const float2*>(ml + (size_t)k * kDecRows * 2);
+                const float2 w = *reinterpret_cast<const float2*>(ml + (size_t)k * PR * 2);
                 const float sc = ex2(w.x - M);
                 if (k < 32) sc_mine = sc;
                 L += sc * w.y;
@@ -78,7 +80,7 @@ __global__ void __launch_bounds__(kCombThreads, kCombCtasPerSm) rpa_combine_kern
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
-        const int qh = head * G + r % G;
+        const int qh = kvh * p.heads + h0 + r % G;
         L = add_sink(L, p.sinks, qh, M);  // the sink joins once, over all pieces
         const float inv = L > 0.f ? p.v_scale / L : 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -107,7 +109,7 @@ __global__ void __launch_bounds__(kCombThreads, kCombCtasPerSm) rpa_combine_kern
                         if (k0 + k < pieces) {
                             const int kk = k0 + k;
                             const float sc = kk < 32 ? __shfl_sync(0xffffffffu, sc_mine, kk)
-                                                     : ex2(ml[(size_t)kk * kDecRows * 2] - M);
+                                                     : ex2(ml[(size_t)kk * PR * 2] - M);
                             if (act) {
                                 acc.x += sc * v[k].x;
                                 acc.y += sc * v[k].y;

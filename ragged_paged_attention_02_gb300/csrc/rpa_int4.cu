@@ -12,56 +12,57 @@
 // and 8 bits further down the same again (5 instructions for 8 codes).  Codes of the two positions go to different accumulators
 // (logits) or output rows (values), whose powers of two are applied at the end.  q is rounded to f16.
 //
-//  * direct kernel: tiles of 8 or 16 query rows (tokens x heads of a kv head).  Keys are on the M side of m16n8k16: S^T = K Q^T,
+//  * direct kernel: tiles of 8 query rows (tokens x heads of a kv head).  Keys are on the M side of m16n8k16: S^T = K Q^T,
 //    O^T += V^T P^T, so that one decoded operand serves all rows; matrix loads of 16-bit units give a thread four codes of a key
 //    (K) or of two keys (V, transposed) just as the operands want them.  One producer warp copies whole blocks of a page and kv
-//    head (or four pieces of one where the page size does not divide 128) into a ring of 128-key stages, four warps take 32
-//    keys of each.  Bound by the bytes of the cache; a key and kv head costs about 11 issue slots at D 128.
+//    head (or four pieces of one where its size is not that of a run) into a ring of stages, the other warps take 32 keys of
+//    each.  Bound by instructions more than by bytes (a key and kv head costs 17 issue slots at D 128, of the 25 that its bytes'
+//    time has), so as few warps as can feed the others issue copies.  (Warps that each copied for themselves took 25.)
 //  * long prompts would decode every key once for each tile.  Sequences with more tokens are unfolded instead, once a call, to
 //    f16 rows in the workspace, over which the tensor-memory prefill kernels run.
 #include <cuda_fp16.h>
 #include <string.h>
 
+#include "rpa_evict.cuh"  // FastDiv
 #include "rpa_internal.cuh"
 
 namespace rpa {
 namespace {
 
-constexpr int kCW = 4;                       // consumer warps
-constexpr int kI4Threads = (kCW + 1) * 32;
-constexpr int kKS = kInt4Keys;               // keys of a stage
+constexpr int R = kInt4Rows;
 // The running maximum moves when a row's grows by more than 2^2: probabilities stay below 4, and P below 4 * 8734 (the
 // greatest scale of float16 values), in f16's range
 constexpr float kRescale = 2.f;
 
-// words of a stage's description: the first four, four and four in one load each
-enum I4Meta : int { mKey0 = 0, mKvBegin, mKvEnd, mLeft, mPos, mNtok, mSwz, mFirst, mHead, mTok, mPart, kMetaWords = 12 };
-
 struct I4Params {
-    AttnParams a;            // a.G: query heads of an item; a.Hkv: the cache's
-    int blocks;              // items' heads a kv head makes
+    AttnParams a;            // a.G: query heads of an item (the last block of a kv head may have fewer); a.Hkv: the cache's
+    int heads, blocks;       // query heads of a kv head, and the items' heads they make
     int BR, brs;             // keys of a copied page run, log2
-    size_t block;            // bytes of a page's block
-    int qdt;                 // OutType of q
-    int stall;               // test hook: the producer issues nothing
+    uint32_t block;          // bytes of a page's block
+    FastDiv page;            // by the page size
+    int stall;               // test hook: no copies are issued
     unsigned long long timeout_ns;
 };
 
-template <int D, int NG, int NT>
+// words of a stage's description: four in one load each
+enum I4Meta : int { mKey0 = 0, mKvBegin, mKvEnd, mLeft, mPos, mNtok, mSwz, mFirst, mHead, mTok, mPart, mHeads, mSwz2, kMetaWords = 16 };
+
+template <int D, int NG>
 struct I4Geom {
-    static constexpr int R = 8 * NT;
-    static constexpr int KB = D + 8 * NG;        // bytes of a key
-    static constexpr int STAGE = kKS * KB;
-    static constexpr int LD = D + 4;             // floats of a row of the merge area: rows of four lanes fall into different banks
-    static constexpr int RED = kCW * R * LD * 4;
+    static constexpr int CW = int4_warps(D);          // consumer warps
+    static constexpr int THREADS = (CW + 1) * 32;
+    static constexpr int KS = 32 * CW;                // keys of a stage
+    static constexpr int KB = D + 8 * NG;             // bytes of a key
+    static constexpr int STAGE = KS * KB;
+    static constexpr int QB = R * D * 2;              // Q of an item
+    static constexpr int LD = D + 4;                  // floats of a row of the merge area: rows of four lanes fall into different banks
+    static constexpr int RED = CW * R * LD * 4;       // ... which lies in the item's last stage
     // resident CTAs that registers are allocated for, and stages: as many as fit beside them
-    static constexpr int CTAS = NG == 8 ? 1 : D == 256 ? 2 : NT == 2 ? 2 : D == 128 ? 3 : 4;
-    static constexpr bool OWN = RED > STAGE;     // the merge area lies behind the stages, else in the item's last stage
-    static constexpr int QB = R * D * 4;         // Q of an item (as the call has it, at most 4 bytes an element)
-    static constexpr int FIT = ((227 * 1024 / CTAS - 2048) - QB - (OWN ? RED : 0)) / STAGE;
+    static constexpr int CTAS = D == 64 ? 4 : 2;
+    static constexpr int FIT = (227 * 1024 / CTAS - 3 * 1024 - QB) / STAGE;
     static constexpr int NS = FIT > 4 ? 4 : FIT;
-    static constexpr int SMEM = NS * STAGE + QB + (OWN ? RED : 0);
-    static_assert(NS >= 2, "a ring");
+    static constexpr int SMEM = NS * STAGE + QB;
+    static_assert(NS >= 2 && RED <= STAGE, "a ring; the merge area");
 };
 
 __device__ __forceinline__ void bulk_copy(uint32_t dst, const uint8_t* src, uint32_t bytes, uint32_t bar, uint64_t pol) {
@@ -76,15 +77,10 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
     return y;
 }
-// Eight neighbouring q values (global or shared) as f16 pairs, rounded to nearest even
-__device__ __forceinline__ uint4 load_q8(const uint8_t* q, size_t e, int qdt) {
-    if (qdt == OT_F32) {
-        const float4 a = *reinterpret_cast<const float4*>(q + e * 4), b = *(reinterpret_cast<const float4*>(q + e * 4) + 1);
-        return make_uint4(pack2<true>(a.x, a.y), pack2<true>(a.z, a.w), pack2<true>(b.x, b.y), pack2<true>(b.z, b.w));
-    }
+// Eight neighbouring 16-bit q values (global or shared) as f16 pairs, rounded to nearest even
+__device__ __forceinline__ uint4 load_q8(const uint8_t* q, size_t e, int bf16) {
     uint4 w = *reinterpret_cast<const uint4*>(q + e * 2);
-    if (qdt == OT_BF16)
-        w = make_uint4(bf16x2_to_f16x2(w.x), bf16x2_to_f16x2(w.y), bf16x2_to_f16x2(w.z), bf16x2_to_f16x2(w.w));
+    if (bf16) w = make_uint4(bf16x2_to_f16x2(w.x), bf16x2_to_f16x2(w.y), bf16x2_to_f16x2(w.z), bf16x2_to_f16x2(w.w));
     return w;
 }
 // D = A B + D, and D = A B, m16n8k16 in f16 with 32-bit sums (not volatile: the compiler may order them)
@@ -113,28 +109,29 @@ __device__ __forceinline__ void load_meta(uint32_t addr, uint32_t* m) {
     }
 }
 
-template <int D, int NG, int NT>
-__global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int4_attn(const I4Params p) {
-    using Gm = I4Geom<D, NG, NT>;
-    constexpr int R = Gm::R, NS = Gm::NS, C = D / 32;  // 16-byte chunks of a row of codes
-    constexpr int CPG = C / NG;                        // ... of a group
+template <int D, int NG>
+__global__ void __launch_bounds__((I4Geom<D, NG>::THREADS), (I4Geom<D, NG>::CTAS)) rpa_int4_attn(const I4Params p) {
+    using Gm = I4Geom<D, NG>;
+    constexpr int NS = Gm::NS, KS = Gm::KS, CW = Gm::CW, C = D / 32, SUBS = 2;  // C: 16-byte chunks of a row of codes
+    constexpr int CPG = C / NG;                                               // ... of a group
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ __align__(8) uint64_t full_bar[NS], empty_bar[NS], merge_bar, q_full, q_empty;
     __shared__ __align__(16) int meta[NS][kMetaWords];
-    __shared__ float red_ml[kCW][R][2];
+    __shared__ float red_ml[CW][R][2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const AttnParams& a = p.a;
     int* ctrl = a.ctrl;
     const uint64_t tmo = p.timeout_ns;
-    const uint32_t smem0 = smem_u32(smem);
+    const uint32_t ring0 = smem_u32(smem);
+    const uint8_t* qbuf = smem + NS * Gm::STAGE;
     if (tid == 0) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(smem_u32(&full_bar[i]), 1);
-            mbar_init(smem_u32(&empty_bar[i]), kCW);
+            mbar_init(smem_u32(&empty_bar[i]), CW);
         }
-        mbar_init(smem_u32(&merge_bar), kCW);
+        mbar_init(smem_u32(&merge_bar), CW);
         mbar_init(smem_u32(&q_full), 1);
-        mbar_init(smem_u32(&q_empty), kCW);
+        mbar_init(smem_u32(&q_empty), CW);
         fence_mbar_init();
     }
     __syncthreads();
@@ -142,21 +139,21 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
     pdl_wait();  // the planner's items are complete from here on
     if ((int)blockIdx.x >= ctrl[kDecCtas]) return;
     const int n_items = ctrl[a.item_count_word];
-    const int BR = p.BR, brs = p.brs, RB = BR * Gm::KB;
+    const int G = a.G, Hq = a.Hq, BR = p.BR, brs = p.brs, RB = BR * Gm::KB;
 
-    if (warp == kCW) {
+    if (warp == CW) {
         // =============================== producer ===============================
         if (p.stall) return;
-        const int ps = a.ps, runs = kKS / BR;
-        const uint64_t pol = l2_policy_evict_first();
-        const uint32_t q_row = (uint32_t)(a.G * D) * (p.qdt == OT_F32 ? 4u : 2u);  // bytes of a token's heads of an item
+        const int ps = a.ps, runs = KS / BR;
+        // K/V is read once, unless several blocks of query heads share it
+        const uint64_t pol = p.blocks > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
         int s = 0;
         uint32_t ph = 0, qph = 0;
         // An item, and the next one's description, which is fetched while this one's keys are on their way: its number, then its
         // unit, then its lengths, then its first page ids, each a stage after what it depends on.
         struct Work {
             Item item;
-            int q_start, q_end, kl, lo, hi, nst0, nst, win0, win;
+            int q_start, q_end, kl, lo, hi, nst0, nst, win0, win, win2;  // (page ids from win0 on, 64 of them)
         } cur, nxt;
         auto fetch_unit = [&](Work& x, int it) { x.item = item_at(a.units, it, a.unit_heads); };
         auto fetch_lengths = [&](Work& x) {
@@ -174,10 +171,12 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
             if (a.has_window && (a.first == 0 || x.lo > a.first)) x.lo = max(x.lo, p_lo - a.window + 1);
             x.hi = max(x.hi, x.lo);
             const int key0 = x.lo & ~(BR - 1);
-            x.nst0 = first_tiles(a, x.item, kKS);
-            x.nst = max(1, x.nst0 + (x.hi > x.lo ? (x.hi - key0 + kKS - 1) / kKS : 0));
-            x.win0 = (x.nst0 ? 0 : key0) / ps;
-            x.win = (x.win0 + lane < a.P) ? __ldg(a.page_indices + (size_t)x.item.seq * a.P + x.win0 + lane) : 0;
+            x.nst0 = first_tiles(a, x.item, KS);
+            x.nst = max(1, x.nst0 + (x.hi > x.lo ? (x.hi - key0 + KS - 1) / KS : 0));
+            x.win0 = p.page.div(x.nst0 ? 0 : key0);
+            const int* ids = a.page_indices + (size_t)x.item.seq * a.P + x.win0 + lane;
+            x.win = (x.win0 + lane < a.P) ? __ldg(ids) : 0;
+            x.win2 = (x.win0 + 32 + lane < a.P) ? __ldg(ids + 32) : 0;
         };
         int it = 0;
         if (lane == 0) it = atomicAdd(ctrl + a.counter_word, 1);
@@ -196,7 +195,9 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
             const int kvh = item.head / p.blocks;
             const int lo = cur.lo, hi = cur.hi, nst0 = cur.nst0, nst = cur.nst, key0 = lo & ~(BR - 1);
             const int p_lo = cur.kl - (cur.q_end - cur.q_start) + item.tok0, tok = cur.q_start + item.tok0;
-            int win0 = cur.win0, win = cur.win, stage_of_next = 0;
+            int win0 = cur.win0, win = cur.win, win2 = cur.win2, stage_of_next = 0;
+            const int h0 = (item.head - kvh * p.blocks) * G, nh = min(G, p.heads - h0);  // its heads of the kv head's
+            const uint32_t q_row = (uint32_t)(nh * D * 2);                             // bytes of a token's
             // Q, once the consumers have the last item's in registers
             if (!mbar_wait(smem_u32(&q_empty), qph ^ 1u, ctrl, tmo)) {
                 ok = false;
@@ -207,58 +208,80 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
             if (lane == 0) mbar_arrive_expect_tx(qfb, (uint32_t)item.ntok * q_row);
             __syncwarp();
             if (lane < item.ntok)
-                bulk_copy(smem0 + NS * Gm::STAGE + lane * q_row,
-                          a.q + ((size_t)(tok + lane) * a.Hq + (size_t)item.head * a.G) * (D * (p.qdt == OT_F32 ? 4 : 2)), q_row, qfb, pol);
+                bulk_copy(ring0 + NS * Gm::STAGE + lane * (G * D * 2), a.q + ((size_t)(tok + lane) * Hq + kvh * p.heads + h0) * (D * 2), q_row,
+                          qfb, pol);
             for (int st = 0; st < nst; ++st) {
                 const bool fs = st < nst0;
-                const int k_stage = fs ? st * kKS : key0 + (st - nst0) * kKS;
+                const int k_stage = fs ? st * KS : key0 + (st - nst0) * KS;
                 const int kv_begin = fs ? 0 : lo, kv_end = fs ? a.first : hi;
-                const int lp_last = max(k_stage, min(k_stage + kKS, kv_end) - 1) / ps;
-                if (lp_last - win0 >= 32) {
-                    win0 = k_stage / ps;
+                const int lp_last = p.page.div(max(k_stage, min(k_stage + KS, kv_end) - 1));
+                if (lp_last - win0 >= 64) {
+                    win0 = p.page.div(k_stage);
                     win = (win0 + lane < a.P) ? __ldg(ptab + win0 + lane) : 0;
+                    win2 = (win0 + 32 + lane < a.P) ? __ldg(ptab + win0 + 32 + lane) : 0;
                 }
                 if (!mbar_wait(smem_u32(&empty_bar[s]), ph ^ 1u, ctrl, tmo)) {
                     ok = false;
                     break;
                 }
-                const uint32_t stage = smem0 + s * Gm::STAGE;
-                const int k0 = k_stage + lane * BR;
-                const int lp = k0 / ps;
-                const int pg = __shfl_sync(0xffffffffu, win, (lp - win0) & 31);
-                const bool want = lane < runs && k0 < kv_end && k0 + BR > kv_begin;
-                const bool good = (unsigned)pg < (unsigned)a.N;
-                const int n_issue = __popc(__ballot_sync(0xffffffffu, want && good));
-                if (__any_sync(0xffffffffu, want && !good)) {
+                const uint32_t stage = ring0 + s * Gm::STAGE;
+                // a lane takes a run of BR keys, and with runs of 4 keys another 32 runs on
+                auto run_of = [&](int r, int& k0, int& lp, bool& want) {
+                    k0 = k_stage + r * BR;
+                    lp = p.page.div(k0);
+                    const int i = lp - win0, x = __shfl_sync(0xffffffffu, win, i & 31), y = __shfl_sync(0xffffffffu, win2, i & 31);
+                    want = r < runs && k0 < kv_end && k0 + BR > kv_begin;
+                    return i < 32 ? x : y;
+                };
+                int k0[2], lp[2], pg[2];
+                bool want[2] = {false, false};
+                pg[0] = run_of(lane, k0[0], lp[0], want[0]);
+                if (BR == 4) pg[1] = run_of(lane + 32, k0[1], lp[1], want[1]);
+                bool good[2], bad = false;
+                int n_issue = 0;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    good[i] = want[i] && (unsigned)pg[i] < (unsigned)a.N;
+                    bad |= want[i] && !good[i];
+                    n_issue += __popc(__ballot_sync(0xffffffffu, good[i]));
+                }
+                if (__any_sync(0xffffffffu, bad)) {
                     // a page id outside [0, N): never dereferenced; its keys read as zero
                     if (lane == 0) set_status(ctrl, RPA_ERR_BAD_PAGE_INDEX);
                     for (int i = lane; i < Gm::STAGE / 16; i += 32)
                         reinterpret_cast<uint4*>(smem + s * Gm::STAGE)[i] = make_uint4(0, 0, 0, 0);
                     fence_proxy_async_smem();
                 }
-                // where the codes' chunks lie goes by a key's slot modulo 8: bit 2 of it for every four keys
-                const uint32_t swz = __ballot_sync(0xffffffffu, ((k_stage + 4 * lane) % ps) & 4);
+                // where the codes' chunks lie goes by a key's slot modulo 8: with runs of 4 keys, bit 2 of it for each run
+                uint32_t swz = 0, swz2 = 0;
+                if (BR == 4) {
+                    swz = __ballot_sync(0xffffffffu, (k0[0] - lp[0] * ps) & 4);
+                    swz2 = __ballot_sync(0xffffffffu, (k0[1] - lp[1] * ps) & 4);
+                }
                 if (lane == 0) {
                     int4* m = reinterpret_cast<int4*>(meta[s]);
                     m[0] = make_int4(k_stage, kv_begin, kv_end, nst - 1 - st);
                     m[1] = make_int4(p_lo, item.ntok, (int)swz, st == 0);
-                    m[2] = make_int4(item.head, tok, item.part, 0);
+                    m[2] = make_int4(kvh * p.heads + h0, tok, item.part, nh);
+                    if (BR == 4) m[3].x = (int)swz2;
                 }
                 __syncwarp();
                 const uint32_t fb = smem_u32(&full_bar[s]);
                 if (lane == 0) mbar_arrive_expect_tx(fb, (uint32_t)(n_issue * RB));
                 __syncwarp();
-                if (want && good) {
-                    const uint8_t* src = a.kv + ((size_t)pg * a.Hkv + kvh) * p.block;
-                    const uint32_t dst = stage + lane * RB;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (!good[i]) continue;
+                    const uint8_t* src = a.kv + ((size_t)pg[i] * a.Hkv + kvh) * p.block;
+                    const uint32_t dst = stage + (lane + 32 * i) * RB;
                     if (BR == ps) {
                         bulk_copy(dst, src, RB, fb, pol);
                     } else {
-                        const int r0 = k0 - lp * ps;
+                        const int r0 = k0[i] - lp[i] * ps;
                         bulk_copy(dst, src + r0 * (D / 2), BR * (D / 2), fb, pol);
-                        bulk_copy(dst + BR * (D / 2), src + (ps + r0) * (D / 2), BR * (D / 2), fb, pol);
+                        bulk_copy(dst + BR * (D / 2), src + (size_t)(ps + r0) * (D / 2), BR * (D / 2), fb, pol);
                         bulk_copy(dst + BR * D, src + (size_t)ps * D + r0 * (NG * 4), BR * NG * 4, fb, pol);
-                        bulk_copy(dst + BR * (D + NG * 4), src + (size_t)ps * D + (ps + r0) * (NG * 4), BR * NG * 4, fb, pol);
+                        bulk_copy(dst + BR * (D + NG * 4), src + (size_t)ps * D + (size_t)(ps + r0) * (NG * 4), BR * NG * 4, fb, pol);
                     }
                 }
                 if (++s == NS) {
@@ -295,104 +318,100 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
     }
 
     // =============================== consumers ===============================
-    // Thread (g = lane / 4, t = lane % 4) holds, of S^T, rows 2t and 2t + 1 of keys g and g + 8 of each 16; of O^T those rows of
-    // channels 32 c + 4 g .. + 3.
+    // ---- Thread (g = lane / 4, t = lane % 4) holds, of S^T, rows 2t and 2t + 1 of keys g and g + 8 of each 16; of O^T those rows
+    // of channels 32 c + 4 g .. + 3.
     const int w = warp, g = lane >> 2, t = lane & 3;
-    const int G = a.G, Hq = a.Hq;
     const uint32_t mb = smem_u32(&merge_bar);
     int s = 0;
     uint32_t ph = 0, mph = 0, qph = 0;
-    uint32_t qf[NT][C][4];
-    float qs[NT][2][NG];          // sums of q over a group, times 2^-20
-    float o_acc[C][2][NT][4];     // [.][i][.][0, 1]: channel 32 c + 4 g + 2 i, rows 2t, 2t + 1, times 2^-24; [2, 3]: the next channel, times 2^-20
-    float psum[NT][NG][4];        // sums of P (rows 2t, 2t + 1, twice)
-    float zs[NT][2][NG];          // sums of p (z + 8 s) over this thread's keys
-    float m_r[NT][2], l_r[NT][2];
-    int pos[NT][2];
+    uint32_t qf[C][4];
+    float qs[2][NG];          // sums of q over a group, times 2^-20
+    float o_acc[C][2][4];     // [.][i][0, 1]: channel 32 c + 4 g + 2 i, rows 2t, 2t + 1, times 2^-24; [2, 3]: the next channel, times 2^-20
+    float psum[NG][4];        // sums of P (rows 2t, 2t + 1, twice)
+    float zs[2][NG];          // sums of p (z + 8 s) over this thread's keys
+    float m_r[2], l_r[2];
+    int pos[2];
     constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
-    // Within a stage: this lane's row of codes for the matrix loads (of the warp's first 16 keys), the (scale, zero) pairs of key g,
+    // Within a stage: this lane's row of codes for the matrix loads (of the first 16 keys), the (scale, zero) pairs of key g,
     // and how far on those of the next 16 keys, and of key g + 8, lie; the place of the row's chunk 0 (of matrices 2, 3: 1)
     const uint32_t row0 = (uint32_t)(((32 * w + (lane & 15)) >> brs) * RB + ((32 * w + (lane & 15)) & (BR - 1)) * (D / 2));
     const uint32_t pair0 = (uint32_t)(((32 * w + g) >> brs) * RB + BR * D + ((32 * w + g) & (BR - 1)) * (NG * 4));
     const uint32_t row16 = BR >= 32 ? 16 * (D / 2) : (16 >> brs) * RB, pair16 = BR >= 32 ? 16 * (NG * 4) : (16 >> brs) * RB;
     const uint32_t pair8 = BR >= 16 ? 8 * (NG * 4) : (8 >> brs) * RB;
-    uint32_t sw0 = ((lane >> 4) ^ ((lane & 7) * D / 256 & (C - 1))) << 4, sw1 = sw0;
+    uint32_t sw[SUBS];
+#pragma unroll
+    for (int i = 0; i < SUBS; ++i) sw[i] = ((lane >> 4) ^ ((lane & 7) * D / 256 & (C - 1))) << 4;
     for (;;) {
         if (!mbar_wait(smem_u32(&full_bar[s]), ph, ctrl, tmo)) return;
         const int4 m0 = *reinterpret_cast<const int4*>(&meta[s][mKey0]), m1 = *reinterpret_cast<const int4*>(&meta[s][mPos]);
         const int kv_begin = m0.y, kv_end = m0.z, left = m0.w;  // left: the item's stages behind this one (-1: no more items)
-        const int p_lo = m1.x, ntok = m1.y;                     // p_lo: position of the tile's first token
         if (left < 0) return;
+        const int p_lo = m1.x, ntok = m1.y;                     // p_lo: position of the tile's first token
         if (m1.w) {
-            const int rows = ntok * G;
+            // row g of Q: channels 32 c + 8 t .. + 7 of each chunk, paired as the masks pair the codes
+            const bool live = g < ntok * G && g % G < meta[s][mHeads];
             if (!mbar_wait(smem_u32(&q_full), qph, ctrl, tmo)) return;
             qph ^= 1u;
+            float sum[NG];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                // row 8 nt + g of Q: channels 32 c + 8 t .. + 7 of each chunk, paired as the masks pair the codes
-                const int r = 8 * nt + g;
-                const bool live = r < rows;
-                float sum[NG];
+            for (int i = 0; i < NG; ++i) sum[i] = 0.f;
+            uint4 x[C];
 #pragma unroll
-                for (int i = 0; i < NG; ++i) sum[i] = 0.f;
-                uint4 x[C];
+            for (int c = 0; c < C; ++c) x[c] = live ? load_q8(qbuf, g * D + 8 * t + 32 * c, a.q_f16 == 0) : make_uint4(0, 0, 0, 0);
 #pragma unroll
-                for (int c = 0; c < C; ++c) x[c] = live ? load_q8(smem + NS * Gm::STAGE, r * D + 8 * t + 32 * c, p.qdt) : make_uint4(0, 0, 0, 0);
+            for (int c = 0; c < C; ++c) {
+                qf[c][0] = __byte_perm(x[c].x, x[c].z, 0x5410);  // channels 0, 4
+                qf[c][1] = __byte_perm(x[c].y, x[c].w, 0x5410);  // 2, 6
+                qf[c][2] = __byte_perm(x[c].x, x[c].z, 0x7632);  // 1, 5
+                qf[c][3] = __byte_perm(x[c].y, x[c].w, 0x7632);  // 3, 7
+                const uint32_t xs[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
 #pragma unroll
-                for (int c = 0; c < C; ++c) {
-                    qf[nt][c][0] = __byte_perm(x[c].x, x[c].z, 0x5410);  // channels 0, 4
-                    qf[nt][c][1] = __byte_perm(x[c].y, x[c].w, 0x5410);  // 2, 6
-                    qf[nt][c][2] = __byte_perm(x[c].x, x[c].z, 0x7632);  // 1, 5
-                    qf[nt][c][3] = __byte_perm(x[c].y, x[c].w, 0x7632);  // 3, 7
-                    const uint32_t xs[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float2 f = f16x2_to_f32x2(xs[i]);
-                        sum[c / CPG] += f.x + f.y;
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    const float2 f = f16x2_to_f32x2(xs[i]);
+                    sum[c / CPG] += f.x + f.y;
                 }
+            }
 #pragma unroll
-                for (int i = 0; i < NG; ++i) {
-                    sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
-                    sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
-#pragma unroll
-                    for (int ri = 0; ri < 2; ++ri) {
-                        qs[nt][ri][i] = __shfl_sync(0xffffffffu, sum[i], 4 * (2 * t + ri)) * 9.5367431640625e-7f;
-                        zs[nt][ri][i] = 0.f;
-                    }
-                    psum[nt][i][0] = psum[nt][i][1] = psum[nt][i][2] = psum[nt][i][3] = 0.f;
-                }
+            for (int i = 0; i < NG; ++i) {
+                sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
+                sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
 #pragma unroll
                 for (int ri = 0; ri < 2; ++ri) {
-                    m_r[nt][ri] = -INFINITY;
-                    l_r[nt][ri] = 0.f;
-                    pos[nt][ri] = p_lo + (8 * nt + 2 * t + ri) / G;
+                    qs[ri][i] = __shfl_sync(0xffffffffu, sum[i], 4 * (2 * t + ri)) * 9.5367431640625e-7f;
+                    zs[ri][i] = 0.f;
                 }
-#pragma unroll
-                for (int c = 0; c < C; ++c)
-#pragma unroll
-                    for (int i = 0; i < 2; ++i)
-                        o_acc[c][i][nt][0] = o_acc[c][i][nt][1] = o_acc[c][i][nt][2] = o_acc[c][i][nt][3] = 0.f;
+                psum[i][0] = psum[i][1] = psum[i][2] = psum[i][3] = 0.f;
             }
+#pragma unroll
+            for (int ri = 0; ri < 2; ++ri) {
+                m_r[ri] = -INFINITY;
+                l_r[ri] = 0.f;
+                pos[ri] = p_lo + (2 * t + ri) / G;
+            }
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) o_acc[c][i][0] = o_acc[c][i][1] = o_acc[c][i][2] = o_acc[c][i][3] = 0.f;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&q_empty));
         }
-        // ---- this warp's 32 keys: [kw, kw + 32)
-        const int kw = m0.x + 32 * w;
+        const int kw = m0.x + 32 * w;  // this warp's 32 keys
         if (kw < kv_end && kw + 32 > kv_begin) {
-            const uint32_t swz = (uint32_t)m1.z, stage = smem0 + s * Gm::STAGE;
+            const uint32_t swz = (uint32_t)m1.z, stage = ring0 + s * Gm::STAGE;
             const bool need_mask = kw < kv_begin || kw + 32 > kv_end || (a.causal && kw + 31 > p_lo) ||
                                    (a.has_window && kw <= p_lo + ntok - 1 - a.window);
             if (BR == 4) {  // where the chunks lie goes by the slot modulo 8, which runs of 4 keys start at 0 or 4
-                const uint32_t r8 = (swz >> (8 * w + ((lane & 15) >> 2)) & 1u) * 4 + (lane & 3);
-                sw0 = ((lane >> 4) ^ (r8 * D / 256 & (C - 1))) << 4;
-                const uint32_t r9 = (swz >> (8 * w + 4 + ((lane & 15) >> 2)) & 1u) * 4 + (lane & 3);
-                sw1 = ((lane >> 4) ^ (r9 * D / 256 & (C - 1))) << 4;
-            }
-            uint64_t x[2][NT][2];    // logits of rows 2t, 2t + 1: key g, key g + 8
-            uint32_t vm[2][2][NG];
+                const uint32_t mine = (w < 4 ? swz : (uint32_t)meta[s][mSwz2]) >> (8 * (w & 3));
 #pragma unroll
-            for (int sub = 0; sub < 2; ++sub) {
+                for (int i = 0; i < SUBS; ++i) {
+                    const uint32_t r8 = (mine >> (4 * i + ((lane & 15) >> 2)) & 1u) * 4 + (lane & 3);
+                    sw[i] = ((lane >> 4) ^ (r8 * D / 256 & (C - 1))) << 4;
+                }
+            }
+            uint64_t x[SUBS][2];    // logits of rows 2t, 2t + 1: key g, key g + 8
+            uint32_t vm[SUBS][2][NG];
+#pragma unroll
+            for (int sub = 0; sub < SUBS; ++sub) {
                 const uint32_t row = stage + row0 + (sub ? row16 : 0u), at = stage + pair0 + (sub ? pair16 : 0u);
                 uint32_t km[2][NG];
 #pragma unroll
@@ -400,40 +419,32 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
                     load_meta<NG>(at + (h ? pair8 : 0u), km[h]);
                     load_meta<NG>(at + (h ? pair8 : 0u) + BR * (NG * 4), vm[sub][h]);
                 }
-                float e[NT][4], o[NT][4];
+                float e[4], o[4];
 #pragma unroll
                 for (int c = 0; c < C; c += 2) {
                     uint32_t f[4];
-                    ldsm_x4(row + ((uint32_t)(c << 4) ^ (sub ? sw1 : sw0)), f[0], f[1], f[2], f[3]);
+                    ldsm_x4(row + ((uint32_t)(c << 4) ^ sw[sub]), f[0], f[1], f[2], f[3]);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int cc = c + h;
                         const uint32_t u0 = f[2 * h], u1 = f[2 * h + 1], v0 = u0 >> 8, v1 = u1 >> 8;
                         const uint32_t ae[4] = {u0 & kLow, u1 & kLow, v0 & kLow, v1 & kLow};
                         const uint32_t ao[4] = {u0 & kHigh, u1 & kHigh, v0 & kHigh, v1 & kHigh};
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            if (cc % CPG == 0) {
-                                mma_first(e[nt], ae, qf[nt][cc][0], qf[nt][cc][1]);
-                                mma_first(o[nt], ao, qf[nt][cc][2], qf[nt][cc][3]);
-                            } else {
-                                mma(e[nt], ae, qf[nt][cc][0], qf[nt][cc][1]);
-                                mma(o[nt], ao, qf[nt][cc][2], qf[nt][cc][3]);
-                            }
+                        if (cc % CPG == 0) {
+                            mma_first(e, ae, qf[cc][0], qf[cc][1]);
+                            mma_first(o, ao, qf[cc][2], qf[cc][3]);
+                        } else {
+                            mma(e, ae, qf[cc][0], qf[cc][1]);
+                            mma(o, ao, qf[cc][2], qf[cc][3]);
                         }
                         if ((cc + 1) % CPG == 0) {
                             const int gi = cc / CPG;
 #pragma unroll
                             for (int hk = 0; hk < 2; ++hk) {
                                 const float2 sz = f16x2_to_f32x2(km[hk][gi]);
-                                const uint64_t ss = f32x2(sz.x, sz.x), zz = f32x2(sz.y, sz.y);
-#pragma unroll
-                                for (int nt = 0; nt < NT; ++nt) {
-                                    const uint64_t raw = ffma2(f32x2(e[nt][2 * hk], e[nt][2 * hk + 1]), f32x2(16.f, 16.f),
-                                                               f32x2(o[nt][2 * hk], o[nt][2 * hk + 1]));
-                                    const uint64_t q2 = f32x2(qs[nt][0][gi], qs[nt][1][gi]);
-                                    x[sub][nt][hk] = ffma2(ss, raw, gi == 0 ? fmul2(zz, q2) : ffma2(zz, q2, x[sub][nt][hk]));
-                                }
+                                const uint64_t ss = f32x2(sz.x, sz.x), zz = f32x2(sz.y, sz.y), q2 = f32x2(qs[0][gi], qs[1][gi]);
+                                const uint64_t raw = ffma2(f32x2(e[2 * hk], e[2 * hk + 1]), f32x2(16.f, 16.f), f32x2(o[2 * hk], o[2 * hk + 1]));
+                                x[sub][hk] = ffma2(ss, raw, gi == 0 ? fmul2(zz, q2) : ffma2(zz, q2, x[sub][hk]));
                             }
                         }
                     }
@@ -443,26 +454,22 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
             if (a.has_cap) {
                 const float ce = a.cap_exp * 1048576.f, cl = a.cap_log2;
 #pragma unroll
-                for (int i = 0; i < 4 * NT; ++i) {
-                    uint64_t& v = x[i / (2 * NT)][i / 2 % NT][i % 2];
+                for (int i = 0; i < 2 * SUBS; ++i) {
                     float y[2];
-                    f32x2_split(v, y[0], y[1]);
+                    f32x2_split(x[i / 2][i % 2], y[0], y[1]);
 #pragma unroll
                     for (int ri = 0; ri < 2; ++ri) y[ri] = cl - 2.f * cl * rcp_approx(1.f + ex2(y[ri] * ce));
-                    v = f32x2(y[0], y[1]);
+                    x[i / 2][i % 2] = f32x2(y[0], y[1]);
                 }
             } else {
                 const float qk = a.qk_log2 * 1048576.f;
                 const uint64_t qk2 = f32x2(qk, qk);
 #pragma unroll
-                for (int i = 0; i < 4 * NT; ++i) {
-                    uint64_t& v = x[i / (2 * NT)][i / 2 % NT][i % 2];
-                    v = fmul2(v, qk2);
-                }
+                for (int i = 0; i < 2 * SUBS; ++i) x[i / 2][i % 2] = fmul2(x[i / 2][i % 2], qk2);
             }
             if (need_mask) {
 #pragma unroll
-                for (int sub = 0; sub < 2; ++sub)
+                for (int sub = 0; sub < SUBS; ++sub)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int j = kw + 16 * sub + g + 8 * h;
@@ -471,113 +478,97 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
 #pragma unroll
                             for (int i = 0; i < NG; ++i) vm[sub][h][i] = 0u;
                         }
+                        float y[2];
+                        f32x2_split(x[sub][h], y[0], y[1]);
 #pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            float y[2];
-                            f32x2_split(x[sub][nt][h], y[0], y[1]);
-#pragma unroll
-                            for (int ri = 0; ri < 2; ++ri) {
-                                const bool okk = in && (!a.causal || j <= pos[nt][ri]) &&
-                                                 (!a.has_window || j > pos[nt][ri] - a.window || j < a.first);
-                                y[ri] = okk ? y[ri] : -INFINITY;
-                            }
-                            x[sub][nt][h] = f32x2(y[0], y[1]);
+                        for (int ri = 0; ri < 2; ++ri) {
+                            const bool okk = in && (!a.causal || j <= pos[ri]) && (!a.has_window || j > pos[ri] - a.window || j < a.first);
+                            y[ri] = okk ? y[ri] : -INFINITY;
                         }
+                        x[sub][h] = f32x2(y[0], y[1]);
                     }
             }
             // ---- the running maximum moves only when a key outgrows it (by 2^2): each lane looks at its own keys, and only
             // then are the rows' maxima formed across lanes
-            float mx[NT][2];
-            bool grew = false;
+            float mx[2];
+            {
+                float y[2][2 * SUBS];
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float y[2][4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) f32x2_split(x[i >> 1][nt][i & 1], y[0][i], y[1][i]);
+                for (int i = 0; i < 2 * SUBS; ++i) f32x2_split(x[i / 2][i % 2], y[0][i], y[1][i]);
 #pragma unroll
                 for (int ri = 0; ri < 2; ++ri) {
-                    mx[nt][ri] = fmax3(fmaxf(y[ri][0], y[ri][1]), y[ri][2], y[ri][3]);
-                    grew |= mx[nt][ri] > m_r[nt][ri] + kRescale;
+                    mx[ri] = fmaxf(y[ri][0], y[ri][1]);
+                    if constexpr (SUBS == 2) mx[ri] = fmax3(mx[ri], y[ri][2], y[ri][3]);
                 }
             }
-            if (__any_sync(0xffffffffu, grew)) {
+            if (__any_sync(0xffffffffu, mx[0] > m_r[0] + kRescale || mx[1] > m_r[1] + kRescale)) {
 #pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
+                for (int ri = 0; ri < 2; ++ri) {
+                    float v = mx[ri];
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                    v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                    const float m_new = fmaxf(m_r[ri], v);
+                    const float alpha = m_r[ri] == -INFINITY ? 0.f : ex2(m_r[ri] - m_new);
+                    m_r[ri] = m_new;
+                    l_r[ri] *= alpha;
 #pragma unroll
-                    for (int ri = 0; ri < 2; ++ri) {
-                        float v = mx[nt][ri];
-                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
-                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
-                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                        const float m_new = fmaxf(m_r[nt][ri], v);
-                        const float alpha = m_r[nt][ri] == -INFINITY ? 0.f : ex2(m_r[nt][ri] - m_new);
-                        m_r[nt][ri] = m_new;
-                        l_r[nt][ri] *= alpha;
-#pragma unroll
-                        for (int i = 0; i < NG; ++i) {
-                            zs[nt][ri][i] *= alpha;
-                            psum[nt][i][ri] *= alpha;
-                        }
-#pragma unroll
-                        for (int c = 0; c < C; ++c)
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                o_acc[c][i][nt][ri] *= alpha;
-                                o_acc[c][i][nt][ri + 2] *= alpha;
-                            }
+                    for (int i = 0; i < NG; ++i) {
+                        zs[ri][i] *= alpha;
+                        psum[i][ri] *= alpha;
                     }
-            }
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const uint64_t nb = f32x2(m_r[nt][0] == -INFINITY ? 0.f : -m_r[nt][0], m_r[nt][1] == -INFINITY ? 0.f : -m_r[nt][1]);
-                uint64_t l2 = f32x2(l_r[nt][0], l_r[nt][1]);
+                    for (int c = 0; c < C; ++c)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float y[2];
-                    f32x2_split(fadd2(x[i >> 1][nt][i & 1], nb), y[0], y[1]);
-                    x[i >> 1][nt][i & 1] = f32x2(ex2(y[0]), ex2(y[1]));
-                    l2 = fadd2(l2, x[i >> 1][nt][i & 1]);
+                        for (int i = 0; i < 2; ++i) {
+                            o_acc[c][i][ri] *= alpha;
+                            o_acc[c][i][ri + 2] *= alpha;
+                        }
                 }
-                f32x2_split(l2, l_r[nt][0], l_r[nt][1]);
+            }
+            {
+                const uint64_t nb = f32x2(m_r[0] == -INFINITY ? 0.f : -m_r[0], m_r[1] == -INFINITY ? 0.f : -m_r[1]);
+                uint64_t l2 = f32x2(l_r[0], l_r[1]);
+#pragma unroll
+                for (int i = 0; i < 2 * SUBS; ++i) {
+                    float y[2];
+                    f32x2_split(fadd2(x[i / 2][i % 2], nb), y[0], y[1]);
+                    x[i / 2][i % 2] = f32x2(ex2(y[0]), ex2(y[1]));
+                    l2 = fadd2(l2, x[i / 2][i % 2]);
+                }
+                f32x2_split(l2, l_r[0], l_r[1]);
             }
             // ---- O^T += V^T P^T, group by group
 #pragma unroll
-            for (int sub = 0; sub < 2; ++sub) {
+            for (int sub = 0; sub < SUBS; ++sub) {
                 const uint32_t row = stage + row0 + (sub ? row16 : 0u) + BR * (D / 2);
-                uint32_t pb[NT][2];
+                uint32_t pb[2];
 #pragma unroll
                 for (int c = 0; c < C; c += 2) {
                     uint32_t f[4];
-                    ldsm_x4_t(row + ((uint32_t)(c << 4) ^ (sub ? sw1 : sw0)), f[0], f[1], f[2], f[3]);
+                    ldsm_x4_t(row + ((uint32_t)(c << 4) ^ sw[sub]), f[0], f[1], f[2], f[3]);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int cc = c + h, gi = cc / CPG;
                         if (cc % CPG == 0) {
                             const float2 a0 = f16x2_to_f32x2(vm[sub][0][gi]), a1 = f16x2_to_f32x2(vm[sub][1][gi]);
                             const float mid0 = fmaf(8.f, a0.x, a0.y), mid1 = fmaf(8.f, a1.x, a1.y);
-#pragma unroll
-                            for (int nt = 0; nt < NT; ++nt) {
-                                const uint64_t y0 = x[sub][nt][0], y1 = x[sub][nt][1];
-                                f32x2_split(ffma2(y0, f32x2(mid0, mid0), ffma2(y1, f32x2(mid1, mid1), f32x2(zs[nt][0][gi], zs[nt][1][gi]))),
-                                            zs[nt][0][gi], zs[nt][1][gi]);
-                                float b0, b1, b2, b3;
-                                f32x2_split(fmul2(y0, f32x2(a0.x, a0.x)), b0, b1);
-                                f32x2_split(fmul2(y1, f32x2(a1.x, a1.x)), b2, b3);
-                                pb[nt][0] = transposed(pack2<true>(b0, b1));
-                                pb[nt][1] = transposed(pack2<true>(b2, b3));
-                                constexpr uint32_t one = 0x3c003c00u;
-                                const uint32_t ones[4] = {one, one, one, one};
-                                mma(psum[nt][gi], ones, pb[nt][0], pb[nt][1]);
-                            }
+                            f32x2_split(ffma2(x[sub][0], f32x2(mid0, mid0), ffma2(x[sub][1], f32x2(mid1, mid1), f32x2(zs[0][gi], zs[1][gi]))),
+                                        zs[0][gi], zs[1][gi]);
+                            float b0, b1, b2, b3;
+                            f32x2_split(fmul2(x[sub][0], f32x2(a0.x, a0.x)), b0, b1);
+                            f32x2_split(fmul2(x[sub][1], f32x2(a1.x, a1.x)), b2, b3);
+                            pb[0] = transposed(pack2<true>(b0, b1));
+                            pb[1] = transposed(pack2<true>(b2, b3));
+                            constexpr uint32_t one = 0x3c003c00u;
+                            const uint32_t ones[4] = {one, one, one, one};
+                            mma(psum[gi], ones, pb[0], pb[1]);
                         }
                         const uint32_t u0 = f[2 * h], u1 = f[2 * h + 1], v0 = u0 >> 8, v1 = u1 >> 8;
                         const uint32_t a0[4] = {u0 & kLow, u0 & kHigh, u1 & kLow, u1 & kHigh};
                         const uint32_t a1[4] = {v0 & kLow, v0 & kHigh, v1 & kLow, v1 & kHigh};
-#pragma unroll
-                        for (int nt = 0; nt < NT; ++nt) {
-                            mma(o_acc[cc][0][nt], a0, pb[nt][0], pb[nt][1]);
-                            mma(o_acc[cc][1][nt], a1, pb[nt][0], pb[nt][1]);
-                        }
+                        mma(o_acc[cc][0], a0, pb[0], pb[1]);
+                        mma(o_acc[cc][1], a1, pb[0], pb[1]);
                     }
                 }
             }
@@ -585,61 +576,62 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
         const int4 m2 = *reinterpret_cast<const int4*>(&meta[s][mHead]);
         __syncwarp();
         const uint32_t slot = smem_u32(&empty_bar[s]);
-        float* red_o = reinterpret_cast<float*>(smem + (Gm::OWN ? NS * Gm::STAGE + Gm::QB : s * Gm::STAGE));  // [kCW][R][LD]
-        if (lane == 0 && (Gm::OWN || left > 0)) mbar_arrive(slot);
+        float* red_o = reinterpret_cast<float*>(smem + s * Gm::STAGE);  // [CW][R][LD]
         if (++s == NS) {
             s = 0;
             ph ^= 1u;
         }
-        if (left > 0) continue;
-        // ---- the item's end: merge the four warps' partials through shared memory
-        if (lane == 0) mbar_arrive(mb);  // A: every warp is done with the stage, and with the merge area's last contents
+        if (left > 0) {
+            if (lane == 0) mbar_arrive(slot);
+            continue;
+        }
+        // ---- the item's end: merge the warps' partials through its last stage
+        if (lane == 0) mbar_arrive(mb);  // A: every warp is done with the stage
         if (!mbar_wait(mb, mph, ctrl, tmo)) return;
         mph ^= 1u;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int ri = 0; ri < 2; ++ri) {
-                float l = l_r[nt][ri];
-                l += __shfl_xor_sync(0xffffffffu, l, 4);
-                l += __shfl_xor_sync(0xffffffffu, l, 8);
-                l += __shfl_xor_sync(0xffffffffu, l, 16);
-                const int r = 8 * nt + 2 * t + ri;
-                if (g == 0) {
-                    red_ml[w][r][0] = m_r[nt][ri];
-                    red_ml[w][r][1] = l;
-                }
-                float add[NG];
-#pragma unroll
-                for (int i = 0; i < NG; ++i) {
-                    float z = zs[nt][ri][i];
-                    z += __shfl_xor_sync(0xffffffffu, z, 4);
-                    z += __shfl_xor_sync(0xffffffffu, z, 8);
-                    z += __shfl_xor_sync(0xffffffffu, z, 16);
-                    add[i] = fmaf(-8.f, psum[nt][i][ri], z);
-                }
-                float* out = red_o + (w * R + r) * Gm::LD + 4 * g;
-#pragma unroll
-                for (int c = 0; c < C; ++c)
-                    *reinterpret_cast<float4*>(out + 32 * c) =
-                        make_float4(fmaf(o_acc[c][0][nt][ri], 16777216.f, add[c / CPG]), fmaf(o_acc[c][0][nt][ri + 2], 1048576.f, add[c / CPG]),
-                                    fmaf(o_acc[c][1][nt][ri], 16777216.f, add[c / CPG]), fmaf(o_acc[c][1][nt][ri + 2], 1048576.f, add[c / CPG]));
+        for (int ri = 0; ri < 2; ++ri) {
+            float l = l_r[ri];
+            l += __shfl_xor_sync(0xffffffffu, l, 4);
+            l += __shfl_xor_sync(0xffffffffu, l, 8);
+            l += __shfl_xor_sync(0xffffffffu, l, 16);
+            const int r = 2 * t + ri;
+            if (g == 0) {
+                red_ml[w][r][0] = m_r[ri];
+                red_ml[w][r][1] = l;
             }
+            float add[NG];
+#pragma unroll
+            for (int i = 0; i < NG; ++i) {
+                float z = zs[ri][i];
+                z += __shfl_xor_sync(0xffffffffu, z, 4);
+                z += __shfl_xor_sync(0xffffffffu, z, 8);
+                z += __shfl_xor_sync(0xffffffffu, z, 16);
+                add[i] = fmaf(-8.f, psum[i][ri], z);
+            }
+            float* out = red_o + (w * R + r) * Gm::LD + 4 * g;
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                *reinterpret_cast<float4*>(out + 32 * c) =
+                    make_float4(fmaf(o_acc[c][0][ri], 16777216.f, add[c / CPG]), fmaf(o_acc[c][0][ri + 2], 1048576.f, add[c / CPG]),
+                                fmaf(o_acc[c][1][ri], 16777216.f, add[c / CPG]), fmaf(o_acc[c][1][ri + 2], 1048576.f, add[c / CPG]));
+        }
         __syncwarp();
         if (lane == 0) mbar_arrive(mb);  // B: every partial is in shared memory
         if (!mbar_wait(mb, mph, ctrl, tmo)) return;
         mph ^= 1u;
-        const int rows = ntok * G, head = m2.x, part = m2.z;
-        for (int e = w * 32 + lane; e < rows * (D / 4); e += kCW * 32) {
-            const int r = e / (D / 4), c = (e % (D / 4)) * 4;
+        const int rows = ntok * G, part = m2.z;
+        for (int e = w * 32 + lane; e < rows * (D / 4); e += CW * 32) {
+            const int r = e / (D / 4), c = (e % (D / 4)) * 4, hr = r % G;
+            if (hr >= m2.w) continue;  // (a block of fewer heads)
             float M = -INFINITY;
 #pragma unroll
-            for (int i = 0; i < kCW; ++i) M = fmaxf(M, red_ml[i][r][0]);
+            for (int i = 0; i < CW; ++i) M = fmaxf(M, red_ml[i][r][0]);
             float L = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
             if (M != -INFINITY) {
 #pragma unroll
-                for (int i = 0; i < kCW; ++i) {
+                for (int i = 0; i < CW; ++i) {
                     const float sc = ex2(red_ml[i][r][0] - M);
                     L += sc * red_ml[i][r][1];
                     const float4 v = *reinterpret_cast<const float4*>(red_o + (i * R + r) * Gm::LD + c);
@@ -650,20 +642,18 @@ __global__ void __launch_bounds__(kI4Threads, (I4Geom<D, NG, NT>::CTAS)) rpa_int
                 }
             }
             if (part < 0) {
-                const int tok = m2.y + r / G, qh = head * G + r % G;
+                const int tok = m2.y + r / G, qh = m2.x + hr;
                 L = add_sink(L, a.sinks, qh, M);
                 const float inv = L > 0.f ? a.v_scale / L : 0.f;
                 store_o4(a.o, ((size_t)tok * Hq + qh) * D + c, o.x * inv, o.y * inv, o.z * inv, o.w * inv, a.odt);
             } else {
-                *reinterpret_cast<float4*>(a.part_o + ((size_t)part * kDecRows + r) * D + c) = o;
-                if (c == 0) *reinterpret_cast<float2*>(a.part_ml + ((size_t)part * kDecRows + r) * 2) = make_float2(M, L);
+                *reinterpret_cast<float4*>(a.part_o + ((size_t)part * R + r) * D + c) = o;
+                if (c == 0) *reinterpret_cast<float2*>(a.part_ml + ((size_t)part * R + r) * 2) = make_float2(M, L);
             }
         }
-        if (!Gm::OWN) {
-            fence_proxy_async_smem();  // the stage will be refilled by bulk copies
-            __syncwarp();
-            if (lane == 0) mbar_arrive(slot);
-        }
+        fence_proxy_async_smem();  // the stage will be refilled by bulk copies
+        __syncwarp();
+        if (lane == 0) mbar_arrive(slot);
     }
 }
 
@@ -673,10 +663,10 @@ struct UnfoldParams {
     uint8_t* rows;       // [room pages][64][2 Hkv][D] f16
     int* table;          // [max_num_seqs][P64]
     const int *kv_lens, *page_indices, *cu, *vbase;
-    const uint8_t* q;    // rounded to f16 into qbuf (where qbuf is set)
+    const uint8_t* q;    // bf16, rounded to f16 into qbuf (where that is set)
     uint8_t* qbuf;
     int* ctrl;
-    int S, T, Hq, Hkv, D, ps, P, N, P64, group, qdt;
+    int S, T, Hq, Hkv, D, ps, P, N, P64, group;
     int has_window, window, first;
 };
 
@@ -766,42 +756,35 @@ __global__ void __launch_bounds__(kUnfoldThreads, kUnfoldCtas) rpa_int4_unfold(c
     if (p.qbuf) {
         const size_t n = (size_t)p.T * p.Hq * p.D / 8;
         for (size_t i = (size_t)blockIdx.x * kUnfoldThreads + tid; i < n; i += (size_t)gridDim.x * kUnfoldThreads)
-            reinterpret_cast<uint4*>(p.qbuf)[i] = load_q8(p.q, i * 8, p.qdt);
+            reinterpret_cast<uint4*>(p.qbuf)[i] = load_q8(p.q, i * 8, 1);
     }
 }
 
-template <int D, int NG, int NT>
+template <int D, int NG>
 struct I4Kern {
-    using Gm = I4Geom<D, NG, NT>;
+    using Gm = I4Geom<D, NG>;
     static cudaError_t prepare(int* bps) {
-        cudaError_t e = cudaFuncSetAttribute(rpa_int4_attn<D, NG, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, Gm::SMEM);
+        cudaError_t e = cudaFuncSetAttribute(rpa_int4_attn<D, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, Gm::SMEM);
         if (e != cudaSuccess) return e;
-        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(bps, rpa_int4_attn<D, NG, NT>, kI4Threads, Gm::SMEM);
+        return cudaOccupancyMaxActiveBlocksPerMultiprocessor(bps, rpa_int4_attn<D, NG>, Gm::THREADS, Gm::SMEM);
     }
     static cudaError_t launch(const I4Params& p, const Launch& l) {
-        return launch_pdl(rpa_int4_attn<D, NG, NT>, l.grid, kI4Threads, Gm::SMEM, l.stream, p);
+        return launch_pdl(rpa_int4_attn<D, NG>, l.grid, Gm::THREADS, Gm::SMEM, l.stream, p);
     }
 };
 
-template <int D, int NG, typename Op>
-cudaError_t i4_rows(int rows, Op op) {
-    if constexpr (D < 256) {
-        if (rows == 16) return op(I4Kern<D, NG, 2>{});
-    }
-    return rows == 8 ? op(I4Kern<D, NG, 1>{}) : cudaErrorInvalidValue;
-}
 template <typename Op>
-cudaError_t i4_dispatch(int D, int group, int rows, Op op) {
-    if (D == 64) return group == 32 ? i4_rows<64, 2>(rows, op) : group == 64 ? i4_rows<64, 1>(rows, op) : cudaErrorInvalidValue;
-    if (D == 128) return group == 32 ? i4_rows<128, 4>(rows, op) : group == 64 ? i4_rows<128, 2>(rows, op) : i4_rows<128, 1>(rows, op);
-    if (D == 256) return group == 32 ? i4_rows<256, 8>(rows, op) : group == 64 ? i4_rows<256, 4>(rows, op) : i4_rows<256, 2>(rows, op);
+cudaError_t i4_dispatch(int D, int group, Op op) {
+    if (D == 64) return group == 32 ? op(I4Kern<64, 2>{}) : group == 64 ? op(I4Kern<64, 1>{}) : cudaErrorInvalidValue;
+    if (D == 128) return group == 32 ? op(I4Kern<128, 4>{}) : group == 64 ? op(I4Kern<128, 2>{}) : op(I4Kern<128, 1>{});
+    if (D == 256) return group == 32 ? op(I4Kern<256, 8>{}) : group == 64 ? op(I4Kern<256, 4>{}) : op(I4Kern<256, 2>{});
     return cudaErrorInvalidValue;
 }
 
 }  // namespace
 
-cudaError_t int4_prepare(int D, int group, int rows, int* bps) {
-    return i4_dispatch(D, group, rows, [&](auto k) { return decltype(k)::prepare(bps); });
+cudaError_t int4_prepare(int D, int group, int* bps) {
+    return i4_dispatch(D, group, [&](auto k) { return decltype(k)::prepare(bps); });
 }
 
 int enqueue_int4(const RpaCfg& c, const KernelSet& ks, const Workspace& ws, MapCache* maps, const AttnParams& a, int num_seqs,
@@ -816,17 +799,18 @@ int enqueue_int4(const RpaCfg& c, const KernelSet& ks, const Workspace& ws, MapC
         p.a.units = ws.dec_units;
         p.a.item_count_word = kNumDecItems;
         p.a.counter_word = kDecCounter;
-        p.blocks = ks.G / ks.Gp;
-        p.BR = kKS;
+        p.heads = ks.G;
+        p.blocks = ks.Hp / (int)c.num_kv_heads;
+        p.BR = int4_warps(ks.D) % 4 ? 32 : 128;  // runs divide a stage, of 32 keys a warp
         while (c.page_size % p.BR) p.BR >>= 1;
         p.brs = 0;
         while ((1 << p.brs) < p.BR) ++p.brs;
-        p.block = (size_t)c.page_size * int4_key_bytes(ks.D, ks.group);
-        p.qdt = ks.odt;
+        p.block = (uint32_t)(c.page_size * int4_key_bytes(ks.D, ks.group));
+        p.page.set((uint32_t)c.page_size);
         p.stall = eo.debug_stall;
         p.timeout_ns = eo.timeout_ns;
-        if (i4_dispatch(ks.D, ks.group, ks.dec_rows,
-                        [&](auto k) { return decltype(k)::launch(p, Launch{ks.sms * ks.dec_bps, st}); }) != cudaSuccess)
+        if (i4_dispatch(ks.D, ks.group, [&](auto k) { return decltype(k)::launch(p, Launch{ks.sms * ks.dec_bps, st}); }) !=
+            cudaSuccess)
             return RPA_ERR_CUDA;
     }
     if (!rec(kEvDecEnd) || !rec(kEvPfStart)) return RPA_ERR_CUDA;
@@ -840,7 +824,7 @@ int enqueue_int4(const RpaCfg& c, const KernelSet& ks, const Workspace& ws, MapC
         u.cu = a.cu_q_lens;
         u.vbase = ws.vbase;
         u.q = a.q;
-        u.qbuf = ws.qbuf;
+        u.qbuf = ks.q_conv ? nullptr : ws.qbuf;  // (q of 32 bits is there already)
         u.ctrl = ws.ctrl;
         u.S = num_seqs;
         u.T = (int)c.num_q_tokens;
@@ -852,12 +836,11 @@ int enqueue_int4(const RpaCfg& c, const KernelSet& ks, const Workspace& ws, MapC
         u.N = a.N;
         u.P64 = ks.P64;
         u.group = ks.group;
-        u.qdt = ks.odt;
         u.has_window = a.has_window;
         u.window = a.window;
         u.first = a.first;
         if (launch_pdl(rpa_int4_unfold, ks.sms * kUnfoldCtas, kUnfoldThreads, 0, st, u) != cudaSuccess) return RPA_ERR_CUDA;
-        const void* q16 = ws.qbuf ? ws.qbuf : a.q;
+        const void* q16 = u.qbuf ? ws.qbuf : a.q;
         if (maps->kv_ptr != ws.room) {
             if ((ks.tc8 ? encode_kv_map_heads(&maps->kv_pf, ws.room, ks.room_pages, 64, 2 * a.Hkv, ks.D, 64)
                         : encode_kv_map(&maps->kv_pf, ws.room, 0, ks.room_pages, 64, a.Hkv, ks.D, 64)) != 0) {

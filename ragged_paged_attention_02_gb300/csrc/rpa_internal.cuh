@@ -95,8 +95,10 @@ constexpr int kDecRows = 16;       // rows of a decode tile (one m16 MMA tile)
 constexpr int kMlaDqk = 576;
 constexpr int kMlaDv = 512;
 constexpr int kMlaRows = 16;
-constexpr int kInt4Keys = 128;            // keys of a stage of the 4-bit kernel
-constexpr int kInt4MinChunk = 256;        // smallest piece of its items
+constexpr int kInt4Rows = 8;              // query rows of a tile of the 4-bit kernel
+constexpr int kInt4Waves = 4;             // target items per CTA
+// consumer warps of its CTAs, each with 32 keys of a stage
+__host__ __device__ constexpr int int4_warps(int D) { return D == 64 ? 4 : D == 128 ? 7 : 5; }
 constexpr int kInt4DirectRows = 64;       // 4-bit K/V: sequences with more query rows a kv head are unfolded to f16
 constexpr int kInt4MaxRoom = 1 << 20;     // pages of 64 keys (the planner's sums of refused sequences count to this)
 constexpr int kMaxGroup = 64;      // query heads per kv head (a prefill tile holds 128 / G tokens)
@@ -152,7 +154,7 @@ struct PlanParams {
     int int4, dec_tokens, direct_tokens;
     int pf_Hkv;      // kv heads a prefill unit stands for
     int room_pages;
-    int min_chunk;   // smallest split-KV piece (keys)
+    int min_chunk, chunk_align;  // smallest split-KV piece, and what pieces are multiples of (keys)
     int* vbase;      // [max_num_seqs + 1]: a sequence's first page of the room (ascending; none: the next one's)
     int max_units;   // capacity of the unit arrays
     int max_dec_units, max_pf_units;  // capacities of the two unit lists
@@ -232,6 +234,8 @@ struct CombParams {
     const int* cu_q_lens;
     int num_seqs, T, Hq, G, D;
     int rows_max;  // most rows of a combine entry (the decode tile's rows)
+    int part_rows;      // rows of a partial slot
+    int blocks, heads;  // entries' heads a kv head makes, and its query heads (one, and G, but for 4-bit K/V: its last may have fewer)
     float v_scale;
     const float* sinks;  // [Hq] sink logits (natural-log domain), or nullptr
     int odt;             // OutType of o
@@ -299,8 +303,8 @@ struct ReadParams {
     int kt, group;  // KvType of the cache, channels of a group of a 4-bit cache
     float k_scale, v_scale;
 };
-// 4-bit K/V (rows: 8 or 16 query rows of a tile); the attention kernels of one call, between its planner and its merge
-cudaError_t int4_prepare(int D, int group, int rows, int* blocks_per_sm);
+// 4-bit K/V; the attention kernels of one call, between its planner and its merge
+cudaError_t int4_prepare(int D, int group, int* blocks_per_sm);
 cudaError_t launch_read(const ReadParams& p, int q_dtype, int sms, cudaStream_t st);
 // occupancy / attributes (call once per device)
 size_t plan_smem_bytes();

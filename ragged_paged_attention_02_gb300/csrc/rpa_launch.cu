@@ -66,8 +66,9 @@ Layout layout(const RpaCfg& c, const KernelSet& ks) {
     L.dec = off; off = align256(off + (size_t)ks.max_dec_units * sizeof(Unit));
     L.pf = off; off = align256(off + (size_t)ks.max_pf_units * sizeof(Unit));
     L.comb = off; off = align256(off + (size_t)ks.max_comb * sizeof(Comb));
-    L.po = off; off = align256(off + (size_t)ks.max_part * kDecRows * ks.D * sizeof(float));
-    L.pml = off; off = align256(off + (size_t)ks.max_part * kDecRows * 2 * sizeof(float));
+    const size_t part_rows = ks.kt == KT_I4 ? kInt4Rows : kDecRows;
+    L.po = off; off = align256(off + (size_t)ks.max_part * part_rows * ks.D * sizeof(float));
+    L.pml = off; off = align256(off + (size_t)ks.max_part * part_rows * 2 * sizeof(float));
     L.qbuf = off;
     if (ks.q_conv || (ks.room_pages > 0 && c.q_dtype != RPA_DT_F16))
         off = align256(off + (size_t)c.num_q_tokens * c.num_q_heads * ks.D * 2);
@@ -96,12 +97,12 @@ void kernels_choose(const RpaCfg& c, int sms, KernelSet* ks) {
     ks->Hp = (int)c.num_kv_heads * (ks->G / ks->Gp);
     ks->pf_H = ks->Hp;
     if (ks->kt == KT_I4) {
-        // tiles of 16 query rows where a kv head has more than 8 query heads (D 256: always 8; registers), of a divisor of its heads
+        // tiles of 8 query rows, of blocks of a kv head's query heads (as even as they come; the last may have fewer)
+        const int blocks = (ks->G + kInt4Rows - 1) / kInt4Rows;
         ks->group = int4_group(c.kv_dtype);
-        ks->dec_rows = ks->G <= 8 || ks->D == 256 ? 8 : kDecRows;
-        ks->Gp = ks->G < ks->dec_rows ? ks->G : ks->dec_rows;
-        while (ks->G % ks->Gp) --ks->Gp;
-        ks->Hp = (int)c.num_kv_heads * (ks->G / ks->Gp);
+        ks->dec_rows = kInt4Rows;
+        ks->Gp = (ks->G + blocks - 1) / blocks;
+        ks->Hp = (int)c.num_kv_heads * ((ks->G + ks->Gp - 1) / ks->Gp);
         ks->pf_H = (int)c.num_kv_heads;
     }
     const bool eight = kt_8bit(ks->kt);
@@ -111,7 +112,9 @@ void kernels_choose(const RpaCfg& c, int sms, KernelSet* ks) {
     const bool want_f16 = ks->kt != KT_BF16;
     const int qd = c.q_dtype;
     if (ks->kt == KT_I4) {
-        // (the direct kernel rounds q as it loads it, the prompts' f16 copy is made with their rows')
+        // (the direct kernel rounds a 16-bit q as it loads it, the prompts' f16 copy is made with their rows)
+        ks->q_conv = ks->q_conv_f16 = qd == RPA_DT_F32;
+        ks->q_f16 = qd != RPA_DT_BF16;
     } else if (qd == RPA_DT_F32) {
         ks->q_conv = 1;
         ks->q_conv_f16 = want_f16;
@@ -122,7 +125,7 @@ void kernels_choose(const RpaCfg& c, int sms, KernelSet* ks) {
         ks->q_conv = 1;  // bf16 q, f16 K/V: q to f16
         ks->q_conv_f16 = 1;
     }
-    ks->q_f16 = eight && (qd == RPA_DT_F16 || qd == RPA_DT_F32);
+    if (eight) ks->q_f16 = qd == RPA_DT_F16 || qd == RPA_DT_F32;
     const double k_sc = c.has_k_scale ? c.k_scale : 1.0;
     ks->qk_log2 = (float)(c.sm_scale * k_sc * kLog2e);
     ks->cap_exp = c.has_soft_cap ? (float)(2.0 * c.sm_scale * k_sc / c.soft_cap * kLog2e) : 0.f;
@@ -175,7 +178,7 @@ cudaError_t kernels_occupancy(KernelSet* ks) {
                  : prefill_tc8_prepare(ks->D, pf_kt, &ks->pf_bps);
     if (e != cudaSuccess) return e;
     if (ks->kt == KT_I4) {
-        e = int4_prepare(ks->D, ks->group, ks->dec_rows, &ks->dec_bps);
+        e = int4_prepare(ks->D, ks->group, &ks->dec_bps);
         if (e != cudaSuccess) return e;
     } else if (ks->tc8 || ks->mla) {
         // the 8-bit tensor-memory kernel (and the latent kernel) takes the decode rows too: the
@@ -204,11 +207,13 @@ void kernels_capacity(const RpaCfg& c, KernelSet* ks) {
     ks->max_part = (int)(ks->max_dec_units * Hkv);
     ks->max_comb = (int)(S * Hkv);
     if (ks->kt == KT_I4) {
-        // a sequence makes tiles of Tt tokens; those with several pieces have at most twice the pieces that the chunk rule aims at
+        // a sequence makes tiles of Tt tokens; those with several pieces have one more each than the chunk rule aims at, and twice
+        // as many together at most
         ks->max_dec_units += (int)(c.num_q_tokens / ks->Tt + 1);
         ks->max_units = ks->max_dec_units + pf_only_units;
         ks->max_pf_units = pf_only_units;
-        ks->max_part = (int)(2 * (kDecWaves * dec_slots + Hkv));
+        const int64_t target = kInt4Waves * dec_slots, tiles = (c.num_q_tokens / ks->Tt + S + 1) * Hkv;
+        ks->max_part = (int)(target + (tiles < target ? tiles : target));
         ks->max_comb = ks->max_part / 2;
     }
 }
@@ -447,7 +452,8 @@ int enqueue_forward(const RpaCfg& c, const KernelSet& ks, const Workspace& ws, M
     pp.pf_Hkv = ks.pf_H;
     pp.room_pages = ks.room_pages;
     pp.vbase = ws.vbase;
-    pp.min_chunk = pp.int4 ? kInt4MinChunk : kMinChunk;
+    pp.chunk_align = pp.int4 ? 32 * int4_warps(ks.D) : kChunkAlign;  // 4-bit K/V: whole stages
+    pp.min_chunk = pp.int4 ? pp.chunk_align : kMinChunk;
     pp.pf_mma_rows = ks.tc ? 2 * kTcRows : ks.mla ? kMlaRows : kTcRows;
     pp.dec_on_pf = (ks.tc8 && !pp.int4) || ks.mla;
     pp.D = ks.D;
@@ -457,7 +463,7 @@ int enqueue_forward(const RpaCfg& c, const KernelSet& ks, const Workspace& ws, M
     pp.hbm_gbs = kHbmGBs;
     pp.force_pf_sms = eo.force_pf_sms;
     pp.force_dec_sms = eo.force_dec_sms;
-    pp.dec_waves = ks.tc8 && !pp.int4 ? kDecWavesTc8 : kDecWaves;
+    pp.dec_waves = pp.int4 ? kInt4Waves : ks.tc8 ? kDecWavesTc8 : kDecWaves;
     pp.epoch = eo.epoch;
     pp.early = eo.plan_early;
     pp.max_units = ks.max_units;
@@ -488,6 +494,9 @@ int enqueue_forward(const RpaCfg& c, const KernelSet& ks, const Workspace& ws, M
     cp.G = ks.Gp;
     cp.D = ks.Dv;  // the width of o and of the split-KV partials
     cp.rows_max = ks.dec_rows;
+    cp.part_rows = ks.kt == KT_I4 ? kInt4Rows : kDecRows;
+    cp.blocks = ks.kt == KT_I4 ? ks.Hp / ap.Hkv : 1;
+    cp.heads = ks.kt == KT_I4 ? ks.G : ks.Gp;
     cp.v_scale = ks.v_scale;
     cp.sinks = ap.sinks;
     cp.odt = ks.odt;

@@ -226,8 +226,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
         const unsigned long long target = (unsigned long long)p.dec_waves * (unsigned long long)max(1, dec_ctas);
         unsigned long long c = (s_total + target - 1) / target;
         if (c < (unsigned long long)p.min_chunk) c = p.min_chunk;
-        const int align = p.int4 ? kInt4Keys : kChunkAlign;
-        c = (c + align - 1) / align * align;
+        c = (c + p.chunk_align - 1) / p.chunk_align * p.chunk_align;
         if (c > (1ull << 30)) c = 1ull << 30;
         chunk = (int)c;
     }
