@@ -83,6 +83,27 @@ __device__ __forceinline__ void exp_chunk(const uint32_t* sv, uint64_t mul2, uin
     }
 }
 
+// Bits of the keys lo .. hi among the 32 from `first` on
+__device__ __forceinline__ uint32_t key_bits(int lo, int hi, int first) {
+    const int a = lo - first, b = hi - first;
+    const uint32_t from = a <= 0 ? 0xffffffffu : a > 31 ? 0u : 0xffffffffu << a;
+    const uint32_t to = b < 0 ? 0u : b >= 31 ? 0xffffffffu : (2u << b) - 1u;
+    return from & to;
+}
+// The 32 logits of one S chunk times `mul`, those without a bit in `allow` to -inf, in place; m4: running maxima
+__device__ __forceinline__ void mask_chunk(uint32_t* sv, uint64_t mul2, uint32_t allow, float* m4) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        float v0, v1;
+        f32x2_split(fmul2(f32x2(__uint_as_float(sv[2 * i]), __uint_as_float(sv[2 * i + 1])), mul2), v0, v1);
+        v0 = allow & (1u << (2 * i)) ? v0 : -INFINITY;
+        v1 = allow & (2u << (2 * i)) ? v1 : -INFINITY;
+        m4[i & 3] = fmax3(m4[i & 3], v0, v1);
+        sv[2 * i] = __float_as_uint(v0);
+        sv[2 * i + 1] = __float_as_uint(v1);
+    }
+}
+
 template <int D, bool F16>
 __global__ void __launch_bounds__(kThreads, 1) rpa_prefill_tc(const __grid_constant__ CUtensorMap kvmap,
                                                               const __grid_constant__ CUtensorMap qmap,
@@ -397,8 +418,8 @@ __global__ void __launch_bounds__(kThreads, 1) rpa_prefill_tc(const __grid_const
                 const bool need_mask = partial || (a.causal && k_lo + kBN - 1 > pos_lo) ||
                                        (a.has_window && k_lo <= pos_hi - a.window);
                 const uint32_t scol = Gm::TM_S(x);
-                // pass 1: row max of the transformed logits; masked or capped values are
-                // written back to TMEM so that pass 2 only exponentiates
+                // pass 1: row max of the transformed logits (capped ones are written back to TMEM so
+                // that pass 2 only exponentiates)
                 const bool rewrite = need_mask || a.has_cap;
                 float mt = -INFINITY;
                 uint64_t ls2[2] = {f32x2(0.f, 0.f), f32x2(0.f, 0.f)};
@@ -454,8 +475,44 @@ __global__ void __launch_bounds__(kThreads, 1) rpa_prefill_tc(const __grid_const
                     tmem_st16(lane_addr + scol + 32, pk);
                     exp_chunk<F16>(sb, mul2, nbase2, ls2, pk);
                     tmem_st16(lane_addr + scol + 48, pk);
+                } else if (!a.has_cap) {
+                    // masked, no cap: as above, the keys a row sees as a bit for each key of a chunk; the logits are scaled
+                    // before they are masked
+                    const int hi = min(kv_end - 1, a.causal ? pos : kv_end);
+                    const int lo = a.has_window ? max(kv_begin, pos - a.window + 1) : kv_begin;
+                    const int first = a.has_window ? min(hi, a.first - 1) : -1;  // the last of the visible first keys
+                    auto allow = [&](int c) { return key_bits(lo, hi, k_lo + 32 * c) | key_bits(kv_begin, first, k_lo + 32 * c); };
+                    const uint64_t qk2 = f32x2(a.qk_log2, a.qk_log2);
+                    float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                    uint32_t sa[32], sb[32];
+#pragma unroll
+                    for (int h = 1; h >= 0; --h) {
+                        tmem_ld32(lane_addr + scol + (2 * h) * 32, sa);
+                        tmem_ld32(lane_addr + scol + (2 * h + 1) * 32, sb);
+                        tmem_ld_wait();
+                        mask_chunk(sa, qk2, allow(2 * h), m4);
+                        mask_chunk(sb, qk2, allow(2 * h + 1), m4);
+                    }
+                    mt = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+                    need = __any_sync(0xffffffffu, mt > m_run + kRescaleLog2);
+                    m_new = need ? fmaxf(m_run, mt) : m_run;
+                    alpha = !need ? 1.f : (m_run == -INFINITY ? 0.f : ex2(m_run - m_new));
+                    const float base = m_new == -INFINITY ? 0.f : m_new;
+                    const uint64_t one2 = f32x2(1.f, 1.f), nbase2 = f32x2(-base, -base);
+                    uint32_t pk[16];
+                    exp_chunk<F16>(sa, one2, nbase2, ls2, pk);
+                    tmem_st16(lane_addr + scol, pk);
+                    exp_chunk<F16>(sb, one2, nbase2, ls2, pk);
+                    tmem_st16(lane_addr + scol + 16, pk);
+#pragma unroll 1
+                    for (int c = 2; c < 4; ++c) {
+                        tmem_ld32(lane_addr + scol + 32 * c, sa);
+                        tmem_ld_wait();
+                        mask_chunk(sa, qk2, allow(c), m4);
+                        exp_chunk<F16>(sa, one2, nbase2, ls2, pk);
+                        tmem_st16(lane_addr + scol + 16 * c, pk);
+                    }
                 } else {
-                    const bool cap = a.has_cap;
 #pragma unroll 1
                     for (int c = 0; c < kBN / 32; ++c) {
                         uint32_t sv[32];
@@ -464,8 +521,7 @@ __global__ void __launch_bounds__(kThreads, 1) rpa_prefill_tc(const __grid_const
 #pragma unroll
                         for (int i = 0; i < 32; ++i) {
                             float v = __uint_as_float(sv[i]);
-                            v = cap ? a.cap_log2 - 2.f * a.cap_log2 * rcp_approx(1.f + ex2(v * a.cap_exp))
-                                    : v * a.qk_log2;
+                            v = a.cap_log2 - 2.f * a.cap_log2 * rcp_approx(1.f + ex2(v * a.cap_exp));
                             const int j = k_lo + c * 32 + i;
                             const bool okk = j >= kv_begin && j < kv_end && (!a.causal || j <= pos) &&
                                              (!a.has_window || j > pos - a.window || j < a.first);
