@@ -110,8 +110,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
     // run while that kernel does.  Unless the caller has said that the inputs are complete at
     // launch (RPA_OPT_PLAN_EARLY), it waits for that kernel before reading them; either way it
     // waits before rewriting what earlier kernels read (below)
-    // (4-bit K/V: vbase is written on the way)
-    if (!p.early || p.int4) pdl_wait();
+    // (where 4-bit K/V have a room, vbase is written on the way)
+    if (!p.early || (p.int4 && p.room_pages > 0)) pdl_wait();
     // per-sequence scratch (shared memory when it fits): class, count, decode / prefill
     // unit ends, partial offset, combine offset, decode sequences with a partial last piece before
     // this one, first query token (S + 1 entries: cu_q_lens), kv_len
@@ -130,7 +130,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
     if (tid == 0) s_bad = 0;
     __syncthreads();
 
-    if (p.int4) give_room(p, s_cls, s_scan, &s_taken);  // (each thread reads back its own entries of s_cls)
+    const bool room = p.int4 && p.room_pages > 0;
+    if (room) give_room(p, s_cls, s_scan, &s_taken);  // (each thread reads back its own entries of s_cls)
     // ---- 1. validate and classify each sequence; per-thread sums of decode (key, kv head)
     // pairs and of the keys prefill units visit, reduced over the block below
     unsigned long long my_total = 0ull, my_pf_keys = 0ull;
@@ -145,7 +146,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
         if (bad) {
             s_bad = 1;
         } else if (ql > 0) {
-            if (p.int4 ? !s_cls[s] : (long long)ql * p.G <= p.dec_rows) {
+            if (p.int4 ? !room || !s_cls[s] : (long long)ql * p.G <= p.dec_rows) {
                 int lo, hi;
                 key_band(kl, ql, 0, ql, p, lo, hi);
                 cls = 1;
