@@ -678,22 +678,44 @@ __global__ void __launch_bounds__(kUnfoldThreads, kUnfoldCtas) rpa_int4_unfold(c
     if (p.ctrl[kNumPfItems] == 0) return;
     const int tid = threadIdx.x, lane = tid & 31;
     const int total = p.vbase[p.S], per_row = p.D / 16;
-    __shared__ int s_seq;
+    // up to kSeqs sequences' first pages, query tokens and keys (beside more a warp searches a task's sequence)
+    constexpr int kSeqs = 512;
+    __shared__ int s_base[kSeqs + 1], s_ql[kSeqs], s_kl[kSeqs], s_seq;
+    const bool few = p.S <= kSeqs;
+    if (few) {
+        for (int i = tid; i < p.S; i += kUnfoldThreads) {
+            s_base[i] = p.vbase[i];
+            s_ql[i] = p.cu[i + 1] - p.cu[i];
+            s_kl[i] = p.kv_lens[i];
+        }
+        __syncthreads();
+    }
     // a task: 64 keys of one kv head
     for (int task = blockIdx.x; task < total * p.Hkv; task += gridDim.x) {
         const int v = task / p.Hkv, h = task - v * p.Hkv;
-        __syncthreads();
-        if (tid < 32) {
-            const int s = find_seq(p.vbase, p.S, v, lane);
-            if (lane == 0) s_seq = s;
+        int s = 0;
+        if (few) {
+            int e = p.S;  // the last sequence whose pages start at or before v
+            while (e - s > 1) {
+                const int m = (s + e) / 2;
+                if (s_base[m] <= v) s = m;
+                else e = m;
+            }
+        } else {
+            __syncthreads();
+            if (tid < 32) {
+                const int x = find_seq(p.vbase, p.S, v, lane);
+                if (lane == 0) s_seq = x;
+            }
+            __syncthreads();
+            s = s_seq;
+            if (s < 0) continue;  // (not reached: vbase covers the pages)
         }
-        __syncthreads();
-        const int s = s_seq;
-        if (s < 0) continue;  // (not reached: vbase covers the pages)
-        const int ql = p.cu[s + 1] - p.cu[s], kl = p.kv_lens[s];
+        const int base = few ? s_base[s] : p.vbase[s];
+        const int ql = few ? s_ql[s] : p.cu[s + 1] - p.cu[s], kl = few ? s_kl[s] : p.kv_lens[s];
         int lo = p.has_window ? max(0, kl - ql - p.window + 1) : 0;
         if (lo <= p.first) lo = 0;
-        const int nf = lo > 0 ? (p.first + 63) / 64 : 0, at = v - p.vbase[s];
+        const int nf = lo > 0 ? (p.first + 63) / 64 : 0, at = v - base;
         const int page64 = at < nf ? at : lo / 64 + at - nf;
         if (h == 0 && tid == 0) p.table[(size_t)s * p.P64 + page64] = v;
         // a thread takes one unit of 16 channels of K and V of a key, kFly keys in flight
@@ -729,26 +751,20 @@ __global__ void __launch_bounds__(kUnfoldThreads, kUnfoldCtas) rpa_int4_unfold(c
                 if (slot >= 64 || page64 * 64 + slot >= kl) continue;
 #pragma unroll
                 for (int is_v = 0; is_v < 2; ++is_v) {
-                    uint4 out[2] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+                    uint32_t out[8] = {0, 0, 0, 0, 0, 0, 0, 0};
                     if (good[b]) {
                         const float2 sz = f16x2_to_f32x2(pairs[b][is_v]);
-                        const uint32_t w[2] = {codes[b][is_v].x, codes[b][is_v].y};
                         float f[16];
+                        int4_values(codes[b][is_v], sz, f);
+                        // the greatest code of a group that ends at f16's largest value may pass it by the scale's rounding
+                        if (fmaf(15.f, sz.x, sz.y) > 65504.f) {
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) {
-                            // rounded to f16; the greatest code of a group that ends at f16's largest value may pass it by the
-                            // scale's rounding
-                            const float y = fmaf(__uint_as_float(((w[k / 8] >> (4 * (k % 8))) & 15u) | 0x4b000000u) - 8388608.f, sz.x, sz.y);
-                            f[k] = y > 65504.f ? 65504.f : y;
+                            for (int k = 0; k < 16; ++k) f[k] = f[k] > 65504.f ? 65504.f : f[k];
                         }
 #pragma unroll
-                        for (int k = 0; k < 2; ++k)
-                            out[k] = make_uint4(pack2<true>(f[8 * k], f[8 * k + 1]), pack2<true>(f[8 * k + 2], f[8 * k + 3]),
-                                                pack2<true>(f[8 * k + 4], f[8 * k + 5]), pack2<true>(f[8 * k + 6], f[8 * k + 7]));
+                        for (int k = 0; k < 8; ++k) out[k] = pack2<true>(f[2 * k], f[2 * k + 1]);
                     }
-                    uint4* dst = reinterpret_cast<uint4*>(p.rows + ((((size_t)v * 64 + slot) * 2 * p.Hkv + 2 * h + is_v) * p.D + 16 * place) * 2);
-                    dst[0] = out[0];
-                    dst[1] = out[1];
+                    store_32(p.rows + ((((size_t)v * 64 + slot) * 2 * p.Hkv + 2 * h + is_v) * p.D + 16 * place) * 2, out);
                 }
             }
         }

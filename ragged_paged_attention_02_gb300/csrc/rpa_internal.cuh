@@ -301,6 +301,7 @@ struct ReadParams {
     int* status;
     int S, T, Hkv, D, ps, P, N, latent;
     int kt, group;  // KvType of the cache, channels of a group of a 4-bit cache
+    int wide;       // k and v start on 32 bytes
     float k_scale, v_scale;
 };
 // 4-bit K/V; the attention kernels of one call, between its planner and its merge
@@ -599,6 +600,20 @@ __device__ __forceinline__ float2 f16x2_to_f32x2(uint32_t v) {
         : "r"(v));
     return make_float2(lo, hi);
 }
+// Sixteen 4-bit codes (in memory order) times a scale plus a zero: the product is exact in 32 bits, the sum rounds once.  A code
+// in the low byte of 0x4b000000 is 2^23 + code.
+__device__ __forceinline__ void int4_values(uint2 codes, float2 sz, float* f) {
+    const uint64_t back = f32x2(-8388608.f, -8388608.f), s2 = f32x2(sz.x, sz.x), z2 = f32x2(sz.y, sz.y);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const uint32_t w = k ? codes.y : codes.x, lo = w & 0x0f0f0f0fu, hi = (w >> 4) & 0x0f0f0f0fu;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint64_t c = f32x2(__uint_as_float(__byte_perm(lo, 0x4b000000u, 0x7540 + i)), __uint_as_float(__byte_perm(hi, 0x4b000000u, 0x7540 + i)));
+            f32x2_split(ffma2(fadd2(c, back), s2, z2), f[8 * k + 2 * i], f[8 * k + 2 * i + 1]);
+        }
+    }
+}
 // Two bf16 (one word) -> f16x2, round to nearest even
 __device__ __forceinline__ uint32_t bf16x2_to_f16x2(uint32_t v) {
     return pack2<true>(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
@@ -627,6 +642,8 @@ __device__ __forceinline__ void store_f32x8(float* p, const uint32_t* v) {
                  "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
                  : "memory");
 }
+// 32 bytes (32-byte aligned) in one store, a whole sector a lane.
+__device__ __forceinline__ void store_32(void* p, const uint32_t* v) { store_f32x8(static_cast<float*>(p), v); }
 // Eight consecutive elements v[0..7] * s (e a multiple of 8).
 __device__ __forceinline__ void store_o8(uint8_t* o, size_t e, const uint32_t* v, float s, int odt) {
     float f[8];

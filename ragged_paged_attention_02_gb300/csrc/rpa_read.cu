@@ -33,45 +33,70 @@ struct Unit16<kRead4> {
     uint32_t scale_zero;
 };
 
-__device__ __forceinline__ void put16(float* o, const float* f) {
+// Sixteen elements; where the output starts on 32 bytes (`wide`) a sector in one store.
+__device__ __forceinline__ void put_words(void* o, const uint32_t* w, int n, bool wide) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) reinterpret_cast<float4*>(o)[i] = make_float4(f[4 * i], f[4 * i + 1], f[4 * i + 2], f[4 * i + 3]);
-}
-template <bool F16>
-__device__ __forceinline__ void put16_2(void* o, const float* f) {
-    uint4* d = static_cast<uint4*>(o);
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-        d[i] = make_uint4(pack2<F16>(f[8 * i], f[8 * i + 1]), pack2<F16>(f[8 * i + 2], f[8 * i + 3]), pack2<F16>(f[8 * i + 4], f[8 * i + 5]),
-                          pack2<F16>(f[8 * i + 6], f[8 * i + 7]));
-}
-__device__ __forceinline__ void put16(__nv_bfloat16* o, const float* f) { put16_2<false>(o, f); }
-__device__ __forceinline__ void put16(__half* o, const float* f) { put16_2<true>(o, f); }
-
-// Loads the unit `place` (16 elements) of a slot's row of kv head h.
-template <int MODE>
-__device__ __forceinline__ void load_unit(const ReadParams& p, int page, int at, int h, int is_v, int place, Unit16<MODE>& x) {
-    if constexpr (MODE == kRead4) {
-        const uint8_t* block = p.kv + ((size_t)page * p.Hkv + h) * ((size_t)p.ps * int4_key_bytes(p.D, p.group));
-        const uint32_t line = (uint32_t)(is_v ? p.ps : 0) + at;
-        x.codes = *reinterpret_cast<const uint2*>(block + (size_t)line * (p.D / 2) + int4_chunk(place / 2, at, p.D) * 16 + (place & 1) * 8);
-        x.scale_zero = reinterpret_cast<const uint32_t*>(block + (size_t)p.ps * p.D)[(size_t)line * (p.D / p.group) + 16 * place / p.group];
-    } else {
-        const int rows = (p.latent ? 1 : 2) * p.Hkv;
-        const size_t row = ((size_t)page * p.ps + at) * rows + (p.latent ? h : 2 * h + is_v);
-        const uint4* s = reinterpret_cast<const uint4*>(p.kv + (row * p.D + 16 * place) * (MODE == kRead16 ? 2 : 1));
-#pragma unroll
-        for (int k = 0; k < (MODE == kRead16 ? 2 : 1); ++k) x.a[k] = s[k];
+    for (int i = 0; i < n; i += 8) {
+        if (wide) {
+            store_32(static_cast<uint32_t*>(o) + i, w + i);
+        } else {
+            static_cast<uint4*>(o)[i / 4] = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+            static_cast<uint4*>(o)[i / 4 + 1] = make_uint4(w[i + 4], w[i + 5], w[i + 6], w[i + 7]);
+        }
     }
 }
+__device__ __forceinline__ void put16(float* o, const float* f, bool wide) {
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(f[i]);
+    put_words(o, w, 16, wide);
+}
+template <bool F16>
+__device__ __forceinline__ void put16_2(void* o, const float* f, bool wide) {
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = pack2<F16>(f[2 * i], f[2 * i + 1]);
+    put_words(o, w, 8, wide);
+}
+__device__ __forceinline__ void put16(__nv_bfloat16* o, const float* f, bool wide) { put16_2<false>(o, f, wide); }
+__device__ __forceinline__ void put16(__half* o, const float* f, bool wide) { put16_2<true>(o, f, wide); }
+
+// Where a token's rows lie: its unit of K of kv head 0, from there on a head's and V's, and of a 4-bit cache the same of the pairs.
+template <int MODE>
+struct Rows {
+    const uint8_t *at, *pair;
+    uint32_t head, v, pair_v;
+    __device__ __forceinline__ Rows(const ReadParams& p, int page, int slot, int place) {
+        if constexpr (MODE == kRead4) {
+            const int ng = p.D / p.group;
+            head = (uint32_t)(p.ps * int4_key_bytes(p.D, p.group));
+            const uint8_t* block = p.kv + (size_t)page * p.Hkv * head;
+            at = block + (uint32_t)(slot * (p.D / 2) + int4_chunk(place / 2, slot, p.D) * 16 + (place & 1) * 8);
+            pair = block + (uint32_t)(p.ps * p.D + slot * ng * 4 + 16 * place / p.group * 4);
+            v = (uint32_t)(p.ps * (p.D / 2));
+            pair_v = (uint32_t)(p.ps * ng * 4);
+        } else {
+            const uint32_t row = (uint32_t)p.D * (MODE == kRead16 ? 2 : 1);
+            head = p.latent ? row : 2 * row;
+            at = p.kv + ((size_t)page * p.ps + slot) * ((size_t)p.Hkv * head) + 16 * place * (MODE == kRead16 ? 2 : 1);
+            v = row;
+        }
+    }
+    __device__ __forceinline__ void load(int h, bool is_v, Unit16<MODE>& x) const {
+        const uint8_t* s = at + (size_t)h * head + (is_v ? v : 0u);
+        if constexpr (MODE == kRead4) {
+            x.codes = *reinterpret_cast<const uint2*>(s);
+            x.scale_zero = *reinterpret_cast<const uint32_t*>(pair + (size_t)h * head + (is_v ? pair_v : 0u));
+        } else {
+#pragma unroll
+            for (int k = 0; k < (MODE == kRead16 ? 2 : 1); ++k) x.a[k] = reinterpret_cast<const uint4*>(s)[k];
+        }
+    }
+};
 template <int MODE>
 __device__ __forceinline__ void widen(const Unit16<MODE>& x, int kt, float* f) {
     if constexpr (MODE == kRead4) {
-        const float2 sz = f16x2_to_f32x2(x.scale_zero);
-        const uint32_t w[2] = {x.codes.x, x.codes.y};
-#pragma unroll
-        for (int k = 0; k < 16; ++k)  // 2^23 + code, exactly
-            f[k] = fmaf(__uint_as_float(((w[k / 8] >> (4 * (k % 8))) & 15u) | 0x4b000000u) - 8388608.f, sz.x, sz.y);
+        int4_values(x.codes, f16x2_to_f32x2(x.scale_zero), f);
     } else if constexpr (MODE == kRead16) {
         const uint32_t w[8] = {x.a[0].x, x.a[0].y, x.a[0].z, x.a[0].w, x.a[1].x, x.a[1].y, x.a[1].z, x.a[1].w};
 #pragma unroll
@@ -156,13 +181,13 @@ __global__ void __launch_bounds__(kReadThreads, kReadCtas) rpa_read_kernel(const
         __syncthreads();
         const long long slot = mine < n ? s_page[mine] : -1;
         if (slot >= 0) {
-            const int page = (int)(slot >> 32), at = (int)slot;
+            const Rows<MODE> from(p, (int)(slot >> 32), (int)slot, place);
             const size_t out = ((size_t)(t0 + mine) * p.Hkv) * p.D + 16 * place;
             for (int r = r0; r < r1; r += kReadFly) {
                 Unit16<MODE> x[kReadFly];
 #pragma unroll
                 for (int b = 0; b < kReadFly; ++b)
-                    if (r + b < r1) load_unit<MODE>(p, page, at, r + b < p.Hkv ? r + b : r + b - p.Hkv, r + b >= p.Hkv, place, x[b]);
+                    if (r + b < r1) from.load(r + b < p.Hkv ? r + b : r + b - p.Hkv, r + b >= p.Hkv, x[b]);
 #pragma unroll
                 for (int b = 0; b < kReadFly; ++b) {
                     if (r + b >= r1) break;
@@ -174,7 +199,7 @@ __global__ void __launch_bounds__(kReadThreads, kReadCtas) rpa_read_kernel(const
 #pragma unroll
                         for (int k = 0; k < 16; ++k) f[k] *= sc;
                     }
-                    put16(reinterpret_cast<QT*>(is_v ? p.v : p.k) + out + (size_t)(is_v ? r + b - p.Hkv : r + b) * p.D, f);
+                    put16(reinterpret_cast<QT*>(is_v ? p.v : p.k) + out + (size_t)(is_v ? r + b - p.Hkv : r + b) * p.D, f, p.wide);
                 }
             }
         }

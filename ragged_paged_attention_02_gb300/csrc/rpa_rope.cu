@@ -663,6 +663,7 @@ int rpa_rope_read(RpaRope* h, const void* kv_pages, const int32_t* kv_lens, cons
     p.group = int4_group(c.kv_dtype);
     p.k_scale = c.has_k_scale ? c.k_scale : 1.f;
     p.v_scale = c.has_v_scale ? c.v_scale : 1.f;
+    p.wide = aligned(k_out, 32) && aligned(v_out, 32);
     if (launch_read(p, c.q_dtype, h->sms, static_cast<cudaStream_t>(stream)) != cudaSuccess) {
         cudaGetLastError();
         return RPA_ERR_CUDA;
