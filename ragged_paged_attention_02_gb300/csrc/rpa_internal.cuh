@@ -97,6 +97,7 @@ constexpr int kMlaDv = 512;
 constexpr int kMlaRows = 16;
 constexpr int kInt4Rows = 8;              // query rows of a tile of the 4-bit kernel
 constexpr int kInt4Waves = 4;             // target items per CTA
+constexpr int kInt4Stages = 5;            // stages of an item that make up for its start and end
 // consumer warps of its CTAs, each with 32 keys of a stage
 __host__ __device__ constexpr int int4_warps(int D) { return D == 64 ? 4 : D == 128 ? 7 : 5; }
 constexpr int kInt4DirectRows = 64;       // 4-bit K/V: sequences with more query rows a kv head are unfolded to f16
@@ -155,6 +156,7 @@ struct PlanParams {
     int pf_Hkv;      // kv heads a prefill unit stands for
     int room_pages;
     int min_chunk, chunk_align;  // smallest split-KV piece, and what pieces are multiples of (keys)
+    int good_chunk;              // pieces are as long as this, if there is so much for every CTA (0: no matter)
     int* vbase;      // [max_num_seqs + 1]: a sequence's first page of the room (ascending; none: the next one's)
     int max_units;   // capacity of the unit arrays
     int max_dec_units, max_pf_units;  // capacities of the two unit lists

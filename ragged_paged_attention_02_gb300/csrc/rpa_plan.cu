@@ -226,6 +226,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
         const int dec_ctas = p.dec_on_pf ? s_split[0] : s_split[1];
         const unsigned long long target = (unsigned long long)p.dec_waves * (unsigned long long)max(1, dec_ctas);
         unsigned long long c = (s_total + target - 1) / target;
+        // 4-bit K/V: pieces long enough to make up for an item's start and end, as long as every CTA has one
+        const unsigned long long one = (s_total + max(1, dec_ctas) - 1) / (unsigned long long)max(1, dec_ctas);
+        if (c < (unsigned long long)p.good_chunk) c = min(one, (unsigned long long)p.good_chunk);
         if (c < (unsigned long long)p.min_chunk) c = p.min_chunk;
         c = (c + p.chunk_align - 1) / p.chunk_align * p.chunk_align;
         if (c > (1ull << 30)) c = 1ull << 30;
