@@ -420,10 +420,13 @@ __global__ void __launch_bounds__((I4Geom<D, NG>::THREADS), (I4Geom<D, NG>::CTAS
                     load_meta<NG>(at + (h ? pair8 : 0u) + BR * (NG * 4), vm[sub][h]);
                 }
                 float e[4], o[4];
+                uint32_t kf[C / 2][4];
+#pragma unroll
+                for (int c = 0; c < C; c += 2)
+                    ldsm_x4(row + ((uint32_t)(c << 4) ^ sw[sub]), kf[c / 2][0], kf[c / 2][1], kf[c / 2][2], kf[c / 2][3]);
 #pragma unroll
                 for (int c = 0; c < C; c += 2) {
-                    uint32_t f[4];
-                    ldsm_x4(row + ((uint32_t)(c << 4) ^ sw[sub]), f[0], f[1], f[2], f[3]);
+                    const uint32_t* f = kf[c / 2];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int cc = c + h;
@@ -450,6 +453,15 @@ __global__ void __launch_bounds__((I4Geom<D, NG>::THREADS), (I4Geom<D, NG>::CTAS
                     }
                 }
             }
+            // the first 16 keys' V, on its way during the softmax
+            uint32_t vf[C / 2][4];
+            auto load_v = [&](int sub) {
+                const uint32_t row = stage + row0 + (sub ? row16 : 0u) + BR * (D / 2);
+#pragma unroll
+                for (int c = 0; c < C; c += 2)
+                    ldsm_x4_t(row + ((uint32_t)(c << 4) ^ sw[sub]), vf[c / 2][0], vf[c / 2][1], vf[c / 2][2], vf[c / 2][3]);
+            };
+            if constexpr (D < 256) load_v(0);
             // ---- scale or soft cap (log2 domain), then masks
             if (a.has_cap) {
                 const float ce = a.cap_exp * 1048576.f, cl = a.cap_log2;
@@ -541,12 +553,11 @@ __global__ void __launch_bounds__((I4Geom<D, NG>::THREADS), (I4Geom<D, NG>::CTAS
             // ---- O^T += V^T P^T, group by group
 #pragma unroll
             for (int sub = 0; sub < SUBS; ++sub) {
-                const uint32_t row = stage + row0 + (sub ? row16 : 0u) + BR * (D / 2);
                 uint32_t pb[2];
+                if (sub || D == 256) load_v(sub);
 #pragma unroll
                 for (int c = 0; c < C; c += 2) {
-                    uint32_t f[4];
-                    ldsm_x4_t(row + ((uint32_t)(c << 4) ^ sw[sub]), f[0], f[1], f[2], f[3]);
+                    const uint32_t* f = vf[c / 2];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int cc = c + h, gi = cc / CPG;
@@ -670,7 +681,7 @@ struct UnfoldParams {
     int has_window, window, first;
 };
 
-constexpr int kUnfoldThreads = 256, kUnfoldCtas = 6;
+constexpr int kUnfoldThreads = 256, kUnfoldCtas = 5;
 
 __global__ void __launch_bounds__(kUnfoldThreads, kUnfoldCtas) rpa_int4_unfold(const UnfoldParams p) {
     pdl_trigger();

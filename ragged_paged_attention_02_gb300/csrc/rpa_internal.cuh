@@ -100,7 +100,11 @@ constexpr int kInt4Waves = 4;             // target items per CTA
 constexpr int kInt4Stages = 5;            // stages of an item that make up for its start and end
 // consumer warps of its CTAs, each with 32 keys of a stage
 __host__ __device__ constexpr int int4_warps(int D) { return D == 64 ? 4 : D == 128 ? 7 : 5; }
-constexpr int kInt4DirectRows = 64;       // 4-bit K/V: sequences with more query rows a kv head are unfolded to f16
+// 4-bit K/V: a sequence whose query rows a kv head number more than kInt4DirectRows + kInt4RowsByItems / n, at most kInt4FewRows, is
+// unfolded to f16, n being the (such sequence, kv head) pairs.  The direct kernel's time goes by rows; a prefill item takes its
+// keys' time (0.11 ms for 8 k) whatever its rows up to a tile, and its keys are not split, so few items leave SMs idle.  With
+// 8 kv heads of 4 query heads, D 128, 8 k keys the two met at 440 rows of one sequence, 190 of 4, 124 of 8, 96 of 12 and 84 of 32.
+constexpr int kInt4DirectRows = 64, kInt4RowsByItems = 3000, kInt4FewRows = 448;
 constexpr int kInt4MaxRoom = 1 << 20;     // pages of 64 keys (the planner's sums of refused sequences count to this)
 constexpr int kMaxGroup = 64;      // query heads per kv head (a prefill tile holds 128 / G tokens)
 constexpr int kDecWaves = 4;       // target decode items per resident CTA (the most of any kernel)
@@ -151,9 +155,9 @@ struct PlanParams {
     int epoch;           // this call's number, published in ctrl[kPlanEpoch] once the plan is out
     int early;           // the inputs are complete at launch: read them before the grid dependency
     // 4-bit K/V: decode units are tiles of dec_tokens tokens, of any sequence; one with more than direct_tokens tokens becomes
-    // prefill units where the f16 room has pages (of 64 keys) left for it
-    int int4, dec_tokens, direct_tokens;
-    int pf_Hkv;      // kv heads a prefill unit stands for
+    // prefill units where the f16 room has pages (of 64 keys) left for it; one of at most few_tokens, only beside many such
+    int int4, dec_tokens, direct_tokens, few_tokens;
+    int pf_Hkv, pf_G;  // kv heads a prefill unit stands for, and query heads of each
     int room_pages;
     int min_chunk, chunk_align;  // smallest split-KV piece, and what pieces are multiples of (keys)
     int good_chunk;              // pieces are as long as this, if there is so much for every CTA (0: no matter)
@@ -328,7 +332,7 @@ struct KernelSet {
     float qk_log2, cap_exp, cap_log2, v_scale;
     // 4-bit K/V: channels of a group; kv heads of a prefill unit; most tokens of a sequence that the direct kernel takes; the room
     // for f16 rows of longer prompts, in pages of 64 keys, and its page table's columns
-    int group, pf_H, direct_tokens, room_pages, P64;
+    int group, pf_H, direct_tokens, few_tokens, room_pages, P64;
     int sms, dec_bps, pf_bps;
     int max_dec_units, max_pf_units, max_units, max_part, max_comb;
 };

@@ -154,6 +154,7 @@ void kernels_choose(const RpaCfg& c, int sms, KernelSet* ks) {
     }
     if (ks->kt == KT_I4) {
         ks->direct_tokens = kInt4DirectRows / ks->G > ks->Tt ? kInt4DirectRows / ks->G : ks->Tt;
+        ks->few_tokens = kInt4FewRows / ks->G;
         // room for prompts of longer sequences: 2^18 keys of 8 heads at D 128 (1 GiB), the longest sequence at least, all of them at most
         const int64_t page = 64 * 4 * c.num_kv_heads * c.head_dim, most = (c.pages_per_seq * c.page_size + 63) / 64;
         ks->P64 = (int)most;
@@ -449,7 +450,9 @@ int enqueue_forward(const RpaCfg& c, const KernelSet& ks, const Workspace& ws, M
     pp.int4 = ks.kt == KT_I4;
     pp.dec_tokens = ks.Tt;
     pp.direct_tokens = ks.direct_tokens;
+    pp.few_tokens = ks.few_tokens;
     pp.pf_Hkv = ks.pf_H;
+    pp.pf_G = ks.G;
     pp.room_pages = ks.room_pages;
     pp.vbase = ws.vbase;
     pp.chunk_align = pp.int4 ? 32 * int4_warps(ks.D) : kChunkAlign;  // 4-bit K/V: whole stages

@@ -67,13 +67,25 @@ __device__ __forceinline__ bool bad_lengths(int q0, int q1, int kl, const PlanPa
 __device__ void give_room(const PlanParams& p, int* cls, int* scan, int* taken) {
     const int S = p.num_seqs;
     if (threadIdx.x == 0) *taken = 0;
+    __syncthreads();
+    // how many rows a sequence may have for the direct kernel goes by the number of such sequences
+    int few = 0;
+    for (int s = threadIdx.x; s < S; s += blockDim.x) {
+        const int q0 = p.cu_q_lens[s], q1 = p.cu_q_lens[s + 1];
+        few += !bad_lengths(q0, q1, p.kv_lens[s], p) && q1 - q0 > p.direct_tokens && q1 - q0 <= p.few_tokens;
+    }
+    if (few) atomicAdd(taken, few);
+    __syncthreads();
+    const int direct = min(p.few_tokens, (kInt4DirectRows + kInt4RowsByItems / max(1, min(*taken, kInt4RowsByItems) * p.pf_Hkv)) / p.pf_G);
+    __syncthreads();
+    if (threadIdx.x == 0) *taken = 0;
     int carry = 0;
     for (int base = 0; base < S; base += blockDim.x) {
         const int s = base + threadIdx.x;
         int pages = 0;
         if (s < S) {
             const int q0 = p.cu_q_lens[s], q1 = p.cu_q_lens[s + 1], kl = p.kv_lens[s];
-            if (!bad_lengths(q0, q1, kl, p) && q1 - q0 > p.direct_tokens) {
+            if (!bad_lengths(q0, q1, kl, p) && q1 - q0 > direct) {
                 int lo, hi;
                 key_band(kl, q1 - q0, 0, q1 - q0, p, lo, hi);
                 pages = int4_pages(lo, hi, p.first);
