@@ -50,8 +50,9 @@ namespace {
 constexpr int kUnit = 16;       // elements of a unit
 constexpr int kRopeThreads = 256;
 constexpr int kRopeCtas = 5;    // resident an SM
-constexpr int kRopeCtas4 = 4;   // ... that write a 4-bit cache
+constexpr int kRopeCtas4 = 3;   // ... that write a 4-bit cache
 constexpr int kTokens = 16;     // tokens of a CTA's round
+constexpr int kTokens4 = 12;    // ... that writes a 4-bit cache
 constexpr int kSeqs = 512;      // sequences whose cu_q_lens and kv_lens a CTA reads into shared memory
 constexpr int kMaxPairs = 288;  // rotary_dim <= 576
 
@@ -167,25 +168,105 @@ __device__ __forceinline__ float max_nan(float a, float b, float c) {
     return r;
 }
 
-// A row of a 4-bit cache.  The row's D / 16 threads (neighbouring lanes, `mask`) hold its values by the pairs they turn;
-// through `row` (shared, D floats) each takes 16 neighbouring channels, and a group's extremes come by shuffles.
-// Differences and quotients are rounded towards the side that the scale and the zero are rounded to, so that no two roundings
-// of one value can meet; codes come from the exact quotient's nearest.
-__device__ __forceinline__ void store_int4(const RopeParams& p, const float* y, int e0, int e1, float* row, int place, uint32_t mask,
-                                           long long slot, int h, bool is_v) {
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        reinterpret_cast<float4*>(row + e0)[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-        reinterpret_cast<float4*>(row + e1)[i] = make_float4(y[8 + 4 * i], y[9 + 4 * i], y[10 + 4 * i], y[11 + 4 * i]);
+// The neighbour of a float16 value, below or above it
+__device__ __forceinline__ __half next_half(__half x, bool up) {
+    const unsigned short b = __half_as_ushort(x);
+    if ((b & 0x7fff) == 0) return __ushort_as_half(up ? 0x0001 : 0x8001);
+    return __ushort_as_half((unsigned short)(((b & 0x8000) != 0) == up ? b - 1 : b + 1));
+}
+
+// A pair of floats is their sum: `lo` holds what rounding `hi` left.  a + b as such a pair (any a, b; or |a| >= |b|).  (The intrinsics
+// are not contracted: a product that a sum's rounding is measured against has to be rounded itself.)
+__device__ __forceinline__ void two_sum(float a, float b, float& hi, float& lo) {
+    const float h = __fadd_rn(a, b), c = __fsub_rn(h, a);
+    lo = __fadd_rn(__fsub_rn(a, __fsub_rn(h, c)), __fsub_rn(b, c));
+    hi = h;
+}
+__device__ __forceinline__ void quick_sum(float a, float b, float& hi, float& lo) {
+    const float h = __fadd_rn(a, b);
+    lo = __fsub_rn(b, __fsub_rn(h, a));
+    hi = h;
+}
+
+// Cosine and sine of a fraction of a turn (in units of 2^-64) as pairs, off by 2^-30 at most: the Taylor series about the nearest
+// quarter turn, their leading terms in pairs (the rest is below 2.6e-3, and 32 bits of it are enough).
+__device__ __forceinline__ void sincos_pairs(unsigned long long turn, float2& cs, float2& sn) {
+    const unsigned long long quarter = (turn + (1ull << 61)) >> 62;
+    const long long r = (long long)(turn - (quarter << 62));  // up to an eighth of a turn
+    const float fh = (float)(int)(r >> 32), fl = (float)(r - ((long long)(int)fh << 32));
+    const float th = fh * 2.3283064365386963e-10f, tl = fl * 5.421010862427522e-20f;  // 2^-32, 2^-64
+    constexpr float kPi = 6.2831854820251465f, kPiLo = -1.7484555314695172e-07f;      // 2 pi
+    float xh = __fmul_rn(th, kPi), xl = fmaf(th, kPi, -xh) + (th * kPiLo + tl * kPi);
+    quick_sum(xh, xl, xh, xl);
+    const float sh = __fmul_rn(xh, xh), sl = fmaf(xh, xh, -sh) + 2.f * xh * xl;  // x^2
+    // sine: x - x^3 / 6 + x^5 (1 / 120 - ...)
+    {
+        constexpr float kSixth = 0.1666666716337204f, kSixthLo = -4.967053879312289e-09f;
+        const float ch = __fmul_rn(sh, xh), cl = fmaf(sh, xh, -ch) + (sh * xl + sl * xh);
+        const float vh = __fmul_rn(ch, kSixth), vl = fmaf(ch, kSixth, -vh) + (ch * kSixthLo + cl * kSixth);
+        const float rest = ch * sh * fmaf(sh, fmaf(sh, fmaf(sh, -2.50521084e-08f, 2.75573192e-06f), -1.98412698e-04f), 8.33333333e-03f);
+        float h, l;
+        quick_sum(xh, -vh, h, l);
+        quick_sum(h, l + (rest + (xl - vl)), sn.x, sn.y);
     }
-    __syncwarp(mask);
-    float x[16];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float4 v = reinterpret_cast<const float4*>(row + 16 * place)[i];
-        x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
+    // cosine: 1 - x^2 / 2 + x^4 / 24 - x^6 (1 / 720 - ...)
+    {
+        constexpr float k24 = 0.0416666679084301f, k24Lo = -1.2417634698280722e-09f;
+        const float qh = __fmul_rn(sh, sh), ql = fmaf(sh, sh, -qh) + 2.f * sh * sl;
+        const float gh = __fmul_rn(qh, k24), gl = fmaf(qh, k24, -gh) + (qh * k24Lo + ql * k24);
+        const float rest = qh * sh * fmaf(sh, fmaf(sh, -2.75573192e-07f, 2.48015873e-05f), -1.38888889e-03f);
+        float h, l, h2, l2;
+        quick_sum(1.f, -0.5f * sh, h, l);
+        quick_sum(h, gh, h2, l2);
+        quick_sum(h2, (l2 + l) + (rest + (gl - 0.5f * sl)), cs.x, cs.y);
     }
-    __syncwarp(mask);  // the buffer is free again
+    if (quarter & 1) {
+        const float2 c = cs;
+        cs = make_float2(-sn.x, -sn.y);
+        sn = c;
+    }
+    if (quarter & 2) {
+        cs = make_float2(-cs.x, -cs.y);
+        sn = make_float2(-sn.x, -sn.y);
+    }
+}
+// u c - w s of pairs c, s, as a pair
+__device__ __forceinline__ void turn_pair(float u, float w, float ch, float cl, float sh, float sl, float& hi, float& lo) {
+    const float p = __fmul_rn(u, ch), q = __fmul_rn(w, sh);
+    float h, l;
+    two_sum(p, -q, h, l);
+    l += (fmaf(u, ch, -p) - fmaf(w, sh, -q)) + (u * cl - w * sl);
+    quick_sum(h, fabsf(h) < INFINITY ? l : 0.f, hi, lo);
+}
+
+// A row of a 4-bit cache.  The row's D / 16 threads (neighbouring lanes, `mask`) hold its values by the pairs they turn, as sums
+// y + yl; through `row` (shared, D floats) each takes 16 neighbouring channels, and a group's extremes come by shuffles.
+// A group's zero and scale are rounded to one side, and its codes to the nearest: each step from the exact values of the sums, so
+// that what 32 bits round away decides no code, and a group's codes do not hang on how its angles' sines were rounded.
+__device__ __forceinline__ void store_int4(const RopeParams& p, const float* y, const float* yl, int e0, int e1, float* row, int place,
+                                           uint32_t mask, long long slot, int h, bool is_v) {
+    auto exchange = [&](const float* from, float* to) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            reinterpret_cast<float4*>(row + e0)[i] = make_float4(from[4 * i], from[4 * i + 1], from[4 * i + 2], from[4 * i + 3]);
+            reinterpret_cast<float4*>(row + e1)[i] = make_float4(from[8 + 4 * i], from[9 + 4 * i], from[10 + 4 * i], from[11 + 4 * i]);
+        }
+        __syncwarp(mask);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float4 v = reinterpret_cast<const float4*>(row + 16 * place)[i];
+            to[4 * i] = v.x; to[4 * i + 1] = v.y; to[4 * i + 2] = v.z; to[4 * i + 3] = v.w;
+        }
+        __syncwarp(mask);  // the buffer is free again
+    };
+    float x[16], xl[16];
+    exchange(y, x);
+    if (!is_v) {
+        exchange(yl, xl);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) xl[i] = 0.f;
+    }
     float lo = x[0], hi = x[0];
 #pragma unroll
     for (int i = 1; i < 16; i += 2) {
@@ -199,13 +280,39 @@ __device__ __forceinline__ void store_int4(const RopeParams& p, const float* y, 
     }
     if (lo < -65504.f || hi > 65504.f) {  // (all of a group's threads)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) x[i] = fminf(fmaxf(x[i], -65504.f), 65504.f);
+        for (int i = 0; i < 16; ++i) {
+            if (fabsf(x[i]) >= 65504.f) xl[i] = 0.f;
+            x[i] = fminf(fmaxf(x[i], -65504.f), 65504.f);
+        }
         lo = fminf(fmaxf(lo, -65504.f), 65504.f);
         hi = fminf(fmaxf(hi, -65504.f), 65504.f);
     }
-    const __half zero = __float2half_rd(lo);
+    float lol = 0.f, hil = 0.f;  // what the extremes' own rounding left
+    if (!is_v) {
+        lol = INFINITY;
+        hil = -INFINITY;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            lol = x[i] == lo ? fminf(lol, xl[i]) : lol;
+            hil = x[i] == hi ? fmaxf(hil, xl[i]) : hil;
+        }
+        for (int o = 1; o < p.group / 16; o <<= 1) {
+            lol = fminf(lol, __shfl_xor_sync(mask, lol, o));
+            hil = fmaxf(hil, __shfl_xor_sync(mask, hil, o));
+        }
+    }
+    __half zero = __float2half_rd(lo);
+    if (__half2float(zero) == lo && lol < 0.f && lo > -65504.f) zero = next_half(zero, false);
     const float z = __half2float(zero);
-    const __half scale = __float2half_ru(__fdiv_ru(__fsub_ru(hi, z), 15.f));
+    float dh, dl;
+    two_sum(hi, -z, dh, dl);
+    dl += hil;
+    __half scale = __float2half_ru(__fdiv_rn(dh, 15.f));
+    {
+        const float c = 15.f * __half2float(scale), b = 15.f * __half2float(next_half(scale, false));  // (exact)
+        if (c < dh || (c == dh && dl > 0.f)) scale = next_half(scale, true);
+        else if (b >= 0.f && (b > dh || (b == dh && dl <= 0.f))) scale = next_half(scale, false);
+    }
     const float s = __half2float(scale), inv = __frcp_rn(s);
     // The quotient's nearest integer, to even: of x (1 / s), off by less than 2^-17 for codes up to 15, unless one of the
     // thread's lies so near the middle of two that only the exact remainder says which.  (1.5 2^23 leaves a sum's integer in its low
@@ -231,11 +338,15 @@ __device__ __forceinline__ void store_int4(const RopeParams& p, const float* y, 
         w[0] = w[1] = 0;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            // what the rounded product leaves of the difference, exactly, against half a step
-            const float d = x[i] - z, r = rintf(d * inv), e = fmaf(-r, s, d), h2 = 0.5f * s;
+            // what r steps leave of the difference, exactly, against half a step
+            float d, e;
+            two_sum(x[i], -z, d, e);
+            e += xl[i];
+            const float r = rintf(d * inv), left = fmaf(-r, s, d), up = (left - 0.5f * s) + e, down = (left + 0.5f * s) + e;
             int c = r == r ? (int)r : 0;
-            if (e > h2 || (e == h2 && (c & 1))) ++c;
-            if (e < -h2 || (e == -h2 && (c & 1))) --c;
+            const bool odd = c & 1;
+            if (up > 0.f || (up == 0.f && odd)) ++c;
+            if (down < 0.f || (down == 0.f && odd)) --c;
             w[i / 8] |= (uint32_t)min(max(c, 0), 15) << (4 * (i % 8));
         }
     }
@@ -250,13 +361,14 @@ __device__ __forceinline__ void store_int4(const RopeParams& p, const float* y, 
 
 template <typename QT, bool HALF, bool INT4>
 __global__ void __launch_bounds__(kRopeThreads, INT4 ? kRopeCtas4 : kRopeCtas) rpa_rope_kernel(const RopeParams p) {
-    constexpr int kBatch = sizeof(QT) == 4 ? 1 : 2;  // rows whose loads a thread has in flight
+    constexpr int kBatch = sizeof(QT) == 4 || INT4 ? 1 : 2;  // rows whose loads a thread has in flight (INT4: beside the one at work)
+    constexpr int kRound = INT4 ? kTokens4 : kTokens;
     // [tokens][4][places] pairs of (cos, sin): place's pairs 2 i and 2 i + 1 at [i][place], so that neighbouring
     // places read neighbouring 16 bytes
     extern __shared__ float4 s_cs[];
-    __shared__ long long s_slot[kTokens];  // cache slot of a token (page * page_size + place; INT4: page, place), or -1
+    __shared__ long long s_slot[kRound];  // cache slot of a token (page * page_size + place; INT4: page, place), or -1
     __shared__ __align__(16) float s_rows[INT4 ? kRopeThreads * kUnit : 4];  // INT4: the rows that are being coded
-    __shared__ int s_pos[kTokens], s_live[kTokens];
+    __shared__ int s_pos[kRound], s_live[kRound];
     __shared__ int s_cu[kSeqs + 1], s_kl[kSeqs];
     __shared__ unsigned long long s_turns[kMaxPairs];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
@@ -307,8 +419,8 @@ __global__ void __launch_bounds__(kRopeThreads, INT4 ? kRopeCtas4 : kRopeCtas) r
         }
         if (tid == 0) s_cu[p.S] = p.cu[p.S];
     }
-    for (; t0 < t_end; t0 += kTokens) {
-        const int n = min(kTokens, t_end - t0);
+    for (; t0 < t_end; t0 += kRound) {
+        const int n = min(kRound, t_end - t0);
         Vec8<QT> x0[kBatch], x1[kBatch];
         // rows from (token `tk` of the round, row r) on, row_step apart, through the tokens
         auto next = [&](int& tk, int& r) {
@@ -357,62 +469,111 @@ __global__ void __launch_bounds__(kRopeThreads, INT4 ? kRopeCtas4 : kRopeCtas) r
             const int k = i / (p.rd / 2), pair = i - k * (p.rd / 2);
             // the angle's fraction of a turn, its upper 32 bits as half turns in [-1, 1)
             const unsigned long long f = s_turns[pair] * (unsigned long long)(long long)s_pos[k];
-            float sn, cs;
-            sincospif((float)(int)((f + 0x80000000ull) >> 32) * 4.656612873077393e-10f, &sn, &cs);
-            cs2[((k * 4 + (pair & 7) / 2) * places + pair / 8) * 2 + (pair & 1)] = make_float2(cs * p.magnitude, sn * p.magnitude);
+            const int at = ((k * 4 + (pair & 7) / 2) * places + pair / 8) * 2 + (pair & 1);
+            if constexpr (INT4) {
+                // pairs, their low halves in a second table: the keys' codes want them
+                float2 c, s;
+                sincos_pairs(f, c, s);
+                const float m = p.magnitude, ch = __fmul_rn(c.x, m), sh = __fmul_rn(s.x, m);
+                cs2[at] = make_float2(ch, sh);
+                cs2[kRound * 8 * places + at] = make_float2(fmaf(c.x, m, -ch) + c.y * m, fmaf(s.x, m, -sh) + s.y * m);
+            } else {
+                float sn, cs;
+                sincospif((float)(int)((f + 0x80000000ull) >> 32) * 4.656612873077393e-10f, &sn, &cs);
+                cs2[at] = make_float2(cs * p.magnitude, sn * p.magnitude);
+            }
         }
         __syncthreads();
-        while (tk < n) {
-            int tb = tk, rb = r;
-#pragma unroll
-            for (int b = 0; b < kBatch; ++b) {
-                if (tb < n && s_live[tb]) {
-                    float y[16];
-                    widen(x0[b], y);
-                    widen(x1[b], y + 8);
-                    if (rot && rb < p.Hq + p.Hkv) {
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float4 cs = s_cs[(tb * 4 + i) * places + place];  // cos, sin of pairs 2 i and 2 i + 1
-#pragma unroll
-                            for (int j = 0; j < 2; ++j) {
-                                const int m = 2 * i + j, a = HALF ? m : 2 * m, c = HALF ? m + 8 : 2 * m + 1;
-                                const float co = j ? cs.z : cs.x, si = j ? cs.w : cs.y, u = y[a], w = y[c];
-                                y[a] = u * co - w * si;
-                                y[c] = w * co + u * si;
-                            }
-                        }
-                    }
-                    if (rb < p.Hq) {
-                        QT* o = reinterpret_cast<QT*>(p.q_out) + ((size_t)(t0 + tb) * p.Hq + rb) * p.D;
-                        store_q8(o + e0, y);
-                        store_q8(o + e1, y + 8);
-                    } else if (s_slot[tb] >= 0) {
-                        const bool is_v = rb >= p.Hq + p.Hkv;
-                        const int h = rb - p.Hq - (is_v ? p.Hkv : 0);
-                        if (is_v ? p.has_vs : p.has_ks) {
-                            const float sc = is_v ? p.v_scale : p.k_scale;
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) y[i] = __fdiv_rn(y[i], sc);
-                        }
-                        if constexpr (INT4) {
-                            const uint32_t mask = ((1u << p.per_row) - 1u) << (lane - place % 32);
-                            store_int4(p, y, e0, e1, s_rows + (size_t)(tid - place) * kUnit, place, mask, s_slot[tb], h, is_v);
-                            next(tb, rb);
-                            continue;
-                        }
-                        const int rows = p.latent ? p.Hkv : 2 * p.Hkv;
-                        const size_t row = ((size_t)s_slot[tb] * rows + (p.latent ? h : 2 * h + (is_v ? 1 : 0))) * p.D *
-                                           (kt_8bit(p.kt) ? 1 : 2);
-                        store_kv8(p.kv, row, e0, y, p.kt);
-                        store_kv8(p.kv, row, e1, y + 8, p.kt);
-                    }
-                }
-                next(tb, rb);
+        // one row of a token
+        auto process = [&](int tb, int rb, const Vec8<QT>& v0, const Vec8<QT>& v1) {
+            if (!s_live[tb]) return;
+                                float y[16];
+                                widen(v0, y);
+                                widen(v1, y + 8);
+                                float yl[INT4 ? 16 : 1];
+                                if constexpr (INT4) {
+                                    if (rb >= p.Hq) {
+            #pragma unroll
+                                        for (int i = 0; i < 16; ++i) yl[i] = 0.f;
+                                    }
+                                    if (rot && rb >= p.Hq && rb < p.Hq + p.Hkv) {
+            #pragma unroll
+                                        for (int i = 0; i < 4; ++i) {
+                                            const float4 cs = s_cs[(tb * 4 + i) * places + place], cl = s_cs[(kRound * 4 + tb * 4 + i) * places + place];
+            #pragma unroll
+                                            for (int j = 0; j < 2; ++j) {
+                                                const int m = 2 * i + j, a = HALF ? m : 2 * m, c = HALF ? m + 8 : 2 * m + 1;
+                                                const float co = j ? cs.z : cs.x, si = j ? cs.w : cs.y, col = j ? cl.z : cl.x, sil = j ? cl.w : cl.y;
+                                                const float u = y[a], w = y[c];
+                                                turn_pair(u, w, co, col, si, sil, y[a], yl[a]);
+                                                turn_pair(w, -u, co, col, si, sil, y[c], yl[c]);
+                                            }
+                                        }
+                                    }
+                                }
+                                if (rot && rb < p.Hq + (INT4 ? 0 : p.Hkv)) {
+            #pragma unroll
+                                    for (int i = 0; i < 4; ++i) {
+                                        const float4 cs = s_cs[(tb * 4 + i) * places + place];  // cos, sin of pairs 2 i and 2 i + 1
+            #pragma unroll
+                                        for (int j = 0; j < 2; ++j) {
+                                            const int m = 2 * i + j, a = HALF ? m : 2 * m, c = HALF ? m + 8 : 2 * m + 1;
+                                            const float co = j ? cs.z : cs.x, si = j ? cs.w : cs.y, u = y[a], w = y[c];
+                                            y[a] = u * co - w * si;
+                                            y[c] = w * co + u * si;
+                                        }
+                                    }
+                                }
+                                if (rb < p.Hq) {
+                                    QT* o = reinterpret_cast<QT*>(p.q_out) + ((size_t)(t0 + tb) * p.Hq + rb) * p.D;
+                                    store_q8(o + e0, y);
+                                    store_q8(o + e1, y + 8);
+                                } else if (s_slot[tb] >= 0) {
+                                    const bool is_v = rb >= p.Hq + p.Hkv;
+                                    const int h = rb - p.Hq - (is_v ? p.Hkv : 0);
+                                    if (is_v ? p.has_vs : p.has_ks) {
+                                        const float sc = is_v ? p.v_scale : p.k_scale;
+            #pragma unroll
+                                        for (int i = 0; i < 16; ++i) y[i] = __fdiv_rn(y[i], sc);
+                                        if constexpr (INT4) {
+            #pragma unroll
+                                            for (int i = 0; i < 16; ++i) yl[i] = 0.f;
+                                        }
+                                    }
+                                    if constexpr (INT4) {
+                                        const uint32_t mask = ((1u << p.per_row) - 1u) << (lane - place % 32);
+                                        store_int4(p, y, yl, e0, e1, s_rows + (size_t)(tid - place) * kUnit, place, mask, s_slot[tb], h, is_v);
+                                        return;
+                                    }
+                                    const int rows = p.latent ? p.Hkv : 2 * p.Hkv;
+                                    const size_t row = ((size_t)s_slot[tb] * rows + (p.latent ? h : 2 * h + (is_v ? 1 : 0))) * p.D *
+                                                       (kt_8bit(p.kt) ? 1 : 2);
+                                    store_kv8(p.kv, row, e0, y, p.kt);
+                                    store_kv8(p.kv, row, e1, y + 8, p.kt);
+                                }
+        };
+        if constexpr (INT4) {
+            // (one copy of the code that makes codes: two are more than the instruction cache takes)
+#pragma unroll 1
+            while (tk < n) {
+                const Vec8<QT> v0 = x0[0], v1 = x1[0];
+                const int tb = tk, rb = r;
+                next(tk, r);
+                if (tk < n) fetch(tk, r);
+                process(tb, rb, v0, v1);
             }
-            tk = tb;
-            r = rb;
-            if (tk < n) fetch(tk, r);
+        } else {
+            while (tk < n) {
+                int tb = tk, rb = r;
+#pragma unroll
+                for (int b = 0; b < kBatch; ++b) {
+                    if (tb < n) process(tb, rb, x0[b], x1[b]);
+                    next(tb, rb);
+                }
+                tk = tb;
+                r = rb;
+                if (tk < n) fetch(tk, r);
+            }
         }
         __syncthreads();  // the round's tables are free again
     }
@@ -428,7 +589,8 @@ __global__ void __launch_bounds__(kRopeThreads, INT4 ? kRopeCtas4 : kRopeCtas) r
 
 template <typename QT>
 cudaError_t launch_rope(const RopeParams& p, int half, int grid, int threads, cudaStream_t st) {
-    const size_t smem = (size_t)kTokens * (p.rd / 2) * sizeof(float2);  // at most 36 KB
+    // at most 36 KB (4-bit: 12 tokens, two tables, rotary_dim <= 256: 24 KB)
+    const size_t smem = (size_t)(p.kt == KT_I4 ? 2 * kTokens4 : kTokens) * (p.rd / 2) * sizeof(float2);
     if (p.kt == KT_I4)
         return half ? launch_pdl(rpa_rope_kernel<QT, true, true>, grid, threads, smem, st, p)
                     : launch_pdl(rpa_rope_kernel<QT, false, true>, grid, threads, smem, st, p);
