@@ -65,6 +65,7 @@ typedef enum RpaDtype {
  *   V codes        alike
  *   K scale, zero  [page_size][D / group] pairs of f16
  *   V scale, zero  alike
+ * (page_size a multiple of 4 as ever, and at most 65536)
  * and a channel's value is  code * scale + zero  of its group (times k_scale or v_scale).  rpa_rope_append writes
  * it, rpa_rope_read reads its rows as values, rpa_forward attends over it. */
 

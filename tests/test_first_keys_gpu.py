@@ -151,3 +151,34 @@ def test_host_no_alloc_and_graph():
     outs = [check(b, 100, 20, q=q, cache=cache, call=c) for c in (None, host, no_alloc, graph)]
     for o in outs[1:]:
         assert torch.equal(o, outs[0])
+
+
+@pytest.mark.parametrize("kv,D", [("bf16", 128), ("fp8_e4m3", 64), ("bf16", 256), ("int4_g64", 128), ("int4_g128", 256)])
+@pytest.mark.parametrize("window,first", [(700, 4), (3000, 900), (5000, 64), (64, 0)])
+def test_the_plan_covers_what_is_seen(kv, D, window, first):
+    """Every (sequence, kv head, token, key) that is seen lies in one item, and items keep to the band and the first keys."""
+    eight = EIGHT if kv == "fp8_e4m3" else {}
+    b = Batch(np.random.default_rng(window + first), [1, 1, 120, 3, 700], [9000, 100, 2000, 6000, 900], 16, 8, 2, D, kv=kv, **eight)
+    q = torch.zeros((b.T, 8, D), dtype=torch.bfloat16, device="cuda")
+    cfg = dict(b.cfg(), sliding_window=window, first_keys=first)
+    att = rpa.RaggedPagedAttention(**cfg)
+    from ragged_paged_attention_02_gb300.binding import cache_shape
+
+    cache = torch.zeros(cache_shape(att._c), dtype=torch.bfloat16 if kv == "bf16" else torch.uint8, device="cuda")
+    att.forward(q, cache, *b.lens(), b.S)
+    assert att.status() == rpa.RPA_OK
+    info, items = att.plan()
+    count = [[np.zeros((a, n), int) for a, n in zip(b.q_lens, b.kv_lens_list)] for _ in range(2)]
+    for s, head, t0, nt, lo, hi, part, piece in items:
+        n, a = b.kv_lens_list[s], b.q_lens[s]
+        p_lo = n - a + t0
+        assert 0 <= lo <= hi <= n
+        count[head][s][t0:t0 + nt, lo:hi] += 1
+        if first and piece == 0 and lo > first:
+            count[head][s][t0:t0 + nt, :first] += 1
+            assert p_lo - window + 1 > first or lo > first
+    for head in range(2):
+        for s, (a, n) in enumerate(zip(b.q_lens, b.kv_lens_list)):
+            pos, j = np.arange(n - a, n)[:, None], np.arange(n)[None]
+            sees = (j <= pos) & ((j > pos - window) | (j < first))
+            assert (count[head][s][sees] == 1).all()

@@ -91,6 +91,30 @@ def test_append(D, group, ps, Hq, Hkv, q, rope, scales):
     assert raw and (out[:2] == 9).all() and (out[cu[b.S]:] == 9).all()
 
 
+def test_positions_and_unaligned_fractions():
+    """Positions far out, given apart from the slots: the codes are those of the exact angles (a rotation in 64 bits)."""
+    b = Batch(np.random.default_rng(11), [1, 33], [40, 100], 16, 4, 2, 128, kv="int4_g64", q="bf16")
+    qs, k, v = new_rows(b)
+    pos = b.rng.integers(0, 2 ** 31, b.T).astype(np.int32)
+    lens, table, cu = b.lens()
+    cache = blank(b, 64)
+    op = rpa.RopeAppend(**b.cfg(), base=500000.0)
+    op.append(qs, k, v, cache, lens, table, cu, b.S, positions=torch.from_numpy(pos).cuda())
+    assert op.status() == rpa.RPA_OK
+    t, page, at, _ = slots_of(b)
+    # 80-bit angles: 2^31 positions times a double frequency lose 2^-22 of a radian in 64 bits
+    w = np.asarray(rpa.rope_frequencies(**b.cfg(), base=500000.0)).astype(np.longdouble)
+    turn = (pos[t].astype(np.longdouble)[:, None] * w / (2 * np.longdouble("3.14159265358979323846264338327950288"))) % 1
+    ang = (2 * np.pi * turn.astype(np.float64))[:, None]
+    x = f64(k)[t]
+    y = np.concatenate((x[..., :64] * np.cos(ang) - x[..., 64:] * np.sin(ang), x[..., 64:] * np.cos(ang) + x[..., :64] * np.sin(ang)), -1)
+    codes, s, z = (c[page, at] for c in i4.unpack(cache.cpu().numpy(), 16, 128, 64)[0])
+    # off by 2^-29 of a pair's size (the sines' 2^-30, their products'), beside the last bits of the 64-bit angle
+    e = 2.0 ** -29 * 2 * np.abs(x).max() + 1e-9
+    assert (np.abs(codes * np.repeat(s, 64, -1) + np.repeat(z, 64, -1) - y) <= np.repeat(s, 64, -1) * 0.5 + e).all()
+    assert (z <= y.reshape(*y.shape[:-1], -1, 64).min(-1) + e).all()
+
+
 def test_groups_without_a_range_and_odd_values():
     """Equal values, zeros, subnormals, values past float16, infinities and NaN, a group each."""
     b = Batch(np.random.default_rng(0), [6], [6], 16, 1, 1, 128, kv="int4_g32", q="f32")
@@ -185,6 +209,27 @@ def test_bad_pages_and_lengths():
         got, had = i4.unpack(mine.cpu().numpy(), 16, 64, 32), i4.unpack(cache.cpu().numpy(), 16, 64, 32)
         assert all(np.array_equal(x[page, at], y[page, at]) for p, r in zip(got, had) for x, y in zip(p, r))
     assert op.status() == rpa.RPA_OK
+
+
+def test_key_rows_with_infinities_and_nan():
+    """K's rows are rotated before they are coded: an infinity saturates its pair, a NaN takes its pair's groups."""
+    b = Batch(np.random.default_rng(12), [3], [3], 16, 1, 1, 64, kv="int4_g32", q="f16")
+    k = torch.zeros(3, 1, 64, dtype=torch.float16, device="cuda")
+    k[0, 0, 40] = float("inf")    # not rotated
+    k[1, 0, 50] = float("nan")
+    k[2, 0, 3] = float("inf")     # rotated with channel 11
+    lens, table, cu = b.lens()
+    cache = blank(b, 32)
+    op = rpa.RopeAppend(**b.cfg(), rotary_dim=16)
+    op.append(torch.zeros_like(k), k, torch.zeros_like(k), cache, lens, table, cu, 1)
+    assert op.status() == rpa.RPA_OK
+    page, at = b.slots(0, np.arange(3))
+    part = tuple(c[page, at, 0] for c in i4.unpack(cache.cpu().numpy(), 16, 64, 32)[0])
+    got = i4.values(part, 32)
+    assert got[0, 40] >= 65504 and np.isfinite(got[0]).all() and (got[0, :32] == 0).all()
+    assert np.isnan(got[1, 32:]).all() and (got[1, :32] == 0).all()
+    # position 2: cos(2 w) and sin(2 w) of pair 3 are positive, so both of its channels are infinite
+    assert (got[2, [3, 11]] >= 65504).all() and np.isfinite(got[2]).all()
 
 
 def test_many_sequences_and_refusals():

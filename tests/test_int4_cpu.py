@@ -20,6 +20,10 @@ def _built():
     (dict(kv_dtype="int4_g32"), rpa.RPA_OK),
     (dict(kv_dtype="int4_g64", page_size=20), rpa.RPA_OK),
     (dict(kv_dtype="int4_g64", page_size=6), rpa.RPA_ERR_UNSUPPORTED),
+    (dict(kv_dtype="int4_g64", page_size=65536), rpa.RPA_OK),
+    (dict(kv_dtype="int4_g64", page_size=65540), rpa.RPA_ERR_UNSUPPORTED),
+    (dict(kv_dtype="int4_g64", num_q_heads=130, num_kv_heads=2), rpa.RPA_ERR_UNSUPPORTED),
+    (dict(kv_dtype="int4_g64", sliding_window=4, first_keys=3), rpa.RPA_OK),
     (dict(kv_dtype="int4_g128"), rpa.RPA_ERR_UNSUPPORTED),  # wider than the head
     (dict(kv_dtype="int4_g128", head_dim=128), rpa.RPA_OK),
     (dict(kv_dtype="int4_g128", head_dim=256, q_dtype="f16"), rpa.RPA_OK),
