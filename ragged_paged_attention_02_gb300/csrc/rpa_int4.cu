@@ -326,12 +326,12 @@ __global__ void __launch_bounds__((I4Geom<D, NG>::THREADS), (I4Geom<D, NG>::CTAS
     uint32_t ph = 0, mph = 0, qph = 0;
     uint32_t qf[C][4];
     float qs[2][NG];          // sums of q over a group, times 2^-20
-    float o_acc[C][2][4];     // [.][i][0, 1]: channel 32 c + 4 g + 2 i, rows 2t, 2t + 1, times 2^-24; [2, 3]: the next channel, times 2^-20
+    float o_acc[C][2][4];     // [.][i][0, 1]: channel 32 c + 4 g + 2 i, rows 2t, 2t + 1, times 2^-24; [2, 3]: and 16 times the next channel
     float psum[NG][4];        // sums of P (rows 2t, 2t + 1, twice)
     float zs[2][NG];          // sums of p (z + 8 s) over this thread's keys
     float m_r[2], l_r[2];
     int pos[2];
-    constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u;
+    constexpr uint32_t kLow = 0x000f000fu, kHigh = 0x00f000f0u, kByte = 0x00ff00ffu;
     // Within a stage: this lane's row of codes for the matrix loads (of the first 16 keys), the (scale, zero) pairs of key g,
     // and how far on those of the next 16 keys, and of key g + 8, lie; the place of the row's chunk 0 (of matrices 2, 3: 1)
     const uint32_t row0 = (uint32_t)(((32 * w + (lane & 15)) >> brs) * RB + ((32 * w + (lane & 15)) & (BR - 1)) * (D / 2));
@@ -575,9 +575,10 @@ __global__ void __launch_bounds__((I4Geom<D, NG>::THREADS), (I4Geom<D, NG>::CTAS
                             const uint32_t ones[4] = {one, one, one, one};
                             mma(psum[gi], ones, pb[0], pb[1]);
                         }
-                        const uint32_t u0 = f[2 * h], u1 = f[2 * h + 1], v0 = u0 >> 8, v1 = u1 >> 8;
-                        const uint32_t a0[4] = {u0 & kLow, u0 & kHigh, u1 & kLow, u1 & kHigh};
-                        const uint32_t a1[4] = {v0 & kLow, v0 & kHigh, v1 & kLow, v1 & kHigh};
+                        const uint32_t u0 = f[2 * h] & kByte, u1 = f[2 * h + 1] & kByte;
+                        const uint32_t v0 = __byte_perm(f[2 * h], 0u, 0x4341), v1 = __byte_perm(f[2 * h + 1], 0u, 0x4341);
+                        const uint32_t a0[4] = {u0 & kLow, u0, u1 & kLow, u1};
+                        const uint32_t a1[4] = {v0 & kLow, v0, v1 & kLow, v1};
                         mma(o_acc[cc][0], a0, pb[0], pb[1]);
                         mma(o_acc[cc][1], a1, pb[0], pb[1]);
                     }
@@ -624,8 +625,8 @@ __global__ void __launch_bounds__((I4Geom<D, NG>::THREADS), (I4Geom<D, NG>::CTAS
 #pragma unroll
             for (int c = 0; c < C; ++c)
                 *reinterpret_cast<float4*>(out + 32 * c) =
-                    make_float4(fmaf(o_acc[c][0][ri], 16777216.f, add[c / CPG]), fmaf(o_acc[c][0][ri + 2], 1048576.f, add[c / CPG]),
-                                fmaf(o_acc[c][1][ri], 16777216.f, add[c / CPG]), fmaf(o_acc[c][1][ri + 2], 1048576.f, add[c / CPG]));
+                    make_float4(fmaf(o_acc[c][0][ri], 16777216.f, add[c / CPG]), fmaf(o_acc[c][0][ri + 2] - o_acc[c][0][ri], 1048576.f, add[c / CPG]),
+                                fmaf(o_acc[c][1][ri], 16777216.f, add[c / CPG]), fmaf(o_acc[c][1][ri + 2] - o_acc[c][1][ri], 1048576.f, add[c / CPG]));
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(mb);  // B: every partial is in shared memory
