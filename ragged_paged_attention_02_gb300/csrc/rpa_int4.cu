@@ -820,28 +820,8 @@ int enqueue_int4(const RpaCfg& c, const KernelSet& ks, const Workspace& ws, MapC
     cudaStream_t st = eo.st;
     auto rec = [&](int k) { return !eo.ev[k] || cudaEventRecord(eo.ev[k], st) == cudaSuccess; };
     const bool has_q = c.num_q_tokens > 0;
-    if (!rec(kEvDecStart)) return RPA_ERR_CUDA;
-    if (has_q) {
-        I4Params p;
-        p.a = a;
-        p.a.units = ws.dec_units;
-        p.a.item_count_word = kNumDecItems;
-        p.a.counter_word = kDecCounter;
-        p.heads = ks.G;
-        p.blocks = ks.Hp / (int)c.num_kv_heads;
-        p.BR = int4_warps(ks.D) % 4 ? 32 : 128;  // runs divide a stage, of 32 keys a warp
-        while (c.page_size % p.BR) p.BR >>= 1;
-        p.brs = 0;
-        while ((1 << p.brs) < p.BR) ++p.brs;
-        p.block = (uint32_t)(c.page_size * int4_key_bytes(ks.D, ks.group));
-        p.page.set((uint32_t)c.page_size);
-        p.stall = eo.debug_stall;
-        p.timeout_ns = eo.timeout_ns;
-        if (i4_dispatch(ks.D, ks.group, [&](auto k) { return decltype(k)::launch(p, Launch{ks.sms * ks.dec_bps, st}); }) !=
-            cudaSuccess)
-            return RPA_ERR_CUDA;
-    }
-    if (!rec(kEvDecEnd) || !rec(kEvPfStart)) return RPA_ERR_CUDA;
+    // (prompts first: where there are none, these two end while the direct kernel is being launched, not after it)
+    if (!rec(kEvPfStart)) return RPA_ERR_CUDA;
     if (has_q && ks.room_pages > 0) {
         UnfoldParams u;
         u.kv = a.kv;
@@ -905,7 +885,28 @@ int enqueue_int4(const RpaCfg& c, const KernelSet& ks, const Workspace& ws, MapC
             cudaSuccess)
             return RPA_ERR_CUDA;
     }
-    return rec(kEvPfEnd) ? RPA_OK : RPA_ERR_CUDA;
+    if (!rec(kEvPfEnd) || !rec(kEvDecStart)) return RPA_ERR_CUDA;
+    if (has_q) {
+        I4Params p;
+        p.a = a;
+        p.a.units = ws.dec_units;
+        p.a.item_count_word = kNumDecItems;
+        p.a.counter_word = kDecCounter;
+        p.heads = ks.G;
+        p.blocks = ks.Hp / (int)c.num_kv_heads;
+        p.BR = int4_warps(ks.D) % 4 ? 32 : 128;  // runs divide a stage, of 32 keys a warp
+        while (c.page_size % p.BR) p.BR >>= 1;
+        p.brs = 0;
+        while ((1 << p.brs) < p.BR) ++p.brs;
+        p.block = (uint32_t)(c.page_size * int4_key_bytes(ks.D, ks.group));
+        p.page.set((uint32_t)c.page_size);
+        p.stall = eo.debug_stall;
+        p.timeout_ns = eo.timeout_ns;
+        if (i4_dispatch(ks.D, ks.group, [&](auto k) { return decltype(k)::launch(p, Launch{ks.sms * ks.dec_bps, st}); }) !=
+            cudaSuccess)
+            return RPA_ERR_CUDA;
+    }
+    return rec(kEvDecEnd) ? RPA_OK : RPA_ERR_CUDA;
 }
 
 }  // namespace rpa
