@@ -30,7 +30,7 @@ namespace rpa {
 namespace {
 
 constexpr int R = kInt4Rows;
-// The running maximum moves when a row's grows by more than 2^2: probabilities stay below 4, and P below 4 * 8734 (the
+// The running maximum moves when a row's grows by more than 2^2: probabilities stay below 4, and P below 4 * 8736 (the
 // greatest scale of float16 values), in f16's range
 constexpr float kRescale = 2.f;
 

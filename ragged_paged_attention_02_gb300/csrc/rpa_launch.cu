@@ -155,14 +155,17 @@ void kernels_choose(const RpaCfg& c, int sms, KernelSet* ks) {
     if (ks->kt == KT_I4) {
         ks->direct_tokens = kInt4DirectRows / ks->G > ks->Tt ? kInt4DirectRows / ks->G : ks->Tt;
         ks->few_tokens = kInt4FewRows / ks->G;
-        // room for prompts of longer sequences: 2^18 keys of 8 heads at D 128 (1 GiB), the longest sequence at least, all of them at most
-        const int64_t page = 64 * 4 * c.num_kv_heads * c.head_dim, most = (c.pages_per_seq * c.page_size + 63) / 64;
+        // room for prompts of longer sequences: 1 GiB (2^18 keys of 8 heads at D 128), more where the longest sequence needs it (up
+        // to 8 GiB), less where all of them do not
+        const int64_t page = 64 * 4 * c.num_kv_heads * c.head_dim, gib = (((int64_t)1 << 30) + page - 1) / page;
+        const int64_t most = (c.pages_per_seq * c.page_size + 63) / 64;
+        const int64_t longest = ((c.pages_per_seq < c.total_num_pages ? c.pages_per_seq : c.total_num_pages) * c.page_size + 63) / 64 + 1;
         ks->P64 = (int)most;
         // (no room in a handle of at most a token a sequence: one that decodes, whose calls are then three kernels; a sequence of
         // many tokens takes the direct kernel's tiles there)
         if (c.num_q_tokens > ks->direct_tokens && c.num_q_tokens > c.max_num_seqs) {
-            int64_t pages = ((int64_t)1 << 30) / page;
-            if (pages < most + 1) pages = most + 1;
+            int64_t pages = longest < 8 * gib ? longest : 8 * gib;
+            if (pages < gib) pages = gib;
             if (pages > c.max_num_seqs * (most + 1)) pages = c.max_num_seqs * (most + 1);
             ks->room_pages = (int)(pages < kInt4MaxRoom ? pages : kInt4MaxRoom);
         }
