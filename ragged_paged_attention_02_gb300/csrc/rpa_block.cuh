@@ -12,14 +12,21 @@ __device__ __forceinline__ void block_scan(const int (&v)[N], int (&r)[N], int (
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int nwarps = blockDim.x >> 5;
     int x[N];
+    int some = 0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) x[i] = v[i];
+    for (int i = 0; i < N; ++i) {
+        x[i] = v[i];
+        some |= v[i];
+    }
+    // (a warp without values has nothing to add up: the shuffles of all warps go through one unit)
+    if (__any_sync(0xffffffffu, some)) {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
+        for (int o = 1; o < 32; o <<= 1) {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int y = __shfl_up_sync(0xffffffffu, x[i], o);
-            if (lane >= o) x[i] += y;
+            for (int i = 0; i < N; ++i) {
+                const int y = __shfl_up_sync(0xffffffffu, x[i], o);
+                if (lane >= o) x[i] += y;
+            }
         }
     }
     if (lane == 31) {
@@ -54,28 +61,26 @@ __device__ __forceinline__ void block_scan(const int (&v)[N], int (&r)[N], int (
     __syncthreads();
 }
 
+// Sum over a warp of a value of 32-bit unsigned integers below 2^27 (all lanes get it): one instruction's.
+__device__ __forceinline__ unsigned long long warp_sum27(unsigned v) { return __reduce_add_sync(0xffffffffu, v); }
+// ... of 64-bit values: 27 bits at a time (a sum over 32 lanes keeps within 32 bits), modulo 2^64
+__device__ __forceinline__ unsigned long long warp_sum64(unsigned long long v) {
+    constexpr unsigned kBits = (1u << 27) - 1;
+    return warp_sum27((unsigned)v & kBits) + (warp_sum27((unsigned)(v >> 27) & kBits) << 27) + (warp_sum27((unsigned)(v >> 54)) << 54);
+}
 // Sums of two 64-bit values per thread over the block (all threads get them).  s_red holds 64.
 __device__ __forceinline__ void block_sum64x2(unsigned long long& a, unsigned long long& b, unsigned long long* s_red) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, nwarps = blockDim.x >> 5;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        a += __shfl_xor_sync(0xffffffffu, a, o);
-        b += __shfl_xor_sync(0xffffffffu, b, o);
-    }
+    a = warp_sum64(a);
+    b = warp_sum64(b);
     if (lane == 0) {
         s_red[warp] = a;
         s_red[32 + warp] = b;
     }
     __syncthreads();
-    unsigned long long x = lane < nwarps ? s_red[lane] : 0ull, y = lane < nwarps ? s_red[32 + lane] : 0ull;
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-        x += __shfl_xor_sync(0xffffffffu, x, o);
-        y += __shfl_xor_sync(0xffffffffu, y, o);
-    }
+    a = warp_sum64(lane < nwarps ? s_red[lane] : 0ull);
+    b = warp_sum64(lane < nwarps ? s_red[32 + lane] : 0ull);
     __syncthreads();
-    a = x;
-    b = y;
 }
 // Minimum of one 64-bit value per thread over the block (all threads get it).  s_red holds 32.
 __device__ __forceinline__ unsigned long long block_min64(unsigned long long v, unsigned long long* s_red) {

@@ -40,6 +40,7 @@ struct I4Params {
     int BR, brs;             // keys of a copied page run, log2
     uint32_t block;          // bytes of a page's block
     FastDiv page;            // by the page size
+    int most_items;          // that the list has room for
     int stall;               // test hook: no copies are issued
     unsigned long long timeout_ns;
 };
@@ -137,8 +138,6 @@ __global__ void __launch_bounds__((I4Geom<D, NG>::THREADS), (I4Geom<D, NG>::CTAS
     __syncthreads();
     pdl_trigger();
     pdl_wait();  // the planner's items are complete from here on
-    if ((int)blockIdx.x >= ctrl[kDecCtas]) return;
-    const int n_items = ctrl[a.item_count_word];
     const int G = a.G, Hq = a.Hq, BR = p.BR, brs = p.brs, RB = BR * Gm::KB;
 
     if (warp == CW) {
@@ -178,18 +177,19 @@ __global__ void __launch_bounds__((I4Geom<D, NG>::THREADS), (I4Geom<D, NG>::CTAS
             x.win = (x.win0 + lane < a.P) ? __ldg(ids) : 0;
             x.win2 = (x.win0 + 32 + lane < a.P) ? __ldg(ids + 32) : 0;
         };
-        int it = 0;
-        if (lane == 0) it = atomicAdd(ctrl + a.counter_word, 1);
-        it = __shfl_sync(0xffffffffu, it, 0);
+        // the first item is the CTA's own, its unit on its way with the number of items (where there is none of that number, what
+        // the list holds there is not used); the others come off a counter
+        int it = blockIdx.x;
+        if (it < p.most_items) fetch_unit(cur, it);
+        const int ctas = ctrl[kDecCtas], n_items = it < ctas ? ctrl[a.item_count_word] : 0;
         bool ok = true;
         if (it < n_items) {
-            fetch_unit(cur, it);
             fetch_lengths(cur);
             fetch_pages(cur);
         }
         while (ok && it < n_items) {
             int more = 0;
-            if (lane == 0) more = atomicAdd(ctrl + a.counter_word, 1);
+            if (lane == 0) more = ctas + atomicAdd(ctrl + a.counter_word, 1);
             const Item& item = cur.item;
             const int* ptab = a.page_indices + (size_t)item.seq * a.P;
             const int kvh = item.head / p.blocks;
@@ -900,6 +900,7 @@ int enqueue_int4(const RpaCfg& c, const KernelSet& ks, const Workspace& ws, MapC
         while ((1 << p.brs) < p.BR) ++p.brs;
         p.block = (uint32_t)(c.page_size * int4_key_bytes(ks.D, ks.group));
         p.page.set((uint32_t)c.page_size);
+        p.most_items = ks.max_dec_units * a.unit_heads;
         p.stall = eo.debug_stall;
         p.timeout_ns = eo.timeout_ns;
         if (i4_dispatch(ks.D, ks.group, [&](auto k) { return decltype(k)::launch(p, Launch{ks.sms * ks.dec_bps, st}); }) !=

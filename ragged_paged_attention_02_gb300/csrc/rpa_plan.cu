@@ -66,16 +66,17 @@ __device__ __forceinline__ bool bad_lengths(int q0, int q1, int kl, const PlanPa
 // start.
 __device__ void give_room(const PlanParams& p, int* cls, int* scan, int* taken) {
     const int S = p.num_seqs;
-    if (threadIdx.x == 0) *taken = 0;
-    __syncthreads();
+    // (taken is 0, and the block past a barrier behind that)
     // how many rows a sequence may have for the direct kernel goes by the number of such sequences
-    int few = 0;
+    int few = 0, more = 0;
     for (int s = threadIdx.x; s < S; s += blockDim.x) {
         const int q0 = p.cu_q_lens[s], q1 = p.cu_q_lens[s + 1];
-        few += !bad_lengths(q0, q1, p.kv_lens[s], p) && q1 - q0 > p.direct_tokens && q1 - q0 <= p.few_tokens;
+        cls[s] = 0;
+        if (bad_lengths(q0, q1, p.kv_lens[s], p) || q1 - q0 <= p.direct_tokens) continue;
+        ++(q1 - q0 <= p.few_tokens ? few : more);
     }
     if (few) atomicAdd(taken, few);
-    __syncthreads();
+    if (!__syncthreads_or(few | more)) return;  // no prompts: nothing reads vbase
     const int direct = min(p.few_tokens, (kInt4DirectRows + kInt4RowsByItems / max(1, min(*taken, kInt4RowsByItems) * p.pf_Hkv)) / p.pf_G);
     __syncthreads();
     if (threadIdx.x == 0) *taken = 0;
@@ -139,7 +140,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
     int* s_kl = s_q0 + S + 1;
     const int Tq = max(1, p.pf_tokens);  // query tokens per prefill tile
 
-    if (tid == 0) s_bad = 0;
+    if (tid == 0) s_bad = s_taken = 0;
     __syncthreads();
 
     const bool room = p.int4 && p.room_pages > 0;
@@ -217,7 +218,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
                 mine = k < mine ? k : mine;
             }
         }
-        const unsigned long long best = block_min64(mine, s_red);
+        const unsigned long long best = both ? block_min64(mine, s_red) : 0ull;  // (`both` is the block's)
         if (tid == 0) {
             int pf_sms = p.n_sms, dec_sms = p.n_sms;
             if (both) {
@@ -239,12 +240,11 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
         const unsigned long long target = (unsigned long long)p.dec_waves * (unsigned long long)max(1, dec_ctas);
         unsigned long long c = (s_total + target - 1) / target;
         // 4-bit K/V: pieces long enough to make up for an item's start and end, as long as every CTA has one
-        const unsigned long long one = (s_total + max(1, dec_ctas) - 1) / (unsigned long long)max(1, dec_ctas);
-        if (c < (unsigned long long)p.good_chunk) c = min(one, (unsigned long long)p.good_chunk);
+        if (c < (unsigned long long)p.good_chunk)
+            c = min((s_total + max(1, dec_ctas) - 1) / (unsigned long long)max(1, dec_ctas), (unsigned long long)p.good_chunk);
         if (c < (unsigned long long)p.min_chunk) c = p.min_chunk;
-        c = (c + p.chunk_align - 1) / p.chunk_align * p.chunk_align;
-        if (c > (1ull << 30)) c = 1ull << 30;
-        chunk = (int)c;
+        const unsigned c32 = (unsigned)min(c, 1ull << 30), al = (unsigned)p.chunk_align;
+        chunk = (int)((c32 + al - 1) / al * al);
     }
 
     // ---- 3. prefix sums: unit ends per class, partial slots, combine entries
@@ -465,10 +465,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
                 rem -= W;
                 if (++s >= S) break;
             }
-            if (s_cls[s] != 1) continue;
-            const int pieces = (s_cnt[s] + chunk - 1) / chunk;
-            if (pieces <= 1 || (p.int4 && s_q0[s + 1] - s_q0[s] > p.dec_tokens)) continue;
-            const int h = rem >> 1;
+            if (s_cls[s] != 1 || s_cnt[s] <= chunk || (p.int4 && s_q0[s + 1] - s_q0[s] > p.dec_tokens)) continue;
+            const int pieces = (s_cnt[s] + chunk - 1) / chunk, h = rem >> 1;
             // Comb: q0, rows, head, part | pieces, 0, 0, 0
             int4* d4 = reinterpret_cast<int4*>(p.comb + s_comb[s] + h);
             if ((rem & 1) == 0)
@@ -481,8 +479,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
     if (p.int4 && n_dec > 0) {
         for (int s = tid >> 5; s < S; s += (int)blockDim.x >> 5) {
             const int ql = s_q0[s + 1] - s_q0[s];
+            if (ql <= p.dec_tokens || s_cls[s] != 1 || s_cnt[s] <= chunk) continue;
             const int pieces = (s_cnt[s] + chunk - 1) / chunk;
-            if (ql <= p.dec_tokens || s_cls[s] != 1 || pieces <= 1) continue;
             for (int i = tid & 31; i < dec_tiles(ql, p) * p.Hkv; i += 32) {
                 const int tile = i / p.Hkv, h = i - tile * p.Hkv, t0 = tile * p.dec_tokens;
                 int4* d4 = reinterpret_cast<int4*>(p.comb + s_comb[s] + i);
@@ -491,8 +489,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
             }
         }
     }
-    // every thread's unit-list and combine-entry stores, before the plan is published
-    __threadfence();
+    // every thread's unit-list and combine-entry stores, before thread 0 publishes the plan (its fence covers them)
     __syncthreads();
     if (tid == 0) {
         ctrl[kNumDecItems] = p.dec_on_pf ? 0 : n_dec * p.Hkv;
@@ -509,7 +506,9 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
         ctrl[kPfCtas] = s_split[0];
         ctrl[kDecCtas] = s_split[1];
         ctrl[kStatus] = 0;
-        publish_epoch(ctrl, p.epoch);
+        // (only a decode kernel behind a concurrent prefill looks at the epoch; the others wait for this grid)
+        if (!p.concurrent) ctrl[kPlanEpoch] = p.epoch;
+        else publish_epoch(ctrl, p.epoch);
     }
 }
 
