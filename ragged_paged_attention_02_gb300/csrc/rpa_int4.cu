@@ -181,7 +181,7 @@ __global__ void __launch_bounds__((I4Geom<D, NG>::THREADS), (I4Geom<D, NG>::CTAS
         // the list holds there is not used); the others come off a counter
         int it = blockIdx.x;
         if (it < p.most_items) fetch_unit(cur, it);
-        const int ctas = ctrl[kDecCtas], n_items = it < ctas ? ctrl[a.item_count_word] : 0;
+        const int ctas = min(ctrl[kDecCtas], (int)gridDim.x), n_items = it < ctas ? ctrl[a.item_count_word] : 0;
         bool ok = true;
         if (it < n_items) {
             fetch_lengths(cur);

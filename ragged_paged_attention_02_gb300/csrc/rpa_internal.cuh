@@ -30,6 +30,7 @@ enum Ctrl : int {
     kPfCtas = 12,  // prefill CTAs that take work (the rest exit at once)
     kDecCtas = 13, // decode CTAs that take work
     kPlanEpoch = 14,  // the epoch of the call whose plan is complete (the planner writes it last)
+    kPfFirst = 15,    // the item that the 64-key-tile prefill kernel begins with (it comes round to those before it)
     kCtrlWords = 32,
 };
 

@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
     extern __shared__ __align__(16) unsigned long long s_keys[];  // kMaxSort keys, then sequence scratch
     __shared__ int s_scan[33 * 5];
     __shared__ unsigned long long s_red[64];
-    __shared__ int s_bad;
+    __shared__ int s_bad, s_long;             // bad lengths; a prefill unit of more keys than a decode piece
     __shared__ int s_split[2];                // prefill CTAs, decode CTAs
     __shared__ int s_taken;                   // pages of the room that are given away
     const int tid = threadIdx.x;
@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
     int* s_kl = s_q0 + S + 1;
     const int Tq = max(1, p.pf_tokens);  // query tokens per prefill tile
 
-    if (tid == 0) s_bad = s_taken = 0;
+    if (tid == 0) s_bad = s_taken = s_long = 0;
     __syncthreads();
 
     const bool room = p.int4 && p.room_pages > 0;
@@ -351,6 +351,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
             d[5] = -1; d[6] = 0; d[7] = 1;
             cost = hi - lo + first_cost(lo, p);
             wseq = s_comb[s];
+            if (cost > chunk) s_long = 1;
             cls_bit = 1;
             pos = u;
         }
@@ -503,6 +504,8 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
         ctrl[kSorted] = do_sort ? 1 : 0;
         ctrl[kCovLo] = S > 0 ? s_q0[0] : 0;
         ctrl[kCovHi] = S > 0 ? s_q0[S] : 0;
+        // (longest items first: decode pieces fill up behind the prefill units then)
+        ctrl[kPfFirst] = p.dec_on_pf && s_long ? n_dec * p.Hkv : 0;
         ctrl[kPfCtas] = s_split[0];
         ctrl[kDecCtas] = s_split[1];
         ctrl[kStatus] = 0;

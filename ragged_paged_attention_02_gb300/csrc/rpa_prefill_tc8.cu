@@ -292,9 +292,8 @@ __global__ void __launch_bounds__(kRegBoundThreads, 1) rpa_prefill_tc8(const __g
         uint32_t ph = 0, mph = 0, qph = 0;
         uint32_t tgp = 0;  // direct mode: tiles copied so far (all items): tile buffer and phase
         bool ok = true;
-        int it = 0;
-        if (lane == 0) it = atomicAdd(ctrl + a.counter_word, 1);
-        it = __shfl_sync(0xffffffffu, it, 0);
+        const int ctas = min(ctrl[kPfCtas], (int)gridDim.x), first = ctrl[kPfFirst];
+        int it = blockIdx.x;  // the first item is the CTA's own, the others come off a counter
         for (;;) {
             if (!mbar_wait(smem_u32(&meta_free[ms]), mph ^ 1u, ctrl, tmo)) break;
             if (it >= n_items) {
@@ -304,9 +303,10 @@ __global__ void __launch_bounds__(kRegBoundThreads, 1) rpa_prefill_tc8(const __g
                 }
                 break;
             }
-            const Item item = item_at(a.units, it, a.unit_heads);
+            const int at = it + first < n_items ? it + first : it + first - n_items;
+            const Item item = item_at(a.units, at, a.unit_heads);
             int nxt = 0;
-            if (lane == 0) nxt = atomicAdd(ctrl + a.counter_word, 1);
+            if (lane == 0) nxt = ctas + atomicAdd(ctrl + a.counter_word, 1);
             const int q_start = a.cu_q_lens[item.seq];
             const int ql = a.cu_q_lens[item.seq + 1] - q_start;
             const int kl = a.kv_lens[item.seq];

@@ -325,6 +325,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_prefix_plan_kernel(const 
         ctrl[kPfCounter] = 0;
         ctrl[kNumPart] = n_part;
         ctrl[kNumUnits] = n_dec + n_pf;
+        ctrl[kPfFirst] = 0;
         ctrl[kPfCtas] = pf_ctas;
         ctrl[kDecCtas] = dec_ctas;
         publish_epoch(ctrl, p.epoch);
