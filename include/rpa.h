@@ -67,7 +67,13 @@ typedef enum RpaDtype {
  *   V scale, zero  alike
  * (page_size a multiple of 4 as ever, and at most 65536)
  * and a channel's value is  code * scale + zero  of its group (times k_scale or v_scale).  rpa_rope_append writes
- * it, rpa_rope_read reads its rows as values, rpa_forward attends over it. */
+ * it, rpa_rope_read reads its rows as values, rpa_forward attends over it.
+ * rpa_forward takes scales from 0 to 8736 (what values of f16's range can have) and rounds q to f16.  It multiplies the codes
+ * themselves, with probabilities times scales rounded to f16 (those below 2^-14 to a multiple of 2^-24: v_scale keeps small
+ * values away from there).  A sequence of many tokens (more than 64 to 448 query rows a kv head, by how many such there are) is
+ * computed from its K and V as f16 values instead, which the call writes to the workspace: the handle has room for
+ * 1 GiB of them, or for one sequence of the most keys that fit into kv_pages (up to 8 GiB), if that is more, and none where
+ * num_q_tokens <= max_num_seqs.  Sequences without room are computed from the codes, more slowly. */
 
 typedef enum RpaStatus {
     RPA_OK = 0,
@@ -97,7 +103,7 @@ typedef struct RpaCfg {
     int64_t pages_per_seq;   /* columns of page_indices */
     int64_t sliding_window;  /* used when has_sliding_window; must be >= 1 */
     int32_t q_dtype;         /* RpaDtype of q and o: BF16, F16 or F32 */
-    int32_t kv_dtype;        /* RpaDtype of kv_pages: BF16, F16, FP8_E4M3, FP8_E5M2 or INT8 */
+    int32_t kv_dtype;        /* RpaDtype of kv_pages: BF16, F16, FP8_E4M3, FP8_E5M2, INT8 or INT4_G* */
     float sm_scale;          /* logit scale, finite */
     float mask_value;        /* additive mask of the page (default -2.38197633e38); must be
                                 <= -1e30 so that masked keys get weight exactly 0 */
@@ -162,7 +168,7 @@ int rpa_create(const RpaCfg* cfg, RpaHandle** out);
  * kv_lens, page_indices, cu_q_lens, num_seqs, q, kv_pages and output o).
  *   q            device, [num_q_tokens, Hq, D] q_dtype, 16-byte aligned
  *   kv_pages     device, [total_num_pages, page_size, 2*Hkv, D] kv_dtype, 16-byte aligned
- *                ([total_num_pages, page_size, Hkv, D] for RPA_KV_LATENT)
+ *                ([total_num_pages, page_size, Hkv, D] for RPA_KV_LATENT; the blocks of a 4-bit cache)
  *   kv_lens      device, int32 [max_num_seqs]
  *   page_indices device, int32 [max_num_seqs, pages_per_seq], row-major
  *   cu_q_lens    device, int32 [max_num_seqs + 1]
@@ -248,7 +254,8 @@ typedef enum RpaOption {
                                       precedes it on the stream: host copies, or kernels that end before
                                       the call, satisfy this); the planner then reads and orders them
                                       while the kernel before it (typically the previous call's
-                                      combine) still runs.  Default 0: it first waits for that kernel */
+                                      combine) still runs.  Default 0: it first waits for that kernel.  A 4-bit
+                                      cache's planner always waits where the handle has room for f16 rows */
     RPA_OPT_TEST_STALL_PRODUCER = 100  /* test hook, 1: the decode kernel's copy warp issues nothing, so
                                       that its consumers' bounded waits run out (status
                                       RPA_ERR_TIMEOUT); the kernel still returns */
@@ -273,7 +280,8 @@ int rpa_set_option(RpaHandle* h, int32_t option, int64_t value);
  * one 32 MiB array in the library's own device memory, which every GPU that
  * loads the library holds until the process exits.  A configuration whose
  * worst-case workspace exceeds 32 MiB returns RPA_ERR_NO_ALLOC_LIMIT before
- * anything is enqueued.  Nothing here calls cudaMalloc, cudaFree or any other
+ * anything is enqueued.  (4-bit K/V: the array has no room for f16 rows, and
+ * every token is computed from the codes.)  Nothing here calls cudaMalloc, cudaFree or any other
  * allocating routine.
  *
  * The first call on each device (with that device current) looks up the
@@ -367,7 +375,8 @@ int rpa_rope_create(const RpaRopeCfg* cfg, RpaRope** out);
  *              contiguous too, and overlaps none of the other tensors
  * The arithmetic is in 32 bits with one rounding at the end.  The angle of position p is p w_i, w_i as
  * rpa_rope_frequencies gives it, modulo a turn, exact to 2^-32 of a turn at any position; the sine then
- * takes it as a 32-bit float, within 2^-26 of a turn near half a turn and exact near 0.  Cache rows hold k / k_scale and v / v_scale (where set), rounded to nearest even;
+ * takes it as a 32-bit float, within 2^-26 of a turn near half a turn and exact near 0 (keys of a 4-bit cache are rotated in pairs of
+ * floats, the sines within 2^-30: a value next to the border of two codes takes the right one).  Cache rows hold k / k_scale and v / v_scale (where set), rounded to nearest even;
  * the 8-bit types saturate, NaN stays NaN (int8: 0); f16 rows overflow to infinity.  4-bit rows: values saturate at
  * +-65504; a group's zero is its least value rounded down to f16, its scale (greatest - zero) / 15 rounded up to f16, a
  * code (value - zero) / scale rounded to nearest even, at most 15; a group with a NaN reads as NaN.

@@ -3,7 +3,7 @@
 The computation lives in ``librpa.so`` (CUDA kernels behind the C ABI of
 ``include/rpa.h``); this package is the Python binding used by the tests and
 the benchmark: ``RaggedPagedAttention``, and around its paged cache
-``RopeAppend``, ``SharedPrefixAttention`` and ``CacheEviction``.  Build the library with ``__graft_entry__.build()`` or
+``RopeAppend`` (which reads its rows too), ``SharedPrefixAttention`` and ``CacheEviction``.  Build the library with ``__graft_entry__.build()`` or
 ``python -m ragged_paged_attention_02_gb300._build``.
 """
 
@@ -15,6 +15,9 @@ from .binding import (  # noqa: F401
     RPA_DT_F32,
     RPA_DT_FP8_E4M3,
     RPA_DT_FP8_E5M2,
+    RPA_DT_INT4_G32,
+    RPA_DT_INT4_G64,
+    RPA_DT_INT4_G128,
     RPA_DT_INT8,
     RPA_ERR_BAD_LENGTHS,
     RPA_ERR_BAD_PAGE_INDEX,

@@ -18,8 +18,15 @@
 //    head (or four pieces of one where its size is not that of a run) into a ring of stages, the other warps take 32 keys of
 //    each.  Bound by instructions more than by bytes (a key and kv head costs 17 issue slots at D 128, of the 25 that its bytes'
 //    time has), so as few warps as can feed the others issue copies.  (Warps that each copied for themselves took 25.)
+//    128 decodes of 512 to 16 k keys (32 query and 8 kv heads, D 128, groups of 64, 1245 MB): 225 us of the call's 234, 5.5 TB/s.
+//    16 decodes of a 4 k window (D 256, groups of 128, soft cap, 143 MB): 46 us of 54, 3.1 TB/s, with 12 warps an SM, whose 168
+//    registers hold q and the outputs: they issue 39 % of the time, waiting for matrix loads and products.  32 sequences of 1 to 5
+//    tokens (D 64, 35 MB, some keys in two or three tiles): 25 us of 39, issue 54 %.  4 decodes: 17 us a call, 8 of them
+//    dependent loads and the planner's latency before the first product.
 //  * long prompts would decode every key once for each tile.  Sequences with more tokens are unfolded instead, once a call, to
-//    f16 rows in the workspace, over which the tensor-memory prefill kernels run.
+//    f16 rows in the workspace, over which the tensor-memory prefill kernels run.  Three prompts of 0.8 to 2 k tokens on top
+//    of 4 to 16 k keys (32 and 8 heads, D 128): 529 us, 40 of them the rows (and q's rounding; 203 MB, 5.1 TB/s) and 468 the
+//    attention (562 GFLOP, 1.2 PFLOP/s).
 #include <cuda_fp16.h>
 #include <string.h>
 

@@ -1,7 +1,7 @@
 // rpa_launch.cu -- host logic shared by rpa_forward and rpa_forward_noalloc.
 //
 // From a validated configuration: which kernels and tiles run (the element types decide the
-// MMA operand type: bf16 for bf16 K/V, f16 for f16 and every 8-bit cache), their occupancy,
+// MMA operand type: bf16 for bf16 K/V, f16 for f16 and every 8- or 4-bit cache), their occupancy,
 // the worst-case workspace layout, and the sequence a call enqueues on its stream:
 //
 //   [q conversion]  only when q's type is not the MMA operand type the kernels read (f32 q, or a
@@ -12,6 +12,8 @@
 //   prefill         tensor-memory kernels (2-byte K/V at D 64 / 128; 8-bit K/V and 2-byte K/V at
 //                   D 256, which also take the decode rows) or the latent-attention kernel (latent
 //                   layout, every row)
+//   (4-bit K/V: the prompts' f16 rows and their prefill kernel, where the handle has room for them, then the
+//                   4-bit kernel, which takes every other row)
 //   combine         split-KV merge, output of the uncovered rows
 //
 // Each kernel is a programmatic dependent of the one before it on the caller's stream (its

@@ -7,7 +7,9 @@
 // A CTA takes blocks of neighbouring tokens (as many as its threads hold a row's units of 16 elements of: 32 at D 128), looks
 // their slots up at once, and then a thread steps over the rows of its token, four in flight.  Neighbouring threads hold a row's
 // units, then the same row of the next token: in a 4-bit block the rows of neighbouring slots lie side by side.  Few tokens spread
-// over CTAs by rows.  Bound by HBM: the rows read and written.
+// over CTAs by rows.  Bound by HBM, the rows read and written: 53.5 k tokens of 8 kv heads at D 128 (groups of 128, 278 MB) take 48 us,
+// 5.8 TB/s, 52 in a stream of calls; 1300 tokens 5.3 us and a call 6, of launch, lookups and two dependent loads.  A row of every
+// token a thread, not every row of a token a warp (75 -> 57 us), and codes two at a time (57 -> 52).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 

@@ -26,6 +26,15 @@
 // Bound by HBM: 8192 tokens of 64 q and 8 kv heads at D 128 (bf16, 344 MB) take 60 us, 5.7 TB/s, 0.84 of the
 // measured copy.  Five CTAs an SM with two rows in flight a thread, when that took 61 us: four CTAs 63 us with two rows,
 // 64 with four (spilled); one token a CTA 79 to 87 us.
+//
+// Rows of a 4-bit cache.  k is rotated in pairs of floats (sines by Taylor series, within 2^-30) and a group's zero, scale and codes
+// are rounded from the exact sums, so that the codes are those of the formula's real values but for values within 2^-30 of a border
+// (with 32-bit sines some next to a border were others).  A row's threads exchange it through shared memory, 16 neighbouring
+// channels each, and form a group's extremes by shuffles.  Bound by instructions: 4.4 k tokens of 32 q and 8 kv heads at D 128 (groups
+// of 32, 120 MB with the rows read back by the call behind) take 32 us, and the two calls 38.  One copy of the coding loop for q, K
+// and V rows with the next row's loads in flight (57 -> 38 us: unrolled by kind it did not stay in the instruction cache); three
+// CTAs an SM of 12 tokens a round (80 registers; with four the loop spilled, 53 us); codes from the reciprocal of the
+// scale, and the exact remainder only for those next to a border (no divisions).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <string.h>
