@@ -279,6 +279,7 @@ class RaggedPagedAttention:
         if r != RPA_OK:
             raise RpaError(r, "rpa_create")
         self._h = h
+        self._forward = lib().rpa_forward
 
     def close(self):
         if getattr(self, "_h", None):
@@ -291,30 +292,40 @@ class RaggedPagedAttention:
         except Exception:
             pass
 
-    def _check(self, q, kv_pages, kv_lens, page_indices, cu_q_lens, out):
+    _q_dtype = None
+
+    def _make_checks(self):
+        """What forward's tensors have to be, from the configuration."""
         import torch
 
         c = self._c
-        T, Hq, D = c.num_q_tokens, c.num_q_heads, c.head_dim
-        qt = {RPA_DT_BF16: torch.bfloat16, RPA_DT_F16: torch.float16, RPA_DT_F32: torch.float32}[c.q_dtype]
-        if q.dtype != qt or tuple(q.shape) != (T, Hq, D) or not q.is_contiguous():
+        T, Hq, S = c.num_q_tokens, c.num_q_heads, c.max_num_seqs
+        self._q_dtype = {RPA_DT_BF16: torch.bfloat16, RPA_DT_F16: torch.float16, RPA_DT_F32: torch.float32}[c.q_dtype]
+        self._q_shape, self._o_shape = (T, Hq, c.head_dim), (T, Hq, self.out_dim)
+        self._kv_shape = cache_shape(c)
+        self._kv_dtype = {RPA_DT_BF16: torch.bfloat16, RPA_DT_F16: torch.float16}.get(c.kv_dtype)  # None: one byte
+        self._lens = (("kv_lens", (S,)), ("page_indices", (S, c.pages_per_seq)), ("cu_q_lens", (S + 1,)))
+        self._i32 = torch.int32
+        # what torch.cuda.current_stream().cuda_stream is, in a tenth of the time
+        self._current = lambda C=torch._C: C._cuda_getCurrentRawStream(C._cuda_getDevice())
+
+    def _check(self, q, kv_pages, kv_lens, page_indices, cu_q_lens, out):
+        if self._q_dtype is None:
+            self._make_checks()
+        qt = self._q_dtype
+        if q.dtype is not qt or q.shape != self._q_shape or not q.is_contiguous():
             raise ValueError(f"q must be a contiguous {qt} tensor [num_q_tokens, Hq, D]")
-        Dv = self.out_dim
-        if out.dtype != qt or tuple(out.shape) != (T, Hq, Dv) or not out.is_contiguous():
-            raise ValueError(f"out must be a contiguous {qt} tensor [num_q_tokens, Hq, {Dv}]")
-        want_kv = cache_shape(c)
-        if tuple(kv_pages.shape) != want_kv or not kv_pages.is_contiguous():
-            raise ValueError(f"kv_pages must be contiguous {want_kv}")
-        if c.kv_dtype == RPA_DT_BF16 and kv_pages.dtype != torch.bfloat16:
-            raise ValueError("kv_pages must be bfloat16")
-        if c.kv_dtype == RPA_DT_F16 and kv_pages.dtype != torch.float16:
-            raise ValueError("kv_pages must be float16")
-        if c.kv_dtype not in (RPA_DT_BF16, RPA_DT_F16) and kv_pages.element_size() != 1:
+        if out.dtype is not qt or out.shape != self._o_shape or not out.is_contiguous():
+            raise ValueError(f"out must be a contiguous {qt} tensor [num_q_tokens, Hq, {self.out_dim}]")
+        if kv_pages.shape != self._kv_shape or not kv_pages.is_contiguous():
+            raise ValueError(f"kv_pages must be contiguous {self._kv_shape}")
+        if self._kv_dtype is not None:
+            if kv_pages.dtype is not self._kv_dtype:
+                raise ValueError(f"kv_pages must be {str(self._kv_dtype)[6:]}")
+        elif kv_pages.element_size() != 1:
             raise ValueError("kv_pages must hold one byte per element (fp8 / int8 / int4 blocks)")
-        for name, t, shape in (("kv_lens", kv_lens, (c.max_num_seqs,)),
-                               ("page_indices", page_indices, (c.max_num_seqs, c.pages_per_seq)),
-                               ("cu_q_lens", cu_q_lens, (c.max_num_seqs + 1,))):
-            if t.dtype != torch.int32 or tuple(t.shape) != shape or not t.is_contiguous():
+        for (name, shape), t in zip(self._lens, (kv_lens, page_indices, cu_q_lens)):
+            if t.dtype is not self._i32 or t.shape != shape or not t.is_contiguous():
                 raise ValueError(f"{name} must be a contiguous int32 tensor {shape}")
 
     @property
@@ -326,12 +337,11 @@ class RaggedPagedAttention:
         if out is None:
             out = q.new_empty((q.shape[0], q.shape[1], self.out_dim))
         self._check(q, kv_pages, kv_lens, page_indices, cu_q_lens, out)
-        for t in (q, kv_pages, kv_lens, page_indices, cu_q_lens, out):
-            if not t.is_cuda:
-                raise ValueError("forward takes CUDA tensors; use forward_host for host buffers")
-        r = lib().rpa_forward(self._h, q.data_ptr(), kv_pages.data_ptr(), kv_lens.data_ptr(),
-                              page_indices.data_ptr(), cu_q_lens.data_ptr(), int(num_seqs),
-                              out.data_ptr(), _stream_ptr(stream))
+        if not (q.is_cuda and kv_pages.is_cuda and kv_lens.is_cuda and page_indices.is_cuda and cu_q_lens.is_cuda and out.is_cuda):
+            raise ValueError("forward takes CUDA tensors; use forward_host for host buffers")
+        r = self._forward(self._h, q.data_ptr(), kv_pages.data_ptr(), kv_lens.data_ptr(),
+                          page_indices.data_ptr(), cu_q_lens.data_ptr(), int(num_seqs),
+                          out.data_ptr(), self._current() if stream is None else _stream_ptr(stream))
         if r != RPA_OK:
             raise RpaError(r, "rpa_forward")
         return out
