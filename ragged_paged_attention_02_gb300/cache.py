@@ -96,6 +96,16 @@ class _Handle:
                 t.record_stream(stream)
         return stream.cuda_stream
 
+    def _fits(self, kv_pages, kinds, plain):
+        """Whether the cache and the plain tensors, whose (dtype, shape) are `kinds`, are contiguous, of their types and shapes, and
+        here: all that the _need functions ask of them, in less time.  Where they are not, those say what is wrong."""
+        here, kv_dtype = self._device, self._kv_dtype
+        for t, (dtype, shape) in zip(plain, kinds):
+            if t.dtype is not dtype or t.shape != shape or t.get_device() != here or not t.is_contiguous():
+                return False
+        return (kv_pages.shape == self._kv_shape and (kv_pages.dtype is kv_dtype if kv_dtype else kv_pages.element_size() == 1)
+                and kv_pages.get_device() == here and kv_pages.is_contiguous())
+
     def _call(self, name, *args):
         if not self._h:
             raise ValueError("the handle is closed")
@@ -167,6 +177,8 @@ class RopeAppend(_Handle):
         self._c = make_rope_cfg(**cfg)
         self._create(self._c)
         self._checks(self._c.cache)
+        self._append_kinds = ((self._i32, self._lens_shape), (self._i32, self._table_shape), (self._i32, self._cu_shape),
+                              (self._q_dtype, self._q_shape))
 
     def _check(self, q, k, v, kv_pages, kv_lens, page_indices, cu_q_lens, positions, q_out):
         T, Hq, D = self._q_shape
@@ -197,16 +209,27 @@ class RopeAppend(_Handle):
 
             with torch.cuda.stream(stream):
                 q_out = torch.zeros(self._q_shape, dtype=self._q_dtype, device=q.device)
-        self._check(q, k, v, kv_pages, kv_lens, page_indices, cu_q_lens, positions, q_out)
+        dtype, D, here = self._q_dtype, self._q_shape[2], self._device
         tensors = (q, k, v, kv_pages, kv_lens, page_indices, cu_q_lens, positions, q_out)
-        self._need_here(tensors)
-        # the distance of two tokens; with one token any will do
-        far = self._q_shape[0] > 1
-        rows = self._kv_rows[1] * self._kv_rows[2]
-        self._call("append", q.data_ptr(), q.stride(0) if far else self._q_shape[1] * self._q_shape[2],
-                   k.data_ptr(), k.stride(0) if far else rows, None if v is None else v.data_ptr(),
-                   0 if v is None else v.stride(0) if far else rows, kv_pages.data_ptr(), kv_lens.data_ptr(),
-                   page_indices.data_ptr(), cu_q_lens.data_ptr(), None if positions is None else positions.data_ptr(),
+        q_far = k_far = v_far = 0  # the distance of two tokens
+        if v is not None and positions is None and self._q_shape[0] > 1:
+            (q_far, q1, q2), (k_far, k1, k2), (v_far, v1, v2) = q.stride(), k.stride(), v.stride()
+            fits = (q.dtype is k.dtype is v.dtype is dtype and q1 == k1 == v1 == D and q2 == k2 == v2 == 1 and not self._latent
+                    and q.shape == self._q_shape and k.shape == v.shape == self._kv_rows
+                    and q.get_device() == k.get_device() == v.get_device() == here
+                    and self._fits(kv_pages, self._append_kinds, (kv_lens, page_indices, cu_q_lens, q_out)))
+        else:
+            fits = False
+        if not fits:
+            self._check(q, k, v, kv_pages, kv_lens, page_indices, cu_q_lens, positions, q_out)
+            self._need_here(tensors)
+            # (with one token any distance will do)
+            far = self._q_shape[0] > 1
+            rows = self._kv_rows[1] * self._kv_rows[2]
+            q_far, k_far = (q.stride(0), k.stride(0)) if far else (self._q_shape[1] * D, rows)
+            v_far = 0 if v is None else v.stride(0) if far else rows
+        self._call("append", q.data_ptr(), q_far, k.data_ptr(), k_far, None if v is None else v.data_ptr(), v_far, kv_pages.data_ptr(),
+                   kv_lens.data_ptr(), page_indices.data_ptr(), cu_q_lens.data_ptr(), None if positions is None else positions.data_ptr(),
                    int(num_seqs), q_out.data_ptr(), self._stream(stream, tensors))
         return q_out
 
