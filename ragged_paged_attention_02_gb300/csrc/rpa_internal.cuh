@@ -106,6 +106,12 @@ __host__ __device__ constexpr int int4_warps(int D) { return D == 64 ? 4 : D == 
 // keys' time (0.11 ms for 8 k) whatever its rows up to a tile, and its keys are not split, so few items leave SMs idle.  With
 // 8 kv heads of 4 query heads, D 128, 8 k keys the two met at 440 rows of one sequence, 190 of 4, 124 of 8, 96 of 12 and 84 of 32.
 constexpr int kInt4DirectRows = 64, kInt4RowsByItems = 3000, kInt4FewRows = 448;
+// ... in tokens: the most that the direct kernel takes of a sequence, where n are longer than kInt4DirectRows
+__host__ __device__ inline int int4_direct_tokens(int n, int Hkv, int G, int few_tokens) {
+    const int n_pairs = (n < 1 ? 1 : n < kInt4RowsByItems ? n : kInt4RowsByItems) * Hkv;
+    const int tokens = (kInt4DirectRows + kInt4RowsByItems / n_pairs) / G;
+    return tokens < few_tokens ? tokens : few_tokens;
+}
 constexpr int kInt4MaxRoom = 1 << 20;     // pages of 64 keys (the planner's sums of refused sequences count to this)
 constexpr int kMaxGroup = 64;      // query heads per kv head (a prefill tile holds 128 / G tokens)
 constexpr int kDecWaves = 4;       // target decode items per resident CTA (the most of any kernel)

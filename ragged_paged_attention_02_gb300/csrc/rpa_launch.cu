@@ -163,9 +163,17 @@ void kernels_choose(const RpaCfg& c, int sms, KernelSet* ks) {
         const int64_t most = (c.pages_per_seq * c.page_size + 63) / 64;
         const int64_t longest = ((c.pages_per_seq < c.total_num_pages ? c.pages_per_seq : c.total_num_pages) * c.page_size + 63) / 64 + 1;
         ks->P64 = (int)most;
-        // (no room in a handle of at most a token a sequence: one that decodes, whose calls are then three kernels; a sequence of
-        // many tokens takes the direct kernel's tiles there)
-        if (c.num_q_tokens > ks->direct_tokens && c.num_q_tokens > c.max_num_seqs) {
+        // The fewest tokens of a call with a sequence that the planner unfolds: one of more than few_tokens, or n of more than
+        // direct_tokens, one of them of more than the rule's for n.
+        int64_t least = ks->few_tokens + 1;
+        for (int64_t n = 1; n <= c.max_num_seqs && (n - 1) * (ks->direct_tokens + 1) < least; ++n) {
+            const int64_t need = int4_direct_tokens((int)n, (int)c.num_kv_heads, ks->G, ks->few_tokens) + 1 + (n - 1) * (ks->direct_tokens + 1);
+            if (need < least) least = need;
+        }
+        // (no room where no call has as many, whose calls are then three kernels and not five (32 sequences of up to 5 drafted
+        // tokens: 39 -> 35 us), nor in a handle of at most a token a sequence, one that decodes: a sequence of many tokens takes
+        // the direct kernel's tiles there)
+        if (c.num_q_tokens >= least && c.num_q_tokens > c.max_num_seqs) {
             int64_t pages = longest < 8 * gib ? longest : 8 * gib;
             if (pages < gib) pages = gib;
             if (pages > c.max_num_seqs * (most + 1)) pages = c.max_num_seqs * (most + 1);

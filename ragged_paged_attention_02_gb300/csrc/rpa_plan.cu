@@ -85,7 +85,7 @@ __device__ void give_room(const PlanParams& p, int* cls, int* scan, int* taken) 
     }
     if (few) atomicAdd(taken, few);
     if (!__syncthreads_or(few | more)) return;  // no prompts: nothing reads vbase
-    const int direct = min(p.few_tokens, (kInt4DirectRows + kInt4RowsByItems / max(1, min(*taken, kInt4RowsByItems) * p.pf_Hkv)) / p.pf_G);
+    const int direct = int4_direct_tokens(*taken, p.pf_Hkv, p.pf_G, p.few_tokens);
     __syncthreads();
     if (threadIdx.x == 0) *taken = 0;
     int carry = 0;

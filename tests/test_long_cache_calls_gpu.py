@@ -203,3 +203,18 @@ def test_steps_of_a_server(D, group):
             g.replay()
         assert rope.status() == rpa.RPA_OK and att.status() == rpa.RPA_OK
         check(qr, out, kl, [1, 1])
+
+
+@pytest.mark.parametrize("q_lens,unfolded", [([113], 1), ([112], 0), ([79, 17, 17], 1), ([78, 17, 17], 0), ([62, 17, 17, 17], 0)])
+def test_tokens_that_make_room(q_lens, unfolded):
+    """The fewest tokens of which a sequence is computed from f16 rows (4 kv heads of 4 query heads: 113), and calls of fewer, for
+    which a handle has no room: each against the definition."""
+    from test_int4_attention_gpu import Case
+
+    c = Case(len(q_lens), q_lens, [300 + 10 * n for n in q_lens], 16, 16, 4, 64, 32, "f16", lead=0, tail=0, spare_seqs=0)
+    kept = []
+    c.check(call=lambda att, out: kept.append((att, att.forward(c.q, c.cache, *c.lens, c.b.S, out=out))))
+    att = kept[0][0]
+    assert att.status() == rpa.RPA_OK
+    info, items = att.plan()
+    assert len({int(i[0]) for i in items[info[1]:]}) == unfolded
