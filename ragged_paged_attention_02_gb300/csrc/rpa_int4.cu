@@ -19,10 +19,13 @@
 //    each.  Bound by instructions more than by bytes (a key and kv head costs 17 issue slots at D 128, of the 25 that its bytes'
 //    time has), so as few warps as can feed the others issue copies.  (Warps that each copied for themselves took 25.)
 //    128 decodes of 512 to 16 k keys (32 query and 8 kv heads, D 128, groups of 64, 1245 MB): 225 us of the call's 234, 5.5 TB/s.
-//    16 decodes of a 4 k window (D 256, groups of 128, soft cap, 143 MB): 46 us of 54, 3.1 TB/s, with 12 warps an SM, whose 168
-//    registers hold q and the outputs: they issue 39 % of the time, waiting for matrix loads and products.  32 sequences of 1 to 5
-//    tokens (D 64, 35 MB, some keys in two or three tiles): 25 us of 39, issue 54 %.  4 decodes: 17 us a call, 8 of them
+//    16 decodes of a 4 k window (D 256, groups of 128, soft cap, 143 MB): 44 us of 52, 3.3 TB/s (64 of them 125 us, 4.5 TB/s): some
+//    45 instructions a key and warp, which 12 warps of 168 registers issue in 39 % of the cycles; three to five consumer warps,
+//    two or three CTAs an SM, and pieces of 4 to 13 stages all take 53 to 59 us.  32 sequences of 1 to 5
+//    tokens (D 64, 35 MB, some keys in two or three tiles): 25 us of 35, issue 54 %.  4 decodes: 17 us a call, 8 of them
 //    dependent loads and the planner's latency before the first product.
+//    Smaller groups cost more: a scale, a zero, a transposed P and its sum for each (16 decodes at D 256 as above: 52 us with groups of
+//    128, 70 of 64, 109 of 32, which spill).
 //  * long prompts would decode every key once for each tile.  Sequences with more tokens are unfolded instead, once a call, to
 //    f16 rows in the workspace, over which the tensor-memory prefill kernels run.  Three prompts of 0.8 to 2 k tokens on top
 //    of 4 to 16 k keys (32 and 8 heads, D 128): 529 us, 40 of them the rows (and q's rounding; 203 MB, 5.1 TB/s) and 468 the
@@ -63,13 +66,16 @@ struct I4Geom {
     static constexpr int KB = D + 8 * NG;             // bytes of a key
     static constexpr int STAGE = KS * KB;
     static constexpr int QB = R * D * 2;              // Q of an item
+    // D 256: Q's operands in shared memory, one copy for all warps (in registers they made the loop spill, 54 -> 52 us below)
+    static constexpr bool QSH = D == 256;
+    static constexpr int QF = QSH ? R * D * 2 : 0;
     static constexpr int LD = D + 4;                  // floats of a row of the merge area: rows of four lanes fall into different banks
     static constexpr int RED = CW * R * LD * 4;       // ... which lies in the item's last stage
     // resident CTAs that registers are allocated for, and stages: as many as fit beside them
     static constexpr int CTAS = D == 64 ? 4 : 2;
-    static constexpr int FIT = (227 * 1024 / CTAS - 3 * 1024 - QB) / STAGE;
+    static constexpr int FIT = (227 * 1024 / CTAS - 3 * 1024 - QB - QF) / STAGE;
     static constexpr int NS = FIT > 4 ? 4 : FIT;
-    static constexpr int SMEM = NS * STAGE + QB;
+    static constexpr int SMEM = NS * STAGE + QB + QF;
     static_assert(NS >= 2 && RED <= STAGE, "a ring; the merge area");
 };
 
@@ -123,7 +129,7 @@ __global__ void __launch_bounds__((I4Geom<D, NG>::THREADS), (I4Geom<D, NG>::CTAS
     constexpr int NS = Gm::NS, KS = Gm::KS, CW = Gm::CW, C = D / 32, SUBS = 2;  // C: 16-byte chunks of a row of codes
     constexpr int CPG = C / NG;                                               // ... of a group
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ __align__(8) uint64_t full_bar[NS], empty_bar[NS], merge_bar, q_full, q_empty;
+    __shared__ __align__(8) uint64_t full_bar[NS], empty_bar[NS], merge_bar, q_full, q_empty, q_shared;
     __shared__ __align__(16) int meta[NS][kMetaWords];
     __shared__ float red_ml[CW][R][2];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -140,6 +146,7 @@ __global__ void __launch_bounds__((I4Geom<D, NG>::THREADS), (I4Geom<D, NG>::CTAS
         mbar_init(smem_u32(&merge_bar), CW);
         mbar_init(smem_u32(&q_full), 1);
         mbar_init(smem_u32(&q_empty), CW);
+        mbar_init(smem_u32(&q_shared), CW);
         fence_mbar_init();
     }
     __syncthreads();
@@ -331,7 +338,8 @@ __global__ void __launch_bounds__((I4Geom<D, NG>::THREADS), (I4Geom<D, NG>::CTAS
     const uint32_t mb = smem_u32(&merge_bar);
     int s = 0;
     uint32_t ph = 0, mph = 0, qph = 0;
-    uint32_t qf[C][4];
+    uint32_t qf[Gm::QSH ? 1 : C][4];
+    uint4* const q_ops = reinterpret_cast<uint4*>(smem + NS * Gm::STAGE + Gm::QB) + lane;  // chunk c's at 32 c
     float qs[2][NG];          // sums of q over a group, times 2^-20
     float o_acc[C][2][4];     // [.][i][0, 1]: channel 32 c + 4 g + 2 i, rows 2t, 2t + 1, times 2^-24; [2, 3]: and 16 times the next channel
     float psum[NG][4];        // sums of P (rows 2t, 2t + 1, twice)
@@ -367,10 +375,14 @@ __global__ void __launch_bounds__((I4Geom<D, NG>::THREADS), (I4Geom<D, NG>::CTAS
             for (int c = 0; c < C; ++c) x[c] = live ? load_q8(qbuf, g * D + 8 * t + 32 * c, a.q_f16 == 0) : make_uint4(0, 0, 0, 0);
 #pragma unroll
             for (int c = 0; c < C; ++c) {
-                qf[c][0] = __byte_perm(x[c].x, x[c].z, 0x5410);  // channels 0, 4
-                qf[c][1] = __byte_perm(x[c].y, x[c].w, 0x5410);  // 2, 6
-                qf[c][2] = __byte_perm(x[c].x, x[c].z, 0x7632);  // 1, 5
-                qf[c][3] = __byte_perm(x[c].y, x[c].w, 0x7632);  // 3, 7
+                // channels 0, 4; 2, 6; 1, 5; 3, 7
+                const uint4 f = make_uint4(__byte_perm(x[c].x, x[c].z, 0x5410), __byte_perm(x[c].y, x[c].w, 0x5410),
+                                           __byte_perm(x[c].x, x[c].z, 0x7632), __byte_perm(x[c].y, x[c].w, 0x7632));
+                if constexpr (Gm::QSH) {
+                    if (c % CW == w) q_ops[32 * c] = f;  // (the last item's are free: its merge has seen every warp)
+                } else {
+                    qf[c][0] = f.x; qf[c][1] = f.y; qf[c][2] = f.z; qf[c][3] = f.w;
+                }
                 const uint32_t xs[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -401,6 +413,10 @@ __global__ void __launch_bounds__((I4Geom<D, NG>::THREADS), (I4Geom<D, NG>::CTAS
                 for (int i = 0; i < 2; ++i) o_acc[c][i][0] = o_acc[c][i][1] = o_acc[c][i][2] = o_acc[c][i][3] = 0.f;
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_u32(&q_empty));
+            if constexpr (Gm::QSH) {
+                if (lane == 0) mbar_arrive(smem_u32(&q_shared));
+                if (!mbar_wait(smem_u32(&q_shared), qph ^ 1u, ctrl, tmo)) return;
+            }
         }
         const int kw = m0.x + 32 * w;  // this warp's 32 keys
         if (kw < kv_end && kw + 32 > kv_begin) {
@@ -440,12 +456,15 @@ __global__ void __launch_bounds__((I4Geom<D, NG>::THREADS), (I4Geom<D, NG>::CTAS
                         const uint32_t u0 = f[2 * h], u1 = f[2 * h + 1], v0 = u0 >> 8, v1 = u1 >> 8;
                         const uint32_t ae[4] = {u0 & kLow, u1 & kLow, v0 & kLow, v1 & kLow};
                         const uint32_t ao[4] = {u0 & kHigh, u1 & kHigh, v0 & kHigh, v1 & kHigh};
+                        uint4 qv;
+                        if constexpr (Gm::QSH) qv = q_ops[32 * cc];
+                        else qv = make_uint4(qf[cc][0], qf[cc][1], qf[cc][2], qf[cc][3]);
                         if (cc % CPG == 0) {
-                            mma_first(e, ae, qf[cc][0], qf[cc][1]);
-                            mma_first(o, ao, qf[cc][2], qf[cc][3]);
+                            mma_first(e, ae, qv.x, qv.y);
+                            mma_first(o, ao, qv.z, qv.w);
                         } else {
-                            mma(e, ae, qf[cc][0], qf[cc][1]);
-                            mma(o, ao, qf[cc][2], qf[cc][3]);
+                            mma(e, ae, qv.x, qv.y);
+                            mma(o, ao, qv.z, qv.w);
                         }
                         if ((cc + 1) % CPG == 0) {
                             const int gi = cc / CPG;
