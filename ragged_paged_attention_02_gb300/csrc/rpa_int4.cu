@@ -19,10 +19,10 @@
 //    each.  Bound by instructions more than by bytes (a key and kv head costs 17 issue slots at D 128, of the 25 that its bytes'
 //    time has), so as few warps as can feed the others issue copies.  (Warps that each copied for themselves took 25.)
 //    128 decodes of 512 to 16 k keys (32 query and 8 kv heads, D 128, groups of 64, 1245 MB): 225 us of the call's 234, 5.5 TB/s.
-//    16 decodes of a 4 k window (D 256, groups of 128, soft cap, 143 MB): 44 us of 52, 3.3 TB/s (64 of them 125 us, 4.5 TB/s): some
+//    16 decodes of a 4 k window (D 256, groups of 128, soft cap, 143 MB): 43 us of 51, 3.4 TB/s (64 of them 125 us, 4.5 TB/s): some
 //    45 instructions a key and warp, which 12 warps of 168 registers issue in 39 % of the cycles; three to five consumer warps,
-//    two or three CTAs an SM, and pieces of 4 to 13 stages all take 53 to 59 us.  32 sequences of 1 to 5
-//    tokens (D 64, 35 MB, some keys in two or three tiles): 25 us of 35, issue 54 %.  4 decodes: 17 us a call, 8 of them
+//    two or three CTAs an SM, and pieces of 4 to 13 stages all took 53 to 59 us where this took 54.  32 sequences of 1 to 5
+//    tokens (D 64, 35 MB, some keys in two or three tiles): 24 us of 35, issue 54 %.  4 decodes: 17 us a call, 8 of them
 //    dependent loads and the planner's latency before the first product.
 //    Smaller groups cost more: a scale, a zero, a transposed P and its sum for each (16 decodes at D 256 as above: 52 us with groups of
 //    128, 70 of 64, 109 of 32, which spill).
@@ -72,7 +72,7 @@ struct I4Geom {
     static constexpr int LD = D + 4;                  // floats of a row of the merge area: rows of four lanes fall into different banks
     static constexpr int RED = CW * R * LD * 4;       // ... which lies in the item's last stage
     // resident CTAs that registers are allocated for, and stages: as many as fit beside them
-    static constexpr int CTAS = D == 64 ? 4 : 2;
+    static constexpr int CTAS = 2;
     static constexpr int FIT = (227 * 1024 / CTAS - 3 * 1024 - QB - QF) / STAGE;
     static constexpr int NS = FIT > 4 ? 4 : FIT;
     static constexpr int SMEM = NS * STAGE + QB + QF;

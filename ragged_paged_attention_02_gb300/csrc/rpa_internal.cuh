@@ -98,9 +98,12 @@ constexpr int kMlaDv = 512;
 constexpr int kMlaRows = 16;
 constexpr int kInt4Rows = 8;              // query rows of a tile of the 4-bit kernel
 constexpr int kInt4Waves = 4;             // target items per CTA
-constexpr int kInt4Stages = 5;            // stages of an item that make up for its start and end
-// consumer warps of its CTAs, each with 32 keys of a stage
-__host__ __device__ constexpr int int4_warps(int D) { return D == 64 ? 4 : D == 128 ? 7 : 5; }
+// keys of an item that make up for its start and end, as whole stages (32 sequences of 1 to 5 tokens, D 64: 768 keys 36.2 us, 1024
+// 34.4, 1280 33.5, and of one token 27.3, 26.5 and 28.9; D 256, 16 decodes: 800 keys 54.3, 960 52.6, 1120 53.2)
+constexpr int kInt4GoodKeys = 1024;
+// consumer warps of its CTAs (two an SM), each with 32 keys of a stage (D 64: four CTAs of four warps are slower, 128 decodes 56.9
+// for 54.4 us, 32 of them 30.6 for 26.5, sequences of 1 to 5 tokens alike; three of six or seven warps 10 % slower still)
+__host__ __device__ constexpr int int4_warps(int D) { return D == 64 ? 8 : D == 128 ? 7 : 5; }
 // 4-bit K/V: a sequence whose query rows a kv head number more than kInt4DirectRows + kInt4RowsByItems / n, at most kInt4FewRows, is
 // unfolded to f16, n being the (such sequence, kv head) pairs.  The direct kernel's time goes by rows; a prefill item takes its
 // keys' time (0.11 ms for 8 k) whatever its rows up to a tile, and its keys are not split, so few items leave SMs idle.  With

@@ -469,7 +469,7 @@ int enqueue_forward(const RpaCfg& c, const KernelSet& ks, const Workspace& ws, M
     pp.room_pages = ks.room_pages;
     pp.vbase = ws.vbase;
     pp.chunk_align = pp.int4 ? 32 * int4_warps(ks.D) : kChunkAlign;  // 4-bit K/V: whole stages
-    pp.good_chunk = pp.int4 ? kInt4Stages * pp.chunk_align : 0;
+    pp.good_chunk = pp.int4 ? (kInt4GoodKeys + pp.chunk_align / 2) / pp.chunk_align * pp.chunk_align : 0;
     pp.min_chunk = pp.int4 ? pp.chunk_align : kMinChunk;
     pp.pf_mma_rows = ks.tc ? 2 * kTcRows : ks.mla ? kMlaRows : kTcRows;
     pp.dec_on_pf = (ks.tc8 && !pp.int4) || ks.mla;
