@@ -218,3 +218,49 @@ def test_tokens_that_make_room(q_lens, unfolded):
     assert att.status() == rpa.RPA_OK
     info, items = att.plan()
     assert len({int(i[0]) for i in items[info[1]:]}) == unfolded
+
+
+def test_pages_past_four_gigabytes():
+    """The same calls over pages at the start and at the end of a cache of 5 GB, where byte offsets need more than 32 bits."""
+    b = Batch(np.random.default_rng(7), [1, 150, 3], [900, 600, 70], 64, 16, 8, 128, kv="int4_g128")
+    N = 72000
+    q, k, v = b.queries(), *(b.queries()[:, :8].contiguous() for _ in "kv")
+    big = torch.full((N, 8, 64 * (128 + 8)), 0x35, dtype=torch.uint8, device="cuda")
+    assert big.numel() > 2 ** 32 + 2 ** 29
+    cfg = dict(b.cfg(), total_num_pages=N)
+    rope, att = rpa.RopeAppend(**cfg), rpa.RaggedPagedAttention(**cfg, sliding_window=300, first_keys=10)
+    lens, table, cu = b.lens()
+    got = []
+    for at in (0, N - b.N):
+        t = table + at
+        big[at:at + b.N] = 0x35
+        qr = rope.append(q, k, v, big, lens, t, cu, b.S)
+        got.append((qr, att.forward(qr, big, lens, t, cu, b.S), *rope.read(big, lens, t, cu, b.S), big[at:at + b.N].clone()))
+        assert rope.status() == rpa.RPA_OK and att.status() == rpa.RPA_OK
+    assert all(torch.equal(x, y) for x, y in zip(*got))
+
+
+@pytest.mark.parametrize("kv,q_lens", [("int4_g64", [1, 120, 1, 7]), ("int4_g64", [1, 1, 1, 1]), ("fp8_e4m3", [1, 120, 1, 7])])
+def test_options_and_profile(kv, q_lens):
+    """Fewer CTAs than the chip has, one after the other, and with the kernels timed: the same results, but for where keys are cut."""
+    eight = dict(k_scale=0.05, v_scale=0.05) if kv == "fp8_e4m3" else {}
+    b = Batch(np.random.default_rng(8), q_lens, [2000, 900, 3, 1500], 16, 16, 4, 128, kv=kv, **eight)
+    cache = b.cache() if eight else int4_cache(b, 64)
+    q, lens = b.queries(), b.lens()
+    make = lambda: rpa.RaggedPagedAttention(**b.cfg(), sliding_window=800, first_keys=9)  # noqa: E731
+    want = make().forward(q, cache, *lens, b.S)
+    for options in ({rpa.RPA_OPT_DECODE_SMS: 3}, {rpa.RPA_OPT_PREFILL_SMS: 5, rpa.RPA_OPT_DECODE_SMS: 1}, {rpa.RPA_OPT_SERIAL: 1}, {rpa.RPA_OPT_PLAN_EARLY: 1}):
+        att = make()
+        for o, x in options.items():
+            att.set_option(o, x)
+        for _ in range(3):
+            got = att.forward(q, cache, *lens, b.S)
+            # P and o are rounded (2^-11 and 2^-8 of values below 4), at other running maxima where the cuts are others
+            assert att.status() == rpa.RPA_OK and (got.float() - want.float()).abs().max() <= 2.0 ** -5
+    att = make()
+    att.profile_begin(4)
+    for _ in range(4):
+        got = att.forward(q, cache, *lens, b.S)
+    ms = att.profile_read(4)
+    assert att.status() == rpa.RPA_OK and torch.equal(got, want)
+    assert np.isfinite(ms).all() and (np.asarray(ms) >= 0).all()
