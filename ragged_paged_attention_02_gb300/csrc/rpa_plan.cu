@@ -26,11 +26,11 @@
 // further back than they end has those first keys in front of its range (its piece
 // 0, when it is split).  Everything here is integer and deterministic.
 //
-// Bound by latency: 10 to 13 k cycles (5 to 7 us) for batches of 4 to 128 sequences, in a dozen phases of 250 to 2000 between
+// Bound by latency: 9 to 13 k cycles (5 to 7 us) for batches of 4 to 128 sequences, in a dozen phases of 250 to 2000 between
 // barriers (loads of the lengths 1400, sums and split 900, scans 1800, descriptors 1500 to 1900, sort 1000 to 2300, lists 1300 to
-// 3900 at 128 sequences).  Sums by the warp's add instruction (800 -> 600), no minimum where there is nothing to split (-500),
-// one fence instead of one a thread and none where no kernel polls the epoch (1700 -> 300 or 1500), no division for sequences
-// that are not split (5900 -> 3900 at 128 sequences).  Loops left rolled, for fewer instructions to fetch, took longer (+500).
+// 3100 at 128 sequences), where the code itself has to be fetched too (a quarter of the stalls behind the barriers').
+// Sums by the warp's add instruction (800 -> 600), no minimum where there is nothing to split (-500), one fence instead of one a thread and none where no kernel polls the epoch (1700 -> 300 or 1500), no division for sequences
+// that are not split (5900 -> 3100 at 128 sequences).  Loops left rolled, for fewer instructions to fetch, took longer (+500).
 #include "rpa_block.cuh"
 
 namespace rpa {
@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
     extern __shared__ __align__(16) unsigned long long s_keys[];  // kMaxSort keys, then sequence scratch
     __shared__ int s_scan[33 * 5];
     __shared__ unsigned long long s_red[64];
-    __shared__ int s_bad, s_long;             // bad lengths; a prefill unit of more keys than a decode piece
+    __shared__ int s_bad, s_long, s_tiled;    // bad lengths; a prefill unit of more keys than a decode piece; several tiles (4-bit K/V)
     __shared__ int s_split[2];                // prefill CTAs, decode CTAs
     __shared__ int s_taken;                   // pages of the room that are given away
     const int tid = threadIdx.x;
@@ -148,7 +148,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
     int* s_kl = s_q0 + S + 1;
     const int Tq = max(1, p.pf_tokens);  // query tokens per prefill tile
 
-    if (tid == 0) s_bad = s_taken = s_long = 0;
+    if (tid == 0) s_bad = s_taken = s_long = s_tiled = 0;
     __syncthreads();
 
     const bool room = p.int4 && p.room_pages > 0;
@@ -172,6 +172,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
                 key_band(kl, ql, 0, ql, p, lo, hi);
                 cls = 1;
                 cnt = hi - lo;
+                if (p.int4 && ql > p.dec_tokens) s_tiled = 1;
                 my_total += (unsigned long long)(cnt + first_cost(lo, p)) * (unsigned long long)(p.Hkv * dec_tiles(ql, p));
             } else {
                 cls = 2;
@@ -485,7 +486,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
         }
     }
     // ... of sequences of several tiles (4-bit K/V): a warp on one sequence at a time
-    if (p.int4 && n_dec > 0) {
+    if (s_tiled) {
         for (int s = tid >> 5; s < S; s += (int)blockDim.x >> 5) {
             const int ql = s_q0[s + 1] - s_q0[s];
             if (ql <= p.dec_tokens || s_cls[s] != 1 || s_cnt[s] <= chunk) continue;
@@ -528,7 +529,10 @@ __global__ void __launch_bounds__(kPlanThreads, 1) rpa_plan_kernel(PlanParams p)
 size_t plan_smem_bytes() { return sizeof(unsigned long long) * kMaxSort + sizeof(int) * kSeqArrays * (kSeqSmem + 1); }
 
 cudaError_t launch_plan(const PlanParams& p, cudaStream_t st, size_t smem) {
-    return launch_pdl(rpa_plan_kernel, 1, kPlanThreads, smem, st, p);
+    // few sequences and tokens, so few units: half the threads get through the barriers and scans sooner (9.9 -> 8.9 k cycles with 4
+    // decodes, 10.7 -> 9.5 k with 16; 32 sequences of 223 units 12.2 -> 12.8 k)
+    const int threads = p.num_seqs <= 16 && p.T <= 512 ? kPlanThreads / 2 : kPlanThreads;
+    return launch_pdl(rpa_plan_kernel, 1, threads, smem, st, p);
 }
 
 cudaError_t plan_prepare() {
