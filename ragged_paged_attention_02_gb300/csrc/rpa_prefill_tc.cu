@@ -184,6 +184,7 @@ __global__ void __launch_bounds__(kThreads, 1) rpa_prefill_tc(const __grid_const
             const int q_start = a.cu_q_lens[item.seq];
             const int ql = a.cu_q_lens[item.seq + 1] - q_start;
             const int kl = a.kv_lens[item.seq];
+            // (plain loads: over a 4-bit cache the table is what the kernel before wrote, while this one may already have started)
             const int* ptab = a.page_indices + (size_t)page_row(a, item.seq) * a.P;
             const int key0 = item.kv_begin - (item.kv_begin & (BR - 1));
             const int nt0 = first_tiles(a, item, kBN);  // tiles of the first keys
@@ -217,7 +218,7 @@ __global__ void __launch_bounds__(kThreads, 1) rpa_prefill_tc(const __grid_const
             }
             qph ^= 1u;
             int win0 = (nt0 ? 0 : key0) / ps;
-            int win = (win0 + lane < a.P) ? __ldg(ptab + win0 + lane) : 0;
+            int win = (win0 + lane < a.P) ? ptab[win0 + lane] : 0;
             for (int t = 0; t < nt && ok; ++t) {
                 const bool ft = t < nt0;
                 const int k_tile = ft ? t * kBN : key0 + (t - nt0) * kBN;
@@ -225,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) rpa_prefill_tc(const __grid_const
                 const int lp_last = min(k_tile + kBN - 1, kv_end - 1) / ps;
                 if (lp_last - win0 >= 32) {
                     win0 = k_tile / ps;
-                    win = (win0 + lane < a.P) ? __ldg(ptab + win0 + lane) : 0;
+                    win = (win0 + lane < a.P) ? ptab[win0 + lane] : 0;
                 }
                 if (!mbar_wait(smem_u32(&kv_empty[s]), ph ^ 1u, ctrl, tmo)) {
                     ok = false;
