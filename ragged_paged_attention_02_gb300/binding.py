@@ -215,7 +215,7 @@ def make_cfg(*, num_q_tokens, num_q_heads, num_kv_heads, head_dim, total_num_pag
     c.has_v_scale, c.v_scale = (0, 1.0) if v_scale is None else (1, float(v_scale))
     c.is_causal = 1 if is_causal else 0
     c.has_sliding_window, c.sliding_window = (0, 0) if sliding_window is None else (1, int(sliding_window))
-    c.first_keys = int(first_keys or 0)
+    c.first_keys = max(-1, min(int(first_keys or 0), 2 ** 31 - 1))  # (more than any sequence has is all of them)
     ptr = _sinks_pointer(sinks, _host_ok)
     c.has_sinks, c.sinks = (0, None) if ptr is None else (1, ptr)
     c.kv_layout = KV_LAYOUTS[kv_layout]

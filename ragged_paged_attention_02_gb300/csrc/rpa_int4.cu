@@ -188,8 +188,8 @@ __global__ void __launch_bounds__((I4Geom<D, NG>::THREADS), (I4Geom<D, NG>::CTAS
             x.nst = max(1, x.nst0 + (x.hi > x.lo ? (x.hi - key0 + KS - 1) / KS : 0));
             x.win0 = p.page.div(x.nst0 ? 0 : key0);
             const int* ids = a.page_indices + (size_t)x.item.seq * a.P + x.win0 + lane;
-            x.win = (x.win0 + lane < a.P) ? __ldg(ids) : 0;
-            x.win2 = (x.win0 + 32 + lane < a.P) ? __ldg(ids + 32) : 0;
+            x.win = (x.win0 + lane < a.P) ? ids[0] : 0;
+            x.win2 = (x.win0 + 32 + lane < a.P) ? ids[32] : 0;
         };
         // the first item is the CTA's own, its unit on its way with the number of items (where there is none of that number, what
         // the list holds there is not used); the others come off a counter
@@ -231,8 +231,8 @@ __global__ void __launch_bounds__((I4Geom<D, NG>::THREADS), (I4Geom<D, NG>::CTAS
                 const int lp_last = p.page.div(max(k_stage, min(k_stage + KS, kv_end) - 1));
                 if (lp_last - win0 >= 64) {
                     win0 = p.page.div(k_stage);
-                    win = (win0 + lane < a.P) ? __ldg(ptab + win0 + lane) : 0;
-                    win2 = (win0 + 32 + lane < a.P) ? __ldg(ptab + win0 + 32 + lane) : 0;
+                    win = (win0 + lane < a.P) ? ptab[win0 + lane] : 0;
+                    win2 = (win0 + 32 + lane < a.P) ? ptab[win0 + 32 + lane] : 0;
                 }
                 if (!mbar_wait(smem_u32(&empty_bar[s]), ph ^ 1u, ctrl, tmo)) {
                     ok = false;

@@ -42,3 +42,8 @@ def test_operators_without_a_window_refuse_it():
     assert rpa.validate_evict_cfg(budget=32, **cfg) == rpa.RPA_ERR_UNSUPPORTED
     assert rpa.validate_evict_cfg(budget=32, **dict(BASE, sliding_window=8)) == rpa.RPA_OK
     assert rpa.validate_rope_cfg(**cfg) == rpa.RPA_OK  # writes rows: no attention
+
+
+def test_numbers_past_32_bits_do_not_wrap():
+    assert rpa.make_cfg(**dict(BASE, sliding_window=8, first_keys=2 ** 32 + 5)).first_keys == 2 ** 31 - 1
+    assert rpa.validate_cfg(**dict(BASE, sliding_window=8, first_keys=-2 ** 32)) == rpa.RPA_ERR_INVALID_ARG
