@@ -77,6 +77,9 @@ __global__ void __launch_bounds__(kCombThreads, kCombCtasPerSm) rpa_combine_kern
                 if (k < 32) sc_mine = sc;
                 L += sc * w.y;
             }
+        } else {
+            // nothing is visible, or every visible logit is a NaN (no maximum takes one): then a piece's sum is too
+            for (int k = lane; k < pieces; k += 32) L += ml[(size_t)k * PR * 2 + 1];
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
@@ -84,7 +87,9 @@ __global__ void __launch_bounds__(kCombThreads, kCombCtasPerSm) rpa_combine_kern
         L = add_sink(L, p.sinks, qh, M);  // the sink joins once, over all pieces
         const float inv = L > 0.f ? p.v_scale / L : 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (M != -INFINITY) {
+        if (M == -INFINITY) {
+            if (L != L) acc = make_float4(L, L, L, L);
+        } else {
             if (held) {
 #pragma unroll
                 for (int k = 0; k < kBatch; ++k) {

@@ -678,6 +678,11 @@ __global__ void __launch_bounds__((I4Geom<D, NG>::THREADS), (I4Geom<D, NG>::CTAS
                     o.z += sc * v.z;
                     o.w += sc * v.w;
                 }
+            } else {
+                // nothing is visible, or every visible logit is a NaN (no maximum takes one): then a sum is too
+#pragma unroll
+                for (int i = 0; i < CW; ++i) L += red_ml[i][r][1];
+                if (L != L) o = make_float4(L, L, L, L);
             }
             if (part < 0) {
                 const int tok = m2.y + r / G, qh = m2.x + hr;
