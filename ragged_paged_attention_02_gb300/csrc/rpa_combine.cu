@@ -84,6 +84,7 @@ __global__ void __launch_bounds__(kCombThreads, kCombCtasPerSm) rpa_combine_kern
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
         const int qh = kvh * p.heads + h0 + r % G;
+        const float top = p.most * L;  // (without keys 0 or a NaN, which nothing passes)
         L = add_sink(L, p.sinks, qh, M);  // the sink joins once, over all pieces
         const float inv = L > 0.f ? p.v_scale / L : 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -126,6 +127,7 @@ __global__ void __launch_bounds__(kCombThreads, kCombCtasPerSm) rpa_combine_kern
                 }
             }
         }
+        acc = make_float4(acc.x > top ? top : acc.x, acc.y > top ? top : acc.y, acc.z > top ? top : acc.z, acc.w > top ? top : acc.w);
         if (act)
             store_o4(p.o, ((size_t)(q0 + r / G) * Hq + qh) * D + 4 * c4, acc.x * inv, acc.y * inv, acc.z * inv,
                      acc.w * inv, p.odt);

@@ -686,6 +686,8 @@ __global__ void __launch_bounds__((I4Geom<D, NG>::THREADS), (I4Geom<D, NG>::CTAS
             }
             if (part < 0) {
                 const int tok = m2.y + r / G, qh = m2.x + hr;
+                const float top = kMostHalf * L;  // values end at 65504 here as they do in f16 rows
+                o = make_float4(o.x > top ? top : o.x, o.y > top ? top : o.y, o.z > top ? top : o.z, o.w > top ? top : o.w);
                 L = add_sink(L, a.sinks, qh, M);
                 const float inv = L > 0.f ? a.v_scale / L : 0.f;
                 store_o4(a.o, ((size_t)tok * Hq + qh) * D + c, o.x * inv, o.y * inv, o.z * inv, o.w * inv, a.odt);
@@ -799,11 +801,7 @@ __global__ void __launch_bounds__(kUnfoldThreads, kUnfoldCtas) rpa_int4_unfold(c
                         const float2 sz = f16x2_to_f32x2(pairs[b][is_v]);
                         float f[16];
                         int4_values(codes[b][is_v], sz, f);
-                        // the greatest code of a group that ends at f16's largest value may pass it by the scale's rounding
-                        if (fmaf(15.f, sz.x, sz.y) > 65504.f) {
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) f[k] = f[k] > 65504.f ? 65504.f : f[k];
-                        }
+                        int4_saturate(sz, f);
 #pragma unroll
                         for (int k = 0; k < 8; ++k) out[k] = pack2<true>(f[2 * k], f[2 * k + 1]);
                     }

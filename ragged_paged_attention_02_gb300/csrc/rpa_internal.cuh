@@ -251,6 +251,7 @@ struct CombParams {
     int num_seqs, T, Hq, G, D;
     int rows_max;  // most rows of a combine entry (the decode tile's rows)
     int part_rows;      // rows of a partial slot
+    float most;         // the greatest mean of values before v_scale (infinity but for 4-bit K/V, whose values end at 65504)
     int blocks, heads;  // entries' heads a kv head makes, and its query heads (one, and G, but for 4-bit K/V: its last may have fewer)
     float v_scale;
     const float* sinks;  // [Hq] sink logits (natural-log domain), or nullptr
@@ -628,6 +629,15 @@ __device__ __forceinline__ void int4_values(uint2 codes, float2 sz, float* f) {
             const uint64_t c = f32x2(__uint_as_float(__byte_perm(lo, 0x4b000000u, 0x7540 + i)), __uint_as_float(__byte_perm(hi, 0x4b000000u, 0x7540 + i)));
             f32x2_split(ffma2(fadd2(c, back), s2, z2), f[8 * k + 2 * i], f[8 * k + 2 * i + 1]);
         }
+    }
+}
+// The scale of a group that ends at float16's largest value is rounded up, so that its greatest code stands for up to 65536: what
+// becomes float16 ends at 65504 (a NaN stays one).
+constexpr float kMostHalf = 65504.f;
+__device__ __forceinline__ void int4_saturate(float2 sz, float* f) {
+    if (fmaf(15.f, sz.x, sz.y) > kMostHalf) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) f[i] = f[i] > kMostHalf ? kMostHalf : f[i];
     }
 }
 // Two bf16 (one word) -> f16x2, round to nearest even

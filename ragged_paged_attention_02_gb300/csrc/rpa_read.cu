@@ -13,6 +13,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 #include "rpa_internal.cuh"
 
 namespace rpa {
@@ -196,6 +198,7 @@ __global__ void __launch_bounds__(kReadThreads, kReadCtas) rpa_read_kernel(const
                     const bool is_v = r + b >= p.Hkv;
                     float f[16];
                     widen<MODE>(x[b], p.kt, f);
+                    if constexpr (MODE == kRead4 && std::is_same<QT, __half>::value) int4_saturate(f16x2_to_f32x2(x[b].scale_zero), f);
                     const float sc = is_v ? p.v_scale : p.k_scale;
                     if (sc != 1.f) {
 #pragma unroll
