@@ -378,8 +378,9 @@ int rpa_rope_create(const RpaRopeCfg* cfg, RpaRope** out);
  *              contiguous too, and overlaps none of the other tensors
  * The arithmetic is in 32 bits with one rounding at the end.  The angle of position p is p w_i, w_i as
  * rpa_rope_frequencies gives it, modulo a turn, exact to 2^-32 of a turn at any position; the sine then
- * takes it as a 32-bit float, within 2^-26 of a turn near half a turn and exact near 0 (keys of a 4-bit cache are rotated in pairs of
- * floats, the sines within 2^-30: a value next to the border of two codes takes the right one).  Cache rows hold k / k_scale and v / v_scale (where set), rounded to nearest even;
+ * takes it as a 32-bit float, within 2^-26 of a turn near half a turn and exact near 0 (values of a 4-bit cache are rotated and
+ * divided by its scales in pairs of floats: a value next to the border of two codes takes the right one, but within 2^-45 of the
+ * value behind a division, 2^-29 of its pair's size behind a rotation).  Cache rows hold k / k_scale and v / v_scale (where set), rounded to nearest even;
  * the 8-bit types saturate, NaN stays NaN (int8: 0); f16 rows overflow to infinity.  4-bit rows: values saturate at
  * +-65504; a group's zero is its least value rounded down to f16, its scale (greatest - zero) / 15 rounded up to f16, a
  * code (value - zero) / scale rounded to nearest even, at most 15; a group with a NaN reads as NaN.

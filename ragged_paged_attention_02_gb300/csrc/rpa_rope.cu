@@ -27,12 +27,12 @@
 // measured copy.  Five CTAs an SM with two rows in flight a thread, when that took 61 us: four CTAs 63 us with two rows,
 // 64 with four (spilled); one token a CTA 79 to 87 us.
 //
-// Rows of a 4-bit cache.  k is rotated in pairs of floats (sines by Taylor series, within 2^-30) and a group's zero, scale and codes
-// are rounded from the exact sums, so that the codes are those of the formula's real values but for values within 2^-30 of a border
-// (with 32-bit sines some next to a border were others).  A row's threads exchange it through shared memory, 16 neighbouring
+// Rows of a 4-bit cache.  k is rotated in pairs of floats (sines by Taylor series, within 2^-30), k and v are divided by the cache's
+// scales into pairs (within 2^-45), and a group's zero, scale and codes are rounded from the pairs' sums, so that they are those of the
+// formula's real values but next to a border by as much (from 32-bit values some were others, most where a group lies far from zero).  A row's threads exchange it through shared memory, 16 neighbouring
 // channels each, and form a group's extremes by shuffles.  Bound by instructions: 4.4 k tokens of 32 q and 8 kv heads at D 128 (groups
-// of 32, 120 MB with the rows read back by the call behind) take 32 us, and the two calls 38.  One copy of the coding loop for q, K
-// and V rows with the next row's loads in flight (57 -> 38 us: unrolled by kind it did not stay in the instruction cache); three
+// of 32, 120 MB with the rows read back by the call behind) take 33 us, and the two calls 39 (one us of it for the lower halves in every code's sum).  One copy of the coding loop for q, K
+// and V rows with the next row's loads in flight (57 -> 38 us then: unrolled by kind it did not stay in the instruction cache); three
 // CTAs an SM of 12 tokens a round (80 registers; with four the loop spilled, 53 us); codes from the reciprocal of the
 // scale, and the exact remainder only for those next to a border (no divisions).
 #include <cuda_bf16.h>
@@ -270,7 +270,8 @@ __device__ __forceinline__ void store_int4(const RopeParams& p, const float* y, 
     };
     float x[16], xl[16];
     exchange(y, x);
-    if (!is_v) {
+    const bool pairs = !is_v || p.has_vs;  // V as it came has no lower halves
+    if (pairs) {
         exchange(yl, xl);
     } else {
 #pragma unroll
@@ -287,17 +288,17 @@ __device__ __forceinline__ void store_int4(const RopeParams& p, const float* y, 
         lo = min_nan(lo, l, l);
         hi = max_nan(hi, h2, h2);
     }
-    if (lo < -65504.f || hi > 65504.f) {  // (all of a group's threads)
+    if (lo <= -65504.f || hi >= 65504.f) {  // (all of a group's threads)
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-            if (fabsf(x[i]) >= 65504.f) xl[i] = 0.f;
+            if (fabsf(x[i]) > 65504.f || (fabsf(x[i]) == 65504.f && x[i] * xl[i] > 0.f)) xl[i] = 0.f;
             x[i] = fminf(fmaxf(x[i], -65504.f), 65504.f);
         }
         lo = fminf(fmaxf(lo, -65504.f), 65504.f);
         hi = fminf(fmaxf(hi, -65504.f), 65504.f);
     }
     float lol = 0.f, hil = 0.f;  // what the extremes' own rounding left
-    if (!is_v) {
+    if (pairs) {
         lol = INFINITY;
         hil = -INFINITY;
 #pragma unroll
@@ -315,7 +316,7 @@ __device__ __forceinline__ void store_int4(const RopeParams& p, const float* y, 
     const float z = __half2float(zero);
     float dh, dl;
     two_sum(hi, -z, dh, dl);
-    dl += hil;
+    two_sum(dh, dl + hil, dh, dl);  // (far from zero a value's lower half is no small part of the group's range)
     __half scale = __float2half_ru(__fdiv_rn(dh, 15.f));
     {
         const float c = 15.f * __half2float(scale), b = 15.f * __half2float(next_half(scale, false));  // (exact)
@@ -323,7 +324,7 @@ __device__ __forceinline__ void store_int4(const RopeParams& p, const float* y, 
         else if (b >= 0.f && (b > dh || (b == dh && dl <= 0.f))) scale = next_half(scale, false);
     }
     const float s = __half2float(scale), inv = __frcp_rn(s);
-    // The quotient's nearest integer, to even: of x (1 / s), off by less than 2^-17 for codes up to 15, unless one of the
+    // The quotient's nearest integer, to even: of (x - z + xl) (1 / s), off by less than 2^-17 for codes up to 15, unless one of the
     // thread's lies so near the middle of two that only the exact remainder says which.  (1.5 2^23 leaves a sum's integer in its low
     // bits, which are collected with their factors 16^i; what that constant's own bits add comes off at the end.)
     constexpr float kMagic = 12582912.f;
@@ -333,7 +334,7 @@ __device__ __forceinline__ void store_int4(const RopeParams& p, const float* y, 
     const uint64_t nz2 = f32x2(-z, -z), inv2 = f32x2(inv, inv), magic2 = f32x2(kMagic, kMagic), back2 = f32x2(-kMagic, -kMagic);
 #pragma unroll
     for (int i = 0; i < 16; i += 2) {
-        const uint64_t t = fmul2(fadd2(f32x2(x[i], x[i + 1]), nz2), inv2), n = fadd2(t, magic2);
+        const uint64_t t = fmul2(fadd2(fadd2(f32x2(x[i], x[i + 1]), nz2), f32x2(xl[i], xl[i + 1])), inv2), n = fadd2(t, magic2);
         float r0, r1, t0, t1, n0, n1;
         f32x2_split(fadd2(n, back2), r0, r1);
         f32x2_split(t, t0, t1);
@@ -350,7 +351,7 @@ __device__ __forceinline__ void store_int4(const RopeParams& p, const float* y, 
             // what r steps leave of the difference, exactly, against half a step
             float d, e;
             two_sum(x[i], -z, d, e);
-            e += xl[i];
+            two_sum(d, e + xl[i], d, e);
             const float r = rintf(d * inv), left = fmaf(-r, s, d), up = (left - 0.5f * s) + e, down = (left + 0.5f * s) + e;
             int c = r == r ? (int)r : 0;
             const bool odd = c & 1;
@@ -543,10 +544,15 @@ __global__ void __launch_bounds__(kRopeThreads, INT4 ? kRopeCtas4 : kRopeCtas) r
                                     if (is_v ? p.has_vs : p.has_ks) {
                                         const float sc = is_v ? p.v_scale : p.k_scale;
             #pragma unroll
-                                        for (int i = 0; i < 16; ++i) y[i] = __fdiv_rn(y[i], sc);
-                                        if constexpr (INT4) {
-            #pragma unroll
-                                            for (int i = 0; i < 16; ++i) yl[i] = 0.f;
+                                        for (int i = 0; i < 16; ++i) {
+                                            const float u = y[i], quotient = __fdiv_rn(u, sc);
+                                            if constexpr (INT4) {
+                                                // (what the quotient's rounding left is a value's lower half too)
+                                                const float rest = (fmaf(-quotient, sc, u) + yl[i]) * __frcp_rn(sc);
+                                                quick_sum(quotient, fabsf(quotient) < INFINITY && fabsf(rest) < INFINITY ? rest : 0.f, y[i], yl[i]);
+                                            } else {
+                                                y[i] = quotient;
+                                            }
                                         }
                                     }
                                     if constexpr (INT4) {
