@@ -74,8 +74,8 @@ typedef enum RpaDtype {
  * themselves, with probabilities times scales rounded to f16 (those below 2^-14 to a multiple of 2^-24: v_scale keeps small
  * values away from there).  A sequence of many tokens (more than 64 to 448 query rows a kv head, by how many such there are) is
  * computed from its K and V as f16 values instead, which the call writes to the workspace: the handle has room for
- * 1 GiB of them, or for one sequence of the most keys that fit into kv_pages (up to 8 GiB), if that is more, and none where
- * num_q_tokens <= max_num_seqs or no call of num_q_tokens can have such a sequence.  Sequences without room are computed from the codes, more slowly.
+ * 1 GiB of them, or for one sequence of the most keys that fit into kv_pages (up to 8 GiB), if that is more; half of that, half
+ * again and so on where rpa_create cannot allocate it; and none where num_q_tokens <= max_num_seqs or no call of num_q_tokens can have such a sequence.  Sequences without room are computed from the codes, more slowly.
  * A query row that sees a NaN logit comes out as NaN, whichever way it is computed. */
 
 typedef enum RpaStatus {

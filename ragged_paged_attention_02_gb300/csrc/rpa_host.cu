@@ -175,11 +175,15 @@ int rpa_create(const RpaCfg* cfg, RpaHandle** out) {
         delete h;
         return RPA_ERR_CUDA;
     }
-    h->ws_bytes = workspace_bytes(c, h->ks);
-    if (cudaMalloc(&h->ws, h->ws_bytes) != cudaSuccess) {
+    // (a 4-bit cache's room for f16 rows only makes prompts faster: as much of it as can be had)
+    for (;; h->ks.room_pages /= 2) {
+        h->ws_bytes = workspace_bytes(c, h->ks);
+        if (cudaMalloc(&h->ws, h->ws_bytes) == cudaSuccess) break;
         cudaGetLastError();
-        delete h;
-        return RPA_ERR_CUDA;
+        if (h->ks.room_pages == 0) {
+            delete h;
+            return RPA_ERR_CUDA;
+        }
     }
     if (h->can_concurrent && (cudaStreamCreateWithFlags(&h->side, cudaStreamNonBlocking) != cudaSuccess ||
                               cudaEventCreateWithFlags(&h->ev_plan, cudaEventDisableTiming) != cudaSuccess ||
