@@ -259,9 +259,10 @@ typedef enum RpaOption {
                                       while the kernel before it (typically the previous call's
                                       combine) still runs.  Default 0: it first waits for that kernel.  A 4-bit
                                       cache's planner always waits where the handle has room for f16 rows */
-    RPA_OPT_TEST_STALL_PRODUCER = 100  /* test hook, 1: the decode kernel's copy warp issues nothing, so
-                                      that its consumers' bounded waits run out (status
-                                      RPA_ERR_TIMEOUT); the kernel still returns */
+    RPA_OPT_TEST_STALL_PRODUCER = 100  /* test hook, 1: the copy warps of the decode kernel and of the 4-bit
+                                      cache's issue nothing, so that their consumers' bounded waits run
+                                      out (status RPA_ERR_TIMEOUT); n > 1: they give up before their n-th
+                                      stage, as if a wait of theirs had run out.  The kernel still returns */
 } RpaOption;
 
 /* Set option `option` of h to `value` for the following calls.  Host only.

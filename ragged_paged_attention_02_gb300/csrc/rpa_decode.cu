@@ -125,12 +125,12 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kvmap, const CUte
 
     if (warp == kCW) {
         // =============================== producer ===============================
-        if (p.debug_stall) return;  // test hook: consumers must time out
+        if (p.debug_stall == 1) return;  // test hook: consumers must time out
         const int BR = p.BR, ps = a.ps;
         const int runs = kKS / BR;  // page runs per stage, one bulk copy each (K and V of the head)
         const uint32_t run_bytes = (uint32_t)(2 * Gm::DH * BR * 128);
         const uint64_t pol_stream = l2_policy_evict_first();
-        int s = 0;
+        int s = 0, filled = 0;
         uint32_t ph = 0;
         int it = 0;
         if (lane == 0) it = atomicAdd(ctrl + a.counter_word, 1);
@@ -160,7 +160,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kvmap, const CUte
                     win0 = k_stage / ps;
                     win = (win0 + lane < a.P) ? __ldg(ptab + win0 + lane) : 0;
                 }
-                if (!mbar_wait(smem_u32(&empty_bar[s]), ph ^ 1u, ctrl, tmo)) {
+                if (!mbar_wait(smem_u32(&empty_bar[s]), ph ^ 1u, ctrl, tmo) || (p.debug_stall && ++filled == p.debug_stall)) {
                     ok = false;
                     break;
                 }
@@ -226,7 +226,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kvmap, const CUte
             }
         } else {
             // gave up: let the copies already issued land before leaving
-            for (int i = 0; i < kNS; ++i) mbar_wait(smem_u32(&full_bar[i]), 0, ctrl, tmo);
+            drain_ring(full_bar, kNS, s, ph, ctrl, tmo);
         }
         return;
     }

@@ -51,7 +51,7 @@ struct I4Params {
     uint32_t block;          // bytes of a page's block
     FastDiv page;            // by the page size
     int most_items;          // that the list has room for
-    int stall;               // test hook: no copies are issued
+    int stall;               // test hook (RPA_OPT_TEST_STALL_PRODUCER)
     unsigned long long timeout_ns;
 };
 
@@ -156,11 +156,11 @@ __global__ void __launch_bounds__((I4Geom<D, NG>::THREADS), (I4Geom<D, NG>::CTAS
 
     if (warp == CW) {
         // =============================== producer ===============================
-        if (p.stall) return;
+        if (p.stall == 1) return;
         const int ps = a.ps, runs = KS / BR;
         // K/V is read once, unless several blocks of query heads share it
         const uint64_t pol = p.blocks > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
-        int s = 0;
+        int s = 0, filled = 0;
         uint32_t ph = 0, qph = 0;
         // An item, and the next one's description, which is fetched while this one's keys are on their way: its number, then its
         // unit, then its lengths, then its first page ids, each a stage after what it depends on.
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__((I4Geom<D, NG>::THREADS), (I4Geom<D, NG>::CTAS
                     win = (win0 + lane < a.P) ? ptab[win0 + lane] : 0;
                     win2 = (win0 + 32 + lane < a.P) ? ptab[win0 + 32 + lane] : 0;
                 }
-                if (!mbar_wait(smem_u32(&empty_bar[s]), ph ^ 1u, ctrl, tmo)) {
+                if (!mbar_wait(smem_u32(&empty_bar[s]), ph ^ 1u, ctrl, tmo) || (p.stall && ++filled == p.stall)) {
                     ok = false;
                     break;
                 }
@@ -325,8 +325,8 @@ __global__ void __launch_bounds__((I4Geom<D, NG>::THREADS), (I4Geom<D, NG>::CTAS
             }
         } else {
             // gave up: let the copies already issued land before leaving
-            for (int i = 0; i < NS; ++i) mbar_wait(smem_u32(&full_bar[i]), 0, ctrl, tmo);
-            mbar_wait(smem_u32(&q_full), 0, ctrl, tmo);
+            drain_ring(full_bar, NS, s, ph, ctrl, tmo);
+            drain_ring(&q_full, 1, 0, qph, ctrl, tmo);
         }
         return;
     }

@@ -230,7 +230,7 @@ struct DecParams {
     int BR;                 // keys per copied page run: gcd(page_size, 64), >= 4
     int br_shift;           // log2(BR)
     int Tt;                 // query tokens per Q copy: 16 / G
-    int debug_stall;        // test hook: the producer issues nothing
+    int debug_stall;        // test hook (RPA_OPT_TEST_STALL_PRODUCER)
     unsigned long long timeout_ns;  // bound of every mbarrier wait
     // >= 0: launched behind the prefill kernel on the same stream (concurrent decode / prefill):
     // the CTAs wait for ctrl[kPlanEpoch] to reach this call's epoch instead of the grid dependency
@@ -786,6 +786,13 @@ __device__ __forceinline__ bool mbar_wait(uint32_t bar, uint32_t parity, int* ct
             return false;
         }
     }
+}
+// A producer that gives up leaves when the copies that it has issued have landed.  Of its ring of n stages the next to be filled is s,
+// in a round of parity ph: those before it were last filled in this round, the others in the one before, whose parity a barrier that
+// was never filled has behind it too.
+__device__ __forceinline__ void drain_ring(const uint64_t* full, int n, int s, uint32_t ph, int* ctrl, uint64_t timeout_ns) {
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) mbar_wait(smem_u32(full + i), i < s ? ph : ph ^ 1u, ctrl, timeout_ns);
 }
 // Wait for *flag (written by another kernel, released with a fence) to equal v, giving up after
 // timeout_ns: then the status word gets RPA_ERR_TIMEOUT and false is returned.

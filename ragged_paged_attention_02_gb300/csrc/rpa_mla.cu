@@ -230,8 +230,8 @@ __global__ void __launch_bounds__(kMlaThreads, 1) rpa_mla_attn(const __grid_cons
             }
         } else {
             // gave up: let the copies already issued land before leaving
-            for (int i = 0; i < kNS; ++i) mbar_wait(smem_u32(&full_bar[i]), 0, ctrl, tmo);
-            for (int i = 0; i < 2; ++i) mbar_wait(smem_u32(&q_full[i]), 0, ctrl, tmo);
+            drain_ring(full_bar, kNS, s, ph, ctrl, tmo);
+            drain_ring(q_full, 2, qb, qph, ctrl, tmo);
         }
         return;
     }
