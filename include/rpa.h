@@ -65,7 +65,7 @@ typedef enum RpaDtype {
  *   V codes        alike
  *   K scale, zero  [page_size][D / group] pairs of f16
  *   V scale, zero  alike
- * (page_size a multiple of 4 as ever, and at most 65536)
+ * (page_size a multiple of 4 as ever, and at most 65536; pages_per_seq * page_size at most 2^31 - 1024)
  * and a channel's value is  code * scale + zero  of its group (times k_scale or v_scale).  The scale of a group whose greatest
  * value is near 65504 is rounded up too, so that its code 15 may stand for up to 65536: rpa_forward, and rpa_rope_read into f16,
  * take such a value as 65504.  rpa_rope_append writes

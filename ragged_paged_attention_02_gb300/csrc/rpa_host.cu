@@ -143,7 +143,8 @@ int rpa_validate_cfg(const RpaCfg* c) {
         c->kv_dtype != RPA_DT_FP8_E5M2 && c->kv_dtype != RPA_DT_INT8 &&
         !(int4_group(c->kv_dtype) && int4_group(c->kv_dtype) <= c->head_dim))
         return RPA_ERR_UNSUPPORTED;
-    if (int4_group(c->kv_dtype) && c->page_size > 65536) return RPA_ERR_UNSUPPORTED;  // 32-bit offsets in a block
+    // 32-bit offsets in a block, and 32-bit numbers of the keys of a stage or page of 64 past a sequence's last
+    if (int4_group(c->kv_dtype) && (c->page_size > 65536 || c->pages_per_seq * c->page_size > lim - 1024)) return RPA_ERR_UNSUPPORTED;
     // masked keys get weight exactly 0 only if the additive mask value is huge and negative
     if (!(c->mask_value <= -1e30f)) return RPA_ERR_UNSUPPORTED;
     return RPA_OK;
