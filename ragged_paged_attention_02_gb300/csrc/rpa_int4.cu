@@ -740,12 +740,7 @@ __global__ void __launch_bounds__(kUnfoldThreads, kUnfoldCtas) rpa_int4_unfold(c
         const int v = task / p.Hkv, h = task - v * p.Hkv;
         int s = 0;
         if (few) {
-            int e = p.S;  // the last sequence whose pages start at or before v
-            while (e - s > 1) {
-                const int m = (s + e) / 2;
-                if (s_base[m] <= v) s = m;
-                else e = m;
-            }
+            s = last_start(s_base, p.S, v);  // the last sequence whose pages start at or before v
         } else {
             __syncthreads();
             if (tid < 32) {

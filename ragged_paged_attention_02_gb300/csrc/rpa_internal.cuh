@@ -719,6 +719,16 @@ __device__ __forceinline__ int find_seq(const int* cu, int S, int t, int lane) {
     }
     return lo < S && cu[lo] <= t && t < cu[lo + 1] ? lo : -1;
 }
+// The last of n ascending starts (in shared memory) that is at or before t (0 where none is); a thread's.
+__device__ __forceinline__ int last_start(const int* starts, int n, int t) {
+    int s = 0;
+    while (n - s > 1) {
+        const int m = (s + n) / 2;
+        if (starts[m] <= t) s = m;
+        else n = m;
+    }
+    return s;
+}
 
 // ---- mbarrier, bulk tensor copies, timer
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {

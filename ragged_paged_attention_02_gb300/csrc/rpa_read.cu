@@ -165,14 +165,7 @@ __global__ void __launch_bounds__(kReadThreads, kReadCtas) rpa_read_kernel(const
         };
         if (few) {
             if (tid < n) {
-                // the last sequence that starts at or before the token
-                const int t = t0 + tid;
-                int s = 0, e = p.S;
-                while (e - s > 1) {
-                    const int m = (s + e) / 2;
-                    if (s_cu[m] <= t) s = m;
-                    else e = m;
-                }
+                const int t = t0 + tid, s = last_start(s_cu, p.S, t);
                 const bool in = p.S > 0 && s_cu[s] <= t && t < s_cu[s + 1];
                 look_up(tid, t, in ? s : -1, in ? s_cu[s] : 0, in ? s_cu[s + 1] - s_cu[s] : 0, in ? s_kl[s] : 0);
             }

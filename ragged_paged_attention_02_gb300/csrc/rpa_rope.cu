@@ -456,14 +456,7 @@ __global__ void __launch_bounds__(kRopeThreads, INT4 ? kRopeCtas4 : kRopeCtas) r
         if (few) {
             __syncthreads();
             if (tid < n) {
-                // the last sequence that starts at or before the token
-                const int t = t0 + tid;
-                int s = 0, end = p.S;
-                while (end - s > 1) {
-                    const int m = (s + end) / 2;
-                    if (s_cu[m] <= t) s = m;
-                    else end = m;
-                }
+                const int t = t0 + tid, s = last_start(s_cu, p.S, t);
                 const bool in = p.S > 0 && s_cu[s] <= t && t < s_cu[s + 1];
                 look_up(tid, t, in ? s : -1, in ? s_cu[s] : 0, in ? s_cu[s + 1] - s_cu[s] : 0, in ? s_kl[s] : 0);
             }
@@ -497,75 +490,75 @@ __global__ void __launch_bounds__(kRopeThreads, INT4 ? kRopeCtas4 : kRopeCtas) r
         // one row of a token
         auto process = [&](int tb, int rb, const Vec8<QT>& v0, const Vec8<QT>& v1) {
             if (!s_live[tb]) return;
-                                float y[16];
-                                widen(v0, y);
-                                widen(v1, y + 8);
-                                float yl[INT4 ? 16 : 1];
-                                if constexpr (INT4) {
-                                    if (rb >= p.Hq) {
-            #pragma unroll
-                                        for (int i = 0; i < 16; ++i) yl[i] = 0.f;
-                                    }
-                                    if (rot && rb >= p.Hq && rb < p.Hq + p.Hkv) {
-            #pragma unroll
-                                        for (int i = 0; i < 4; ++i) {
-                                            const float4 cs = s_cs[(tb * 4 + i) * places + place], cl = s_cs[(kRound * 4 + tb * 4 + i) * places + place];
-            #pragma unroll
-                                            for (int j = 0; j < 2; ++j) {
-                                                const int m = 2 * i + j, a = HALF ? m : 2 * m, c = HALF ? m + 8 : 2 * m + 1;
-                                                const float co = j ? cs.z : cs.x, si = j ? cs.w : cs.y, col = j ? cl.z : cl.x, sil = j ? cl.w : cl.y;
-                                                const float u = y[a], w = y[c];
-                                                turn_pair(u, w, co, col, si, sil, y[a], yl[a]);
-                                                turn_pair(w, -u, co, col, si, sil, y[c], yl[c]);
-                                            }
-                                        }
-                                    }
-                                }
-                                if (rot && rb < p.Hq + (INT4 ? 0 : p.Hkv)) {
-            #pragma unroll
-                                    for (int i = 0; i < 4; ++i) {
-                                        const float4 cs = s_cs[(tb * 4 + i) * places + place];  // cos, sin of pairs 2 i and 2 i + 1
-            #pragma unroll
-                                        for (int j = 0; j < 2; ++j) {
-                                            const int m = 2 * i + j, a = HALF ? m : 2 * m, c = HALF ? m + 8 : 2 * m + 1;
-                                            const float co = j ? cs.z : cs.x, si = j ? cs.w : cs.y, u = y[a], w = y[c];
-                                            y[a] = u * co - w * si;
-                                            y[c] = w * co + u * si;
-                                        }
-                                    }
-                                }
-                                if (rb < p.Hq) {
-                                    QT* o = reinterpret_cast<QT*>(p.q_out) + ((size_t)(t0 + tb) * p.Hq + rb) * p.D;
-                                    store_q8(o + e0, y);
-                                    store_q8(o + e1, y + 8);
-                                } else if (s_slot[tb] >= 0) {
-                                    const bool is_v = rb >= p.Hq + p.Hkv;
-                                    const int h = rb - p.Hq - (is_v ? p.Hkv : 0);
-                                    if (is_v ? p.has_vs : p.has_ks) {
-                                        const float sc = is_v ? p.v_scale : p.k_scale;
-            #pragma unroll
-                                        for (int i = 0; i < 16; ++i) {
-                                            const float u = y[i], quotient = __fdiv_rn(u, sc);
-                                            if constexpr (INT4) {
-                                                // (what the quotient's rounding left is a value's lower half too)
-                                                const float rest = (fmaf(-quotient, sc, u) + yl[i]) * __frcp_rn(sc);
-                                                quick_sum(quotient, fabsf(quotient) < INFINITY && fabsf(rest) < INFINITY ? rest : 0.f, y[i], yl[i]);
-                                            } else {
-                                                y[i] = quotient;
-                                            }
-                                        }
-                                    }
-                                    if constexpr (INT4) {
-                                        const uint32_t mask = ((1u << p.per_row) - 1u) << (lane - place % 32);
-                                        store_int4(p, y, yl, e0, e1, s_rows + (size_t)(tid - place) * kUnit, place, mask, s_slot[tb], h, is_v);
-                                        return;
-                                    }
-                                    const int rows = p.latent ? p.Hkv : 2 * p.Hkv;
-                                    const size_t row = ((size_t)s_slot[tb] * rows + (p.latent ? h : 2 * h + (is_v ? 1 : 0))) * p.D *
-                                                       (kt_8bit(p.kt) ? 1 : 2);
-                                    store_kv8(p.kv, row, e0, y, p.kt);
-                                    store_kv8(p.kv, row, e1, y + 8, p.kt);
-                                }
+            float y[16];
+            widen(v0, y);
+            widen(v1, y + 8);
+            float yl[INT4 ? 16 : 1];
+            if constexpr (INT4) {
+                if (rb >= p.Hq) {
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) yl[i] = 0.f;
+                }
+                if (rot && rb >= p.Hq && rb < p.Hq + p.Hkv) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float4 cs = s_cs[(tb * 4 + i) * places + place], cl = s_cs[(kRound * 4 + tb * 4 + i) * places + place];
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const int m = 2 * i + j, a = HALF ? m : 2 * m, c = HALF ? m + 8 : 2 * m + 1;
+                            const float co = j ? cs.z : cs.x, si = j ? cs.w : cs.y, col = j ? cl.z : cl.x, sil = j ? cl.w : cl.y;
+                            const float u = y[a], w = y[c];
+                            turn_pair(u, w, co, col, si, sil, y[a], yl[a]);
+                            turn_pair(w, -u, co, col, si, sil, y[c], yl[c]);
+                        }
+                    }
+                }
+            }
+            if (rot && rb < p.Hq + (INT4 ? 0 : p.Hkv)) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float4 cs = s_cs[(tb * 4 + i) * places + place];  // cos, sin of pairs 2 i and 2 i + 1
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+                        const int m = 2 * i + j, a = HALF ? m : 2 * m, c = HALF ? m + 8 : 2 * m + 1;
+                        const float co = j ? cs.z : cs.x, si = j ? cs.w : cs.y, u = y[a], w = y[c];
+                        y[a] = u * co - w * si;
+                        y[c] = w * co + u * si;
+                    }
+                }
+            }
+            if (rb < p.Hq) {
+                QT* o = reinterpret_cast<QT*>(p.q_out) + ((size_t)(t0 + tb) * p.Hq + rb) * p.D;
+                store_q8(o + e0, y);
+                store_q8(o + e1, y + 8);
+            } else if (s_slot[tb] >= 0) {
+                const bool is_v = rb >= p.Hq + p.Hkv;
+                const int h = rb - p.Hq - (is_v ? p.Hkv : 0);
+                if (is_v ? p.has_vs : p.has_ks) {
+                    const float sc = is_v ? p.v_scale : p.k_scale;
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float u = y[i], quotient = __fdiv_rn(u, sc);
+                        if constexpr (INT4) {
+                            // (what the quotient's rounding left is a value's lower half too)
+                            const float rest = (fmaf(-quotient, sc, u) + yl[i]) * __frcp_rn(sc);
+                            quick_sum(quotient, fabsf(quotient) < INFINITY && fabsf(rest) < INFINITY ? rest : 0.f, y[i], yl[i]);
+                        } else {
+                            y[i] = quotient;
+                        }
+                    }
+                }
+                if constexpr (INT4) {
+                    const uint32_t mask = ((1u << p.per_row) - 1u) << (lane - place % 32);
+                    store_int4(p, y, yl, e0, e1, s_rows + (size_t)(tid - place) * kUnit, place, mask, s_slot[tb], h, is_v);
+                    return;
+                }
+                const int rows = p.latent ? p.Hkv : 2 * p.Hkv;
+                const size_t row = ((size_t)s_slot[tb] * rows + (p.latent ? h : 2 * h + (is_v ? 1 : 0))) * p.D *
+                                   (kt_8bit(p.kt) ? 1 : 2);
+                store_kv8(p.kv, row, e0, y, p.kt);
+                store_kv8(p.kv, row, e1, y + 8, p.kt);
+            }
         };
         if constexpr (INT4) {
             // (one copy of the code that makes codes: two are more than the instruction cache takes)
