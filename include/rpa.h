@@ -261,7 +261,7 @@ typedef enum RpaOption {
                                       cache's planner always waits where the handle has room for f16 rows */
     RPA_OPT_TEST_STALL_PRODUCER = 100  /* test hook, 1: the copy warps of the decode kernel and of the 4-bit
                                       cache's issue nothing, so that their consumers' bounded waits run
-                                      out (status RPA_ERR_TIMEOUT); n > 1: they give up before their n-th
+                                      out (status RPA_ERR_TIMEOUT); 2: they give up behind their last
                                       stage, as if a wait of theirs had run out.  The kernel still returns */
 } RpaOption;
 

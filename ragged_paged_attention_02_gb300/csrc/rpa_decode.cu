@@ -130,7 +130,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kvmap, const CUte
         const int runs = kKS / BR;  // page runs per stage, one bulk copy each (K and V of the head)
         const uint32_t run_bytes = (uint32_t)(2 * Gm::DH * BR * 128);
         const uint64_t pol_stream = l2_policy_evict_first();
-        int s = 0, filled = 0;
+        int s = 0;
         uint32_t ph = 0;
         int it = 0;
         if (lane == 0) it = atomicAdd(ctrl + a.counter_word, 1);
@@ -160,7 +160,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kvmap, const CUte
                     win0 = k_stage / ps;
                     win = (win0 + lane < a.P) ? __ldg(ptab + win0 + lane) : 0;
                 }
-                if (!mbar_wait(smem_u32(&empty_bar[s]), ph ^ 1u, ctrl, tmo) || (p.debug_stall && ++filled == p.debug_stall)) {
+                if (!mbar_wait(smem_u32(&empty_bar[s]), ph ^ 1u, ctrl, tmo)) {
                     ok = false;
                     break;
                 }
@@ -219,7 +219,7 @@ __device__ __forceinline__ void decode_body(const CUtensorMap& kvmap, const CUte
             }
             it = __shfl_sync(0xffffffffu, nxt, 0);
         }
-        if (ok && mbar_wait(smem_u32(&empty_bar[s]), ph ^ 1u, ctrl, tmo)) {
+        if (ok && !p.debug_stall && mbar_wait(smem_u32(&empty_bar[s]), ph ^ 1u, ctrl, tmo)) {
             if (lane == 0) {
                 meta[s][mStop] = 1;
                 mbar_arrive(smem_u32(&full_bar[s]));

@@ -309,7 +309,7 @@ int rpa_set_option(RpaHandle* h, int32_t option, int64_t value) {
             h->plan_early = (int)value;
             return RPA_OK;
         case RPA_OPT_TEST_STALL_PRODUCER:
-            if (value < 0 || value > 1000000) return RPA_ERR_INVALID_ARG;
+            if (value < 0 || value > 2) return RPA_ERR_INVALID_ARG;
             h->debug_stall = (int)value;
             return RPA_OK;
         default:

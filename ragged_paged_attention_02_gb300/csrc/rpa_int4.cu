@@ -160,7 +160,7 @@ __global__ void __launch_bounds__((I4Geom<D, NG>::THREADS), (I4Geom<D, NG>::CTAS
         const int ps = a.ps, runs = KS / BR;
         // K/V is read once, unless several blocks of query heads share it
         const uint64_t pol = p.blocks > 1 ? l2_policy_evict_last() : l2_policy_evict_first();
-        int s = 0, filled = 0;
+        int s = 0;
         uint32_t ph = 0, qph = 0;
         // An item, and the next one's description, which is fetched while this one's keys are on their way: its number, then its
         // unit, then its lengths, then its first page ids, each a stage after what it depends on.
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__((I4Geom<D, NG>::THREADS), (I4Geom<D, NG>::CTAS
                     win = (win0 + lane < a.P) ? ptab[win0 + lane] : 0;
                     win2 = (win0 + 32 + lane < a.P) ? ptab[win0 + 32 + lane] : 0;
                 }
-                if (!mbar_wait(smem_u32(&empty_bar[s]), ph ^ 1u, ctrl, tmo) || (p.stall && ++filled == p.stall)) {
+                if (!mbar_wait(smem_u32(&empty_bar[s]), ph ^ 1u, ctrl, tmo)) {
                     ok = false;
                     break;
                 }
@@ -318,7 +318,7 @@ __global__ void __launch_bounds__((I4Geom<D, NG>::THREADS), (I4Geom<D, NG>::CTAS
                 cur = nxt;
             }
         }
-        if (ok && mbar_wait(smem_u32(&empty_bar[s]), ph ^ 1u, ctrl, tmo)) {
+        if (ok && !p.stall && mbar_wait(smem_u32(&empty_bar[s]), ph ^ 1u, ctrl, tmo)) {
             if (lane == 0) {
                 meta[s][mLeft] = -1;
                 mbar_arrive(smem_u32(&full_bar[s]));
