@@ -169,10 +169,8 @@ __global__ void __launch_bounds__(kThreads, 1) rpa_prefill_tc(const __grid_const
         for (;;) {
             const bool stop = it >= n_items;
             if (!mbar_wait(smem_u32(&q_empty), qph ^ 1u, ctrl, tmo) ||
-                !mbar_wait(smem_u32(&meta_free), qph ^ 1u, ctrl, tmo)) {
-                ok = false;
+                !mbar_wait(smem_u32(&meta_free), qph ^ 1u, ctrl, tmo))
                 break;
-            }
             if (stop) {
                 if (lane == 0) {
                     meta[tStop] = 1;
@@ -282,11 +280,6 @@ __global__ void __launch_bounds__(kThreads, 1) rpa_prefill_tc(const __grid_const
             }
             if (!ok) break;
             it = __shfl_sync(0xffffffffu, nxt, 0);
-        }
-        if (!ok) {
-            // gave up: let the copies already issued land before leaving
-            drain_ring(kv_full, kNS, s, ph, ctrl, tmo);
-            drain_ring(&q_full, 1, 0, qph, ctrl, tmo);
         }
     } else if (warp == kMma) {
         // =============================== MMA issuer ===============================

@@ -291,15 +291,11 @@ __global__ void __launch_bounds__(kRegBoundThreads, 1) rpa_prefill_tc8(const __g
         int s = 0, ms = 0;
         uint32_t ph = 0, mph = 0, qph = 0;
         uint32_t tgp = 0;  // direct mode: tiles copied so far (all items): tile buffer and phase
-        uint32_t k_ahead = 0;  // ... and, where it gives up, whether the next one's K has been too
         bool ok = true;
         const int ctas = min(ctrl[kPfCtas], (int)gridDim.x), first = ctrl[kPfFirst];
         int it = blockIdx.x;  // the first item is the CTA's own, the others come off a counter
         for (;;) {
-            if (!mbar_wait(smem_u32(&meta_free[ms]), mph ^ 1u, ctrl, tmo)) {
-                ok = false;
-                break;
-            }
+            if (!mbar_wait(smem_u32(&meta_free[ms]), mph ^ 1u, ctrl, tmo)) break;
             if (it >= n_items) {
                 if (lane == 0) {
                     meta[ms][eStop] = 1;
@@ -374,11 +370,11 @@ __global__ void __launch_bounds__(kRegBoundThreads, 1) rpa_prefill_tc8(const __g
                     static_assert(Gm::NBK == Gm::NBV, "direct mode: K and V rings alike");
                     const int b2 = kbuf(tgp);
                     const uint32_t par = kpar(tgp);
+                    ++tgp;
                     const int tasks = runs * Gm::CB;
 #pragma unroll 1
                     for (int kv = 0; kv < 2 && ok; ++kv) {
                         if (!mbar_wait(smem_u32(kv ? &v_free[b2] : &k_free[b2]), par ^ 1u, ctrl, tmo)) {
-                            k_ahead = kv;
                             ok = false;
                             break;
                         }
@@ -430,7 +426,6 @@ __global__ void __launch_bounds__(kRegBoundThreads, 1) rpa_prefill_tc8(const __g
                             if (task(t0 + lane, x, y, dst) == 1) tma_load_2d(dst, &kvmap, fb, x, y);
                         }
                     }
-                    if (ok) ++tgp;
                     continue;
                 }
                 if (!mbar_wait(smem_u32(&raw_empty[s]), ph ^ 1u, ctrl, tmo)) {
@@ -458,16 +453,6 @@ __global__ void __launch_bounds__(kRegBoundThreads, 1) rpa_prefill_tc8(const __g
             }
             if (!ok) break;
             it = __shfl_sync(0xffffffffu, nxt, 0);
-        }
-        if (!ok) {
-            // gave up: let the copies already issued land before leaving
-            if constexpr (DIRECT) {
-                drain_ring(k_full, Gm::NBK, kbuf(tgp + k_ahead), kpar(tgp + k_ahead), ctrl, tmo);
-                drain_ring(v_land, Gm::NBV, kbuf(tgp), kpar(tgp), ctrl, tmo);
-            } else {
-                drain_ring(raw_full, Gm::NRAW, s, ph, ctrl, tmo);
-            }
-            drain_ring(&q_full, 1, 0, qph, ctrl, tmo);
         }
     } else if (warp >= kConv0 && warp < kConv0 + kNConv) {
         // =============================== converters ===============================
