@@ -70,27 +70,21 @@ __global__ void __launch_bounds__(kCombThreads, kCombCtasPerSm) rpa_combine_kern
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
         float L = 0.f, sc_mine = 0.f;  // sc_mine: 2^(m_lane - M) for piece `lane` (the first 32)
-        if (M != -INFINITY) {
-            for (int k = lane; k < pieces; k += 32) {
-                const float2 w = *reinterpret_cast<const float2*>(ml + (size_t)k * PR * 2);
-                const float sc = ex2(w.x - M);
-                if (k < 32) sc_mine = sc;
-                L += sc * w.y;
-            }
-        } else {
-            // nothing is visible, or every visible logit is a NaN (no maximum takes one): then a piece's sum is too
-            for (int k = lane; k < pieces; k += 32) L += ml[(size_t)k * PR * 2 + 1];
+        // (nothing is visible, or every visible logit is a NaN, which no maximum takes: L is 0, or the NaN that a piece's l is)
+        const float base = M == -INFINITY ? 0.f : M;
+        for (int k = lane; k < pieces; k += 32) {
+            const float2 w = *reinterpret_cast<const float2*>(ml + (size_t)k * PR * 2);
+            const float sc = ex2(w.x - base);
+            if (k < 32) sc_mine = sc;
+            L += sc * w.y;
         }
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) L += __shfl_xor_sync(0xffffffffu, L, o);
         const int qh = kvh * p.heads + h0 + r % G;
-        const float top = p.most * L;  // (without keys 0 or a NaN, which nothing passes)
         L = add_sink(L, p.sinks, qh, M);  // the sink joins once, over all pieces
-        const float inv = L > 0.f ? p.v_scale / L : 0.f;
+        const float inv = L > 0.f ? p.v_scale / L : 0.f * L;  // (a NaN stays one)
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (M == -INFINITY) {
-            if (L != L) acc = make_float4(L, L, L, L);
-        } else {
+        if (M != -INFINITY) {
             if (held) {
 #pragma unroll
                 for (int k = 0; k < kBatch; ++k) {
@@ -127,7 +121,6 @@ __global__ void __launch_bounds__(kCombThreads, kCombCtasPerSm) rpa_combine_kern
                 }
             }
         }
-        acc = make_float4(acc.x > top ? top : acc.x, acc.y > top ? top : acc.y, acc.z > top ? top : acc.z, acc.w > top ? top : acc.w);
         if (act)
             store_o4(p.o, ((size_t)(q0 + r / G) * Hq + qh) * D + 4 * c4, acc.x * inv, acc.y * inv, acc.z * inv,
                      acc.w * inv, p.odt);

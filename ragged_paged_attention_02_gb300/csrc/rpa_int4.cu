@@ -665,31 +665,28 @@ __global__ void __launch_bounds__((I4Geom<D, NG>::THREADS), (I4Geom<D, NG>::CTAS
             float M = -INFINITY;
 #pragma unroll
             for (int i = 0; i < CW; ++i) M = fmaxf(M, red_ml[i][r][0]);
+            // (nothing is visible, or every visible logit is a NaN, which no maximum takes: L is 0, or the NaN that a warp's l is)
+            const float base = M == -INFINITY ? 0.f : M;
             float L = 0.f;
             float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (M != -INFINITY) {
 #pragma unroll
-                for (int i = 0; i < CW; ++i) {
-                    const float sc = ex2(red_ml[i][r][0] - M);
-                    L += sc * red_ml[i][r][1];
+            for (int i = 0; i < CW; ++i) {
+                const float sc = ex2(red_ml[i][r][0] - base);
+                L += sc * red_ml[i][r][1];
+                if (M != -INFINITY) {
                     const float4 v = *reinterpret_cast<const float4*>(red_o + (i * R + r) * Gm::LD + c);
                     o.x += sc * v.x;
                     o.y += sc * v.y;
                     o.z += sc * v.z;
                     o.w += sc * v.w;
                 }
-            } else {
-                // nothing is visible, or every visible logit is a NaN (no maximum takes one): then a sum is too
-#pragma unroll
-                for (int i = 0; i < CW; ++i) L += red_ml[i][r][1];
-                if (L != L) o = make_float4(L, L, L, L);
             }
+            const float top = kMostHalf * L;  // values end at 65504 here as they do in f16 rows (and means of them do, of pieces too)
+            o = make_float4(o.x > top ? top : o.x, o.y > top ? top : o.y, o.z > top ? top : o.z, o.w > top ? top : o.w);
             if (part < 0) {
                 const int tok = m2.y + r / G, qh = m2.x + hr;
-                const float top = kMostHalf * L;  // values end at 65504 here as they do in f16 rows
-                o = make_float4(o.x > top ? top : o.x, o.y > top ? top : o.y, o.z > top ? top : o.z, o.w > top ? top : o.w);
                 L = add_sink(L, a.sinks, qh, M);
-                const float inv = L > 0.f ? a.v_scale / L : 0.f;
+                const float inv = L > 0.f ? a.v_scale / L : 0.f * L;  // (a NaN stays one)
                 store_o4(a.o, ((size_t)tok * Hq + qh) * D + c, o.x * inv, o.y * inv, o.z * inv, o.w * inv, a.odt);
             } else {
                 *reinterpret_cast<float4*>(a.part_o + ((size_t)part * R + r) * D + c) = o;

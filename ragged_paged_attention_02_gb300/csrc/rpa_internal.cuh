@@ -251,7 +251,6 @@ struct CombParams {
     int num_seqs, T, Hq, G, D;
     int rows_max;  // most rows of a combine entry (the decode tile's rows)
     int part_rows;      // rows of a partial slot
-    float most;         // the greatest mean of values before v_scale (infinity but for 4-bit K/V, whose values end at 65504)
     int blocks, heads;  // entries' heads a kv head makes, and its query heads (one, and G, but for 4-bit K/V: its last may have fewer)
     float v_scale;
     const float* sinks;  // [Hq] sink logits (natural-log domain), or nullptr

@@ -512,7 +512,6 @@ int enqueue_forward(const RpaCfg& c, const KernelSet& ks, const Workspace& ws, M
     cp.D = ks.Dv;  // the width of o and of the split-KV partials
     cp.rows_max = ks.dec_rows;
     cp.part_rows = ks.kt == KT_I4 ? kInt4Rows : kDecRows;
-    cp.most = ks.kt == KT_I4 ? kMostHalf : INFINITY;
     cp.blocks = ks.kt == KT_I4 ? ks.Hp / ap.Hkv : 1;
     cp.heads = ks.kt == KT_I4 ? ks.G : ks.Gp;
     cp.v_scale = ks.v_scale;
