@@ -68,7 +68,7 @@ typedef enum RpaDtype {
  * (page_size a multiple of 4 as ever, and at most 65536; pages_per_seq * page_size at most 2^31 - 1024)
  * and a channel's value is  code * scale + zero  of its group (times k_scale or v_scale).  The scale of a group whose greatest
  * value is near 65504 is rounded up too, so that its code 15 may stand for up to 65536: rpa_forward, and rpa_rope_read into f16,
- * take such a value as 65504.  rpa_rope_append writes
+ * take such a value as 65504 (a prompt's V as 65472, one step less, and -65504 as -65472: means of them stay in f16's range).  rpa_rope_append writes
  * it, rpa_rope_read reads its rows as values, rpa_forward attends over it.
  * rpa_forward takes scales from 0 to 8736 (what values of f16's range can have) and rounds q to f16.  It multiplies the codes
  * themselves, with probabilities times scales rounded to f16 (those below 2^-14 to a multiple of 2^-24: v_scale keeps small

@@ -108,6 +108,8 @@ __device__ __forceinline__ void mma_first(float* d, const uint32_t* a, uint32_t 
         : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
 }
+// x within [-top, top]; a NaN of either stays what x is
+__device__ __forceinline__ float within(float x, float top) { return x > top ? top : x < -top ? -top : x; }
 template <int NG>
 __device__ __forceinline__ void load_meta(uint32_t addr, uint32_t* m) {
     if constexpr (NG == 1) {
@@ -681,8 +683,8 @@ __global__ void __launch_bounds__((I4Geom<D, NG>::THREADS), (I4Geom<D, NG>::CTAS
                     o.w += sc * v.w;
                 }
             }
-            const float top = kMostHalf * L;  // values end at 65504 here as they do in f16 rows (and means of them do, of pieces too)
-            o = make_float4(o.x > top ? top : o.x, o.y > top ? top : o.y, o.z > top ? top : o.z, o.w > top ? top : o.w);
+            const float top = kMostHalf * L;  // values end at +-65504 here as they do in f16 rows, and means of them do, whatever P's rounding adds
+            o = make_float4(within(o.x, top), within(o.y, top), within(o.z, top), within(o.w, top));
             if (part < 0) {
                 const int tok = m2.y + r / G, qh = m2.x + hr;
                 L = add_sink(L, a.sinks, qh, M);
@@ -713,6 +715,13 @@ struct UnfoldParams {
 };
 
 constexpr int kUnfoldThreads = 256, kUnfoldCtas = 5;
+
+// V's rows end one step in front of f16's last value: a mean of them with P rounded (by 2^-11 at most) is then none past it
+constexpr float kMostRow = 65472.f;
+__device__ __forceinline__ void saturate_row(float* f) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) f[i] = within(f[i], kMostRow);
+}
 
 __global__ void __launch_bounds__(kUnfoldThreads, kUnfoldCtas) rpa_int4_unfold(const UnfoldParams p) {
     pdl_trigger();
@@ -793,7 +802,8 @@ __global__ void __launch_bounds__(kUnfoldThreads, kUnfoldCtas) rpa_int4_unfold(c
                         const float2 sz = f16x2_to_f32x2(pairs[b][is_v]);
                         float f[16];
                         int4_values(codes[b][is_v], sz, f);
-                        int4_saturate(sz, f);
+                        if (!is_v) int4_saturate(sz, f);
+                        else if (fmaxf(fabsf(sz.y), fmaf(15.f, sz.x, sz.y)) > kMostRow) saturate_row(f);
 #pragma unroll
                         for (int k = 0; k < 8; ++k) out[k] = pack2<true>(f[2 * k], f[2 * k + 1]);
                     }

@@ -81,3 +81,45 @@ def test_one_key_of_all_the_weight(D, group, kv_lens, q):
         got = f64(out[:3])
         assert np.isfinite(got).all()
         assert (np.abs(got - want) <= (2.0 ** -10 if q == "f16" else 0) * np.abs(want) + 0.125).all()
+
+
+@pytest.mark.parametrize("D,group,apart", [(64, 32, 256), (128, 64, 224), (256, 128, 160)])
+def test_means_of_the_last_values(D, group, apart):
+    """Channels that are 65504, or -65504, in every key: so is their mean, whatever P's rounding adds.  Two keys of a row draw its weight,
+    the second up to 2^2 times the first, which holds the running maximum (`apart` keys on, where the same warp meets it): P is then
+    up to 4 steps of 8736 and rounded by up to 8, and 8 times that over both weights can pass the 16 that are left to infinity."""
+    S, H = 400, 8  # (as many that the two keys lie in one piece)
+    b = Batch(np.random.default_rng([3, D]), [1] * S, [1000] * S, 16, H, 2, D, kv="int4_g%d" % group, q="f16")
+    v = b.rng.uniform(-65504, 65504, (b.N, 16, 2, D))
+    v[..., 0::4], v[..., 1::4] = 65504, -65504
+    k = np.zeros((b.N, 16, 2, D))
+    k[..., 0] = -1000
+    for s in range(S):
+        page, at = b.slots(s, [0, apart])
+        k[page[0], at[0], :, 0], k[page[1], at[1], :, 0] = 0, 1
+    parts = [i4.coded(x, group) for x in (k, v)]
+    cache = torch.from_numpy(i4.pack(parts, 16, D, group)).cuda()
+    q = torch.zeros(b.T, H, D, dtype=torch.float16, device="cuda")
+    q[:, :, 0] = torch.from_numpy(b.rng.uniform(0.1, 1.38, (b.T, H)) * np.sqrt(D)).half().cuda()
+    att = rpa.RaggedPagedAttention(**b.cfg())
+    out = f64(att.forward(q, cache, *b.lens(), b.S))[:S]
+    assert att.status() == rpa.RPA_OK and np.isfinite(out).all()
+    # (P's rounding moves the mean by up to 8 * 8 / 2, o is rounded to a multiple of 32 there)
+    assert (out[..., 0::4] >= 65504 - 64).all() and (out[..., 1::4] <= -65504 + 64).all()
+
+
+@pytest.mark.parametrize("D,group", [(64, 32), (128, 64), (256, 128)])
+def test_means_of_the_last_values_of_prompts(D, group):
+    """The same in a prompt's f16 rows: P is rounded there by up to 2^-11 of it, the rows end at 65472, one step in front of 65504."""
+    n = 600
+    b = Batch(np.random.default_rng([4, D]), [n], [n], 64, 8, 2, D, kv="int4_g%d" % group, q="f16")
+    v = b.rng.uniform(-65504, 65504, (b.N, 64, 2, D))
+    v[..., 0::4], v[..., 1::4] = 65504, -65504
+    parts = [i4.coded(x, group) for x in (b.rng.standard_normal((b.N, 64, 2, D)), v)]
+    cache = torch.from_numpy(i4.pack(parts, 64, D, group)).cuda()
+    att, q = rpa.RaggedPagedAttention(**b.cfg()), b.queries()
+    for scale in (1, 4):  # some keys of the weight, and few
+        out = f64(att.forward(q * scale, cache, *b.lens(), b.S))[:n]
+        assert att.status() == rpa.RPA_OK and np.isfinite(out).all() and att.plan()[0][2] > 0
+        # (a row of 65472, P's 2^-11 of it, and o's rounding)
+        assert (out[..., 0::4] >= 65504 - 96).all() and (out[..., 1::4] <= -65504 + 96).all()
