@@ -66,16 +66,17 @@ typedef enum RpaDtype {
  *   K scale, zero  [page_size][D / group] pairs of f16
  *   V scale, zero  alike
  * (page_size a multiple of 4 as ever, and at most 65536; pages_per_seq * page_size at most 2^31 - 1024)
- * and a channel's value is  code * scale + zero  of its group (times k_scale or v_scale).  The scale of a group whose greatest
- * value is near 65504 is rounded up too, so that its code 15 may stand for up to 65536: rpa_forward, and rpa_rope_read into f16,
- * take such a value as 65504 (a prompt's V as 65472, one step less, and -65504 as -65472: means of them stay in f16's range).  rpa_rope_append writes
- * it, rpa_rope_read reads its rows as values, rpa_forward attends over it.
+ * and a channel's value is  code * scale + zero  of its group (times k_scale or v_scale).  rpa_rope_append writes it,
+ * rpa_rope_read reads its rows as values, rpa_forward attends over it.  The scale of a group whose greatest value is near
+ * 65504 is rounded up too, so that its code 15 may stand for up to 65536: rpa_forward, and rpa_rope_read into f16, take such
+ * a value as 65504 (a prompt's V as 65472, one step less, and -65504 as -65472: means of them stay in f16's range).
  * rpa_forward takes scales from 0 to 8736 (what values of f16's range can have) and rounds q to f16.  It multiplies the codes
  * themselves, with probabilities times scales rounded to f16 (those below 2^-14 to a multiple of 2^-24: v_scale keeps small
  * values away from there).  A sequence of many tokens (more than 64 to 448 query rows a kv head, by how many such there are) is
  * computed from its K and V as f16 values instead, which the call writes to the workspace: the handle has room for
  * 1 GiB of them, or for one sequence of the most keys that fit into kv_pages (up to 8 GiB), if that is more; half of that, half
- * again and so on where rpa_create cannot allocate it; and none where num_q_tokens <= max_num_seqs or no call of num_q_tokens can have such a sequence.  Sequences without room are computed from the codes, more slowly.
+ * again and so on where rpa_create cannot allocate it; and none where num_q_tokens <= max_num_seqs or no call of num_q_tokens
+ * can have such a sequence.  Sequences without room are computed from the codes, more slowly.
  * A query row that sees a NaN logit comes out as NaN, whichever way it is computed. */
 
 typedef enum RpaStatus {
@@ -381,8 +382,8 @@ int rpa_rope_create(const RpaRopeCfg* cfg, RpaRope** out);
  * rpa_rope_frequencies gives it, modulo a turn, exact to 2^-32 of a turn at any position; the sine then
  * takes it as a 32-bit float, within 2^-26 of a turn near half a turn and exact near 0 (values of a 4-bit cache are rotated and
  * divided by its scales in pairs of floats: a value next to the border of two codes takes the right one, but within 2^-45 of the
- * value behind a division, 2^-29 of its pair's size behind a rotation).  Cache rows hold k / k_scale and v / v_scale (where set), rounded to nearest even;
- * the 8-bit types saturate, NaN stays NaN (int8: 0); f16 rows overflow to infinity.  4-bit rows: values saturate at
+ * value behind a division, 2^-29 of its pair's size behind a rotation).  Cache rows hold k / k_scale and v / v_scale (where
+ * set), rounded to nearest even; the 8-bit types saturate, NaN stays NaN (int8: 0); f16 rows overflow to infinity.  4-bit rows: values saturate at
  * +-65504; a group's zero is its least value rounded down to f16, its scale (greatest - zero) / 15 rounded up to f16, a
  * code (value - zero) / scale rounded to nearest even, at most 15; a group with a NaN reads as NaN.
  * Rows of q_out and slots of the cache that no token of the call stands for are left as they were, as

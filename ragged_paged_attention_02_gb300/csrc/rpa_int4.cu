@@ -18,7 +18,7 @@
 //    head (or four pieces of one where its size is not that of a run) into a ring of stages, the other warps take 32 keys of
 //    each.  Bound by instructions more than by bytes (a key and kv head costs 17 issue slots at D 128, of the 25 that its bytes'
 //    time has), so as few warps as can feed the others issue copies.  (Warps that each copied for themselves took 25.)
-//    128 decodes of 512 to 16 k keys (32 query and 8 kv heads, D 128, groups of 64, 1245 MB): 225 us of the call's 234, 5.5 TB/s.
+//    128 decodes of 512 to 16 k keys (32 query and 8 kv heads, D 128, groups of 64, 1245 MB): 225 us of the call's 232, 5.5 TB/s.
 //    16 decodes of a 4 k window (D 256, groups of 128, soft cap, 143 MB): 43 us of 51, 3.4 TB/s (64 of them 125 us, 4.5 TB/s): some
 //    45 instructions a key and warp, which 12 warps of 168 registers issue in 39 % of the cycles; three to five consumer warps,
 //    two or three CTAs an SM, and pieces of 4 to 13 stages all took 53 to 59 us where this took 54.  32 sequences of 1 to 5
