@@ -34,7 +34,7 @@ def test_giving_up(kv, Hq, D, kv_lens):
     att = rpa.RaggedPagedAttention(**b.cfg())
     want = att.forward(q, cache, *lens, b.S)
     assert att.status() == rpa.RPA_OK
-    att.set_option(rpa.RPA_OPT_WAIT_TIMEOUT_MS, 100)
+    att.set_option(rpa.RPA_OPT_WAIT_TIMEOUT_MS, 300)
     for stall in (2, 0, 2):
         att.set_option(rpa.RPA_OPT_TEST_STALL_PRODUCER, stall)
         t0 = time.perf_counter()
@@ -43,9 +43,9 @@ def test_giving_up(kv, Hq, D, kv_lens):
         took = time.perf_counter() - t0
         assert torch.equal(got, want)  # every stage was there
         if stall:
-            assert status == rpa.RPA_ERR_TIMEOUT and 0.09 < took < 0.19, (status, took)
+            assert status == rpa.RPA_ERR_TIMEOUT and 0.29 < took < 0.55, (status, took)
         else:
-            assert status == rpa.RPA_OK and took < 0.09
+            assert status == rpa.RPA_OK and took < 0.29
 
 
 def test_the_hook_takes_two_values():
